@@ -301,6 +301,149 @@ tmg_status tmg_gemm_skinny_noalloc(const void *A, const void *B, void *D,
                                    int64_t lda, int64_t ldb, int64_t ldd,
                                    void *stream);
 
+/* ------------------------------------------------- mixture of experts
+ *
+ * Routing, the products grouped by expert and the weighted sum that follows
+ * them.  Tokens t < T choose k of E experts; the pairs (t, j) are sorted by
+ * expert, keeping their order, and each pair's place in that order is its
+ * slot: the row of the grouped products' operands that belongs to it.  The
+ * FlyDSL pages have no counterpart; the products read their operands in the
+ * convention of tmg_gemm (A rows by K, each expert's B as N by K). */
+
+/* The activation of the grouped and the dense products. */
+typedef enum {
+    TMG_ACT_NONE = 0,
+    TMG_ACT_RELU = 1,
+    TMG_ACT_SILU = 2,
+    TMG_ACT_GELU = 3,         /* erf form */
+    TMG_ACT_SWIGLU = 4,       /* D[:, f] = silu(z[:, f]) * z[:, N/2 + f] */
+    TMG_ACT_SWIGLU_GRAD = 5   /* z is the gradient of a SwiGLU result; D its inputs' gradients */
+} tmg_activation;
+
+/* Choose experts and plan the grouped products.
+ *   logits     device, (T, E) of `dtype` (TMG_F32 or TMG_BF16), unit column
+ *              stride, row stride ld (>= E).
+ *   k          choices per token, 1 <= k <= 16, k <= E <= 1024.
+ *   normalize  1: weights are the softmax over the chosen logits; 0: the
+ *              softmax over all E logits, at the chosen ones.
+ *   weights    out, fp32 (T, k);  experts  out, int32 (T, k), by falling logit.
+ *   offsets    out, int32 (E + 1): expert e's rows are offsets[e] ..
+ *              offsets[e + 1] - 1.
+ *   rows       out, int32 (T * k): the token of each row; -1 past offsets[E].
+ *   slots      out, int32 (T, k): the row of each pair.
+ * Equal logits go to the lower expert.  Logits of -inf and NaN are never
+ * chosen; where a token has fewer than k others, its remaining choices are
+ * expert -1, weight 0, slot -1, and take no row.  T * k < 2^31.  Results do
+ * not depend on timing.  Workspace: 4 E bytes per SM, per (device, stream). */
+tmg_status tmg_moe_route(const void *logits, int64_t T, int64_t E, int64_t k,
+                         int64_t ld, tmg_dtype dtype, int normalize,
+                         float *weights, int32_t *experts, int32_t *offsets,
+                         int32_t *rows, int32_t *slots, void *stream);
+
+/* Gradient of the logits, (T, E) contiguous of `dtype`, given the weights'
+ * (dweights, fp32 (T, k)) and tmg_moe_route's experts. */
+tmg_status tmg_moe_route_backward(const void *logits, int64_t T, int64_t E,
+                                  int64_t k, int64_t ld, tmg_dtype dtype,
+                                  int normalize, const int32_t *experts,
+                                  const float *dweights, void *dlogits,
+                                  void *stream);
+
+/* out[t] = bf16(residual[t] + sum_j weights[t, j] * Y[slots[t, j]]), fp32 sums
+ * in the order of j.
+ *   Y         device, bf16 (R, H), row stride ldy.
+ *   slots     int32 (T, k), k <= 16; a slot outside 0 .. R - 1 adds nothing.
+ *   weights   fp32 (T, k) or NULL (ones);  residual  bf16 (T, H), row stride
+ *             ldr, or NULL;  out  bf16 (T, H), row stride ldo (>= H).
+ * With weights NULL it is the gradient of the gather by `rows`. */
+tmg_status tmg_moe_combine(const void *Y, int64_t R, int64_t ldy,
+                           const int32_t *slots, const float *weights,
+                           const void *residual, int64_t ldr, void *out,
+                           int64_t ldo, int64_t T, int64_t H, int64_t k,
+                           void *stream);
+
+/* Its gradients: dY[slots[t, j]] = bf16(weights[t, j] * dOut[t]) ((R, H)
+ * contiguous; rows that no slot names are left as they are) and, unless
+ * dweights is NULL, dweights[t, j] = sum_h dOut[t, h] * Y[slots[t, j], h]
+ * (fp32; 0 where the slot is outside).  Y may be NULL when dweights is. */
+tmg_status tmg_moe_combine_backward(const void *dOut, int64_t ldo,
+                                    const void *Y, int64_t R, int64_t ldy,
+                                    const int32_t *slots, const float *weights,
+                                    void *dY, float *dweights, int64_t T,
+                                    int64_t H, int64_t k, void *stream);
+
+/* D[r] = act(A[rows[r]] . B[e]^T * scale_a[rows[r]] * scale_b[e]) for
+ * offsets[e] <= r < offsets[e + 1], fp32 sums, bf16 results.  Rows outside
+ * every group are left as they are. */
+typedef struct {
+    const void *A;          /* device, (T, K) of in_dtype; row r of D reads row rows[r] (out of range: zeros) */
+    const void *B;          /* device, (E, N, K) of in_dtype through its strides */
+    void *D;                /* device, bf16 (R, N); SWIGLU: (R, N/2); SWIGLU_GRAD: (R, 2N) */
+    const int32_t *offsets; /* device, int32 (E + 1), not falling, within 0 .. R (clamped to it) */
+    const int32_t *rows;    /* device, int32 (R), or NULL: row r reads row r, T = R */
+    const float *scale_a;   /* device, fp32 (T) or NULL */
+    const float *scale_b;   /* device, fp32 (E, N) contiguous, or NULL */
+    void *preact;           /* SWIGLU: bf16 (R, N), z is written to it, or NULL;
+                               SWIGLU_GRAD: bf16 (R, 2N), the SwiGLU's inputs, read */
+    int64_t R, N, K, E, T;
+    int64_t lda, a_col;             /* strides of A, in elements */
+    int64_t b_expert, b_row, b_col; /* strides of B */
+    int64_t ldd, ld_preact;         /* row strides; unit column strides */
+    tmg_dtype in_dtype;             /* TMG_BF16 or TMG_E4M3 */
+    tmg_activation activation;      /* NONE, SWIGLU (N even) or SWIGLU_GRAD */
+} tmg_grouped_args;
+
+/* The grouped product.  Operands whose rows (for B: rows along K, or along N)
+ * are contiguous and 16-byte aligned are read in place; others are copied
+ * to workspace first (bf16; E4M3: UNSUPPORTED).  E <= 1024; R, N, K, T below
+ * 2^31; the offsets stay on the device.  K == 0 gives z = 0. */
+tmg_status tmg_grouped_gemm(const tmg_grouped_args *args, void *stream);
+
+/* dB[e] = bf16(sum over the rows r of group e of dD[r]^T A[rows[r]]), (E, N, K)
+ * contiguous, fp32 sums; a group without rows gives zeros.
+ *   dD  device, bf16 (R, N), strides ldd and d_col;  A  device, bf16 (T, K),
+ *   strides lda and a_col;  offsets, rows as above. */
+tmg_status tmg_grouped_gemm_wgrad(const void *dD, int64_t ldd, int64_t d_col,
+                                  const void *A, int64_t lda, int64_t a_col,
+                                  void *dB, const int32_t *offsets,
+                                  const int32_t *rows, int64_t R, int64_t N,
+                                  int64_t K, int64_t E, int64_t T,
+                                  void *stream);
+
+/* Dense product with the whole epilogue, fp32 until the one rounding:
+ *   z = (A . B^T) * scale_a[m] * scale_b[n] + bias[n];  preact = bf16(z);
+ *   D = bf16(act(z) + residual). */
+typedef struct {
+    const void *A;          /* device, (M, K) of in_dtype */
+    const void *B;          /* device, (N, K) of in_dtype */
+    void *D;                /* device, bf16 (M, N), row stride ldd */
+    const float *scale_a;   /* fp32 (M) or NULL */
+    const float *scale_b;   /* fp32 (N) or NULL */
+    const float *bias;      /* fp32 (N) or NULL */
+    const void *residual;   /* bf16 (M, N), row stride ld_residual, or NULL; may be D */
+    void *preact;           /* bf16 (M, N), row stride ld_preact, or NULL */
+    int64_t M, N, K;
+    int64_t lda, a_col, b_row, b_col;   /* strides of A and B, in elements */
+    int64_t ldd, ld_residual, ld_preact;
+    tmg_dtype in_dtype;                 /* TMG_BF16 or TMG_E4M3 */
+    tmg_activation activation;          /* NONE, RELU, SILU or GELU */
+} tmg_linear_args;
+
+tmg_status tmg_linear(const tmg_linear_args *args, void *stream);
+
+/* Gradients of tmg_linear (bf16, no scales): dz = bf16(dD * act'(preact)),
+ * dA = dz . B, dB = dz^T . A, dbias[n] = sum_m of the fp32 dz (in a fixed
+ * order).  The residual's gradient is dD itself.
+ *   dD, preact  device, bf16 (M, N), row strides ldd, ldp (preact: NULL with
+ *               TMG_ACT_NONE);  A (M, K), B (N, K)  bf16, row strides lda, ldb.
+ *   dA          bf16 (M, K) or NULL;  dB  bf16 (N, K) or NULL;
+ *   dbias       fp32 (N) or NULL.  Contiguous.
+ * Workspace: dz and the column sums of 64 rows each, per (device, stream). */
+tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
+                               int64_t ldp, const void *A, int64_t lda,
+                               const void *B, int64_t ldb, void *dA, void *dB,
+                               float *dbias, int64_t M, int64_t N, int64_t K,
+                               tmg_activation activation, void *stream);
+
 /* Synchronise `stream`, then report: TMG_ERR_CUDA for a sticky or pending
  * CUDA error, TMG_ERR_TIMEOUT if a kernel's bounded wait ran out since the
  * last check (the device error word is cleared and the skinny-path scratch

@@ -20,9 +20,12 @@ import torch
 
 from . import _native
 from ._native import (BF16, E4M3, EPILOGUES, F32, PATHS, Layout, TmgError, make_layout)  # noqa: F401
+from .grouped import (Routing, grouped_gemm, grouped_gemm_wgrad, linear, linear_backward, moe_combine,  # noqa: F401
+                      moe_combine_backward, moe_route, moe_route_backward)
 
 __all__ = ["gemm", "gemm_host", "gemm_fused", "gemm_w4a8", "gemm_w4a8_preshuffled", "w4a8_preshuffle",
-           "w4a8_preshuffled_bytes", "gemm_mxfp4", "check", "make_layout", "Layout", "TmgError",
+           "w4a8_preshuffled_bytes", "gemm_mxfp4", "moe_route", "moe_route_backward", "moe_combine",
+           "moe_combine_backward", "grouped_gemm", "grouped_gemm_wgrad", "linear", "linear_backward", "Routing", "check", "make_layout", "Layout", "TmgError",
            "set_wait_budget_ns", "debug_wait_timeout", "launch_count", "version",
            "shutdown", "PATHS"]
 

@@ -23,7 +23,9 @@ PATHS = {"auto": 0, "ffma": 1, "tc": 2, "skinny": 3, "skinny_ffma": 4, "tc_singl
 
 # Every function include/tmg.h declares.
 EXPORTS = ("tmg_gemm", "tmg_gemm_ex", "tmg_gemm_host", "tmg_gemm_fused", "tmg_gemm_w4a8",
-           "tmg_gemm_w4a8_preshuffled", "tmg_w4a8_preshuffle", "tmg_w4a8_preshuffled_bytes", "tmg_gemm_mxfp4", "tmg_gemm_skinny_noalloc", "tmg_check", "tmg_last_error",
+           "tmg_gemm_w4a8_preshuffled", "tmg_w4a8_preshuffle", "tmg_w4a8_preshuffled_bytes", "tmg_gemm_mxfp4", "tmg_gemm_skinny_noalloc",
+           "tmg_moe_route", "tmg_moe_route_backward", "tmg_moe_combine", "tmg_moe_combine_backward",
+           "tmg_grouped_gemm", "tmg_grouped_gemm_wgrad", "tmg_linear", "tmg_linear_backward", "tmg_check", "tmg_last_error",
            "tmg_set_wait_budget_ns", "tmg_debug_wait_timeout", "tmg_debug_bounds_probe", "tmg_debug_build",
            "tmg_launch_count",
            "tmg_version", "tmg_shutdown")
@@ -41,6 +43,21 @@ class Layout(ctypes.Structure):
         ("shape", (ctypes.c_int64 * 2) * 2),
         ("stride", (ctypes.c_int64 * 2) * 2),
     ]
+
+
+def _struct(pointers, integers, enums):
+    return [(n, ctypes.c_void_p) for n in pointers.split()] + [(n, ctypes.c_int64) for n in integers.split()] + \
+        [(n, ctypes.c_int) for n in enums.split()]
+
+
+class GroupedArgs(ctypes.Structure):          # tmg_grouped_args
+    _fields_ = _struct("A B D offsets rows scale_a scale_b preact",
+                       "R N K E T lda a_col b_expert b_row b_col ldd ld_preact", "in_dtype activation")
+
+
+class LinearArgs(ctypes.Structure):           # tmg_linear_args
+    _fields_ = _struct("A B D scale_a scale_b bias residual preact",
+                       "M N K lda a_col b_row b_col ldd ld_residual ld_preact", "in_dtype activation")
 
 
 def make_layout(shape, stride) -> Layout:
@@ -106,6 +123,17 @@ def lib():
     L.tmg_gemm_mxfp4.restype = ctypes.c_int
     L.tmg_gemm_skinny_noalloc.argtypes = [P, P, P, I64, I64, I64, I64, I64, I64, P]
     L.tmg_gemm_skinny_noalloc.restype = ctypes.c_int
+    I = ctypes.c_int
+    for name, args in (("tmg_moe_route", [P, I64, I64, I64, I64, I, I, P, P, P, P, P, P]),
+                       ("tmg_moe_route_backward", [P, I64, I64, I64, I64, I, I, P, P, P, P]),
+                       ("tmg_moe_combine", [P, I64, I64, P, P, P, I64, P, I64, I64, I64, I64, P]),
+                       ("tmg_moe_combine_backward", [P, I64, P, I64, I64, P, P, P, P, I64, I64, I64, P]),
+                       ("tmg_grouped_gemm", [ctypes.POINTER(GroupedArgs), P]),
+                       ("tmg_grouped_gemm_wgrad", [P, I64, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, P]),
+                       ("tmg_linear", [ctypes.POINTER(LinearArgs), P]),
+                       ("tmg_linear_backward", [P, I64, P, I64, P, I64, P, I64, P, P, P, I64, I64, I64, I, P])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = I
     L.tmg_check.argtypes = [P]
     L.tmg_check.restype = ctypes.c_int
     L.tmg_last_error.argtypes = []

@@ -1,0 +1,133 @@
+// act_grad.cu — the elementwise part of the dense product's gradient:
+// dz = dD act'(z) rounded to bf16 for the two products that follow, and the
+// bias gradient, the column sums of the fp32 dz (before that rounding), added
+// up in a fixed order: rows of a chunk by one thread, then the chunks.
+#include <cuda_bf16.h>
+
+#include "act.cuh"
+#include "grouped.h"
+
+namespace tmg {
+namespace {
+
+constexpr int kRowsPerChunk = 64, kCols = 256;   // a block: 32 threads x 8 columns, 8 row lanes
+
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(256)
+    act_grad_kernel(const __nv_bfloat16 *__restrict__ dD, int64_t ldd, const __nv_bfloat16 *__restrict__ Z, int64_t ldp,
+                    int64_t M, int64_t N, __nv_bfloat16 *__restrict__ dz, float *__restrict__ partials)
+{
+    __shared__ float red[8][kCols];
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + tx * 8;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRowsPerChunk;
+    float sum[8] = {};
+    for (int64_t m = m0 + ty; m < min(M, m0 + kRowsPerChunk); m += 8) {
+        if (VEC) {
+            if (c >= N)
+                break;
+            const uint4 d = *reinterpret_cast<const uint4 *>(dD + m * ldd + c);
+            const uint32_t du[4] = {d.x, d.y, d.z, d.w};
+            uint32_t zu[4] = {}, ou[4];
+            if constexpr (ACT != kActNone) {
+                const uint4 z = *reinterpret_cast<const uint4 *>(Z + m * ldp + c);
+                zu[0] = z.x, zu[1] = z.y, zu[2] = z.z, zu[3] = z.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(du[i] << 16) * act_grad<ACT>(__uint_as_float(zu[i] << 16));
+                const float b = __uint_as_float(du[i] & 0xffff0000u) * act_grad<ACT>(__uint_as_float(zu[i] & 0xffff0000u));
+                sum[2 * i] += a;
+                sum[2 * i + 1] += b;
+                ou[i] = pack_bf16x2(a, b);
+            }
+            if (dz)
+                *reinterpret_cast<uint4 *>(dz + m * N + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < N) {
+                    float v = __bfloat162float(dD[m * ldd + c + i]);
+                    if constexpr (ACT != kActNone)
+                        v *= act_grad<ACT>(__bfloat162float(Z[m * ldp + c + i]));
+                    sum[i] += v;
+                    if (dz)
+                        dz[m * N + c + i] = __float2bfloat16_rn(v);
+                }
+        }
+    }
+    if (!partials)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        red[ty][tx * 8 + i] = sum[i];
+    __syncthreads();
+    const int64_t n = static_cast<int64_t>(blockIdx.y) * kCols + threadIdx.x;
+    if (n < N) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            v += red[w][threadIdx.x];
+        partials[static_cast<int64_t>(blockIdx.x) * N + n] = v;
+    }
+}
+
+__global__ void __launch_bounds__(256)
+    column_sum_kernel(const float *__restrict__ partials, int chunks, int64_t N, float *__restrict__ out)
+{
+    __shared__ float red[8][32];
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + tx;
+    float v = 0.f;
+    if (n < N)
+        for (int i = ty; i < chunks; i += 8)
+            v += partials[static_cast<int64_t>(i) * N + n];
+    red[ty][tx] = v;
+    __syncthreads();
+    if (ty == 0 && n < N) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            s += red[w][tx];
+        out[n] = s;
+    }
+}
+
+template <int ACT>
+cudaError_t launch_act(const void *dD, int64_t ldd, const void *Z, int64_t ldp, int64_t M, int64_t N, void *dz,
+                       float *partials, cudaStream_t s)
+{
+    auto ok = [](const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; };
+    const bool vec = N % 8 == 0 && ok(dD, ldd) && (ACT == kActNone || ok(Z, ldp)) && ok(dz, N);
+    const dim3 grid(static_cast<unsigned>(act_grad_chunks(M)), static_cast<unsigned>((N + kCols - 1) / kCols));
+    const __nv_bfloat16 *d = static_cast<const __nv_bfloat16 *>(dD), *z = static_cast<const __nv_bfloat16 *>(Z);
+    note_launch();
+    if (vec)
+        act_grad_kernel<ACT, true><<<grid, 256, 0, s>>>(d, ldd, z, ldp, M, N, static_cast<__nv_bfloat16 *>(dz), partials);
+    else
+        act_grad_kernel<ACT, false><<<grid, 256, 0, s>>>(d, ldd, z, ldp, M, N, static_cast<__nv_bfloat16 *>(dz), partials);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int act_grad_chunks(int64_t M) { return static_cast<int>((M + kRowsPerChunk - 1) / kRowsPerChunk); }
+
+cudaError_t launch_act_grad(const void *dD, int64_t ldd, const void *preact, int64_t ldp, int act, int64_t M, int64_t N,
+                            void *dz, float *partials, float *dbias, cudaStream_t s)
+{
+    cudaError_t e;
+    switch (act) {
+    case kActRelu: e = launch_act<kActRelu>(dD, ldd, preact, ldp, M, N, dz, dbias ? partials : nullptr, s); break;
+    case kActSilu: e = launch_act<kActSilu>(dD, ldd, preact, ldp, M, N, dz, dbias ? partials : nullptr, s); break;
+    case kActGelu: e = launch_act<kActGelu>(dD, ldd, preact, ldp, M, N, dz, dbias ? partials : nullptr, s); break;
+    default: e = launch_act<kActNone>(dD, ldd, preact, ldp, M, N, dz, dbias ? partials : nullptr, s); break;
+    }
+    if (e != cudaSuccess || !dbias)
+        return e;
+    note_launch();
+    column_sum_kernel<<<static_cast<unsigned>((N + 31) / 32), 256, 0, s>>>(partials, act_grad_chunks(M), N, dbias);
+    return cudaGetLastError();
+}
+
+}  // namespace tmg

@@ -28,8 +28,7 @@
 #include <string>
 #include <utility>
 
-#include "internal.h"
-#include "tmg.h"
+#include "host.h"
 
 namespace tmg {
 
@@ -42,12 +41,6 @@ std::atomic<uint64_t> g_budget_ns{2000000000ull};
 std::atomic<uint64_t> g_launches{0};
 std::mutex g_mu;
 
-struct DeviceState {
-    bool ready = false;
-    int num_sms = 0;
-    int cc_major = 0, cc_minor = 0;
-    uint32_t *err_word = nullptr;
-};
 std::map<int, DeviceState> g_dev;
 
 struct Scratch {
@@ -65,6 +58,8 @@ struct Scratch {
     size_t pack_bytes[3] = {0, 0, 0};
     void *host_ws[3] = {nullptr, nullptr, nullptr};  // tmg_gemm_host: device A, B, D
     size_t host_ws_bytes[3] = {0, 0, 0};
+    void *ws[kWsCount] = {};           // workspace()
+    size_t ws_bytes[kWsCount] = {};
     cudaStream_t copy_in = nullptr, copy_out = nullptr;
     static constexpr int kHostEvents = 2 + 3 * 16;
     cudaEvent_t ev[kHostEvents] = {};
@@ -77,9 +72,11 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+}  // namespace
+
 // TMG_LOG=1 (any value but "0"): one line on stderr per GEMM call naming the
 // kernel family, tile and schedule the dispatch chose.
-bool log_on()
+static bool log_on()
 {
     static const bool on = [] {
         const char *v = getenv("TMG_LOG");
@@ -88,7 +85,6 @@ bool log_on()
     return on;
 }
 
-void log_choice(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
 void log_choice(const char *fmt, ...)
 {
     if (!log_on())
@@ -101,7 +97,6 @@ void log_choice(const char *fmt, ...)
     fprintf(stderr, "tmg: %s\n", buf);
 }
 
-tmg_status fail(tmg_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 tmg_status fail(tmg_status st, const char *fmt, ...)
 {
     char buf[512];
@@ -112,6 +107,8 @@ tmg_status fail(tmg_status st, const char *fmt, ...)
     t_last_error = buf;
     return st;
 }
+
+void clear_error() { t_last_error.clear(); }
 
 tmg_status cuda_fail(cudaError_t e, const char *what)
 {
@@ -161,6 +158,8 @@ ErrCtx err_ctx(const DeviceState &ds)
 {
     return ErrCtx{ds.err_word, g_budget_ns.load()};
 }
+
+namespace {
 
 // ------------------------------------------------------------- layouts
 
@@ -303,6 +302,56 @@ tmg_status encode_2d(CUtensorMap *map, CUtensorMapDataType dt, int elem, const v
     g_maps.emplace(key, *map);
     return TMG_OK;
 }
+
+}  // namespace
+
+tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const int64_t *dims,
+                     const int64_t *strides, const int *box)
+{
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        es[i] = 1;
+        if (i + 1 < rank)
+            st[i] = static_cast<cuuint64_t>(strides[i]);
+    }
+    const CUresult r = g_encode(map, dt, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(TMG_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for a rank-%d operand", (int)r, rank);
+    return TMG_OK;
+}
+
+void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lk(g_mu);
+    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    cudaError_t e;
+    if (sc.ws_bytes[which] < bytes) {
+        if (sc.ws[which])
+            cudaFree(sc.ws[which]);
+        sc.ws[which] = nullptr;
+        sc.ws_bytes[which] = 0;
+        if ((e = cudaMalloc(&sc.ws[which], bytes)) != cudaSuccess) {
+            *st = cuda_fail(e, "cudaMalloc(workspace)");
+            return nullptr;
+        }
+        if (which == kWsCounters && (e = cudaMemsetAsync(sc.ws[which], 0, bytes, s)) != cudaSuccess) {
+            *st = cuda_fail(e, "cudaMemsetAsync(counters)");
+            return nullptr;
+        }
+        sc.ws_bytes[which] = bytes;
+    }
+    *st = TMG_OK;
+    return sc.ws[which];
+}
+
+namespace {
 
 // TMA limits: 16-byte aligned base, row stride a multiple of 16 bytes and
 // below 2^40, dimensions below 2^31 (kernel coordinates are int32).
@@ -1388,6 +1437,8 @@ tmg_status tmg_check(void *stream)
                     cudaMemset(kv.second.counters, 0, kv.second.counters_bytes);
                 if (kv.second.tc2_counters)
                     cudaMemset(kv.second.tc2_counters, 0, kv.second.tc2_counters_bytes);
+                if (kv.second.ws[kWsCounters])
+                    cudaMemset(kv.second.ws[kWsCounters], 0, kv.second.ws_bytes[kWsCounters]);
             }
         }
         cudaDeviceSynchronize();
@@ -1468,6 +1519,9 @@ void tmg_shutdown(void)
             if (q)
                 cudaFree(q);
         for (void *q : kv.second.host_ws)
+            if (q)
+                cudaFree(q);
+        for (void *q : kv.second.ws)
             if (q)
                 cudaFree(q);
         if (kv.second.copy_in) {

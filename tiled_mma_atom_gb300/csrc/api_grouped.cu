@@ -1,0 +1,402 @@
+// api_grouped.cu — C ABI of the routing, the expert-grouped products and the
+// dense product with the residual epilogue (include/tmg.h): argument checks
+// and launches.
+#include <cstring>
+#include <exception>
+
+#include "act.cuh"
+#include "grouped.h"
+#include "host.h"
+
+namespace tmg {
+namespace {
+
+constexpr int64_t kMax31 = (int64_t{1} << 31) - 1;
+
+// No C++ exception leaves a C entry point.
+template <class F>
+tmg_status guarded(F &&body)
+{
+    try {
+        clear_error();
+        return body();
+    } catch (const std::exception &x) {
+        return fail(TMG_ERR_CUDA, "host error: %s", x.what());
+    } catch (...) {
+        return fail(TMG_ERR_CUDA, "host error");
+    }
+}
+
+tmg_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? TMG_OK : cuda_fail(e, what); }
+
+// (a - 1) * b + ... of a strided operand must stay within int64.
+bool extents_ok(int64_t rows, int64_t row_stride, int64_t cols, int64_t col_stride, int64_t outer = 1, int64_t outer_stride = 0)
+{
+    if (row_stride < 0 || col_stride < 0 || outer_stride < 0)
+        return false;
+    const __int128 off = static_cast<__int128>(rows > 0 ? rows - 1 : 0) * row_stride +
+                         static_cast<__int128>(cols > 0 ? cols - 1 : 0) * col_stride +
+                         static_cast<__int128>(outer > 0 ? outer - 1 : 0) * outer_stride;
+    return off < (static_cast<__int128>(1) << 60);
+}
+
+// An output's rows must not overlap.
+bool out_rows_ok(int64_t rows, int64_t cols, int64_t ld) { return rows <= 1 || ld >= cols; }
+
+// Common checks of both products; the launch follows in run_product.
+tmg_status check_product(const GroupedArgs &a, int64_t a_col)
+{
+    if (a.R < 0 || a.N < 0 || a.K < 0 || a.T < 0)
+        return fail(TMG_ERR_INVALID_ARG, "negative extent R=%lld N=%lld K=%lld T=%lld", (long long)a.R, (long long)a.N,
+                    (long long)a.K, (long long)a.T);
+    if (a.R > kMax31 || a.N > kMax31 || a.K > kMax31 || a.T > kMax31)
+        return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+    if (!extents_ok(a.T, a.lda, a.K, a_col) || !extents_ok(a.N, a.b_row, a.K, a.b_col, a.E, a.b_expert) ||
+        !extents_ok(a.R, a.ldd, a.N, 1))
+        return fail(TMG_ERR_INVALID_ARG, "negative strides, or offsets beyond int64");
+    return TMG_OK;
+}
+
+tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, int64_t a_col, cudaStream_t s)
+{
+    return launched(launch_grouped_ffma(a, a_col, err_ctx(ds), s), "grouped FFMA launch");
+}
+
+}  // namespace
+}  // namespace tmg
+
+using namespace tmg;
+
+extern "C" {
+
+tmg_status tmg_moe_route(const void *logits, int64_t T, int64_t E, int64_t k, int64_t ld, tmg_dtype dtype, int normalize,
+                         float *weights, int32_t *experts, int32_t *offsets, int32_t *rows, int32_t *slots, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (dtype != TMG_F32 && dtype != TMG_BF16)
+            return fail(TMG_ERR_INVALID_ARG, "logits are fp32 or bf16 (dtype %d)", (int)dtype);
+        if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 16 || k > E)
+            return fail(TMG_ERR_INVALID_ARG, "routing needs T >= 0, 1 <= E <= 1024 and 1 <= k <= min(16, E) (T=%lld E=%lld "
+                        "k=%lld)", (long long)T, (long long)E, (long long)k);
+        if (T > 1 && ld < E)
+            return fail(TMG_ERR_INVALID_ARG, "row stride %lld below E=%lld", (long long)ld, (long long)E);
+        if (T * k > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "T * k beyond 2^31");
+        if (!offsets || (T > 0 && (!logits || !weights || !experts || !rows || !slots)))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (T == 0)
+            return launched(cudaMemsetAsync(offsets, 0, (E + 1) * sizeof(int32_t), s), "cudaMemsetAsync(offsets)");
+        RouteArgs a{};
+        a.logits = logits;
+        a.bf16 = dtype == TMG_BF16;
+        a.T = T;
+        a.ld = ld;
+        a.E = static_cast<int>(E);
+        a.k = static_cast<int>(k);
+        a.normalize = normalize != 0;
+        a.weights = weights;
+        a.experts = experts;
+        a.offsets = offsets;
+        a.rows = rows;
+        a.slots = slots;
+        a.counts = static_cast<int32_t *>(workspace(
+            kWsRoute, static_cast<size_t>(route_blocks(T, ds->num_sms)) * E * sizeof(int32_t), s, &st));
+        if (!a.counts)
+            return st;
+        return launched(launch_route(a, ds->num_sms, s), "routing launch");
+    });
+}
+
+tmg_status tmg_moe_route_backward(const void *logits, int64_t T, int64_t E, int64_t k, int64_t ld, tmg_dtype dtype,
+                                  int normalize, const int32_t *experts, const float *dweights, void *dlogits,
+                                  void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (dtype != TMG_F32 && dtype != TMG_BF16)
+            return fail(TMG_ERR_INVALID_ARG, "logits are fp32 or bf16 (dtype %d)", (int)dtype);
+        if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 16 || k > E)
+            return fail(TMG_ERR_INVALID_ARG, "routing needs T >= 0, 1 <= E <= 1024 and 1 <= k <= min(16, E) (T=%lld E=%lld "
+                        "k=%lld)", (long long)T, (long long)E, (long long)k);
+        if (T > 1 && ld < E)
+            return fail(TMG_ERR_INVALID_ARG, "row stride %lld below E=%lld", (long long)ld, (long long)E);
+        if (T == 0)
+            return TMG_OK;
+        if (T * k > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "T * k beyond 2^31");
+        if (!logits || !experts || !dweights || !dlogits)
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        return launched(launch_route_backward(logits, dtype == TMG_BF16, T, ld, static_cast<int>(E), static_cast<int>(k),
+                                              normalize != 0, experts, dweights, dlogits, ds->num_sms,
+                                              static_cast<cudaStream_t>(stream)),
+                        "routing gradient launch");
+    });
+}
+
+tmg_status tmg_moe_combine(const void *Y, int64_t R, int64_t ldy, const int32_t *slots, const float *weights,
+                           const void *residual, int64_t ldr, void *out, int64_t ldo, int64_t T, int64_t H, int64_t k,
+                           void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (T < 0 || H < 0 || R < 0 || k < 1 || k > 16)
+            return fail(TMG_ERR_INVALID_ARG, "combine needs T, H, R >= 0 and 1 <= k <= 16");
+        if (!extents_ok(R, ldy, H, 1) || !extents_ok(T, residual ? ldr : 0, H, 1) || !extents_ok(T, ldo, H, 1) ||
+            !out_rows_ok(T, H, ldo))
+            return fail(TMG_ERR_INVALID_ARG, "row strides out of range (the output's must be at least H)");
+        if (T == 0 || H == 0)
+            return TMG_OK;
+        if (T > kMax31 / 16 || H > kMax31 || T * ((H + 1023) / 1024) > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+        if (!slots || !out || (R > 0 && !Y))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        return launched(launch_combine(CombineArgs{Y, slots, weights, residual, out, T, H, R, ldy, ldr, ldo,
+                                                   static_cast<int>(k)},
+                                       static_cast<cudaStream_t>(stream)),
+                        "combine launch");
+    });
+}
+
+tmg_status tmg_moe_combine_backward(const void *dOut, int64_t ldo, const void *Y, int64_t R, int64_t ldy,
+                                    const int32_t *slots, const float *weights, void *dY, float *dweights, int64_t T,
+                                    int64_t H, int64_t k, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (T < 0 || H < 0 || R < 0 || k < 1 || k > 16)
+            return fail(TMG_ERR_INVALID_ARG, "combine needs T, H, R >= 0 and 1 <= k <= 16");
+        if (!extents_ok(R, dweights ? ldy : 0, H, 1) || !extents_ok(T, ldo, H, 1))
+            return fail(TMG_ERR_INVALID_ARG, "row strides out of range");
+        if (T == 0)
+            return TMG_OK;
+        if (T > kMax31 / 16 || H > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+        if (!slots || (H > 0 && !dOut) || (R > 0 && H > 0 && (!dY || (dweights && !Y))))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        return launched(launch_combine_backward(CombineGradArgs{dOut, Y, slots, weights, dY, dweights, T, H, R, ldo, ldy,
+                                                                static_cast<int>(k)},
+                                                static_cast<cudaStream_t>(stream)),
+                        "combine gradient launch");
+    });
+}
+
+tmg_status tmg_grouped_gemm(const tmg_grouped_args *g, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (!g)
+            return fail(TMG_ERR_INVALID_ARG, "null argument struct");
+        if (g->in_dtype == TMG_F32)
+            return fail(TMG_ERR_UNSUPPORTED, "the grouped product takes bf16 or E4M3 inputs");
+        if (g->in_dtype != TMG_BF16 && g->in_dtype != TMG_E4M3)
+            return fail(TMG_ERR_INVALID_ARG, "unknown input dtype %d", (int)g->in_dtype);
+        if (g->activation != TMG_ACT_NONE && g->activation != TMG_ACT_SWIGLU && g->activation != TMG_ACT_SWIGLU_GRAD)
+            return fail(TMG_ERR_INVALID_ARG, "activation %d is not one of the grouped product's", (int)g->activation);
+        if (g->E < 1 || g->E > 1024)
+            return fail(TMG_ERR_INVALID_ARG, "E=%lld is not in 1 .. 1024", (long long)g->E);
+        GroupedArgs a{};
+        a.A = g->A;
+        a.B = g->B;
+        a.D = g->D;
+        a.R = g->R;
+        a.T = g->rows ? g->T : g->R;
+        a.N = g->N;
+        a.K = g->K;
+        a.E = g->E;
+        a.lda = g->lda;
+        a.ldd = g->ldd;
+        a.b_expert = g->b_expert;
+        a.b_row = g->b_row;
+        a.b_col = g->b_col;
+        a.offsets = g->offsets;
+        a.rows = g->rows;
+        a.e4m3 = g->in_dtype == TMG_E4M3;
+        a.epi.scale_a = g->scale_a;
+        a.epi.scale_b = g->scale_b;
+        a.epi.preact = g->activation == TMG_ACT_NONE ? nullptr : g->preact;
+        a.epi.ld_preact = g->ld_preact;
+        a.epi.act = g->activation;
+        tmg_status st;
+        if ((st = check_product(a, g->a_col)) != TMG_OK)
+            return st;
+        const bool grad = g->activation == TMG_ACT_SWIGLU_GRAD;
+        if (g->activation == TMG_ACT_SWIGLU && g->N % 2)
+            return fail(TMG_ERR_INVALID_ARG, "swiglu needs an even N (N=%lld)", (long long)g->N);
+        const int64_t cols = grad ? 2 * g->N : a.out_n();
+        if (!out_rows_ok(g->R, cols, g->ldd))
+            return fail(TMG_ERR_INVALID_ARG, "row stride %lld of D below its %lld columns", (long long)g->ldd,
+                        (long long)cols);
+        if (grad && !g->preact && g->R > 0 && g->N > 0)
+            return fail(TMG_ERR_INVALID_ARG, "swiglu_grad reads preact, which is NULL");
+        if (a.epi.preact && (g->ld_preact < 0 || !out_rows_ok(g->R, grad ? 2 * g->N : g->N, g->ld_preact)))
+            return fail(TMG_ERR_INVALID_ARG, "row stride %lld of preact too small", (long long)g->ld_preact);
+        if (g->R == 0 || g->N == 0)
+            return TMG_OK;
+        if (!g->offsets || !g->D || (g->K > 0 && (!g->B || (a.T > 0 && !g->A))))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        return run_product(*ds, a, g->a_col, static_cast<cudaStream_t>(stream));
+    });
+}
+
+tmg_status tmg_grouped_gemm_wgrad(const void *dD, int64_t ldd, int64_t d_col, const void *A, int64_t lda, int64_t a_col,
+                                  void *dB, const int32_t *offsets, const int32_t *rows, int64_t R, int64_t N, int64_t K,
+                                  int64_t E, int64_t T, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (R < 0 || N < 0 || K < 0 || T < 0)
+            return fail(TMG_ERR_INVALID_ARG, "negative extent R=%lld N=%lld K=%lld T=%lld", (long long)R, (long long)N,
+                        (long long)K, (long long)T);
+        if (E < 1 || E > 1024)
+            return fail(TMG_ERR_INVALID_ARG, "E=%lld is not in 1 .. 1024", (long long)E);
+        if (R > kMax31 || N > kMax31 || K > kMax31 || T > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+        if (!rows)
+            T = R;
+        if (!extents_ok(R, ldd, N, d_col) || !extents_ok(T, lda, K, a_col))
+            return fail(TMG_ERR_INVALID_ARG, "negative strides, or offsets beyond int64");
+        if (N == 0 || K == 0)
+            return TMG_OK;
+        if (!dB || !offsets || (R > 0 && !dD) || (T > 0 && R > 0 && !A))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        const WgradArgs a{dD, A, dB, R, T, N, K, E, ldd, lda, offsets, rows};
+        return launched(launch_wgrad_ffma(a, d_col, a_col, err_ctx(*ds), static_cast<cudaStream_t>(stream)),
+                        "grouped weight gradient launch");
+    });
+}
+
+tmg_status tmg_linear(const tmg_linear_args *g, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (!g)
+            return fail(TMG_ERR_INVALID_ARG, "null argument struct");
+        if (g->in_dtype == TMG_F32)
+            return fail(TMG_ERR_UNSUPPORTED, "the dense product with the residual epilogue takes bf16 or E4M3 inputs");
+        if (g->in_dtype != TMG_BF16 && g->in_dtype != TMG_E4M3)
+            return fail(TMG_ERR_INVALID_ARG, "unknown input dtype %d", (int)g->in_dtype);
+        if (g->activation < TMG_ACT_NONE || g->activation > TMG_ACT_GELU)
+            return fail(TMG_ERR_INVALID_ARG, "activation %d is not one of the dense product's", (int)g->activation);
+        GroupedArgs a{};
+        a.A = g->A;
+        a.B = g->B;
+        a.D = g->D;
+        a.R = a.T = g->M;
+        a.N = g->N;
+        a.K = g->K;
+        a.E = 1;
+        a.lda = g->lda;
+        a.ldd = g->ldd;
+        a.b_row = g->b_row;
+        a.b_col = g->b_col;
+        a.e4m3 = g->in_dtype == TMG_E4M3;
+        a.epi = ProductEpi{g->scale_a, g->scale_b, g->bias, g->residual, g->preact, g->ld_residual, g->ld_preact,
+                           static_cast<int>(g->activation)};
+        tmg_status st;
+        if ((st = check_product(a, g->a_col)) != TMG_OK)
+            return st;
+        if (!out_rows_ok(g->M, g->N, g->ldd) || (g->preact && !out_rows_ok(g->M, g->N, g->ld_preact)) ||
+            (g->residual && !extents_ok(g->M, g->ld_residual, g->N, 1)))
+            return fail(TMG_ERR_INVALID_ARG, "row stride of D, preact or residual out of range");
+        if (g->M == 0 || g->N == 0)
+            return TMG_OK;
+        if (!g->D || (g->K > 0 && (!g->A || !g->B)))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        return run_product(*ds, a, g->a_col, static_cast<cudaStream_t>(stream));
+    });
+}
+
+tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, int64_t ldp, const void *A, int64_t lda,
+                               const void *B, int64_t ldb, void *dA, void *dB, float *dbias, int64_t M, int64_t N,
+                               int64_t K, tmg_activation activation, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (activation < TMG_ACT_NONE || activation > TMG_ACT_GELU)
+            return fail(TMG_ERR_INVALID_ARG, "activation %d is not one of the dense product's", (int)activation);
+        if (M < 0 || N < 0 || K < 0)
+            return fail(TMG_ERR_INVALID_ARG, "negative extent M=%lld N=%lld K=%lld", (long long)M, (long long)N,
+                        (long long)K);
+        if (M > kMax31 || N > kMax31 || K > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+        const bool act = activation != TMG_ACT_NONE;
+        if (!extents_ok(M, ldd, N, 1) || !extents_ok(M, act ? ldp : 0, N, 1) || !extents_ok(M, lda, K, 1) ||
+            !extents_ok(N, ldb, K, 1))
+            return fail(TMG_ERR_INVALID_ARG, "negative strides, or offsets beyond int64");
+        if (M > 0 && N > 0 && (!dD || (act && !preact)))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer (dD, or the preact that the activation's gradient reads)");
+        if ((dA && K > 0 && N > 0 && !B) || (dB && K > 0 && M > 0 && !A))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer: dA needs B, dB needs A");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const void *dz = dD;
+        int64_t ldz = ldd;
+        if (M > 0 && N > 0 && (act || dbias)) {
+            const size_t part = static_cast<size_t>(act_grad_chunks(M)) * N * sizeof(float);
+            const size_t grad = act ? static_cast<size_t>(M) * N * 2 : 0;
+            char *ws = static_cast<char *>(workspace(kWsGrad, (part + 255) / 256 * 256 + grad, s, &st));
+            if (!ws)
+                return st;
+            void *z = act ? ws + (part + 255) / 256 * 256 : nullptr;
+            if ((st = launched(launch_act_grad(dD, ldd, preact, ldp, activation, M, N, z, reinterpret_cast<float *>(ws),
+                                               dbias, s),
+                               "activation gradient launch")) != TMG_OK)
+                return st;
+            if (act) {
+                dz = z;
+                ldz = N;
+            }
+        } else if (dbias && N > 0) {
+            if ((st = launched(cudaMemsetAsync(dbias, 0, N * sizeof(float), s), "cudaMemsetAsync(dbias)")) != TMG_OK)
+                return st;
+        }
+        // dA (M, K) = dz (M, N) . B: B read as (K, N); dB (N, K) = dz^T . A
+        auto flat = [](int64_t r, int64_t c, int64_t sr, int64_t sc) {
+            tmg_layout L;
+            std::memset(&L, 0, sizeof L);
+            L.depth[0] = L.depth[1] = 1;
+            L.shape[0][0] = r;
+            L.shape[1][0] = c;
+            L.shape[0][1] = L.shape[1][1] = 1;
+            L.stride[0][0] = sr;
+            L.stride[1][0] = sc;
+            return L;
+        };
+        if (dA) {
+            const tmg_layout lz = flat(M, N, ldz, 1), lb = flat(K, N, 1, ldb);
+            if ((st = tmg_gemm_ex(dz, B, dA, M, K, N, TMG_BF16, &lz, &lb, nullptr, TMG_PATH_AUTO, stream)) != TMG_OK)
+                return st;
+        }
+        if (dB) {
+            const tmg_layout lz = flat(N, M, 1, ldz), la = flat(K, M, 1, lda);
+            if ((st = tmg_gemm_ex(dz, A, dB, N, K, M, TMG_BF16, &lz, &la, nullptr, TMG_PATH_AUTO, stream)) != TMG_OK)
+                return st;
+        }
+        return TMG_OK;
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,100 @@
+// grouped.h — arguments of the expert-grouped products and of the dense
+// product with the residual epilogue, as their kernels take them.
+#pragma once
+
+#include "internal.h"
+
+namespace tmg {
+
+// What follows the sum z = (A . B^T) in the epilogue, in fp32:
+//   z *= scale_a[row of A] * scale_b[n], z += bias[n]; preact = bf16(z);
+//   D = bf16(act(z) + residual).
+// swiglu: z has 2 F columns, D = silu(z[f]) z[F + f]; preact holds both halves.
+// swiglu_grad: z is the gradient of a SwiGLU result, preact (an input) holds
+// its two halves; D (2 F columns) their gradients.
+struct ProductEpi {
+    const float *scale_a;
+    const float *scale_b;      // (E, rows of B)
+    const float *bias;         // dense product only
+    const void *residual;      // bf16, dense product only
+    void *preact;              // bf16: written, or read by swiglu_grad
+    int64_t ld_residual, ld_preact;
+    int act;                   // kAct*
+};
+
+// D[r] = A[rows ? rows[r] : r] . B[e]^T for offsets[e] <= r < offsets[e + 1]
+// (offsets null: one group of all R rows).
+struct GroupedArgs {
+    const void *A, *B;
+    void *D;
+    int64_t R;                 // rows of D (and of A without `rows`)
+    int64_t T;                 // rows of A
+    int64_t N, K, E;           // rows of each expert's B, contraction, experts
+    int64_t lda, ldd;          // row strides, in elements; unit column strides
+    int64_t b_expert, b_row, b_col;
+    const int32_t *offsets, *rows;
+    bool e4m3;
+    ProductEpi epi;
+    // columns of the output tile grid: N, or F with swiglu
+    __host__ __device__ int64_t out_n() const { return epi.act == 4 ? N / 2 : N; }
+};
+
+// CUDA-core kernels: any strides, any sizes.
+cudaError_t launch_grouped_ffma(const GroupedArgs &a, int64_t a_col, const ErrCtx &err, cudaStream_t s);
+
+// dB[e][n][k] = sum over the rows r of group e of dD[r][n] A[rows ? rows[r] : r][k].
+struct WgradArgs {
+    const void *dD, *A;
+    void *dB;                  // (E, N, K) contiguous
+    int64_t R, T, N, K, E;
+    int64_t ldd, lda;
+    const int32_t *offsets, *rows;
+};
+cudaError_t launch_wgrad_ffma(const WgradArgs &a, int64_t d_col, int64_t a_col, const ErrCtx &err, cudaStream_t s);
+
+// ------------------------------------------------------------- routing
+struct RouteArgs {
+    const void *logits;
+    bool bf16;
+    int64_t T, ld;
+    int E, k;
+    bool normalize;
+    float *weights;
+    int32_t *experts, *offsets, *rows, *slots;
+    int32_t *counts;           // workspace: route_blocks() x E
+};
+int route_blocks(int64_t T, int num_sms);
+cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
+                                  const int32_t *experts, const float *dweights, void *dlogits, int num_sms,
+                                  cudaStream_t s);
+struct CombineArgs {
+    const void *Y;             // bf16 (R, H), row stride ldy
+    const int32_t *slots;      // (T, k)
+    const float *weights;      // (T, k) or null (ones)
+    const void *residual;      // bf16 (T, H) or null
+    void *out;                 // bf16 (T, H)
+    int64_t T, H, R, ldy, ldr, ldo;
+    int k;
+};
+cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
+struct CombineGradArgs {
+    const void *dOut, *Y;      // bf16 (T, H), (R, H)
+    const int32_t *slots;
+    const float *weights;      // or null (ones)
+    void *dY;                  // bf16 (R, H) contiguous
+    float *dweights;           // (T, k) or null
+    int64_t T, H, R, ldo, ldy;
+    int k;
+};
+cudaError_t launch_combine_backward(const CombineGradArgs &a, cudaStream_t s);
+
+// --------------------------------------- gradient of the dense product
+// dz = bf16(dD act'(preact)) (M, N) contiguous; column sums of the fp32 dz in
+// dbias through `partials` (act_grad_chunks(M) x N fp32).  act none: only the
+// sums (dz null).  dbias null: only dz.
+int act_grad_chunks(int64_t M);
+cudaError_t launch_act_grad(const void *dD, int64_t ldd, const void *preact, int64_t ldp, int act, int64_t M, int64_t N,
+                            void *dz, float *partials, float *dbias, cudaStream_t s);
+
+}  // namespace tmg
