@@ -393,8 +393,9 @@ typedef struct {
 } tmg_grouped_args;
 
 /* The grouped product.  Operands whose rows (for B: rows along K, or along N)
- * are contiguous and 16-byte aligned are read in place; others are copied
- * to workspace first (bf16; E4M3: UNSUPPORTED).  E <= 1024; R, N, K, T below
+ * are contiguous and 16-byte aligned (E4M3, SWIGLU: along K; SWIGLU also N/2 a
+ * multiple of 8) are read in place; others are copied to workspace first.
+ * E <= 1024; R, N, K, T below
  * 2^31; the offsets stay on the device.  K == 0 gives z = 0. */
 tmg_status tmg_grouped_gemm(const tmg_grouped_args *args, void *stream);
 

@@ -7,6 +7,8 @@
 #include "act.cuh"
 #include "grouped.h"
 #include "host.h"
+#include "swap_kernel.cuh"
+#include "wgrad.h"
 
 namespace tmg {
 namespace {
@@ -44,22 +46,219 @@ bool extents_ok(int64_t rows, int64_t row_stride, int64_t cols, int64_t col_stri
 bool out_rows_ok(int64_t rows, int64_t cols, int64_t ld) { return rows <= 1 || ld >= cols; }
 
 // Common checks of both products; the launch follows in run_product.
-tmg_status check_product(const GroupedArgs &a, int64_t a_col)
+tmg_status check_product(const GroupedArgs &a)
 {
     if (a.R < 0 || a.N < 0 || a.K < 0 || a.T < 0)
         return fail(TMG_ERR_INVALID_ARG, "negative extent R=%lld N=%lld K=%lld T=%lld", (long long)a.R, (long long)a.N,
                     (long long)a.K, (long long)a.T);
     if (a.R > kMax31 || a.N > kMax31 || a.K > kMax31 || a.T > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
-    if (!extents_ok(a.T, a.lda, a.K, a_col) || !extents_ok(a.N, a.b_row, a.K, a.b_col, a.E, a.b_expert) ||
+    if (!extents_ok(a.T, a.lda, a.K, a.a_col) || !extents_ok(a.N, a.b_row, a.K, a.b_col, a.E, a.b_expert) ||
         !extents_ok(a.R, a.ldd, a.N, 1))
         return fail(TMG_ERR_INVALID_ARG, "negative strides, or offsets beyond int64");
     return TMG_OK;
 }
 
-tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, int64_t a_col, cudaStream_t s)
+bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether TMA reads a (rows, cols) operand of `elem`-byte elements in place:
+// 16-byte aligned base and rows, positive strides below 2^40 bytes.
+bool rows_in_place(const void *p, int64_t rows, int64_t row, int64_t cols, int64_t col, int elem)
 {
-    return launched(launch_grouped_ffma(a, a_col, err_ctx(ds), s), "grouped FFMA launch");
+    return aligned(p) && cols > 0 && rows > 0 && (cols == 1 || col == 1) &&
+           (rows == 1 || (row > 0 && row * elem % 16 == 0 && row * elem < (int64_t{1} << 40)));
+}
+
+// A stride for a dimension of extent 1, where the caller's says nothing.
+int64_t stride_or(int64_t extent, int64_t stride, int64_t least) { return extent > 1 ? stride : least; }
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Copy an operand of E blocks (rows, K) to workspace `which` at `offset`
+// bytes of `total`.
+tmg_status pack(const DeviceState &ds, Workspace which, Pack3Args a, int elem, size_t total, int64_t offset, cudaStream_t s,
+                char **out)
+{
+    tmg_status st;
+    char *ws = static_cast<char *>(workspace(which, total < 16 ? 16 : total, s, &st));
+    if (!ws)
+        return st;
+    a.dst = ws + offset;
+    const cudaError_t e = launch_pack3(a, elem, ds.num_sms, s);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "operand copy launch");
+    *out = ws;
+    return TMG_OK;
+}
+
+tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t s)
+{
+    const bool swiglu = a.epi.act == kActSwiglu;
+    const int elem = a.e4m3 ? 1 : 2, align = 16 / elem, kb = a.e4m3 ? 128 : 64;
+    const int64_t halves = swiglu ? 2 : 1, F = a.N / halves;
+    const CUtensorMapDataType dt = a.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    tmg_status st;
+    SwapArgs p;
+    std::memset(&p, 0, sizeof p);
+    // the contraction that the kernel sees: an empty one is one of zeros, and
+    // a copied operand's rows are padded (the other's out-of-range reads are zeros)
+    const int64_t K = a.K > 0 ? a.K : align;
+
+    // A: rows of K
+    const void *A = a.A;
+    int64_t lda = stride_or(a.T, a.lda, up(K, align));
+    const int64_t T = a.T > 0 ? a.T : 1;
+    if (!rows_in_place(A, a.T, a.lda, a.K, a.a_col, elem)) {
+        lda = up(K, align);
+        char *ws;
+        if ((st = pack(ds, kWsPackA, Pack3Args{A, nullptr, 1, a.T, a.K, 0, a.lda, a.a_col, T, lda, 0}, elem, T * lda * elem,
+                       0, s, &ws)) != TMG_OK)
+            return st;
+        A = ws;
+    }
+    // B: K-major rows, MN-major rows (plain bf16), or a K-major copy
+    const void *B = a.B;
+    int64_t brow = a.b_row, bexp = a.b_expert, Fp = F;
+    const bool e_ok = a.E == 1 || (a.b_expert > 0 && a.b_expert * elem % 16 == 0 && a.b_expert * elem < (int64_t{1} << 40));
+    bool maj = false;
+    if (e_ok && (!swiglu || F % 8 == 0) && rows_in_place(B, a.N, a.b_row, a.K, a.b_col, elem)) {
+        brow = stride_or(a.N, a.b_row, up(K, align));
+    } else if (e_ok && !swiglu && !a.e4m3 && rows_in_place(B, a.K, a.b_col, a.N, a.b_row, elem)) {
+        maj = true;
+        brow = stride_or(a.K, a.b_col, up(a.N, align));
+    } else {
+        Fp = swiglu ? up(F, 8) : F;
+        brow = up(K, align);
+        bexp = halves * Fp * brow;
+        char *ws = nullptr;
+        for (int64_t h = 0; h < halves; ++h)
+            if ((st = pack(ds, kWsPackB,
+                           Pack3Args{static_cast<const char *>(a.B) + h * F * a.b_row * elem, nullptr, a.E, F, a.K, a.b_expert,
+                                     a.b_row, a.b_col, Fp, brow, bexp},
+                           elem, a.E * bexp * elem, h * Fp * brow * elem, s, &ws)) != TMG_OK)
+                return st;
+        B = ws;
+    }
+    bexp = stride_or(a.E, bexp, maj ? K * brow : halves * Fp * brow);
+
+    if (swiglu) {
+        const int64_t dims[5] = {K, 8, 2, Fp / 8, a.E}, strides[4] = {brow * elem, Fp * brow * elem, 8 * brow * elem, bexp * elem};
+        const int box[5] = {kb, 8, 2, 8, 1};
+        st = encode_nd(&p.tmW, dt, 5, B, dims, strides, box);
+    } else if (maj) {
+        const int64_t dims[3] = {a.N, K, a.E}, strides[2] = {brow * elem, bexp * elem};
+        const int box[3] = {64, 64, 1};
+        st = encode_nd(&p.tmW, dt, 3, B, dims, strides, box);
+    } else {
+        const int64_t dims[3] = {K, a.N, a.E}, strides[2] = {brow * elem, bexp * elem};
+        const int box[3] = {kb, 128, 1};
+        st = encode_nd(&p.tmW, dt, 3, B, dims, strides, box);
+    }
+    if (st != TMG_OK)
+        return st;
+    const int64_t xdims[2] = {K, T}, xstrides[1] = {lda * elem};
+    for (int i = 0; i < (a.rows ? 1 : 4); ++i) {
+        const int box[2] = {kb, a.rows ? 1 : 16 << i};
+        if ((st = encode_nd(&p.tmX[i], dt, 2, A, xdims, xstrides, box)) != TMG_OK)
+            return st;
+    }
+    p.D = a.D;
+    p.offsets = a.offsets;
+    p.rows = a.rows;
+    p.epi = a.epi;
+    p.ldd = a.ldd;
+    p.R = static_cast<int>(a.R);
+    p.T = static_cast<int>(T);
+    p.N = static_cast<int>(F);
+    p.K = static_cast<int>(K);
+    p.E = static_cast<int>(a.E);
+    p.maj = maj;
+    // Widest tile: all rows of an evenly filled group, with room for half as
+    // many again; narrower stages make a deeper ring.
+    const int64_t even = (a.R + a.E - 1) / a.E;
+    const int64_t room = a.E == 1 ? even : even + even / 2 + 8;
+    p.maxw = static_cast<int>(room >= kSwMaxW ? kSwMaxW : up(room, 32));
+    p.stage_bytes = 16384 + sw_box_rows(p.maxw / 2) * 128;
+    p.stages = kSwMaxStages;
+    while (sw_smem(p.stages, p.stage_bytes, p.E) > 232448)
+        --p.stages;
+    p.group = 16 * p.maxw * K * elem <= (int64_t{32} << 20) ? 16 : 8;
+    const int64_t tiles_n = (F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+    if ((a.R / 32 + a.E) * tiles_n > kMax31)
+        return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
+    const int pairs = ds.num_sms / 2;
+    p.split_cost = 8 + p.maxw * 24 / kSwMaxW;
+    if ((K + kb - 1) / kb > p.split_cost) {
+        p.partials = static_cast<float *>(workspace(kWsPartials, pairs * sw_partial_floats(p.maxw) * sizeof(float), s, &st));
+        if (!p.partials)
+            return st;
+        p.counters = static_cast<uint32_t *>(workspace(kWsCounters, static_cast<size_t>(pairs) * 32 * sizeof(uint32_t), s, &st));
+        if (!p.counters)
+            return st;
+    } else {
+        p.split_cost = -1;
+    }
+    const int epi = swiglu ? kSwSwiglu : a.epi.act == kActSwigluGrad ? kSwSwigluGrad : a.offsets ? kSwPlain : kSwDense;
+    log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s",
+               a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", p.R, (long long)a.N, (long long)a.K, p.E, 256, p.maxw,
+               p.stages, maj ? "MN-major" : "K-major", a.rows ? ", gathered rows" : "");
+    return launched(launch_swap(p, epi, a.e4m3, ds.num_sms, err_ctx(ds), s), "grouped product launch");
+}
+
+tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
+{
+    tmg_status st;
+    WgradTmaArgs p;
+    std::memset(&p, 0, sizeof p);
+    const void *op[2] = {a.dD, a.A};
+    const int64_t rows[2] = {a.R, a.T}, cols[2] = {a.N, a.K}, row[2] = {a.ldd, a.lda}, col[2] = {a.d_col, a.a_col};
+    CUtensorMap *maps[2][2] = {{&p.tmD, &p.tmDg}, {&p.tmA, &p.tmAg}};
+    for (int i = 0; i < 2; ++i) {
+        int64_t ld = stride_or(rows[i], row[i], up(cols[i], 8)), n = rows[i] > 0 ? rows[i] : 1;
+        if (!rows_in_place(op[i], rows[i], row[i], cols[i], col[i], 2)) {
+            ld = up(cols[i], 8);
+            char *ws;
+            if ((st = pack(ds, i ? kWsPackB : kWsPackA,
+                           Pack3Args{op[i], nullptr, 1, rows[i], cols[i], 0, row[i], col[i], n, ld, 0}, 2, n * ld * 2, 0, s,
+                           &ws)) != TMG_OK)
+                return st;
+            op[i] = ws;
+        }
+        const int64_t dims[2] = {cols[i], n}, strides[1] = {ld * 2};
+        for (int g = 0; g < 2; ++g) {
+            const int box[2] = {64, g ? 1 : 64};
+            if ((st = encode_nd(maps[i][g], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box)) != TMG_OK)
+                return st;
+        }
+    }
+    p.dB = a.dB;
+    p.offsets = a.offsets;
+    p.rows = a.rows;
+    p.R = static_cast<int>(a.R > 0 ? a.R : 1);
+    p.T = static_cast<int>(a.T > 0 ? a.T : 1);
+    p.N = static_cast<int>(a.N);
+    p.K = static_cast<int>(a.K);
+    p.E = static_cast<int>(a.E);
+    p.group = 8;
+    p.vec_ok = a.K % 8 == 0 && aligned(a.dB);
+    const int64_t per = ((a.N + 255) / 256) * ((a.K + 255) / 256);
+    if ((a.R / 64 + 2 * a.E) * per > kMax31)
+        return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tile blocks");
+    const int pairs = ds.num_sms / 2;
+    p.split_cost = 32;
+    if ((a.R + 63) / 64 > p.split_cost) {
+        p.partials = static_cast<float *>(workspace(kWsPartials, wgrad_partial_bytes(ds.num_sms), s, &st));
+        if (!p.partials)
+            return st;
+        p.counters = static_cast<uint32_t *>(workspace(kWsCounters, static_cast<size_t>(pairs) * 32 * sizeof(uint32_t), s, &st));
+        if (!p.counters)
+            return st;
+    } else {
+        p.split_cost = -1;
+    }
+    log_choice("bf16 grouped weight gradient: %d rows, N=%d K=%d E=%d -> wgrad_kernel: 256 x 256 tiles%s", p.R, p.N, p.K, p.E,
+               a.rows ? ", gathered rows" : "");
+    return launched(launch_wgrad(p, ds.num_sms, err_ctx(ds), s), "grouped weight gradient launch");
 }
 
 }  // namespace
@@ -217,6 +416,7 @@ tmg_status tmg_grouped_gemm(const tmg_grouped_args *g, void *stream)
         a.K = g->K;
         a.E = g->E;
         a.lda = g->lda;
+        a.a_col = g->a_col;
         a.ldd = g->ldd;
         a.b_expert = g->b_expert;
         a.b_row = g->b_row;
@@ -230,12 +430,12 @@ tmg_status tmg_grouped_gemm(const tmg_grouped_args *g, void *stream)
         a.epi.ld_preact = g->ld_preact;
         a.epi.act = g->activation;
         tmg_status st;
-        if ((st = check_product(a, g->a_col)) != TMG_OK)
+        if ((st = check_product(a)) != TMG_OK)
             return st;
         const bool grad = g->activation == TMG_ACT_SWIGLU_GRAD;
         if (g->activation == TMG_ACT_SWIGLU && g->N % 2)
             return fail(TMG_ERR_INVALID_ARG, "swiglu needs an even N (N=%lld)", (long long)g->N);
-        const int64_t cols = grad ? 2 * g->N : a.out_n();
+        const int64_t cols = grad ? 2 * g->N : g->activation == TMG_ACT_SWIGLU ? g->N / 2 : g->N;
         if (!out_rows_ok(g->R, cols, g->ldd))
             return fail(TMG_ERR_INVALID_ARG, "row stride %lld of D below its %lld columns", (long long)g->ldd,
                         (long long)cols);
@@ -250,7 +450,7 @@ tmg_status tmg_grouped_gemm(const tmg_grouped_args *g, void *stream)
         DeviceState *ds = nullptr;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
-        return run_product(*ds, a, g->a_col, static_cast<cudaStream_t>(stream));
+        return run_product(*ds, a, static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -278,9 +478,8 @@ tmg_status tmg_grouped_gemm_wgrad(const void *dD, int64_t ldd, int64_t d_col, co
         tmg_status st;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
-        const WgradArgs a{dD, A, dB, R, T, N, K, E, ldd, lda, offsets, rows};
-        return launched(launch_wgrad_ffma(a, d_col, a_col, err_ctx(*ds), static_cast<cudaStream_t>(stream)),
-                        "grouped weight gradient launch");
+        return run_wgrad(*ds, WgradArgs{dD, A, dB, R, T, N, K, E, ldd, d_col, lda, a_col, offsets, rows},
+                         static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -304,6 +503,7 @@ tmg_status tmg_linear(const tmg_linear_args *g, void *stream)
         a.K = g->K;
         a.E = 1;
         a.lda = g->lda;
+        a.a_col = g->a_col;
         a.ldd = g->ldd;
         a.b_row = g->b_row;
         a.b_col = g->b_col;
@@ -311,7 +511,7 @@ tmg_status tmg_linear(const tmg_linear_args *g, void *stream)
         a.epi = ProductEpi{g->scale_a, g->scale_b, g->bias, g->residual, g->preact, g->ld_residual, g->ld_preact,
                            static_cast<int>(g->activation)};
         tmg_status st;
-        if ((st = check_product(a, g->a_col)) != TMG_OK)
+        if ((st = check_product(a)) != TMG_OK)
             return st;
         if (!out_rows_ok(g->M, g->N, g->ldd) || (g->preact && !out_rows_ok(g->M, g->N, g->ld_preact)) ||
             (g->residual && !extents_ok(g->M, g->ld_residual, g->N, 1)))
@@ -323,7 +523,7 @@ tmg_status tmg_linear(const tmg_linear_args *g, void *stream)
         DeviceState *ds = nullptr;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
-        return run_product(*ds, a, g->a_col, static_cast<cudaStream_t>(stream));
+        return run_product(*ds, a, static_cast<cudaStream_t>(stream));
     });
 }
 

@@ -30,28 +30,31 @@ struct GroupedArgs {
     int64_t R;                 // rows of D (and of A without `rows`)
     int64_t T;                 // rows of A
     int64_t N, K, E;           // rows of each expert's B, contraction, experts
-    int64_t lda, ldd;          // row strides, in elements; unit column strides
+    int64_t lda, a_col, ldd;   // strides in elements; D has unit column stride
     int64_t b_expert, b_row, b_col;
     const int32_t *offsets, *rows;
     bool e4m3;
     ProductEpi epi;
-    // columns of the output tile grid: N, or F with swiglu
-    __host__ __device__ int64_t out_n() const { return epi.act == 4 ? N / 2 : N; }
 };
 
-// CUDA-core kernels: any strides, any sizes.
-cudaError_t launch_grouped_ffma(const GroupedArgs &a, int64_t a_col, const ErrCtx &err, cudaStream_t s);
+// Copy of an operand with 16-byte rows: dst[e][r][k], r < rows_p, k < Kp, of
+// src[e s_e + r s_row + k s_col]; zeros for r >= rows and k >= K.
+struct Pack3Args {
+    const void *src;
+    void *dst;
+    int64_t E, rows, K, s_e, s_row, s_col;
+    int64_t rows_p, Kp, d_e;
+};
+cudaError_t launch_pack3(const Pack3Args &a, int elem, int num_sms, cudaStream_t s);
 
 // dB[e][n][k] = sum over the rows r of group e of dD[r][n] A[rows ? rows[r] : r][k].
 struct WgradArgs {
     const void *dD, *A;
     void *dB;                  // (E, N, K) contiguous
     int64_t R, T, N, K, E;
-    int64_t ldd, lda;
+    int64_t ldd, d_col, lda, a_col;
     const int32_t *offsets, *rows;
 };
-cudaError_t launch_wgrad_ffma(const WgradArgs &a, int64_t d_col, int64_t a_col, const ErrCtx &err, cudaStream_t s);
-
 // ------------------------------------------------------------- routing
 struct RouteArgs {
     const void *logits;

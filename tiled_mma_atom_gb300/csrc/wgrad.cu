@@ -1,0 +1,460 @@
+// wgrad.cu — the weight gradient of the expert-grouped product on CTA pairs:
+// dB[e] (N, K) = dD_eᵀ · A_e, the contraction over the rows of group e.
+//
+// Both operands are stored with the contraction as their outer dimension, so
+// both are MN-major MMA operands: 64 x 64 boxes (64 rows of 128 bytes, 128-byte
+// swizzle).  A pair tile is 256 columns of dD by 256 (at the edge: 128) columns
+// of A.  A block of the contraction is 64 rows of the group.
+//
+// Groups end anywhere.  Rows past the end belong to the next group and may hold
+// NaN or infinities, so zeroing one operand is not enough; the last block of a
+// group reads both operands by TMA gathers of four rows each whose indices past
+// the end are out of range and read as zeros, up to the next multiple of 16
+// rows (one MMA step), and the steps beyond are not issued.  With `rows`, A is
+// read by gathers throughout, its row numbers fetched 256 at a time, one batch
+// ahead.  A group without rows is one such block of zeros: its tile is written
+// as zeros like any other.
+//
+// Schedule: every group has the same tiles (bands of `group` column tiles);
+// they go round robin, or, where the last wave would leave pairs idle for
+// longer than a split costs, the first tiles are cut into equal runs of blocks
+// and summed from fp32 partials in pair order.  Roles as in swap_kernel.cuh.
+#include "grouped.h"
+#include "tc2_kernel.cuh"
+#include "wgrad.h"
+
+namespace tmg {
+namespace {
+
+constexpr int kWgStages = 6;
+constexpr int kWgStageBytes = 32768;
+constexpr int kWgBars = (2 * kWgStages + 4) * 8 + 16 + 1024;      // barriers, TMEM address, abort flag, row numbers
+constexpr int64_t kWgPiece = 32 * 256;
+
+__host__ __device__ inline int wg_smem(int E) { return 1024 + kWgStages * kWgStageBytes + kWgBars + 8 * (E + 1); }
+
+__device__ __forceinline__ void tma_gather4_pair_to(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, const int4 &r)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+                 " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+                 : "memory");
+}
+
+// Blocks of a group's contraction (one of zeros for an empty group).
+__device__ __forceinline__ int wg_blocks(int rows) { return rows > 0 ? (rows + 63) / 64 : 1; }
+
+// The walk of a pair: its run of split blocks first, then whole tiles.
+struct WgWalk {
+    const int *off, *unit;        // group offsets; blocks before each group
+    int per, E, nclusters, total, next_tile;
+    int64_t u, u_end;
+    bool first;
+
+    __device__ WgWalk(int c, int nc, int sk, int64_t U, int total_, int per_, int E_, const int *off_, const int *unit_)
+        : off(off_), unit(unit_), per(per_), E(E_), nclusters(nc), total(total_), next_tile(sk + c), u(U * c / nc),
+          u_end(U * (c + 1) / nc), first(true)
+    {
+    }
+
+    __device__ int rows(int e) const { return max(off[e + 1] - off[e], 0); }
+
+    __device__ bool next(int &e, int &local, int &kb0, int &kb1, bool &partial, int &slot, int64_t &unit0, int &blocks)
+    {
+        if (u < u_end) {
+            int lo = 0, hi = E;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (unit[mid] <= u)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            e = lo;
+            blocks = wg_blocks(rows(e));
+            const int64_t in = u - unit[e];
+            local = static_cast<int>(in / blocks);
+            unit0 = unit[e] + static_cast<int64_t>(local) * blocks;
+            kb0 = static_cast<int>(u - unit0);
+            kb1 = static_cast<int>(min(static_cast<int64_t>(blocks), kb0 + (u_end - u)));
+            partial = kb0 != 0 || kb1 != blocks;
+            slot = first ? 0 : 1;
+            first = false;
+            u += kb1 - kb0;
+            return true;
+        }
+        if (next_tile >= total)
+            return false;
+        e = next_tile / per;
+        local = next_tile % per;
+        next_tile += nclusters;
+        blocks = wg_blocks(rows(e));
+        kb0 = 0;
+        kb1 = blocks;
+        partial = false;
+        slot = 0;
+        unit0 = 0;
+        return true;
+    }
+};
+
+__global__ void __launch_bounds__(320, 1) wgrad_kernel(const __grid_constant__ WgradTmaArgs p, ErrCtx err)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kWgStages * kWgStageBytes);
+    uint64_t *empty = full + kWgStages;
+    uint64_t *tfull = empty + kWgStages;
+    uint64_t *tempty = tfull + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *row_numbers = reinterpret_cast<int *>(tmem_slot + 4);
+    int *off = row_numbers + 256, *unit = off + p.E + 1;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+    const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
+
+    for (int i = threadIdx.x; i <= p.E; i += 320)
+        off[i] = min(max(__ldg(p.offsets + i), 0), p.R);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWgStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 16);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane < 4)
+        tma_prefetch_desc(lane == 0 ? &p.tmD : lane == 1 ? &p.tmA : lane == 2 ? &p.tmDg : &p.tmAg);
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    __syncthreads();
+    if (warp == 2) {                 // blocks before each group
+        int run = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < p.E ? wg_blocks(off[e + 1] - off[e]) * per : 0;
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o)
+                    inc += x;
+            }
+            if (e < p.E)
+                unit[e] = run + inc - n;
+            run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0)
+            unit[p.E] = run;
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int total = p.E * per, rem = total % nclusters;
+    int sk = 0;
+    int64_t U = 0;
+    if (rem && p.split_cost >= 0) {
+        const int take = rem + (total > nclusters ? nclusters : 0);
+        const int e = take / per, blocks = e < p.E ? wg_blocks(off[e + 1] - off[e]) : 0;
+        const int64_t units = unit[e] + static_cast<int64_t>(take % per) * blocks;
+        // blocks of a tile, on average, times the share of pairs idle in the last wave
+        if (static_cast<int64_t>(unit[p.E]) / total * (nclusters - rem) > static_cast<int64_t>(p.split_cost) * nclusters &&
+            units >= nclusters) {
+            sk = take;
+            U = units;
+        }
+    }
+    WgWalk walk(cluster, nclusters, sk, U, total, per, p.E, off, unit);
+    int e, local_tile, kb0, kb1, slot, blocks, tn, tk;
+    int64_t unit0;
+    bool partial;
+
+    if (warp == 0) {
+        // ---------------------------------------------- TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        while (ok && walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
+            tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
+            const int lo = off[e], hi = lo + walk.rows(e);
+            const int kcols = p.K - tk * 256 <= 128 ? 64 : 128;               // columns of A per CTA
+            const int n0 = tn * 256 + static_cast<int>(rank) * 128, k0 = tk * 256 + static_cast<int>(rank) * kcols;
+            const int abox = kcols / 64;
+            int next[8];
+            auto fetch = [&](int batch) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = lo + batch * 256 + 32 * j + lane;
+                    int v = p.T;
+                    if (r < hi) {
+                        v = __ldg(p.rows + r);
+                        v = v < 0 || v >= p.T ? p.T : v;
+                    }
+                    next[j] = v;
+                }
+            };
+            if (p.rows)
+                fetch(kb0 >> 2);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (p.rows && (kb == kb0 || (kb & 3) == 0)) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        row_numbers[32 * j + lane] = next[j];
+                    __syncwarp();
+                    if ((kb >> 2) * 4 + 4 < kb1)
+                        fetch((kb >> 2) + 1);
+                }
+                const int r0 = lo + kb * 64;
+                const int left = hi - r0;
+                const bool whole = left >= 64;
+                const int rows16 = whole ? 64 : (max(left, 1) + 15) & ~15;
+                if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                if (rank == 0)
+                    mbar_arrive_expect_tx_w(&full[stage], 2u * static_cast<uint32_t>((2 + abox) * rows16 * 128));
+                const uint32_t bar0 = mapa_shared(smem_u32(&full[stage]), 0);
+                uint8_t *sd = smem + stage * kWgStageBytes, *sa = sd + 16384;
+                const int g = lane & 15, b = lane >> 4;                       // a gather: box b, rows 4 g .. 4 g + 3
+                if (whole) {
+                    tma_load_2d_pair_w(sd, &p.tmD, bar0, n0, r0);
+                    tma_load_2d_pair_w(sd + kMnBoxBytes, &p.tmD, bar0, n0 + kMnBox, r0);
+                } else if (4 * g < rows16) {
+                    int4 r;
+                    r.x = 4 * g + 0 < left ? r0 + 4 * g + 0 : p.R;
+                    r.y = 4 * g + 1 < left ? r0 + 4 * g + 1 : p.R;
+                    r.z = 4 * g + 2 < left ? r0 + 4 * g + 2 : p.R;
+                    r.w = 4 * g + 3 < left ? r0 + 4 * g + 3 : p.R;
+                    tma_gather4_pair_to(smem_u32(sd) + b * kMnBoxBytes + g * 512, &p.tmDg, bar0, n0 + b * kMnBox, r);
+                }
+                __syncwarp();
+                if (whole && !p.rows) {
+                    tma_load_2d_pair_w(sa, &p.tmA, bar0, k0, r0);
+                    if (abox == 2)
+                        tma_load_2d_pair_w(sa + kMnBoxBytes, &p.tmA, bar0, k0 + kMnBox, r0);
+                } else if (4 * g < rows16 && b < abox) {
+                    int4 r;
+                    if (p.rows) {
+                        r = reinterpret_cast<const int4 *>(row_numbers)[(kb & 3) * 16 + g];
+                    } else {
+                        r.x = 4 * g + 0 < left ? r0 + 4 * g + 0 : p.T;
+                        r.y = 4 * g + 1 < left ? r0 + 4 * g + 1 : p.T;
+                        r.z = 4 * g + 2 < left ? r0 + 4 * g + 2 : p.T;
+                        r.w = 4 * g + 3 < left ? r0 + 4 * g + 3 : p.T;
+                    }
+                    tma_gather4_pair_to(smem_u32(sa) + b * kMnBoxBytes + g * 512, &p.tmAg, bar0, k0 + b * kMnBox, r);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == kWgStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        for (int i = 0; i < kWgStages && i < issued; ++i) {
+            int s = stage - 1 - i;
+            uint32_t ph = phase;
+            if (s < 0) {
+                s += kWgStages;
+                ph ^= 1u;
+            }
+            if (rank == 0)
+                mbar_wait_cluster(&full[s], ph, err, abort_flag, kSiteDrain);
+            mbar_wait_cluster(&empty[s], ph, err, abort_flag, kSiteDrain);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // -------------------------------------------- MMA issuer
+            int stage = 0;
+            uint32_t phase = 0;
+            int count = 0;
+            bool ok = true;
+            while (ok && walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
+                tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
+                const int rows = walk.rows(e);
+                const uint32_t idesc = idesc_bf16_major(256, p.K - tk * 256 <= 128 ? 128 : 256, 3);
+                const int acc = count & 1;
+                const uint32_t acc_phase = (count >> 1) & 1;
+                ++count;
+                if (!mbar_wait_cluster_warp(&tempty[acc], acc_phase ^ 1u, err, abort_flag, kSiteMmaTmemEmpty))
+                    break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * 256;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_cluster_warp(&full[stage], phase, err, abort_flag, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t s0 = smem_u32(smem + stage * kWgStageBytes);
+                    const uint64_t adesc = sdesc_mnmajor_sw128(s0), bdesc = sdesc_mnmajor_sw128(s0 + 16384);
+                    const int steps = min(4, (max(rows - kb * 64, 1) + 15) / 16);
+                    for (int k = 0; k < steps; ++k)
+                        mma_bf16_pair_w(d_tmem, adesc + k * (kMnKStepBytes >> 4), bdesc + k * (kMnKStepBytes >> 4), idesc,
+                                        (kb != kb0) || (k != 0));
+                    mma_commit_pair_w(&empty[stage], 0x3);
+                    if (++stage == kWgStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                mma_commit_pair_w(&tfull[acc], 0x3);
+            }
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        const int ew = warp - 2, half = ew / 4, q = warp & 3;
+        int count = 0;
+        const int64_t d_limit = static_cast<int64_t>(p.E) * p.N * p.K;
+        const int64_t p_limit = nclusters * 16 * kWgPiece;
+        while (walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
+            tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
+            const int acc = count & 1;
+            const uint32_t acc_phase = (count >> 1) & 1;
+            ++count;
+            const int width = p.K - tk * 256 <= 128 ? 128 : 256;
+            const int n = tn * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+            if (!mbar_wait_cluster(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull))
+                break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+            const int c1 = min(width / 32, (p.K - tk * 256 + 31) / 32);       // chunks with columns
+            bool finish = !partial;
+            int c_first = 0, c_last = 0;
+            if (partial) {
+                const int64_t mine = ((static_cast<int64_t>(2 * cluster + slot) * 2 + rank) * 4 + q) * kWgPiece;
+#pragma unroll 1
+                for (int c = half; c < c1; c += 2) {
+                    uint32_t r[32];
+                    tmem_ld32(tbase + c * 32, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int64_t at = mine + ((c * 8 + j) * 32 + lane) * 4;
+                        if (span_ok(at, 4, p_limit, err, kBndPartials))
+                            *reinterpret_cast<uint4 *>(p.partials + at) =
+                                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+                if (half < c1) {
+                    __threadfence();
+                    __syncwarp();
+                    c_first = unit_owner(unit0, U, nclusters);
+                    c_last = unit_owner(unit0 + blocks - 1, U, nclusters);
+                    const int64_t at = ((static_cast<int64_t>(e) * per + local_tile) * 2 + rank) * 8 + ew;
+                    uint32_t old = 0;
+                    if (lane == 0 && bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters))
+                        old = atomicAdd(p.counters + at, 1u);
+                    old = __shfl_sync(0xffffffffu, old, 0);
+                    finish = old == static_cast<uint32_t>(c_last - c_first);
+                    if (finish) {
+                        __threadfence();
+                        if (lane == 0)
+                            p.counters[at] = 0;
+                    }
+                }
+            }
+            if (finish) {
+                const int64_t row_off = (static_cast<int64_t>(e) * p.N + n) * p.K;
+                __nv_bfloat16 *drow = static_cast<__nv_bfloat16 *>(p.dB) + row_off;
+#pragma unroll 1
+                for (int c = half; c < c1; c += 2) {
+                    float v[32];
+                    if (!partial) {
+                        uint32_t r[32];
+                        tmem_ld32(tbase + c * 32, r);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __uint_as_float(r[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = 0.f;
+                        for (int cc = c_first; cc <= c_last; ++cc) {
+                            const int s2 = U * cc / nclusters >= unit0 ? 0 : 1;       // its run begins in this tile
+                            const int64_t src = ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * kWgPiece;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int64_t at = src + ((c * 8 + j) * 32 + lane) * 4;
+                                if (!span_ok(at, 4, p_limit, err, kBndPartials))
+                                    continue;
+                                const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.partials + at));
+                                v[4 * j] += f.x;
+                                v[4 * j + 1] += f.y;
+                                v[4 * j + 2] += f.z;
+                                v[4 * j + 3] += f.w;
+                            }
+                        }
+                    }
+                    const int col0 = tk * 256 + c * 32;
+                    if (n < p.N && span_ok(row_off + col0, min(32, p.K - col0), d_limit, err, kBndStoreD))
+                        store_row_chunk(drow, col0, p.K, p.vec_ok, v);
+                }
+            }
+            if (!partial) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+}  // namespace
+
+size_t wgrad_partial_bytes(int num_sms) { return static_cast<size_t>(num_sms / 2) * 16 * kWgPiece * sizeof(float); }
+
+cudaError_t launch_wgrad(const WgradTmaArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
+{
+    const int smem = wg_smem(a.E);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(wgrad_kernel), smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms / 2));
+    cfg.blockDim = dim3(320);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    note_launch();
+    e = cudaLaunchKernelEx(&cfg, wgrad_kernel, a, err);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace tmg

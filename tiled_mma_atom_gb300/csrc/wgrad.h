@@ -1,0 +1,23 @@
+// wgrad.h — arguments of the grouped weight gradient's tensor-core kernel.
+#pragma once
+
+#include "internal.h"
+
+namespace tmg {
+
+struct WgradTmaArgs {
+    CUtensorMap tmD, tmA;      // dD (R, N) and A (T, K), boxes of 64 columns x 64 rows
+    CUtensorMap tmDg, tmAg;    // the same, boxes of 64 columns x 1 row (gathers)
+    void *dB;                  // (E, N, K) contiguous
+    const int32_t *offsets, *rows;
+    int R, T, N, K, E;
+    int group;                 // column tiles of dD per band
+    int split_cost;            // cost of a split in blocks of 64 rows; < 0: never split
+    int vec_ok;
+    float *partials;           // wgrad_partial_bytes()
+    uint32_t *counters;        // 16 per tile of two waves
+};
+size_t wgrad_partial_bytes(int num_sms);
+cudaError_t launch_wgrad(const WgradTmaArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s);
+
+}  // namespace tmg
