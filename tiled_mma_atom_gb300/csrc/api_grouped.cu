@@ -91,6 +91,24 @@ tmg_status pack(const DeviceState &ds, Workspace which, Pack3Args a, int elem, s
     return TMG_OK;
 }
 
+// A's rows by number into workspace, rows of K elements: *A and *lda become the
+// copy's.
+tmg_status gather(const DeviceState &ds, const void **A, int64_t *lda, int64_t src_rows, int64_t K, int elem,
+                  const int32_t *numbers, int64_t R, cudaStream_t s)
+{
+    const int64_t ld = up(K, 16 / elem);
+    tmg_status st;
+    void *ws = workspace(kWsGather, static_cast<size_t>(R > 0 ? R : 1) * ld * elem, s, &st);
+    if (!ws)
+        return st;
+    const cudaError_t e = launch_gather_rows(*A, *lda * elem, src_rows, K * elem, numbers, R, ws, ld * elem, ds.num_sms, s);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "row gather launch");
+    *A = ws;
+    *lda = ld;
+    return TMG_OK;
+}
+
 tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t s)
 {
     const bool swiglu = a.epi.act == kActSwiglu;
@@ -104,18 +122,29 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     // a copied operand's rows are padded (the other's out-of-range reads are zeros)
     const int64_t K = a.K > 0 ? a.K : align;
 
-    // A: rows of K
+    // Widest tile: all rows of an evenly filled group, with room for half as
+    // many again; narrower stages make a deeper ring.
+    const int64_t even = (a.R + a.E - 1) / a.E;
+    const int64_t room = a.E == 1 ? even : even + even / 2 + 8;
+    p.maxw = static_cast<int>(room >= kSwMaxW ? kSwMaxW : up(room, 32));
+    p.gather = a.rows && p.maxw <= kSwGatherW;
+
+    // A: rows of K read in place, or copied; with row numbers and wide tiles,
+    // gathered into workspace
     const void *A = a.A;
-    int64_t lda = stride_or(a.T, a.lda, up(K, align));
-    const int64_t T = a.T > 0 ? a.T : 1;
+    int64_t lda = stride_or(a.T, a.lda, up(K, align)), T = a.T > 0 ? a.T : 1;
+    char *ws = nullptr;
     if (!rows_in_place(A, a.T, a.lda, a.K, a.a_col, elem)) {
         lda = up(K, align);
-        char *ws;
-        if ((st = pack(ds, kWsPackA, Pack3Args{A, nullptr, 1, a.T, a.K, 0, a.lda, a.a_col, T, lda, 0}, elem, T * lda * elem,
-                       0, s, &ws)) != TMG_OK)
+        if ((st = pack(ds, kWsPackA, Pack3Args{A, nullptr, 1, a.T, a.K, 0, a.lda, a.a_col, T, lda, 0}, elem, T * lda * elem, 0,
+                       s, &ws)) != TMG_OK)
             return st;
         A = ws;
     }
+    if (a.rows && !p.gather && (st = gather(ds, &A, &lda, T, K, elem, a.rows, a.R, s)) != TMG_OK)
+        return st;
+    if (a.rows && !p.gather)
+        T = a.R;
     // B: K-major rows, MN-major rows (plain bf16), or a K-major copy
     const void *B = a.B;
     int64_t brow = a.b_row, bexp = a.b_expert, Fp = F;
@@ -130,7 +159,6 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
         Fp = swiglu ? up(F, 8) : F;
         brow = up(K, align);
         bexp = halves * Fp * brow;
-        char *ws = nullptr;
         for (int64_t h = 0; h < halves; ++h)
             if ((st = pack(ds, kWsPackB,
                            Pack3Args{static_cast<const char *>(a.B) + h * F * a.b_row * elem, nullptr, a.E, F, a.K, a.b_expert,
@@ -157,8 +185,8 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     if (st != TMG_OK)
         return st;
     const int64_t xdims[2] = {K, T}, xstrides[1] = {lda * elem};
-    for (int i = 0; i < (a.rows ? 1 : 4); ++i) {
-        const int box[2] = {kb, a.rows ? 1 : 16 << i};
+    for (int i = 0; i < (p.gather ? 1 : 4); ++i) {
+        const int box[2] = {kb, p.gather ? 1 : 16 << i};
         if ((st = encode_nd(&p.tmX[i], dt, 2, A, xdims, xstrides, box)) != TMG_OK)
             return st;
     }
@@ -168,16 +196,12 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     p.epi = a.epi;
     p.ldd = a.ldd;
     p.R = static_cast<int>(a.R);
-    p.T = static_cast<int>(T);
+    p.T = static_cast<int>(a.T);
+    p.map_rows = static_cast<int>(T);
     p.N = static_cast<int>(F);
     p.K = static_cast<int>(K);
     p.E = static_cast<int>(a.E);
     p.maj = maj;
-    // Widest tile: all rows of an evenly filled group, with room for half as
-    // many again; narrower stages make a deeper ring.
-    const int64_t even = (a.R + a.E - 1) / a.E;
-    const int64_t room = a.E == 1 ? even : even + even / 2 + 8;
-    p.maxw = static_cast<int>(room >= kSwMaxW ? kSwMaxW : up(room, 32));
     p.stage_bytes = 16384 + sw_box_rows(p.maxw / 2) * 128;
     p.stages = kSwMaxStages;
     while (sw_smem(p.stages, p.stage_bytes, p.E) > 232448)
@@ -201,7 +225,7 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     const int epi = swiglu ? kSwSwiglu : a.epi.act == kActSwigluGrad ? kSwSwigluGrad : a.offsets ? kSwPlain : kSwDense;
     log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s",
                a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", p.R, (long long)a.N, (long long)a.K, p.E, 256, p.maxw,
-               p.stages, maj ? "MN-major" : "K-major", a.rows ? ", gathered rows" : "");
+               p.stages, maj ? "MN-major" : "K-major", p.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "");
     return launched(launch_swap(p, epi, a.e4m3, ds.num_sms, err_ctx(ds), s), "grouped product launch");
 }
 
@@ -212,30 +236,32 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
     std::memset(&p, 0, sizeof p);
     const void *op[2] = {a.dD, a.A};
     const int64_t rows[2] = {a.R, a.T}, cols[2] = {a.N, a.K}, row[2] = {a.ldd, a.lda}, col[2] = {a.d_col, a.a_col};
-    CUtensorMap *maps[2][2] = {{&p.tmD, &p.tmDg}, {&p.tmA, &p.tmAg}};
     for (int i = 0; i < 2; ++i) {
         int64_t ld = stride_or(rows[i], row[i], up(cols[i], 8)), n = rows[i] > 0 ? rows[i] : 1;
         if (!rows_in_place(op[i], rows[i], row[i], cols[i], col[i], 2)) {
             ld = up(cols[i], 8);
-            char *ws;
+            char *ws = nullptr;
             if ((st = pack(ds, i ? kWsPackB : kWsPackA,
                            Pack3Args{op[i], nullptr, 1, rows[i], cols[i], 0, row[i], col[i], n, ld, 0}, 2, n * ld * 2, 0, s,
                            &ws)) != TMG_OK)
                 return st;
             op[i] = ws;
         }
-        const int64_t dims[2] = {cols[i], n}, strides[1] = {ld * 2};
-        for (int g = 0; g < 2; ++g) {
-            const int box[2] = {64, g ? 1 : 64};
-            if ((st = encode_nd(maps[i][g], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box)) != TMG_OK)
+        if (i && a.rows) {
+            if ((st = gather(ds, &op[i], &ld, n, cols[i], 2, a.rows, a.R, s)) != TMG_OK)
                 return st;
+            n = a.R > 0 ? a.R : 1;
         }
+        const int64_t dims[2] = {cols[i], n}, strides[1] = {ld * 2};
+        const int box[2] = {64, 64};
+        if ((st = encode_nd(i ? &p.tmA : &p.tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box)) != TMG_OK)
+            return st;
+        (i ? p.A : p.dD) = static_cast<const uint16_t *>(op[i]);
+        (i ? p.lda : p.ldd) = ld;
     }
     p.dB = a.dB;
     p.offsets = a.offsets;
-    p.rows = a.rows;
-    p.R = static_cast<int>(a.R > 0 ? a.R : 1);
-    p.T = static_cast<int>(a.T > 0 ? a.T : 1);
+    p.R = static_cast<int>(a.R);
     p.N = static_cast<int>(a.N);
     p.K = static_cast<int>(a.K);
     p.E = static_cast<int>(a.E);
@@ -257,7 +283,7 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
         p.split_cost = -1;
     }
     log_choice("bf16 grouped weight gradient: %d rows, N=%d K=%d E=%d -> wgrad_kernel: 256 x 256 tiles%s", p.R, p.N, p.K, p.E,
-               a.rows ? ", gathered rows" : "");
+               a.rows ? ", rows gathered first" : "");
     return launched(launch_wgrad(p, ds.num_sms, err_ctx(ds), s), "grouped weight gradient launch");
 }
 

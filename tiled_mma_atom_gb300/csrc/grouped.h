@@ -46,6 +46,11 @@ struct Pack3Args {
     int64_t rows_p, Kp, d_e;
 };
 cudaError_t launch_pack3(const Pack3Args &a, int elem, int num_sms, cudaStream_t s);
+// dst[r] = src[numbers[r]] (zeros where that is not one of src_rows): rows of
+// `bytes` bytes, all addresses and strides multiples of 16, dst zero-padded to
+// dst_stride.
+cudaError_t launch_gather_rows(const void *src, int64_t stride, int64_t src_rows, int64_t bytes, const int32_t *numbers,
+                               int64_t rows, void *dst, int64_t dst_stride, int num_sms, cudaStream_t s);
 
 // dB[e][n][k] = sum over the rows r of group e of dD[r][n] A[rows ? rows[r] : r][k].
 struct WgradArgs {

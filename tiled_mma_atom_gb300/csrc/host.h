@@ -41,6 +41,7 @@ tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const v
 enum Workspace {
     kWsPackA,          // operand copies with 16-byte rows
     kWsPackB,
+    kWsGather,         // rows gathered by number
     kWsPartials,       // fp32 partial tiles of split contractions
     kWsCounters,       // arrival counters: zero on entry, zero again on exit
     kWsRoute,          // per-block expert counts of the routing plan

@@ -2,7 +2,8 @@
 // read in place (unaligned or broadcast rows, strides in both directions, an
 // empty contraction) copied to workspace: dst[e][r][k], rows of Kp elements,
 // zero-padded past `rows` and K.  32 x 32 tiles through shared memory: reads
-// run along the source's smaller stride, writes along k.
+// run along the source's smaller stride, writes along k.  And the gather of
+// rows by number, for products whose tiles are too wide for TMA gathers.
 #include "grouped.h"
 
 namespace tmg {
@@ -33,7 +34,55 @@ __global__ void __launch_bounds__(256) pack3_kernel(Pack3Args a, int64_t tiles_k
     }
 }
 
+// Rows in 16-byte pieces: dst[r] = src[numbers[r]], zeros where that is no row
+// and past the row's bytes.  Four pieces per thread in flight.
+__global__ void __launch_bounds__(256)
+    gather_rows_kernel(const char *__restrict__ src, int64_t stride, int64_t src_rows, int bytes,
+                       const int32_t *__restrict__ numbers, int64_t rows, char *__restrict__ dst, int64_t dst_stride)
+{
+    const int64_t pieces = dst_stride / 16, total = rows * pieces, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t at = i + j * step, r = at / pieces;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (at >= total)
+                continue;
+            const int64_t from = __ldg(numbers + r), b = at % pieces * 16;
+            if (from < 0 || from >= src_rows || b >= bytes)
+                continue;
+            const char *p = src + from * stride + b;
+            if (b + 16 <= bytes) {
+                v[j] = __ldg(reinterpret_cast<const uint4 *>(p));
+            } else {
+                uint32_t w[4] = {};
+                for (int c = 0; b + c < bytes; ++c)
+                    w[c / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[c])) << (8 * (c & 3));
+                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * step < total)
+                reinterpret_cast<uint4 *>(dst)[i + j * step] = v[j];
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_gather_rows(const void *src, int64_t stride, int64_t src_rows, int64_t bytes, const int32_t *numbers,
+                               int64_t rows, void *dst, int64_t dst_stride, int num_sms, cudaStream_t s)
+{
+    const int64_t total = rows * (dst_stride / 16), blocks = (total + 1023) / 1024;
+    if (total == 0)
+        return cudaSuccess;
+    note_launch();
+    gather_rows_kernel<<<static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8), 256, 0, s>>>(
+        static_cast<const char *>(src), stride, src_rows, static_cast<int>(bytes), numbers, rows, static_cast<char *>(dst),
+        dst_stride);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_pack3(const Pack3Args &a, int elem, int num_sms, cudaStream_t s)
 {

@@ -20,8 +20,11 @@
 // neighbour's values never enter.  For SwiGLU a 5-D map (K, 8, 2, F/8, E)
 // lays eight gate rows and their eight up rows next to each other in the tile,
 // so gate and up of one column end in the same thread.  A: boxes of 16 to 128
-// rows, or, with `rows`, TMA gathers of four rows each (an index out of range
-// reads zeros), so no gathered copy of the tokens is made.  Rows of the next
+// rows, or, with `gather`, TMA gathers of four named rows each (an index out of
+// range reads zeros).  A gather takes 46 ns of an SM's TMA unit, so this is for
+// tiles of at most 64 rows (8 gathers a K block and CTA, the 0.37 us that the
+// block's weights take from HBM); for wider tiles the caller copies the rows
+// first (65528 x 2048 x 2048: 1263 us gathered here, COPY_US copied).  Rows of the next
 // group that a box brings along give columns that no one reads.
 //
 // Roles per CTA (ten warps): 0 TMA producer, 1 MMA issuer (CTA 0 of the pair)
@@ -50,6 +53,8 @@ struct SwapArgs {
     int64_t ldd;
     int R, T, N, K, E;         // N: output columns of the tile grid (F with SwiGLU)
     int maj;                   // weights MN-major
+    int gather;                // row r of D is row rows[r] of the map (else its own row)
+    int map_rows;              // rows of the map
     int maxw;                  // widest tile, a multiple of 32
     int stages, stage_bytes;
     int group;                 // row tiles per band
@@ -63,7 +68,8 @@ constexpr int kSwMaxW = 256;
 __host__ __device__ inline int64_t sw_partial_floats(int maxw) { return 2ll * 2 * 4 * 32 * maxw; }
 constexpr int kSwStaging = 8 * 2048;
 constexpr int kSwMaxStages = 12;
-constexpr int kSwBars = (2 * kSwMaxStages + 4) * 8 + 16 + 512;       // barriers, TMEM address, abort flag, row numbers
+constexpr int kSwGatherW = 64;       // widest tile with gathers
+constexpr int kSwBars = (2 * kSwMaxStages + 4) * 8 + 16 + kSwGatherW * 2;  // barriers, TMEM address, abort flag, row numbers
 __host__ __device__ inline int sw_box_rows(int half) { return half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128; }
 __host__ inline int sw_smem(int stages, int stage_bytes, int E)
 {
@@ -222,30 +228,38 @@ __device__ __forceinline__ void put_frag(uint32_t base, int lane, const uint32_t
     __syncwarp();
 }
 
-// 32 rows x 32 columns of a row-major matrix as fragment words; zeros outside.
-__device__ __forceinline__ void get_frag(uint32_t base, int lane, uint32_t (&w)[16], const __nv_bfloat16 *M, int64_t ld,
-                                         int64_t r0, int nt, int n0, int cols)
+// 32 rows x 32 columns of a row-major matrix, zeros outside, in two steps:
+// the loads (four 16-byte pieces per lane, issued early), and the way through
+// the staging tile to fragment words.
+__device__ __forceinline__ void load_rows(uint4 (&v)[4], int lane, const __nv_bfloat16 *M, int64_t ld, int64_t r0, int nt,
+                                          int n0, int cols)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int u = i * 32 + lane, row = u / 4, piece = u % 4;
-        const int n = n0 + piece * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
+        const int u = i * 32 + lane, row = u / 4;
+        const int n = n0 + u % 4 * 8;
+        v[i] = make_uint4(0, 0, 0, 0);
         if (row < nt && n < cols) {
             const __nv_bfloat16 *p = M + (r0 + row) * ld + n;
             if (n + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-                v = *reinterpret_cast<const uint4 *>(p);
+                v[i] = *reinterpret_cast<const uint4 *>(p);
             } else {
                 uint32_t u4[4] = {};
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (n + j < cols)
                         u4[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[j]) << (16 * (j & 1));
-                v = make_uint4(u4[0], u4[1], u4[2], u4[3]);
+                v[i] = make_uint4(u4[0], u4[1], u4[2], u4[3]);
             }
         }
-        sts128(stage_addr<32>(base, row, piece), v);
     }
+}
+
+__device__ __forceinline__ void rows_frag(uint32_t base, int lane, const uint4 (&v)[4], uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sts128(stage_addr<32>(base, (i * 32 + lane) / 4, lane % 4), v[i]);
     __syncwarp();
 #pragma unroll
     for (int g = 0; g < 4; ++g)
@@ -271,11 +285,31 @@ __device__ __forceinline__ void pack_frag(const float (&v)[32], uint32_t (&w)[16
 // One 32-row x 32-lane chunk of a finished sum: the epilogue and the stores.
 // n0: the first output column of the warp's lanes (SwiGLU: 16 columns);
 // sb: scale_b of this thread's four lanes (index 2 h + s), bias likewise;
-// sa_lane: scale_a of row `lane` of the chunk.
+// sa_lane: scale_a of row `lane` of the chunk; pre: the chunk's residual, or the
+// two halves of preact that swiglu_grad reads.
+struct EpiReads {
+    uint4 a[4], b[4];
+};
+
+// Issue a chunk's epilogue reads (ahead of the sum that they meet).
 template <int EPI>
+__device__ __forceinline__ void read_ahead(const SwapArgs &p, EpiReads &pre, int lane, int64_t r0, int nt, int n0)
+{
+    if constexpr (EPI == kSwDense) {
+        if (p.epi.residual)
+            load_rows(pre.a, lane, static_cast<const __nv_bfloat16 *>(p.epi.residual), p.epi.ld_residual, r0, nt, n0, p.N);
+    }
+    if constexpr (EPI == kSwSwigluGrad) {
+        const __nv_bfloat16 *P = static_cast<const __nv_bfloat16 *>(p.epi.preact);
+        load_rows(pre.a, lane, P, p.epi.ld_preact, r0, nt, n0, p.N);
+        load_rows(pre.b, lane, P + p.N, p.epi.ld_preact, r0, nt, n0, p.N);
+    }
+}
+
+template <int EPI, class Ahead>
 __device__ __forceinline__ void finish_chunk(const SwapArgs &p, float (&v)[32], uint32_t stg, int lane, int64_t r0, int nt,
                                              int n0, float sa_lane, const float (&sb)[4], const float (&bias)[4],
-                                             const ErrCtx &err)
+                                             EpiReads &pre, Ahead &&ahead, const ErrCtx &err)
 {
     __nv_bfloat16 *D = static_cast<__nv_bfloat16 *>(p.D);
     __nv_bfloat16 *P = static_cast<__nv_bfloat16 *>(p.epi.preact);
@@ -326,7 +360,8 @@ __device__ __forceinline__ void finish_chunk(const SwapArgs &p, float (&v)[32], 
                 v[i] = act_f<kActGelu>(v[i]);
         }
         if (p.epi.residual) {
-            get_frag(stg, lane, w, static_cast<const __nv_bfloat16 *>(p.epi.residual), p.epi.ld_residual, r0, nt, n0, p.N);
+            rows_frag(stg, lane, pre.a, w);
+            ahead();
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -365,8 +400,9 @@ __device__ __forceinline__ void finish_chunk(const SwapArgs &p, float (&v)[32], 
         put_frag<16>(stg, lane, x, D, p.ldd, r0, nt, n0, p.N, d_limit, err);
     } else {
         uint32_t u[16];
-        get_frag(stg, lane, w, P, p.epi.ld_preact, r0, nt, n0, p.N);
-        get_frag(stg, lane, u, P + p.N, p.epi.ld_preact, r0, nt, n0, p.N);
+        rows_frag(stg, lane, pre.a, w);
+        rows_frag(stg, lane, pre.b, u);
+        ahead();
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -411,8 +447,10 @@ __device__ __forceinline__ SwapTile swap_tile(int t, const int *off, const int *
     return x;
 }
 
+constexpr int kSwThreads = 320;
+
 template <int IN, int EPI>
-__global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ SwapArgs p, ErrCtx err)
+__global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_constant__ SwapArgs p, ErrCtx err)
 {
     constexpr int KB = kb_elems(IN);
     extern __shared__ uint8_t smem_raw[];
@@ -426,7 +464,7 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *row_numbers = reinterpret_cast<int *>(tmem_slot + 4);
-    int *off = row_numbers + 128, *start = off + p.E + 1;
+    int *off = row_numbers + kSwGatherW / 2, *start = off + p.E + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
@@ -434,7 +472,7 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
     constexpr int OUT = EPI == kSwSwiglu ? 128 : 256;          // output columns of a tile
     const int tiles_n = (p.N + OUT - 1) / OUT, num_kb = (p.K + KB - 1) / KB;
 
-    for (int i = threadIdx.x; i <= p.E; i += 320)
+    for (int i = threadIdx.x; i <= p.E; i += kSwThreads)
         off[i] = p.offsets ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -448,8 +486,8 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0 && lane < 5)
-        tma_prefetch_desc(lane == 0 ? &p.tmW : &p.tmX[p.rows ? 0 : lane - 1]);
+    if (warp == 0 && lane < (p.gather ? 2 : 5))
+        tma_prefetch_desc(lane == 0 ? &p.tmW : &p.tmX[lane - 1]);
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
@@ -503,24 +541,21 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
             const SwapTile x = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group);
             const int half = x.w / 2, xrow = x.row0 + static_cast<int>(rank) * half;
             const int box = sw_box_rows(half);
-            const CUtensorMap *tmx = &p.tmX[p.rows ? 0 : box == 16 ? 0 : box == 32 ? 1 : box == 64 ? 2 : 3];
-            int4 four = make_int4(p.T, p.T, p.T, p.T);
-            if (p.rows) {
+            const CUtensorMap *tmx = &p.tmX[p.gather || box == 16 ? 0 : box == 32 ? 1 : box == 64 ? 2 : 3];
+            int4 four = make_int4(0, 0, 0, 0);
+            if (p.gather) {
                 __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 32 * j + lane;
-                    int r = p.T;             // past the last row: zeros
-                    if (t < half && static_cast<int>(rank) * half + t < x.rows) {
-                        r = __ldg(p.rows + xrow + t);
-                        r = r < 0 || r >= p.T ? p.T : r;
-                    }
-                    row_numbers[t] = r;
+                int r = p.map_rows;             // past the last row: zeros
+                if (lane < half && static_cast<int>(rank) * half + lane < x.rows) {
+                    r = __ldg(p.rows + xrow + lane);
+                    r = r < 0 || r >= p.map_rows ? p.map_rows : r;
                 }
+                row_numbers[lane] = r;
                 __syncwarp();
-                four = reinterpret_cast<const int4 *>(row_numbers)[lane];
+                if (lane < half / 4)
+                    four = reinterpret_cast<const int4 *>(row_numbers)[lane];
             }
-            const uint32_t tx = 2u * (16384u + static_cast<uint32_t>(p.rows ? half : box) * 128u);
+            const uint32_t tx = 2u * (16384u + static_cast<uint32_t>(p.gather ? half : box) * 128u);
             const int n0 = x.tn * OUT + static_cast<int>(rank) * (OUT / 2);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
@@ -539,7 +574,7 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
                 } else {
                     tma_load_3d_pair_w(sw, &p.tmW, bar0, kb * KB, n0, x.e);
                 }
-                if (p.rows) {
+                if (p.gather) {
                     if (lane < half / 4)
                         tma_gather4_pair(smem_u32(sx) + lane * 512, tmx, bar0, kb * KB, four);
                     __syncwarp();
@@ -637,11 +672,18 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
                         bias[i] = __ldg(p.epi.bias + n);
                 }
             }
+            const int chunks = (x.rows + 31) / 32;
+            EpiReads pre;
+            auto ahead = [&](int c) {
+                if (c < chunks)
+                    read_ahead<EPI>(p, pre, lane, x.row0 + c * 32, min(32, x.rows - c * 32), n0);
+            };
+            if (!partial)
+                ahead(half);
             if (!mbar_wait_cluster(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull))
                 break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kSwMaxW;
-            const int chunks = (x.rows + 31) / 32;
             const int64_t piece = 32 * p.maxw;
             const int64_t limit = nclusters * sw_partial_floats(p.maxw);
             bool finish = !partial;
@@ -683,6 +725,8 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
                 }
             }
             if (finish) {
+                if (partial)
+                    ahead(half);
 #pragma unroll 1
                 for (int c = half; c < chunks; c += 2) {
                     const int64_t r0 = x.row0 + c * 32;
@@ -715,7 +759,7 @@ __global__ void __launch_bounds__(320, 1) swap_kernel(const __grid_constant__ Sw
                             }
                         }
                     }
-                    finish_chunk<EPI>(p, v, stg, lane, r0, nt, n0, sa, sb, bias, err);
+                    finish_chunk<EPI>(p, v, stg, lane, r0, nt, n0, sa, sb, bias, pre, [&] { ahead(c + 2); }, err);
                 }
             }
             if (!partial) {
@@ -746,7 +790,7 @@ cudaError_t launch_swap_as(const SwapArgs &a, int num_sms, const ErrCtx &err, cu
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
-    cfg.blockDim = dim3(320);
+    cfg.blockDim = dim3(kSwThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -7,18 +7,18 @@
 // of A.  A block of the contraction is 64 rows of the group.
 //
 // Groups end anywhere.  Rows past the end belong to the next group and may hold
-// NaN or infinities, so zeroing one operand is not enough; the last block of a
-// group reads both operands by TMA gathers of four rows each whose indices past
-// the end are out of range and read as zeros, up to the next multiple of 16
-// rows (one MMA step), and the steps beyond are not issued.  With `rows`, A is
-// read by gathers throughout, its row numbers fetched 256 at a time, one batch
-// ahead.  A group without rows is one such block of zeros: its tile is written
-// as zeros like any other.
+// NaN or infinities, so zeroing one operand is not enough: the last block of a
+// group is not read by TMA but copied by four warps, zero-filled past the end
+// up to the next multiple of 16 rows (one MMA step); the steps beyond are not
+// issued.  Rows by number are gathered into workspace before this kernel.  A
+// group without rows is one such block of zeros: its tile is written as zeros
+// like any other.
 //
 // Schedule: every group has the same tiles (bands of `group` column tiles);
 // they go round robin, or, where the last wave would leave pairs idle for
 // longer than a split costs, the first tiles are cut into equal runs of blocks
 // and summed from fp32 partials in pair order.  Roles as in swap_kernel.cuh.
+#include "copy.cuh"
 #include "grouped.h"
 #include "tc2_kernel.cuh"
 #include "wgrad.h"
@@ -28,18 +28,11 @@ namespace {
 
 constexpr int kWgStages = 6;
 constexpr int kWgStageBytes = 32768;
-constexpr int kWgBars = (2 * kWgStages + 4) * 8 + 16 + 1024;      // barriers, TMEM address, abort flag, row numbers
+constexpr int kWgBars = (2 * kWgStages + 4) * 8 + 16;             // barriers, TMEM address, abort flag
 constexpr int64_t kWgPiece = 32 * 256;
+constexpr int kWgThreads = 448;                  // producer, MMA, eight epilogue, four copying warps
 
 __host__ __device__ inline int wg_smem(int E) { return 1024 + kWgStages * kWgStageBytes + kWgBars + 8 * (E + 1); }
-
-__device__ __forceinline__ void tma_gather4_pair_to(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, const int4 &r)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-                 " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-                 : "memory");
-}
 
 // Blocks of a group's contraction (one of zeros for an empty group).
 __device__ __forceinline__ int wg_blocks(int rows) { return rows > 0 ? (rows + 63) / 64 : 1; }
@@ -98,7 +91,7 @@ struct WgWalk {
     }
 };
 
-__global__ void __launch_bounds__(320, 1) wgrad_kernel(const __grid_constant__ WgradTmaArgs p, ErrCtx err)
+__global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_constant__ WgradTmaArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -109,19 +102,18 @@ __global__ void __launch_bounds__(320, 1) wgrad_kernel(const __grid_constant__ W
     uint64_t *tempty = tfull + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *row_numbers = reinterpret_cast<int *>(tmem_slot + 4);
-    int *off = row_numbers + 256, *unit = off + p.E + 1;
+    int *off = reinterpret_cast<int *>(tmem_slot + 4), *unit = off + p.E + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
     const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
 
-    for (int i = threadIdx.x; i <= p.E; i += 320)
+    for (int i = threadIdx.x; i <= p.E; i += kWgThreads)
         off[i] = min(max(__ldg(p.offsets + i), 0), p.R);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kWgStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + 2 * kCopyWarps);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -131,8 +123,8 @@ __global__ void __launch_bounds__(320, 1) wgrad_kernel(const __grid_constant__ W
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0 && lane < 4)
-        tma_prefetch_desc(lane == 0 ? &p.tmD : lane == 1 ? &p.tmA : lane == 2 ? &p.tmDg : &p.tmAg);
+    if (warp == 0 && lane < 2)
+        tma_prefetch_desc(lane ? &p.tmA : &p.tmD);
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
@@ -193,73 +185,25 @@ __global__ void __launch_bounds__(320, 1) wgrad_kernel(const __grid_constant__ W
             const int kcols = p.K - tk * 256 <= 128 ? 64 : 128;               // columns of A per CTA
             const int n0 = tn * 256 + static_cast<int>(rank) * 128, k0 = tk * 256 + static_cast<int>(rank) * kcols;
             const int abox = kcols / 64;
-            int next[8];
-            auto fetch = [&](int batch) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = lo + batch * 256 + 32 * j + lane;
-                    int v = p.T;
-                    if (r < hi) {
-                        v = __ldg(p.rows + r);
-                        v = v < 0 || v >= p.T ? p.T : v;
-                    }
-                    next[j] = v;
-                }
-            };
-            if (p.rows)
-                fetch(kb0 >> 2);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (p.rows && (kb == kb0 || (kb & 3) == 0)) {
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        row_numbers[32 * j + lane] = next[j];
-                    __syncwarp();
-                    if ((kb >> 2) * 4 + 4 < kb1)
-                        fetch((kb >> 2) + 1);
-                }
                 const int r0 = lo + kb * 64;
-                const int left = hi - r0;
-                const bool whole = left >= 64;
-                const int rows16 = whole ? 64 : (max(left, 1) + 15) & ~15;
+                const bool whole = hi - r0 >= 64;
                 if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
                     ok = false;
                     break;
                 }
+                const int boxes = whole ? 2 + abox : 0;
                 if (rank == 0)
-                    mbar_arrive_expect_tx_w(&full[stage], 2u * static_cast<uint32_t>((2 + abox) * rows16 * 128));
+                    mbar_arrive_expect_tx_w(&full[stage], 2u * static_cast<uint32_t>(boxes * kMnBoxBytes));
                 const uint32_t bar0 = mapa_shared(smem_u32(&full[stage]), 0);
                 uint8_t *sd = smem + stage * kWgStageBytes, *sa = sd + 16384;
-                const int g = lane & 15, b = lane >> 4;                       // a gather: box b, rows 4 g .. 4 g + 3
                 if (whole) {
                     tma_load_2d_pair_w(sd, &p.tmD, bar0, n0, r0);
                     tma_load_2d_pair_w(sd + kMnBoxBytes, &p.tmD, bar0, n0 + kMnBox, r0);
-                } else if (4 * g < rows16) {
-                    int4 r;
-                    r.x = 4 * g + 0 < left ? r0 + 4 * g + 0 : p.R;
-                    r.y = 4 * g + 1 < left ? r0 + 4 * g + 1 : p.R;
-                    r.z = 4 * g + 2 < left ? r0 + 4 * g + 2 : p.R;
-                    r.w = 4 * g + 3 < left ? r0 + 4 * g + 3 : p.R;
-                    tma_gather4_pair_to(smem_u32(sd) + b * kMnBoxBytes + g * 512, &p.tmDg, bar0, n0 + b * kMnBox, r);
-                }
-                __syncwarp();
-                if (whole && !p.rows) {
                     tma_load_2d_pair_w(sa, &p.tmA, bar0, k0, r0);
                     if (abox == 2)
                         tma_load_2d_pair_w(sa + kMnBoxBytes, &p.tmA, bar0, k0 + kMnBox, r0);
-                } else if (4 * g < rows16 && b < abox) {
-                    int4 r;
-                    if (p.rows) {
-                        r = reinterpret_cast<const int4 *>(row_numbers)[(kb & 3) * 16 + g];
-                    } else {
-                        r.x = 4 * g + 0 < left ? r0 + 4 * g + 0 : p.T;
-                        r.y = 4 * g + 1 < left ? r0 + 4 * g + 1 : p.T;
-                        r.z = 4 * g + 2 < left ? r0 + 4 * g + 2 : p.T;
-                        r.w = 4 * g + 3 < left ? r0 + 4 * g + 3 : p.T;
-                    }
-                    tma_gather4_pair_to(smem_u32(sa) + b * kMnBoxBytes + g * 512, &p.tmAg, bar0, k0 + b * kMnBox, r);
                 }
-                __syncwarp();
                 ++issued;
                 if (++stage == kWgStages) {
                     stage = 0;
@@ -317,6 +261,49 @@ __global__ void __launch_bounds__(320, 1) wgrad_kernel(const __grid_constant__ W
                 if (!ok)
                     break;
                 mma_commit_pair_w(&tfull[acc], 0x3);
+            }
+        }
+    } else if (warp >= 10) {
+        // ------------------------------------ copies of the ends of groups
+        const int cw = warp - 10, piece = lane & 7, sub = lane >> 3;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
+            tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
+            const int lo = off[e], hi = lo + walk.rows(e);
+            const int kcols = p.K - tk * 256 <= 128 ? 64 : 128;
+            const int n0 = tn * 256 + static_cast<int>(rank) * 128, k0 = tk * 256 + static_cast<int>(rank) * kcols;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const int r0 = lo + kb * 64, left = hi - r0;
+                // 16 rows per warp: rows past the MMA's last step are not needed
+                if (left < 64 && cw * 16 < max(left, 1)) {
+                    const uint32_t sd = smem_u32(smem + stage * kWgStageBytes), sa = sd + 16384;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int b = i >> 2, r = cw * 16 + 4 * (i & 3) + sub;
+                        const uint32_t at = b * kMnBoxBytes + r * 128 + ((piece ^ (r & 7)) << 4);
+                        const int n = n0 + b * kMnBox + piece * 8, k = k0 + b * kMnBox + piece * 8;
+                        int bytes = r < left ? min(16, max(0, (p.N - n) * 2)) : 0;
+                        copy16(sd + at, bytes ? p.dD + (r0 + r) * p.ldd + n : p.dD, bytes);
+                        if (b * kMnBox < kcols) {
+                            bytes = r < left ? min(16, max(0, (p.K - k) * 2)) : 0;
+                            copy16(sa + at, bytes ? p.A + (r0 + r) * p.lda + k : p.A, bytes);
+                        }
+                    }
+                    copies_done();
+                    arrive_copied(&full[stage]);
+                } else if (lane == 0) {
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&full[stage]), 0));     // nothing to hand over
+                }
+                if (++stage == kWgStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
         }
     } else {
@@ -442,7 +429,7 @@ cudaError_t launch_wgrad(const WgradTmaArgs &a, int num_sms, const ErrCtx &err, 
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
-    cfg.blockDim = dim3(320);
+    cfg.blockDim = dim3(kWgThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -6,11 +6,12 @@
 namespace tmg {
 
 struct WgradTmaArgs {
-    CUtensorMap tmD, tmA;      // dD (R, N) and A (T, K), boxes of 64 columns x 64 rows
-    CUtensorMap tmDg, tmAg;    // the same, boxes of 64 columns x 1 row (gathers)
+    CUtensorMap tmD, tmA;      // dD (R, N) and A (R, K), boxes of 64 columns x 64 rows
+    const uint16_t *dD, *A;    // the same operands, for the rows that warps copy
+    int64_t ldd, lda;          // row strides in elements
     void *dB;                  // (E, N, K) contiguous
-    const int32_t *offsets, *rows;
-    int R, T, N, K, E;
+    const int32_t *offsets;
+    int R, N, K, E;
     int group;                 // column tiles of dD per band
     int split_cost;            // cost of a split in blocks of 64 rows; < 0: never split
     int vec_ok;
