@@ -91,6 +91,18 @@ tmg_status pack(const DeviceState &ds, Workspace which, Pack3Args a, int elem, s
     return TMG_OK;
 }
 
+// The tile counter and the arrival counters of split tiles, zero between
+// launches.
+tmg_status counters(int pairs, cudaStream_t s, uint32_t **feed, uint32_t **split)
+{
+    tmg_status st;
+    *feed = static_cast<uint32_t *>(workspace(kWsCounters, (32 + static_cast<size_t>(pairs) * 32) * sizeof(uint32_t), s, &st));
+    if (!*feed)
+        return st;
+    *split = *feed + 32;
+    return TMG_OK;
+}
+
 // A's rows by number into workspace, rows of K elements: *A and *lda become the
 // copy's.
 tmg_status gather(const DeviceState &ds, const void **A, int64_t *lda, int64_t src_rows, int64_t K, int elem,
@@ -216,12 +228,11 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
         p.partials = static_cast<float *>(workspace(kWsPartials, pairs * sw_partial_floats(p.maxw) * sizeof(float), s, &st));
         if (!p.partials)
             return st;
-        p.counters = static_cast<uint32_t *>(workspace(kWsCounters, static_cast<size_t>(pairs) * 32 * sizeof(uint32_t), s, &st));
-        if (!p.counters)
-            return st;
     } else {
         p.split_cost = -1;
     }
+    if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
+        return st;
     const int epi = swiglu ? kSwSwiglu : a.epi.act == kActSwigluGrad ? kSwSwigluGrad : a.offsets ? kSwPlain : kSwDense;
     log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s",
                a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", p.R, (long long)a.N, (long long)a.K, p.E, 256, p.maxw,
@@ -253,11 +264,12 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
             n = a.R > 0 ? a.R : 1;
         }
         const int64_t dims[2] = {cols[i], n}, strides[1] = {ld * 2};
-        const int box[2] = {64, 64};
-        if ((st = encode_nd(i ? &p.tmA : &p.tmD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box)) != TMG_OK)
-            return st;
-        (i ? p.A : p.dD) = static_cast<const uint16_t *>(op[i]);
-        (i ? p.lda : p.ldd) = ld;
+        CUtensorMap *maps[3] = {i ? &p.tmA : &p.tmD, i ? &p.tmA16 : &p.tmD16, i ? &p.tmAg : &p.tmDg};
+        for (int b = 0; b < 3; ++b) {
+            const int box[2] = {64, b == 0 ? 64 : b == 1 ? 16 : 1};
+            if ((st = encode_nd(maps[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box)) != TMG_OK)
+                return st;
+        }
     }
     p.dB = a.dB;
     p.offsets = a.offsets;
@@ -276,12 +288,11 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
         p.partials = static_cast<float *>(workspace(kWsPartials, wgrad_partial_bytes(ds.num_sms), s, &st));
         if (!p.partials)
             return st;
-        p.counters = static_cast<uint32_t *>(workspace(kWsCounters, static_cast<size_t>(pairs) * 32 * sizeof(uint32_t), s, &st));
-        if (!p.counters)
-            return st;
     } else {
         p.split_cost = -1;
     }
+    if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
+        return st;
     log_choice("bf16 grouped weight gradient: %d rows, N=%d K=%d E=%d -> wgrad_kernel: 256 x 256 tiles%s", p.R, p.N, p.K, p.E,
                a.rows ? ", rows gathered first" : "");
     return launched(launch_wgrad(p, ds.num_sms, err_ctx(ds), s), "grouped weight gradient launch");

@@ -35,37 +35,34 @@ __global__ void __launch_bounds__(256) pack3_kernel(Pack3Args a, int64_t tiles_k
 }
 
 // Rows in 16-byte pieces: dst[r] = src[numbers[r]], zeros where that is no row
-// and past the row's bytes.  Four pieces per thread in flight.
+// and past the row's bytes.  A warp takes a row at a time, eight pieces per
+// lane in flight.
 __global__ void __launch_bounds__(256)
     gather_rows_kernel(const char *__restrict__ src, int64_t stride, int64_t src_rows, int bytes,
                        const int32_t *__restrict__ numbers, int64_t rows, char *__restrict__ dst, int64_t dst_stride)
 {
-    const int64_t pieces = dst_stride / 16, total = rows * pieces, step = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 4 * step) {
-        uint4 v[4];
+    const int lane = threadIdx.x % 32, pieces = static_cast<int>(dst_stride / 16), whole = bytes / 16;
+    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; r < rows; r += gridDim.x * 8ll) {
+        const int64_t from = __ldg(numbers + r);
+        const bool there = from >= 0 && from < src_rows;
+        const char *p = src + (there ? from : 0) * stride;
+        uint4 *d = reinterpret_cast<uint4 *>(dst + r * dst_stride);
+        for (int i = lane; i < pieces; i += 256) {
+            uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t at = i + j * step, r = at / pieces;
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (at >= total)
-                continue;
-            const int64_t from = __ldg(numbers + r), b = at % pieces * 16;
-            if (from < 0 || from >= src_rows || b >= bytes)
-                continue;
-            const char *p = src + from * stride + b;
-            if (b + 16 <= bytes) {
-                v[j] = __ldg(reinterpret_cast<const uint4 *>(p));
-            } else {
-                uint32_t w[4] = {};
-                for (int c = 0; b + c < bytes; ++c)
-                    w[c / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[c])) << (8 * (c & 3));
-                v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 8; ++j) {
+                const int at = i + 32 * j;
+                v[j] = there && at < whole ? __ldg(reinterpret_cast<const uint4 *>(p) + at) : make_uint4(0, 0, 0, 0);
             }
-        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (i + j * step < total)
-                reinterpret_cast<uint4 *>(dst)[i + j * step] = v[j];
+            for (int j = 0; j < 8; ++j)
+                if (i + 32 * j < pieces)
+                    d[i + 32 * j] = v[j];
+        }
+        __syncwarp();
+        // the last, partial piece
+        if (there && whole < pieces && lane < bytes - whole * 16)
+            reinterpret_cast<char *>(d + whole)[lane] = p[whole * 16 + lane];
     }
 }
 
@@ -74,8 +71,8 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_gather_rows(const void *src, int64_t stride, int64_t src_rows, int64_t bytes, const int32_t *numbers,
                                int64_t rows, void *dst, int64_t dst_stride, int num_sms, cudaStream_t s)
 {
-    const int64_t total = rows * (dst_stride / 16), blocks = (total + 1023) / 1024;
-    if (total == 0)
+    const int64_t blocks = (rows + 7) / 8;
+    if (rows == 0)
         return cudaSuccess;
     note_launch();
     gather_rows_kernel<<<static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8), 256, 0, s>>>(

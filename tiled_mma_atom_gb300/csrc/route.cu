@@ -13,8 +13,10 @@
 // Plan.  A stable counting sort.  Blocks take contiguous runs of tokens and
 // leave their counts per expert; the second kernel adds up the counts of
 // experts and blocks before its own and ranks its pairs in order: 32 pairs at
-// a time per warp, the lanes with the same expert found by match.any.  No
-// atomic decides an order, so the plan does not depend on timing.
+// a time per warp, the lanes with the same expert found by match.any.  Atomics
+// only count, none decides an order, so the plan does not depend on timing.
+// Up to kOneBlockTokens tokens one block does it all in one launch: beyond,
+// its warps' tokens in a row cost more than the second launch.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -58,16 +60,12 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// The choices of tokens t0 .. t1 - 1, one warp per token; counts (shared) gets
+// each expert's number; pairs (shared, or null) the chosen experts in order.
 template <int C>
-__global__ void __launch_bounds__(256) route_topk_kernel(RouteArgs a, int tokens_per_block)
+__device__ __forceinline__ void choose(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *counts, int32_t *pairs)
 {
-    extern __shared__ int32_t counts[];
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        counts[e] = 0;
-    __syncthreads();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
-    const int64_t t1 = min(a.T, t0 + tokens_per_block);
     for (int64_t t = t0 + warp; t < t1; t += warps) {
         uint32_t key[C];
 #pragma unroll
@@ -75,9 +73,9 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouteArgs a, int tokens
             const int e = lane + 32 * c;
             key[c] = e < a.E ? logit_key(load_logit(a.logits, t * a.ld + e, a.bf16)) : 0;
         }
-        uint32_t all = 0;
         float sum_all = 0.f;
         if (!a.normalize) {
+            uint32_t all = 0;
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 all = max(all, key[c]);
@@ -118,74 +116,59 @@ __global__ void __launch_bounds__(256) route_topk_kernel(RouteArgs a, int tokens
         if (lane < a.k) {
             a.weights[t * a.k + lane] = mine >= 0 ? ex / sum : 0.f;
             a.experts[t * a.k + lane] = mine;
+            if (pairs)
+                pairs[(t - t0) * a.k + lane] = mine;
             if (mine >= 0)
                 atomicAdd(&counts[mine], 1);
         }
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = counts[e];
 }
 
-// Shared memory: base[E], warp counts [warps][E], scan scratch [33].
-__global__ void __launch_bounds__(256) route_plan_kernel(RouteArgs a, int tokens_per_block, int blocks)
+// Warp 0: base[e] += the pairs of all experts before e; block 0 writes the
+// offsets.  Returns the number of all pairs (in warp 0).
+__device__ __forceinline__ int add_expert_prefix(const RouteArgs &a, int32_t *base, const int32_t *total)
 {
-    extern __shared__ int32_t sm[];
-    const int E = a.E, warps = blockDim.x / 32, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int32_t *base = sm, *wc = sm + E, *total = wc + warps * E;
-    // counts of this expert in the blocks before, and in all of them
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int before = 0, sum = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const int n = __ldg(a.counts + static_cast<int64_t>(b) * E + e);
-            if (b < static_cast<int>(blockIdx.x))
-                before += n;
-            sum += n;
-        }
-        base[e] = before;
-        total[e] = sum;
-    }
-    for (int i = threadIdx.x; i < warps * E; i += blockDim.x)
-        wc[i] = 0;
-    __syncthreads();
-    if (warp == 0) {                 // exclusive prefix over the experts
-        int run = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane, n = e < E ? total[e] : 0;
-            int inc = n;
+    const int lane = threadIdx.x % 32;
+    int run = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane, n = e < a.E ? total[e] : 0;
+        int inc = n;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kFull, inc, o);
-                if (lane >= o)
-                    inc += v;
-            }
-            if (e < E) {
-                base[e] += run + inc - n;
-                if (blockIdx.x == 0)
-                    a.offsets[e] = run + inc - n;
-            }
-            run += __shfl_sync(kFull, inc, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o)
+                inc += v;
         }
-        if (lane == 0) {
-            total[0] = run;
+        if (e < a.E) {
+            base[e] += run + inc - n;
             if (blockIdx.x == 0)
-                a.offsets[E] = run;
+                a.offsets[e] = run + inc - n;
         }
+        run += __shfl_sync(kFull, inc, 31);
     }
-    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block * a.k;
-    const int64_t p1 = min(a.T * a.k, p0 + static_cast<int64_t>(tokens_per_block) * a.k);
+    if (lane == 0 && blockIdx.x == 0)
+        a.offsets[a.E] = run;
+    return run;
+}
+
+// Slots and rows of the pairs p0 .. p1 - 1, whose experts are pairs[p - p0];
+// base[e]: the first slot of this block's pairs of expert e.  wc: warps x E
+// counters, zero.
+__device__ __forceinline__ void rank_pairs(const RouteArgs &a, int64_t p0, int64_t p1, const int32_t *pairs,
+                                           const int32_t *base, int32_t *wc)
+{
+    const int E = a.E, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     // each warp's pairs are contiguous: [w0, w1)
     const int64_t each = ((p1 - p0 + warps - 1) / warps + 31) / 32 * 32;
     const int64_t w0 = min(p1, p0 + warp * each), w1 = min(p1, w0 + each);
     for (int64_t p = w0; p < w1; p += 32) {
-        const int e = p + lane < w1 ? a.experts[p + lane] : -1;
+        const int e = p + lane < w1 ? pairs[p + lane - p0] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         if (e >= 0 && lane == __ffs(same) - 1)
             wc[warp * E + e] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
-    const int rows_used = total[0];
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int run = base[e];
         for (int w = 0; w < warps; ++w) {
@@ -197,7 +180,7 @@ __global__ void __launch_bounds__(256) route_plan_kernel(RouteArgs a, int tokens
     __syncthreads();
     for (int64_t p = w0; p < w1; p += 32) {
         const int64_t i = p + lane;
-        const int e = i < w1 ? a.experts[i] : -1;
+        const int e = i < w1 ? pairs[i - p0] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         const int first = e >= 0 ? wc[warp * E + e] : 0;
         __syncwarp();
@@ -212,8 +195,91 @@ __global__ void __launch_bounds__(256) route_plan_kernel(RouteArgs a, int tokens
         }
         __syncwarp();
     }
+}
+
+// One block.  Shared memory: counts (totals) [E], base [E], pairs [T k], warp
+// counters [warps][E].
+template <int C>
+__global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a)
+{
+    extern __shared__ int32_t sm[];
+    __shared__ int used;
+    const int warps = blockDim.x / 32;
+    int32_t *counts = sm, *base = sm + a.E, *wc = base + a.E, *pairs = wc + warps * a.E;
+    for (int i = threadIdx.x; i < (2 + warps) * a.E; i += blockDim.x)
+        sm[i] = 0;
+    __syncthreads();
+    choose<C>(a, 0, a.T, counts, pairs);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int n = add_expert_prefix(a, base, counts);
+        if (threadIdx.x == 0)
+            used = n;
+    }
+    __syncthreads();
+    rank_pairs(a, 0, a.T * a.k, pairs, base, wc);
+    for (int64_t i = used + threadIdx.x; i < a.T * a.k; i += blockDim.x)
+        a.rows[i] = -1;              // rows that no pair takes
+}
+
+template <int C>
+__global__ void __launch_bounds__(1024) route_choose_kernel(RouteArgs a, int tokens_per_block)
+{
+    extern __shared__ int32_t counts[];
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        counts[e] = 0;
+    __syncthreads();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
+    choose<C>(a, t0, min(a.T, t0 + tokens_per_block), counts, nullptr);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = counts[e];
+}
+
+// Shared memory: base [E], totals [E], warp counters [warps][E].
+__global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens_per_block, int blocks)
+{
+    extern __shared__ int32_t sm[];
+    __shared__ int used;
+    const int E = a.E, warps = blockDim.x / 32, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int32_t *base = sm, *total = sm + E, *wc = total + E;
+    for (int i = threadIdx.x; i < (2 + warps) * E; i += blockDim.x)
+        sm[i] = 0;
+    __syncthreads();
+    // counts in the blocks before this one, and in all: each warp adds up
+    // every warps-th block, 128 experts at a time
+    for (int e0 = 0; e0 < E; e0 += 128) {
+        int before[4] = {}, sum[4] = {};
+#pragma unroll 4
+        for (int b = warp; b < blocks; b += warps)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int e = e0 + 32 * c + lane;
+                const int n = e < E ? __ldg(a.counts + static_cast<int64_t>(b) * E + e) : 0;
+                sum[c] += n;
+                before[c] += b < static_cast<int>(blockIdx.x) ? n : 0;
+            }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int e = e0 + 32 * c + lane;
+            if (e < E && sum[c]) {
+                atomicAdd(&total[e], sum[c]);
+                atomicAdd(&base[e], before[c]);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int n = add_expert_prefix(a, base, total);
+        if (lane == 0)
+            used = n;
+    }
+    __syncthreads();
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block * a.k;
+    const int64_t p1 = min(a.T * a.k, p0 + static_cast<int64_t>(tokens_per_block) * a.k);
+    rank_pairs(a, p0, p1, a.experts + p0, base, wc);
     // rows that no pair takes
-    for (int64_t i = rows_used + static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.T * a.k;
+    for (int64_t i = used + static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.T * a.k;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x)
         a.rows[i] = -1;
 }
@@ -258,21 +324,26 @@ __global__ void __launch_bounds__(256)
         const float w = e >= 0 ? ex / sum : 0.f;
         const float mean = warp_sum(w * dw);
         const float g = w * (dw - (normalize ? mean : 0.f));
+        float d[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            d[c] = !normalize && v[c] != 0.f ? -(v[c] / sum) * mean : 0.f;
+        for (int j = 0; j < k; ++j) {
+            const int ej = __shfl_sync(kFull, e, j);
+            const float gj = __shfl_sync(kFull, g, j);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (ej == lane + 32 * c)
+                    d[c] += gj;
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = lane + 32 * c;
-            float d = !normalize && v[c] != 0.f ? -(v[c] / sum) * mean : 0.f;
-            for (int j = 0; j < k; ++j) {
-                const int ej = __shfl_sync(kFull, e, j);
-                const float gj = __shfl_sync(kFull, g, j);
-                if (ej == i)
-                    d += gj;
-            }
             if (i < E) {
                 if (bf16)
-                    static_cast<__nv_bfloat16 *>(out)[t * E + i] = __float2bfloat16_rn(d);
+                    static_cast<__nv_bfloat16 *>(out)[t * E + i] = __float2bfloat16_rn(d[c]);
                 else
-                    static_cast<float *>(out)[t * E + i] = d;
+                    static_cast<float *>(out)[t * E + i] = d[c];
             }
         }
     }
@@ -404,7 +475,37 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineGradArgs a
     }
 }
 
-int tokens_per_block(int64_t T, int num_sms) { return static_cast<int>((T + num_sms - 1) / num_sms); }
+constexpr int64_t kOneBlockTokens = 128;
+
+// Two blocks per SM.
+int tokens_per_block(int64_t T, int num_sms) { return static_cast<int>((T + 2 * num_sms - 1) / (2 * num_sms)); }
+
+template <int C>
+cudaError_t launch_route_as(const RouteArgs &a, int num_sms, cudaStream_t s)
+{
+    note_launch();
+    if (a.T <= kOneBlockTokens) {
+        // a warp per token; fewer counters where there are fewer tokens
+        const int warps = static_cast<int>(a.T < 4 ? 4 : a.T < 16 ? a.T : 16);
+        const int bytes = static_cast<int>(((2 + warps) * a.E + a.T * a.k) * sizeof(int32_t));
+        const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(route_one_kernel<C>), bytes);
+        if (e != cudaSuccess)
+            return e;
+        route_one_kernel<C><<<1, warps * 32, bytes, s>>>(a);
+        return cudaGetLastError();
+    }
+    const int each = tokens_per_block(a.T, num_sms), blocks = route_blocks(a.T, num_sms);
+    route_choose_kernel<C><<<blocks, 1024, a.E * sizeof(int32_t), s>>>(a, each);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    const int bytes = static_cast<int>(18 * a.E * sizeof(int32_t));
+    if ((e = ensure_smem_attr(reinterpret_cast<const void *>(route_plan_kernel), bytes)) != cudaSuccess)
+        return e;
+    note_launch();
+    route_plan_kernel<<<blocks, 512, bytes, s>>>(a, each, blocks);
+    return cudaGetLastError();
+}
 
 bool vec8(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 
@@ -416,23 +517,13 @@ int route_blocks(int64_t T, int num_sms)
     return static_cast<int>((T + each - 1) / each);
 }
 
+// Registers per lane for E experts: 2, 4, 8 or 32 of 32 experts each.
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t s)
 {
-    const int each = tokens_per_block(a.T, num_sms), blocks = route_blocks(a.T, num_sms);
-    const size_t sm1 = a.E * sizeof(int32_t), sm2 = (10 * static_cast<size_t>(a.E)) * sizeof(int32_t);
-    note_launch();
-    if (a.E <= 64)
-        route_topk_kernel<2><<<blocks, 256, sm1, s>>>(a, each);
-    else if (a.E <= 256)
-        route_topk_kernel<8><<<blocks, 256, sm1, s>>>(a, each);
-    else
-        route_topk_kernel<32><<<blocks, 256, sm1, s>>>(a, each);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    note_launch();
-    route_plan_kernel<<<blocks, 256, sm2, s>>>(a, each, blocks);
-    return cudaGetLastError();
+    return a.E <= 64    ? launch_route_as<2>(a, num_sms, s)
+           : a.E <= 128 ? launch_route_as<4>(a, num_sms, s)
+           : a.E <= 256 ? launch_route_as<8>(a, num_sms, s)
+                        : launch_route_as<32>(a, num_sms, s);
 }
 
 cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
@@ -440,13 +531,12 @@ cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int6
                                   cudaStream_t s)
 {
     const int blocks = static_cast<int>(std::min<int64_t>((T + 7) / 8, num_sms * 8));
+    auto kern = E <= 64    ? route_backward_kernel<2>
+                : E <= 128 ? route_backward_kernel<4>
+                : E <= 256 ? route_backward_kernel<8>
+                           : route_backward_kernel<32>;
     note_launch();
-    if (E <= 64)
-        route_backward_kernel<2><<<blocks, 256, 0, s>>>(logits, bf16, T, ld, E, k, normalize, experts, dweights, dlogits);
-    else if (E <= 256)
-        route_backward_kernel<8><<<blocks, 256, 0, s>>>(logits, bf16, T, ld, E, k, normalize, experts, dweights, dlogits);
-    else
-        route_backward_kernel<32><<<blocks, 256, 0, s>>>(logits, bf16, T, ld, E, k, normalize, experts, dweights, dlogits);
+    kern<<<blocks, 256, 0, s>>>(logits, bf16, T, ld, E, k, normalize, experts, dweights, dlogits);
     return cudaGetLastError();
 }
 

@@ -9,11 +9,11 @@
 // Work.  The group offsets are read on the device: every CTA scans them into
 // a table of tile numbers, so the host never waits for the routing.  Within a
 // group the tiles go in bands of `group` row tiles, row tiles fastest, so that
-// the pairs running together share weight tiles and A panels in L2.  Whole
-// tiles go round robin; where the last wave would leave pairs idle for longer
-// than a split costs, it and the wave before are cut into equal runs of K
-// blocks (stream-K) and summed from fp32 partials in pair order: results do
-// not depend on timing.
+// the pairs running together share weight tiles and A panels in L2.  Each pair
+// takes the next whole tile as it gets free (feed.cuh); where the last wave
+// would leave pairs idle for longer than a split costs, it and another wave are
+// cut into equal runs of K blocks first (stream-K) and summed from fp32 partials
+// in pair order: results do not depend on timing.
 //
 // Operands.  Weights: K-major through a 3-D map (K, N, E), or MN-major (N, K,
 // E) in 64 x 64 boxes; out-of-range rows and K read as zeros, per expert, so a
@@ -27,15 +27,16 @@
 // first (65528 x 2048 x 2048: 1263 us gathered here, COPY_US copied).  Rows of the next
 // group that a box brings along give columns that no one reads.
 //
-// Roles per CTA (ten warps): 0 TMA producer, 1 MMA issuer (CTA 0 of the pair)
-// and TMEM owner, 2..9 epilogue, two warps per TMEM lane quarter taking
-// 32-column chunks in turn.  The accumulator is double-buffered (2 x 256
+// Roles per CTA (eleven warps): 0 TMA producer, 1 MMA issuer (CTA 0 of the
+// pair) and TMEM owner, 2..9 epilogue, two warps per TMEM lane quarter taking
+// 32-column chunks in turn, 10 the tile feed.  The accumulator is double-buffered (2 x 256
 // columns).  Lanes are output columns and registers are rows there, so the
 // epilogue reads 16x256b fragments, whose pairs stmatrix transposes into a
 // 2 KB tile per warp; D, preact and the residual move in 16-byte pieces.
 #pragma once
 
 #include "act.cuh"
+#include "feed.cuh"
 #include "grouped.h"
 #include "tc2_kernel.cuh"
 
@@ -61,6 +62,7 @@ struct SwapArgs {
     int split_cost;            // cost of a stream-K tail in K blocks; < 0: never split
     float *partials;           // sw_partial_floats(maxw) per pair
     uint32_t *counters;        // 16 per tile of two waves
+    uint32_t *feed;            // the tile counter
 };
 
 constexpr int kSwMaxW = 256;
@@ -69,7 +71,7 @@ __host__ __device__ inline int64_t sw_partial_floats(int maxw) { return 2ll * 2 
 constexpr int kSwStaging = 8 * 2048;
 constexpr int kSwMaxStages = 12;
 constexpr int kSwGatherW = 64;       // widest tile with gathers
-constexpr int kSwBars = (2 * kSwMaxStages + 4) * 8 + 16 + kSwGatherW * 2;  // barriers, TMEM address, abort flag, row numbers
+constexpr int kSwBars = (2 * kSwMaxStages + 4) * 8 + sizeof(FeedSmem) + 16 + kSwGatherW * 2;  // barriers, feed, TMEM address, abort flag, row numbers
 __host__ __device__ inline int sw_box_rows(int half) { return half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128; }
 __host__ inline int sw_smem(int stages, int stage_bytes, int E)
 {
@@ -437,17 +439,58 @@ __device__ __forceinline__ SwapTile swap_tile(int t, const int *off, const int *
     SwapTile x;
     x.e = lo;
     const int first = off[lo], rows = off[lo + 1] - first, tiles = (rows + maxw - 1) / maxw;
-    // rows spread evenly over the group's tiles, to multiples of 32
-    const int each = ((rows + tiles - 1) / tiles + 31) & ~31;
     int tm;
     tile_coords(t - start[lo], tiles, tiles_n, group, tm, x.tn);
-    x.row0 = first + tm * each;
-    x.rows = min(each, rows - tm * each);
-    x.w = (x.rows + 31) & ~31;
+    // the group's rows in 32s, spread evenly over its tiles
+    const int grains = (rows + 31) >> 5;
+    const int g0 = static_cast<int>(static_cast<int64_t>(grains) * tm / tiles);
+    const int g1 = static_cast<int>(static_cast<int64_t>(grains) * (tm + 1) / tiles);
+    x.row0 = first + 32 * g0;
+    x.rows = min(32 * g1, rows) - 32 * g0;
+    x.w = 32 * (g1 - g0);
     return x;
 }
 
-constexpr int kSwThreads = 320;
+constexpr int kSwThreads = 352;
+
+// The segments of a pair: its run of split K blocks (the units of the first sk
+// tiles), then whole tiles.
+struct SwapWalk {
+    Feed feed;
+    int sk, num_kb, runs = 0;
+    int64_t u, u_end;
+    const ErrCtx &err;
+    volatile int *abort;
+
+    __device__ SwapWalk(FeedSmem *f, int c, int nc, int total, int sk_, int nkb, const ErrCtx &e, volatile int *ab)
+        : feed(f, c, nc, total - sk_), sk(sk_), num_kb(nkb), err(e), abort(ab)
+    {
+        const int64_t U = static_cast<int64_t>(sk) * num_kb;
+        u = U * c / nc;
+        u_end = U * (c + 1) / nc;
+    }
+
+    // Tile, K blocks, whether a piece of a split tile, and the pair's partial
+    // slot for it (0 first piece, 1 last).
+    __device__ __forceinline__ bool next(int &tile, int &kb0, int &kb1, bool &partial, int &slot)
+    {
+        kb0 = slot = 0;
+        kb1 = num_kb;
+        partial = false;
+        if (u >= u_end) {
+            const bool more = feed.next(tile, err, abort);
+            tile += sk;
+            return more;
+        }
+        tile = static_cast<int>(u / num_kb);
+        kb0 = static_cast<int>(u % num_kb);
+        kb1 = static_cast<int>(min(static_cast<int64_t>(num_kb), kb0 + (u_end - u)));
+        partial = kb0 != 0 || kb1 != num_kb;
+        slot = runs++ ? 1 : 0;
+        u += kb1 - kb0;
+        return true;
+    }
+};
 
 template <int IN, int EPI>
 __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_constant__ SwapArgs p, ErrCtx err)
@@ -461,7 +504,8 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     uint64_t *empty = full + kSwMaxStages;
     uint64_t *tfull = empty + kSwMaxStages;
     uint64_t *tempty = tfull + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
+    FeedSmem *feed_smem = reinterpret_cast<FeedSmem *>(tempty + 2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(feed_smem + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *row_numbers = reinterpret_cast<int *>(tmem_slot + 4);
     int *off = row_numbers + kSwGatherW / 2, *start = off + p.E + 1;
@@ -483,6 +527,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 16);
         }
+        feed_init(feed_smem);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -527,7 +572,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
             static_cast<int64_t>(take) * num_kb >= nclusters)
             sk = take;
     }
-    SegWalk walk(cluster, nclusters, total - sk, sk, num_kb);
+    SwapWalk walk(feed_smem, cluster, nclusters, total, sk, num_kb, err, abort_flag);
     int tile, kb0, kb1, slot;
     bool partial;
 
@@ -647,6 +692,8 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 mma_commit_pair_w(&tfull[acc], 0x3);
             }
         }
+    } else if (warp == 10) {
+        feed_run(feed_smem, rank, total - sk, nclusters, p.feed, err, abort_flag);
     } else {
         // ---------------------------------------------------- epilogue
         const int ew = warp - 2, half = ew / 4, q = warp & 3;
@@ -672,7 +719,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                         bias[i] = __ldg(p.epi.bias + n);
                 }
             }
-            const int chunks = (x.rows + 31) / 32;
+            const int chunks = x.w / 32;
             EpiReads pre;
             auto ahead = [&](int c) {
                 if (c < chunks)

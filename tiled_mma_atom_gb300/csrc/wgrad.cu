@@ -8,17 +8,19 @@
 //
 // Groups end anywhere.  Rows past the end belong to the next group and may hold
 // NaN or infinities, so zeroing one operand is not enough: the last block of a
-// group is not read by TMA but copied by four warps, zero-filled past the end
-// up to the next multiple of 16 rows (one MMA step); the steps beyond are not
-// issued.  Rows by number are gathered into workspace before this kernel.  A
-// group without rows is one such block of zeros: its tile is written as zeros
-// like any other.
+// group is read in pieces up to the next multiple of 16 rows (one MMA step):
+// boxes of 16 rows while they lie inside the group, and for the rest TMA
+// gathers of four rows each whose indices past the end are out of range and
+// read as zeros.  The MMA steps beyond are not issued.  Rows by number are
+// gathered into workspace before this kernel.  A group without rows is one such
+// block of zeros: its tile is written as zeros like any other.
 //
-// Schedule: every group has the same tiles (bands of `group` column tiles);
-// they go round robin, or, where the last wave would leave pairs idle for
-// longer than a split costs, the first tiles are cut into equal runs of blocks
-// and summed from fp32 partials in pair order.  Roles as in swap_kernel.cuh.
-#include "copy.cuh"
+// Schedule: every group has the same tiles (bands of `group` column tiles), of
+// as many blocks as the group has; pairs take them as they get free (feed.cuh).
+// Where the last wave would leave pairs idle for longer than a split costs, the
+// first tiles are cut into equal runs of blocks and summed from fp32 partials in
+// pair order.  Roles as in swap_kernel.cuh.
+#include "feed.cuh"
 #include "grouped.h"
 #include "tc2_kernel.cuh"
 #include "wgrad.h"
@@ -28,11 +30,19 @@ namespace {
 
 constexpr int kWgStages = 6;
 constexpr int kWgStageBytes = 32768;
-constexpr int kWgBars = (2 * kWgStages + 4) * 8 + 16;             // barriers, TMEM address, abort flag
+constexpr int kWgBars = (2 * kWgStages + 4) * 8 + sizeof(FeedSmem) + 16;  // barriers, feed, TMEM address, abort flag
 constexpr int64_t kWgPiece = 32 * 256;
-constexpr int kWgThreads = 448;                  // producer, MMA, eight epilogue, four copying warps
+constexpr int kWgThreads = 352;                  // producer, MMA, eight epilogue warps, feed
 
 __host__ __device__ inline int wg_smem(int E) { return 1024 + kWgStages * kWgStageBytes + kWgBars + 8 * (E + 1); }
+
+__device__ __forceinline__ void tma_gather4_pair_to(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, const int4 &r)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+                 " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+                 : "memory");
+}
 
 // Blocks of a group's contraction (one of zeros for an empty group).
 __device__ __forceinline__ int wg_blocks(int rows) { return rows > 0 ? (rows + 63) / 64 : 1; }
@@ -40,13 +50,17 @@ __device__ __forceinline__ int wg_blocks(int rows) { return rows > 0 ? (rows + 6
 // The walk of a pair: its run of split blocks first, then whole tiles.
 struct WgWalk {
     const int *off, *unit;        // group offsets; blocks before each group
-    int per, E, nclusters, total, next_tile;
+    Feed feed;
+    int per, E, sk;
     int64_t u, u_end;
     bool first;
+    const ErrCtx &err;
+    volatile int *abort;
 
-    __device__ WgWalk(int c, int nc, int sk, int64_t U, int total_, int per_, int E_, const int *off_, const int *unit_)
-        : off(off_), unit(unit_), per(per_), E(E_), nclusters(nc), total(total_), next_tile(sk + c), u(U * c / nc),
-          u_end(U * (c + 1) / nc), first(true)
+    __device__ WgWalk(FeedSmem *f, int c, int nc, int sk_, int64_t U, int total, int per_, int E_, const int *off_,
+                      const int *unit_, const ErrCtx &er, volatile int *ab)
+        : off(off_), unit(unit_), feed(f, c, nc, total - sk_), per(per_), E(E_), sk(sk_), u(U * c / nc),
+          u_end(U * (c + 1) / nc), first(true), err(er), abort(ab)
     {
     }
 
@@ -76,11 +90,11 @@ struct WgWalk {
             u += kb1 - kb0;
             return true;
         }
-        if (next_tile >= total)
+        int tile;
+        if (!feed.next(tile, err, abort))
             return false;
-        e = next_tile / per;
-        local = next_tile % per;
-        next_tile += nclusters;
+        e = (tile + sk) / per;
+        local = (tile + sk) % per;
         blocks = wg_blocks(rows(e));
         kb0 = 0;
         kb1 = blocks;
@@ -100,7 +114,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     uint64_t *empty = full + kWgStages;
     uint64_t *tfull = empty + kWgStages;
     uint64_t *tempty = tfull + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
+    FeedSmem *feed_smem = reinterpret_cast<FeedSmem *>(tempty + 2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(feed_smem + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *off = reinterpret_cast<int *>(tmem_slot + 4), *unit = off + p.E + 1;
 
@@ -113,18 +128,24 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
         off[i] = min(max(__ldg(p.offsets + i), 0), p.R);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kWgStages; ++s) {
-            mbar_init(&full[s], 1 + 2 * kCopyWarps);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 16);
         }
+        feed_init(feed_smem);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0 && lane < 2)
-        tma_prefetch_desc(lane ? &p.tmA : &p.tmD);
+    if (warp == 0 && lane < 6)
+        tma_prefetch_desc(lane == 0   ? &p.tmA
+                          : lane == 1 ? &p.tmD
+                          : lane == 2 ? &p.tmA16
+                          : lane == 3 ? &p.tmD16
+                          : lane == 4 ? &p.tmAg
+                                      : &p.tmDg);
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
@@ -168,7 +189,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
             U = units;
         }
     }
-    WgWalk walk(cluster, nclusters, sk, U, total, per, p.E, off, unit);
+    WgWalk walk(feed_smem, cluster, nclusters, sk, U, total, per, p.E, off, unit, err, abort_flag);
     int e, local_tile, kb0, kb1, slot, blocks, tn, tk;
     int64_t unit0;
     bool partial;
@@ -186,15 +207,15 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
             const int n0 = tn * 256 + static_cast<int>(rank) * 128, k0 = tk * 256 + static_cast<int>(rank) * kcols;
             const int abox = kcols / 64;
             for (int kb = kb0; kb < kb1; ++kb) {
-                const int r0 = lo + kb * 64;
-                const bool whole = hi - r0 >= 64;
+                const int r0 = lo + kb * 64, left = hi - r0;
+                const bool whole = left >= 64;
+                const int rows16 = whole ? 64 : (max(left, 1) + 15) & ~15;
                 if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
                     ok = false;
                     break;
                 }
-                const int boxes = whole ? 2 + abox : 0;
                 if (rank == 0)
-                    mbar_arrive_expect_tx_w(&full[stage], 2u * static_cast<uint32_t>(boxes * kMnBoxBytes));
+                    mbar_arrive_expect_tx_w(&full[stage], 2u * static_cast<uint32_t>((2 + abox) * rows16 * 128));
                 const uint32_t bar0 = mapa_shared(smem_u32(&full[stage]), 0);
                 uint8_t *sd = smem + stage * kWgStageBytes, *sa = sd + 16384;
                 if (whole) {
@@ -203,6 +224,29 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                     tma_load_2d_pair_w(sa, &p.tmA, bar0, k0, r0);
                     if (abox == 2)
                         tma_load_2d_pair_w(sa + kMnBoxBytes, &p.tmA, bar0, k0 + kMnBox, r0);
+                } else {
+                    for (int i = 0; i + 16 <= left; i += 16) {
+                        tma_load_2d_pair_w(sd + i * 128, &p.tmD16, bar0, n0, r0 + i);
+                        tma_load_2d_pair_w(sd + kMnBoxBytes + i * 128, &p.tmD16, bar0, n0 + kMnBox, r0 + i);
+                        tma_load_2d_pair_w(sa + i * 128, &p.tmA16, bar0, k0, r0 + i);
+                        if (abox == 2)
+                            tma_load_2d_pair_w(sa + kMnBoxBytes + i * 128, &p.tmA16, bar0, k0 + kMnBox, r0 + i);
+                    }
+                    // lane 4 b + g: rows 4 g .. 4 g + 3 of the last sixteen, box b
+                    // of dD (0, 1) or A (2, 3)
+                    const int in = rows16 - 16 + 4 * (lane & 3), b = lane >> 2;
+                    if (max(left, 0) % 16 || left <= 0) {
+                        if (b < 2 + abox) {
+                            int4 r;
+                            r.x = in + 0 < left ? r0 + in + 0 : p.R;
+                            r.y = in + 1 < left ? r0 + in + 1 : p.R;
+                            r.z = in + 2 < left ? r0 + in + 2 : p.R;
+                            r.w = in + 3 < left ? r0 + in + 3 : p.R;
+                            tma_gather4_pair_to(smem_u32(b < 2 ? sd : sa) + (b & 1) * kMnBoxBytes + in * 128,
+                                                b < 2 ? &p.tmDg : &p.tmAg, bar0, (b < 2 ? n0 : k0) + (b & 1) * kMnBox, r);
+                        }
+                        __syncwarp();
+                    }
                 }
                 ++issued;
                 if (++stage == kWgStages) {
@@ -263,49 +307,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 mma_commit_pair_w(&tfull[acc], 0x3);
             }
         }
-    } else if (warp >= 10) {
-        // ------------------------------------ copies of the ends of groups
-        const int cw = warp - 10, piece = lane & 7, sub = lane >> 3;
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        while (ok && walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
-            tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
-            const int lo = off[e], hi = lo + walk.rows(e);
-            const int kcols = p.K - tk * 256 <= 128 ? 64 : 128;
-            const int n0 = tn * 256 + static_cast<int>(rank) * 128, k0 = tk * 256 + static_cast<int>(rank) * kcols;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
-                    ok = false;
-                    break;
-                }
-                const int r0 = lo + kb * 64, left = hi - r0;
-                // 16 rows per warp: rows past the MMA's last step are not needed
-                if (left < 64 && cw * 16 < max(left, 1)) {
-                    const uint32_t sd = smem_u32(smem + stage * kWgStageBytes), sa = sd + 16384;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int b = i >> 2, r = cw * 16 + 4 * (i & 3) + sub;
-                        const uint32_t at = b * kMnBoxBytes + r * 128 + ((piece ^ (r & 7)) << 4);
-                        const int n = n0 + b * kMnBox + piece * 8, k = k0 + b * kMnBox + piece * 8;
-                        int bytes = r < left ? min(16, max(0, (p.N - n) * 2)) : 0;
-                        copy16(sd + at, bytes ? p.dD + (r0 + r) * p.ldd + n : p.dD, bytes);
-                        if (b * kMnBox < kcols) {
-                            bytes = r < left ? min(16, max(0, (p.K - k) * 2)) : 0;
-                            copy16(sa + at, bytes ? p.A + (r0 + r) * p.lda + k : p.A, bytes);
-                        }
-                    }
-                    copies_done();
-                    arrive_copied(&full[stage]);
-                } else if (lane == 0) {
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&full[stage]), 0));     // nothing to hand over
-                }
-                if (++stage == kWgStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
+    } else if (warp == 10) {
+        feed_run(feed_smem, rank, total - sk, nclusters, p.feed, err, abort_flag);
     } else {
         // ---------------------------------------------------- epilogue
         const int ew = warp - 2, half = ew / 4, q = warp & 3;

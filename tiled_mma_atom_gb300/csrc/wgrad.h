@@ -7,8 +7,8 @@ namespace tmg {
 
 struct WgradTmaArgs {
     CUtensorMap tmD, tmA;      // dD (R, N) and A (R, K), boxes of 64 columns x 64 rows
-    const uint16_t *dD, *A;    // the same operands, for the rows that warps copy
-    int64_t ldd, lda;          // row strides in elements
+    CUtensorMap tmD16, tmA16;  // the same, boxes of 16 rows
+    CUtensorMap tmDg, tmAg;    // the same, boxes of one row (gathers)
     void *dB;                  // (E, N, K) contiguous
     const int32_t *offsets;
     int R, N, K, E;
@@ -17,6 +17,7 @@ struct WgradTmaArgs {
     int vec_ok;
     float *partials;           // wgrad_partial_bytes()
     uint32_t *counters;        // 16 per tile of two waves
+    uint32_t *feed;            // the tile counter
 };
 size_t wgrad_partial_bytes(int num_sms);
 cudaError_t launch_wgrad(const WgradTmaArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s);

@@ -86,14 +86,13 @@ def moe_route(logits: torch.Tensor, k: int, *, normalize: bool = True, stream=No
         raise TypeError(f"unsupported logits dtype {logits.dtype}: use float32 or bfloat16")
     _check("logits", logits, logits.dtype, (T, E))
     dev = logits.device
-    n = T * k
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    plan = torch.empty(3 * n + E + 1, dtype=torch.int32, device=dev)     # one allocation for the whole plan
-    experts, slots, rows, offsets = plan[:n].view(T, k), plan[n:2 * n].view(T, k), plan[2 * n:3 * n], plan[3 * n:]
-    p = plan.data_ptr()
+    i32 = torch.int32
+    weights, experts = torch.empty((T, k), dtype=torch.float32, device=dev), torch.empty((T, k), dtype=i32, device=dev)
+    offsets, rows = torch.empty(E + 1, dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev)
+    slots = torch.empty((T, k), dtype=i32, device=dev)
     st = _native.lib().tmg_moe_route(logits.data_ptr(), T, E, k, logits.stride(0), dt, 1 if normalize else 0,
-                                     weights.data_ptr(), p, p + 12 * n, p + 8 * n, p + 4 * n,
-                                     _stream(stream, (logits, weights, plan)))
+                                     weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+                                     slots.data_ptr(), _stream(stream, (logits, weights, experts, offsets, rows, slots)))
     if st:
         _native.raise_on(st)
     return Routing(weights, experts, offsets, rows, slots)
