@@ -308,7 +308,13 @@ tmg_status tmg_gemm_skinny_noalloc(const void *A, const void *B, void *D,
  * expert, keeping their order, and each pair's place in that order is its
  * slot: the row of the grouped products' operands that belongs to it.  The
  * FlyDSL pages have no counterpart; the products read their operands in the
- * convention of tmg_gemm (A rows by K, each expert's B as N by K). */
+ * convention of tmg_gemm (A rows by K, each expert's B as N by K).
+ *
+ * Workspace of these calls and of tmg_linear is per (device, stream) and grown
+ * on demand, so a call that needs more than the ones before must not come
+ * inside a stream capture: make it once outside.  A captured graph stays valid
+ * when later calls grow the workspace (the old one is kept until
+ * tmg_shutdown). */
 
 /* The activation of the grouped and the dense products. */
 typedef enum {

@@ -341,6 +341,30 @@ def test_grouped_on_another_stream(tmg):
     tmg.check(s)
 
 
+def test_captured_graph_survives_growing_workspace(tmg):
+    """A graph with a split contraction (partials in workspace), replayed after
+    larger calls on the same stream have outgrown its workspace."""
+    A, B, off = ints((4, 4096), 53), ints((1, 512, 4096), 54), offsets_of([4])
+    dA, dB, dO, D = A.to(DEV), B.to(DEV), off.to(DEV), torch.empty((4, 512), dtype=BF16, device=DEV)
+    big, W, o2 = ints((900, 4096), 55).to(DEV), ints((2, 520, 4096), 56).to(DEV), offsets_of([300, 600]).to(DEV)
+    rows = torch.arange(900, dtype=torch.int32, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        tmg.grouped_gemm(dA, dB, dO, D)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            tmg.grouped_gemm(dA, dB, dO, D)
+        tmg.grouped_gemm(big, W, o2, rows=rows)
+        tmg.grouped_gemm_wgrad(big, big, o2)
+        D.zero_()
+        for _ in range(2):
+            g.replay()
+    torch.cuda.current_stream().wait_stream(s)
+    exact(D, product(A, B, off)[0])
+    tmg.check(s)
+
+
 # ------------------------------------------------------------- weight gradient
 
 def wgrad(dD, A, off, rows):

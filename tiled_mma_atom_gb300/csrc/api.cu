@@ -27,6 +27,7 @@
 #include <mutex>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "host.h"
 
@@ -65,6 +66,7 @@ struct Scratch {
     cudaEvent_t ev[kHostEvents] = {};
 };
 std::map<std::pair<int, uintptr_t>, Scratch> g_scratch;
+std::vector<std::pair<int, void *>> g_retired;     // outgrown workspaces, by device
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -333,19 +335,28 @@ void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st)
     Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
     cudaError_t e;
     if (sc.ws_bytes[which] < bytes) {
+        // A grown buffer's old one stays until tmg_shutdown: a CUDA graph
+        // captured earlier on this stream may still name it.  Growing by half
+        // at least keeps what is kept below twice the largest.
+        const size_t half_more = sc.ws_bytes[which] + sc.ws_bytes[which] / 2;
+        const size_t size = bytes > half_more ? bytes : half_more;
+        void *fresh = nullptr;
         if (sc.ws[which])
-            cudaFree(sc.ws[which]);
-        sc.ws[which] = nullptr;
-        sc.ws_bytes[which] = 0;
-        if ((e = cudaMalloc(&sc.ws[which], bytes)) != cudaSuccess) {
+            g_retired.reserve(g_retired.size() + 1);
+        if ((e = cudaMalloc(&fresh, size)) != cudaSuccess) {
+            cudaGetLastError();       // not a launch error of a later call
             *st = cuda_fail(e, "cudaMalloc(workspace)");
             return nullptr;
         }
-        if (which == kWsCounters && (e = cudaMemsetAsync(sc.ws[which], 0, bytes, s)) != cudaSuccess) {
+        if (which == kWsCounters && (e = cudaMemsetAsync(fresh, 0, size, s)) != cudaSuccess) {
+            cudaFree(fresh);
             *st = cuda_fail(e, "cudaMemsetAsync(counters)");
             return nullptr;
         }
-        sc.ws_bytes[which] = bytes;
+        if (sc.ws[which])
+            g_retired.emplace_back(dev, sc.ws[which]);
+        sc.ws[which] = fresh;
+        sc.ws_bytes[which] = size;
     }
     *st = TMG_OK;
     return sc.ws[which];
@@ -1534,6 +1545,11 @@ void tmg_shutdown(void)
         }
     }
     g_scratch.clear();
+    for (auto &r : g_retired) {
+        cudaSetDevice(r.first);
+        cudaFree(r.second);
+    }
+    g_retired.clear();
     cudaSetDevice(cur);
     std::lock_guard<std::mutex> lk2(g_map_mu);
     g_maps.clear();

@@ -37,7 +37,8 @@ tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const v
                      const int64_t *strides, const int *box);
 
 // Workspaces of the grouped products, the dense product with the residual
-// epilogue and the routing, per (device, stream), grown on demand.
+// epilogue and the routing, per (device, stream), grown on demand; an outgrown
+// one is kept until tmg_shutdown.
 enum Workspace {
     kWsPackA,          // operand copies with 16-byte rows
     kWsPackB,
