@@ -6,6 +6,7 @@
 
 #include "act.cuh"
 #include "grouped.h"
+#include "launch.cuh"
 
 namespace tmg {
 namespace {
@@ -18,6 +19,8 @@ __global__ void __launch_bounds__(256)
                     int64_t M, int64_t N, __nv_bfloat16 *__restrict__ dz, float *__restrict__ partials)
 {
     __shared__ float red[8][kCols];
+    grid_release();
+    grid_wait();
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + tx * 8;
     const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRowsPerChunk;
@@ -76,6 +79,8 @@ __global__ void __launch_bounds__(256)
     column_sum_kernel(const float *__restrict__ partials, int chunks, int64_t N, float *__restrict__ out)
 {
     __shared__ float red[8][32];
+    grid_release();
+    grid_wait();
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + tx;
     float v = 0.f;
@@ -101,12 +106,8 @@ cudaError_t launch_act(const void *dD, int64_t ldd, const void *Z, int64_t ldp, 
     const bool vec = N % 8 == 0 && ok(dD, ldd) && (ACT == kActNone || ok(Z, ldp)) && ok(dz, N);
     const dim3 grid(static_cast<unsigned>(act_grad_chunks(M)), static_cast<unsigned>((N + kCols - 1) / kCols));
     const __nv_bfloat16 *d = static_cast<const __nv_bfloat16 *>(dD), *z = static_cast<const __nv_bfloat16 *>(Z);
-    note_launch();
-    if (vec)
-        act_grad_kernel<ACT, true><<<grid, 256, 0, s>>>(d, ldd, z, ldp, M, N, static_cast<__nv_bfloat16 *>(dz), partials);
-    else
-        act_grad_kernel<ACT, false><<<grid, 256, 0, s>>>(d, ldd, z, ldp, M, N, static_cast<__nv_bfloat16 *>(dz), partials);
-    return cudaGetLastError();
+    return launch_overlapped(vec ? act_grad_kernel<ACT, true> : act_grad_kernel<ACT, false>, grid, 256, 0, 1, s, d, ldd, z, ldp, M,
+                             N, static_cast<__nv_bfloat16 *>(dz), partials);
 }
 
 }  // namespace
@@ -125,9 +126,8 @@ cudaError_t launch_act_grad(const void *dD, int64_t ldd, const void *preact, int
     }
     if (e != cudaSuccess || !dbias)
         return e;
-    note_launch();
-    column_sum_kernel<<<static_cast<unsigned>((N + 31) / 32), 256, 0, s>>>(partials, act_grad_chunks(M), N, dbias);
-    return cudaGetLastError();
+    return launch_overlapped(column_sum_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 256, 0, 1, s, partials,
+                             act_grad_chunks(M), N, dbias);
 }
 
 }  // namespace tmg

@@ -121,6 +121,36 @@ tmg_status gather(const DeviceState &ds, const void **A, int64_t *lda, int64_t s
     return TMG_OK;
 }
 
+// Nanoseconds that a CTA pair takes for one K block of a tile of w columns
+// (measured on the CTA-pair GEMM; below 128 columns the MMA issue is the limit).
+float block_ns(int w)
+{
+    return w <= 128 ? 210.f : w <= 160 ? 226.f : w <= 192 ? 244.f : w <= 224 ? 281.f : 320.f;
+}
+
+// Widest tile.  One group: the width whose waves of tiles take the least time
+// (4096 rows by 4096 columns: 19 x 16 tiles of 224 are four waves of 76 pairs,
+// 16 x 16 of 256 are four waves too).  Several: all rows of an evenly filled
+// group, with room for half as many again; narrower tiles make a deeper ring.
+int tile_width(const GroupedArgs &a, int64_t tiles_n, int pairs)
+{
+    if (a.E > 1) {
+        const int64_t even = (a.R + a.E - 1) / a.E, room = even + even / 2 + 8;
+        return static_cast<int>(room >= kSwMaxW ? kSwMaxW : up(room, 32));
+    }
+    int best = 0;
+    double best_ns = 0;
+    for (int w = kSwMaxW; w >= 32; w -= 32) {
+        const int64_t tiles = (a.R + w - 1) / w * tiles_n;
+        const double ns = static_cast<double>((tiles + pairs - 1) / pairs) * block_ns(w);
+        if (!best || ns < best_ns || (ns == best_ns && a.R <= w)) {
+            best = w;
+            best_ns = ns;
+        }
+    }
+    return best;
+}
+
 tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t s)
 {
     const bool swiglu = a.epi.act == kActSwiglu;
@@ -134,11 +164,9 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     // a copied operand's rows are padded (the other's out-of-range reads are zeros)
     const int64_t K = a.K > 0 ? a.K : align;
 
-    // Widest tile: all rows of an evenly filled group, with room for half as
-    // many again; narrower stages make a deeper ring.
-    const int64_t even = (a.R + a.E - 1) / a.E;
-    const int64_t room = a.E == 1 ? even : even + even / 2 + 8;
-    p.maxw = static_cast<int>(room >= kSwMaxW ? kSwMaxW : up(room, 32));
+    const int pairs = ds.num_sms / 2;
+    const int64_t tiles_n = (F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+    p.maxw = tile_width(a, tiles_n, pairs);
     p.gather = a.rows && p.maxw <= kSwGatherW;
 
     // A: rows of K read in place, or copied; with row numbers and wide tiles,
@@ -219,17 +247,18 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     while (sw_smem(p.stages, p.stage_bytes, p.E) > 232448)
         --p.stages;
     p.group = 16 * p.maxw * K * elem <= (int64_t{32} << 20) ? 16 : 8;
-    const int64_t tiles_n = (F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
     if ((a.R / 32 + a.E) * tiles_n > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
-    const int pairs = ds.num_sms / 2;
-    p.split_cost = 8 + p.maxw * 24 / kSwMaxW;
-    if ((K + kb - 1) / kb > p.split_cost) {
+    // A split tile's partials go through L2 and its epilogue starts over: 6 us
+    // with one 32-column chunk per epilogue warp, 4 us more for every other
+    p.block_ns = block_ns(p.maxw);
+    p.split_ns = 6000.f + 4000.f * ((p.maxw + 63) / 64 - 1);
+    if ((K + kb - 1) / kb * p.block_ns > p.split_ns) {
         p.partials = static_cast<float *>(workspace(kWsPartials, pairs * sw_partial_floats(p.maxw) * sizeof(float), s, &st));
         if (!p.partials)
             return st;
     } else {
-        p.split_cost = -1;
+        p.split_ns = -1.f;
     }
     if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
         return st;

@@ -1,0 +1,54 @@
+// launch.cuh — launches that overlap the end of the kernel before them in the
+// stream (programmatic dependent launch).
+//
+// A kernel launched so may start while its predecessor's last blocks still
+// run: it sets up what depends on no memory (barriers, TMEM, descriptors) and
+// then waits for the predecessor's end and the visibility of its writes, before
+// its first read or write of global memory.  Every kernel of these calls also
+// lets its own successor start early, at its own start: the successor's blocks
+// take the SMs' free room and wait there.  A predecessor or successor that is
+// not launched so simply runs in stream order.  Measured on calls of one
+// product in a row: PDL_MEASURED.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace tmg {
+
+// First statement that may touch global memory comes after this.
+__device__ __forceinline__ void grid_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The next kernel in the stream may start.
+__device__ __forceinline__ void grid_release()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    note_launch();
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace tmg

@@ -5,6 +5,7 @@
 // run along the source's smaller stride, writes along k.  And the gather of
 // rows by number, for products whose tiles are too wide for TMA gathers.
 #include "grouped.h"
+#include "launch.cuh"
 
 namespace tmg {
 namespace {
@@ -17,6 +18,8 @@ __global__ void __launch_bounds__(256) pack3_kernel(Pack3Args a, int64_t tiles_k
     T *dst = static_cast<T *>(a.dst);
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
     const bool along_rows = a.s_row < a.s_col;
+    grid_release();
+    grid_wait();
     for (int64_t i = blockIdx.x; i < tiles_k * tiles_r * a.E; i += gridDim.x) {
         const int64_t k0 = i % tiles_k * 32, r0 = i / tiles_k % tiles_r * 32, e = i / (tiles_k * tiles_r);
 #pragma unroll
@@ -42,6 +45,8 @@ __global__ void __launch_bounds__(256)
                        const int32_t *__restrict__ numbers, int64_t rows, char *__restrict__ dst, int64_t dst_stride)
 {
     const int lane = threadIdx.x % 32, pieces = static_cast<int>(dst_stride / 16), whole = bytes / 16;
+    grid_release();
+    grid_wait();
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; r < rows; r += gridDim.x * 8ll) {
         const int64_t from = __ldg(numbers + r);
         const bool there = from >= 0 && from < src_rows;
@@ -74,11 +79,9 @@ cudaError_t launch_gather_rows(const void *src, int64_t stride, int64_t src_rows
     const int64_t blocks = (rows + 7) / 8;
     if (rows == 0)
         return cudaSuccess;
-    note_launch();
-    gather_rows_kernel<<<static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8), 256, 0, s>>>(
-        static_cast<const char *>(src), stride, src_rows, static_cast<int>(bytes), numbers, rows, static_cast<char *>(dst),
-        dst_stride);
-    return cudaGetLastError();
+    return launch_overlapped(gather_rows_kernel, dim3(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8)), 256, 0,
+                             1, s, static_cast<const char *>(src), stride, src_rows, static_cast<int>(bytes), numbers, rows,
+                             static_cast<char *>(dst), dst_stride);
 }
 
 cudaError_t launch_pack3(const Pack3Args &a, int elem, int num_sms, cudaStream_t s)
@@ -87,12 +90,7 @@ cudaError_t launch_pack3(const Pack3Args &a, int elem, int num_sms, cudaStream_t
     if (total == 0)
         return cudaSuccess;
     const unsigned blocks = static_cast<unsigned>(total < num_sms * 8 ? total : num_sms * 8);
-    note_launch();
-    if (elem == 1)
-        pack3_kernel<uint8_t><<<blocks, 256, 0, s>>>(a, tk, tr);
-    else
-        pack3_kernel<uint16_t><<<blocks, 256, 0, s>>>(a, tk, tr);
-    return cudaGetLastError();
+    return launch_overlapped(elem == 1 ? pack3_kernel<uint8_t> : pack3_kernel<uint16_t>, dim3(blocks), 256, 0, 1, s, a, tk, tr);
 }
 
 }  // namespace tmg

@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "grouped.h"
+#include "launch.cuh"
 
 namespace tmg {
 namespace {
@@ -208,6 +209,8 @@ __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a)
     int32_t *counts = sm, *base = sm + a.E, *wc = base + a.E, *pairs = wc + warps * a.E;
     for (int i = threadIdx.x; i < (2 + warps) * a.E; i += blockDim.x)
         sm[i] = 0;
+    grid_release();
+    grid_wait();
     __syncthreads();
     choose<C>(a, 0, a.T, counts, pairs);
     __syncthreads();
@@ -228,6 +231,8 @@ __global__ void __launch_bounds__(1024) route_choose_kernel(RouteArgs a, int tok
     extern __shared__ int32_t counts[];
     for (int e = threadIdx.x; e < a.E; e += blockDim.x)
         counts[e] = 0;
+    grid_release();
+    grid_wait();
     __syncthreads();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
     choose<C>(a, t0, min(a.T, t0 + tokens_per_block), counts, nullptr);
@@ -245,6 +250,8 @@ __global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens
     int32_t *base = sm, *total = sm + E, *wc = total + E;
     for (int i = threadIdx.x; i < (2 + warps) * E; i += blockDim.x)
         sm[i] = 0;
+    grid_release();
+    grid_wait();
     __syncthreads();
     // counts in the blocks before this one, and in all: each warp adds up
     // every warps-th block, 128 experts at a time
@@ -294,6 +301,8 @@ __global__ void __launch_bounds__(256)
 {
     const int lane = threadIdx.x % 32;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
+    grid_release();
+    grid_wait();
     for (int64_t t = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32; t < T; t += warps) {
         int e = -1;
         float dw = 0.f, x = kNegInf;
@@ -399,6 +408,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a,
 {
     const int64_t t = blockIdx.x / parts;
     const int64_t h = ((blockIdx.x % parts) * kCombineThreads + threadIdx.x) * 8;
+    grid_release();
+    grid_wait();
     if (h >= a.H)
         return;
     float acc[8] = {};
@@ -426,6 +437,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineGradArgs a
 {
     __shared__ float part[8][kMaxChoices];
     const int64_t t = blockIdx.x;
+    grid_release();
+    grid_wait();
     float dot[kMaxChoices];
 #pragma unroll
     for (int j = 0; j < kMaxChoices; ++j)
@@ -483,7 +496,6 @@ int tokens_per_block(int64_t T, int num_sms) { return static_cast<int>((T + 2 * 
 template <int C>
 cudaError_t launch_route_as(const RouteArgs &a, int num_sms, cudaStream_t s)
 {
-    note_launch();
     if (a.T <= kOneBlockTokens) {
         // a warp per token; fewer counters where there are fewer tokens
         const int warps = static_cast<int>(a.T < 4 ? 4 : a.T < 16 ? a.T : 16);
@@ -491,20 +503,16 @@ cudaError_t launch_route_as(const RouteArgs &a, int num_sms, cudaStream_t s)
         const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(route_one_kernel<C>), bytes);
         if (e != cudaSuccess)
             return e;
-        route_one_kernel<C><<<1, warps * 32, bytes, s>>>(a);
-        return cudaGetLastError();
+        return launch_overlapped(route_one_kernel<C>, dim3(1), warps * 32, bytes, 1, s, a);
     }
     const int each = tokens_per_block(a.T, num_sms), blocks = route_blocks(a.T, num_sms);
-    route_choose_kernel<C><<<blocks, 1024, a.E * sizeof(int32_t), s>>>(a, each);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_overlapped(route_choose_kernel<C>, dim3(blocks), 1024, a.E * sizeof(int32_t), 1, s, a, each);
     if (e != cudaSuccess)
         return e;
     const int bytes = static_cast<int>(18 * a.E * sizeof(int32_t));
     if ((e = ensure_smem_attr(reinterpret_cast<const void *>(route_plan_kernel), bytes)) != cudaSuccess)
         return e;
-    note_launch();
-    route_plan_kernel<<<blocks, 512, bytes, s>>>(a, each, blocks);
-    return cudaGetLastError();
+    return launch_overlapped(route_plan_kernel, dim3(blocks), 512, bytes, 1, s, a, each, blocks);
 }
 
 bool vec8(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
@@ -535,32 +543,22 @@ cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int6
                 : E <= 128 ? route_backward_kernel<4>
                 : E <= 256 ? route_backward_kernel<8>
                            : route_backward_kernel<32>;
-    note_launch();
-    kern<<<blocks, 256, 0, s>>>(logits, bf16, T, ld, E, k, normalize, experts, dweights, dlogits);
-    return cudaGetLastError();
+    return launch_overlapped(kern, dim3(blocks), 256, 0, 1, s, logits, bf16, T, ld, E, k, normalize, experts, dweights, dlogits);
 }
 
 cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s)
 {
     const int64_t parts = (a.H + kCombineThreads * 8 - 1) / (kCombineThreads * 8);
     const bool vec = a.H % 8 == 0 && vec8(a.Y, a.ldy) && vec8(a.out, a.ldo) && (!a.residual || vec8(a.residual, a.ldr));
-    note_launch();
-    if (vec)
-        combine_kernel<true><<<static_cast<unsigned>(a.T * parts), kCombineThreads, 0, s>>>(a, parts);
-    else
-        combine_kernel<false><<<static_cast<unsigned>(a.T * parts), kCombineThreads, 0, s>>>(a, parts);
-    return cudaGetLastError();
+    return launch_overlapped(vec ? combine_kernel<true> : combine_kernel<false>, dim3(static_cast<unsigned>(a.T * parts)),
+                             kCombineThreads, 0, 1, s, a, parts);
 }
 
 cudaError_t launch_combine_backward(const CombineGradArgs &a, cudaStream_t s)
 {
     const bool vec = a.H % 8 == 0 && vec8(a.Y, a.ldy) && vec8(a.dOut, a.ldo) && vec8(a.dY, a.H);
-    note_launch();
-    if (vec)
-        combine_backward_kernel<true><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
-    else
-        combine_backward_kernel<false><<<static_cast<unsigned>(a.T), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(vec ? combine_backward_kernel<true> : combine_backward_kernel<false>,
+                             dim3(static_cast<unsigned>(a.T)), 256, 0, 1, s, a);
 }
 
 }  // namespace tmg

@@ -38,6 +38,8 @@
 #include "act.cuh"
 #include "feed.cuh"
 #include "grouped.h"
+#include "launch.cuh"
+#include "pieces.cuh"
 #include "tc2_kernel.cuh"
 
 namespace tmg {
@@ -59,7 +61,8 @@ struct SwapArgs {
     int maxw;                  // widest tile, a multiple of 32
     int stages, stage_bytes;
     int group;                 // row tiles per band
-    int split_cost;            // cost of a stream-K tail in K blocks; < 0: never split
+    float block_ns;            // a K block of a tile of maxw columns
+    float split_ns;            // what a stream-K tail adds; < 0: never split
     float *partials;           // sw_partial_floats(maxw) per pair
     uint32_t *counters;        // 16 per tile of two waves
     uint32_t *feed;            // the tile counter
@@ -516,8 +519,6 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     constexpr int OUT = EPI == kSwSwiglu ? 128 : 256;          // output columns of a tile
     const int tiles_n = (p.N + OUT - 1) / OUT, num_kb = (p.K + KB - 1) / KB;
 
-    for (int i = threadIdx.x; i <= p.E; i += kSwThreads)
-        off[i] = p.offsets ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&full[s], 1);
@@ -537,6 +538,10 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
+    grid_release();
+    grid_wait();
+    for (int i = threadIdx.x; i <= p.E; i += kSwThreads)
+        off[i] = p.offsets ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
     __syncthreads();
     if (warp == 2) {                 // tiles before each group
         int run = 0;
@@ -562,14 +567,18 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    // Whole tiles, or the last waves split: the saving is the share of the
-    // last wave's K blocks that idle pairs would have waited.
+    // Whole tiles, or the last waves split.  Times in ns: a K block of a tile
+    // takes p.block_ns of a pair, and HBM (6.7 TB/s) takes 4.8 for the 32 KB of
+    // its weights (narrow tiles read their weights once each); a split adds
+    // p.split_ns.
     const int total = start[p.E], rem = total % nclusters;
     int sk = 0;
-    if (rem && p.split_cost >= 0) {
+    if (rem && p.split_ns >= 0) {
         const int take = rem + (total > nclusters ? nclusters : 0);
-        if (static_cast<int64_t>(num_kb) * (nclusters - rem) > static_cast<int64_t>(p.split_cost) * nclusters &&
-            static_cast<int64_t>(take) * num_kb >= nclusters)
+        const float blocks = static_cast<float>(total) * num_kb, hbm = p.maxw < kSwMaxW ? 4.8f * blocks : 0.f;
+        const float whole = fmaxf(hbm, (total / nclusters + 1.f) * num_kb * p.block_ns);
+        const float split = fmaxf(hbm, blocks / nclusters * p.block_ns) + p.split_ns;
+        if (whole > split && static_cast<int64_t>(take) * num_kb >= nclusters)
             sk = take;
     }
     SwapWalk walk(feed_smem, cluster, nclusters, total, sk, num_kb, err, abort_flag);
@@ -754,21 +763,11 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 if (half < chunks) {
-                    __threadfence();
-                    __syncwarp();
                     c_first = unit_owner(static_cast<int64_t>(tile) * num_kb, U, nclusters);
                     c_last = unit_owner(static_cast<int64_t>(tile + 1) * num_kb - 1, U, nclusters);
                     const int64_t at = (static_cast<int64_t>(tile) * 2 + rank) * 8 + ew;
-                    uint32_t old = 0;
-                    if (lane == 0 && bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters))
-                        old = atomicAdd(p.counters + at, 1u);
-                    old = __shfl_sync(0xffffffffu, old, 0);
-                    finish = old == static_cast<uint32_t>(c_last - c_first);
-                    if (finish) {
-                        __threadfence();     // last to arrive: the other pairs' pieces are visible
-                        if (lane == 0)
-                            p.counters[at] = 0;
-                    }
+                    finish = last_arrival(p.counters + at, c_last - c_first,
+                                          bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters));
                 }
             }
             if (finish) {
@@ -790,21 +789,10 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] = 0.f;
-                        for (int cc = c_first; cc <= c_last; ++cc) {
+                        add_pieces(v, p.partials, limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
                             const int s2 = static_cast<int>((U * cc / nclusters) / num_kb) == tile ? 0 : 1;
-                            const int64_t src = ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * piece;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int64_t at = src + ((c * 8 + j) * 32 + lane) * 4;
-                                if (!span_ok(at, 4, limit, err, kBndPartials))
-                                    continue;
-                                const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.partials + at));
-                                v[4 * j] += f.x;
-                                v[4 * j + 1] += f.y;
-                                v[4 * j + 2] += f.z;
-                                v[4 * j + 3] += f.w;
-                            }
-                        }
+                            return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * piece;
+                        }, err);
                     }
                     finish_chunk<EPI>(p, v, stg, lane, r0, nt, n0, sa, sb, bias, pre, [&] { ahead(c + 2); }, err);
                 }
@@ -835,21 +823,7 @@ cudaError_t launch_swap_as(const SwapArgs &a, int num_sms, const ErrCtx &err, cu
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms / 2));
-    cfg.blockDim = dim3(kSwThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    note_launch();
-    e = cudaLaunchKernelEx(&cfg, kern, a, err);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_overlapped(kern, dim3(2 * (num_sms / 2)), kSwThreads, smem, 2, s, a, err);
 }
 
 }  // namespace

@@ -22,6 +22,8 @@
 // pair order.  Roles as in swap_kernel.cuh.
 #include "feed.cuh"
 #include "grouped.h"
+#include "launch.cuh"
+#include "pieces.cuh"
 #include "tc2_kernel.cuh"
 #include "wgrad.h"
 
@@ -124,8 +126,6 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
     const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
 
-    for (int i = threadIdx.x; i <= p.E; i += kWgThreads)
-        off[i] = min(max(__ldg(p.offsets + i), 0), p.R);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kWgStages; ++s) {
             mbar_init(&full[s], 1);
@@ -150,6 +150,10 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
+    grid_release();
+    grid_wait();
+    for (int i = threadIdx.x; i <= p.E; i += kWgThreads)
+        off[i] = min(max(__ldg(p.offsets + i), 0), p.R);
     __syncthreads();
     if (warp == 2) {                 // blocks before each group
         int run = 0;
@@ -348,21 +352,11 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 if (half < c1) {
-                    __threadfence();
-                    __syncwarp();
                     c_first = unit_owner(unit0, U, nclusters);
                     c_last = unit_owner(unit0 + blocks - 1, U, nclusters);
                     const int64_t at = ((static_cast<int64_t>(e) * per + local_tile) * 2 + rank) * 8 + ew;
-                    uint32_t old = 0;
-                    if (lane == 0 && bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters))
-                        old = atomicAdd(p.counters + at, 1u);
-                    old = __shfl_sync(0xffffffffu, old, 0);
-                    finish = old == static_cast<uint32_t>(c_last - c_first);
-                    if (finish) {
-                        __threadfence();
-                        if (lane == 0)
-                            p.counters[at] = 0;
-                    }
+                    finish = last_arrival(p.counters + at, c_last - c_first,
+                                          bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters));
                 }
             }
             if (finish) {
@@ -381,21 +375,10 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             v[j] = 0.f;
-                        for (int cc = c_first; cc <= c_last; ++cc) {
+                        add_pieces(v, p.partials, p_limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
                             const int s2 = U * cc / nclusters >= unit0 ? 0 : 1;       // its run begins in this tile
-                            const int64_t src = ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * kWgPiece;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int64_t at = src + ((c * 8 + j) * 32 + lane) * 4;
-                                if (!span_ok(at, 4, p_limit, err, kBndPartials))
-                                    continue;
-                                const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.partials + at));
-                                v[4 * j] += f.x;
-                                v[4 * j + 1] += f.y;
-                                v[4 * j + 2] += f.z;
-                                v[4 * j + 3] += f.w;
-                            }
-                        }
+                            return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * kWgPiece;
+                        }, err);
                     }
                     const int col0 = tk * 256 + c * 32;
                     if (n < p.N && span_ok(row_off + col0, min(32, p.K - col0), d_limit, err, kBndStoreD))
@@ -430,21 +413,7 @@ cudaError_t launch_wgrad(const WgradTmaArgs &a, int num_sms, const ErrCtx &err, 
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(wgrad_kernel), smem);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms / 2));
-    cfg.blockDim = dim3(kWgThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    note_launch();
-    e = cudaLaunchKernelEx(&cfg, wgrad_kernel, a, err);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_overlapped(wgrad_kernel, dim3(2 * (num_sms / 2)), kWgThreads, smem, 2, s, a, err);
 }
 
 }  // namespace tmg
