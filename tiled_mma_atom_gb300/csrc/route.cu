@@ -401,9 +401,25 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *row, int64_t h, int64_t H,
     }
 }
 
+// The same as eight packed bf16.
+template <bool VEC>
+__device__ __forceinline__ uint4 load_packed8(const __nv_bfloat16 *row, int64_t h, int64_t H)
+{
+    if constexpr (VEC) {
+        return *reinterpret_cast<const uint4 *>(row + h);
+    } else {
+        float f[8];
+        load8<false>(row, h, H, f);
+        return pack8(f);        // bf16 values: exact
+    }
+}
+
+// Both kernels are bound by HBM: every Y row is read or written once.  A thread
+// keeps the k rows' loads of its eight columns in flight together (KMAX: the
+// next of 2, 4, 8, 16 choices).  COMBINE_MEASURED
 constexpr int kCombineThreads = 128;
 
-template <bool VEC>
+template <bool VEC, int KMAX>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a, int64_t parts)
 {
     const int64_t t = blockIdx.x / parts;
@@ -412,68 +428,86 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a,
     grid_wait();
     if (h >= a.H)
         return;
-    float acc[8] = {};
+    int32_t slot[KMAX];
+    float w[KMAX], acc[8] = {};
+    uint4 y[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+        const int32_t at = j < a.k ? __ldg(a.slots + t * a.k + j) : -1;
+        slot[j] = at < a.R ? at : -1;
+        w[j] = j < a.k && a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
+    }
     if (a.residual)
         load8<VEC>(static_cast<const __nv_bfloat16 *>(a.residual) + t * a.ldr, h, a.H, acc);
-    const __nv_bfloat16 *Y = static_cast<const __nv_bfloat16 *>(a.Y);
-    for (int j = 0; j < a.k; ++j) {
-        const int64_t slot = __ldg(a.slots + t * a.k + j);
-        if (slot < 0 || slot >= a.R)
-            continue;
-        const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
-        float y[8];
-        load8<VEC>(Y + slot * a.ldy, h, a.H, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            acc[i] = fmaf(w, y[i], acc[i]);
-    }
+    for (int j = 0; j < KMAX; ++j)
+        if (slot[j] >= 0)
+            y[j] = load_packed8<VEC>(static_cast<const __nv_bfloat16 *>(a.Y) + slot[j] * a.ldy, h, a.H);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+        if (slot[j] >= 0) {
+            float f[8];
+            unpack8(y[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[i] = fmaf(w[j], f[i], acc[i]);
+        }
     store8<VEC>(static_cast<__nv_bfloat16 *>(a.out) + t * a.ldo, h, a.H, acc);
 }
 
-constexpr int kMaxChoices = 16;
-
-template <bool VEC>
+template <bool VEC, int KMAX>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineGradArgs a)
 {
-    __shared__ float part[8][kMaxChoices];
+    __shared__ float part[8][KMAX];
     const int64_t t = blockIdx.x;
     grid_release();
     grid_wait();
-    float dot[kMaxChoices];
+    int32_t slot[KMAX];
+    float w[KMAX], dot[KMAX];
 #pragma unroll
-    for (int j = 0; j < kMaxChoices; ++j)
+    for (int j = 0; j < KMAX; ++j) {
+        const int32_t s = j < a.k ? __ldg(a.slots + t * a.k + j) : -1;
+        slot[j] = s < a.R ? s : -1;
+        w[j] = j < a.k && a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
         dot[j] = 0.f;
+    }
+    const __nv_bfloat16 *Y = static_cast<const __nv_bfloat16 *>(a.Y);
+    __nv_bfloat16 *dY = static_cast<__nv_bfloat16 *>(a.dY);
     for (int64_t h = threadIdx.x * 8; h < a.H; h += 256 * 8) {
         float d[8];
+        uint4 y[KMAX];
         load8<VEC>(static_cast<const __nv_bfloat16 *>(a.dOut) + t * a.ldo, h, a.H, d);
+        if (a.dweights) {
 #pragma unroll
-        for (int j = 0; j < kMaxChoices; ++j) {
-            if (j >= a.k)
-                break;
-            const int64_t slot = __ldg(a.slots + t * a.k + j);
-            if (slot < 0 || slot >= a.R)
-                continue;
-            const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
-            if (a.dweights) {
-                float y[8];
-                load8<VEC>(static_cast<const __nv_bfloat16 *>(a.Y) + slot * a.ldy, h, a.H, y);
+            for (int j = 0; j < KMAX; ++j)
+                if (slot[j] >= 0)
+                    y[j] = load_packed8<VEC>(Y + slot[j] * a.ldy, h, a.H);
+        }
+#pragma unroll
+        for (int j = 0; j < KMAX; ++j)
+            if (slot[j] >= 0) {
+                float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    dot[j] = fmaf(d[i], y[i], dot[j]);
+                    o[i] = w[j] * d[i];
+                store8<VEC>(dY + slot[j] * a.H, h, a.H, o);
             }
-            float o[8];
+        if (a.dweights) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                o[i] = w * d[i];
-            store8<VEC>(static_cast<__nv_bfloat16 *>(a.dY) + slot * a.H, h, a.H, o);
+            for (int j = 0; j < KMAX; ++j)
+                if (slot[j] >= 0) {
+                    float f[8];
+                    unpack8(y[j], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dot[j] = fmaf(d[i], f[i], dot[j]);
+                }
         }
     }
     if (!a.dweights)
         return;
 #pragma unroll
-    for (int j = 0; j < kMaxChoices; ++j) {
-        if (j >= a.k)
-            break;
+    for (int j = 0; j < KMAX; ++j) {
         const float v = warp_sum(dot[j]);
         if (threadIdx.x % 32 == 0)
             part[threadIdx.x / 32][j] = v;
@@ -482,8 +516,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineGradArgs a
     if (threadIdx.x < a.k) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
-            v += part[w][threadIdx.x];
+        for (int i = 0; i < 8; ++i)
+            v += part[i][threadIdx.x];
         a.dweights[t * a.k + threadIdx.x] = v;
     }
 }
@@ -550,15 +584,21 @@ cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s)
 {
     const int64_t parts = (a.H + kCombineThreads * 8 - 1) / (kCombineThreads * 8);
     const bool vec = a.H % 8 == 0 && vec8(a.Y, a.ldy) && vec8(a.out, a.ldo) && (!a.residual || vec8(a.residual, a.ldr));
-    return launch_overlapped(vec ? combine_kernel<true> : combine_kernel<false>, dim3(static_cast<unsigned>(a.T * parts)),
-                             kCombineThreads, 0, 1, s, a, parts);
+    auto kern = a.k <= 2   ? (vec ? combine_kernel<true, 2> : combine_kernel<false, 2>)
+                : a.k <= 4 ? (vec ? combine_kernel<true, 4> : combine_kernel<false, 4>)
+                : a.k <= 8 ? (vec ? combine_kernel<true, 8> : combine_kernel<false, 8>)
+                           : (vec ? combine_kernel<true, 16> : combine_kernel<false, 16>);
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(a.T * parts)), kCombineThreads, 0, 1, s, a, parts);
 }
 
 cudaError_t launch_combine_backward(const CombineGradArgs &a, cudaStream_t s)
 {
     const bool vec = a.H % 8 == 0 && vec8(a.Y, a.ldy) && vec8(a.dOut, a.ldo) && vec8(a.dY, a.H);
-    return launch_overlapped(vec ? combine_backward_kernel<true> : combine_backward_kernel<false>,
-                             dim3(static_cast<unsigned>(a.T)), 256, 0, 1, s, a);
+    auto kern = a.k <= 2   ? (vec ? combine_backward_kernel<true, 2> : combine_backward_kernel<false, 2>)
+                : a.k <= 4 ? (vec ? combine_backward_kernel<true, 4> : combine_backward_kernel<false, 4>)
+                : a.k <= 8 ? (vec ? combine_backward_kernel<true, 8> : combine_backward_kernel<false, 8>)
+                           : (vec ? combine_backward_kernel<true, 16> : combine_backward_kernel<false, 16>);
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(a.T)), 256, 0, 1, s, a);
 }
 
 }  // namespace tmg
