@@ -340,7 +340,8 @@ typedef enum {
  * Equal logits go to the lower expert.  Logits of -inf and NaN are never
  * chosen; where a token has fewer than k others, its remaining choices are
  * expert -1, weight 0, slot -1, and take no row.  T * k < 2^31.  Results do
- * not depend on timing.  Workspace: 8 E bytes per SM, per (device, stream). */
+ * not depend on timing.  Workspace: 4 E bytes per SM (more beyond 4095 tokens per
+ * half SM), per (device, stream). */
 tmg_status tmg_moe_route(const void *logits, int64_t T, int64_t E, int64_t k,
                          int64_t ld, tmg_dtype dtype, int normalize,
                          float *weights, int32_t *experts, int32_t *offsets,

@@ -369,8 +369,7 @@ tmg_status tmg_moe_route(const void *logits, int64_t T, int64_t E, int64_t k, in
         a.offsets = offsets;
         a.rows = rows;
         a.slots = slots;
-        a.counts = static_cast<int32_t *>(workspace(
-            kWsRoute, static_cast<size_t>(route_blocks(T, ds->num_sms)) * E * sizeof(int32_t), s, &st));
+        a.counts = static_cast<uint16_t *>(workspace(kWsRoute, route_counts_bytes(T, a.E, ds->num_sms), s, &st));
         if (!a.counts)
             return st;
         return launched(launch_route(a, ds->num_sms, s), "routing launch");

@@ -69,9 +69,9 @@ struct RouteArgs {
     bool normalize;
     float *weights;
     int32_t *experts, *offsets, *rows, *slots;
-    int32_t *counts;           // workspace: route_blocks() x E
+    uint16_t *counts;          // workspace: route_counts_bytes()
 };
-int route_blocks(int64_t T, int num_sms);
+size_t route_counts_bytes(int64_t T, int E, int num_sms);
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
                                   const int32_t *experts, const float *dweights, void *dlogits, int num_sms,

@@ -8,12 +8,14 @@
 // values inverted); -inf and NaN map to 0, which is never selected.  Each of
 // the k steps is a warp-wide maximum of the keys and a warp-wide minimum of
 // the experts that hold it (two redux instructions), so equal logits go to
-// the lowest expert.
+// the lowest expert.  A bf16 logit's key has 16 bits: with the inverted expert
+// number below it, one maximum finds both.
 //
 // Plan.  A stable counting sort.  Blocks take contiguous runs of tokens and
-// leave their counts per expert; the second kernel adds up the counts of
-// experts and blocks before its own and ranks its pairs in order: 32 pairs at
-// a time per warp, the lanes with the same expert found by match.any.  Atomics
+// leave their counts per expert (16 bits); a block of the second kernel takes
+// two such runs, adds up the counts of experts and runs before its own and
+// ranks its pairs in order: 32 pairs at a time per warp, the lanes with the
+// same expert found by match.any.  Atomics
 // only count, none decides an order, so the plan does not depend on timing.
 // Up to kOneBlockTokens tokens one block does it all in one launch: beyond,
 // its warps' tokens in a row cost more than the second launch.
@@ -28,6 +30,9 @@ namespace tmg {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
+
+// Entries of a row of the counts table (8-byte rows of 16-bit counts).
+__host__ __device__ __forceinline__ int count_row(int E) { return (E + 3) & ~3; }
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float load_logit(const void *p, int64_t i, bool bf16)
@@ -63,7 +68,7 @@ __device__ __forceinline__ float warp_sum(float v)
 
 // The choices of tokens t0 .. t1 - 1, one warp per token; counts (shared) gets
 // each expert's number; pairs (shared, or null) the chosen experts in order.
-template <int C>
+template <int C, bool BF16>
 __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *counts, int32_t *pairs)
 {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -72,7 +77,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t0, int64_t t
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = lane + 32 * c;
-            key[c] = e < a.E ? logit_key(load_logit(a.logits, t * a.ld + e, a.bf16)) : 0;
+            key[c] = e < a.E ? logit_key(load_logit(a.logits, t * a.ld + e, BF16)) : 0;
         }
         float sum_all = 0.f;
         if (!a.normalize) {
@@ -87,25 +92,48 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t0, int64_t t
                     sum_all += exp_from(key_logit(key[c]), key_logit(all));
             sum_all = warp_sum(sum_all);
         }
+        if constexpr (BF16) {
+            // a bf16's fp32 key ends in sixteen equal bits: zeros above, ones
+            // below zero
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                key[c] = key[c] ? (key[c] & 0xffff0000u) | (0xffffu - static_cast<uint32_t>(lane + 32 * c)) : 0;
+        }
         uint32_t mine_key = 0;       // lane j < k: the j-th choice
         int mine = -1;
         for (int j = 0; j < a.k; ++j) {
-            uint32_t best = 0;
-            int at = 0x7fffffff;
+            uint32_t best = 0, top;
+            int e;
+            if constexpr (BF16) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (key[c] > best) {
-                    best = key[c];
-                    at = lane + 32 * c;
-                }
-            const uint32_t top = __reduce_max_sync(kFull, best);
-            if (top == 0)
-                break;
-            const int e = static_cast<int>(__reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(at) : 0x7fffffffu));
+                for (int c = 0; c < C; ++c)
+                    best = max(best, key[c]);
+                top = __reduce_max_sync(kFull, best);
+                if (top == 0)
+                    break;
+                e = static_cast<int>(0xffffu - (top & 0xffffu));
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (lane + 32 * c == e)
-                    key[c] = 0;
+                for (int c = 0; c < C; ++c)
+                    if (key[c] == top)
+                        key[c] = 0;
+                top = top & 0x80000000u ? top & 0xffff0000u : top | 0xffffu;
+            } else {
+                int at = 0x7fffffff;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (key[c] > best) {
+                        best = key[c];
+                        at = lane + 32 * c;
+                    }
+                top = __reduce_max_sync(kFull, best);
+                if (top == 0)
+                    break;
+                e = static_cast<int>(__reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(at) : 0x7fffffffu));
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (lane + 32 * c == e)
+                        key[c] = 0;
+            }
             if (lane == j) {
                 mine_key = top;
                 mine = e;
@@ -200,7 +228,7 @@ __device__ __forceinline__ void rank_pairs(const RouteArgs &a, int64_t p0, int64
 
 // One block.  Shared memory: counts (totals) [E], base [E], pairs [T k], warp
 // counters [warps][E].
-template <int C>
+template <int C, bool BF16>
 __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a)
 {
     extern __shared__ int32_t sm[];
@@ -212,7 +240,7 @@ __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a)
     grid_release();
     grid_wait();
     __syncthreads();
-    choose<C>(a, 0, a.T, counts, pairs);
+    choose<C, BF16>(a, 0, a.T, counts, pairs);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int n = add_expert_prefix(a, base, counts);
@@ -225,7 +253,7 @@ __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a)
         a.rows[i] = -1;              // rows that no pair takes
 }
 
-template <int C>
+template <int C, bool BF16>
 __global__ void __launch_bounds__(1024) route_choose_kernel(RouteArgs a, int tokens_per_block)
 {
     extern __shared__ int32_t counts[];
@@ -235,14 +263,15 @@ __global__ void __launch_bounds__(1024) route_choose_kernel(RouteArgs a, int tok
     grid_wait();
     __syncthreads();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
-    choose<C>(a, t0, min(a.T, t0 + tokens_per_block), counts, nullptr);
+    choose<C, BF16>(a, t0, min(a.T, t0 + tokens_per_block), counts, nullptr);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = counts[e];
+    const int row = count_row(a.E);
+    for (int e = threadIdx.x; e < row; e += blockDim.x)
+        a.counts[static_cast<int64_t>(blockIdx.x) * row + e] = e < a.E ? static_cast<uint16_t>(counts[e]) : 0;
 }
 
 // Shared memory: base [E], totals [E], warp counters [warps][E].
-__global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens_per_block, int blocks)
+__global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens_per_block, int runs)
 {
     extern __shared__ int32_t sm[];
     __shared__ int used;
@@ -253,27 +282,30 @@ __global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens
     grid_release();
     grid_wait();
     __syncthreads();
-    // counts in the blocks before this one, and in all: each warp adds up
-    // every warps-th block, 128 experts at a time
+    // counts in the runs before this block's, and in all: each warp adds up
+    // every warps-th run, 128 experts at a time, four per lane
+    const int row = count_row(E), first = 2 * blockIdx.x;
     for (int e0 = 0; e0 < E; e0 += 128) {
         int before[4] = {}, sum[4] = {};
-#pragma unroll 4
-        for (int b = warp; b < blocks; b += warps)
+        const int e = e0 + 4 * lane;
+#pragma unroll 8
+        for (int b = warp; b < runs; b += warps) {
+            const uint2 n = e < E ? __ldg(reinterpret_cast<const uint2 *>(a.counts + static_cast<int64_t>(b) * row + e))
+                                  : make_uint2(0, 0);
+            const int in = b < first ? 1 : 0, v[4] = {static_cast<int>(n.x & 0xffffu), static_cast<int>(n.x >> 16),
+                                                      static_cast<int>(n.y & 0xffffu), static_cast<int>(n.y >> 16)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int e = e0 + 32 * c + lane;
-                const int n = e < E ? __ldg(a.counts + static_cast<int64_t>(b) * E + e) : 0;
-                sum[c] += n;
-                before[c] += b < static_cast<int>(blockIdx.x) ? n : 0;
-            }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int e = e0 + 32 * c + lane;
-            if (e < E && sum[c]) {
-                atomicAdd(&total[e], sum[c]);
-                atomicAdd(&base[e], before[c]);
+                sum[c] += v[c];
+                before[c] += in * v[c];
             }
         }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (e + c < E && sum[c]) {
+                atomicAdd(&total[e + c], sum[c]);
+                atomicAdd(&base[e + c], before[c]);
+            }
     }
     __syncthreads();
     if (warp == 0) {
@@ -282,8 +314,8 @@ __global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens
             used = n;
     }
     __syncthreads();
-    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block * a.k;
-    const int64_t p1 = min(a.T * a.k, p0 + static_cast<int64_t>(tokens_per_block) * a.k);
+    const int64_t span = 2 * static_cast<int64_t>(tokens_per_block) * a.k, p0 = blockIdx.x * span;
+    const int64_t p1 = min(a.T * a.k, p0 + span);
     rank_pairs(a, p0, p1, a.experts + p0, base, wc);
     // rows that no pair takes
     for (int64_t i = used + static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.T * a.k;
@@ -524,55 +556,73 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineGradArgs a
 
 constexpr int64_t kOneBlockTokens = 128;
 
-// Two blocks per SM.
-int tokens_per_block(int64_t T, int num_sms) { return static_cast<int>((T + 2 * num_sms - 1) / (2 * num_sms)); }
+// Runs of tokens: two per SM, and at most 4095 tokens, so that a run's counts
+// fit 16 bits.
+int tokens_per_run(int64_t T, int num_sms)
+{
+    return static_cast<int>(std::min<int64_t>((T + 2 * num_sms - 1) / (2 * num_sms), 4095));
+}
 
-template <int C>
+int route_runs(int64_t T, int num_sms)
+{
+    const int each = tokens_per_run(T, num_sms);
+    return static_cast<int>((T + each - 1) / each);
+}
+
+// Dynamic shared memory above the default limit needs an attribute.
+cudaError_t smem_limit(const void *kern, int bytes) { return bytes > 48 * 1024 ? ensure_smem_attr(kern, bytes) : cudaSuccess; }
+
+template <int C, bool BF16>
 cudaError_t launch_route_as(const RouteArgs &a, int num_sms, cudaStream_t s)
 {
+    cudaError_t e;
     if (a.T <= kOneBlockTokens) {
         // a warp per token; fewer counters where there are fewer tokens
         const int warps = static_cast<int>(a.T < 4 ? 4 : a.T < 16 ? a.T : 16);
         const int bytes = static_cast<int>(((2 + warps) * a.E + a.T * a.k) * sizeof(int32_t));
-        const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(route_one_kernel<C>), bytes);
-        if (e != cudaSuccess)
+        if ((e = smem_limit(reinterpret_cast<const void *>(route_one_kernel<C, BF16>), bytes)) != cudaSuccess)
             return e;
-        return launch_overlapped(route_one_kernel<C>, dim3(1), warps * 32, bytes, 1, s, a);
+        return launch_overlapped(route_one_kernel<C, BF16>, dim3(1), warps * 32, bytes, 1, s, a);
     }
-    const int each = tokens_per_block(a.T, num_sms), blocks = route_blocks(a.T, num_sms);
-    cudaError_t e = launch_overlapped(route_choose_kernel<C>, dim3(blocks), 1024, a.E * sizeof(int32_t), 1, s, a, each);
-    if (e != cudaSuccess)
+    const int each = tokens_per_run(a.T, num_sms), runs = route_runs(a.T, num_sms);
+    if ((e = launch_overlapped(route_choose_kernel<C, BF16>, dim3(runs), 1024, a.E * sizeof(int32_t), 1, s, a, each)) !=
+        cudaSuccess)
         return e;
     const int bytes = static_cast<int>(18 * a.E * sizeof(int32_t));
-    if ((e = ensure_smem_attr(reinterpret_cast<const void *>(route_plan_kernel), bytes)) != cudaSuccess)
+    if ((e = smem_limit(reinterpret_cast<const void *>(route_plan_kernel), bytes)) != cudaSuccess)
         return e;
-    return launch_overlapped(route_plan_kernel, dim3(blocks), 512, bytes, 1, s, a, each, blocks);
+    return launch_overlapped(route_plan_kernel, dim3((runs + 1) / 2), 512, bytes, 1, s, a, each, runs);
+}
+
+template <int C>
+cudaError_t launch_route_of(const RouteArgs &a, int num_sms, cudaStream_t s)
+{
+    return a.bf16 ? launch_route_as<C, true>(a, num_sms, s) : launch_route_as<C, false>(a, num_sms, s);
 }
 
 bool vec8(const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
 
 }  // namespace
 
-int route_blocks(int64_t T, int num_sms)
+size_t route_counts_bytes(int64_t T, int E, int num_sms)
 {
-    const int each = tokens_per_block(T, num_sms);
-    return static_cast<int>((T + each - 1) / each);
+    return static_cast<size_t>(T > kOneBlockTokens ? route_runs(T, num_sms) : 1) * count_row(E) * sizeof(uint16_t);
 }
 
 // Registers per lane for E experts: 2, 4, 8 or 32 of 32 experts each.
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t s)
 {
-    return a.E <= 64    ? launch_route_as<2>(a, num_sms, s)
-           : a.E <= 128 ? launch_route_as<4>(a, num_sms, s)
-           : a.E <= 256 ? launch_route_as<8>(a, num_sms, s)
-                        : launch_route_as<32>(a, num_sms, s);
+    return a.E <= 64    ? launch_route_of<2>(a, num_sms, s)
+           : a.E <= 128 ? launch_route_of<4>(a, num_sms, s)
+           : a.E <= 256 ? launch_route_of<8>(a, num_sms, s)
+                        : launch_route_of<32>(a, num_sms, s);
 }
 
 cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
                                   const int32_t *experts, const float *dweights, void *dlogits, int num_sms,
                                   cudaStream_t s)
 {
-    const int blocks = static_cast<int>(std::min<int64_t>((T + 7) / 8, num_sms * 8));
+    const int blocks = static_cast<int>(std::min<int64_t>((T + 7) / 8, num_sms * 16));
     auto kern = E <= 64    ? route_backward_kernel<2>
                 : E <= 128 ? route_backward_kernel<4>
                 : E <= 256 ? route_backward_kernel<8>
