@@ -72,13 +72,21 @@ template <int C, bool BF16>
 __device__ __forceinline__ void choose(const RouteArgs &a, int64_t t0, int64_t t1, int32_t *counts, int32_t *pairs)
 {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    for (int64_t t = t0 + warp; t < t1; t += warps) {
-        uint32_t key[C];
+    float next[C];               // the warp's next token's logits, in flight
+    auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = lane + 32 * c;
-            key[c] = e < a.E ? logit_key(load_logit(a.logits, t * a.ld + e, BF16)) : 0;
+            next[c] = t < t1 && e < a.E ? load_logit(a.logits, t * a.ld + e, BF16) : kNegInf;
         }
+    };
+    fetch(t0 + warp);
+    for (int64_t t = t0 + warp; t < t1; t += warps) {
+        uint32_t key[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            key[c] = logit_key(next[c]);
+        fetch(t + warps);
         float sum_all = 0.f;
         if (!a.normalize) {
             uint32_t all = 0;
@@ -183,42 +191,51 @@ __device__ __forceinline__ int add_expert_prefix(const RouteArgs &a, int32_t *ba
 // Slots and rows of the pairs p0 .. p1 - 1, whose experts are pairs[p - p0];
 // base[e]: the first slot of this block's pairs of expert e.  wc: warps x E
 // counters, zero.
-__device__ __forceinline__ void rank_pairs(const RouteArgs &a, int64_t p0, int64_t p1, const int32_t *pairs,
-                                           const int32_t *base, int32_t *wc)
+__device__ __forceinline__ void rank_pairs(const RouteArgs &a, int p0, int p1, const int32_t *pairs, const int32_t *base,
+                                           int32_t *wc)
 {
     const int E = a.E, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const unsigned k = a.k;
     // each warp's pairs are contiguous: [w0, w1)
-    const int64_t each = ((p1 - p0 + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t w0 = min(p1, p0 + warp * each), w1 = min(p1, w0 + each);
-    for (int64_t p = w0; p < w1; p += 32) {
+    const int each = ((p1 - p0 + 31) / 32 + warps - 1) / warps * 32;
+    const int w0 = min(p1, p0 + warp * each), w1 = min(p1, w0 + each);
+    int32_t *mine = wc + warp * E;
+    for (int p = w0; p < w1; p += 32) {
         const int e = p + lane < w1 ? pairs[p + lane - p0] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         if (e >= 0 && lane == __ffs(same) - 1)
-            wc[warp * E + e] += __popc(same);
+            mine[e] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int run = base[e];
-        for (int w = 0; w < warps; ++w) {
-            const int n = wc[w * E + e];
-            wc[w * E + e] = run;
-            run += n;
+        for (int w = 0; w < warps; w += 8) {
+            int n[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                n[i] = w + i < warps ? wc[(w + i) * E + e] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (w + i < warps) {
+                    wc[(w + i) * E + e] = run;
+                    run += n[i];
+                }
         }
     }
     __syncthreads();
-    for (int64_t p = w0; p < w1; p += 32) {
-        const int64_t i = p + lane;
+    for (int p = w0; p < w1; p += 32) {
+        const int i = p + lane;
         const int e = i < w1 ? pairs[i - p0] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
-        const int first = e >= 0 ? wc[warp * E + e] : 0;
+        const int first = e >= 0 ? mine[e] : 0;
         __syncwarp();
         if (e >= 0) {
             const int slot = first + __popc(same & ((1u << lane) - 1));
             if (lane == __ffs(same) - 1)
-                wc[warp * E + e] = first + __popc(same);
+                mine[e] = first + __popc(same);
             a.slots[i] = slot;
-            a.rows[slot] = static_cast<int32_t>(i / a.k);
+            a.rows[slot] = static_cast<int>(static_cast<unsigned>(i) / k);
         } else if (i < w1) {
             a.slots[i] = -1;
         }
@@ -248,8 +265,9 @@ __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a)
             used = n;
     }
     __syncthreads();
-    rank_pairs(a, 0, a.T * a.k, pairs, base, wc);
-    for (int64_t i = used + threadIdx.x; i < a.T * a.k; i += blockDim.x)
+    const int all = static_cast<int>(a.T) * a.k;
+    rank_pairs(a, 0, all, pairs, base, wc);
+    for (int i = used + threadIdx.x; i < all; i += blockDim.x)
         a.rows[i] = -1;              // rows that no pair takes
 }
 
@@ -270,8 +288,10 @@ __global__ void __launch_bounds__(1024) route_choose_kernel(RouteArgs a, int tok
         a.counts[static_cast<int64_t>(blockIdx.x) * row + e] = e < a.E ? static_cast<uint16_t>(counts[e]) : 0;
 }
 
-// Shared memory: base [E], totals [E], warp counters [warps][E].
-__global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens_per_block, int runs)
+// Shared memory: base [E], totals [E], warp counters [warps][E], the block's
+// pairs where they fit (kPlanPairs).
+constexpr int kPlanPairs = 4096;
+__global__ void __launch_bounds__(1024) route_plan_kernel(RouteArgs a, int tokens_per_block, int runs)
 {
     extern __shared__ int32_t sm[];
     __shared__ int used;
@@ -281,6 +301,16 @@ __global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens
         sm[i] = 0;
     grid_release();
     grid_wait();
+    // this block's pairs, in flight together with the counts
+    const int all = static_cast<int>(a.T * a.k), span = 2 * tokens_per_block * a.k;
+    const int p0 = blockIdx.x * span, p1 = all - p0 < span ? all : p0 + span;
+    const int32_t *pairs = a.experts + p0;
+    if (span <= kPlanPairs) {
+        int32_t *here = wc + warps * E;
+        for (int i = threadIdx.x; i < p1 - p0; i += blockDim.x)
+            here[i] = __ldg(pairs + i);
+        pairs = here;
+    }
     __syncthreads();
     // counts in the runs before this block's, and in all: each warp adds up
     // every warps-th run, 128 experts at a time, four per lane
@@ -288,7 +318,7 @@ __global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens
     for (int e0 = 0; e0 < E; e0 += 128) {
         int before[4] = {}, sum[4] = {};
         const int e = e0 + 4 * lane;
-#pragma unroll 8
+#pragma unroll 10
         for (int b = warp; b < runs; b += warps) {
             const uint2 n = e < E ? __ldg(reinterpret_cast<const uint2 *>(a.counts + static_cast<int64_t>(b) * row + e))
                                   : make_uint2(0, 0);
@@ -314,12 +344,9 @@ __global__ void __launch_bounds__(512) route_plan_kernel(RouteArgs a, int tokens
             used = n;
     }
     __syncthreads();
-    const int64_t span = 2 * static_cast<int64_t>(tokens_per_block) * a.k, p0 = blockIdx.x * span;
-    const int64_t p1 = min(a.T * a.k, p0 + span);
-    rank_pairs(a, p0, p1, a.experts + p0, base, wc);
+    rank_pairs(a, p0, p1, pairs, base, wc);
     // rows that no pair takes
-    for (int64_t i = used + static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.T * a.k;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    for (int64_t i = used + blockIdx.x * 1024ll + threadIdx.x; i < all; i += gridDim.x * 1024ll)
         a.rows[i] = -1;
 }
 
@@ -588,10 +615,10 @@ cudaError_t launch_route_as(const RouteArgs &a, int num_sms, cudaStream_t s)
     if ((e = launch_overlapped(route_choose_kernel<C, BF16>, dim3(runs), 1024, a.E * sizeof(int32_t), 1, s, a, each)) !=
         cudaSuccess)
         return e;
-    const int bytes = static_cast<int>(18 * a.E * sizeof(int32_t));
+    const int span = 2 * each * a.k, bytes = static_cast<int>((34 * a.E + (span <= kPlanPairs ? span : 0)) * sizeof(int32_t));
     if ((e = smem_limit(reinterpret_cast<const void *>(route_plan_kernel), bytes)) != cudaSuccess)
         return e;
-    return launch_overlapped(route_plan_kernel, dim3((runs + 1) / 2), 512, bytes, 1, s, a, each, runs);
+    return launch_overlapped(route_plan_kernel, dim3((runs + 1) / 2), 1024, bytes, 1, s, a, each, runs);
 }
 
 template <int C>
@@ -622,7 +649,7 @@ cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int6
                                   const int32_t *experts, const float *dweights, void *dlogits, int num_sms,
                                   cudaStream_t s)
 {
-    const int blocks = static_cast<int>(std::min<int64_t>((T + 7) / 8, num_sms * 16));
+    const int blocks = static_cast<int>(std::min<int64_t>((T + 7) / 8, num_sms * 32));
     auto kern = E <= 64    ? route_backward_kernel<2>
                 : E <= 128 ? route_backward_kernel<4>
                 : E <= 256 ? route_backward_kernel<8>
