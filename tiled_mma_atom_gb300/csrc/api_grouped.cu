@@ -309,7 +309,6 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
     p.K = static_cast<int>(a.K);
     p.E = static_cast<int>(a.E);
     p.group = 8;
-    p.vec_ok = a.K % 8 == 0 && aligned(a.dB);
     const int64_t per = ((a.N + 255) / 256) * ((a.K + 255) / 256);
     if ((a.R / 64 + 2 * a.E) * per > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tile blocks");

@@ -29,11 +29,11 @@ struct FeedSmem {
     int pad[2];
 };
 
-__device__ __forceinline__ void feed_init(FeedSmem *f)
+__device__ __forceinline__ void feed_init(FeedSmem *f, int readers = kFeedReaders)
 {
     for (int i = 0; i < kFeedSlots; ++i) {
         mbar_init(&f->full[i], 1);
-        mbar_init(&f->empty[i], kFeedReaders);
+        mbar_init(&f->empty[i], readers);
     }
 }
 

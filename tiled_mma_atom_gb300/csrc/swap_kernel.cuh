@@ -40,6 +40,7 @@
 #include "grouped.h"
 #include "launch.cuh"
 #include "pieces.cuh"
+#include "staging.cuh"
 #include "tc2_kernel.cuh"
 
 namespace tmg {
@@ -152,18 +153,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t &a, uint
                  : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // The warp's staging tile: 32 rows of COLS bf16 (COLS = 32 or 16), 16-byte
 // pieces swizzled so that the eight rows of a matrix touch different banks.
 template <int COLS>
@@ -207,19 +196,7 @@ __device__ __forceinline__ void store_staged(uint32_t base, int lane, __nv_bfloa
         const uint4 v = lds128(stage_addr<COLS>(base, row, piece));
         if (row >= nt || n >= cols)
             continue;
-        const int64_t off = (r0 + row) * ld + n;
-        if (!span_ok(off, min(8, cols - n), limit, err, kBndStoreD))
-            continue;
-        __nv_bfloat16 *p = M + off;
-        if (n + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-            *reinterpret_cast<uint4 *>(p) = v;
-        } else {
-            const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (n + j < cols)
-                    reinterpret_cast<uint16_t *>(p)[j] = static_cast<uint16_t>(u4[j / 2] >> (16 * (j & 1)));
-        }
+        store_piece(M, (r0 + row) * ld + n, v, min(8, cols - n), limit, err);
     }
 }
 

@@ -11,7 +11,8 @@
 // group is read in pieces up to the next multiple of 16 rows (one MMA step):
 // boxes of 16 rows while they lie inside the group, and for the rest TMA
 // gathers of four rows each whose indices past the end are out of range and
-// read as zeros.  The MMA steps beyond are not issued.  Rows by number are
+// read as zeros (issued by a warp of their own: 16 gathers take 0.7 us, which
+// the producer would lose on the next tile).  The MMA steps beyond are not issued.  Rows by number are
 // gathered into workspace before this kernel.  A group without rows is one such
 // block of zeros: its tile is written as zeros like any other.
 //
@@ -24,19 +25,24 @@
 #include "grouped.h"
 #include "launch.cuh"
 #include "pieces.cuh"
+#include "staging.cuh"
 #include "tc2_kernel.cuh"
 #include "wgrad.h"
 
 namespace tmg {
 namespace {
 
-constexpr int kWgStages = 6;
+constexpr int kWgMaxStages = 6;
+constexpr int kWgStaging = 8 * 4096;             // a warp's 32 rows of 64 columns
 constexpr int kWgStageBytes = 32768;
-constexpr int kWgBars = (2 * kWgStages + 4) * 8 + sizeof(FeedSmem) + 16;  // barriers, feed, TMEM address, abort flag
+constexpr int kWgBars = (3 * kWgMaxStages + 4) * 8 + sizeof(FeedSmem) + 16;  // barriers, feed, TMEM address, abort flag
 constexpr int64_t kWgPiece = 32 * 256;
-constexpr int kWgThreads = 352;                  // producer, MMA, eight epilogue warps, feed
+constexpr int kWgThreads = 384;                  // producer, MMA, eight epilogue warps, feed, group ends
 
-__host__ __device__ inline int wg_smem(int E) { return 1024 + kWgStages * kWgStageBytes + kWgBars + 8 * (E + 1); }
+__host__ inline int wg_smem(int stages, int E)
+{
+    return 1024 + stages * kWgStageBytes + kWgStaging + kWgBars + 8 * (E + 1);
+}
 
 __device__ __forceinline__ void tma_gather4_pair_to(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, const int4 &r)
 {
@@ -112,11 +118,13 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kWgStages * kWgStageBytes);
-    uint64_t *empty = full + kWgStages;
-    uint64_t *tfull = empty + kWgStages;
+    uint8_t *staging = smem + p.stages * kWgStageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(staging + kWgStaging);
+    uint64_t *empty = full + kWgMaxStages;
+    uint64_t *tfull = empty + kWgMaxStages;
     uint64_t *tempty = tfull + 2;
-    FeedSmem *feed_smem = reinterpret_cast<FeedSmem *>(tempty + 2);
+    uint64_t *go = tempty + 2;                   // the producer has set up a stage with a group's end
+    FeedSmem *feed_smem = reinterpret_cast<FeedSmem *>(go + kWgMaxStages);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(feed_smem + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *off = reinterpret_cast<int *>(tmem_slot + 4), *unit = off + p.E + 1;
@@ -127,15 +135,16 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kWgStages; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&go[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 16);
         }
-        feed_init(feed_smem);
+        feed_init(feed_smem, kFeedReaders + 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -236,34 +245,21 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                         if (abox == 2)
                             tma_load_2d_pair_w(sa + kMnBoxBytes + i * 128, &p.tmA16, bar0, k0 + kMnBox, r0 + i);
                     }
-                    // lane 4 b + g: rows 4 g .. 4 g + 3 of the last sixteen, box b
-                    // of dD (0, 1) or A (2, 3)
-                    const int in = rows16 - 16 + 4 * (lane & 3), b = lane >> 2;
-                    if (max(left, 0) % 16 || left <= 0) {
-                        if (b < 2 + abox) {
-                            int4 r;
-                            r.x = in + 0 < left ? r0 + in + 0 : p.R;
-                            r.y = in + 1 < left ? r0 + in + 1 : p.R;
-                            r.z = in + 2 < left ? r0 + in + 2 : p.R;
-                            r.w = in + 3 < left ? r0 + in + 3 : p.R;
-                            tma_gather4_pair_to(smem_u32(b < 2 ? sd : sa) + (b & 1) * kMnBoxBytes + in * 128,
-                                                b < 2 ? &p.tmDg : &p.tmAg, bar0, (b < 2 ? n0 : k0) + (b & 1) * kMnBox, r);
-                        }
-                        __syncwarp();
-                    }
+                    if (lane == 0 && (left <= 0 || (left & 15)))
+                        mbar_arrive(&go[stage]);       // the last, partial sixteen: warp 11
                 }
                 ++issued;
-                if (++stage == kWgStages) {
+                if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
         }
-        for (int i = 0; i < kWgStages && i < issued; ++i) {
+        for (int i = 0; i < p.stages && i < issued; ++i) {
             int s = stage - 1 - i;
             uint32_t ph = phase;
             if (s < 0) {
-                s += kWgStages;
+                s += p.stages;
                 ph ^= 1u;
             }
             if (rank == 0)
@@ -301,7 +297,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                         mma_bf16_pair_w(d_tmem, adesc + k * (kMnKStepBytes >> 4), bdesc + k * (kMnKStepBytes >> 4), idesc,
                                         (kb != kb0) || (k != 0));
                     mma_commit_pair_w(&empty[stage], 0x3);
-                    if (++stage == kWgStages) {
+                    if (++stage == p.stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -310,6 +306,37 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                     break;
                 mma_commit_pair_w(&tfull[acc], 0x3);
             }
+        }
+    } else if (warp == 11) {
+        // ------------------- gathers of the last, partial sixteen rows of a group
+        int stage = 0;
+        uint32_t phases = 0;             // one bit per stage
+        while (walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
+            const int r0 = off[e] + (blocks - 1) * 64, left = walk.rows(e) - (blocks - 1) * 64;
+            const int at = (stage + kb1 - kb0 - 1) % p.stages;
+            stage = (stage + kb1 - kb0) % p.stages;
+            if (kb1 != blocks || (left > 0 && !(left & 15)))
+                continue;
+            if (!mbar_wait_warp(&go[at], (phases >> at) & 1u, err, abort_flag, kSiteProducerEmpty))
+                break;
+            phases ^= 1u << at;
+            tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
+            const int kcols = p.K - tk * 256 <= 128 ? 64 : 128;
+            const int n0 = tn * 256 + static_cast<int>(rank) * 128, k0 = tk * 256 + static_cast<int>(rank) * kcols;
+            // lane 4 b + g: rows 4 g .. 4 g + 3 of the sixteen, box b of dD
+            // (0, 1) or A (2, 3)
+            const int in = ((max(left, 1) + 15) & ~15) - 16 + 4 * (lane & 3), b = lane >> 2;
+            if (b < 2 + kcols / 64) {
+                int4 r;
+                r.x = in + 0 < left ? r0 + in + 0 : p.R;
+                r.y = in + 1 < left ? r0 + in + 1 : p.R;
+                r.z = in + 2 < left ? r0 + in + 2 : p.R;
+                r.w = in + 3 < left ? r0 + in + 3 : p.R;
+                const uint32_t sd = smem_u32(smem + at * kWgStageBytes) + (b < 2 ? 0 : 16384);
+                tma_gather4_pair_to(sd + (b & 1) * kMnBoxBytes + in * 128, b < 2 ? &p.tmDg : &p.tmAg,
+                                    mapa_shared(smem_u32(&full[at]), 0), (b < 2 ? n0 : k0) + (b & 1) * kMnBox, r);
+            }
+            __syncwarp();
         }
     } else if (warp == 10) {
         feed_run(feed_smem, rank, total - sk, nclusters, p.feed, err, abort_flag);
@@ -330,13 +357,14 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            const int c1 = min(width / 32, (p.K - tk * 256 + 31) / 32);       // chunks with columns
+            const int c1 = min(width / 32, (p.K - tk * 256 + 31) / 32);       // 32-column chunks with columns
+            const int pairs = (c1 + 1) / 2;                                   // of which the warp takes every other two
             bool finish = !partial;
             int c_first = 0, c_last = 0;
             if (partial) {
                 const int64_t mine = ((static_cast<int64_t>(2 * cluster + slot) * 2 + rank) * 4 + q) * kWgPiece;
 #pragma unroll 1
-                for (int c = half; c < c1; c += 2) {
+                for (int c = 2 * half; c < c1; c += (c & 1) ? 3 : 1) {
                     uint32_t r[32];
                     tmem_ld32(tbase + c * 32, r);
 #pragma unroll
@@ -351,7 +379,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
-                if (half < c1) {
+                if (half < pairs) {
                     c_first = unit_owner(unit0, U, nclusters);
                     c_last = unit_owner(unit0 + blocks - 1, U, nclusters);
                     const int64_t at = ((static_cast<int64_t>(e) * per + local_tile) * 2 + rank) * 8 + ew;
@@ -360,29 +388,51 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 }
             }
             if (finish) {
-                const int64_t row_off = (static_cast<int64_t>(e) * p.N + n) * p.K;
-                __nv_bfloat16 *drow = static_cast<__nv_bfloat16 *>(p.dB) + row_off;
+                __nv_bfloat16 *D = static_cast<__nv_bfloat16 *>(p.dB);
+                const int64_t first = static_cast<int64_t>(e) * p.N * p.K;
+                const int n0 = n - lane;
+                const uint32_t stg = smem_u32(staging + ew * 4096);
 #pragma unroll 1
-                for (int c = half; c < c1; c += 2) {
-                    float v[32];
-                    if (!partial) {
-                        uint32_t r[32];
-                        tmem_ld32(tbase + c * 32, r);
+                for (int pr = half; pr < pairs; pr += 2) {
+                    // this lane's row, 64 columns, to the staging tile in
+                    // 16-byte pieces (swizzled)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __uint_as_float(r[j]);
-                    } else {
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = 2 * pr + h;
+                        float v[32];
+                        if (!partial) {
+                            uint32_t r[32];
+                            tmem_ld32(tbase + c * 32, r);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = 0.f;
-                        add_pieces(v, p.partials, p_limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
-                            const int s2 = U * cc / nclusters >= unit0 ? 0 : 1;       // its run begins in this tile
-                            return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * kWgPiece;
-                        }, err);
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __uint_as_float(r[j]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = 0.f;
+                            if (c < c1)
+                                add_pieces(v, p.partials, p_limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
+                                    const int s2 = U * cc / nclusters >= unit0 ? 0 : 1;   // its run begins in this tile
+                                    return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * kWgPiece;
+                                }, err);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            sts128(stg + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4),
+                                   make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                              pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
                     }
-                    const int col0 = tk * 256 + c * 32;
-                    if (n < p.N && span_ok(row_off + col0, min(32, p.K - col0), d_limit, err, kBndStoreD))
-                        store_row_chunk(drow, col0, p.K, p.vec_ok, v);
+                    __syncwarp();
+                    // whole 128-byte lines out: eight lanes a row
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + (lane >> 3), piece = lane & 7, col = tk * 256 + pr * 64 + piece * 8;
+                        const uint4 v = lds128(stg + row * 128 + ((piece ^ (row & 7)) << 4));
+                        if (n0 + row >= p.N || col >= p.K)
+                            continue;
+                        store_piece(D, first + static_cast<int64_t>(n0 + row) * p.K + col, v, min(8, p.K - col), d_limit, err);
+                    }
+                    __syncwarp();
                 }
             }
             if (!partial) {
@@ -409,11 +459,15 @@ size_t wgrad_partial_bytes(int num_sms) { return static_cast<size_t>(num_sms / 2
 
 cudaError_t launch_wgrad(const WgradTmaArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    const int smem = wg_smem(a.E);
+    WgradTmaArgs p = a;
+    p.stages = kWgMaxStages;
+    while (wg_smem(p.stages, p.E) > 232448)
+        --p.stages;
+    const int smem = wg_smem(p.stages, p.E);
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(wgrad_kernel), smem);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(wgrad_kernel, dim3(2 * (num_sms / 2)), kWgThreads, smem, 2, s, a, err);
+    return launch_overlapped(wgrad_kernel, dim3(2 * (num_sms / 2)), kWgThreads, smem, 2, s, p, err);
 }
 
 }  // namespace tmg

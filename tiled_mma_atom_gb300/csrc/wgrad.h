@@ -14,7 +14,7 @@ struct WgradTmaArgs {
     int R, N, K, E;
     int group;                 // column tiles of dD per band
     int split_cost;            // cost of a split in blocks of 64 rows; < 0: never split
-    int vec_ok;
+    int stages;                // set by the launch
     float *partials;           // wgrad_partial_bytes()
     uint32_t *counters;        // 16 per tile of two waves
     uint32_t *feed;            // the tile counter
