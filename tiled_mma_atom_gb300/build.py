@@ -23,7 +23,7 @@ BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libtmg_debug.so")
 SOURCES = ["api.cu", "ffma.cu", "tc_bf16.cu", "tc2_bf16.cu", "tc2_fused.cu", "skinny.cu", "mxfp4.cu",
            "mxfp4_pair.cu", "pack.cu", "w4a8.cu", "w4a8_skinny.cu",
-           "api_grouped.cu", "swap.cu", "swap_e4m3.cu", "wgrad.cu", "pack3.cu", "route.cu", "act_grad.cu"]
+           "api_grouped.cu", "swap.cu", "swap_e4m3.cu", "split.cu", "wgrad.cu", "pack3.cu", "route.cu", "act_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall",
                 "-I", CSRC, "-I", INCLUDE]

@@ -1,12 +1,14 @@
 // api_grouped.cu — C ABI of the routing, the expert-grouped products and the
 // dense product with the residual epilogue (include/tmg.h): argument checks
 // and launches.
+#include <algorithm>
 #include <cstring>
 #include <exception>
 
 #include "act.cuh"
 #include "grouped.h"
 #include "host.h"
+#include "split.h"
 #include "swap_kernel.cuh"
 #include "wgrad.h"
 
@@ -153,6 +155,60 @@ int tile_width(const GroupedArgs &a, int64_t tiles_n, int pairs)
     return best;
 }
 
+// The product over clusters: cluster 0 means the pair kernel.
+struct SplitPlan {
+    int cluster = 0, w = 0, tiles = 0;
+};
+constexpr int kSplitGatherW = 32;      // widest tile whose rows TMA gathers (8 gathers of 46 ns a K block)
+
+// Estimated times in ns of the pair kernel and of the cluster kernel for every
+// width w and cluster size S; the latter where it is expected to be faster.
+// Measured (weights of 1024 .. 14000 x 1024 .. 8192, 1 to 1024 rows): the pair
+// kernel takes 5.8 us and block_ns for a K block of a tile; a wave of the
+// cluster kernel 3.8 us + 20 w, 215 for a K block (260 at 256 columns) and, with
+// S > 1, 500 + 17 w for the exchange; both at least what HBM (6.7 TB/s) takes
+// for the weights, the cluster kernel also what its operands take into the
+// SMs (15 TB/s).
+SplitPlan split_plan(const GroupedArgs &a, int64_t F, bool swiglu, int64_t num_kb, int elem, int64_t pair_tiles_n, int maxw,
+                     int num_sms)
+{
+    SplitPlan best;
+    const int64_t pairs = num_sms / 2, tiles_n = (F + (swiglu ? 63 : 127)) / (swiglu ? 64 : 128);
+    const int64_t groups = std::min(a.E, a.R);              // at most so many have rows
+    auto row_tiles = [&](int64_t w) { return a.E == 1 ? (a.R + w - 1) / w : std::min(a.R, groups + a.R / w); };
+    const double hbm = static_cast<double>(groups) * a.N * a.K * elem / 6700.0;
+    const int64_t pair_tiles = row_tiles(maxw) * pair_tiles_n;
+    const double whole = static_cast<double>((pair_tiles + pairs - 1) / pairs) * num_kb * block_ns(maxw);
+    const double shared = static_cast<double>(pair_tiles) / pairs * num_kb * block_ns(maxw) + 6000 + 4000 * ((maxw + 63) / 64 - 1);
+    double best_ns = 5800 + std::max(hbm, std::min(whole, shared)) + 8 * maxw;
+    const int64_t even = (a.R + groups - 1) / groups;
+    const int64_t least = a.E == 1 ? 16 : std::min<int64_t>(256, even + even / 2 + 8);     // a group's rows in one tile
+    for (int64_t w = 16; w <= 256; w *= 2) {
+        const int64_t tiles = row_tiles(w) * tiles_n;
+        if (w >= least && tiles <= 4 * num_sms) {
+            const double gather = a.rows && w <= kSplitGatherW ? 11.5 * w : 0;
+            const double block = std::max(w <= 128 ? 215.0 : 260.0, gather), fixed = 3800 + 20.0 * w;
+            const double traffic = static_cast<double>(tiles) * num_kb * (16384 + 128 * w) / 15000;
+            for (int64_t S = 1; S <= 8 && (S == 1 || num_kb >= 4 * S); S *= 2) {
+                const int64_t fits = split_clusters(static_cast<int>(S));
+                if (fits < 1)
+                    continue;
+                const double wave = fixed + (num_kb + S - 1) / S * block + (S > 1 ? 500 + 17.0 * w : 0);
+                const double ns = std::max({static_cast<double>((tiles + fits - 1) / fits) * wave, hbm + 4500, traffic + fixed});
+                if (ns < best_ns) {
+                    best_ns = ns;
+                    best.cluster = static_cast<int>(S);
+                    best.w = static_cast<int>(w);
+                    best.tiles = static_cast<int>(tiles);
+                }
+            }
+        }
+        if (w >= a.R)
+            break;
+    }
+    return best;
+}
+
 tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t s)
 {
     const bool swiglu = a.epi.act == kActSwiglu;
@@ -169,7 +225,8 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     const int pairs = ds.num_sms / 2;
     const int64_t tiles_n = (F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
     p.maxw = tile_width(a, tiles_n, pairs);
-    p.gather = a.rows && p.maxw <= kSwGatherW;
+    const SplitPlan plan = split_plan(a, F, swiglu, (K + kb - 1) / kb, elem, tiles_n, p.maxw, ds.num_sms);
+    p.gather = a.rows && (plan.cluster ? plan.w <= kSplitGatherW : p.maxw <= kSwGatherW);
 
     // A: rows of K read in place, or copied; with row numbers and wide tiles,
     // gathered into workspace
@@ -211,6 +268,43 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     }
     bexp = stride_or(a.E, bexp, maj ? K * brow : halves * Fp * brow);
 
+    const int64_t xdims[2] = {K, T}, xstrides[1] = {lda * elem};
+    const int epi = swiglu ? kSwSwiglu : a.epi.act == kActSwigluGrad ? kSwSwigluGrad : a.offsets ? kSwPlain : kSwDense;
+    if (plan.cluster) {
+        SplitArgs q;
+        std::memset(&q, 0, sizeof q);
+        const int64_t dims[3] = {maj ? a.N : K, maj ? K : halves * Fp, a.E}, strides[2] = {brow * elem, bexp * elem};
+        const int box[3] = {maj ? 64 : kb, maj || swiglu ? 64 : 128, 1}, xbox[2] = {kb, p.gather ? 1 : plan.w};
+        if ((st = encode_nd(&q.tmW, dt, 3, B, dims, strides, box)) != TMG_OK ||
+            (st = encode_nd(&q.tmX, dt, 2, A, xdims, xstrides, xbox)) != TMG_OK)
+            return st;
+        q.D = a.D;
+        q.offsets = a.offsets;
+        q.rows = a.rows;
+        q.epi = a.epi;
+        q.ldd = a.ldd;
+        q.R = static_cast<int>(a.R);
+        q.T = static_cast<int>(a.T);
+        q.N = static_cast<int>(F);
+        q.K = static_cast<int>(K);
+        q.E = static_cast<int>(a.E);
+        q.half_rows = static_cast<int>(Fp);
+        q.maj = maj;
+        q.gather = p.gather;
+        q.map_rows = static_cast<int>(T);
+        q.w = plan.w;
+        q.tmem_cols = 32;
+        while (q.tmem_cols < q.w)
+            q.tmem_cols *= 2;
+        q.stage_bytes = 16384 + q.w * 128;
+        q.stages = 196608 / q.stage_bytes < kSplitMaxStages ? 196608 / q.stage_bytes : kSplitMaxStages;
+        q.ring_bytes = q.stages * q.stage_bytes;
+        log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> split_kernel: 128 x %d tiles, each over %d CTAs, weights %s%s",
+                   a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", q.R, (long long)a.N, (long long)a.K, q.E, q.w,
+                   plan.cluster, maj ? "MN-major" : "K-major",
+                   q.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "");
+        return launched(launch_split(q, epi, a.e4m3, plan.cluster, plan.tiles, err_ctx(ds), s), "split product launch");
+    }
     if (swiglu) {
         const int64_t dims[5] = {K, 8, 2, Fp / 8, a.E}, strides[4] = {brow * elem, Fp * brow * elem, 8 * brow * elem, bexp * elem};
         const int box[5] = {kb, 8, 2, 8, 1};
@@ -226,7 +320,6 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     }
     if (st != TMG_OK)
         return st;
-    const int64_t xdims[2] = {K, T}, xstrides[1] = {lda * elem};
     for (int i = 0; i < (p.gather ? 1 : 4); ++i) {
         const int box[2] = {kb, p.gather ? 1 : 16 << i};
         if ((st = encode_nd(&p.tmX[i], dt, 2, A, xdims, xstrides, box)) != TMG_OK)
@@ -264,7 +357,6 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     }
     if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
         return st;
-    const int epi = swiglu ? kSwSwiglu : a.epi.act == kActSwigluGrad ? kSwSwigluGrad : a.offsets ? kSwPlain : kSwDense;
     log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s",
                a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", p.R, (long long)a.N, (long long)a.K, p.E, 256, p.maxw,
                p.stages, maj ? "MN-major" : "K-major", p.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "");
