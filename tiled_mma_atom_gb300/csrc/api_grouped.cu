@@ -123,19 +123,21 @@ tmg_status gather(const DeviceState &ds, const void **A, int64_t *lda, int64_t s
     return TMG_OK;
 }
 
-// Nanoseconds that a CTA pair takes for one K block of a tile of w columns
-// (measured on the CTA-pair GEMM; below 128 columns the MMA issue is the limit).
+// Nanoseconds that a CTA pair takes for one K block of a tile of w columns, over
+// whole waves of tiles (measured: 256 to 8191 rows by 4096 to 14000 columns, K
+// 2000 to 8192).  Narrower tiles cost more per column: every tile reads the
+// weights again.
 float block_ns(int w)
 {
-    return w <= 128 ? 210.f : w <= 160 ? 226.f : w <= 192 ? 244.f : w <= 224 ? 281.f : 320.f;
+    return w <= 128 ? 260.f : w <= 160 ? 285.f : w <= 192 ? 305.f : w <= 224 ? 324.f : 350.f;
 }
 
 // Widest tile.  One group: the width whose waves of tiles take the least time
-// (4096 rows by 4096 columns: 19 x 16 tiles of 224 are four waves of 76 pairs,
-// 16 x 16 of 256 are four waves too: 79.5 us against 87).  Narrower tiles read
-// the weights more often, so they have to save 5 % (65536 x 1024 x 2048: 192
-// columns save 2 % of the waves' time and took 178 us, TILE256 with 256).  Several: all rows of an evenly filled
-// group, with room for half as many again; narrower tiles make a deeper ring.
+// (4096 x 4096 x 4096: 19 x 16 tiles of 224 columns are four waves of 76 pairs
+// like 16 x 16 of 256, and take 79.5 us against 87; 700 x 5000 x 2000: 21.4 us
+// in one wave of 256 columns, 28.8 in two of 192).  Several: all rows of an
+// evenly filled group, with room for half as many again; narrower tiles make a
+// deeper ring.
 int tile_width(const GroupedArgs &a, int64_t tiles_n, int pairs)
 {
     if (a.E > 1) {
