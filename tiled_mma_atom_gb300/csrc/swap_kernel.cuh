@@ -421,13 +421,13 @@ __device__ __forceinline__ SwapTile swap_tile(int t, const int *off, const int *
     const int first = off[lo], rows = off[lo + 1] - first, tiles = (rows + maxw - 1) / maxw;
     int tm;
     tile_coords(t - start[lo], tiles, tiles_n, group, tm, x.tn);
-    // the group's rows in 32s, spread evenly over its tiles
-    const int grains = (rows + 31) >> 5;
-    const int g0 = static_cast<int>(static_cast<int64_t>(grains) * tm / tiles);
-    const int g1 = static_cast<int>(static_cast<int64_t>(grains) * (tm + 1) / tiles);
+    // the group's rows in 32s, spread evenly over its tiles: the first few
+    // take one more
+    const int grains = (rows + 31) >> 5, each = grains / tiles, more = grains - each * tiles;
+    const int g0 = tm * each + min(tm, more);
+    x.w = 32 * (each + (tm < more ? 1 : 0));
     x.row0 = first + 32 * g0;
-    x.rows = min(32 * g1, rows) - 32 * g0;
-    x.w = 32 * (g1 - g0);
+    x.rows = min(x.w, rows - 32 * g0);
     return x;
 }
 
@@ -445,9 +445,12 @@ struct SwapWalk {
     __device__ SwapWalk(FeedSmem *f, int c, int nc, int total, int sk_, int nkb, const ErrCtx &e, volatile int *ab)
         : feed(f, c, nc, total - sk_), sk(sk_), num_kb(nkb), err(e), abort(ab)
     {
-        const int64_t U = static_cast<int64_t>(sk) * num_kb;
-        u = U * c / nc;
-        u_end = U * (c + 1) / nc;
+        u = u_end = 0;
+        if (sk) {
+            const int64_t U = static_cast<int64_t>(sk) * num_kb;
+            u = U * c / nc;
+            u_end = U * (c + 1) / nc;
+        }
     }
 
     // Tile, K blocks, whether a piece of a split tile, and the pair's partial
@@ -640,10 +643,14 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
             int local = 0;
             bool ok = true;
             const uint64_t astep = (p.maj ? kMnKStepBytes : 32) >> 4;
-            while (ok && walk.next(tile, kb0, kb1, partial, slot)) {
-                const SwapTile x = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group);
-                const uint32_t idesc = (IN == kInE4m3 ? idesc_e4m3_f32(256, x.w) : idesc_bf16_f32(256, x.w)) |
-                                       (p.maj ? 1u << 15 : 0u);
+            // The next tile is fetched and decoded (0.3 us) while the last K
+            // blocks of this one are under way, so the MMAs go on without a gap.
+            const uint32_t base = (IN == kInE4m3 ? idesc_e4m3_f32(256, 0) : idesc_bf16_f32(256, 0)) | (p.maj ? 1u << 15 : 0u);
+            bool more = walk.next(tile, kb0, kb1, partial, slot);
+            int w = more ? swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group).w : 0;
+            while (ok && more) {
+                const uint32_t idesc = base | static_cast<uint32_t>(w >> 3) << 17;
+                const int b0 = kb0, b1 = kb1, turn = max(b0, b1 - 3);
                 const int acc = local & 1;
                 const uint32_t acc_phase = (local >> 1) & 1;
                 ++local;
@@ -651,7 +658,12 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                     break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * kSwMaxW;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = b0; kb < b1; ++kb) {
+                    if (kb == turn) {
+                        more = walk.next(tile, kb0, kb1, partial, slot);
+                        if (more)
+                            w = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group).w;
+                    }
                     if (!mbar_wait_cluster_warp(&full[stage], phase, err, abort_flag, kSiteMmaFull)) {
                         ok = false;
                         break;
@@ -663,9 +675,9 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if constexpr (IN == kInE4m3)
-                            mma_e4m3_pair_w(d_tmem, adesc + k * astep, bdesc + k * 2, idesc, (kb != kb0) || (k != 0));
+                            mma_e4m3_pair_w(d_tmem, adesc + k * astep, bdesc + k * 2, idesc, (kb != b0) || (k != 0));
                         else
-                            mma_bf16_pair_w(d_tmem, adesc + k * astep, bdesc + k * 2, idesc, (kb != kb0) || (k != 0));
+                            mma_bf16_pair_w(d_tmem, adesc + k * astep, bdesc + k * 2, idesc, (kb != b0) || (k != 0));
                     }
                     mma_commit_pair_w(&empty[stage], 0x3);
                     if (++stage == p.stages) {

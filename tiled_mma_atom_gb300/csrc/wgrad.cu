@@ -67,8 +67,8 @@ struct WgWalk {
 
     __device__ WgWalk(FeedSmem *f, int c, int nc, int sk_, int64_t U, int total, int per_, int E_, const int *off_,
                       const int *unit_, const ErrCtx &er, volatile int *ab)
-        : off(off_), unit(unit_), feed(f, c, nc, total - sk_), per(per_), E(E_), sk(sk_), u(U * c / nc),
-          u_end(U * (c + 1) / nc), first(true), err(er), abort(ab)
+        : off(off_), unit(unit_), feed(f, c, nc, total - sk_), per(per_), E(E_), sk(sk_), u(U ? U * c / nc : 0),
+          u_end(U ? U * (c + 1) / nc : 0), first(true), err(er), abort(ab)
     {
     }
 
