@@ -14,8 +14,9 @@
 //
 // Operands are the pair kernel's: weights K-major or MN-major through 3-D maps
 // (SwiGLU: 64 gate rows and their 64 up rows, two boxes), A by boxes of the tile's width or TMA
-// gathers of named rows.  Warps: 0 TMA producer, 1 MMA issuer and TMEM owner,
-// 2..9 epilogue; all ten add up the partials.
+// gathers of named rows.  Warps: 0 the weights' TMA producer, 1 MMA issuer and
+// TMEM owner, 2..9 epilogue, 2 before that the rows' producer; all ten add up the
+// partials.
 #pragma once
 
 #include "act.cuh"
@@ -208,9 +209,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
     const uint32_t part = smem_u32(smem);                      // the partial tile, over the ring
 
-    if (work && warp == 0) {
-        // ---------------------------------------------- TMA producer
-        if (p.gather) {
+    if (work && (warp == 0 || warp == 2)) {
+        // ------------------ TMA producers: the weights (warp 0), the rows (warp 2)
+        if (warp == 2 && p.gather) {
             for (int i = lane; i < wt; i += 32) {
                 int r = p.map_rows;                            // past the last row: zeros
                 if (i < rows) {
@@ -228,18 +229,19 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty))
                 break;
-            mbar_arrive_expect_tx_w(&full[stage], tx);
             uint8_t *sw = smem + stage * p.stage_bytes, *sx = sw + 16384;
-            if constexpr (EPI == kSwSwiglu) {
-                tma_load_3d_w(sw, &p.tmW, &full[stage], kb * KB, n0, e);
-                tma_load_3d_w(sw + 8192, &p.tmW, &full[stage], kb * KB, p.half_rows + n0, e);
-            } else if (p.maj) {
-                tma_load_3d_w(sw, &p.tmW, &full[stage], n0, kb * KB, e);
-                tma_load_3d_w(sw + kMnBoxBytes, &p.tmW, &full[stage], n0 + kMnBox, kb * KB, e);
-            } else {
-                tma_load_3d_w(sw, &p.tmW, &full[stage], kb * KB, n0, e);
-            }
-            if (p.gather) {
+            if (warp == 0) {
+                mbar_arrive_expect_tx_w(&full[stage], tx);
+                if constexpr (EPI == kSwSwiglu) {
+                    tma_load_3d_w(sw, &p.tmW, &full[stage], kb * KB, n0, e);
+                    tma_load_3d_w(sw + 8192, &p.tmW, &full[stage], kb * KB, p.half_rows + n0, e);
+                } else if (p.maj) {
+                    tma_load_3d_w(sw, &p.tmW, &full[stage], n0, kb * KB, e);
+                    tma_load_3d_w(sw + kMnBoxBytes, &p.tmW, &full[stage], n0 + kMnBox, kb * KB, e);
+                } else {
+                    tma_load_3d_w(sw, &p.tmW, &full[stage], kb * KB, n0, e);
+                }
+            } else if (p.gather) {
                 for (int i = lane; i < wt / 4; i += 32)
                     tma_gather4(smem_u32(sx) + i * 512, &p.tmX, &full[stage], kb * KB,
                                 reinterpret_cast<const int4 *>(row_numbers)[i]);
@@ -279,7 +281,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
             }
         }
         mma_commit_w(done);
-    } else if (work) {
+    }
+    if (work && warp >= 2) {
         // ------------------------- the accumulator to the partial tile [row of A][128]
         if (mbar_wait_warp(done, 0, err, abort_flag, kSiteEpiTmemFull)) {
             tc_fence_after();
