@@ -24,15 +24,22 @@
 // range reads zeros).  A gather takes 46 ns of an SM's TMA unit, so this is for
 // tiles of at most 64 rows (8 gathers a K block and CTA, the 0.37 us that the
 // block's weights take from HBM); for wider tiles the caller copies the rows
-// first (65528 x 2048 x 2048: 1263 us gathered here, COPY_US copied).  Rows of the next
-// group that a box brings along give columns that no one reads.
+// first (65528 x 2048 x 2048: 1263 us gathered here, 390 copied, of them 45 for
+// the copy).  Rows of the next group that a box brings along give columns that
+// no one reads.
 //
 // Roles per CTA (eleven warps): 0 TMA producer, 1 MMA issuer (CTA 0 of the
 // pair) and TMEM owner, 2..9 epilogue, two warps per TMEM lane quarter taking
-// 32-column chunks in turn, 10 the tile feed.  The accumulator is double-buffered (2 x 256
-// columns).  Lanes are output columns and registers are rows there, so the
-// epilogue reads 16x256b fragments, whose pairs stmatrix transposes into a
+// 32-column chunks in turn, 10 the tile feed.  The accumulator is double-buffered
+// (2 x 256 columns).  Lanes are output columns and registers are rows there, so
+// the epilogue reads 16x256b fragments, whose pairs stmatrix transposes into a
 // 2 KB tile per warp; D, preact and the residual move in 16-byte pieces.
+//
+// What bounds it.  Wide tiles: the tensor pipe, busy 73 - 80 % of the time
+// (8191 x 4096 x 4096 170 us, 1.62 PFLOP/s; 65528 rows over 64 groups, 2048 x
+// 2048, 341 us, 1.61), the rest being the first operands of each CTA, the last
+// wave and the shared-memory traffic of the epilogue.  Few rows a group: the
+// weights' bytes (488 rows over 64 groups, 252 MB, 46.7 us, 5.4 TB/s).
 #pragma once
 
 #include "act.cuh"
