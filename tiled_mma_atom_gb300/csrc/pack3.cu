@@ -41,10 +41,10 @@ __global__ void __launch_bounds__(256) pack3_kernel(Pack3Args a, int64_t tiles_k
 // and past the row's bytes.  A warp takes a row at a time, eight pieces per
 // lane in flight.
 __global__ void __launch_bounds__(256)
-    gather_rows_kernel(const char *__restrict__ src, int64_t stride, int64_t src_rows, int bytes,
+    gather_rows_kernel(const char *__restrict__ src, int64_t stride, int64_t src_rows, int64_t bytes,
                        const int32_t *__restrict__ numbers, int64_t rows, char *__restrict__ dst, int64_t dst_stride)
 {
-    const int lane = threadIdx.x % 32, pieces = static_cast<int>(dst_stride / 16), whole = bytes / 16;
+    const int lane = threadIdx.x % 32, pieces = static_cast<int>(dst_stride / 16), whole = static_cast<int>(bytes / 16), tail = static_cast<int>(bytes % 16);
     grid_release();
     grid_wait();
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; r < rows; r += gridDim.x * 8ll) {
@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(256)
         }
         __syncwarp();
         // the last, partial piece
-        if (there && whole < pieces && lane < bytes - whole * 16)
-            reinterpret_cast<char *>(d + whole)[lane] = p[whole * 16 + lane];
+        if (there && whole < pieces && lane < tail)
+            reinterpret_cast<char *>(d + whole)[lane] = p[bytes - tail + lane];
     }
 }
 
@@ -80,7 +80,7 @@ cudaError_t launch_gather_rows(const void *src, int64_t stride, int64_t src_rows
     if (rows == 0)
         return cudaSuccess;
     return launch_overlapped(gather_rows_kernel, dim3(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8)), 256, 0,
-                             1, s, static_cast<const char *>(src), stride, src_rows, static_cast<int>(bytes), numbers, rows,
+                             1, s, static_cast<const char *>(src), stride, src_rows, bytes, numbers, rows,
                              static_cast<char *>(dst), dst_stride);
 }
 
