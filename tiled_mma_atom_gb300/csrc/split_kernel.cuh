@@ -162,9 +162,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         tmem_relinquish();
     }
     grid_release();
-    grid_wait();
+    if constexpr (EPI != kSwDense)
+        grid_wait();
     for (int i = threadIdx.x; i <= p.E; i += kSplitThreads)
-        off[i] = p.offsets ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
+        off[i] = EPI != kSwDense ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -212,6 +213,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
     const uint32_t part = smem_u32(smem);                      // the partial tile, over the ring
+    if constexpr (EPI == kSwDense)                             // all up to here depends on sizes only
+        grid_wait();
 
     if (work && (warp == 0 || warp == 2)) {
         // ------------------ TMA producers: the weights (warp 0), the rows (warp 2)
