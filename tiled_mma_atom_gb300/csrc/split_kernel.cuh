@@ -125,6 +125,44 @@ __device__ __forceinline__ void save_piece(__nv_bfloat16 *M, int64_t off, const 
                 n, limit, err);
 }
 
+// What the epilogue of eight columns of a row reads: scales, bias, and the
+// residual or the two halves of preact.
+struct PieceReads {
+    float scale_a, scale_b[8], scale_u[8], bias[8], a[8], b[8];
+};
+
+template <int EPI>
+__device__ __forceinline__ void read_piece(const SplitArgs &p, PieceReads &rd, int64_t row, int col, int n, int e)
+{
+    if (p.epi.scale_a) {
+        const int64_t src = p.rows ? __ldg(p.rows + row) : row;
+        rd.scale_a = src >= 0 && src < p.T ? __ldg(p.epi.scale_a + src) : 0.f;
+    }
+    if (p.epi.scale_b) {
+        const float *s = p.epi.scale_b + e * static_cast<int64_t>(EPI == kSwSwiglu ? 2 * p.N : p.N) + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            rd.scale_b[j] = j < n ? __ldg(s + j) : 0.f;
+            if constexpr (EPI == kSwSwiglu)
+                rd.scale_u[j] = j < n ? __ldg(s + p.N + j) : 0.f;
+        }
+    }
+    if constexpr (EPI == kSwDense) {
+        if (p.epi.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                rd.bias[j] = j < n ? __ldg(p.epi.bias + col + j) : 0.f;
+        }
+        if (p.epi.residual)
+            load_piece(static_cast<const __nv_bfloat16 *>(p.epi.residual) + row * p.epi.ld_residual + col, n, rd.a);
+    }
+    if constexpr (EPI == kSwSwigluGrad) {
+        const __nv_bfloat16 *P = static_cast<const __nv_bfloat16 *>(p.epi.preact) + row * p.epi.ld_preact + col;
+        load_piece(P, n, rd.a);
+        load_piece(P + p.N, n, rd.b);
+    }
+}
+
 template <int IN, int EPI>
 __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_constant__ SplitArgs p, ErrCtx err)
 {
@@ -138,7 +176,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *row_numbers = reinterpret_cast<int *>(smem + p.ring_bytes + kSplitBars - 1024);
-    int *off = row_numbers + 256, *start = off + p.E + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank(), S = cluster_size();
@@ -162,52 +199,50 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         tmem_relinquish();
     }
     grid_release();
-    if constexpr (EPI != kSwDense)
-        grid_wait();
-    for (int i = threadIdx.x; i <= p.E; i += kSplitThreads)
-        off[i] = EPI != kSwDense ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) {                 // tiles before each group
-        int run = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < p.E ? (max(off[e + 1] - off[e], 0) + p.w - 1) / p.w * tiles_n : 0;
-            int inc = n;
+    const uint32_t tmem = *tmem_slot;
+
+    // This cluster's tile (the grid is an upper bound): group, rows, columns.
+    // Every warp finds it from the offsets by itself.
+    int e = 0, row0 = 0, rows = 0, tn = 0;
+    bool work = false;
+    auto take = [&](int group, int first, int end, int t) {
+        work = true;
+        e = group;
+        tn = t % tiles_n;
+        row0 = first + t / tiles_n * p.w;
+        rows = min(p.w, end - row0);
+    };
+    if constexpr (EPI == kSwDense) {
+        if (tile < (p.R + p.w - 1) / p.w * tiles_n)
+            take(0, 0, p.R, tile);
+    } else {
+        grid_wait();
+        int before = 0;              // tiles of the groups before
+        for (int e0 = 0; e0 < p.E && !work; e0 += 32) {
+            int a = 0, b = 0;
+            if (e0 + lane < p.E) {
+                a = min(max(__ldg(p.offsets + e0 + lane), 0), p.R);
+                b = min(max(__ldg(p.offsets + e0 + lane + 1), 0), p.R);
+            }
+            int inc = (max(b - a, 0) + p.w - 1) / p.w * tiles_n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o)
                     inc += x;
             }
-            if (e < p.E)
-                start[e] = run + inc - n;
-            run += __shfl_sync(0xffffffffu, inc, 31);
+            const uint32_t past = __ballot_sync(0xffffffffu, tile < before + inc);
+            const int l = past ? __ffs(past) - 1 : 31;
+            const int start = l ? __shfl_sync(0xffffffffu, inc, l - 1) : 0;
+            a = __shfl_sync(0xffffffffu, a, l);
+            b = __shfl_sync(0xffffffffu, b, l);
+            if (past)
+                take(e0 + l, a, b, tile - before - start);
+            before += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0)
-            start[p.E] = run;
-    }
-    __syncthreads();
-    const uint32_t tmem = *tmem_slot;
-
-    // This cluster's tile (the grid is an upper bound): group, rows, columns.
-    const bool work = tile < start[p.E];
-    int e = 0, row0 = 0, rows = 0, tn = 0;
-    if (work) {
-        int lo = 0, hi = p.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (start[mid] <= tile)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        e = lo;
-        const int t = tile - start[e];
-        tn = t % tiles_n;
-        row0 = off[e] + t / tiles_n * p.w;
-        rows = min(p.w, off[e + 1] - row0);
     }
     const int wt = (rows + 15) & ~15;                          // MMA width
     const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
@@ -289,6 +324,20 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         }
         mma_commit_w(done);
     }
+    // The rows of this CTA's share, in eight-column pieces, the warps that are
+    // free first.  Their epilogue operands are read ahead of the sum.
+    constexpr int PER = OUT / 8;
+    const int r_begin = static_cast<int>(static_cast<int64_t>(rows) * rank / S);
+    const int r_end = static_cast<int>(static_cast<int64_t>(rows) * (rank + 1) / S);
+    const int item0 = (threadIdx.x + kSplitThreads - 64) % kSplitThreads, items = work ? (r_end - r_begin) * PER : 0;
+    PieceReads rd;
+    auto read = [&](int i) {
+        const int col = tn * OUT + i % PER * 8;
+        if (i < items && col < p.N)
+            read_piece<EPI>(p, rd, row0 + r_begin + i / PER, col, min(8, p.N - col), e);
+    };
+    if (warp >= 2)
+        read(item0);
     if (work && warp >= 2) {
         // ------------------------- the accumulator to the partial tile [row of A][128]
         if (mbar_wait_warp(done, 0, err, abort_flag, kSiteEpiTmemFull)) {
@@ -314,49 +363,43 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     }
     if (work) {
         // ------------------------- this CTA's share of the rows: sum, epilogue
-        const int r_begin = static_cast<int>(static_cast<int64_t>(rows) * rank / S);
-        const int r_end = static_cast<int>(static_cast<int64_t>(rows) * (rank + 1) / S);
-        constexpr int PER = OUT / 8;                           // eight-column pieces of a row
         __nv_bfloat16 *D = static_cast<__nv_bfloat16 *>(p.D);
         __nv_bfloat16 *P = static_cast<__nv_bfloat16 *>(p.epi.preact);
         const int64_t dcols = EPI == kSwSwigluGrad ? 2ll * p.N : p.N;
         const int64_t d_limit = (p.R - 1) * p.ldd + dcols;
         const int64_t p_limit = (p.R - 1) * p.epi.ld_preact + (EPI == kSwDense ? p.N : 2ll * p.N);
-        for (int i = threadIdx.x; i < (r_end - r_begin) * PER; i += kSplitThreads) {
+        for (int i = item0; i < items; i += kSplitThreads) {
             const int r = r_begin + i / PER, c = i % PER * 8, col = tn * OUT + c, n = min(8, p.N - col);
             if (n <= 0)
                 continue;
+            if (warp < 2 || i != item0)
+                read(i);
             const int64_t row = row0 + r;
             float z[8], u[8];
             sum_partials(part, r, c, S, z);
             if constexpr (EPI == kSwSwiglu)
                 sum_partials(part, r, 64 + c, S, u);
             if (p.epi.scale_a) {
-                const int64_t src = p.rows ? __ldg(p.rows + row) : row;
-                const float f = src >= 0 && src < p.T ? __ldg(p.epi.scale_a + src) : 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    z[j] *= f;
+                    z[j] *= rd.scale_a;
                     if constexpr (EPI == kSwSwiglu)
-                        u[j] *= f;
+                        u[j] *= rd.scale_a;
                 }
             }
             if (p.epi.scale_b) {
-                const float *s = p.epi.scale_b + e * static_cast<int64_t>(EPI == kSwSwiglu ? 2 * p.N : p.N) + col;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) {
-                        z[j] *= __ldg(s + j);
-                        if constexpr (EPI == kSwSwiglu)
-                            u[j] *= __ldg(s + p.N + j);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    z[j] *= rd.scale_b[j];
+                    if constexpr (EPI == kSwSwiglu)
+                        u[j] *= rd.scale_u[j];
+                }
             }
             if constexpr (EPI == kSwDense) {
                 if (p.epi.bias) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (j < n)
-                            z[j] += __ldg(p.epi.bias + col + j);
+                        z[j] += rd.bias[j];
                 }
                 if (P)
                     save_piece(P, row * p.epi.ld_preact + col, z, n, p_limit, err);
@@ -367,11 +410,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
                            : p.epi.act == kActGelu ? act_f<kActGelu>(z[j])
                                                    : z[j];
                 if (p.epi.residual) {
-                    float f[8];
-                    load_piece(static_cast<const __nv_bfloat16 *>(p.epi.residual) + row * p.epi.ld_residual + col, n, f);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        z[j] += f[j];
+                        z[j] += rd.a[j];
                 }
             } else if constexpr (EPI == kSwSwiglu) {
                 if (P) {
@@ -382,12 +423,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
                 for (int j = 0; j < 8; ++j)
                     z[j] = silu_f(z[j]) * u[j];
             } else if constexpr (EPI == kSwSwigluGrad) {
-                float g[8], v[8];
-                load_piece(P + row * p.epi.ld_preact + col, n, g);
-                load_piece(P + row * p.epi.ld_preact + p.N + col, n, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    swiglu_grad(z[j], g[j], v[j], z[j], u[j]);
+                    swiglu_grad(z[j], rd.a[j], rd.b[j], z[j], u[j]);
                 save_piece(D, row * p.ldd + p.N + col, u, n, d_limit, err);
             }
             save_piece(D, row * p.ldd + col, z, n, d_limit, err);
@@ -401,7 +439,7 @@ template <int IN, int EPI>
 cudaError_t launch_split_as(const SplitArgs &a, int cluster, int tiles, const ErrCtx &err, cudaStream_t s)
 {
     auto kern = split_kernel<IN, EPI>;
-    const int smem = 1024 + a.ring_bytes + kSplitBars + 8 * (a.E + 1);
+    const int smem = 1024 + a.ring_bytes + kSplitBars;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess)
         return e;
