@@ -165,12 +165,12 @@ constexpr int kSplitGatherW = 32;      // widest tile whose rows TMA gathers (8 
 
 // Estimated times in ns of the pair kernel and of the cluster kernel for every
 // width w and cluster size S; the latter where it is expected to be faster.
-// Measured (weights of 1024 .. 14000 x 1024 .. 8192, 1 to 1024 rows): the pair
-// kernel takes 5.8 us and block_ns for a K block of a tile; a wave of the
-// cluster kernel 3.8 us + 20 w, 215 for a K block (260 at 256 columns) and, with
-// S > 1, 500 + 17 w for the exchange; both at least what HBM (6.7 TB/s) takes
-// for the weights, the cluster kernel also what its operands take into the
-// SMs (15 TB/s).
+// Fitted to 63 sizes (weights of 1024 .. 14000 x 1000 .. 8192, 1 to 1024 rows),
+// where the choice is within 1 % of the fastest on average: the pair kernel takes
+// 5.5 us + 8 w and block_ns for a K block of a tile; a wave of the cluster kernel
+// 3.5 us + 27 w, 205 for a K block (320 at 256 columns) and, with S > 1, 7 w for
+// the exchange; both at least what HBM (6.7 TB/s) takes for the weights and 2.8
+// and 4.3 us.
 SplitPlan split_plan(const GroupedArgs &a, int64_t F, bool swiglu, int64_t num_kb, int elem, int64_t pair_tiles_n, int maxw,
                      int num_sms)
 {
@@ -182,21 +182,20 @@ SplitPlan split_plan(const GroupedArgs &a, int64_t F, bool swiglu, int64_t num_k
     const int64_t pair_tiles = row_tiles(maxw) * pair_tiles_n;
     const double whole = static_cast<double>((pair_tiles + pairs - 1) / pairs) * num_kb * block_ns(maxw);
     const double shared = static_cast<double>(pair_tiles) / pairs * num_kb * block_ns(maxw) + 6000 + 4000 * ((maxw + 63) / 64 - 1);
-    double best_ns = 5800 + std::max(hbm, std::min(whole, shared)) + 8 * maxw;
+    double best_ns = 5500 + std::max(hbm + 2800, std::min(whole, shared)) + 8 * maxw;
     const int64_t even = (a.R + groups - 1) / groups;
     const int64_t least = a.E == 1 ? 16 : std::min<int64_t>(256, even + even / 2 + 8);     // a group's rows in one tile
     for (int64_t w = 16; w <= 256; w *= 2) {
         const int64_t tiles = row_tiles(w) * tiles_n;
         if (w >= least && tiles <= 4 * num_sms) {
             const double gather = a.rows && w <= kSplitGatherW ? 11.5 * w : 0;
-            const double block = std::max(w <= 128 ? 215.0 : 260.0, gather), fixed = 3800 + 20.0 * w;
-            const double traffic = static_cast<double>(tiles) * num_kb * (16384 + 128 * w) / 15000;
+            const double block = std::max(w <= 128 ? 205.0 : 320.0, gather), fixed = 3500 + 27.0 * w;
             for (int64_t S = 1; S <= 8 && (S == 1 || num_kb >= 4 * S); S *= 2) {
                 const int64_t fits = split_clusters(static_cast<int>(S));
                 if (fits < 1)
                     continue;
-                const double wave = fixed + (num_kb + S - 1) / S * block + (S > 1 ? 500 + 17.0 * w : 0);
-                const double ns = std::max({static_cast<double>((tiles + fits - 1) / fits) * wave, hbm + 4500, traffic + fixed});
+                const double wave = fixed + (num_kb + S - 1) / S * block + (S > 1 ? 7.0 * w : 0);
+                const double ns = std::max(static_cast<double>((tiles + fits - 1) / fits) * wave, hbm + 4300);
                 if (ns < best_ns) {
                     best_ns = ns;
                     best.cluster = static_cast<int>(S);
