@@ -8,9 +8,9 @@
 // share of the tile's rows of A, adds the S partials in rank order (so results
 // do not depend on timing) and runs the epilogue on them, eight output columns
 // per thread.  A split through global memory costs a pair 6 us and more
-// (partials, fence, counter, partials back); this one 0.8 us at 16 rows
-// and 2.7 at 128.  At 16 x 4096 x 4096 with the weights in L2 the product took
-// 16.4 us with the pair kernel and takes 8.6 so.
+// (partials, fence, counter, partials back); this one 0.8 us at 16 rows and 2.7 at
+// 128.  At 16 x 4096 x 4096 with the weights in L2 the product took 16.8 us with
+// the pair kernel and takes 8.6 so.
 //
 // Operands are the pair kernel's: weights K-major or MN-major through 3-D maps
 // (SwiGLU: 64 gate rows and their 64 up rows, two boxes), A by boxes of the
@@ -18,9 +18,9 @@
 // 1 MMA issuer and TMEM owner, 2..9 epilogue, 2 before that the rows' producer;
 // all ten add up the partials.
 //
-// Bound by HBM where the weights do not come from L2 (one token's 8 experts, 67
-// MB: 17.7 us against 9.9; a call of 17 us spends 6 on launch, first operands,
-// exchange and epilogue).
+// Bound by HBM where the weights do not come from L2: one token's 8 experts, 67
+// MB, 17.1 us; 16 x 8192 x 8192, 134 MB, 24.7.  A kernel that only reads takes
+// 14.7 us for 63 MB and 24.6 for 126.
 #pragma once
 
 #include "act.cuh"
