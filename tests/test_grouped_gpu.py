@@ -523,6 +523,65 @@ def test_linear_few_rows_exact(tmg, M, N, K):
         exact(D, want)
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 1000, 2048), (150, 1000, 96), (900, 1000, 200), (2500, 1000, 64)])
+def test_linear_residual_in_place_exact(tmg, M, N, K):
+    A, B, X = ints((M, K), 81), ints((N, K), 82), ints((M, N), 83)
+    dX = X.to(DEV)
+    tmg.linear(A.to(DEV), B.to(DEV), dX, residual=dX)
+    tmg.check()
+    exact(dX, A.to(W) @ B.to(W).T + X.to(W))
+
+
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_calls_in_a_row_see_each_other(tmg, M):
+    """Launches overlap: every call reads what the one before wrote, as its rows, its
+    residual and (a signed permutation, made by a product itself) its weight."""
+    K, steps = 512, 6
+    perm = torch.randperm(K, generator=gen(84))
+    sign = (torch.randint(0, 2, (K,), generator=gen(85)) * 2 - 1).float()
+    P = torch.zeros(K, K)
+    P[torch.arange(K), perm] = sign
+    x0 = torch.randint(-1, 2, (M, K), generator=gen(86)).float()
+    want = [x0]
+    for _ in range(steps):
+        want.append(want[-1] @ P.T + want[-1])
+    dP, eye, x, zero = (t.to(BF16).to(DEV) for t in (P, torch.eye(K), x0, torch.zeros(K, K)))
+    for _ in range(20):
+        y, w = x, zero.clone()
+        for i in range(steps):
+            tmg.linear(eye, dP.T.contiguous(), w)         # w = P again
+            y = tmg.linear(y, w, residual=y)
+            w.zero_() if i % 2 else tmg.linear(eye, zero, w)
+        g = tmg.grouped_gemm(y, dP[None], torch.tensor([0, M], dtype=torch.int32, device=DEV))
+        assert torch.equal(y.cpu().float(), want[-1])
+        assert torch.equal(g.cpu().float(), want[-1] @ P.T)
+    tmg.check()
+
+
+def test_linear_results_past_32_bits(tmg):
+    """More than 2^31 elements of D, of the residual and of preact."""
+    M, N, K = 280000, 8192, 16
+    A, B = ints((M, K), 87).to(DEV), ints((N, K), 88).to(DEV)
+    res = torch.ones((M, N), dtype=BF16, device=DEV)
+    pre = torch.empty_like(res)
+    D = tmg.linear(A, B, residual=res, preact=pre)
+    tmg.check()
+    for r in (slice(0, 50), slice(M - 50, M)):
+        z = A[r].cpu().to(W) @ B.cpu().to(W).T
+        exact(pre[r], z)
+        exact(D[r], z + 1)
+
+
+def test_wgrad_results_past_32_bits(tmg):
+    E, N, K, R = 260, 2048, 4224, 40
+    off = offsets_of([0] * (E - 1) + [R])
+    d, A = ints((R, N), 89), ints((R, K), 90)
+    dB = tmg.grouped_gemm_wgrad(d.to(DEV), A.to(DEV), off.to(DEV))
+    tmg.check()
+    exact(dB[E - 1], d.to(W).T @ A.to(W))
+    assert not dB[E - 2].any() and not dB[0].any()
+
+
 @pytest.mark.parametrize("act", sorted(ACTS))
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (77, 136, 64), (600, 264, 200), (130, 45, 33), (0, 16, 8)])
 def test_linear_backward(tmg, act, M, N, K):

@@ -237,6 +237,19 @@ def test_combine_unused_rows_are_not_read(tmg):
     assert (out[0] == 1.0).all() and (out[1] == 0.0).all()
 
 
+def test_combine_past_32_bits(tmg):
+    """Rows of Y, out and dY beyond 2^31 elements."""
+    T, H = 530000, 4096
+    Y = torch.zeros((T, H), dtype=BF16, device=DEV)
+    Y[T - 40:] = torch.randint(-4, 5, (40, H), generator=gen(40)).to(BF16).to(DEV)
+    slots = torch.arange(T, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    out = tmg.moe_combine(Y, slots)
+    dY, dw = tmg.moe_combine_backward(out, Y, slots)
+    tmg.check()
+    assert torch.equal(out[T - 50:], Y[T - 50:]) and torch.equal(dY[T - 50:], Y[T - 50:])
+    assert torch.equal(dw[T - 50:, 0].cpu().to(W), Y[T - 50:].cpu().to(W).square().sum(1))
+
+
 @pytest.mark.parametrize("T,k,H", [(1, 1, 8), (1, 8, 4096), (37, 2, 200), (130, 6, 1023), (20, 16, 5000), (3, 3, 1), (0, 2, 16)])
 @pytest.mark.parametrize("weighted", [True, False])
 def test_combine_backward(tmg, T, k, H, weighted):
