@@ -15,7 +15,6 @@ recorded on it, so their memory is not reused before its work is done.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple
 
 import torch
@@ -26,6 +25,8 @@ from ._native import BF16, E4M3, F32
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4, "swiglu_grad": 5}
 _INPUTS = {torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
 _LOGITS = {torch.float32: F32, torch.bfloat16: BF16}
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_current = torch._C._cuda_getCurrentRawStream
 
 
 class Routing(NamedTuple):
@@ -38,8 +39,7 @@ class Routing(NamedTuple):
 
 
 def _stream(stream, tensors) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(tensors[0].device.index)
+    """The handle of a stream that is not None."""
     if hasattr(stream, "cuda_stream"):
         if stream != torch.cuda.current_stream():
             for t in tensors:
@@ -51,10 +51,10 @@ def _stream(stream, tensors) -> int:
 
 def _check(name, t, dtype, shape, device=None, inner=True):
     """A CUDA tensor of this dtype and shape (unit column stride when `inner`)."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda or (device is not None and t.device != device):
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {shape}"
                          f"{'' if device is None else f' on {device}'}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if inner and t.dim() and shape[-1] > 1 and t.stride(-1) != 1:
+    if inner and t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name} needs a unit column stride, got strides {t.stride()}")
     return t
 
@@ -63,7 +63,7 @@ def _flat(name, t, dtype, shape, device):
     """The pointer of an optional contiguous tensor."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return t.data_ptr()
 
@@ -84,15 +84,16 @@ def moe_route(logits: torch.Tensor, k: int, *, normalize: bool = True, stream=No
     dt = _LOGITS.get(logits.dtype)
     if dt is None:
         raise TypeError(f"unsupported logits dtype {logits.dtype}: use float32 or bfloat16")
-    _check("logits", logits, logits.dtype, (T, E))
+    if logits.stride(1) != 1:
+        _check("logits", logits, logits.dtype, (T, E))
     dev = logits.device
-    i32 = torch.int32
-    weights, experts = torch.empty((T, k), dtype=torch.float32, device=dev), torch.empty((T, k), dtype=i32, device=dev)
-    offsets, rows = torch.empty(E + 1, dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev)
-    slots = torch.empty((T, k), dtype=i32, device=dev)
+    weights, experts = torch.empty((T, k), dtype=_f32, device=dev), torch.empty((T, k), dtype=_i32, device=dev)
+    offsets, rows = torch.empty(E + 1, dtype=_i32, device=dev), torch.empty(T * k, dtype=_i32, device=dev)
+    slots = torch.empty((T, k), dtype=_i32, device=dev)
+    s = _current(dev.index) if stream is None else _stream(stream, (logits, weights, experts, offsets, rows, slots))
     st = _native.lib().tmg_moe_route(logits.data_ptr(), T, E, k, logits.stride(0), dt, 1 if normalize else 0,
                                      weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                                     slots.data_ptr(), _stream(stream, (logits, weights, experts, offsets, rows, slots)))
+                                     slots.data_ptr(), s)
     if st:
         _native.raise_on(st)
     return Routing(weights, experts, offsets, rows, slots)
@@ -106,14 +107,15 @@ def moe_route_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: to
     dt = _LOGITS.get(logits.dtype)
     if dt is None:
         raise TypeError(f"unsupported logits dtype {logits.dtype}: use float32 or bfloat16")
-    _check("logits", logits, logits.dtype, (T, E))
+    if logits.stride(1) != 1:
+        _check("logits", logits, logits.dtype, (T, E))
     k = experts.shape[-1]
     dev = logits.device
     d = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    s = _current(dev.index) if stream is None else _stream(stream, (logits, experts, dweights, d))
     st = _native.lib().tmg_moe_route_backward(logits.data_ptr(), T, E, k, logits.stride(0), dt, 1 if normalize else 0,
-                                              _flat("experts", experts, torch.int32, (T, k), dev),
-                                              _flat("dweights", dweights, torch.float32, (T, k), dev), d.data_ptr(),
-                                              _stream(stream, (logits, experts, dweights, d)))
+                                              _flat("experts", experts, _i32, (T, k), dev),
+                                              _flat("dweights", dweights, _f32, (T, k), dev), d.data_ptr(), s)
     if st:
         _native.raise_on(st)
     return d
@@ -128,18 +130,19 @@ def moe_combine(Y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | No
     R, H = _matrix("Y", Y)
     T, k = _matrix("slots", slots)
     dev = Y.device
-    _check("Y", Y, torch.bfloat16, (R, H))
+    _check("Y", Y, _bf16, (R, H))
     if residual is not None:
-        _check("residual", residual, torch.bfloat16, (T, H), dev)
+        _check("residual", residual, _bf16, (T, H), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H), dtype=_bf16, device=dev)
     else:
-        _check("out", out, torch.bfloat16, (T, H), dev)
-    st = _native.lib().tmg_moe_combine(Y.data_ptr(), R, Y.stride(0), _flat("slots", slots, torch.int32, (T, k), dev),
-                                       _flat("weights", weights, torch.float32, (T, k), dev),
+        _check("out", out, _bf16, (T, H), dev)
+    s = _current(dev.index) if stream is None else _stream(stream, (Y, slots, weights, residual, out))
+    st = _native.lib().tmg_moe_combine(Y.data_ptr(), R, Y.stride(0), _flat("slots", slots, _i32, (T, k), dev),
+                                       _flat("weights", weights, _f32, (T, k), dev),
                                        None if residual is None else residual.data_ptr(),
                                        0 if residual is None else residual.stride(0), out.data_ptr(), out.stride(0),
-                                       T, H, k, _stream(stream, (Y, slots, weights, residual, out)))
+                                       T, H, k, s)
     if st:
         _native.raise_on(st)
     return out
@@ -153,16 +156,16 @@ def moe_combine_backward(dOut: torch.Tensor, Y: torch.Tensor, slots: torch.Tenso
     T, H = _matrix("dOut", dOut)
     R, _ = _matrix("Y", Y)
     dev = dOut.device
-    _check("dOut", dOut, torch.bfloat16, (T, H))
-    _check("Y", Y, torch.bfloat16, (R, H), dev)
+    _check("dOut", dOut, _bf16, (T, H))
+    _check("Y", Y, _bf16, (R, H), dev)
     k = slots.shape[-1]
-    dY = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    dY = torch.empty((R, H), dtype=_bf16, device=dev)
+    dw = torch.empty((T, k), dtype=_f32, device=dev)
+    s = _current(dev.index) if stream is None else _stream(stream, (dOut, Y, slots, weights, dY, dw))
     st = _native.lib().tmg_moe_combine_backward(dOut.data_ptr(), dOut.stride(0), Y.data_ptr(), R, Y.stride(0),
-                                                _flat("slots", slots, torch.int32, (T, k), dev),
-                                                _flat("weights", weights, torch.float32, (T, k), dev), dY.data_ptr(),
-                                                dw.data_ptr(), T, H, k,
-                                                _stream(stream, (dOut, Y, slots, weights, dY, dw)))
+                                                _flat("slots", slots, _i32, (T, k), dev),
+                                                _flat("weights", weights, _f32, (T, k), dev), dY.data_ptr(),
+                                                dw.data_ptr(), T, H, k, s)
     if st:
         _native.raise_on(st)
     return dY, dw
@@ -199,22 +202,21 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, D: tor
     if act == 5 and preact is None:
         raise ValueError("swiglu_grad reads preact")
     if act and preact is not None:
-        _check("preact", preact, torch.bfloat16, (R, pcols), dev)
+        _check("preact", preact, _bf16, (R, pcols), dev)
     elif preact is not None:
         raise ValueError("preact goes with swiglu and swiglu_grad")
     if D is None:
-        D = torch.empty((R, cols), dtype=torch.bfloat16, device=dev)
+        D = torch.empty((R, cols), dtype=_bf16, device=dev)
     else:
-        _check("D", D, torch.bfloat16, (R, cols), dev)
-    a = _native.GroupedArgs(A.data_ptr(), B.data_ptr(), D.data_ptr(),
-                            _flat("offsets", offsets, torch.int32, (E + 1,), dev),
-                            _flat("rows", rows, torch.int32, (R,), dev),
-                            _flat("scale_a", scale_a, torch.float32, (T,), dev),
-                            _flat("scale_b", scale_b, torch.float32, (E, N), dev),
-                            None if preact is None else preact.data_ptr(), R, N, K, E, T, *A.stride(), *B.stride(),
-                            D.stride(0), 0 if preact is None else preact.stride(0), dt, act)
-    st = _native.lib().tmg_grouped_gemm(ctypes.byref(a),
-                                        _stream(stream, (A, B, offsets, rows, preact, scale_a, scale_b, D)))
+        _check("D", D, _bf16, (R, cols), dev)
+    a = _native.pack_grouped(A.data_ptr(), B.data_ptr(), D.data_ptr(), _flat("offsets", offsets, _i32, (E + 1,), dev),
+                             0 if rows is None else _flat("rows", rows, _i32, (R,), dev),
+                             0 if scale_a is None else _flat("scale_a", scale_a, _f32, (T,), dev),
+                             0 if scale_b is None else _flat("scale_b", scale_b, _f32, (E, N), dev),
+                             0 if preact is None else preact.data_ptr(), R, N, K, E, T, *A.stride(), *B.stride(),
+                             D.stride(0), 0 if preact is None else preact.stride(0), dt, act)
+    s = _current(dev.index) if stream is None else _stream(stream, (A, B, offsets, rows, preact, scale_a, scale_b, D))
+    st = _native.lib().tmg_grouped_gemm(a, s)
     if st:
         _native.raise_on(st)
     return D
@@ -229,17 +231,17 @@ def grouped_gemm_wgrad(dD: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor,
     T, K = _matrix("A", A)
     E = offsets.shape[0] - 1
     dev = dD.device
-    _check("dD", dD, torch.bfloat16, (R, N), inner=False)
-    _check("A", A, torch.bfloat16, (T, K), dev, inner=False)
+    _check("dD", dD, _bf16, (R, N), inner=False)
+    _check("A", A, _bf16, (T, K), dev, inner=False)
     if rows is None and T != R:
         raise ValueError(f"without rows, A must have dD's {R} rows, got {T}")
     if dB is None:
-        dB = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev)
+        dB = torch.empty((E, N, K), dtype=_bf16, device=dev)
+    s = _current(dev.index) if stream is None else _stream(stream, (dD, A, offsets, rows, dB))
     st = _native.lib().tmg_grouped_gemm_wgrad(dD.data_ptr(), *dD.stride(), A.data_ptr(), *A.stride(),
-                                              _flat("dB", dB, torch.bfloat16, (E, N, K), dev),
-                                              _flat("offsets", offsets, torch.int32, (E + 1,), dev),
-                                              _flat("rows", rows, torch.int32, (R,), dev), R, N, K, E, T,
-                                              _stream(stream, (dD, A, offsets, rows, dB)))
+                                              _flat("dB", dB, _bf16, (E, N, K), dev),
+                                              _flat("offsets", offsets, _i32, (E + 1,), dev),
+                                              _flat("rows", rows, _i32, (R,), dev), R, N, K, E, T, s)
     if st:
         _native.raise_on(st)
     return dB
@@ -266,23 +268,22 @@ def linear(A: torch.Tensor, B: torch.Tensor, D: torch.Tensor | None = None, *, b
     if not 0 <= act <= 3:
         raise ValueError(f"unknown activation {activation!r}; one of 'none', 'relu', 'silu', 'gelu'")
     if D is None:
-        D = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        D = torch.empty((M, N), dtype=_bf16, device=dev)
     else:
-        _check("D", D, torch.bfloat16, (M, N), dev)
+        _check("D", D, _bf16, (M, N), dev)
     if residual is not None:
-        _check("residual", residual, torch.bfloat16, (M, N), dev)
+        _check("residual", residual, _bf16, (M, N), dev)
     if preact is not None:
-        _check("preact", preact, torch.bfloat16, (M, N), dev)
-    a = _native.LinearArgs(A.data_ptr(), B.data_ptr(), D.data_ptr(),
-                           _flat("scale_a", scale_a, torch.float32, (M,), dev),
-                           _flat("scale_b", scale_b, torch.float32, (N,), dev),
-                           _flat("bias", bias, torch.float32, (N,), dev),
-                           None if residual is None else residual.data_ptr(),
-                           None if preact is None else preact.data_ptr(), M, N, K, *A.stride(), *B.stride(),
-                           D.stride(0), 0 if residual is None else residual.stride(0),
-                           0 if preact is None else preact.stride(0), dt, act)
-    st = _native.lib().tmg_linear(ctypes.byref(a),
-                                  _stream(stream, (A, B, D, bias, residual, preact, scale_a, scale_b)))
+        _check("preact", preact, _bf16, (M, N), dev)
+    a = _native.pack_linear(A.data_ptr(), B.data_ptr(), D.data_ptr(),
+                            0 if scale_a is None else _flat("scale_a", scale_a, _f32, (M,), dev),
+                            0 if scale_b is None else _flat("scale_b", scale_b, _f32, (N,), dev),
+                            0 if bias is None else _flat("bias", bias, _f32, (N,), dev),
+                            0 if residual is None else residual.data_ptr(), 0 if preact is None else preact.data_ptr(),
+                            M, N, K, *A.stride(), *B.stride(), D.stride(0), 0 if residual is None else residual.stride(0),
+                            0 if preact is None else preact.stride(0), dt, act)
+    s = _current(dev.index) if stream is None else _stream(stream, (A, B, D, bias, residual, preact, scale_a, scale_b))
+    st = _native.lib().tmg_linear(a, s)
     if st:
         _native.raise_on(st)
     return D
@@ -301,22 +302,23 @@ def linear_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, preac
     act = ACTIVATIONS.get(activation, -1)
     if not 0 <= act <= 3:
         raise ValueError(f"unknown activation {activation!r}; one of 'none', 'relu', 'silu', 'gelu'")
-    _check("dD", dD, torch.bfloat16, (M, N))
-    _check("A", A, torch.bfloat16, (M, K), dev)
-    _check("B", B, torch.bfloat16, (N, K), dev)
+    _check("dD", dD, _bf16, (M, N))
+    _check("A", A, _bf16, (M, K), dev)
+    _check("B", B, _bf16, (N, K), dev)
     if act:
         if preact is None:
             raise ValueError(f"the gradient of {activation} reads preact")
-        _check("preact", preact, torch.bfloat16, (M, N), dev)
+        _check("preact", preact, _bf16, (M, N), dev)
     else:
         preact = None
-    dA = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    dB = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
-    dbias = torch.empty((N,), dtype=torch.float32, device=dev)
+    dA = torch.empty((M, K), dtype=_bf16, device=dev)
+    dB = torch.empty((N, K), dtype=_bf16, device=dev)
+    dbias = torch.empty((N,), dtype=_f32, device=dev)
+    s = _current(dev.index) if stream is None else _stream(stream, (dD, A, B, preact, dA, dB, dbias))
     st = _native.lib().tmg_linear_backward(dD.data_ptr(), dD.stride(0), None if preact is None else preact.data_ptr(),
                                            0 if preact is None else preact.stride(0), A.data_ptr(), A.stride(0),
                                            B.data_ptr(), B.stride(0), dA.data_ptr(), dB.data_ptr(), dbias.data_ptr(),
-                                           M, N, K, act, _stream(stream, (dD, A, B, preact, dA, dB, dbias)))
+                                           M, N, K, act, s)
     if st:
         _native.raise_on(st)
     return dA, dB, dbias
