@@ -58,7 +58,7 @@ struct WgradArgs {
     void *dB;                  // (E, N, K) contiguous
     int64_t R, T, N, K, E;
     int64_t ldd, d_col, lda, a_col;
-    const int32_t *offsets, *rows;
+    const int32_t *offsets, *rows;     // offsets null: one group of all R rows
 };
 // ------------------------------------------------------------- routing
 struct RouteArgs {
