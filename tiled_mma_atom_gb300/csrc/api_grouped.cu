@@ -129,16 +129,16 @@ tmg_status gather(const DeviceState &ds, const void **A, int64_t *lda, int64_t s
 // weights again.
 float block_ns(int w)
 {
-    return w <= 128 ? 260.f : w <= 160 ? 285.f : w <= 192 ? 305.f : w <= 224 ? 324.f : 350.f;
+    return w <= 128 ? 245.f : w <= 160 ? 255.f : w <= 192 ? 262.f : w <= 224 ? 266.f : 295.f;
 }
 
 // Widest tile.  One group: the width whose waves of tiles take the least time
 // (4096 x 4096 x 4096: 19 x 16 tiles of 224 columns are four waves of 76 pairs
-// like 16 x 16 of 256, and take 79.5 us against 87; 700 x 5000 x 2000: 21.4 us
-// in one wave of 256 columns, 28.8 in two of 192).  Several: all rows of an
+// like 16 x 16 of 256, and take 79.5 us against 87; 1024 x 8192 x 8192: 82 us in
+// two waves of 256 columns, 103 in three of 224).  Several: all rows of an
 // evenly filled group, with room for half as many again; narrower tiles make a
 // deeper ring.
-int tile_width(const GroupedArgs &a, int64_t tiles_n, int pairs)
+int tile_width(const GroupedArgs &a, int64_t tiles_n, int64_t num_kb, int pairs)
 {
     if (a.E > 1) {
         const int64_t even = (a.R + a.E - 1) / a.E, room = even + even / 2 + 8;
@@ -147,8 +147,9 @@ int tile_width(const GroupedArgs &a, int64_t tiles_n, int pairs)
     int best = 0;
     double best_ns = 0;
     for (int w = kSwMaxW; w >= 32; w -= 32) {
-        const int64_t tiles = (a.R + w - 1) / w * tiles_n;
-        const double ns = static_cast<double>((tiles + pairs - 1) / pairs) * block_ns(w);
+        SwapTail tail;
+        const int64_t tiles = std::min((a.R + w - 1) / w * tiles_n, kMax31);
+        const double ns = swap_time(static_cast<int>(tiles), pairs, static_cast<int>(num_kb), w, block_ns(w), 0.f, tail);
         if (!best || ns < 0.95 * best_ns || (a.R <= w && ns <= best_ns)) {
             best = w;
             best_ns = ns;
@@ -180,9 +181,10 @@ SplitPlan split_plan(const GroupedArgs &a, int64_t F, bool swiglu, int64_t num_k
     auto row_tiles = [&](int64_t w) { return a.E == 1 ? (a.R + w - 1) / w : std::min(a.R, groups + a.R / w); };
     const double hbm = static_cast<double>(groups) * a.N * a.K * elem / 6700.0;
     const int64_t pair_tiles = row_tiles(maxw) * pair_tiles_n;
-    const double whole = static_cast<double>((pair_tiles + pairs - 1) / pairs) * num_kb * block_ns(maxw);
-    const double shared = static_cast<double>(pair_tiles) / pairs * num_kb * block_ns(maxw) + 6000 + 4000 * ((maxw + 63) / 64 - 1);
-    double best_ns = 5500 + std::max(hbm + 2800, std::min(whole, shared)) + 8 * maxw;
+    SwapTail tail;
+    double best_ns = 5500 + 8 * maxw + swap_time(static_cast<int>(std::min(pair_tiles, kMax31)), static_cast<int>(pairs),
+                                                 static_cast<int>(num_kb), maxw, block_ns(maxw),
+                                                 static_cast<float>(hbm) + 2800, tail);
     const int64_t even = (a.R + groups - 1) / groups;
     const int64_t least = a.E == 1 ? 16 : std::min<int64_t>(256, even + even / 2 + 8);     // a group's rows in one tile
     for (int64_t w = 16; w <= 256; w *= 2) {
@@ -225,7 +227,7 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
 
     const int pairs = ds.num_sms / 2;
     const int64_t tiles_n = (F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
-    p.maxw = tile_width(a, tiles_n, pairs);
+    p.maxw = tile_width(a, tiles_n, (K + kb - 1) / kb, pairs);
     const SplitPlan plan = split_plan(a, F, swiglu, (K + kb - 1) / kb, elem, tiles_n, p.maxw, ds.num_sms);
     p.gather = a.rows && (plan.cluster ? plan.w <= kSplitGatherW : p.maxw <= kSwGatherW);
 
@@ -345,16 +347,12 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     p.group = 16 * p.maxw * K * elem <= (int64_t{32} << 20) ? 16 : 8;
     if ((a.R / 32 + a.E) * tiles_n > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
-    // A split tile's partials go through L2 and its epilogue starts over: 6 us
-    // with one 32-column chunk per epilogue warp, 4 us more for every other
     p.block_ns = block_ns(p.maxw);
-    p.split_ns = 6000.f + 4000.f * ((p.maxw + 63) / 64 - 1);
-    if ((K + kb - 1) / kb * p.block_ns > p.split_ns) {
+    // no split of a tile this short pays (two pieces, half a tile saved)
+    if ((K + kb - 1) / kb * p.block_ns * 0.5f > 2500.f + p.maxw / 256.f * 5200.f) {
         p.partials = static_cast<float *>(workspace(kWsPartials, pairs * sw_partial_floats(p.maxw) * sizeof(float), s, &st));
         if (!p.partials)
             return st;
-    } else {
-        p.split_ns = -1.f;
     }
     if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
         return st;

@@ -9,9 +9,11 @@
 // Tiles keep their order, and with it the reuse of operands in L2; which pair
 // computes a tile does not change its value.
 //
-// Warp 10 of CTA 0 fetches one tile ahead and sends it to both CTAs with
-// st.async, which counts its bytes on the receiver's barrier; warp 10 of each
-// CTA arms that barrier.  The warps that read a slot (19 over the pair) free it
+// Warp 10 of CTA 0 fetches one tile ahead of the pair's producer, no more: pairs
+// start up to 40 us apart when launches overlap, and the first to start would
+// take the tiles of the last.  It sends the number to both CTAs with st.async,
+// which counts its bytes on the receiver's barrier; warp 10 of each CTA arms
+// that barrier.  The warps that read a slot (19 over the pair) free it
 // by arriving on CTA 0.  The pair that fetches the last number resets the
 // counter, so it is zero again for the next launch.
 #pragma once
@@ -25,8 +27,8 @@ constexpr int kFeedReaders = 19;        // producer and eight epilogue warps of 
 
 struct FeedSmem {
     uint64_t full[kFeedSlots], empty[kFeedSlots];
+    uint64_t taken;                   // CTA 0: its producer has taken a tile
     int tile[kFeedSlots];
-    int pad[2];
 };
 
 __device__ __forceinline__ void feed_init(FeedSmem *f, int readers = kFeedReaders)
@@ -35,6 +37,7 @@ __device__ __forceinline__ void feed_init(FeedSmem *f, int readers = kFeedReader
         mbar_init(&f->full[i], 1);
         mbar_init(&f->empty[i], readers);
     }
+    mbar_init(&f->taken, 1);
 }
 
 __device__ __forceinline__ void st_async_u32(uint32_t addr, uint32_t v, uint32_t bar)
@@ -52,9 +55,11 @@ __device__ __forceinline__ void feed_run(FeedSmem *f, uint32_t rank, int whole, 
     const uint32_t last = static_cast<uint32_t>(whole - nclusters) + static_cast<uint32_t>(nclusters) - 1;
     int slot = 0;
     uint32_t phase = 0;
-    for (;;) {
+    for (uint32_t n = 0;; ++n) {
         int tile = 0;
         if (rank == 0) {
+            if (n > 0 && !mbar_wait_warp(&f->taken, (n - 1) & 1u, err, abort, kSiteProducerEmpty))
+                return;
             if (!mbar_wait_cluster_warp(&f->empty[slot], phase ^ 1u, err, abort, kSiteProducerEmpty))
                 return;
             uint32_t v = 0;
@@ -93,6 +98,7 @@ struct Feed {
     int whole, nclusters, first;      // first: the pair's fixed tile, or -1 once taken
     int slot = 0;
     uint32_t phase = 0;
+    bool producer = false;            // CTA 0's producer
 
     __device__ Feed(FeedSmem *f_, int cluster, int nclusters_, int whole_)
         : f(f_), whole(whole_), nclusters(nclusters_), first(cluster)
@@ -112,8 +118,11 @@ struct Feed {
             return false;
         tile = *const_cast<volatile int *>(&f->tile[slot]);
         __syncwarp();
-        if ((threadIdx.x & 31) == 0)
+        if ((threadIdx.x & 31) == 0) {
             mbar_arrive_cluster(mapa_shared(smem_u32(&f->empty[slot]), 0));
+            if (producer)
+                mbar_arrive_cluster(smem_u32(&f->taken));
+        }
         if (++slot == kFeedSlots) {
             slot = 0;
             phase ^= 1u;

@@ -10,10 +10,10 @@
 // a table of tile numbers, so the host never waits for the routing.  Within a
 // group the tiles go in bands of `group` row tiles, row tiles fastest, so that
 // the pairs running together share weight tiles and A panels in L2.  Each pair
-// takes the next whole tile as it gets free (feed.cuh); where the last wave
-// would leave pairs idle for longer than a split costs, it and another wave are
-// cut into equal runs of K blocks first (stream-K) and summed from fp32 partials
-// in pair order: results do not depend on timing.
+// takes the next whole tile as it gets free (feed.cuh); where few tiles would be
+// left for the last wave, those are cut along K over several pairs first
+// (swap_time) and summed from fp32 partials in pair order: results do not depend
+// on timing.
 //
 // Operands.  Weights: K-major through a 3-D map (K, N, E), or MN-major (N, K,
 // E) in 64 x 64 boxes; out-of-range rows and K read as zeros, per expert, so a
@@ -70,8 +70,7 @@ struct SwapArgs {
     int stages, stage_bytes;
     int group;                 // row tiles per band
     float block_ns;            // a K block of a tile of maxw columns
-    float split_ns;            // what a stream-K tail adds; < 0: never split
-    float *partials;           // sw_partial_floats(maxw) per pair
+    float *partials;           // sw_partial_floats(maxw) per pair; null: no tile is split
     uint32_t *counters;        // 16 per tile of two waves
     uint32_t *feed;            // the tile counter
 };
@@ -87,6 +86,35 @@ __host__ __device__ inline int sw_box_rows(int half) { return half <= 16 ? 16 : 
 __host__ inline int sw_smem(int stages, int stage_bytes, int E)
 {
     return 1024 + stages * stage_bytes + kSwStaging + kSwBars + 8 * (E + 1);
+}
+
+// Nanoseconds that `total` tiles of w columns take over np pairs, and how the last
+// wave is split (tail): where at most half the pairs have a tile in it, each of
+// its tiles is cut along K over 2 to 8 pairs, before their whole tiles, so that
+// the sums are under way while those run.  A cut adds 2.5 us + w / 256 (4 + 0.6 us
+// a piece) (measured at 128 to 256 columns; 2489 x 5648 x 8192, 230 tiles: 151
+// us whole, 129 with two tiles over eight pairs each).  block_ns: a K block of a
+// tile; hbm_ns: the time of the weights' bytes.
+struct SwapTail {
+    int tiles, pairs;
+};
+__host__ __device__ inline float swap_time(int total, int np, int num_kb, int w, float block_ns, float hbm_ns, SwapTail &tail)
+{
+    const int q = total / np, rem = total - q * np;
+    const float tile = num_kb * block_ns;
+    const float whole = (q + (rem ? 1 : 0)) * tile;
+    const float best = whole > hbm_ns ? whole : hbm_ns;
+    const int each = rem == 0 ? 0 : np / rem < 8 ? np / rem : 8;
+    tail.tiles = tail.pairs = 0;
+    if (each < 2 || num_kb < each)
+        return best;
+    const float shared = q * tile + tile / each;
+    const float cut = (shared > hbm_ns ? shared : hbm_ns) + 2500.f + w * (1.f / 256.f) * (4000.f + 600.f * each);
+    if (cut >= best)
+        return best;
+    tail.tiles = rem;
+    tail.pairs = rem * each;
+    return cut;
 }
 
 cudaError_t launch_swap(const SwapArgs &a, int epi, bool e4m3, int num_sms, const ErrCtx &err, cudaStream_t s);
@@ -449,14 +477,14 @@ struct SwapWalk {
     const ErrCtx &err;
     volatile int *abort;
 
-    __device__ SwapWalk(FeedSmem *f, int c, int nc, int total, int sk_, int nkb, const ErrCtx &e, volatile int *ab)
-        : feed(f, c, nc, total - sk_), sk(sk_), num_kb(nkb), err(e), abort(ab)
+    __device__ SwapWalk(FeedSmem *f, int c, int nc, int total, const SwapTail &t, int nkb, const ErrCtx &e, volatile int *ab)
+        : feed(f, c, nc, total - t.tiles), sk(t.tiles), num_kb(nkb), err(e), abort(ab)
     {
         u = u_end = 0;
-        if (sk) {
+        if (c < t.pairs) {
             const int64_t U = static_cast<int64_t>(sk) * num_kb;
-            u = U * c / nc;
-            u_end = U * (c + 1) / nc;
+            u = U * c / t.pairs;
+            u_end = U * (c + 1) / t.pairs;
         }
     }
 
@@ -555,21 +583,14 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    // Whole tiles, or the last waves split.  Times in ns: a K block of a tile
-    // takes p.block_ns of a pair, and HBM (6.7 TB/s) takes 4.8 for the 32 KB of
-    // its weights (narrow tiles read their weights once each); a split adds
-    // p.split_ns.
-    const int total = start[p.E], rem = total % nclusters;
-    int sk = 0;
-    if (rem && p.split_ns >= 0) {
-        const int take = rem + (total > nclusters ? nclusters : 0);
-        const float blocks = static_cast<float>(total) * num_kb, hbm = p.maxw < kSwMaxW ? 4.8f * blocks : 0.f;
-        const float whole = fmaxf(hbm, (total / nclusters + 1.f) * num_kb * p.block_ns);
-        const float split = fmaxf(hbm, blocks / nclusters * p.block_ns) + p.split_ns;
-        if (whole > split && static_cast<int64_t>(take) * num_kb >= nclusters)
-            sk = take;
-    }
-    SwapWalk walk(feed_smem, cluster, nclusters, total, sk, num_kb, err, abort_flag);
+    // HBM (6.7 TB/s) takes 4.8 ns for the 32 KB of a K block's weights (narrow
+    // tiles read their weights once each).
+    const int total = start[p.E];
+    SwapTail tail{0, 0};
+    if (p.partials)
+        swap_time(total, nclusters, num_kb, p.maxw, p.block_ns, p.maxw < kSwMaxW ? 4.8f * total * num_kb : 0.f, tail);
+    const int sk = tail.tiles;
+    SwapWalk walk(feed_smem, cluster, nclusters, total, tail, num_kb, err, abort_flag);
     int tile, kb0, kb1, slot;
     bool partial;
     // The dense product's tiles depend on sizes only: its warps wait for the
@@ -582,6 +603,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
+        walk.feed.producer = rank == 0;
         while (ok && walk.next(tile, kb0, kb1, partial, slot)) {
             const SwapTile x = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group);
             if constexpr (EPI == kSwDense)
@@ -769,8 +791,8 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 if (half < chunks) {
-                    c_first = unit_owner(static_cast<int64_t>(tile) * num_kb, U, nclusters);
-                    c_last = unit_owner(static_cast<int64_t>(tile + 1) * num_kb - 1, U, nclusters);
+                    c_first = unit_owner(static_cast<int64_t>(tile) * num_kb, U, tail.pairs);
+                    c_last = unit_owner(static_cast<int64_t>(tile + 1) * num_kb - 1, U, tail.pairs);
                     const int64_t at = (static_cast<int64_t>(tile) * 2 + rank) * 8 + ew;
                     finish = last_arrival(p.counters + at, c_last - c_first,
                                           bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters));
@@ -796,7 +818,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                         for (int i = 0; i < 32; ++i)
                             v[i] = 0.f;
                         add_pieces(v, p.partials, limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
-                            const int s2 = static_cast<int>((U * cc / nclusters) / num_kb) == tile ? 0 : 1;
+                            const int s2 = static_cast<int>((U * cc / tail.pairs) / num_kb) == tile ? 0 : 1;
                             return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * piece;
                         }, err);
                     }

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
+        walk.feed.producer = rank == 0;
         while (ok && walk.next(e, local_tile, kb0, kb1, partial, slot, unit0, blocks)) {
             tile_coords(local_tile, tiles_n, tiles_k, p.group, tn, tk);
             const int lo = off[e], hi = lo + walk.rows(e);
