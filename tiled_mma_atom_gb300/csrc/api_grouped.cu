@@ -404,13 +404,10 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
     if ((a.R / 64 + 2 * a.E) * per > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tile blocks");
     const int pairs = ds.num_sms / 2;
-    p.split_cost = 32;
-    if ((a.R + 63) / 64 > p.split_cost) {
+    if ((a.R + 63) / 64 > 2 * kWgCutBlocks) {      // else no cut pays
         p.partials = static_cast<float *>(workspace(kWsPartials, wgrad_partial_bytes(ds.num_sms), s, &st));
         if (!p.partials)
             return st;
-    } else {
-        p.split_cost = -1;
     }
     if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
         return st;

@@ -19,9 +19,8 @@
 //
 // Schedule: every group has the same tiles (bands of `group` column tiles), of
 // as many blocks as the group has; pairs take them as they get free (feed.cuh).
-// Where the last wave would leave pairs idle for longer than a split costs, the
-// first tiles are cut into equal runs of blocks and summed from fp32 partials in
-// pair order.  Roles as in swap_kernel.cuh.
+// Where few tiles would be left for the last wave, as many of the first are cut
+// over 2 to 8 pairs each and summed from fp32 partials in pair order.  Roles as in swap_kernel.cuh.
 //
 // Bound by the tensor pipe (65 % busy) and, in short groups, by the epilogue:
 // 65528 rows over 64 groups, 2048 x 1024, 185 us (1.49 PFLOP/s).
@@ -69,10 +68,10 @@ struct WgWalk {
     const ErrCtx &err;
     volatile int *abort;
 
-    __device__ WgWalk(FeedSmem *f, int c, int nc, int sk_, int64_t U, int total, int per_, int E_, const int *off_,
+    __device__ WgWalk(FeedSmem *f, int c, int nc, int sk_, int64_t U, int cut, int total, int per_, int E_, const int *off_,
                       const int *unit_, const ErrCtx &er, volatile int *ab)
-        : off(off_), unit(unit_), feed(f, c, nc, total - sk_), per(per_), E(E_), sk(sk_), u(U ? U * c / nc : 0),
-          u_end(U ? U * (c + 1) / nc : 0), first(true), err(er), abort(ab)
+        : off(off_), unit(unit_), feed(f, c, nc, total - sk_), per(per_), E(E_), sk(sk_), u(c < cut ? U * c / cut : 0),
+          u_end(c < cut ? U * (c + 1) / cut : 0), first(true), err(er), abort(ab)
     {
     }
 
@@ -193,20 +192,21 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     const uint32_t tmem_base = *tmem_slot;
 
     const int total = p.E * per, rem = total % nclusters;
-    int sk = 0;
+    int sk = 0, cut = 0;             // split tiles, pairs that share their blocks
     int64_t U = 0;
-    if (rem && p.split_cost >= 0) {
-        const int take = rem + (total > nclusters ? nclusters : 0);
-        const int e = take / per, blocks = e < p.E ? wg_blocks(off[e + 1] - off[e]) : 0;
-        const int64_t units = unit[e] + static_cast<int64_t>(take % per) * blocks;
-        // blocks of a tile, on average, times the share of pairs idle in the last wave
-        if (static_cast<int64_t>(unit[p.E]) / total * (nclusters - rem) > static_cast<int64_t>(p.split_cost) * nclusters &&
-            units >= nclusters) {
-            sk = take;
+    const int each = rem ? min(8, nclusters / rem) : 0;
+    if (p.partials && each >= 2) {
+        const int e = rem / per, blocks = e < p.E ? wg_blocks(off[e + 1] - off[e]) : 0;
+        const int64_t units = unit[e] + static_cast<int64_t>(rem % per) * blocks;
+        // a tile's blocks, on average, less a piece's, against what a cut costs
+        // in blocks (6.5 us + 0.6 a piece)
+        if (unit[p.E] / total * (each - 1) > (kWgCutBlocks + 2 * each) * each && units >= rem * each) {
+            sk = rem;
+            cut = rem * each;
             U = units;
         }
     }
-    WgWalk walk(feed_smem, cluster, nclusters, sk, U, total, per, p.E, off, unit, err, abort_flag);
+    WgWalk walk(feed_smem, cluster, nclusters, sk, U, cut, total, per, p.E, off, unit, err, abort_flag);
     int e, local_tile, kb0, kb1, slot, blocks, tn, tk;
     int64_t unit0;
     bool partial;
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 if (half < pairs) {
-                    c_first = unit_owner(unit0, U, nclusters);
-                    c_last = unit_owner(unit0 + blocks - 1, U, nclusters);
+                    c_first = unit_owner(unit0, U, cut);
+                    c_last = unit_owner(unit0 + blocks - 1, U, cut);
                     const int64_t at = ((static_cast<int64_t>(e) * per + local_tile) * 2 + rank) * 8 + ew;
                     finish = last_arrival(p.counters + at, c_last - c_first,
                                           bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters));
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                                 v[j] = 0.f;
                             if (c < c1)
                                 add_pieces(v, p.partials, p_limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
-                                    const int s2 = U * cc / nclusters >= unit0 ? 0 : 1;   // its run begins in this tile
+                                    const int s2 = U * cc / cut >= unit0 ? 0 : 1;   // its run begins in this tile
                                     return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * kWgPiece;
                                 }, err);
                         }

@@ -5,6 +5,8 @@
 
 namespace tmg {
 
+constexpr int kWgCutBlocks = 22;    // cost of a tile's cut in blocks of 64 rows, two more for every piece
+
 struct WgradTmaArgs {
     CUtensorMap tmD, tmA;      // dD (R, N) and A (R, K), boxes of 64 columns x 64 rows
     CUtensorMap tmD16, tmA16;  // the same, boxes of 16 rows
@@ -13,9 +15,8 @@ struct WgradTmaArgs {
     const int32_t *offsets;
     int R, N, K, E;
     int group;                 // column tiles of dD per band
-    int split_cost;            // cost of a split in blocks of 64 rows; < 0: never split
     int stages;                // set by the launch
-    float *partials;           // wgrad_partial_bytes()
+    float *partials;           // wgrad_partial_bytes(); null: no tile is cut
     uint32_t *counters;        // 16 per tile of two waves
     uint32_t *feed;            // the tile counter
 };
