@@ -727,13 +727,20 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
             if ((st = launched(cudaMemsetAsync(dbias, 0, N * sizeof(float), s), "cudaMemsetAsync(dbias)")) != TMG_OK)
                 return st;
         }
-        // dA (M, K) = dz (M, N) . B: B read as (K, N); dB (N, K) = dz^T . A.  Where
-        // its tiles fill the CTA pairs, the GEMM's pair kernel reads the
-        // MN-major operands in place (8191 x 4096 x 4096: dA 139 us against 143
-        // with the dense product, dB 161 against 189 with the weight gradient);
-        // else it would copy them (165 x 6408 x 736: dA 35 against 12; 2795 x 624
-        // x 4024: dB 31 against 22; one row of 4096 x 4096: dB 73 against 15).
+        // dA (M, K) = dz (M, N) . B: B read as (K, N); dB (N, K) = dz^T . A.  Each
+        // by the kernel that is faster.  Where the tiles do not fill the CTA pairs,
+        // the GEMM would copy the MN-major operands (165 x 6408 x 736: dA 35 us
+        // against 12 with the dense product; 2795 x 624 x 4024: dB 30 against 22
+        // with the weight gradient; one row of 4096 x 4096: dB 73 against 15).
+        // Where they do, its pair kernel reads them in place and is faster on short
+        // contractions (8191 x 4096 x 4096: dA 144 against 148; 1024 x 4096 x 4096:
+        // dB 26 against 30), slower on long ones (2048 x 8192 x 8192: dA 164 against
+        // 150; 6080 x 4520 x 3400: 151 against 144, dB 156 against 146; 8191 x 4096
+        // x 4096: dB 165 against 159).
         auto fills = [&](int64_t rows, int64_t cols) { return (rows + 255) / 256 * ((cols + 255) / 256) >= ds->num_sms / 2; };
+        const bool some = M > 0 && N > 0 && K > 0;
+        const bool a_product = some && (!fills(M, K) || N > 4096);
+        const bool b_wgrad = some && (!fills(N, K) || M < 64 || (M > 6000 && M >= N && M >= K));
         auto flat = [](int64_t r, int64_t c, int64_t sr, int64_t sc) {
             tmg_layout L;
             std::memset(&L, 0, sizeof L);
@@ -745,7 +752,7 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
             L.stride[1][0] = sc;
             return L;
         };
-        if (dA && !fills(M, K) && M > 0 && K > 0 && N > 0) {
+        if (dA && a_product) {
             GroupedArgs a{};
             a.A = dz;
             a.B = B;
@@ -764,7 +771,7 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
             if ((st = tmg_gemm_ex(dz, B, dA, M, K, N, TMG_BF16, &lz, &lb, nullptr, TMG_PATH_AUTO, stream)) != TMG_OK)
                 return st;
         }
-        if (dB && (!fills(N, K) || M < 64) && M > 0 && K > 0 && N > 0) {
+        if (dB && b_wgrad) {
             if ((st = run_wgrad(*ds, WgradArgs{dz, A, dB, M, M, N, K, 1, ldz, 1, lda, 1, nullptr, nullptr}, s)) != TMG_OK)
                 return st;
         } else if (dB) {
