@@ -393,6 +393,13 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
                 return st;
         }
     }
+    if (aligned(a.dB) && a.K % 8 == 0 && a.N * a.K * 2 < (int64_t{1} << 40)) {
+        const int64_t dims[3] = {a.K, a.N, a.E}, strides[2] = {a.K * 2, a.N * a.K * 2};
+        const int box[3] = {64, 32, 1};
+        if ((st = encode_nd(&p.tmOut, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.dB, dims, strides, box)) != TMG_OK)
+            return st;
+        p.tma_out = 1;
+    }
     p.dB = a.dB;
     p.offsets = a.offsets;
     p.R = static_cast<int>(a.R);

@@ -22,6 +22,10 @@
 // Where few tiles would be left for the last wave, as many of the first are cut
 // over 2 to 8 pairs each and summed from fp32 partials in pair order.  Roles as in swap_kernel.cuh.
 //
+// Results leave by TMA from swizzled 4 KB tiles, a warp's 32 rows of 64 columns,
+// where dB has 16-byte rows (128 groups of 16 rows, 2048 x 1024, 537 MB of dB: 97
+// us, 5.5 TB/s, against 124 with stores of each lane).
+//
 // Bound by the tensor pipe (65 % busy) and, in short groups, by the epilogue:
 // 65528 rows over 64 groups, 2048 x 1024, 185 us (1.49 PFLOP/s).
 #include "feed.cuh"
@@ -52,6 +56,15 @@ __device__ __forceinline__ void tma_gather4_pair_to(uint32_t dst, const CUtensor
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
                  " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+                 : "memory");
+}
+
+// The warp's staging tile (32 rows of 128 bytes, swizzled) to dB; rows and columns
+// outside are left out.
+__device__ __forceinline__ void tma_store_tile(const CUtensorMap *map, uint32_t src, int col, int row, int e)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row), "r"(e), "r"(src)
                  : "memory");
 }
 
@@ -399,6 +412,11 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 const uint32_t stg = smem_u32(staging + ew * 4096);
 #pragma unroll 1
                 for (int pr = half; pr < pairs; pr += 2) {
+                    if (p.tma_out) {
+                        if (lane == 0)                          // the tile's last store has read it
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                    }
                     // this lane's row, 64 columns, to the staging tile in
                     // 16-byte pieces (swizzled)
 #pragma unroll
@@ -427,6 +445,13 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                                    make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
                                               pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
                     }
+                    if (p.tma_out) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0 && n0 < p.N)
+                            tma_store_tile(&p.tmOut, stg, tk * 256 + pr * 64, n0, e);
+                        continue;
+                    }
                     __syncwarp();
                     // whole 128-byte lines out: eight lanes a row
 #pragma unroll
@@ -447,6 +472,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
             }
         }
+        if (p.tma_out && lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     __syncwarp();

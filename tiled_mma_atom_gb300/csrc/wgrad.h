@@ -11,6 +11,8 @@ struct WgradTmaArgs {
     CUtensorMap tmD, tmA;      // dD (R, N) and A (R, K), boxes of 64 columns x 64 rows
     CUtensorMap tmD16, tmA16;  // the same, boxes of 16 rows
     CUtensorMap tmDg, tmAg;    // the same, boxes of one row (gathers)
+    CUtensorMap tmOut;         // dB (E, N, K), boxes of 64 columns x 32 rows
+    int tma_out;               // tmOut is there (16-byte rows)
     void *dB;                  // (E, N, K) contiguous
     const int32_t *offsets;
     int R, N, K, E;
