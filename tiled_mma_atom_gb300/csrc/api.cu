@@ -319,8 +319,12 @@ tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const v
         if (i + 1 < rank)
             st[i] = static_cast<cuuint64_t>(strides[i]);
     }
+    const int inner = box[0] * (dt == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 ? 2 : 1);
+    const CUtensorMapSwizzle swizzle = inner == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
+                                       : inner == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                     : CU_TENSOR_MAP_SWIZZLE_128B;
     const CUresult r = g_encode(map, dt, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(TMG_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for a rank-%d operand", (int)r, rank);

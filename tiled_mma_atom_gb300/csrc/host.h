@@ -32,7 +32,8 @@ void log_choice(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
 
 // A tiled tensor map of `rank` dimensions: dims[i] extents (innermost first),
 // strides[i] bytes between elements of dimension i + 1, box[i] extents of one
-// copy; out-of-range elements read as zero.  Encoded anew on every call.
+// copy (inner extent of 32, 64 or 128 bytes, swizzled over as many); out-of-range
+// elements read as zero and are not written.  Encoded anew on every call.
 tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const int64_t *dims,
                      const int64_t *strides, const int *box);
 
