@@ -35,11 +35,11 @@
 // the epilogue reads 16x256b fragments, whose pairs stmatrix transposes into a
 // 2 KB tile per warp; D, preact and the residual move in 16-byte pieces.
 //
-// What bounds it.  Wide tiles: the tensor pipe, busy 73 - 80 % of the time
-// (8191 x 4096 x 4096 170 us, 1.62 PFLOP/s; 65528 rows over 64 groups, 2048 x
-// 2048, 341 us, 1.61), the rest being the first operands of each CTA, the last
-// wave and the shared-memory traffic of the epilogue.  Few rows a group: the
-// weights' bytes (488 rows over 64 groups, 252 MB, 46.7 us, 5.4 TB/s).
+// What bounds it.  Wide tiles: the operands' way into the SMs, 13 - 14.5 TB/s,
+// with the tensor pipe busy 73 - 81 % (8191 x 4096 x 4096 143 us, with bias, GELU,
+// residual and preact 164; 65528 rows over 64 groups, 2048 x 2048, 341 us, 1.61
+// PFLOP/s).  Few rows a group: the
+// weights' bytes (488 rows over 64 groups, 271 MB, 45.4 us, 5.9 TB/s).
 #pragma once
 
 #include "act.cuh"
