@@ -304,6 +304,25 @@ def test_grouped_few_rows_exact(tmg, sizes, N, K):
     exact(D2, want)
 
 
+@pytest.mark.parametrize("sizes", [[700, 330], [0, 1000, 3, 0]])
+@pytest.mark.parametrize("activation", ["none", "swiglu"])
+def test_grouped_cut_tiles(tmg, sizes, activation):
+    """A last wave of few tiles with a long contraction: cut over several CTA pairs."""
+    off, N, K = offsets_of(sizes), 5120, 4096
+    R = int(off[-1])
+    A, B = normal((R, K), 93), normal((len(sizes), N, K), 94, K ** -0.5)
+    dA, dB, dO = A.to(DEV), B.to(DEV), off.to(DEV)
+    outs = [tmg.grouped_gemm(dA, dB, dO, activation=activation) for _ in range(3)]
+    tmg.check()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    z, err = product(A, B, off)
+    if activation == "none":
+        close(outs[0], z, err)
+    else:
+        g, u, eg, eu = z[:, :N // 2], z[:, N // 2:], err[:, :N // 2], err[:, N // 2:]
+        close(outs[0], silu(g) * u, 1.1 * eg * u.abs() + silu(g).abs() * eu + eg * eu, (g * u).abs())
+
+
 def test_grouped_one_group_takes_all(tmg):
     """All rows in one of many groups: more row tiles than an even spread has."""
     sizes = [0] * 20 + [3000] + [0] * 11
@@ -414,6 +433,21 @@ def test_wgrad_split_contraction_exact(tmg, sizes):
     assert torch.equal(dB1, dB2)
 
 
+@pytest.mark.parametrize("sizes", [[3000], [5000, 3000], [4100, 0, 3900]])
+def test_wgrad_few_tiles_of_many_rows_exact(tmg, sizes):
+    """Tiles cut over several CTA pairs, in one group and across groups."""
+    off, N, K = offsets_of(sizes), 300, 520
+    R = int(off[-1])
+    d, A = ints((R, N), 91), ints((R, K), 92)
+    first = None
+    for _ in range(3):
+        dB = tmg.grouped_gemm_wgrad(d.to(DEV), A.to(DEV), off.to(DEV))
+        tmg.check()
+        first = dB if first is None else first
+        assert torch.equal(dB, first)
+    exact(first, torch.stack([d[r].to(W).T @ A[r].to(W) for _, r in groups(off)]))
+
+
 def test_wgrad_strides(tmg):
     off = offsets_of(SIZES["ragged"])
     R, N, K = int(off[-1]), 72, 80
@@ -521,6 +555,20 @@ def test_linear_few_rows_exact(tmg, M, N, K):
         D = tmg.linear(A.to(DEV), B.to(DEV), bias=bias.to(DEV), residual=res.to(DEV))
         tmg.check()
         exact(D, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 5120, 4096), (300, 10000, 4000), (2000, 2700, 4100)])
+def test_linear_cut_tiles_exact(tmg, M, N, K):
+    """A last wave of few tiles with a long contraction, with everything the epilogue takes."""
+    A, B, res = ints((M, K), 95), ints((N, K), 96), ints((M, N), 97)
+    bias = torch.randint(-8, 9, (N,), generator=gen(98)).float()
+    pre = torch.zeros((M, N), dtype=BF16, device=DEV)
+    z = (A.to(DEV).double() @ B.to(DEV).double().T).cpu() + bias.to(W)
+    for _ in range(2):
+        D = tmg.linear(A.to(DEV), B.to(DEV), bias=bias.to(DEV), activation="relu", residual=res.to(DEV), preact=pre)
+        tmg.check()
+        exact(pre, z)
+        exact(D, z.clamp(min=0) + res.to(W))
 
 
 @pytest.mark.parametrize("M,N,K", [(16, 1000, 2048), (150, 1000, 96), (900, 1000, 200), (2500, 1000, 64)])

@@ -38,8 +38,8 @@
 // What bounds it.  Wide tiles: the operands' way into the SMs, 13 - 14.5 TB/s,
 // with the tensor pipe busy 73 - 81 % (8191 x 4096 x 4096 143 us, with bias, GELU,
 // residual and preact 164; 65528 rows over 64 groups, 2048 x 2048, 341 us, 1.61
-// PFLOP/s).  Few rows a group: the
-// weights' bytes (488 rows over 64 groups, 271 MB, 45.4 us, 5.9 TB/s).
+// PFLOP/s).  Few rows a group: the weights' bytes (488 rows over 64 groups, 271 MB,
+// 45.4 us, 5.9 TB/s).
 #pragma once
 
 #include "act.cuh"
@@ -74,7 +74,7 @@ struct SwapArgs {
     int group;                 // row tiles per band
     float block_ns;            // a K block of a tile of maxw columns
     float *partials;           // sw_partial_floats(maxw) per pair; null: no tile is split
-    uint32_t *counters;        // 16 per tile of two waves
+    uint32_t *counters;        // 16 per cut tile
     uint32_t *feed;            // the tile counter
 };
 

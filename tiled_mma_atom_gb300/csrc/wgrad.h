@@ -19,7 +19,7 @@ struct WgradTmaArgs {
     int group;                 // column tiles of dD per band
     int stages;                // set by the launch
     float *partials;           // wgrad_partial_bytes(); null: no tile is cut
-    uint32_t *counters;        // 16 per tile of two waves
+    uint32_t *counters;        // 16 per cut tile
     uint32_t *feed;            // the tile counter
 };
 size_t wgrad_partial_bytes(int num_sms);
