@@ -308,7 +308,7 @@ tmg_status encode_2d(CUtensorMap *map, CUtensorMapDataType dt, int elem, const v
 }  // namespace
 
 tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const int64_t *dims,
-                     const int64_t *strides, const int *box)
+                     const int64_t *strides, const int *box, bool reread)
 {
     cuuint64_t d[5], st[5];
     cuuint32_t b[5], es[5];
@@ -323,8 +323,15 @@ tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const v
     const CUtensorMapSwizzle swizzle = inner == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
                                        : inner == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                      : CU_TENSOR_MAP_SWIZZLE_128B;
+    // Rows that begin inside a 32-byte sector take a fifth one for every 128
+    // bytes.  Where they are read from L2 over and over, 256-byte promotion costs
+    // more still (2489 x 5632 x 8184 163 us against 151; whole sectors, 8192: 125
+    // either way); where they come from HBM once, it pays (16 x 8192 x 8184 26.4
+    // us against 27.1).
+    const bool sectors = reinterpret_cast<uintptr_t>(base) % 32 == 0 && (rank < 2 || strides[0] % 32 == 0);
+    const CUtensorMapL2promotion promotion = sectors || !reread ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
     const CUresult r = g_encode(map, dt, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                swizzle, promotion,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(TMG_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled failed (%d) for a rank-%d operand", (int)r, rank);

@@ -308,24 +308,25 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
                    q.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "");
         return launched(launch_split(q, epi, a.e4m3, plan.cluster, plan.tiles, err_ctx(ds), s), "split product launch");
     }
+    const bool reread = p.maxw > kSwGatherW;
     if (swiglu) {
         const int64_t dims[5] = {K, 8, 2, Fp / 8, a.E}, strides[4] = {brow * elem, Fp * brow * elem, 8 * brow * elem, bexp * elem};
         const int box[5] = {kb, 8, 2, 8, 1};
-        st = encode_nd(&p.tmW, dt, 5, B, dims, strides, box);
+        st = encode_nd(&p.tmW, dt, 5, B, dims, strides, box, reread);
     } else if (maj) {
         const int64_t dims[3] = {a.N, K, a.E}, strides[2] = {brow * elem, bexp * elem};
         const int box[3] = {64, 64, 1};
-        st = encode_nd(&p.tmW, dt, 3, B, dims, strides, box);
+        st = encode_nd(&p.tmW, dt, 3, B, dims, strides, box, reread);
     } else {
         const int64_t dims[3] = {K, a.N, a.E}, strides[2] = {brow * elem, bexp * elem};
         const int box[3] = {kb, 128, 1};
-        st = encode_nd(&p.tmW, dt, 3, B, dims, strides, box);
+        st = encode_nd(&p.tmW, dt, 3, B, dims, strides, box, reread);
     }
     if (st != TMG_OK)
         return st;
     for (int i = 0; i < (p.gather ? 1 : 4); ++i) {
         const int box[2] = {kb, p.gather ? 1 : 16 << i};
-        if ((st = encode_nd(&p.tmX[i], dt, 2, A, xdims, xstrides, box)) != TMG_OK)
+        if ((st = encode_nd(&p.tmX[i], dt, 2, A, xdims, xstrides, box, reread)) != TMG_OK)
             return st;
     }
     p.D = a.D;
@@ -404,7 +405,7 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
         CUtensorMap *maps[3] = {i ? &p.tmA : &p.tmD, i ? &p.tmA16 : &p.tmD16, i ? &p.tmAg : &p.tmDg};
         for (int b = 0; b < 3; ++b) {
             const int box[2] = {64, b == 0 ? 64 : b == 1 ? 16 : 1};
-            if ((st = encode_nd(maps[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box)) != TMG_OK)
+            if ((st = encode_nd(maps[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, op[i], dims, strides, box, true)) != TMG_OK)
                 return st;
         }
     }

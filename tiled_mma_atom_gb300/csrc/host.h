@@ -33,9 +33,10 @@ void log_choice(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
 // A tiled tensor map of `rank` dimensions: dims[i] extents (innermost first),
 // strides[i] bytes between elements of dimension i + 1, box[i] extents of one
 // copy (inner extent of 32, 64 or 128 bytes, swizzled over as many); out-of-range
-// elements read as zero and are not written.  Encoded anew on every call.
+// elements read as zero and are not written.  reread: many tiles read each
+// element.  Encoded anew on every call.
 tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const int64_t *dims,
-                     const int64_t *strides, const int *box);
+                     const int64_t *strides, const int *box, bool reread = false);
 
 // Workspaces of the grouped products, the dense product with the residual
 // epilogue and the routing, per (device, stream), grown on demand; an outgrown
