@@ -759,11 +759,13 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
         // contractions (8191 x 4096 x 4096: dA 144 against 148; 1024 x 4096 x 4096:
         // dB 26 against 30), slower on long ones (2048 x 8192 x 8192: dA 164 against
         // 150; 6080 x 4520 x 3400: 151 against 144, dB 156 against 146; 8191 x 4096
-        // x 4096: dB 165 against 159).
+        // x 4096: dB 165 against 159) and where rows begin inside a sector (2833 x
+        // 6648 x 6800: dA 183 against 161, dB 169 against 161; 74 x 7016 x 6296: dB
+        // 36 against 29).
         auto fills = [&](int64_t rows, int64_t cols) { return (rows + 255) / 256 * ((cols + 255) / 256) >= ds->num_sms / 2; };
         const bool some = M > 0 && N > 0 && K > 0;
-        const bool a_product = some && (!fills(M, K) || N > 4096);
-        const bool b_wgrad = some && (!fills(N, K) || M < 64 || (M > 6000 && M >= N && M >= K));
+        const bool a_product = some && (!fills(M, K) || N > 4096 || (ldz | ldb) % 16);
+        const bool b_wgrad = some && (!fills(N, K) || M < 64 || (M > 6000 && M >= N && M >= K) || (ldz | lda) % 16);
         auto flat = [](int64_t r, int64_t c, int64_t sr, int64_t sc) {
             tmg_layout L;
             std::memset(&L, 0, sizeof L);
