@@ -445,7 +445,7 @@ tmg_status tmg_linear(const tmg_linear_args *args, void *stream);
  *               TMG_ACT_NONE);  A (M, K), B (N, K)  bf16, row strides lda, ldb.
  *   dA          bf16 (M, K) or NULL;  dB  bf16 (N, K) or NULL;
  *   dbias       fp32 (N) or NULL.  Contiguous.
- * Workspace: dz and the column sums of 128 rows each, per (device, stream). */
+ * Workspace: dz and the column sums of 32 or 128 rows each, per (device, stream). */
 tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
                                int64_t ldp, const void *A, int64_t lda,
                                const void *B, int64_t ldb, void *dA, void *dB,

@@ -15,21 +15,25 @@
 namespace tmg {
 namespace {
 
-constexpr int kRowsPerChunk = 128, kCols = 256;   // a block: 32 threads x 8 columns, 8 row lanes, 4 rows of each in flight
+constexpr int kCols = 256;    // a block: 32 threads x 8 columns, 8 row lanes, 4 rows of each in flight
+
+// Rows of a chunk: 128, or 32 where that leaves few blocks (gradient of 158 x 7544 x
+// 6088 with GELU 86.2 us with 128, 77.4 with 32).
+int chunk_rows(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + kCols - 1) / kCols) >= 512 ? 128 : 32; }
 
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256)
     act_grad_kernel(const __nv_bfloat16 *__restrict__ dD, int64_t ldd, const __nv_bfloat16 *__restrict__ Z, int64_t ldp,
-                    int64_t M, int64_t N, __nv_bfloat16 *__restrict__ dz, float *__restrict__ partials)
+                    int64_t M, int64_t N, int chunk, __nv_bfloat16 *__restrict__ dz, float *__restrict__ partials)
 {
     __shared__ float red[8][kCols];
     grid_release();
     grid_wait();
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + tx * 8;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRowsPerChunk;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * chunk;
     float sum[8] = {};
-    const int64_t m1 = min(M, m0 + kRowsPerChunk);
+    const int64_t m1 = min(M, m0 + chunk);
     if (VEC && c < N) {
         for (int64_t m = m0 + ty; m < m1; m += 32) {
             uint4 d[4], z[4];
@@ -119,15 +123,15 @@ cudaError_t launch_act(const void *dD, int64_t ldd, const void *Z, int64_t ldp, 
 {
     auto ok = [](const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; };
     const bool vec = N % 8 == 0 && ok(dD, ldd) && (ACT == kActNone || ok(Z, ldp)) && ok(dz, N);
-    const dim3 grid(static_cast<unsigned>(act_grad_chunks(M)), static_cast<unsigned>((N + kCols - 1) / kCols));
+    const dim3 grid(static_cast<unsigned>(act_grad_chunks(M, N)), static_cast<unsigned>((N + kCols - 1) / kCols));
     const __nv_bfloat16 *d = static_cast<const __nv_bfloat16 *>(dD), *z = static_cast<const __nv_bfloat16 *>(Z);
     return launch_overlapped(vec ? act_grad_kernel<ACT, true> : act_grad_kernel<ACT, false>, grid, 256, 0, 1, s, d, ldd, z, ldp, M,
-                             N, static_cast<__nv_bfloat16 *>(dz), partials);
+                             N, chunk_rows(M, N), static_cast<__nv_bfloat16 *>(dz), partials);
 }
 
 }  // namespace
 
-int act_grad_chunks(int64_t M) { return static_cast<int>((M + kRowsPerChunk - 1) / kRowsPerChunk); }
+int act_grad_chunks(int64_t M, int64_t N) { return static_cast<int>((M + chunk_rows(M, N) - 1) / chunk_rows(M, N)); }
 
 cudaError_t launch_act_grad(const void *dD, int64_t ldd, const void *preact, int64_t ldp, int act, int64_t M, int64_t N,
                             void *dz, float *partials, float *dbias, cudaStream_t s)
@@ -142,7 +146,7 @@ cudaError_t launch_act_grad(const void *dD, int64_t ldd, const void *preact, int
     if (e != cudaSuccess || !dbias)
         return e;
     return launch_overlapped(column_sum_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 256, 0, 1, s, partials,
-                             act_grad_chunks(M), N, dbias);
+                             act_grad_chunks(M, N), N, dbias);
 }
 
 }  // namespace tmg

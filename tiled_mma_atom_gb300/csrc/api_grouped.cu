@@ -732,7 +732,7 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
         const void *dz = dD;
         int64_t ldz = ldd;
         if (M > 0 && N > 0 && (act || dbias)) {
-            const size_t part = static_cast<size_t>(act_grad_chunks(M)) * N * sizeof(float);
+            const size_t part = static_cast<size_t>(act_grad_chunks(M, N)) * N * sizeof(float);
             const size_t grad = act ? static_cast<size_t>(M) * N * 2 : 0;
             char *ws = static_cast<char *>(workspace(kWsGrad, (part + 255) / 256 * 256 + grad, s, &st));
             if (!ws)

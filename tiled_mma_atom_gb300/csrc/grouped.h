@@ -99,9 +99,9 @@ cudaError_t launch_combine_backward(const CombineGradArgs &a, cudaStream_t s);
 
 // --------------------------------------- gradient of the dense product
 // dz = bf16(dD act'(preact)) (M, N) contiguous; column sums of the fp32 dz in
-// dbias through `partials` (act_grad_chunks(M) x N fp32).  act none: only the
+// dbias through `partials` (act_grad_chunks(M, N) x N fp32).  act none: only the
 // sums (dz null).  dbias null: only dz.
-int act_grad_chunks(int64_t M);
+int act_grad_chunks(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const void *dD, int64_t ldd, const void *preact, int64_t ldp, int act, int64_t M, int64_t N,
                             void *dz, float *partials, float *dbias, cudaStream_t s);
 
