@@ -1,0 +1,21 @@
+"""Source check (no GPU): kernels that start before their predecessor has ended
+(launch.cuh) read nothing through non-coherent loads, which are for data that
+nothing writes while the grid lives."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tiled_mma_atom_gb300", "csrc")
+
+
+def read(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def test_overlapped_kernels_use_plain_loads():
+    names = sorted(n for n in os.listdir(CSRC) if "grid_wait()" in read(n))
+    assert {"act_grad.cu", "pack3.cu", "route.cu", "split_kernel.cuh", "swap_kernel.cuh", "wgrad.cu"} <= set(names)
+    for name in names + ["feed.cuh", "pieces.cuh", "staging.cuh", "act.cuh"]:
+        text = read(name)
+        assert "__ldg" not in text and "ld.global.nc" not in text, name
+        assert not re.search(r"const\s+[\w:]+\s*\*\s*__restrict__", text), name

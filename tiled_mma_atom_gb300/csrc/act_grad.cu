@@ -23,8 +23,8 @@ int chunk_rows(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + kCols - 1)
 
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256)
-    act_grad_kernel(const __nv_bfloat16 *__restrict__ dD, int64_t ldd, const __nv_bfloat16 *__restrict__ Z, int64_t ldp,
-                    int64_t M, int64_t N, int chunk, __nv_bfloat16 *__restrict__ dz, float *__restrict__ partials)
+    act_grad_kernel(const __nv_bfloat16 *dD, int64_t ldd, const __nv_bfloat16 *Z, int64_t ldp, int64_t M, int64_t N, int chunk,
+                    __nv_bfloat16 *dz, float *partials)
 {
     __shared__ float red[8][kCols];
     grid_release();
@@ -66,16 +66,21 @@ __global__ void __launch_bounds__(256)
         }
     } else if (!VEC) {
         for (int64_t m = m0 + ty; m < m1; m += 8) {
+            float v[8], z[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (c + i < N) {
-                    float v = __bfloat162float(dD[m * ldd + c + i]);
-                    if constexpr (ACT != kActNone)
-                        v *= act_grad<ACT>(__bfloat162float(Z[m * ldp + c + i]));
-                    sum[i] += v;
-                    if (dz)
-                        dz[m * N + c + i] = __float2bfloat16_rn(v);
-                }
+            for (int i = 0; i < 8; ++i) {
+                v[i] = c + i < N ? __bfloat162float(dD[m * ldd + c + i]) : 0.f;
+                if constexpr (ACT != kActNone)
+                    z[i] = c + i < N ? __bfloat162float(Z[m * ldp + c + i]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (ACT != kActNone)
+                    v[i] *= act_grad<ACT>(z[i]);
+                sum[i] += v[i];
+                if (dz && c + i < N)
+                    dz[m * N + c + i] = __float2bfloat16_rn(v[i]);
+            }
         }
     }
     if (!partials)
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    column_sum_kernel(const float *__restrict__ partials, int chunks, int64_t N, float *__restrict__ out)
+    column_sum_kernel(const float *partials, int chunks, int64_t N, float *out)
 {
     __shared__ float red[8][32];
     grid_release();

@@ -7,7 +7,11 @@
 // its first read or write of global memory.  Every kernel of these calls also
 // lets its own successor start early, at its own start: the successor's blocks
 // take the SMs' free room and wait there.  A predecessor or successor that is
-// not launched so simply runs in stream order.  Measured on one call after
+// not launched so simply runs in stream order.
+//
+// What such a kernel reads may therefore still be written while its grid lives, so
+// it uses plain loads after the wait: no __ldg and no `const __restrict__` pointers
+// (non-coherent loads, for data that nothing writes during the grid's life).  Measured on one call after
 // another: a product of one tile 7.1 -> 5.8 us, 488 rows over 64 groups
 // 48.1 -> 46.9.
 #pragma once

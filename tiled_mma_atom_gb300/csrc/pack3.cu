@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(Pack3Args a, int elem, u
                 if (at + 16 <= bytes) {
 #pragma unroll
                     for (int j = 0; j < kWords; ++j)
-                        u[h].w[j] = __ldg(reinterpret_cast<const W *>(p) + j);
+                        u[h].w[j] = reinterpret_cast<const W *>(p)[j];
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -90,14 +90,14 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(Pack3Args a, int elem, u
 // and past the row's bytes.  A warp takes a row at a time, eight pieces per
 // lane in flight.
 __global__ void __launch_bounds__(256)
-    gather_rows_kernel(const char *__restrict__ src, int64_t stride, int64_t src_rows, int64_t bytes,
-                       const int32_t *__restrict__ numbers, int64_t rows, char *__restrict__ dst, int64_t dst_stride)
+    gather_rows_kernel(const char *src, int64_t stride, int64_t src_rows, int64_t bytes, const int32_t *numbers, int64_t rows,
+                       char *dst, int64_t dst_stride)
 {
     const int lane = threadIdx.x % 32, pieces = static_cast<int>(dst_stride / 16), whole = static_cast<int>(bytes / 16), tail = static_cast<int>(bytes % 16);
     grid_release();
     grid_wait();
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; r < rows; r += gridDim.x * 8ll) {
-        const int64_t from = __ldg(numbers + r);
+        const int64_t from = numbers[r];
         const bool there = from >= 0 && from < src_rows;
         const char *p = src + (there ? from : 0) * stride;
         uint4 *d = reinterpret_cast<uint4 *>(dst + r * dst_stride);
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int at = i + 32 * j;
-                v[j] = there && at < whole ? __ldg(reinterpret_cast<const uint4 *>(p) + at) : make_uint4(0, 0, 0, 0);
+                v[j] = there && at < whole ? reinterpret_cast<const uint4 *>(p)[at] : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(1024) route_plan_kernel(RouteArgs a, int token
     if (span <= kPlanPairs) {
         int32_t *here = wc + warps * E;
         for (int i = threadIdx.x; i < p1 - p0; i += blockDim.x)
-            here[i] = __ldg(pairs + i);
+            here[i] = pairs[i];
         pairs = here;
     }
     __syncthreads();
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(1024) route_plan_kernel(RouteArgs a, int token
         const int e = e0 + 4 * lane;
 #pragma unroll 10
         for (int b = warp; b < runs; b += warps) {
-            const uint2 n = e < E ? __ldg(reinterpret_cast<const uint2 *>(a.counts + static_cast<int64_t>(b) * row + e))
+            const uint2 n = e < E ? *reinterpret_cast<const uint2 *>(a.counts + static_cast<int64_t>(b) * row + e)
                                   : make_uint2(0, 0);
             const int in = b < first ? 1 : 0, v[4] = {static_cast<int>(n.x & 0xffffu), static_cast<int>(n.x >> 16),
                                                       static_cast<int>(n.y & 0xffffu), static_cast<int>(n.y >> 16)};
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(1024) route_plan_kernel(RouteArgs a, int token
 // with the softmax p over all, dlogit_e = p_e ([e selected] dw - sum_i p_i dw_i).
 template <int C>
 __global__ void __launch_bounds__(256)
-    route_backward_kernel(const void *__restrict__ logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
-                          const int32_t *__restrict__ experts, const float *__restrict__ dweights, void *__restrict__ out)
+    route_backward_kernel(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
+                          const int32_t *experts, const float *dweights, void *out)
 {
     const int lane = threadIdx.x % 32;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
@@ -493,9 +493,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a,
     uint4 y[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-        const int32_t at = j < a.k ? __ldg(a.slots + t * a.k + j) : -1;
+        const int32_t at = j < a.k ? a.slots[t * a.k + j] : -1;
         slot[j] = at < a.R ? at : -1;
-        w[j] = j < a.k && a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
+        w[j] = j < a.k && a.weights ? a.weights[t * a.k + j] : 1.f;
     }
     if (a.residual)
         load8<VEC>(static_cast<const __nv_bfloat16 *>(a.residual) + t * a.ldr, h, a.H, acc);
@@ -526,9 +526,9 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineGradArgs a
     float w[KMAX], dot[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-        const int32_t s = j < a.k ? __ldg(a.slots + t * a.k + j) : -1;
+        const int32_t s = j < a.k ? a.slots[t * a.k + j] : -1;
         slot[j] = s < a.R ? s : -1;
-        w[j] = j < a.k && a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
+        w[j] = j < a.k && a.weights ? a.weights[t * a.k + j] : 1.f;
         dot[j] = 0.f;
     }
     const __nv_bfloat16 *Y = static_cast<const __nv_bfloat16 *>(a.Y);

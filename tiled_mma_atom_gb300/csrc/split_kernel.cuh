@@ -135,23 +135,23 @@ template <int EPI>
 __device__ __forceinline__ void read_piece(const SplitArgs &p, PieceReads &rd, int64_t row, int col, int n, int e)
 {
     if (p.epi.scale_a) {
-        const int64_t src = p.rows ? __ldg(p.rows + row) : row;
-        rd.scale_a = src >= 0 && src < p.T ? __ldg(p.epi.scale_a + src) : 0.f;
+        const int64_t src = p.rows ? p.rows[row] : row;
+        rd.scale_a = src >= 0 && src < p.T ? p.epi.scale_a[src] : 0.f;
     }
     if (p.epi.scale_b) {
         const float *s = p.epi.scale_b + e * static_cast<int64_t>(EPI == kSwSwiglu ? 2 * p.N : p.N) + col;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            rd.scale_b[j] = j < n ? __ldg(s + j) : 0.f;
+            rd.scale_b[j] = j < n ? s[j] : 0.f;
             if constexpr (EPI == kSwSwiglu)
-                rd.scale_u[j] = j < n ? __ldg(s + p.N + j) : 0.f;
+                rd.scale_u[j] = j < n ? s[p.N + j] : 0.f;
         }
     }
     if constexpr (EPI == kSwDense) {
         if (p.epi.bias) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                rd.bias[j] = j < n ? __ldg(p.epi.bias + col + j) : 0.f;
+                rd.bias[j] = j < n ? p.epi.bias[col + j] : 0.f;
         }
         if (p.epi.residual)
             load_piece(static_cast<const __nv_bfloat16 *>(p.epi.residual) + row * p.epi.ld_residual + col, n, rd.a);
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         for (int e0 = 0; e0 < p.E && !work; e0 += 32) {
             int a = 0, b = 0;
             if (e0 + lane < p.E) {
-                a = min(max(__ldg(p.offsets + e0 + lane), 0), p.R);
-                b = min(max(__ldg(p.offsets + e0 + lane + 1), 0), p.R);
+                a = min(max(p.offsets[e0 + lane], 0), p.R);
+                b = min(max(p.offsets[e0 + lane + 1], 0), p.R);
             }
             int inc = (max(b - a, 0) + p.w - 1) / p.w * tiles_n;
 #pragma unroll
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
             for (int i = lane; i < wt; i += 32) {
                 int r = p.map_rows;                            // past the last row: zeros
                 if (i < rows) {
-                    r = __ldg(p.rows + row0 + i);
+                    r = p.rows[row0 + i];
                     r = r < 0 || r >= p.map_rows ? p.map_rows : r;
                 }
                 row_numbers[i] = r;

@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     if constexpr (EPI != kSwDense)
         grid_wait();
     for (int i = threadIdx.x; i <= p.E; i += kSwThreads)
-        off[i] = EPI != kSwDense ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
+        off[i] = EPI != kSwDense ? min(max(p.offsets[i], 0), p.R) : (i ? p.R : 0);
     __syncthreads();
     if (warp == 2) {                 // tiles before each group
         int run = 0;
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 __syncwarp();
                 int r = p.map_rows;             // past the last row: zeros
                 if (lane < half && static_cast<int>(rank) * half + lane < x.rows) {
-                    r = __ldg(p.rows + xrow + lane);
+                    r = p.rows[xrow + lane];
                     r = r < 0 || r >= p.map_rows ? p.map_rows : r;
                 }
                 row_numbers[lane] = r;
@@ -800,9 +800,9 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 const int64_t at = EPI == kSwSwiglu ? (i & 1) * static_cast<int64_t>(p.N) + n : n;
                 if (n < p.N) {
                     if (p.epi.scale_b)
-                        sb[i] = __ldg(p.epi.scale_b + x.e * static_cast<int64_t>(EPI == kSwSwiglu ? 2 * p.N : p.N) + at);
+                        sb[i] = p.epi.scale_b[x.e * static_cast<int64_t>(EPI == kSwSwiglu ? 2 * p.N : p.N) + at];
                     if (EPI == kSwDense && p.epi.bias)
-                        bias[i] = __ldg(p.epi.bias + n);
+                        bias[i] = p.epi.bias[n];
                 }
             }
             const int chunks = x.w / 32;
@@ -818,8 +818,8 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 const int64_t r = x.row0 + c * 32 + lane;
                 if (!p.epi.scale_a || c >= chunks || c * 32 + lane >= x.rows)
                     return 1.f;
-                const int src = p.rows ? __ldg(p.rows + r) : static_cast<int>(r);
-                return src >= 0 && src < p.T ? __ldg(p.epi.scale_a + src) : 0.f;
+                const int src = p.rows ? p.rows[r] : static_cast<int>(r);
+                return src >= 0 && src < p.T ? p.epi.scale_a[src] : 0.f;
             };
             float sa_next = EPI == kSwSwigluGrad ? 1.f : scale_of(half);
             if (!partial)

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     grid_release();
     grid_wait();
     for (int i = threadIdx.x; i <= p.E; i += kWgThreads)
-        off[i] = p.offsets ? min(max(__ldg(p.offsets + i), 0), p.R) : (i ? p.R : 0);
+        off[i] = p.offsets ? min(max(p.offsets[i], 0), p.R) : (i ? p.R : 0);
     __syncthreads();
     if (warp == 2) {                 // blocks before each group
         int run = 0;
