@@ -314,7 +314,10 @@ tmg_status tmg_gemm_skinny_noalloc(const void *A, const void *B, void *D,
  * on demand, so a call that needs more than the ones before must not come
  * inside a stream capture: make it once outside.  A captured graph stays valid
  * when later calls grow the workspace (the old one is kept until
- * tmg_shutdown). */
+ * tmg_shutdown).  Host threads may call on one stream at the same time: each
+ * call's kernels follow one another.  Graphs hold the workspace of the stream
+ * they were captured on, so two captured on one stream must not run at the same
+ * time, nor one of them beside other calls on that stream. */
 
 /* The activation of the grouped and the dense products. */
 typedef enum {

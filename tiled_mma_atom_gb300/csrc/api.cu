@@ -45,6 +45,7 @@ std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
 
 struct Scratch {
+    std::recursive_mutex calls;        // StreamLock
     float *partials = nullptr;
     size_t partials_bytes = 0;
     uint32_t *counters = nullptr;
@@ -67,6 +68,20 @@ struct Scratch {
 };
 std::map<std::pair<int, uintptr_t>, Scratch> g_scratch;
 std::vector<std::pair<int, void *>> g_retired;     // outgrown workspaces, by device
+
+// What is kept for a stream of a device (g_mu held).  NULL and cudaStreamLegacy
+// name one stream; cudaStreamPerThread names another one in every host thread,
+// told apart by its id (with the top bit, which no handle has).
+Scratch &scratch_of(int dev, cudaStream_t s)
+{
+    uintptr_t key = reinterpret_cast<uintptr_t>(s);
+    unsigned long long id = 0;
+    if (s == cudaStreamLegacy)
+        key = 0;
+    else if (s == cudaStreamPerThread && cudaStreamGetId(s, &id) == cudaSuccess)
+        key = static_cast<uintptr_t>(id) | uintptr_t{1} << 63;
+    return g_scratch[{dev, key}];
+}
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -338,12 +353,23 @@ tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const v
     return TMG_OK;
 }
 
+StreamLock::StreamLock(cudaStream_t s)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        mu_ = &scratch_of(dev, s).calls;
+    }
+    mu_->lock();
+}
+
 void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st)
 {
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    Scratch &sc = scratch_of(dev, s);
     cudaError_t e;
     if (sc.ws_bytes[which] < bytes) {
         // A grown buffer's old one stays until tmg_shutdown: a CUDA graph
@@ -418,7 +444,7 @@ TcPlan plan_tc(const void *A, const void *B, void *D, int64_t M, int64_t N, int6
 Scratch *skinny_scratch(int dev, cudaStream_t s, size_t pbytes, size_t cbytes, tmg_status *st)
 {
     std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    Scratch &sc = scratch_of(dev, s);
     cudaError_t e;
     if (sc.partials_bytes < pbytes) {
         if (sc.partials)
@@ -454,7 +480,7 @@ Scratch *skinny_scratch(int dev, cudaStream_t s, size_t pbytes, size_t cbytes, t
 uint8_t *mx_scale_scratch(int dev, cudaStream_t s, size_t bytes, tmg_status *st)
 {
     std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    Scratch &sc = scratch_of(dev, s);
     if (sc.mx_scales_bytes < bytes) {
         if (sc.mx_scales)
             cudaFree(sc.mx_scales);
@@ -482,7 +508,7 @@ tmg_status tc2_scratch(int dev, cudaStream_t s, TcArgs &a)
     if (pb == 0)
         return TMG_OK;
     std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    Scratch &sc = scratch_of(dev, s);
     cudaError_t e;
     if (sc.tc2_partials_bytes < pb) {
         if (sc.tc2_partials)
@@ -576,7 +602,7 @@ void *pack_scratch(int which, size_t bytes, cudaStream_t s, tmg_status *st)
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    Scratch &sc = scratch_of(dev, s);
     if (sc.pack_bytes[which] < bytes) {
         if (sc.pack[which])
             cudaFree(sc.pack[which]);
@@ -601,7 +627,7 @@ Scratch *host_scratch(cudaStream_t s, const size_t (&bytes)[3], tmg_status *st)
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = g_scratch[{dev, reinterpret_cast<uintptr_t>(s)}];
+    Scratch &sc = scratch_of(dev, s);
     cudaError_t e;
     if (!sc.copy_in) {
         if ((e = cudaStreamCreateWithFlags(&sc.copy_in, cudaStreamNonBlocking)) != cudaSuccess ||
@@ -890,6 +916,7 @@ tmg_status tmg_gemm_ex(const void *A, const void *B, void *D, int64_t M, int64_t
     if ((st = device_state(&ds)) != TMG_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     const int dt = dtype == TMG_F32 ? 0 : 1;
 
     if (K == 0) {
@@ -995,6 +1022,7 @@ tmg_status tmg_gemm_host(const void *A, const void *B, void *D, int64_t M, int64
         cudaGetLastError();
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     const size_t elem = dtype == TMG_F32 ? 4 : 2;
     const size_t bytes[3] = {static_cast<size_t>(M) * K * elem + 16, static_cast<size_t>(N) * K * elem + 16,
                              static_cast<size_t>(M) * N * elem};
@@ -1076,6 +1104,7 @@ tmg_status tmg_gemm_fused(const void *A, const void *B, void *D, int64_t M, int6
     if ((st = device_state(&ds)) != TMG_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     const Tc2Epi epi{scale_a, scale_b, bias, static_cast<int>(epilogue), 0};
     if (K == 0) {
         cudaError_t e = launch_fused_k0(D, M, N, epi, s);
@@ -1142,6 +1171,7 @@ tmg_status gemm_w4a8_impl(const void *A, const void *B, bool shuffled, void *D, 
     if ((st = device_state(&ds)) != TMG_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     cudaError_t e;
     if (K == 0) {
         e = cudaMemsetAsync(D, 0, static_cast<size_t>(M) * N * sizeof(int32_t), s);
@@ -1288,6 +1318,7 @@ tmg_status tmg_gemm_mxfp4(const void *A, const void *B, const void *scaleA, cons
     if ((st = device_state(&ds)) != TMG_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     if (K == 0) {
         cudaError_t e = launch_zero_fill(D, to_dev(row_major(M, N)), M, N, 1, s);
         return e == cudaSuccess ? TMG_OK : cuda_fail(e, "zero_fill launch");
@@ -1389,6 +1420,7 @@ tmg_status tmg_gemm_skinny_noalloc(const void *A, const void *B, void *D, int64_
         return fail(TMG_ERR_INVALID_ARG, "N=%lld exceeds the fixed-scratch skinny limit of %lld", (long long)N,
                     (long long)fs.max_tiles * 128);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const StreamLock lock(s);
     if (K == 0) {
         tmg_layout ld = row_major(M, N);
         ld.stride[0][0] = ldd;

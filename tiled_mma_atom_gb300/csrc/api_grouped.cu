@@ -466,6 +466,7 @@ tmg_status tmg_moe_route(const void *logits, int64_t T, int64_t E, int64_t k, in
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const StreamLock lock(s);
         if (T == 0)
             return launched(cudaMemsetAsync(offsets, 0, (E + 1) * sizeof(int32_t), s), "cudaMemsetAsync(offsets)");
         RouteArgs a{};
@@ -627,6 +628,7 @@ tmg_status tmg_grouped_gemm(const tmg_grouped_args *g, void *stream)
         DeviceState *ds = nullptr;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
+        const StreamLock lock(static_cast<cudaStream_t>(stream));
         return run_product(*ds, a, static_cast<cudaStream_t>(stream));
     });
 }
@@ -655,6 +657,7 @@ tmg_status tmg_grouped_gemm_wgrad(const void *dD, int64_t ldd, int64_t d_col, co
         tmg_status st;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
+        const StreamLock lock(static_cast<cudaStream_t>(stream));
         return run_wgrad(*ds, WgradArgs{dD, A, dB, R, T, N, K, E, ldd, d_col, lda, a_col, offsets, rows},
                          static_cast<cudaStream_t>(stream));
     });
@@ -700,6 +703,7 @@ tmg_status tmg_linear(const tmg_linear_args *g, void *stream)
         DeviceState *ds = nullptr;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
+        const StreamLock lock(static_cast<cudaStream_t>(stream));
         return run_product(*ds, a, static_cast<cudaStream_t>(stream));
     });
 }
@@ -729,6 +733,7 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const StreamLock lock(s);
         const void *dz = dD;
         int64_t ldz = ldd;
         if (M > 0 && N > 0 && (act || dbias)) {

@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "internal.h"
 #include "tmg.h"
 
@@ -52,5 +54,19 @@ enum Workspace {
     kWsCount
 };
 void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st);
+
+// Held by an entry point from its first workspace to its last launch: another host
+// thread's call on the same stream must not come between the kernel that fills a
+// workspace and the one that reads it.  Recursive: entry points call one another.
+class StreamLock {
+public:
+    explicit StreamLock(cudaStream_t s);
+    ~StreamLock() { mu_->unlock(); }
+    StreamLock(const StreamLock &) = delete;
+    StreamLock &operator=(const StreamLock &) = delete;
+
+private:
+    std::recursive_mutex *mu_;
+};
 
 }  // namespace tmg
