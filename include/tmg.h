@@ -313,8 +313,8 @@ tmg_status tmg_gemm_skinny_noalloc(const void *A, const void *B, void *D,
  * Workspace of these calls and of tmg_linear is per (device, stream) and grown
  * on demand, so a call that needs more than the ones before must not come
  * inside a stream capture: make it once outside.  A captured graph stays valid
- * when later calls grow the workspace (the old one is kept until
- * tmg_shutdown).  Host threads may call on one stream at the same time: each
+ * when later calls grow the workspace (what a capture has seen is kept until
+ * tmg_shutdown), calls of the other GEMM paths included.  Host threads may call on one stream at the same time: each
  * call's kernels follow one another.  Graphs hold the workspace of the stream
  * they were captured on, so two captured on one stream must not run at the same
  * time, nor one of them beside other calls on that stream. */
@@ -457,8 +457,8 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
 
 /* Synchronise `stream`, then report: TMG_ERR_CUDA for a sticky or pending
  * CUDA error, TMG_ERR_TIMEOUT if a kernel's bounded wait ran out since the
- * last check (the device error word is cleared and the skinny-path scratch
- * counters are reset), else TMG_OK. */
+ * last check (the device error word is cleared and the tile counters in the
+ * workspaces are reset), else TMG_OK. */
 tmg_status tmg_check(void *stream);
 
 /* Message for the calling thread's last non-OK status ("" if none).  The

@@ -22,6 +22,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <unordered_map>
 #include <mutex>
@@ -46,28 +47,26 @@ std::map<int, DeviceState> g_dev;
 
 struct Scratch {
     std::recursive_mutex calls;        // StreamLock
-    float *partials = nullptr;
-    size_t partials_bytes = 0;
-    uint32_t *counters = nullptr;
-    size_t counters_bytes = 0;
-    uint8_t *mx_scales = nullptr;      // MXFP4 scales in chunk order
-    size_t mx_scales_bytes = 0;
-    float *tc2_partials = nullptr;     // pair kernel stream-K partial tiles
-    size_t tc2_partials_bytes = 0;
-    uint32_t *tc2_counters = nullptr;  // pair kernel stream-K tile counters
-    size_t tc2_counters_bytes = 0;
-    void *pack[3] = {nullptr, nullptr, nullptr};   // packed A, packed B, dense D
-    size_t pack_bytes[3] = {0, 0, 0};
     void *host_ws[3] = {nullptr, nullptr, nullptr};  // tmg_gemm_host: device A, B, D
     size_t host_ws_bytes[3] = {0, 0, 0};
     void *ws[kWsCount] = {};           // workspace()
     size_t ws_bytes[kWsCount] = {};
+    bool ws_captured[kWsCount] = {};   // handed out while the stream was captured
     cudaStream_t copy_in = nullptr, copy_out = nullptr;
     static constexpr int kHostEvents = 2 + 3 * 16;
     cudaEvent_t ev[kHostEvents] = {};
 };
 std::map<std::pair<int, uintptr_t>, Scratch> g_scratch;
-std::vector<std::pair<int, void *>> g_retired;     // outgrown workspaces, by device
+struct Retired {                       // an outgrown workspace
+    int dev;
+    Workspace which;
+    void *p;
+    size_t bytes;
+};
+std::vector<Retired> g_retired;
+
+// Zero on allocation, and left at zero by the kernels.
+bool is_counters(Workspace w) { return w == kWsCounters || w == kWsTc2Counters || w == kWsSkinnyCounters; }
 
 // What is kept for a stream of a device (g_mu held).  NULL and cudaStreamLegacy
 // name one stream; cudaStreamPerThread names another one in every host thread,
@@ -357,46 +356,68 @@ StreamLock::StreamLock(cudaStream_t s)
 {
     int dev = 0;
     cudaGetDevice(&dev);
-    {
+    try {
         std::lock_guard<std::mutex> lk(g_mu);
         mu_ = &scratch_of(dev, s).calls;
+    } catch (...) {                    // no memory for the stream's entry: one lock for all
+        static std::recursive_mutex all;
+        mu_ = &all;
     }
     mu_->lock();
 }
 
 void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st)
-{
+try {
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lk(g_mu);
     Scratch &sc = scratch_of(dev, s);
     cudaError_t e;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+        cudaGetLastError();
+        capture = cudaStreamCaptureStatusActive;
+    }
     if (sc.ws_bytes[which] < bytes) {
-        // A grown buffer's old one stays until tmg_shutdown: a CUDA graph
-        // captured earlier on this stream may still name it.  Growing by half
-        // at least keeps what is kept below twice the largest.
+        // A CUDA graph captured earlier on this stream may name the old buffer: it
+        // then stays until tmg_shutdown.  Growing by half at least keeps what is
+        // kept below twice the largest.
+        if (sc.ws[which] && sc.ws_captured[which]) {
+            g_retired.push_back(Retired{dev, which, sc.ws[which], sc.ws_bytes[which]});
+        } else if (sc.ws[which]) {
+            cudaStreamSynchronize(s);
+            cudaFree(sc.ws[which]);
+        }
         const size_t half_more = sc.ws_bytes[which] + sc.ws_bytes[which] / 2;
-        const size_t size = bytes > half_more ? bytes : half_more;
+        size_t size = bytes > half_more ? bytes : half_more;
+        sc.ws[which] = nullptr;
+        sc.ws_bytes[which] = 0;
+        sc.ws_captured[which] = false;
         void *fresh = nullptr;
-        if (sc.ws[which])
-            g_retired.reserve(g_retired.size() + 1);
-        if ((e = cudaMalloc(&fresh, size)) != cudaSuccess) {
+        if ((e = cudaMalloc(&fresh, size)) == cudaErrorMemoryAllocation && size > bytes) {
+            cudaGetLastError();
+            e = cudaMalloc(&fresh, size = bytes);
+        }
+        if (e != cudaSuccess) {
             cudaGetLastError();       // not a launch error of a later call
             *st = cuda_fail(e, "cudaMalloc(workspace)");
             return nullptr;
         }
-        if (which == kWsCounters && (e = cudaMemsetAsync(fresh, 0, size, s)) != cudaSuccess) {
+        if (is_counters(which) && (e = cudaMemsetAsync(fresh, 0, size, s)) != cudaSuccess) {
             cudaFree(fresh);
             *st = cuda_fail(e, "cudaMemsetAsync(counters)");
             return nullptr;
         }
-        if (sc.ws[which])
-            g_retired.emplace_back(dev, sc.ws[which]);
         sc.ws[which] = fresh;
         sc.ws_bytes[which] = size;
     }
+    if (capture != cudaStreamCaptureStatusNone)
+        sc.ws_captured[which] = true;
     *st = TMG_OK;
     return sc.ws[which];
+} catch (const std::exception &x) {
+    *st = fail(TMG_ERR_CUDA, "host error: %s", x.what());
+    return nullptr;
 }
 
 namespace {
@@ -441,97 +462,19 @@ TcPlan plan_tc(const void *A, const void *B, void *D, int64_t M, int64_t N, int6
     return p;
 }
 
-Scratch *skinny_scratch(int dev, cudaStream_t s, size_t pbytes, size_t cbytes, tmg_status *st)
-{
-    std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = scratch_of(dev, s);
-    cudaError_t e;
-    if (sc.partials_bytes < pbytes) {
-        if (sc.partials)
-            cudaFree(sc.partials);
-        sc.partials = nullptr;
-        sc.partials_bytes = 0;
-        if ((e = cudaMalloc(&sc.partials, pbytes)) != cudaSuccess) {
-            *st = cuda_fail(e, "cudaMalloc(skinny partials)");
-            return nullptr;
-        }
-        sc.partials_bytes = pbytes;
-    }
-    if (sc.counters_bytes < cbytes) {
-        if (sc.counters)
-            cudaFree(sc.counters);
-        sc.counters = nullptr;
-        sc.counters_bytes = 0;
-        if ((e = cudaMalloc(&sc.counters, cbytes)) != cudaSuccess) {
-            *st = cuda_fail(e, "cudaMalloc(skinny counters)");
-            return nullptr;
-        }
-        if ((e = cudaMemsetAsync(sc.counters, 0, cbytes, s)) != cudaSuccess) {
-            *st = cuda_fail(e, "cudaMemsetAsync(skinny counters)");
-            return nullptr;
-        }
-        sc.counters_bytes = cbytes;
-    }
-    *st = TMG_OK;
-    return &sc;
-}
-
-// Per-(device, stream) buffer for the MXFP4 scale relayout, grown on demand.
-uint8_t *mx_scale_scratch(int dev, cudaStream_t s, size_t bytes, tmg_status *st)
-{
-    std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = scratch_of(dev, s);
-    if (sc.mx_scales_bytes < bytes) {
-        if (sc.mx_scales)
-            cudaFree(sc.mx_scales);
-        sc.mx_scales = nullptr;
-        sc.mx_scales_bytes = 0;
-        cudaError_t e = cudaMalloc(&sc.mx_scales, bytes);
-        if (e != cudaSuccess) {
-            *st = cuda_fail(e, "cudaMalloc(MXFP4 scale relayout)");
-            return nullptr;
-        }
-        sc.mx_scales_bytes = bytes;
-    }
-    *st = TMG_OK;
-    return sc.mx_scales;
-}
-
 // mode: 0 = choose, 1 = one-CTA tiles, 2 = CTA-pair tiles.
-// Per-(device, stream) stream-K scratch of the pair kernel, grown on demand;
-// counters are zeroed when allocated and reset by the kernel after use.
-tmg_status tc2_scratch(int dev, cudaStream_t s, TcArgs &a)
+// Stream-K scratch of the pair kernel; the kernel leaves the counters at zero.
+tmg_status tc2_scratch(cudaStream_t s, TcArgs &a)
 {
     const size_t pb = tc2_partials_bytes(a), cb = tc2_counters_bytes(a);
     a.partials = nullptr;
     a.counters = nullptr;
     if (pb == 0)
         return TMG_OK;
-    std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = scratch_of(dev, s);
-    cudaError_t e;
-    if (sc.tc2_partials_bytes < pb) {
-        if (sc.tc2_partials)
-            cudaFree(sc.tc2_partials);
-        sc.tc2_partials = nullptr;
-        sc.tc2_partials_bytes = 0;
-        if ((e = cudaMalloc(&sc.tc2_partials, pb)) != cudaSuccess)
-            return cuda_fail(e, "cudaMalloc(pair stream-K partials)");
-        sc.tc2_partials_bytes = pb;
-    }
-    if (sc.tc2_counters_bytes < cb) {
-        if (sc.tc2_counters)
-            cudaFree(sc.tc2_counters);
-        sc.tc2_counters = nullptr;
-        sc.tc2_counters_bytes = 0;
-        if ((e = cudaMalloc(&sc.tc2_counters, cb)) != cudaSuccess)
-            return cuda_fail(e, "cudaMalloc(pair stream-K counters)");
-        if ((e = cudaMemsetAsync(sc.tc2_counters, 0, cb, s)) != cudaSuccess)
-            return cuda_fail(e, "cudaMemsetAsync(pair stream-K counters)");
-        sc.tc2_counters_bytes = cb;
-    }
-    a.partials = sc.tc2_partials;
-    a.counters = sc.tc2_counters;
+    tmg_status st;
+    if (!(a.partials = static_cast<float *>(workspace(kWsTc2Partials, pb, s, &st))) ||
+        !(a.counters = static_cast<uint32_t *>(workspace(kWsTc2Counters, cb, s, &st))))
+        return st;
     return TMG_OK;
 }
 
@@ -581,9 +524,7 @@ tmg_status run_tc(const DeviceState &ds, const TcPlan &p, void *D, int64_t K, in
     a.K = static_cast<int>(K);
     if (pair) {
         tc2_plan(a, ds.num_sms);
-        int dev = 0;
-        cudaGetDevice(&dev);
-        if ((st = tc2_scratch(dev, s, a)) != TMG_OK)
+        if ((st = tc2_scratch(s, a)) != TMG_OK)
             return st;
     }
     if (pair)
@@ -595,28 +536,10 @@ tmg_status run_tc(const DeviceState &ds, const TcPlan &p, void *D, int64_t K, in
     return e == cudaSuccess ? TMG_OK : cuda_fail(e, pair ? "tc2_bf16 launch" : "tc_bf16 launch");
 }
 
-// Per-(device, stream) buffer `which` (0: packed A, 1: packed B, 2: dense D)
-// of the general-layout path, grown on demand.
+// Buffer `which` (0: packed A, 1: packed B, 2: dense D) of the general-layout path.
 void *pack_scratch(int which, size_t bytes, cudaStream_t s, tmg_status *st)
 {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    std::lock_guard<std::mutex> lk(g_mu);
-    Scratch &sc = scratch_of(dev, s);
-    if (sc.pack_bytes[which] < bytes) {
-        if (sc.pack[which])
-            cudaFree(sc.pack[which]);
-        sc.pack[which] = nullptr;
-        sc.pack_bytes[which] = 0;
-        cudaError_t e = cudaMalloc(&sc.pack[which], bytes);
-        if (e != cudaSuccess) {
-            *st = cuda_fail(e, "cudaMalloc(general-layout workspace)");
-            return nullptr;
-        }
-        sc.pack_bytes[which] = bytes;
-    }
-    *st = TMG_OK;
-    return sc.pack[which];
+    return workspace(static_cast<Workspace>(kWsLayoutA + which), bytes, s, st);
 }
 
 tmg_status run_skinny(const DeviceState &ds, const TcPlan &p, void *D, int64_t K, cudaStream_t s);
@@ -714,9 +637,7 @@ bool run_tc2_inplace(const DeviceState &ds, const void *A, const void *B, void *
     a.N = static_cast<int>(N);
     a.K = static_cast<int>(K);
     tc2_plan(a, ds.num_sms);
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if ((*st = tc2_scratch(dev, s, a)) != TMG_OK)
+    if ((*st = tc2_scratch(s, a)) != TMG_OK)
         return true;
     log_choice("bf16 %dx%dx%d -> tc2_gemm_kernel (CTA pairs), MN-major operands read in place (A %s, B %s): "
                "256x%d tiles, %d pairs, %d data-parallel + %d stream-K tiles, groups of %d M-tiles", a.M, a.N, a.K,
@@ -790,13 +711,12 @@ tmg_status run_skinny(const DeviceState &ds, const TcPlan &p, void *D, int64_t K
         return st;
     const int64_t units = ((p.N + 127) / 128) * ((K + 63) / 64);
     a.grid = static_cast<int>(units < ds.num_sms ? units : ds.num_sms);
-    int dev = 0;
-    cudaGetDevice(&dev);
-    Scratch *sc = skinny_scratch(dev, s, skinny_partials_bytes(a.grid, a.mp), skinny_counters_bytes(p.N), &st);
-    if (!sc)
+    a.partials = static_cast<float *>(workspace(kWsSkinnyPartials, skinny_partials_bytes(a.grid, a.mp), s, &st));
+    if (!a.partials)
         return st;
-    a.partials = sc->partials;
-    a.counters = sc->counters;
+    a.counters = static_cast<uint32_t *>(workspace(kWsSkinnyCounters, skinny_counters_bytes(p.N), s, &st));
+    if (!a.counters)
+        return st;
     a.D = D;
     a.ldd = p.ldd;
     a.M = static_cast<int>(p.M);
@@ -1131,9 +1051,7 @@ tmg_status tmg_gemm_fused(const void *A, const void *B, void *D, int64_t M, int6
     a.N = static_cast<int>(N);
     a.K = static_cast<int>(K);
     tc2_plan(a, ds->num_sms);
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if ((st = tc2_scratch(dev, s, a)) != TMG_OK)
+    if ((st = tc2_scratch(s, a)) != TMG_OK)
         return st;
     log_choice("%s %dx%dx%d fused (epilogue %d, scale_a %s, scale_b %s) -> tc2_gemm_kernel (CTA pairs): 256x%d tiles, "
                "%d pairs, %d data-parallel + %d stream-K tiles, groups of %d M-tiles", e4m3 ? "e4m3" : "bf16", a.M, a.N,
@@ -1226,8 +1144,6 @@ tmg_status gemm_w4a8_impl(const void *A, const void *B, bool shuffled, void *D, 
     // (integers up to 2^24 are); the first segment stores its int32 result,
     // the others add to it.
     constexpr int64_t kSeg = 8192;
-    int dev = 0;
-    cudaGetDevice(&dev);
     for (int64_t k0 = 0; k0 < K; k0 += kSeg) {
         const int64_t kc = K - k0 < kSeg ? K - k0 : kSeg;
         TcArgs a;
@@ -1245,7 +1161,7 @@ tmg_status gemm_w4a8_impl(const void *A, const void *B, bool shuffled, void *D, 
         a.N = static_cast<int>(N);
         a.K = static_cast<int>(kc);
         tc2_plan(a, ds->num_sms);
-        if ((st = tc2_scratch(dev, s, a)) != TMG_OK)
+        if ((st = tc2_scratch(s, a)) != TMG_OK)
             return st;
         const Tc2Epi epi{nullptr, nullptr, nullptr, kEpiNone, k0 == 0 ? 1 : 2};
         log_choice("w4a8 %dx%dx%d, K segment at %lld -> tc2_gemm_kernel on the unpacked bf16 copies: 256x%d tiles, "
@@ -1357,12 +1273,10 @@ tmg_status tmg_gemm_mxfp4(const void *A, const void *B, const void *scaleA, cons
     a.sA = static_cast<const uint8_t *>(scaleA);
     a.sB = static_cast<const uint8_t *>(scaleB);
     {
-        int dev = 0;
-        cudaGetDevice(&dev);
         const bool wide = pair && mxfp4_pair_wide_scales();
         const size_t ra = mxfp4_relaid_scale_bytes(M, K, 128, wide);
         const size_t rb = mxfp4_relaid_scale_bytes(N, K, pair ? a.bn : 128, wide);
-        uint8_t *buf = mx_scale_scratch(dev, s, ra + rb, &st);
+        uint8_t *buf = static_cast<uint8_t *>(workspace(kWsMxScales, ra + rb, s, &st));
         if (!buf)
             return st;
         a.relA = buf;
@@ -1487,13 +1401,13 @@ tmg_status tmg_check(void *stream)
             for (auto &kv : g_scratch) {
                 if (kv.first.first != dev)
                     continue;
-                if (kv.second.counters)
-                    cudaMemset(kv.second.counters, 0, kv.second.counters_bytes);
-                if (kv.second.tc2_counters)
-                    cudaMemset(kv.second.tc2_counters, 0, kv.second.tc2_counters_bytes);
-                if (kv.second.ws[kWsCounters])
-                    cudaMemset(kv.second.ws[kWsCounters], 0, kv.second.ws_bytes[kWsCounters]);
+                for (int i = 0; i < kWsCount; ++i)
+                    if (is_counters(static_cast<Workspace>(i)) && kv.second.ws[i])
+                        cudaMemset(kv.second.ws[i], 0, kv.second.ws_bytes[i]);
             }
+            for (const Retired &r : g_retired)
+                if (r.dev == dev && is_counters(r.which))
+                    cudaMemset(r.p, 0, r.bytes);
         }
         cudaDeviceSynchronize();
         if (bounds)
@@ -1559,19 +1473,6 @@ void tmg_shutdown(void)
     cudaGetDevice(&cur);
     for (auto &kv : g_scratch) {
         cudaSetDevice(kv.first.first);
-        if (kv.second.partials)
-            cudaFree(kv.second.partials);
-        if (kv.second.counters)
-            cudaFree(kv.second.counters);
-        if (kv.second.mx_scales)
-            cudaFree(kv.second.mx_scales);
-        if (kv.second.tc2_partials)
-            cudaFree(kv.second.tc2_partials);
-        if (kv.second.tc2_counters)
-            cudaFree(kv.second.tc2_counters);
-        for (void *q : kv.second.pack)
-            if (q)
-                cudaFree(q);
         for (void *q : kv.second.host_ws)
             if (q)
                 cudaFree(q);
@@ -1588,9 +1489,9 @@ void tmg_shutdown(void)
         }
     }
     g_scratch.clear();
-    for (auto &r : g_retired) {
-        cudaSetDevice(r.first);
-        cudaFree(r.second);
+    for (const Retired &r : g_retired) {
+        cudaSetDevice(r.dev);
+        cudaFree(r.p);
     }
     g_retired.clear();
     cudaSetDevice(cur);

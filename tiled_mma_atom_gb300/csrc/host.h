@@ -40,10 +40,10 @@ void log_choice(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
 tmg_status encode_nd(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const int64_t *dims,
                      const int64_t *strides, const int *box, bool reread = false);
 
-// Workspaces of the grouped products, the dense product with the residual
-// epilogue and the routing, per (device, stream), grown on demand; an outgrown
-// one is kept until tmg_shutdown.
+// Workspaces per (device, stream), grown on demand; an outgrown one that a captured
+// graph may name is kept until tmg_shutdown.
 enum Workspace {
+    // the grouped products, the dense product with the residual epilogue, routing
     kWsPackA,          // operand copies with 16-byte rows
     kWsPackB,
     kWsGather,         // rows gathered by number
@@ -51,6 +51,15 @@ enum Workspace {
     kWsCounters,       // arrival counters: zero on entry, zero again on exit
     kWsRoute,          // per-block expert counts of the routing plan
     kWsGrad,           // dz of the dense product's gradient and its column partials
+    // the other GEMM paths, which the dense product's gradient takes too
+    kWsTc2Partials,    // pair kernel: stream-K partial tiles and tile counters
+    kWsTc2Counters,
+    kWsSkinnyPartials, // skinny kernel: the same
+    kWsSkinnyCounters,
+    kWsLayoutA,        // general layouts: packed A, packed B, dense D
+    kWsLayoutB,
+    kWsLayoutD,
+    kWsMxScales,       // MXFP4 scales in chunk order
     kWsCount
 };
 void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st);
