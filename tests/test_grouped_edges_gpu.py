@@ -1,0 +1,43 @@
+"""Edges of the grouped and dense products and their gradients: empty operands,
+NaN and infinities through the activations, extents near the limits.  Inputs
+are integers or powers of two, so results are exact."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def tmg():
+    import __graft_entry__
+    __graft_entry__.build()
+    import tiled_mma_atom_gb300 as t
+    yield t
+    t.check()
+
+
+def ints(shape, seed):
+    return torch.randint(-2, 3, shape, generator=torch.Generator().manual_seed(seed)).float().to(BF16)
+
+
+def test_wgrad_without_rows_is_zero_whatever_the_workspace_holds(tmg):
+    """R = 0 with row numbers given (an empty torch tensor has no address, so
+    through the C ABI), after a call that gathered NaN."""
+    from tiled_mma_atom_gb300 import _native
+    N, K, E, T = 40, 64, 3, 50
+    A, rows = torch.full((T, K), math.nan, dtype=BF16, device=DEV), torch.zeros(100, dtype=torch.int32, device=DEV)
+    tmg.grouped_gemm_wgrad(torch.zeros(100, N, dtype=BF16, device=DEV), A,
+                           torch.tensor([0, 30, 60, 100], dtype=torch.int32, device=DEV), rows=rows)
+    dB = torch.full((E, N, K), 7.0, dtype=BF16, device=DEV)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    d = torch.zeros(8, N, dtype=BF16, device=DEV)
+    st = _native.lib().tmg_grouped_gemm_wgrad(d.data_ptr(), N, 1, A.data_ptr(), K, 1, dB.data_ptr(), off.data_ptr(),
+                                              rows.data_ptr(), 0, N, K, E, T, torch.cuda.current_stream().cuda_stream)
+    assert st == _native.OK
+    tmg.check()
+    assert (dB == 0).all()

@@ -112,7 +112,7 @@ tmg_status gather(const DeviceState &ds, const void **A, int64_t *lda, int64_t s
 {
     const int64_t ld = up(K, 16 / elem);
     tmg_status st;
-    void *ws = workspace(kWsGather, static_cast<size_t>(R > 0 ? R : 1) * ld * elem, s, &st);
+    void *ws = workspace(kWsGather, static_cast<size_t>(R) * ld * elem, s, &st);
     if (!ws)
         return st;
     const cudaError_t e = launch_gather_rows(*A, *lda * elem, src_rows, K * elem, numbers, R, ws, ld * elem, ds.num_sms, s);
@@ -378,6 +378,7 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     return launched(launch_swap(p, epi, a.e4m3, ds.num_sms, err_ctx(ds), s), "grouped product launch");
 }
 
+// a.R > 0.
 tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
 {
     tmg_status st;
@@ -399,7 +400,7 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
         if (i && a.rows) {
             if ((st = gather(ds, &op[i], &ld, n, cols[i], 2, a.rows, a.R, s)) != TMG_OK)
                 return st;
-            n = a.R > 0 ? a.R : 1;
+            n = a.R;
         }
         const int64_t dims[2] = {cols[i], n}, strides[1] = {ld * 2};
         CUtensorMap *maps[3] = {i ? &p.tmA : &p.tmD, i ? &p.tmA16 : &p.tmD16, i ? &p.tmAg : &p.tmDg};
@@ -657,9 +658,11 @@ tmg_status tmg_grouped_gemm_wgrad(const void *dD, int64_t ldd, int64_t d_col, co
         tmg_status st;
         if ((st = device_state(&ds)) != TMG_OK)
             return st;
-        const StreamLock lock(static_cast<cudaStream_t>(stream));
-        return run_wgrad(*ds, WgradArgs{dD, A, dB, R, T, N, K, E, ldd, d_col, lda, a_col, offsets, rows},
-                         static_cast<cudaStream_t>(stream));
+        const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const StreamLock lock(s);
+        if (R == 0)                    // the kernel's operand maps have a row at least
+            return launched(cudaMemsetAsync(dB, 0, static_cast<size_t>(E) * N * K * 2, s), "cudaMemsetAsync(dB)");
+        return run_wgrad(*ds, WgradArgs{dD, A, dB, R, T, N, K, E, ldd, d_col, lda, a_col, offsets, rows}, s);
     });
 }
 
