@@ -422,7 +422,9 @@ tmg_status tmg_grouped_gemm_wgrad(const void *dD, int64_t ldd, int64_t d_col,
 
 /* Dense product with the whole epilogue, fp32 until the one rounding:
  *   z = (A . B^T) * scale_a[m] * scale_b[n] + bias[n];  preact = bf16(z);
- *   D = bf16(act(z) + residual). */
+ *   D = bf16(act(z) + residual).
+ * NaN in z is NaN in D under every activation (RELU too, where tmg_gemm_fused's
+ * gives 0); the gradient of RELU is 0 where z is NaN. */
 typedef struct {
     const void *A;          /* device, (M, K) of in_dtype */
     const void *B;          /* device, (N, K) of in_dtype */

@@ -41,3 +41,19 @@ def test_wgrad_without_rows_is_zero_whatever_the_workspace_holds(tmg):
     assert st == _native.OK
     tmg.check()
     assert (dB == 0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 264, 64), (900, 1000, 200), (5, 24, 0)])
+def test_linear_relu_keeps_nan(tmg, M, N, K):
+    """relu(NaN) is NaN, of -inf 0, of +inf +inf, in every kernel of the product."""
+    A, B, bias = ints((M, K), 1), ints((N, K), 2), torch.zeros(N)
+    bias[5], bias[6], bias[7] = math.nan, math.inf, -math.inf
+    pre = torch.empty(M, N, dtype=BF16, device=DEV)
+    D = tmg.linear(A.to(DEV), B.to(DEV), bias=bias.to(DEV), activation="relu", preact=pre)
+    tmg.check()
+    z = A.double() @ B.double().T + bias.double()
+    want = torch.relu(z).to(BF16)
+    assert torch.isnan(want[:, 5]).all()
+    for got, ref in ((pre, z.to(BF16)), (D, want)):
+        assert torch.equal(torch.isnan(got.cpu()), torch.isnan(ref))
+        assert torch.equal(got.cpu().nan_to_num(1.0), ref.nan_to_num(1.0))

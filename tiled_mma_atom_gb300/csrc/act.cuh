@@ -56,7 +56,7 @@ template <int ACT>
 __device__ __forceinline__ float act_f(float z)
 {
     if constexpr (ACT == kActRelu)
-        return fmaxf(z, 0.f);
+        return z <= 0.f ? 0.f : z;          // NaN stays NaN, as fmaxf would not have it
     if constexpr (ACT == kActSilu)
         return silu_f(z);
     if constexpr (ACT == kActGelu) {
