@@ -57,3 +57,20 @@ def test_linear_relu_keeps_nan(tmg, M, N, K):
     for got, ref in ((pre, z.to(BF16)), (D, want)):
         assert torch.equal(torch.isnan(got.cpu()), torch.isnan(ref))
         assert torch.equal(got.cpu().nan_to_num(1.0), ref.nan_to_num(1.0))
+
+
+def test_linear_backward_of_very_wide_outputs(tmg):
+    """More column blocks of dz than a grid has in its second dimension."""
+    M, N, K = 3, 256 * 65535 + 8, 8
+    A, B, pre = ints((M, K), 3).to(DEV), torch.zeros(N, K, dtype=BF16, device=DEV), torch.zeros(M, N, dtype=BF16, device=DEV)
+    dD = torch.zeros(M, N, dtype=BF16, device=DEV)
+    at = torch.tensor([0, 1000, 256 * 65535 - 1, 256 * 65535, N - 1], device=DEV)
+    dD[:, at], pre[:, at], B[at] = ints((M, 5), 4).to(DEV), 1.0, ints((5, K), 5).to(DEV)
+    pre[1, at[2]] = -1.0
+    dA, dB, db = tmg.linear_backward(dD, A, B, preact=pre, activation="relu")
+    tmg.check()
+    dz = dD[:, at].double() * (pre[:, at] > 0)
+    assert torch.equal(dA, (dz @ B[at].double()).to(BF16))
+    assert torch.equal(dB[at], (dz.T @ A.double()).to(BF16)) and torch.equal(db[at].double(), dz.sum(0))
+    dB[at], db[at] = 0, 0
+    assert not dB.any() and not db.any()

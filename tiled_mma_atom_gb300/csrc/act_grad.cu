@@ -24,14 +24,14 @@ int chunk_rows(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + kCols - 1)
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256)
     act_grad_kernel(const __nv_bfloat16 *dD, int64_t ldd, const __nv_bfloat16 *Z, int64_t ldp, int64_t M, int64_t N, int chunk,
-                    __nv_bfloat16 *dz, float *partials)
+                    int chunks, __nv_bfloat16 *dz, float *partials)
 {
     __shared__ float red[8][kCols];
     grid_release();
     grid_wait();
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-    const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + tx * 8;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * chunk;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x / chunks) * kCols, c = n0 + tx * 8;
+    const int64_t row = blockIdx.x % chunks, m0 = row * chunk;
     float sum[8] = {};
     const int64_t m1 = min(M, m0 + chunk);
     if (VEC && c < N) {
@@ -89,13 +89,13 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < 8; ++i)
         red[ty][tx * 8 + i] = sum[i];
     __syncthreads();
-    const int64_t n = static_cast<int64_t>(blockIdx.y) * kCols + threadIdx.x;
+    const int64_t n = n0 + threadIdx.x;
     if (n < N) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w)
             v += red[w][threadIdx.x];
-        partials[static_cast<int64_t>(blockIdx.x) * N + n] = v;
+        partials[row * N + n] = v;
     }
 }
 
@@ -128,10 +128,12 @@ cudaError_t launch_act(const void *dD, int64_t ldd, const void *Z, int64_t ldp, 
 {
     auto ok = [](const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; };
     const bool vec = N % 8 == 0 && ok(dD, ldd) && (ACT == kActNone || ok(Z, ldp)) && ok(dz, N);
-    const dim3 grid(static_cast<unsigned>(act_grad_chunks(M, N)), static_cast<unsigned>((N + kCols - 1) / kCols));
+    // one dimension: wide results have more column blocks than a grid's second may
+    const int chunks = act_grad_chunks(M, N);
+    const dim3 grid(static_cast<unsigned>(chunks * ((N + kCols - 1) / kCols)));
     const __nv_bfloat16 *d = static_cast<const __nv_bfloat16 *>(dD), *z = static_cast<const __nv_bfloat16 *>(Z);
     return launch_overlapped(vec ? act_grad_kernel<ACT, true> : act_grad_kernel<ACT, false>, grid, 256, 0, 1, s, d, ldd, z, ldp, M,
-                             N, chunk_rows(M, N), static_cast<__nv_bfloat16 *>(dz), partials);
+                             N, chunk_rows(M, N), chunks, static_cast<__nv_bfloat16 *>(dz), partials);
 }
 
 }  // namespace

@@ -53,7 +53,8 @@ cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, int threads, size_t
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     note_launch();
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const cudaError_t last = cudaGetLastError();      // cleared: not an error of the next launch
+    return e != cudaSuccess ? e : last;
 }
 
 }  // namespace tmg
