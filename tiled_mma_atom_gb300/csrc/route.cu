@@ -196,12 +196,13 @@ __device__ __forceinline__ void rank_pairs(const RouteArgs &a, int p0, int p1, c
 {
     const int E = a.E, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const unsigned k = a.k;
-    // each warp's pairs are contiguous: [w0, w1)
-    const int each = ((p1 - p0 + 31) / 32 + warps - 1) / warps * 32;
-    const int w0 = min(p1, p0 + warp * each), w1 = min(p1, w0 + each);
+    // each warp's pairs are contiguous: p0 + [w0, w1), with room for what lies past
+    // the last pair (p0 itself may be near 2^31)
+    const int here = p1 - p0, each = ((here + 31) / 32 + warps - 1) / warps * 32;
+    const int w0 = min(here, warp * each), w1 = min(here, w0 + each);
     int32_t *mine = wc + warp * E;
     for (int p = w0; p < w1; p += 32) {
-        const int e = p + lane < w1 ? pairs[p + lane - p0] : -1;
+        const int e = p + lane < w1 ? pairs[p + lane] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         if (e >= 0 && lane == __ffs(same) - 1)
             mine[e] += __popc(same);
@@ -226,7 +227,7 @@ __device__ __forceinline__ void rank_pairs(const RouteArgs &a, int p0, int p1, c
     __syncthreads();
     for (int p = w0; p < w1; p += 32) {
         const int i = p + lane;
-        const int e = i < w1 ? pairs[i - p0] : -1;
+        const int e = i < w1 ? pairs[i] : -1;
         const uint32_t same = __match_any_sync(kFull, e);
         const int first = e >= 0 ? mine[e] : 0;
         __syncwarp();
@@ -234,10 +235,10 @@ __device__ __forceinline__ void rank_pairs(const RouteArgs &a, int p0, int p1, c
             const int slot = first + __popc(same & ((1u << lane) - 1));
             if (lane == __ffs(same) - 1)
                 mine[e] = first + __popc(same);
-            a.slots[i] = slot;
-            a.rows[slot] = static_cast<int>(static_cast<unsigned>(i) / k);
+            a.slots[p0 + i] = slot;
+            a.rows[slot] = static_cast<int>(static_cast<unsigned>(p0 + i) / k);
         } else if (i < w1) {
-            a.slots[i] = -1;
+            a.slots[p0 + i] = -1;
         }
         __syncwarp();
     }
