@@ -74,3 +74,57 @@ def test_linear_backward_of_very_wide_outputs(tmg):
     assert torch.equal(dB[at], (dz.T @ A.double()).to(BF16)) and torch.equal(db[at].double(), dz.sum(0))
     dB[at], db[at] = 0, 0
     assert not dB.any() and not db.any()
+
+
+TOP = 2 ** 31 - 8
+
+
+@pytest.fixture
+def patient(tmg):
+    """Contractions of 2^31 terms take a second or so of one cluster: longer waits."""
+    tmg.set_wait_budget_ns(60_000_000_000)
+    yield tmg
+    tmg.set_wait_budget_ns(2_000_000_000)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,N", [(1, 8), (3, 16)])
+def test_linear_contraction_just_below_2_31(patient, M, N):
+    A, B = torch.zeros(M, TOP, dtype=BF16, device=DEV), torch.zeros(N, TOP, dtype=BF16, device=DEV)
+    at = torch.tensor([0, 77, 2 ** 30, TOP - 60, TOP - 1], device=DEV)
+    A[:, at], B[:, at] = ints((M, 5), 6).to(DEV), ints((N, 5), 7).to(DEV)
+    D = patient.linear(A, B)
+    patient.check()
+    assert torch.equal(D, (A[:, at].double() @ B[:, at].double().T).to(BF16))
+
+
+def test_linear_columns_just_below_2_31(patient):
+    K = 8
+    A, B = ints((2, K), 8).to(DEV), torch.zeros(TOP, K, dtype=BF16, device=DEV)
+    at = torch.tensor([0, 300, 2 ** 30, TOP - 9, TOP - 1], device=DEV)
+    B[at] = ints((5, K), 9).to(DEV)
+    D = patient.linear(A, B)
+    patient.check()
+    assert torch.equal(D[:, at], (A.double() @ B[at].double().T).to(BF16))
+    D[:, at] = 0
+    assert not D[0].any() and not D[1].any()
+
+
+@pytest.mark.parametrize("sizes", [[0, TOP], [TOP - 40, 40]])
+def test_grouped_rows_just_below_2_31(patient, sizes):
+    N, K = 8, 8
+    off = torch.tensor([0, sizes[0], TOP], dtype=torch.int32, device=DEV)
+    A, B = torch.zeros(TOP, K, dtype=BF16, device=DEV), ints((2, N, K), 10).to(DEV)
+    at = torch.tensor([0, 255, 2 ** 30, TOP - 41, TOP - 40, TOP - 1], device=DEV)
+    A[at] = ints((6, K), 11).to(DEV)
+    D = patient.grouped_gemm(A, B, off)
+    dB = patient.grouped_gemm_wgrad(D, A, off)
+    patient.check()
+    want, grad = torch.zeros(6, N, device=DEV, dtype=torch.float64), torch.zeros(2, N, K, device=DEV, dtype=torch.float64)
+    for i, r in enumerate(at.tolist()):
+        e = 0 if r < sizes[0] else 1
+        want[i] = B[e].double() @ A[r].double()
+        grad[e] += torch.outer(want[i], A[r].double())
+    assert torch.equal(D[at].double(), want) and torch.equal(dB, grad.to(BF16))
+    D[at] = 0
+    assert all(not part.any() for part in D.view(torch.int64).split(1 << 28))

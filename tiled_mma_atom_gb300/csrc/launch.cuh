@@ -34,6 +34,12 @@ __device__ __forceinline__ void grid_release()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// n / d rounded up; n may be close to 2^31.
+__host__ __device__ __forceinline__ int ceil_div(int n, int d)
+{
+    return static_cast<int>((static_cast<unsigned>(n) + static_cast<unsigned>(d) - 1u) / static_cast<unsigned>(d));
+}
+
 template <class... P, class... A>
 cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A &&...args)
 {

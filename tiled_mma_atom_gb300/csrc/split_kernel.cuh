@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     const uint32_t rank = cluster_ctarank(), S = cluster_size();
     const int tile = blockIdx.x / S;
     constexpr int OUT = EPI == kSwSwiglu ? 64 : 128;           // output columns of a tile
-    const int tiles_n = (p.N + OUT - 1) / OUT, num_kb = (p.K + KB - 1) / KB;
+    const int tiles_n = ceil_div(p.N, OUT), num_kb = ceil_div(p.K, KB);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         rows = min(p.w, end - row0);
     };
     if constexpr (EPI == kSwDense) {
-        if (tile < (p.R + p.w - 1) / p.w * tiles_n)
+        if (tile < ceil_div(p.R, p.w) * tiles_n)
             take(0, 0, p.R, tile);
     } else {
         grid_wait();
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
                 a = min(max(p.offsets[e0 + lane], 0), p.R);
                 b = min(max(p.offsets[e0 + lane + 1], 0), p.R);
             }
-            int inc = (max(b - a, 0) + p.w - 1) / p.w * tiles_n;
+            int inc = ceil_div(max(b - a, 0), p.w) * tiles_n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, inc, o);

@@ -306,7 +306,7 @@ __device__ __forceinline__ void load_rows(uint4 (&v)[4], int lane, const __nv_bf
         v[i] = make_uint4(0, 0, 0, 0);
         if (row < nt && n < cols) {
             const __nv_bfloat16 *p = M + (r0 + row) * ld + n;
-            if (n + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+            if (cols - n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
                 v[i] = *reinterpret_cast<const uint4 *>(p);
             } else {
                 uint32_t u4[4] = {};
@@ -502,12 +502,12 @@ __device__ __forceinline__ SwapTile swap_tile(int t, const int *off, const int *
     }
     SwapTile x;
     x.e = lo;
-    const int first = off[lo], rows = off[lo + 1] - first, tiles = (rows + maxw - 1) / maxw;
+    const int first = off[lo], rows = off[lo + 1] - first, tiles = ceil_div(rows, maxw);
     int tm;
     tile_coords(t - start[lo], tiles, tiles_n, group, tm, x.tn);
     // the group's rows in 32s, spread evenly over its tiles: the first few
     // take one more
-    const int grains = (rows + 31) >> 5, each = grains / tiles, more = grains - each * tiles;
+    const int grains = ceil_div(rows, 32), each = grains / tiles, more = grains - each * tiles;
     const int g0 = tm * each + min(tm, more);
     x.w = 32 * (each + (tm < more ? 1 : 0));
     x.row0 = first + 32 * g0;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
     constexpr int OUT = EPI == kSwSwiglu ? 128 : 256;          // output columns of a tile
-    const int tiles_n = (p.N + OUT - 1) / OUT, num_kb = (p.K + KB - 1) / KB;
+    const int tiles_n = ceil_div(p.N, OUT), num_kb = ceil_div(p.K, KB);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
         int run = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < p.E ? (max(off[e + 1] - off[e], 0) + p.maxw - 1) / p.maxw * tiles_n : 0;
+            const int n = e < p.E ? ceil_div(max(off[e + 1] - off[e], 0), p.maxw) * tiles_n : 0;
             int inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

@@ -69,7 +69,7 @@ __device__ __forceinline__ void tma_store_tile(const CUtensorMap *map, uint32_t 
 }
 
 // Blocks of a group's contraction (one of zeros for an empty group).
-__device__ __forceinline__ int wg_blocks(int rows) { return rows > 0 ? (rows + 63) / 64 : 1; }
+__device__ __forceinline__ int wg_blocks(int rows) { return rows > 0 ? ceil_div(rows, 64) : 1; }
 
 // The walk of a pair: its run of split blocks first, then whole tiles.
 struct WgWalk {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-    const int tiles_n = (p.N + 255) / 256, tiles_k = (p.K + 255) / 256, per = tiles_n * tiles_k;
+    const int tiles_n = ceil_div(p.N, 256), tiles_k = ceil_div(p.K, 256), per = tiles_n * tiles_k;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
