@@ -10,8 +10,10 @@ and W2 (E, H, F)::
     y = moe_combine(grouped_gemm(h, W2, r.offsets), r.slots, r.weights, residual=x)
 
 Shapes never depend on values: the plan stays on the GPU, and no call waits
-for it.  Tensors given together with a `stream` other than the current one are
-recorded on it, so their memory is not reused before its work is done.
+for it.  A `stream` other than the current one (a torch stream or a raw handle)
+must be made to wait for the inputs, and the current one for the results, by the
+caller; the tensors are recorded on both, so their memory is not reused before
+the work on them is done.
 """
 from __future__ import annotations
 
@@ -38,15 +40,35 @@ class Routing(NamedTuple):
     slots: torch.Tensor       # (T, k) int32: the row of each (token, choice), -1 where there is none
 
 
-def _stream(stream, tensors) -> int:
-    """The handle of a stream that is not None."""
-    if hasattr(stream, "cuda_stream"):
-        if stream != torch.cuda.current_stream():
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        return int(stream.cuda_stream)
-    return int(stream)
+def _side(stream, dev):
+    """The stream of a call as a torch stream, or None where it is the current one."""
+    if not hasattr(stream, "cuda_stream"):       # a raw handle; 0 and 1 name the default stream
+        handle = int(stream)
+        stream = torch.cuda.default_stream(dev) if handle in (0, 1) else torch.cuda.ExternalStream(handle, dev)
+    return None if stream.cuda_stream == _current(dev.index) else stream
+
+
+def _empty(side):
+    """torch.empty for the outputs of a call.  On another stream (`side`) they are that
+    stream's memory, since the current one's may still be read by what is queued there,
+    and recorded on the current stream, where the caller will use them."""
+    if side is None:
+        return torch.empty
+
+    def empty(*shape, **kind):
+        with torch.cuda.stream(side):
+            t = torch.empty(*shape, **kind)
+        t.record_stream(torch.cuda.current_stream(t.device))
+        return t
+    return empty
+
+
+def _handle(side, tensors):
+    """The handle of another stream, with the call's tensors recorded on it."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(side)
+    return side.cuda_stream
 
 
 def _check(name, t, dtype, shape, device=None, inner=True):
@@ -87,10 +109,12 @@ def moe_route(logits: torch.Tensor, k: int, *, normalize: bool = True, stream=No
     if logits.stride(1) != 1:
         _check("logits", logits, logits.dtype, (T, E))
     dev = logits.device
-    weights, experts = torch.empty((T, k), dtype=_f32, device=dev), torch.empty((T, k), dtype=_i32, device=dev)
-    offsets, rows = torch.empty(E + 1, dtype=_i32, device=dev), torch.empty(T * k, dtype=_i32, device=dev)
-    slots = torch.empty((T, k), dtype=_i32, device=dev)
-    s = _current(dev.index) if stream is None else _stream(stream, (logits, weights, experts, offsets, rows, slots))
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
+    weights, experts = new((T, k), dtype=_f32, device=dev), new((T, k), dtype=_i32, device=dev)
+    offsets, rows = new(E + 1, dtype=_i32, device=dev), new(T * k, dtype=_i32, device=dev)
+    slots = new((T, k), dtype=_i32, device=dev)
+    s = _current(dev.index) if side is None else _handle(side, (logits, weights, experts, offsets, rows, slots))
     st = _native.lib().tmg_moe_route(logits.data_ptr(), T, E, k, logits.stride(0), dt, 1 if normalize else 0,
                                      weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
                                      slots.data_ptr(), s)
@@ -111,8 +135,10 @@ def moe_route_backward(logits: torch.Tensor, experts: torch.Tensor, dweights: to
         _check("logits", logits, logits.dtype, (T, E))
     k = experts.shape[-1]
     dev = logits.device
-    d = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    s = _current(dev.index) if stream is None else _stream(stream, (logits, experts, dweights, d))
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
+    d = new((T, E), dtype=logits.dtype, device=dev)
+    s = _current(dev.index) if side is None else _handle(side, (logits, experts, dweights, d))
     st = _native.lib().tmg_moe_route_backward(logits.data_ptr(), T, E, k, logits.stride(0), dt, 1 if normalize else 0,
                                               _flat("experts", experts, _i32, (T, k), dev),
                                               _flat("dweights", dweights, _f32, (T, k), dev), d.data_ptr(), s)
@@ -130,14 +156,16 @@ def moe_combine(Y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | No
     R, H = _matrix("Y", Y)
     T, k = _matrix("slots", slots)
     dev = Y.device
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
     _check("Y", Y, _bf16, (R, H))
     if residual is not None:
         _check("residual", residual, _bf16, (T, H), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=_bf16, device=dev)
+        out = new((T, H), dtype=_bf16, device=dev)
     else:
         _check("out", out, _bf16, (T, H), dev)
-    s = _current(dev.index) if stream is None else _stream(stream, (Y, slots, weights, residual, out))
+    s = _current(dev.index) if side is None else _handle(side, (Y, slots, weights, residual, out))
     st = _native.lib().tmg_moe_combine(Y.data_ptr(), R, Y.stride(0), _flat("slots", slots, _i32, (T, k), dev),
                                        _flat("weights", weights, _f32, (T, k), dev),
                                        None if residual is None else residual.data_ptr(),
@@ -156,12 +184,14 @@ def moe_combine_backward(dOut: torch.Tensor, Y: torch.Tensor, slots: torch.Tenso
     T, H = _matrix("dOut", dOut)
     R, _ = _matrix("Y", Y)
     dev = dOut.device
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
     _check("dOut", dOut, _bf16, (T, H))
     _check("Y", Y, _bf16, (R, H), dev)
     k = slots.shape[-1]
-    dY = torch.empty((R, H), dtype=_bf16, device=dev)
-    dw = torch.empty((T, k), dtype=_f32, device=dev)
-    s = _current(dev.index) if stream is None else _stream(stream, (dOut, Y, slots, weights, dY, dw))
+    dY = new((R, H), dtype=_bf16, device=dev)
+    dw = new((T, k), dtype=_f32, device=dev)
+    s = _current(dev.index) if side is None else _handle(side, (dOut, Y, slots, weights, dY, dw))
     st = _native.lib().tmg_moe_combine_backward(dOut.data_ptr(), dOut.stride(0), Y.data_ptr(), R, Y.stride(0),
                                                 _flat("slots", slots, _i32, (T, k), dev),
                                                 _flat("weights", weights, _f32, (T, k), dev), dY.data_ptr(),
@@ -192,6 +222,8 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, D: tor
     if dt is None or B.dtype != A.dtype:
         raise TypeError(f"A and B must both be bfloat16 or both float8_e4m3fn, got {A.dtype} and {B.dtype}")
     dev = A.device
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
     if KB != K or B.device != dev:
         raise ValueError(f"B must be (E, N, {K}) on {dev}, got {tuple(B.shape)} on {B.device}")
     act = ACTIVATIONS.get(activation, -1)
@@ -206,7 +238,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, D: tor
     elif preact is not None:
         raise ValueError("preact goes with swiglu and swiglu_grad")
     if D is None:
-        D = torch.empty((R, cols), dtype=_bf16, device=dev)
+        D = new((R, cols), dtype=_bf16, device=dev)
     else:
         _check("D", D, _bf16, (R, cols), dev)
     a = _native.pack_grouped(A.data_ptr(), B.data_ptr(), D.data_ptr(), _flat("offsets", offsets, _i32, (E + 1,), dev),
@@ -215,7 +247,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, D: tor
                              0 if scale_b is None else _flat("scale_b", scale_b, _f32, (E, N), dev),
                              0 if preact is None else preact.data_ptr(), R, N, K, E, T, *A.stride(), *B.stride(),
                              D.stride(0), 0 if preact is None else preact.stride(0), dt, act)
-    s = _current(dev.index) if stream is None else _stream(stream, (A, B, offsets, rows, preact, scale_a, scale_b, D))
+    s = _current(dev.index) if side is None else _handle(side, (A, B, offsets, rows, preact, scale_a, scale_b, D))
     st = _native.lib().tmg_grouped_gemm(a, s)
     if st:
         _native.raise_on(st)
@@ -231,13 +263,15 @@ def grouped_gemm_wgrad(dD: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor,
     T, K = _matrix("A", A)
     E = offsets.shape[0] - 1
     dev = dD.device
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
     _check("dD", dD, _bf16, (R, N), inner=False)
     _check("A", A, _bf16, (T, K), dev, inner=False)
     if rows is None and T != R:
         raise ValueError(f"without rows, A must have dD's {R} rows, got {T}")
     if dB is None:
-        dB = torch.empty((E, N, K), dtype=_bf16, device=dev)
-    s = _current(dev.index) if stream is None else _stream(stream, (dD, A, offsets, rows, dB))
+        dB = new((E, N, K), dtype=_bf16, device=dev)
+    s = _current(dev.index) if side is None else _handle(side, (dD, A, offsets, rows, dB))
     st = _native.lib().tmg_grouped_gemm_wgrad(dD.data_ptr(), *dD.stride(), A.data_ptr(), *A.stride(),
                                               _flat("dB", dB, _bf16, (E, N, K), dev),
                                               _flat("offsets", offsets, _i32, (E + 1,), dev),
@@ -262,13 +296,15 @@ def linear(A: torch.Tensor, B: torch.Tensor, D: torch.Tensor | None = None, *, b
     if dt is None or B.dtype != A.dtype:
         raise TypeError(f"A and B must both be bfloat16 or both float8_e4m3fn, got {A.dtype} and {B.dtype}")
     dev = A.device
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
     if KB != K or B.device != dev:
         raise ValueError(f"B must be (N, {K}) on {dev}, got {tuple(B.shape)} on {B.device}")
     act = ACTIVATIONS.get(activation, -1)
     if not 0 <= act <= 3:
         raise ValueError(f"unknown activation {activation!r}; one of 'none', 'relu', 'silu', 'gelu'")
     if D is None:
-        D = torch.empty((M, N), dtype=_bf16, device=dev)
+        D = new((M, N), dtype=_bf16, device=dev)
     else:
         _check("D", D, _bf16, (M, N), dev)
     if residual is not None:
@@ -282,7 +318,7 @@ def linear(A: torch.Tensor, B: torch.Tensor, D: torch.Tensor | None = None, *, b
                             0 if residual is None else residual.data_ptr(), 0 if preact is None else preact.data_ptr(),
                             M, N, K, *A.stride(), *B.stride(), D.stride(0), 0 if residual is None else residual.stride(0),
                             0 if preact is None else preact.stride(0), dt, act)
-    s = _current(dev.index) if stream is None else _stream(stream, (A, B, D, bias, residual, preact, scale_a, scale_b))
+    s = _current(dev.index) if side is None else _handle(side, (A, B, D, bias, residual, preact, scale_a, scale_b))
     st = _native.lib().tmg_linear(a, s)
     if st:
         _native.raise_on(st)
@@ -299,6 +335,8 @@ def linear_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, preac
     M, N = _matrix("dD", dD)
     K = _matrix("A", A)[1]
     dev = dD.device
+    side = None if stream is None else _side(stream, dev)
+    new = _empty(side)
     act = ACTIVATIONS.get(activation, -1)
     if not 0 <= act <= 3:
         raise ValueError(f"unknown activation {activation!r}; one of 'none', 'relu', 'silu', 'gelu'")
@@ -311,10 +349,10 @@ def linear_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, preac
         _check("preact", preact, _bf16, (M, N), dev)
     else:
         preact = None
-    dA = torch.empty((M, K), dtype=_bf16, device=dev)
-    dB = torch.empty((N, K), dtype=_bf16, device=dev)
-    dbias = torch.empty((N,), dtype=_f32, device=dev)
-    s = _current(dev.index) if stream is None else _stream(stream, (dD, A, B, preact, dA, dB, dbias))
+    dA = new((M, K), dtype=_bf16, device=dev)
+    dB = new((N, K), dtype=_bf16, device=dev)
+    dbias = new((N,), dtype=_f32, device=dev)
+    s = _current(dev.index) if side is None else _handle(side, (dD, A, B, preact, dA, dB, dbias))
     st = _native.lib().tmg_linear_backward(dD.data_ptr(), dD.stride(0), None if preact is None else preact.data_ptr(),
                                            0 if preact is None else preact.stride(0), A.data_ptr(), A.stride(0),
                                            B.data_ptr(), B.stride(0), dA.data_ptr(), dB.data_ptr(), dbias.data_ptr(),
