@@ -2,6 +2,7 @@
 // dense product with the residual epilogue (include/tmg.h): argument checks
 // and launches.
 #include <algorithm>
+#include <cstdio>
 #include <cstring>
 #include <exception>
 
@@ -132,6 +133,11 @@ float block_ns(int w)
     return w <= 128 ? 245.f : w <= 160 ? 255.f : w <= 192 ? 262.f : w <= 224 ? 266.f : 295.f;
 }
 
+constexpr float kHbm = 6700.f;         // bytes a nanosecond
+
+// HBM's time for one group's weights.
+float weight_ns(const GroupedArgs &a) { return static_cast<float>(a.N) * a.K * (a.e4m3 ? 1 : 2) / kHbm; }
+
 // Widest tile.  One group: the width whose waves of tiles take the least time
 // (4096 x 4096 x 4096: 19 x 16 tiles of 224 columns are four waves of 76 pairs
 // like 16 x 16 of 256, and take 79.5 us against 87; 1024 x 8192 x 8192: 82 us in
@@ -149,7 +155,8 @@ int tile_width(const GroupedArgs &a, int64_t tiles_n, int64_t num_kb, int pairs)
     for (int w = kSwMaxW; w >= 32; w -= 32) {
         SwapTail tail;
         const int64_t tiles = std::min((a.R + w - 1) / w * tiles_n, kMax31);
-        const double ns = swap_time(static_cast<int>(tiles), pairs, static_cast<int>(num_kb), w, block_ns(w), 0.f, tail);
+        const double ns = swap_time(static_cast<int>(tiles), pairs, static_cast<int>(num_kb), w, block_ns(w), weight_ns(a),
+                                    tail);
         if (!best || ns < 0.95 * best_ns || (a.R <= w && ns <= best_ns)) {
             best = w;
             best_ns = ns;
@@ -179,7 +186,7 @@ SplitPlan split_plan(const GroupedArgs &a, int64_t F, bool swiglu, int64_t num_k
     const int64_t pairs = num_sms / 2, tiles_n = (F + (swiglu ? 63 : 127)) / (swiglu ? 64 : 128);
     const int64_t groups = std::min(a.E, a.R);              // at most so many have rows
     auto row_tiles = [&](int64_t w) { return a.E == 1 ? (a.R + w - 1) / w : std::min(a.R, groups + a.R / w); };
-    const double hbm = static_cast<double>(groups) * a.N * a.K * elem / 6700.0;
+    const double hbm = static_cast<double>(groups) * weight_ns(a);
     const int64_t pair_tiles = row_tiles(maxw) * pair_tiles_n;
     SwapTail tail;
     double best_ns = 5500 + 8 * maxw + swap_time(static_cast<int>(std::min(pair_tiles, kMax31)), static_cast<int>(pairs),
@@ -364,17 +371,32 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     if ((a.R / 32 + a.E) * tiles_n > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
     p.block_ns = block_ns(p.maxw);
-    // no split of a tile this short pays (two pieces, half a tile saved)
-    if ((K + kb - 1) / kb * p.block_ns * 0.5f > 2500.f + p.maxw / 256.f * 5200.f) {
+    // room for the pieces of cut tiles: the kernel cuts none without.  The dense
+    // product's tiles are known here, a grouped one's only there.
+    const int num_kb = static_cast<int>((K + kb - 1) / kb);
+    SwapTail tail{0, 0};
+    if (epi == kSwDense) {
+        const int total = static_cast<int>((a.R + p.maxw - 1) / p.maxw * tiles_n);
+        p.hbm_ns = weight_ns(a) / total;
+        swap_time(total, pairs, num_kb, p.maxw, p.block_ns, total * p.hbm_ns, tail);
+    } else {
+        // narrow tiles, most of them a group's only ones, read their weights once each
+        p.hbm_ns = p.maxw < kSwMaxW ? 32768.f / kHbm * num_kb : 0.f;
+    }
+    if (epi == kSwDense ? tail.tiles > 0 : swap_may_cut(num_kb, p.maxw, p.block_ns)) {
         p.partials = static_cast<float *>(workspace(kWsPartials, pairs * sw_partial_floats(p.maxw) * sizeof(float), s, &st));
         if (!p.partials)
             return st;
     }
     if ((st = counters(pairs, s, &p.feed, &p.counters)) != TMG_OK)
         return st;
-    log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s",
+    char cuts[48] = "";
+    if (tail.tiles)
+        snprintf(cuts, sizeof cuts, ", %d tiles cut over %d pairs", tail.tiles, tail.pairs);
+    log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s%s",
                a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", p.R, (long long)a.N, (long long)a.K, p.E, 256, p.maxw,
-               p.stages, maj ? "MN-major" : "K-major", p.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "");
+               p.stages, maj ? "MN-major" : "K-major", p.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "",
+               cuts);
     return launched(launch_swap(p, epi, a.e4m3, ds.num_sms, err_ctx(ds), s), "grouped product launch");
 }
 

@@ -73,6 +73,7 @@ struct SwapArgs {
     int stages, stage_bytes;
     int group;                 // row tiles per band
     float block_ns;            // a K block of a tile of maxw columns
+    float hbm_ns;              // HBM's time for the weights, a tile's share
     float *partials;           // sw_partial_floats(maxw) per pair; null: no tile is split
     uint32_t *counters;        // 16 per cut tile
     uint32_t *feed;            // the tile counter
@@ -94,13 +95,24 @@ __host__ inline int sw_smem(int stages, int stage_bytes, int staging, int E)
 // Nanoseconds that `total` tiles of w columns take over np pairs, and how the last
 // wave is split (tail): where at most half the pairs have a tile in it, each of
 // its tiles is cut along K over 2 to 8 pairs, before their whole tiles, so that
-// the sums are under way while those run.  A cut adds 2.5 us + w / 256 (4 + 0.6 us
-// a piece) (measured at 128 to 256 columns; 2489 x 5648 x 8192, 230 tiles: 151
-// us whole, 129 with two tiles over eight pairs each).  block_ns: a K block of a
-// tile; hbm_ns: the time of the weights' bytes.
+// the sums are under way while those run.  A cut adds swap_cut_ns (measured at 128
+// to 256 columns).  2489 x 5648 x 8192, 230 tiles: 151 us whole, 127 with two tiles
+// over eight pairs each; 875 x 6064 x 5920, 96 tiles: 52.8 and 42.6.  block_ns: a K
+// block of a tile; hbm_ns: the time of the weights' bytes.
 struct SwapTail {
     int tiles, pairs;
 };
+__host__ __device__ inline float swap_cut_ns(int w, int each)
+{
+    return 2500.f + w * (1.f / 256.f) * (4000.f + 600.f * each);
+}
+// Only where half a tile is worth more than a cut in two: shorter ones would gain
+// little by more pieces (2489 x 5648 x 3000 75.4 us whole, 79.6 cut; 5486 x 6192 x
+// 2896 117 and 115).
+__host__ __device__ inline bool swap_may_cut(int num_kb, int w, float block_ns)
+{
+    return num_kb * block_ns * 0.5f > swap_cut_ns(w, 2);
+}
 __host__ __device__ inline float swap_time(int total, int np, int num_kb, int w, float block_ns, float hbm_ns, SwapTail &tail)
 {
     const int q = total / np, rem = total - q * np;
@@ -109,10 +121,10 @@ __host__ __device__ inline float swap_time(int total, int np, int num_kb, int w,
     const float best = whole > hbm_ns ? whole : hbm_ns;
     const int each = rem == 0 ? 0 : np / rem < 8 ? np / rem : 8;
     tail.tiles = tail.pairs = 0;
-    if (each < 2 || num_kb < each)
+    if (each < 2 || num_kb < each || !swap_may_cut(num_kb, w, block_ns))
         return best;
     const float shared = q * tile + tile / each;
-    const float cut = (shared > hbm_ns ? shared : hbm_ns) + 2500.f + w * (1.f / 256.f) * (4000.f + 600.f * each);
+    const float cut = (shared > hbm_ns ? shared : hbm_ns) + swap_cut_ns(w, each);
     if (cut >= best)
         return best;
     tail.tiles = rem;
@@ -632,12 +644,10 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    // HBM (6.7 TB/s) takes 4.8 ns for the 32 KB of a K block's weights (narrow
-    // tiles read their weights once each).
     const int total = start[p.E];
     SwapTail tail{0, 0};
     if (p.partials)
-        swap_time(total, nclusters, num_kb, p.maxw, p.block_ns, p.maxw < kSwMaxW ? 4.8f * total * num_kb : 0.f, tail);
+        swap_time(total, nclusters, num_kb, p.maxw, p.block_ns, total * p.hbm_ns, tail);
     const int sk = tail.tiles;
     SwapWalk walk(feed_smem, cluster, nclusters, total, tail, num_kb, err, abort_flag);
     int tile, kb0, kb1, slot;
