@@ -30,3 +30,11 @@ def test_dense_tiles_are_cut_where_the_estimate_says():
     assert len(lines) == 2 and all("swap_kernel" in line for line in lines)
     assert "24 tiles cut over 72 pairs" in lines[0]
     assert "cut" not in lines[1]
+
+
+def test_gradient_copies_no_operand_for_less_than_256_rows():
+    """200 x 4096 x 20480: 80 tiles would fill the CTA pairs, but the GEMM reads
+    MN-major operands in place from 256 rows on only."""
+    lines = log_of("tmg.linear_backward(normal(200, 4096), normal(200, 20480), normal(4096, 20480))")
+    assert "dense: 200 rows" in lines[0]
+    assert not any("200x20480x4096" in line for line in lines)

@@ -781,10 +781,11 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
                 return st;
         }
         // dA (M, K) = dz (M, N) . B: B read as (K, N); dB (N, K) = dz^T . A.  Each
-        // by the kernel that is faster.  Where the tiles do not fill the CTA pairs,
-        // the GEMM would copy the MN-major operands (165 x 6408 x 736: dA 35 us
-        // against 12 with the dense product; 2795 x 624 x 4024: dB 30 against 22
-        // with the weight gradient; one row of 4096 x 4096: dB 73 against 15).
+        // by the kernel that is faster.  Where the tiles do not fill the CTA pairs, or
+        // there are less than 256 rows, the GEMM would copy the MN-major operands (165
+        // x 6408 x 736: dA 35 us against 12 with the dense product; 250 x 4096 x 24576:
+        // all 196 against 116; 2795 x 624 x 4024: dB 30 against 22 with the weight
+        // gradient; one row of 4096 x 4096: dB 73 against 15).
         // Where they do, its pair kernel reads them in place and is faster on short
         // contractions (8191 x 4096 x 4096: dA 144 against 148; 1024 x 4096 x 4096:
         // dB 26 against 30), slower on long ones (2048 x 8192 x 8192: dA 164 against
@@ -792,7 +793,9 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact, 
         // x 4096: dB 165 against 159) and where rows begin inside a sector (2833 x
         // 6648 x 6800: dA 183 against 161, dB 169 against 161; 74 x 7016 x 6296: dB
         // 36 against 29).
-        auto fills = [&](int64_t rows, int64_t cols) { return (rows + 255) / 256 * ((cols + 255) / 256) >= ds->num_sms / 2; };
+        auto fills = [&](int64_t rows, int64_t cols) {
+            return rows >= 256 && (rows + 255) / 256 * ((cols + 255) / 256) >= ds->num_sms / 2;
+        };
         const bool some = M > 0 && N > 0 && K > 0;
         const bool a_product = some && (!fills(M, K) || N > 4096 || (ldz | ldb) % 16);
         const bool b_wgrad = some && (!fills(N, K) || M < 64 || (M > 6000 && M >= N && M >= K) || (ldz | lda) % 16);
