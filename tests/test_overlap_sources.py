@@ -19,3 +19,15 @@ def test_overlapped_kernels_use_plain_loads():
         text = read(name)
         assert "__ldg" not in text and "ld.global.nc" not in text, name
         assert not re.search(r"const\s+[\w:]+\s*\*\s*__restrict__", text), name
+
+
+def test_kernels_settle_after_giving_up():
+    """A kernel whose wait ran out leaves only when its loads have landed and its MMAs
+    have run: those waits do not stop at the abort flag, and have a limit of their own."""
+    flat = lambda name: re.sub(r"\s+", " ", read(name))
+    body = flat("feed.cuh").split("void settle(")[1].split("constexpr")[0]
+    assert "nullptr, kSiteDrain" in body and "1000000000ull" in body
+    for name, loads, mmas in (("swap_kernel.cuh", "settle(full,", "settle(empty,"), ("wgrad.cu", "settle(full,", "settle(empty,"),
+                              ("split_kernel.cuh", "settle(full,", "settle(done,")):
+        text = flat(name)
+        assert loads in text and mmas in text, name

@@ -22,6 +22,22 @@
 
 namespace tmg {
 
+// A kernel that has given up leaves shared memory and TMEM only when its loads have
+// landed and its MMAs have run: wait for the last n uses of the ring before (stage,
+// phase), whatever the abort flag says, with a limit of a second at least.  Out of
+// line: no call reaches it unless a wait ran out, and its code would cost the others
+// (0.3 us of 7.7 at 16 x 4096 x 4096).
+static __device__ __noinline__ void settle(uint64_t *bars, int stages, int stage, uint32_t phase, int n, uint32_t *error,
+                                           uint64_t budget_ns)
+{
+    const ErrCtx last{error, budget_ns > 1000000000ull ? budget_ns : 1000000000ull};
+    for (int i = 0; i < n && i < stages; ++i) {
+        const int s = stage - 1 - i;
+        if (!mbar_wait_cluster(&bars[s < 0 ? s + stages : s], s < 0 ? phase ^ 1u : phase, last, nullptr, kSiteDrain))
+            return;
+    }
+}
+
 constexpr int kFeedSlots = 2;
 constexpr int kFeedReaders = 19;        // producer and eight epilogue warps of both CTAs, the MMA warp
 

@@ -24,6 +24,7 @@
 #pragma once
 
 #include "act.cuh"
+#include "feed.cuh"
 #include "grouped.h"
 #include "launch.cuh"
 #include "split.h"
@@ -251,6 +252,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     if constexpr (EPI == kSwDense)                             // all up to here depends on sizes only
         grid_wait();
 
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
     if (work && (warp == 0 || warp == 2)) {
         // ------------------ TMA producers: the weights (warp 0), the rows (warp 2)
         if (warp == 2 && p.gather) {
@@ -266,9 +269,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         }
         const uint32_t tx = 16384u + static_cast<uint32_t>(p.gather ? wt : p.w) * 128u;
         const int n0 = tn * OUT;
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb, ++issued) {
             if (!mbar_wait_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty))
                 break;
             uint8_t *sw = smem + stage * p.stage_bytes, *sx = sw + 16384;
@@ -300,8 +301,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         // -------------------------------------------- MMA issuer
         const uint32_t idesc = (IN == kInE4m3 ? idesc_e4m3_f32(128, wt) : idesc_bf16_f32(128, wt)) | (p.maj ? 1u << 15 : 0u);
         const uint64_t astep = (p.maj ? kMnKStepBytes : 32) >> 4;
-        int stage = 0;
-        uint32_t phase = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait_warp(&full[stage], phase, err, abort_flag, kSiteMmaFull))
                 break;
@@ -357,6 +356,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     }
     __syncwarp();
     cluster_sync();                  // every CTA's partial tile is written
+    if (work && warp < 2 && *abort_flag) {
+        if (warp == 0)               // rows and weights share the stages' barriers
+            settle(full, p.stages, stage, phase, issued, err.word, err.budget_ns);
+        else
+            settle(done, 1, 0, 1, 1, err.word, err.budget_ns);
+        __syncwarp();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, p.tmem_cols);

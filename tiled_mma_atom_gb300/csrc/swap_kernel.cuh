@@ -729,6 +729,9 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 mbar_wait_cluster(&full[s], ph, err, abort_flag, kSiteDrain);
             mbar_wait_cluster(&empty[s], ph, err, abort_flag, kSiteDrain);
         }
+        if (*abort_flag && rank == 0)
+            settle(full, p.stages, stage, phase, static_cast<int>(min(issued, static_cast<int64_t>(p.stages))), err.word,
+                   err.budget_ns);
     } else if (warp == 1) {
         if (rank == 0) {
             // -------------------------------------------- MMA issuer
@@ -783,6 +786,8 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                     break;
                 mma_commit_pair_w(&tfull[acc], 0x3);
             }
+            if (*abort_flag)         // the last K block's commit (or, before the first, none)
+                settle(empty, p.stages, stage, phase, 1, err.word, err.budget_ns);
         }
     } else if (warp == 10) {
         if constexpr (EPI == kSwDense)

@@ -284,6 +284,9 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                 mbar_wait_cluster(&full[s], ph, err, abort_flag, kSiteDrain);
             mbar_wait_cluster(&empty[s], ph, err, abort_flag, kSiteDrain);
         }
+        if (*abort_flag && rank == 0)
+            settle(full, p.stages, stage, phase, static_cast<int>(min(issued, static_cast<int64_t>(p.stages))), err.word,
+                   err.budget_ns);
     } else if (warp == 1) {
         if (rank == 0) {
             // -------------------------------------------- MMA issuer
@@ -324,6 +327,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) wgrad_kernel(const __grid_const
                     break;
                 mma_commit_pair_w(&tfull[acc], 0x3);
             }
+            if (*abort_flag)         // the last K block's commit (or, before the first, none)
+                settle(empty, p.stages, stage, phase, 1, err.word, err.budget_ns);
         }
     } else if (warp == 11) {
         // ------------------- gathers of the last, partial sixteen rows of a group
