@@ -374,7 +374,7 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     // room for the pieces of cut tiles: the kernel cuts none without.  The dense
     // product's tiles are known here, a grouped one's only there.
     const int num_kb = static_cast<int>((K + kb - 1) / kb);
-    SwapTail tail{0, 0};
+    SwapTail tail{0, 1};
     if (epi == kSwDense) {
         const int total = static_cast<int>((a.R + p.maxw - 1) / p.maxw * tiles_n);
         p.hbm_ns = weight_ns(a) / total;
@@ -392,7 +392,7 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
         return st;
     char cuts[48] = "";
     if (tail.tiles)
-        snprintf(cuts, sizeof cuts, ", %d tiles cut over %d pairs", tail.tiles, tail.pairs);
+        snprintf(cuts, sizeof cuts, ", %d tiles cut over %d pairs", tail.tiles, tail.tiles * tail.each);
     log_choice("%s %s: %d rows, N=%lld K=%lld E=%d -> swap_kernel: %d x up to %d tiles, %d stages, weights %s%s%s",
                a.e4m3 ? "e4m3" : "bf16", a.offsets ? "grouped" : "dense", p.R, (long long)a.N, (long long)a.K, p.E, 256, p.maxw,
                p.stages, maj ? "MN-major" : "K-major", p.gather ? ", rows gathered by TMA" : a.rows ? ", rows gathered first" : "",

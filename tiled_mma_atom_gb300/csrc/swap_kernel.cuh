@@ -80,8 +80,8 @@ struct SwapArgs {
 };
 
 constexpr int kSwMaxW = 256;
-// fp32 partials of a pair: 2 pieces, 2 CTAs, 4 lane quarters of 32 x maxw
-__host__ __device__ inline int64_t sw_partial_floats(int maxw) { return 2ll * 2 * 4 * 32 * maxw; }
+// fp32 partials of a pair's piece: 2 CTAs, 4 lane quarters of 32 x maxw
+__host__ __device__ inline int64_t sw_partial_floats(int maxw) { return 2ll * 4 * 32 * maxw; }
 constexpr int kSwStage = 2048;       // a warp's staging tile: two of them for the dense product's TMA stores
 constexpr int kSwMaxStages = 12;
 constexpr int kSwGatherW = 64;       // widest tile with gathers
@@ -100,7 +100,7 @@ __host__ inline int sw_smem(int stages, int stage_bytes, int staging, int E)
 // over eight pairs each; 875 x 6064 x 5920, 96 tiles: 52.8 and 42.6.  block_ns: a K
 // block of a tile; hbm_ns: the time of the weights' bytes.
 struct SwapTail {
-    int tiles, pairs;
+    int tiles, each;           // tiles that are cut, pieces of each
 };
 __host__ __device__ inline float swap_cut_ns(int w, int each)
 {
@@ -120,7 +120,8 @@ __host__ __device__ inline float swap_time(int total, int np, int num_kb, int w,
     const float whole = (q + (rem ? 1 : 0)) * tile;
     const float best = whole > hbm_ns ? whole : hbm_ns;
     const int each = rem == 0 ? 0 : np / rem < 8 ? np / rem : 8;
-    tail.tiles = tail.pairs = 0;
+    tail.tiles = 0;
+    tail.each = 1;
     if (each < 2 || num_kb < each || !swap_may_cut(num_kb, w, block_ns))
         return best;
     const float shared = q * tile + tile / each;
@@ -128,7 +129,7 @@ __host__ __device__ inline float swap_time(int total, int np, int num_kb, int w,
     if (cut >= best)
         return best;
     tail.tiles = rem;
-    tail.pairs = rem * each;
+    tail.each = each;
     return cut;
 }
 
@@ -529,44 +530,36 @@ __device__ __forceinline__ SwapTile swap_tile(int t, const int *off, const int *
 
 constexpr int kSwThreads = 352;
 
-// The segments of a pair: its run of split K blocks (the units of the first sk
-// tiles), then whole tiles.
+// The walk of a pair: its piece of a cut tile, if it has one, then whole tiles.
 struct SwapWalk {
     Feed feed;
-    int sk, num_kb, runs = 0;
-    int64_t u, u_end;
+    int cut, each, num_kb;           // cut tiles, pieces of each
+    int c;                           // the pair, or -1 once its piece is taken
     const ErrCtx &err;
     volatile int *abort;
 
-    __device__ SwapWalk(FeedSmem *f, int c, int nc, int total, const SwapTail &t, int nkb, const ErrCtx &e, volatile int *ab)
-        : feed(f, c, nc, total - t.tiles), sk(t.tiles), num_kb(nkb), err(e), abort(ab)
+    __device__ SwapWalk(FeedSmem *f, int c_, int nc, int total, const SwapTail &t, int nkb, const ErrCtx &e, volatile int *ab)
+        : feed(f, c_, nc, total - t.tiles), cut(t.tiles), each(t.each), num_kb(nkb),
+          c(c_ < t.tiles * t.each ? c_ : -1), err(e), abort(ab)
     {
-        u = u_end = 0;
-        if (c < t.pairs) {
-            const int64_t U = static_cast<int64_t>(sk) * num_kb;
-            u = U * c / t.pairs;
-            u_end = U * (c + 1) / t.pairs;
-        }
     }
 
-    // Tile, K blocks, whether a piece of a split tile, and the pair's partial
-    // slot for it (0 first piece, 1 last).
-    __device__ __forceinline__ bool next(int &tile, int &kb0, int &kb1, bool &partial, int &slot)
+    // Tile, K blocks, and whether they are a piece of a cut tile.
+    __device__ __forceinline__ bool next(int &tile, int &kb0, int &kb1, bool &partial)
     {
-        kb0 = slot = 0;
-        kb1 = num_kb;
-        partial = false;
-        if (u >= u_end) {
+        partial = c >= 0;
+        if (!partial) {
+            kb0 = 0;
+            kb1 = num_kb;
             const bool more = feed.next(tile, err, abort);
-            tile += sk;
+            tile += cut;
             return more;
         }
-        tile = static_cast<int>(u / num_kb);
-        kb0 = static_cast<int>(u % num_kb);
-        kb1 = static_cast<int>(min(static_cast<int64_t>(num_kb), kb0 + (u_end - u)));
-        partial = kb0 != 0 || kb1 != num_kb;
-        slot = runs++ ? 1 : 0;
-        u += kb1 - kb0;
+        tile = c / each;
+        const int i = c - tile * each;
+        kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * i / each);
+        kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (i + 1) / each);
+        c = -1;
         return true;
     }
 };
@@ -645,12 +638,11 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     const uint32_t tmem_base = *tmem_slot;
 
     const int total = start[p.E];
-    SwapTail tail{0, 0};
+    SwapTail tail{0, 1};
     if (p.partials)
         swap_time(total, nclusters, num_kb, p.maxw, p.block_ns, total * p.hbm_ns, tail);
-    const int sk = tail.tiles;
     SwapWalk walk(feed_smem, cluster, nclusters, total, tail, num_kb, err, abort_flag);
-    int tile, kb0, kb1, slot;
+    int tile, kb0, kb1;
     bool partial;
     // The dense product's tiles depend on sizes only: its warps wait for the
     // preceding kernel after their first tile is decoded (4096 x 4096 x 4096 in a
@@ -663,7 +655,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
         int64_t issued = 0;
         bool ok = true;
         walk.feed.producer = rank == 0;
-        while (ok && walk.next(tile, kb0, kb1, partial, slot)) {
+        while (ok && walk.next(tile, kb0, kb1, partial)) {
             const SwapTile x = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group);
             if constexpr (EPI == kSwDense)
                 grid_wait();
@@ -743,7 +735,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
             // The next tile is fetched and decoded (0.3 us) while the last K
             // blocks of this one are under way, so the MMAs go on without a gap.
             const uint32_t base = (IN == kInE4m3 ? idesc_e4m3_f32(256, 0) : idesc_bf16_f32(256, 0)) | (p.maj ? 1u << 15 : 0u);
-            bool more = walk.next(tile, kb0, kb1, partial, slot);
+            bool more = walk.next(tile, kb0, kb1, partial);
             int w = more ? swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group).w : 0;
             while (ok && more) {
                 const uint32_t idesc = base | static_cast<uint32_t>(w >> 3) << 17;
@@ -757,7 +749,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 const uint32_t d_tmem = tmem_base + acc * kSwMaxW;
                 for (int kb = b0; kb < b1; ++kb) {
                     if (kb == turn) {
-                        more = walk.next(tile, kb0, kb1, partial, slot);
+                        more = walk.next(tile, kb0, kb1, partial);
                         if (more)
                             w = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group).w;
                     }
@@ -792,14 +784,13 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
     } else if (warp == 10) {
         if constexpr (EPI == kSwDense)
             grid_wait();
-        feed_run(feed_smem, rank, total - sk, nclusters, p.feed, err, abort_flag);
+        feed_run(feed_smem, rank, total - tail.tiles, nclusters, p.feed, err, abort_flag);
     } else {
         // ---------------------------------------------------- epilogue
         const int ew = warp - 2, half = ew / 4, q = warp & 3;
         Staging stg{smem_u32(staging + ew * p.staging), 0, p.tma_d || p.tma_p};
-        const int64_t U = static_cast<int64_t>(sk) * num_kb;
         int local = 0;
-        while (walk.next(tile, kb0, kb1, partial, slot)) {
+        while (walk.next(tile, kb0, kb1, partial)) {
             const SwapTile x = swap_tile(tile, off, start, p.E, p.maxw, tiles_n, p.group);
             const int acc = local & 1;
             const uint32_t acc_phase = (local >> 1) & 1;
@@ -848,7 +839,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
             bool finish = !partial;
             int c_first = 0, c_last = 0;
             if (partial) {
-                const int64_t mine = ((static_cast<int64_t>(2 * cluster + slot) * 2 + rank) * 4 + q) * piece;
+                const int64_t mine = ((static_cast<int64_t>(cluster) * 2 + rank) * 4 + q) * piece;
 #pragma unroll 1
                 for (int c = half; c < chunks; c += 2) {
                     float v[32];
@@ -866,8 +857,8 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
                 if (half < chunks) {
-                    c_first = unit_owner(static_cast<int64_t>(tile) * num_kb, U, tail.pairs);
-                    c_last = unit_owner(static_cast<int64_t>(tile + 1) * num_kb - 1, U, tail.pairs);
+                    c_first = tile * walk.each;
+                    c_last = c_first + walk.each - 1;
                     const int64_t at = (static_cast<int64_t>(tile) * 2 + rank) * 8 + ew;
                     finish = last_arrival(p.counters + at, c_last - c_first,
                                           bounds_ok(at, 2ll * nclusters * 16, err, kBndCounters));
@@ -891,8 +882,7 @@ __global__ void __launch_bounds__(kSwThreads, 1) swap_kernel(const __grid_consta
                         for (int i = 0; i < 32; ++i)
                             v[i] = 0.f;
                         add_pieces(v, p.partials, limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
-                            const int s2 = static_cast<int>((U * cc / tail.pairs) / num_kb) == tile ? 0 : 1;
-                            return ((static_cast<int64_t>(2 * cc + s2) * 2 + rank) * 4 + q) * piece;
+                            return ((static_cast<int64_t>(cc) * 2 + rank) * 4 + q) * piece;
                         }, err);
                     }
                     finish_chunk<EPI>(p, v, stg, lane, r0, nt, n0, sa, sb, bias, pre, [&] { ahead(c + 2); }, err);
