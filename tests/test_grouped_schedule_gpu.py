@@ -38,3 +38,41 @@ def test_gradient_copies_no_operand_for_less_than_256_rows():
     lines = log_of("tmg.linear_backward(normal(200, 4096), normal(200, 20480), normal(4096, 20480))")
     assert "dense: 200 rows" in lines[0]
     assert not any("200x20480x4096" in line for line in lines)
+
+
+GRADIENT = """
+def ints(m, n, seed):
+    return torch.randint(-2, 3, (m, n), generator=torch.Generator('cuda').manual_seed(seed), device='cuda').to(torch.bfloat16)
+M, N, K = {size}
+dD, A, B, pre = ints(M, N, 1), ints(M, K, 2), ints(N, K, 3), ints(M, N, 4)
+dA, dB, db = tmg.linear_backward(dD, A, B, preact=pre, activation="relu")
+tmg.check()
+dz = torch.where(pre > 0, dD, 0).double()
+assert torch.equal(dA, (dz @ B.double()).to(torch.bfloat16)), "dA"
+assert torch.equal(dB, (dz.T @ A.double()).to(torch.bfloat16)), "dB"
+assert torch.equal(db.double(), dz.sum(0)), "dbias"
+"""
+
+
+# every branch of the gradient's choice: integers, so all three results are exact
+@pytest.mark.parametrize("size,dA,dB", [
+    ((1024, 4096, 4096), "product", "gemm"),         # dA's tiles do not fill the pairs
+    ((8191, 4096, 4096), "gemm", "wgrad"),           # the longest side is the rows; dz in chunks of 128 rows
+    ((2048, 4096, 4096), "gemm", "gemm"),
+    ((2048, 8192, 4096), "product", "gemm"),         # a contraction of more than 4096 columns
+    ((2560, 2048, 2560), "gemm", "gemm stream-K"),
+    ((2048, 4104, 4104), "product", "wgrad"),        # rows that begin inside a sector
+    ((48, 4096, 8192), "product", "wgrad"),          # less than 64 rows
+    ((255, 4096, 20480), "product", "gemm"),         # less than 256 rows
+])
+def test_every_branch_of_the_dense_gradient_is_exact(size, dA, dB):
+    M, N, K = size
+    lines = log_of(GRADIENT.format(size=size))
+    gemm = [line for line in lines if "tc2_gemm_kernel" in line and "read in place" in line]
+    taken = {"product": any(f"dense: {M} rows, N={K} K={N} " in line for line in lines),
+             "gemm": any(f"bf16 {M}x{K}x{N} " in line for line in gemm)}
+    assert taken[dA], lines
+    taken = {"wgrad": any(f"weight gradient: {M} rows, N={N} K={K} " in line for line in lines),
+             "gemm": any(f"bf16 {N}x{K}x{M} " in line for line in gemm),
+             "gemm stream-K": any(f"bf16 {N}x{K}x{M} " in line and "+ 0 stream-K" not in line for line in gemm)}
+    assert taken[dB], lines
