@@ -31,3 +31,11 @@ def test_kernels_settle_after_giving_up():
                               ("split_kernel.cuh", "settle(full,", "settle(done,")):
         text = flat(name)
         assert loads in text and mmas in text, name
+
+
+def test_pieces_are_read_after_the_whole_warp_has_seen_the_arrival():
+    """Between lane 0's acquire and the other lanes' reads stands a barrier of the warp:
+    the shuffle that hands out the count orders no memory."""
+    body = read("pieces.cuh").split("bool last_arrival(")[1].split("template")[0]
+    before, after = body.split("atom.add.acq_rel.gpu")
+    assert "__syncwarp()" in before and "__syncwarp()" in after.split("__shfl_sync")[0]

@@ -9,7 +9,8 @@ namespace tmg {
 
 // A warp has stored its piece of a split tile: arrive on the tile's counter;
 // true for the last of `others` + 1 arrivals, which then sees every piece.  The
-// warp's stores are ordered by the syncwarp and lane 0's cumulative fence.
+// warp's stores come before lane 0's release by the first syncwarp, its lanes' reads
+// of the pieces after lane 0's acquire by the second (a shuffle orders no memory).
 __device__ __forceinline__ bool last_arrival(uint32_t *counter, int others, bool ok)
 {
     uint32_t old = 0;
@@ -19,6 +20,7 @@ __device__ __forceinline__ bool last_arrival(uint32_t *counter, int others, bool
         if (old == static_cast<uint32_t>(others))
             *counter = 0;
     }
+    __syncwarp();
     return __shfl_sync(0xffffffffu, old, 0) == static_cast<uint32_t>(others) && others >= 0;
 }
 
