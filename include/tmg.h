@@ -312,7 +312,7 @@ tmg_status tmg_gemm_skinny_noalloc(const void *A, const void *B, void *D,
  *
  * Workspace of these calls and of tmg_linear is per (device, stream) and grown
  * on demand, so a call that needs more than the ones before must not come
- * inside a stream capture: make it once outside.  A captured graph stays valid
+ * inside a stream capture (a relaxed one excepted): make it once outside.  A captured graph stays valid
  * when later calls grow the workspace (what a capture has seen is kept until
  * tmg_shutdown), calls of the other GEMM paths included.  Host threads may call on one stream at the same time: each
  * call's kernels follow one another.  Graphs hold the workspace of the stream

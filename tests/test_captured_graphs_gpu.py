@@ -85,3 +85,29 @@ def test_graphs_survive_growing_workspaces(tmg, monkeypatch):
                 assert torch.equal(a, b), n
         assert all(bool((t == 7).all()) for t in others)
     tmg.check(s)
+
+
+def test_first_call_inside_a_relaxed_capture(tmg):
+    """The tile counters are made while the stream is captured; a call outside the graph
+    comes before its first replay."""
+    torch.cuda.synchronize()
+    tmg.shutdown()
+    A, B = ints((1000, 4096), 20), ints((5120, 4096), 21)
+    want = tmg.linear(A, B)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        D, one = torch.empty_like(want), torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s, capture_error_mode="relaxed"):
+            tmg.linear(A, B, D)
+        tmg.linear(A, B, one)
+        for _ in range(2):
+            D.zero_()
+            g.replay()
+        s.synchronize()
+        assert torch.equal(one, want) and torch.equal(D, want)
+        again = tmg.linear(A, B)
+        s.synchronize()
+    assert torch.equal(again, want)
+    tmg.check(s)

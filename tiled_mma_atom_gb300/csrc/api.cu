@@ -366,6 +366,24 @@ StreamLock::StreamLock(cudaStream_t s)
     mu_->lock();
 }
 
+// Zero new counters before what follows on `s`.  While `s` is captured (a relaxed
+// capture: others refuse the allocation), a memset on it would be a node of the
+// graph, and calls before its first replay would find what the memory held: then on
+// a stream of its own.
+static cudaError_t zero_now(void *p, size_t bytes, cudaStream_t s, cudaStreamCaptureStatus capture)
+{
+    if (capture == cudaStreamCaptureStatusNone)
+        return cudaMemsetAsync(p, 0, bytes, s);
+    cudaStream_t own = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e != cudaSuccess)
+        return e;
+    if ((e = cudaMemsetAsync(p, 0, bytes, own)) == cudaSuccess)
+        e = cudaStreamSynchronize(own);
+    cudaStreamDestroy(own);
+    return e;
+}
+
 void *workspace(Workspace which, size_t bytes, cudaStream_t s, tmg_status *st)
 try {
     int dev = 0;
@@ -403,7 +421,7 @@ try {
             *st = cuda_fail(e, "cudaMalloc(workspace)");
             return nullptr;
         }
-        if (is_counters(which) && (e = cudaMemsetAsync(fresh, 0, size, s)) != cudaSuccess) {
+        if (is_counters(which) && (e = zero_now(fresh, size, s, capture)) != cudaSuccess) {
             cudaFree(fresh);
             *st = cuda_fail(e, "cudaMemsetAsync(counters)");
             return nullptr;
