@@ -459,8 +459,8 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
 
 /* Synchronise `stream`, then report: TMG_ERR_CUDA for a sticky or pending
  * CUDA error, TMG_ERR_TIMEOUT if a kernel's bounded wait ran out since the
- * last check (the device error word is cleared and the tile counters in the
- * workspaces are reset), else TMG_OK. */
+ * last check (the device is synchronised, its error word cleared and the tile
+ * counters in the workspaces reset), else TMG_OK. */
 tmg_status tmg_check(void *stream);
 
 /* Message for the calling thread's last non-OK status ("" if none).  The

@@ -67,3 +67,28 @@ def test_threads_on_one_stream(tmg, stream):
     assert not errors, errors
     assert not bad, bad
     tmg.check()
+
+
+def test_check_after_a_timeout_leaves_other_streams_alone(tmg):
+    """A wait that ran out on one stream: the check resets the tile counters only when
+    the calls under way on another have finished."""
+    g = torch.Generator().manual_seed(9)
+    A, B = (torch.randint(-2, 3, s, generator=g).float().to(BF16).to(DEV) for s in ((1000, 4096), (5120, 4096)))
+    want = tmg.linear(A, B)
+    busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        outs = [torch.empty_like(want) for _ in range(60)]
+        tmg.linear(A, B, outs[0])
+        busy.synchronize()
+        for rounds in range(20):
+            for D in outs:
+                tmg.linear(A, B, D)
+    tmg.debug_wait_timeout(1000, stream=other)
+    with pytest.raises(tmg.TmgError, match="TIMEOUT"):
+        tmg.check(other)
+    with torch.cuda.stream(busy):
+        outs.append(tmg.linear(A, B))
+    busy.synchronize()
+    assert all(torch.equal(D, want) for D in outs)
+    tmg.check()

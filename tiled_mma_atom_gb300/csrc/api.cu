@@ -1411,6 +1411,7 @@ tmg_status tmg_check(void *stream)
         return cuda_fail(e, "reading the device error word");
     if (w != 0) {
         const bool bounds = (w & kErrBounds) != 0;
+        cudaDeviceSynchronize();      // other streams' kernels may be using the counters
         cudaMemset(ds->err_word, 0, sizeof w);
         int dev = 0;
         cudaGetDevice(&dev);
