@@ -43,6 +43,25 @@ def test_wgrad_without_rows_is_zero_whatever_the_workspace_holds(tmg):
     assert (dB == 0).all()
 
 
+@pytest.mark.parametrize("R", [5, 300, 4000])
+@pytest.mark.parametrize("gather", [False, True])
+def test_no_group_has_rows(tmg, R, gather):
+    """What the routing leaves when every token is masked: rows, and none in a group."""
+    N, K, E = 264, 136, 6
+    A, B, d = ints((R, K), 12).to(DEV), ints((E, N, K), 13).to(DEV), ints((R, N), 14).to(DEV)
+    r = tmg.moe_route(torch.full((R, E), -math.inf, device=DEV), 1)
+    assert not r.offsets.any() and (r.rows == -1).all() and (r.slots == -1).all()
+    rows = r.rows if gather else None
+    for act, cols, pre in (("none", N, None), ("swiglu", N // 2, None), ("swiglu_grad", 2 * N, torch.ones(R, 2 * N, dtype=BF16, device=DEV))):
+        D = torch.full((R, cols), 7.5, dtype=BF16, device=DEV)
+        tmg.grouped_gemm(A, B, r.offsets, D, rows=rows, activation=act, preact=pre)
+        assert (D == 7.5).all()
+    assert not tmg.grouped_gemm_wgrad(d, A, r.offsets, rows=rows).any()
+    out = tmg.moe_combine(A, r.slots, r.weights, residual=A)
+    assert torch.equal(out, A)
+    tmg.check()
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 264, 64), (900, 1000, 200), (5, 24, 0)])
 def test_linear_relu_keeps_nan(tmg, M, N, K):
     """relu(NaN) is NaN, of -inf 0, of +inf +inf, in every kernel of the product."""
