@@ -3,6 +3,11 @@
 // bias gradient, the column sums of the fp32 dz (before that rounding), added
 // up in a fixed order: rows of a chunk by one thread, then the chunks.
 //
+// dz is rounded because the products' tensor instructions take bf16: dA and dB are
+// then off by 0.0023 of their size, against 0.0017 with dz held in fp32 (8191 x 4096
+// x 4096, GELU; the results' own rounding is 0.0017 of it).  With activation none dz
+// is dD itself and nothing is rounded.
+//
 // Bound by its 6 bytes an element.  A thread keeps four rows' loads in flight:
 // with one, the gradient of an 8191 x 4096 x 4096 product with GELU (dz 41 us of
 // it) took 347 us and takes 342.

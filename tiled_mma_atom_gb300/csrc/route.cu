@@ -476,8 +476,8 @@ __device__ __forceinline__ uint4 load_packed8(const __nv_bfloat16 *row, int64_t 
 
 // Both kernels are bound by HBM: every Y row is read or written once.  A thread
 // keeps the k rows' loads of its eight columns in flight together (KMAX: the
-// next of 2, 4, 8, 16 choices).  8191 tokens of 8 choices, 4096 columns: 109 us
-// (6.2 TB/s, of measured 6.8), the gradient 171 (6.6 TB/s).
+// next of 2, 4, 8, 16 choices).  8191 tokens of 8 choices, 4096 columns: 104 -
+// 109 us (6.2 - 6.5 TB/s, of measured 6.8), the gradient 169 - 172 (6.6 - 6.8 TB/s).
 constexpr int kCombineThreads = 128;
 
 template <bool VEC, int KMAX>
