@@ -111,3 +111,28 @@ def test_first_call_inside_a_relaxed_capture(tmg):
         s.synchronize()
     assert torch.equal(again, want)
     tmg.check(s)
+
+
+def test_growth_inside_a_relaxed_capture(tmg):
+    """A call inside the capture outgrows what one before it left, and one inside it
+    again: the old buffers are kept, and the capture stays valid."""
+    torch.cuda.synchronize()
+    tmg.shutdown()
+    sets = [(ints((n, 201), 30 + n)[:, 1:], ints((3 * n, 201), 31 + n)[:, 1:]) for n in (50, 300, 900)]
+    want = [tmg.linear(A, B) for A, B in sets]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        outs = [torch.empty_like(w) for w in want]
+        tmg.linear(*sets[0], outs[0])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s, capture_error_mode="relaxed"):
+            for (A, B), D in zip(sets, outs):
+                tmg.linear(A, B, D)
+        for _ in range(2):
+            for D in outs:
+                D.zero_()
+            g.replay()
+        s.synchronize()
+    assert all(torch.equal(D, w) for D, w in zip(outs, want))
+    tmg.check(s)

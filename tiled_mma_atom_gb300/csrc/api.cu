@@ -397,20 +397,20 @@ try {
         capture = cudaStreamCaptureStatusActive;
     }
     if (sc.ws_bytes[which] < bytes) {
-        // A CUDA graph captured earlier on this stream may name the old buffer: it
-        // then stays until tmg_shutdown.  Growing by half at least keeps what is
-        // kept below twice the largest.
-        if (sc.ws[which] && sc.ws_captured[which]) {
-            g_retired.push_back(Retired{dev, which, sc.ws[which], sc.ws_bytes[which]});
+        // A CUDA graph captured on this stream, earlier or just now, may name the old
+        // buffer: it then stays until tmg_shutdown.  Growing by half at least keeps
+        // what is kept below twice the largest.
+        const bool keep = sc.ws[which] && (sc.ws_captured[which] || capture != cudaStreamCaptureStatusNone);
+        const size_t half_more = sc.ws_bytes[which] + sc.ws_bytes[which] / 2;
+        size_t size = bytes > half_more ? bytes : half_more;
+        if (keep) {
+            g_retired.reserve(g_retired.size() + 1);
         } else if (sc.ws[which]) {
             cudaStreamSynchronize(s);
             cudaFree(sc.ws[which]);
+            sc.ws[which] = nullptr;
+            sc.ws_bytes[which] = 0;
         }
-        const size_t half_more = sc.ws_bytes[which] + sc.ws_bytes[which] / 2;
-        size_t size = bytes > half_more ? bytes : half_more;
-        sc.ws[which] = nullptr;
-        sc.ws_bytes[which] = 0;
-        sc.ws_captured[which] = false;
         void *fresh = nullptr;
         if ((e = cudaMalloc(&fresh, size)) == cudaErrorMemoryAllocation && size > bytes) {
             cudaGetLastError();
@@ -426,6 +426,9 @@ try {
             *st = cuda_fail(e, "cudaMemsetAsync(counters)");
             return nullptr;
         }
+        if (keep)
+            g_retired.push_back(Retired{dev, which, sc.ws[which], sc.ws_bytes[which]});
+        sc.ws_captured[which] = false;
         sc.ws[which] = fresh;
         sc.ws_bytes[which] = size;
     }
