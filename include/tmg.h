@@ -457,6 +457,75 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
                                float *dbias, int64_t M, int64_t N, int64_t K,
                                tmg_activation activation, void *stream);
 
+/* The whole expert layer in one call:
+ *   z = x[t] . W1[e]^T (2 F columns), h = silu(z[f]) * z[F + f],
+ *   out[t] = bf16(residual[t] + sum_j w[t, j] * W2[e[t, j]] . h),
+ * with experts e and weights w as tmg_moe_route chooses them from the logits.
+ * Sums are fp32; h is rounded to bf16. */
+typedef struct {
+    const void *x;          /* device, bf16 (T, H), row stride ldx */
+    const void *logits;     /* device, (T, E) of logits_dtype, row stride ld_logits (>= E) */
+    const void *W1;         /* device, bf16 (E, 2 F, H) contiguous */
+    const void *W2;         /* device, bf16 (E, H, F) contiguous */
+    const void *residual;   /* bf16 (T, H), row stride ld_residual, or NULL; may be out */
+    void *out;              /* bf16 (T, H), row stride ld_out (>= H) */
+    int64_t T, H, F, E, k;  /* 1 <= E <= 1024, 1 <= k <= min(16, E); T * k < 2^31 */
+    int64_t ldx, ld_logits, ld_residual, ld_out;
+    tmg_dtype logits_dtype; /* TMG_F32 or TMG_BF16 */
+    int normalize;          /* as for tmg_moe_route */
+} tmg_moe_args;
+
+tmg_status tmg_moe_layer(const tmg_moe_args *args, void *stream);
+
+/* ------------------------------------------- projections with adapters
+ *
+ * Rows of many requests share a projection, and each row may add the low-rank
+ * adapter of its request, a = adapters[m]:
+ *   u[m] = bf16(scales[a] * x[m] . A[a]^T);
+ *   D[m] = bf16(x[m] . W^T + u[m] . B[a]^T + bias + residual[m]).
+ * A row whose adapter is not one of 0 .. L - 1 (-1, say) has u = 0 and adds
+ * nothing: what another row's adapter holds, infinities and NaN too, never
+ * reaches it.  Rows of one request are best adjacent: the time grows with the
+ * number of different adapters in 128 or 256 rows in a row. */
+typedef struct {
+    const void *x;          /* device, bf16 (M, K), row stride ldx */
+    const void *W;          /* device, bf16 (N, K), row stride ldw */
+    const void *A;          /* device, bf16 (L, r, K) contiguous */
+    const void *B;          /* device, bf16 (L, N, r) contiguous */
+    void *D;                /* device, bf16 (M, N), row stride ldd */
+    const int32_t *adapters;/* device, int32 (M) */
+    const float *scales;    /* device, fp32 (L) or NULL (ones) */
+    const float *bias;      /* device, fp32 (N) or NULL */
+    const void *residual;   /* bf16 (M, N), row stride ld_residual, or NULL; may be D */
+    void *u;                /* bf16 (M, r) contiguous, for the gradient, or NULL */
+    int64_t M, N, K, r, L;  /* 1 <= r <= 256, 1 <= L <= 1024 */
+    int64_t ldx, ldw, ldd, ld_residual;
+} tmg_lora_args;
+
+tmg_status tmg_lora_linear(const tmg_lora_args *args, void *stream);
+
+/* Its gradients, with W frozen:
+ *   dU[m] = bf16(scales[a] * dD[m] . B[a]);  dx = bf16(dD . W + dU . A[a]);
+ *   dA[l] = sum over the rows m of adapter l of dU[m]^T x[m];
+ *   dB[l] = sum over them of dD[m]^T u[m];
+ * zeros for an adapter without rows.  The residual's gradient is dD; W's and the
+ * bias's are tmg_linear_backward's.  Sums are fp32 and in a fixed order. */
+typedef struct {
+    const void *dD;         /* device, bf16 (M, N), row stride ldd */
+    const void *x, *W;      /* as above; x may be NULL without dA, W without dx */
+    const void *A, *B;      /* as above; A may be NULL without dx */
+    const int32_t *adapters;
+    const float *scales;
+    const void *u;          /* bf16 (M, r) contiguous, as tmg_lora_linear left it; NULL without dB */
+    void *dx;               /* bf16 (M, K) contiguous, or NULL */
+    void *dA;               /* bf16 (L, r, K) contiguous, or NULL */
+    void *dB;               /* bf16 (L, N, r) contiguous, or NULL */
+    int64_t M, N, K, r, L;
+    int64_t ldd, ldx, ldw;
+} tmg_lora_grad_args;
+
+tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *args, void *stream);
+
 /* Synchronise `stream`, then report: TMG_ERR_CUDA for a sticky or pending
  * CUDA error, TMG_ERR_TIMEOUT if a kernel's bounded wait ran out since the
  * last check (the device is synchronised, its error word cleared and the tile

@@ -26,7 +26,8 @@ PATHS = {"auto": 0, "ffma": 1, "tc": 2, "skinny": 3, "skinny_ffma": 4, "tc_singl
 EXPORTS = ("tmg_gemm", "tmg_gemm_ex", "tmg_gemm_host", "tmg_gemm_fused", "tmg_gemm_w4a8",
            "tmg_gemm_w4a8_preshuffled", "tmg_w4a8_preshuffle", "tmg_w4a8_preshuffled_bytes", "tmg_gemm_mxfp4", "tmg_gemm_skinny_noalloc",
            "tmg_moe_route", "tmg_moe_route_backward", "tmg_moe_combine", "tmg_moe_combine_backward",
-           "tmg_grouped_gemm", "tmg_grouped_gemm_wgrad", "tmg_linear", "tmg_linear_backward", "tmg_check", "tmg_last_error",
+           "tmg_grouped_gemm", "tmg_grouped_gemm_wgrad", "tmg_linear", "tmg_linear_backward", "tmg_moe_layer",
+           "tmg_lora_linear", "tmg_lora_linear_backward", "tmg_check", "tmg_last_error",
            "tmg_set_wait_budget_ns", "tmg_debug_wait_timeout", "tmg_debug_bounds_probe", "tmg_debug_build",
            "tmg_launch_count",
            "tmg_version", "tmg_shutdown")
@@ -61,10 +62,25 @@ class LinearArgs(ctypes.Structure):           # tmg_linear_args
                        "M N K lda a_col b_row b_col ldd ld_residual ld_preact", "in_dtype activation")
 
 
-# The same two structs as bytes, which pass for a pointer to them: filling a
+class MoeArgs(ctypes.Structure):              # tmg_moe_args
+    _fields_ = _struct("x logits W1 W2 residual out", "T H F E k ldx ld_logits ld_residual ld_out", "logits_dtype normalize")
+
+
+class LoraArgs(ctypes.Structure):             # tmg_lora_args
+    _fields_ = _struct("x W A B D adapters scales bias residual u", "M N K r L ldx ldw ldd ld_residual", "")
+
+
+class LoraGradArgs(ctypes.Structure):         # tmg_lora_grad_args
+    _fields_ = _struct("dD x W A B adapters scales u dx dA dB", "M N K r L ldd ldx ldw", "")
+
+
+# The same structs as bytes, which pass for a pointer to them: filling a
 # ctypes structure costs the host 1 us more of about 10 a call.
 pack_grouped = struct.Struct("8Q12q2i").pack
 pack_linear = struct.Struct("8Q10q2i").pack
+pack_moe = struct.Struct("6Q9q2i").pack
+pack_lora = struct.Struct("10Q9q").pack
+pack_lora_grad = struct.Struct("11Q8q").pack
 
 
 def make_layout(shape, stride) -> Layout:
@@ -138,6 +154,9 @@ def lib():
                        ("tmg_grouped_gemm", [P, P]),
                        ("tmg_grouped_gemm_wgrad", [P, I64, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, P]),
                        ("tmg_linear", [P, P]),
+                       ("tmg_moe_layer", [P, P]),
+                       ("tmg_lora_linear", [P, P]),
+                       ("tmg_lora_linear_backward", [P, P]),
                        ("tmg_linear_backward", [P, I64, P, I64, P, I64, P, I64, P, P, P, I64, I64, I64, I, P])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = I

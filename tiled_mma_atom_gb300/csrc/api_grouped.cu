@@ -4,49 +4,17 @@
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
-#include <exception>
 
 #include "act.cuh"
 #include "grouped.h"
 #include "host.h"
+#include "product.h"
 #include "split.h"
 #include "swap_kernel.cuh"
 #include "wgrad.h"
 
 namespace tmg {
 namespace {
-
-constexpr int64_t kMax31 = (int64_t{1} << 31) - 1;
-
-// No C++ exception leaves a C entry point.
-template <class F>
-tmg_status guarded(F &&body)
-{
-    try {
-        clear_error();
-        return body();
-    } catch (const std::exception &x) {
-        return fail(TMG_ERR_CUDA, "host error: %s", x.what());
-    } catch (...) {
-        return fail(TMG_ERR_CUDA, "host error");
-    }
-}
-
-tmg_status launched(cudaError_t e, const char *what) { return e == cudaSuccess ? TMG_OK : cuda_fail(e, what); }
-
-// (a - 1) * b + ... of a strided operand must stay within int64.
-bool extents_ok(int64_t rows, int64_t row_stride, int64_t cols, int64_t col_stride, int64_t outer = 1, int64_t outer_stride = 0)
-{
-    if (row_stride < 0 || col_stride < 0 || outer_stride < 0)
-        return false;
-    const __int128 off = static_cast<__int128>(rows > 0 ? rows - 1 : 0) * row_stride +
-                         static_cast<__int128>(cols > 0 ? cols - 1 : 0) * col_stride +
-                         static_cast<__int128>(outer > 0 ? outer - 1 : 0) * outer_stride;
-    return off < (static_cast<__int128>(1) << 60);
-}
-
-// An output's rows must not overlap.
-bool out_rows_ok(int64_t rows, int64_t cols, int64_t ld) { return rows <= 1 || ld >= cols; }
 
 // Common checks of both products; the launch follows in run_product.
 tmg_status check_product(const GroupedArgs &a)
@@ -62,23 +30,8 @@ tmg_status check_product(const GroupedArgs &a)
     return TMG_OK;
 }
 
-bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-// Whether TMA reads a (rows, cols) operand of `elem`-byte elements in place:
-// 16-byte aligned base and rows, positive strides below 2^40 bytes.
-bool rows_in_place(const void *p, int64_t rows, int64_t row, int64_t cols, int64_t col, int elem)
-{
-    return aligned(p) && cols > 0 && rows > 0 && (cols == 1 || col == 1) &&
-           (rows == 1 || (row > 0 && row * elem % 16 == 0 && row * elem < (int64_t{1} << 40)));
-}
-
-// A stride for a dimension of extent 1, where the caller's says nothing.
-int64_t stride_or(int64_t extent, int64_t stride, int64_t least) { return extent > 1 ? stride : least; }
-
-int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-// Copy an operand of E blocks (rows, K) to workspace `which` at `offset`
-// bytes of `total`.
 tmg_status pack(const DeviceState &ds, Workspace which, Pack3Args a, int elem, size_t total, int64_t offset, cudaStream_t s,
                 char **out)
 {
@@ -93,6 +46,8 @@ tmg_status pack(const DeviceState &ds, Workspace which, Pack3Args a, int elem, s
     *out = ws;
     return TMG_OK;
 }
+
+namespace {
 
 // The tile counter and the arrival counters of split tiles, zero between
 // launches.
@@ -218,6 +173,8 @@ SplitPlan split_plan(const GroupedArgs &a, int64_t F, bool swiglu, int64_t num_k
     }
     return best;
 }
+
+}  // namespace
 
 tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t s)
 {
@@ -400,7 +357,6 @@ tmg_status run_product(const DeviceState &ds, const GroupedArgs &a, cudaStream_t
     return launched(launch_swap(p, epi, a.e4m3, ds.num_sms, err_ctx(ds), s), "grouped product launch");
 }
 
-// a.R > 0.
 tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
 {
     tmg_status st;
@@ -462,7 +418,6 @@ tmg_status run_wgrad(const DeviceState &ds, const WgradArgs &a, cudaStream_t s)
     return launched(launch_wgrad(p, ds.num_sms, err_ctx(ds), s), "grouped weight gradient launch");
 }
 
-}  // namespace
 }  // namespace tmg
 
 using namespace tmg;

@@ -1,0 +1,339 @@
+// api_layers.cu — C ABI of the calls that run several products: the whole expert
+// layer, and the dense product with low-rank adapters (include/tmg.h).
+#include <algorithm>
+#include <cstring>
+
+#include "act.cuh"
+#include "lora.h"
+#include "product.h"
+
+namespace tmg {
+namespace {
+
+// Pieces of one workspace, 256-byte aligned.
+struct Pieces {
+    size_t bytes = 0;
+    size_t take(size_t n)
+    {
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    }
+};
+
+// The layer by the separate operators: plan, up products, down products, sum.
+tmg_status moe_by_groups(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
+{
+    tmg_status st;
+    const int64_t R = g.T * g.k;
+    Pieces p;
+    const size_t weights = p.take(R * 4), experts = p.take(R * 4), offsets = p.take((g.E + 1) * 4), rows = p.take(R * 4),
+                 slots = p.take(R * 4), hidden = p.take(R * up(g.F, 8) * 2), answers = p.take(R * up(g.H, 8) * 2);
+    char *ws = static_cast<char *>(workspace(kWsLayer, p.bytes, s, &st));
+    if (!ws)
+        return st;
+    RouteArgs r{};
+    r.logits = g.logits;
+    r.bf16 = g.logits_dtype == TMG_BF16;
+    r.T = g.T;
+    r.ld = g.ld_logits;
+    r.E = static_cast<int>(g.E);
+    r.k = static_cast<int>(g.k);
+    r.normalize = g.normalize != 0;
+    r.weights = reinterpret_cast<float *>(ws + weights);
+    r.experts = reinterpret_cast<int32_t *>(ws + experts);
+    r.offsets = reinterpret_cast<int32_t *>(ws + offsets);
+    r.rows = reinterpret_cast<int32_t *>(ws + rows);
+    r.slots = reinterpret_cast<int32_t *>(ws + slots);
+    r.counts = static_cast<uint16_t *>(workspace(kWsRoute, route_counts_bytes(g.T, r.E, ds.num_sms), s, &st));
+    if (!r.counts)
+        return st;
+    if ((st = launched(launch_route(r, ds.num_sms, s), "routing launch")) != TMG_OK)
+        return st;
+    GroupedArgs a{};
+    a.R = R;
+    a.E = g.E;
+    a.b_col = a.a_col = 1;
+    a.offsets = r.offsets;
+    if (g.F > 0) {
+        a.A = g.x;
+        a.B = g.W1;
+        a.D = ws + hidden;
+        a.T = g.T;
+        a.N = 2 * g.F;
+        a.K = a.b_row = g.H;
+        a.lda = g.ldx;
+        a.ldd = up(g.F, 8);
+        a.b_expert = 2 * g.F * g.H;
+        a.rows = r.rows;
+        a.epi.act = kActSwiglu;
+        if ((st = run_product(ds, a, s)) != TMG_OK)
+            return st;
+    }
+    a.A = ws + hidden;
+    a.B = g.W2;
+    a.D = ws + answers;
+    a.T = R;
+    a.N = g.H;
+    a.K = a.b_row = g.F;
+    a.lda = up(g.F, 8);
+    a.ldd = up(g.H, 8);
+    a.b_expert = g.H * g.F;
+    a.rows = nullptr;
+    a.epi.act = kActNone;
+    if ((st = run_product(ds, a, s)) != TMG_OK)
+        return st;
+    return launched(launch_combine(CombineArgs{a.D, r.slots, r.weights, g.residual, g.out, g.T, g.H, R, a.ldd, g.ld_residual,
+                                               g.ld_out, r.k},
+                                   s),
+                    "combine launch");
+}
+
+// D = x . W^T + U . F[adapters]^T + bias + residual.  The factors' own strides are
+// their contiguous ones; across: W is (K, N), F (L, r, N), as the input's gradient has
+// them.
+struct AdaptedArgs {
+    const void *x, *W, *U, *F;
+    void *D;
+    const int32_t *adapters;
+    const float *bias;
+    const void *residual;
+    int64_t M, N, K, r, L;
+    int64_t ldx, ldw, ldu, ldd, ld_residual;
+    bool across;
+};
+
+tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t s)
+{
+    tmg_status st;
+    LoraPairArgs p;
+    std::memset(&p, 0, sizeof p);
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int64_t K = a.K > 0 ? a.K : 8;       // an empty contraction is one of zeros
+    const int pairs = ds.num_sms / 2;
+    static const int wide[] = {256, 128};
+    const int bn = a.across ? tc2_pick_bn_of(a.M, a.N, K, 64, ds.num_sms, wide, 2) : tc2_pick_bn(a.M, a.N, K, ds.num_sms);
+    if ((a.M + 255) / 256 * ((a.N + bn - 1) / bn) > kMax31)
+        return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
+    char *ws = nullptr;
+    const void *x = a.x, *W = a.W, *F = a.F;
+    int64_t ldx = stride_or(a.M, a.ldx, up(K, 8)), ldw = a.ldw;
+    if (!rows_in_place(x, a.M, a.ldx, a.K, 1, 2)) {
+        ldx = up(K, 8);
+        if ((st = pack(ds, kWsPackA, Pack3Args{x, nullptr, 1, a.M, a.K, 0, a.ldx, 1, a.M, ldx, 0}, 2, a.M * ldx * 2, 0, s,
+                       &ws)) != TMG_OK)
+            return st;
+        x = ws;
+    }
+    const int64_t wrows = a.across ? a.K : a.N, wcols = a.across ? a.N : a.K, wmin = a.across ? K : a.N;
+    if (!rows_in_place(W, wrows, a.ldw, wcols, 1, 2)) {
+        ldw = up(wcols > 0 ? wcols : 8, 8);
+        if ((st = pack(ds, kWsPackB, Pack3Args{W, nullptr, 1, wrows, wcols, 0, a.ldw, 1, wmin, ldw, 0}, 2, wmin * ldw * 2, 0, s,
+                       &ws)) != TMG_OK)
+            return st;
+        W = ws;
+    }
+    ldw = stride_or(wmin, ldw, up(a.across ? a.N : K, 8));
+    const int64_t frows = a.across ? a.r : a.N, fcols = a.across ? a.N : a.r;
+    int64_t ldf = fcols;
+    if (!rows_in_place(F, a.L * frows, ldf, fcols, 1, 2)) {
+        ldf = up(fcols, 8);
+        if ((st = pack(ds, kWsFactor, Pack3Args{F, nullptr, 1, a.L * frows, fcols, 0, fcols, 1, a.L * frows, ldf, 0}, 2,
+                       a.L * frows * ldf * 2, 0, s, &ws)) != TMG_OK)
+            return st;
+        F = ws;
+    }
+    const int64_t xd[2] = {K, a.M}, xs[1] = {ldx * 2}, ud[2] = {a.r, a.M}, us[1] = {a.ldu * 2};
+    const int rows[2] = {64, 128}, half[3] = {64, a.across ? 64 : bn / 2, 1};
+    const int64_t wd[2] = {a.across ? a.N : K, a.across ? K : a.N}, wst[1] = {ldw * 2};
+    const int64_t fd[3] = {fcols, frows, a.L}, fs[2] = {ldf * 2, frows * ldf * 2};
+    if ((st = encode_nd(&p.tmX, bf16, 2, x, xd, xs, rows, true)) != TMG_OK ||
+        (st = encode_nd(&p.tmU, bf16, 2, a.U, ud, us, rows, true)) != TMG_OK ||
+        (st = encode_nd(&p.tmW, bf16, 2, W, wd, wst, half, true)) != TMG_OK ||
+        (st = encode_nd(&p.tmF, bf16, 3, F, fd, fs, half, true)) != TMG_OK)
+        return st;
+    TcArgs t;
+    std::memset(&t, 0, sizeof t);
+    t.M = p.M = static_cast<int>(a.M);
+    t.N = p.N = static_cast<int>(a.N);
+    t.K = p.K = static_cast<int>(K);
+    t.bn = bn;
+    tc2_plan(t, ds.num_sms);
+    p.dp_tiles = t.dp_tiles;
+    p.sk_tiles = t.sk_tiles;
+    p.group_m = t.group_m;
+    if (t.sk_tiles > 0) {
+        p.partials = static_cast<float *>(workspace(kWsPartials, tc2_partials_bytes(t), s, &st));
+        if (!p.partials)
+            return st;
+        p.counters = static_cast<uint32_t *>(workspace(kWsCounters, (32 + static_cast<size_t>(pairs) * 32) * sizeof(uint32_t), s, &st));
+        if (!p.counters)
+            return st;
+        p.counters += 32;
+    }
+    p.D = a.D;
+    p.adapters = a.adapters;
+    p.bias = a.bias;
+    p.residual = a.residual;
+    p.ldd = a.ldd;
+    p.ld_residual = a.ld_residual;
+    p.L = static_cast<int>(a.L);
+    p.r = static_cast<int>(a.r);
+    p.vec_ok = a.ldd % 8 == 0 && aligned(a.D);
+    log_choice("bf16 with adapters: %d rows, N=%d K=%d rank %d -> lora_pair_kernel: 256 x %d tiles, weights %s", p.M, p.N, p.K,
+               p.r, bn, a.across ? "MN-major" : "K-major");
+    return launched(launch_lora_pair(p, bn, a.across, t.pairs, err_ctx(ds), s), "product with adapters launch");
+}
+
+// Limits of the adapters' extents and pointers, common to both directions.
+tmg_status check_lora(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
+{
+    if (M < 0 || N < 0 || K < 0 || r < 1 || r > 256 || L < 1 || L > 1024)
+        return fail(TMG_ERR_INVALID_ARG, "adapters need M, N, K >= 0, 1 <= rank <= 256 and 1 <= L <= 1024 (M=%lld N=%lld K=%lld "
+                    "rank=%lld L=%lld)", (long long)M, (long long)N, (long long)K, (long long)r, (long long)L);
+    if (M > kMax31 || N > kMax31 || K > kMax31 || M * ((std::max(N, K) + 255) / 256) > kMax31)
+        return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+    return TMG_OK;
+}
+
+}  // namespace
+}  // namespace tmg
+
+using namespace tmg;
+
+extern "C" {
+
+tmg_status tmg_moe_layer(const tmg_moe_args *g, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (!g)
+            return fail(TMG_ERR_INVALID_ARG, "null argument struct");
+        if (g->logits_dtype != TMG_F32 && g->logits_dtype != TMG_BF16)
+            return fail(TMG_ERR_INVALID_ARG, "logits are fp32 or bf16 (dtype %d)", (int)g->logits_dtype);
+        if (g->T < 0 || g->H < 0 || g->F < 0 || g->E < 1 || g->E > 1024 || g->k < 1 || g->k > 16 || g->k > g->E)
+            return fail(TMG_ERR_INVALID_ARG, "the expert layer needs T, H, F >= 0, 1 <= E <= 1024 and 1 <= k <= min(16, E) "
+                        "(T=%lld H=%lld F=%lld E=%lld k=%lld)", (long long)g->T, (long long)g->H, (long long)g->F,
+                        (long long)g->E, (long long)g->k);
+        if (g->T > kMax31 / 16 || g->H > kMax31 || g->F > kMax31 / 2 || g->T * ((g->H + 1023) / 1024) > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+        if (g->T > 1 && g->ld_logits < g->E)
+            return fail(TMG_ERR_INVALID_ARG, "row stride %lld of the logits below E=%lld", (long long)g->ld_logits,
+                        (long long)g->E);
+        if (!extents_ok(g->T, g->ldx, g->H, 1) || !extents_ok(g->T, g->residual ? g->ld_residual : 0, g->H, 1) ||
+            !extents_ok(g->T, g->ld_out, g->H, 1) || !out_rows_ok(g->T, g->H, g->ld_out) ||
+            !extents_ok(g->E, 1, 1, 1, 2 * g->F, g->H > 0 ? g->H * g->E : 0))
+            return fail(TMG_ERR_INVALID_ARG, "row strides out of range (the output's must be at least H)");
+        if (g->T == 0 || g->H == 0)
+            return TMG_OK;
+        if (!g->logits || !g->out || !g->x || (g->F > 0 && (!g->W1 || !g->W2)))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        tmg_status st;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const StreamLock lock(s);
+        return moe_by_groups(*ds, *g, s);
+    });
+}
+
+tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (!g)
+            return fail(TMG_ERR_INVALID_ARG, "null argument struct");
+        tmg_status st;
+        if ((st = check_lora(g->M, g->N, g->K, g->r, g->L)) != TMG_OK)
+            return st;
+        if (!extents_ok(g->M, g->ldx, g->K, 1) || !extents_ok(g->N, g->ldw, g->K, 1) || !extents_ok(g->M, g->ldd, g->N, 1) ||
+            !out_rows_ok(g->M, g->N, g->ldd) || (g->residual && !extents_ok(g->M, g->ld_residual, g->N, 1)))
+            return fail(TMG_ERR_INVALID_ARG, "row stride of x, W, D or residual out of range");
+        if (g->M == 0)
+            return TMG_OK;
+        if (!g->adapters || (g->K > 0 && (!g->x || !g->A)) || (g->N > 0 && (!g->D || !g->B || (g->K > 0 && !g->W))))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer");
+        DeviceState *ds = nullptr;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const StreamLock lock(s);
+        const int64_t ldu = g->u && g->r % 8 == 0 && aligned(g->u) ? g->r : up(g->r, 8);
+        void *u = g->u;
+        if (!u || ldu != g->r || !aligned(u)) {
+            u = workspace(kWsLayer, g->M * ldu * 2, s, &st);
+            if (!u)
+                return st;
+        }
+        RankArgs k{g->x, g->A, g->adapters, g->scales, u, g->M, g->K, g->L, g->ldx, ldu, static_cast<int>(g->r), false};
+        if ((st = launched(launch_lora_rank(k, s), "adapter rank launch")) != TMG_OK)
+            return st;
+        if (g->u && u != g->u) {               // the caller's own, in its layout
+            k.U = g->u;
+            k.ldu = g->r;
+            if ((st = launched(launch_lora_rank(k, s), "adapter rank launch")) != TMG_OK)
+                return st;
+        }
+        if (g->N == 0)
+            return TMG_OK;
+        return run_adapted(*ds,
+                           AdaptedArgs{g->x, g->W, u, g->B, g->D, g->adapters, g->bias, g->residual, g->M, g->N, g->K, g->r,
+                                       g->L, g->ldx, g->ldw, ldu, g->ldd, g->ld_residual, false},
+                           s);
+    });
+}
+
+tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *g, void *stream)
+{
+    return guarded([&]() -> tmg_status {
+        if (!g)
+            return fail(TMG_ERR_INVALID_ARG, "null argument struct");
+        tmg_status st;
+        if ((st = check_lora(g->M, g->N, g->K, g->r, g->L)) != TMG_OK)
+            return st;
+        if (!extents_ok(g->M, g->ldd, g->N, 1) || !extents_ok(g->M, g->ldx, g->K, 1) || !extents_ok(g->N, g->ldw, g->K, 1))
+            return fail(TMG_ERR_INVALID_ARG, "row stride of dD, x or W out of range");
+        const bool in = g->M > 0;
+        if ((in && !g->adapters) || (in && g->N > 0 && !g->dD))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer (adapters or dD)");
+        if (in && g->N > 0 && ((g->dx && g->K > 0 && (!g->W || !g->A || !g->B)) || (g->dA && g->K > 0 && (!g->x || !g->B)) ||
+                               (g->dB && !g->u)))
+            return fail(TMG_ERR_INVALID_ARG, "null pointer: dx needs W, A and B, dA needs x and B, dB needs u");
+        DeviceState *ds = nullptr;
+        if ((st = device_state(&ds)) != TMG_OK)
+            return st;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const StreamLock lock(s);
+        const int64_t ldu = up(g->r, 8);
+        char *ws = static_cast<char *>(workspace(kWsLayer, std::max<int64_t>(g->M, 1) * ldu * 2, s, &st));
+        if (!ws)
+            return st;
+        const int r = static_cast<int>(g->r);
+        void *dU = ws;
+        if (in && (g->dx || g->dA) && g->K > 0 &&
+            (st = launched(launch_lora_rank(RankArgs{g->dD, g->B, g->adapters, g->scales, dU, g->M, g->N, g->L, g->ldd, ldu, r,
+                                                     true},
+                                            s),
+                           "adapter rank launch")) != TMG_OK)
+            return st;
+        if (g->dA && g->K > 0 &&
+            (st = launched(launch_lora_factor_grad(FactorGradArgs{g->x, dU, g->adapters, g->dA, g->M, g->K, g->L, g->ldx, ldu,
+                                                                  r, false},
+                                                   s),
+                           "adapter gradient launch")) != TMG_OK)
+            return st;
+        if (g->dB && g->N > 0 &&
+            (st = launched(launch_lora_factor_grad(FactorGradArgs{g->dD, g->u, g->adapters, g->dB, g->M, g->N, g->L, g->ldd,
+                                                                  g->r, r, true},
+                                                   s),
+                           "adapter gradient launch")) != TMG_OK)
+            return st;
+        if (!g->dx || !in || g->K == 0)
+            return TMG_OK;
+        return run_adapted(*ds,
+                           AdaptedArgs{g->dD, g->W, dU, g->A, g->dx, g->adapters, nullptr, nullptr, g->M, g->K, g->N, g->r,
+                                       g->L, g->ldd, g->ldw, ldu, g->K, 0, true},
+                           s);
+    });
+}
+
+}  // extern "C"

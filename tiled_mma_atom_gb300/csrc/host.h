@@ -51,6 +51,8 @@ enum Workspace {
     kWsCounters,       // arrival counters: zero on entry, zero again on exit
     kWsRoute,          // per-block expert counts of the routing plan
     kWsGrad,           // dz of the dense product's gradient and its column partials
+    kWsFactor,         // adapters' factors with 16-byte rows
+    kWsLayer,          // what the expert layer and the products with adapters keep between their kernels
     // the other GEMM paths, which the dense product's gradient takes too
     kWsTc2Partials,    // pair kernel: stream-K partial tiles and tile counters
     kWsTc2Counters,

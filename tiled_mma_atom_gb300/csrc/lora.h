@@ -1,0 +1,53 @@
+// lora.h — arguments of the kernels of dense projections with low-rank adapters.
+#pragma once
+
+#include "internal.h"
+
+namespace tmg {
+
+// U[m][j] = bf16(scales[a] sum_c X[m][c] F[a][j][c]) with a = adapters[m], or, `across`,
+// of F[a][c][j]; zeros where a is not one of 0 .. L - 1.  F is contiguous per
+// adapter, (r, C) or (C, r).
+struct RankArgs {
+    const void *X, *F;
+    const int32_t *adapters;
+    const float *scales;       // (L) or null (ones)
+    void *U;                   // bf16 (M, r), row stride ldu
+    int64_t M, C, L, ldx, ldu;
+    int r;
+    bool across;
+};
+cudaError_t launch_lora_rank(const RankArgs &a, cudaStream_t s);
+
+// D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] on CTA pairs, or with
+// W (K, N) and F (L, r, N) given along their rows (`maj`).
+struct LoraPairArgs {
+    CUtensorMap tmX, tmU;      // (M, K), (M, r): boxes of 128 rows of 64
+    CUtensorMap tmW;           // (N, K): bn / 2 rows of 64; maj: (K, N), 64 x 64
+    CUtensorMap tmF;           // (L, N, r): bn / 2 rows of 64; maj: (L, r, N), 64 x 64
+    void *D;
+    const int32_t *adapters;
+    const float *bias;         // or null
+    const void *residual;      // or null
+    int64_t ldd, ld_residual;
+    int M, N, K, L, r;
+    int vec_ok;                // rows of D are 16-byte aligned
+    int dp_tiles, sk_tiles, group_m;   // tc2_plan's
+    float *partials;
+    uint32_t *counters;
+};
+cudaError_t launch_lora_pair(const LoraPairArgs &a, int bn, bool maj, int pairs, const ErrCtx &err, cudaStream_t s);
+
+// G[l] = sum over the rows m with adapters[m] == l of Z[m]^T Y[m], (r, C), or, `across`, its
+// transpose (C, r); contiguous, zeros for an adapter without rows.
+struct FactorGradArgs {
+    const void *Y, *Z;         // bf16 (M, C), (M, r), row strides ldy, ldz
+    const int32_t *adapters;
+    void *G;
+    int64_t M, C, L, ldy, ldz;
+    int r;
+    bool across;
+};
+cudaError_t launch_lora_factor_grad(const FactorGradArgs &a, cudaStream_t s);
+
+}  // namespace tmg
