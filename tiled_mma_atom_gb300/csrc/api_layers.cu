@@ -89,17 +89,72 @@ tmg_status moe_by_groups(const DeviceState &ds, const tmg_moe_args &g, cudaStrea
                     "combine launch");
 }
 
+// Rows of `cols` elements that TMA can read: in place, or copied to workspace `which`
+// (rows_p rows, the ones past `rows` zeros).
+struct Rows {
+    const void *p;
+    int64_t ld;
+};
+tmg_status tma_rows(const DeviceState &ds, Workspace which, const void *src, int64_t ld, int64_t rows, int64_t cols,
+                    int64_t rows_p, cudaStream_t s, Rows *out)
+{
+    const int64_t least = up(std::max<int64_t>(cols, 1), 8);
+    if (rows_in_place(src, rows, ld, cols, 1, 2)) {
+        *out = Rows{src, stride_or(rows, ld, least)};
+        return TMG_OK;
+    }
+    char *ws = nullptr;
+    const tmg_status st = pack(ds, which, Pack3Args{src, nullptr, 1, rows, cols, 0, ld, 1, rows_p, least, 0}, 2,
+                               rows_p * least * 2, 0, s, &ws);
+    *out = Rows{ws, least};
+    return st;
+}
+
+// Rows by which the tensor cores take the ranks' side over, from more than these on.
+constexpr int64_t kRankRows = 64;
+
+// U = bf16(scales X . F[adapters]^T), (M, r) with rows of ldu; x: X's rows as tma_rows
+// gave them where M > kRankRows.
+tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cudaStream_t s)
+{
+    if (a.M <= kRankRows || a.C == 0)
+        return launched(launch_lora_rank(a, s), "adapter rank launch");
+    tmg_status st;
+    const int64_t rows = a.across ? a.C : a.r, cols = a.across ? a.r : a.C;
+    Rows f;
+    if ((st = tma_rows(ds, kWsFactor, a.F, cols, a.L * rows, cols, a.L * rows, s, &f)) != TMG_OK)
+        return st;
+    LoraRankArgs p;
+    std::memset(&p, 0, sizeof p);
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int64_t xd[2] = {a.C, a.M}, xs[1] = {x.ld * 2}, fd[3] = {cols, rows, a.L}, fs[2] = {f.ld * 2, rows * f.ld * 2};
+    const int xbox[2] = {64, 128}, fbox[3] = {64, a.across ? 64 : (a.r + 15) & ~15, 1};
+    if ((st = encode_nd(&p.tmX, bf16, 2, x.p, xd, xs, xbox)) != TMG_OK ||
+        (st = encode_nd(&p.tmF, bf16, 3, f.p, fd, fs, fbox, true)) != TMG_OK)
+        return st;
+    p.adapters = a.adapters;
+    p.scales = a.scales;
+    p.U = a.U;
+    p.ldu = a.ldu;
+    p.M = static_cast<int>(a.M);
+    p.C = static_cast<int>(a.C);
+    p.L = static_cast<int>(a.L);
+    p.r = a.r;
+    return launched(launch_lora_rank_tc(p, a.across, ds.num_sms, err_ctx(ds), s), "adapter rank launch");
+}
+
 // D = x . W^T + U . F[adapters]^T + bias + residual.  The factors' own strides are
 // their contiguous ones; across: W is (K, N), F (L, r, N), as the input's gradient has
 // them.
 struct AdaptedArgs {
-    const void *x, *W, *U, *F;
+    Rows x;                    // as tma_rows gave them
+    const void *W, *U, *F;
     void *D;
     const int32_t *adapters;
     const float *bias;
     const void *residual;
     int64_t M, N, K, r, L;
-    int64_t ldx, ldw, ldu, ldd, ld_residual;
+    int64_t ldw, ldu, ldd, ld_residual;
     bool across;
 };
 
@@ -115,42 +170,21 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     const int bn = a.across ? tc2_pick_bn_of(a.M, a.N, K, 64, ds.num_sms, wide, 2) : tc2_pick_bn(a.M, a.N, K, ds.num_sms);
     if ((a.M + 255) / 256 * ((a.N + bn - 1) / bn) > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
-    char *ws = nullptr;
-    const void *x = a.x, *W = a.W, *F = a.F;
-    int64_t ldx = stride_or(a.M, a.ldx, up(K, 8)), ldw = a.ldw;
-    if (!rows_in_place(x, a.M, a.ldx, a.K, 1, 2)) {
-        ldx = up(K, 8);
-        if ((st = pack(ds, kWsPackA, Pack3Args{x, nullptr, 1, a.M, a.K, 0, a.ldx, 1, a.M, ldx, 0}, 2, a.M * ldx * 2, 0, s,
-                       &ws)) != TMG_OK)
-            return st;
-        x = ws;
-    }
-    const int64_t wrows = a.across ? a.K : a.N, wcols = a.across ? a.N : a.K, wmin = a.across ? K : a.N;
-    if (!rows_in_place(W, wrows, a.ldw, wcols, 1, 2)) {
-        ldw = up(wcols > 0 ? wcols : 8, 8);
-        if ((st = pack(ds, kWsPackB, Pack3Args{W, nullptr, 1, wrows, wcols, 0, a.ldw, 1, wmin, ldw, 0}, 2, wmin * ldw * 2, 0, s,
-                       &ws)) != TMG_OK)
-            return st;
-        W = ws;
-    }
-    ldw = stride_or(wmin, ldw, up(a.across ? a.N : K, 8));
+    Rows W, f;
+    const int64_t wrows = a.across ? a.K : a.N, wcols = a.across ? a.N : a.K;
+    if ((st = tma_rows(ds, kWsPackB, a.W, a.ldw, wrows, wcols, a.across ? K : a.N, s, &W)) != TMG_OK)
+        return st;
     const int64_t frows = a.across ? a.r : a.N, fcols = a.across ? a.N : a.r;
-    int64_t ldf = fcols;
-    if (!rows_in_place(F, a.L * frows, ldf, fcols, 1, 2)) {
-        ldf = up(fcols, 8);
-        if ((st = pack(ds, kWsFactor, Pack3Args{F, nullptr, 1, a.L * frows, fcols, 0, fcols, 1, a.L * frows, ldf, 0}, 2,
-                       a.L * frows * ldf * 2, 0, s, &ws)) != TMG_OK)
-            return st;
-        F = ws;
-    }
-    const int64_t xd[2] = {K, a.M}, xs[1] = {ldx * 2}, ud[2] = {a.r, a.M}, us[1] = {a.ldu * 2};
+    if ((st = tma_rows(ds, kWsFactor, a.F, fcols, a.L * frows, fcols, a.L * frows, s, &f)) != TMG_OK)
+        return st;
+    const int64_t xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2}, ud[2] = {a.r, a.M}, us[1] = {a.ldu * 2};
     const int rows[2] = {64, 128}, half[3] = {64, a.across ? 64 : bn / 2, 1};
-    const int64_t wd[2] = {a.across ? a.N : K, a.across ? K : a.N}, wst[1] = {ldw * 2};
-    const int64_t fd[3] = {fcols, frows, a.L}, fs[2] = {ldf * 2, frows * ldf * 2};
-    if ((st = encode_nd(&p.tmX, bf16, 2, x, xd, xs, rows, true)) != TMG_OK ||
+    const int64_t wd[2] = {a.across ? a.N : K, a.across ? K : a.N}, wst[1] = {W.ld * 2};
+    const int64_t fd[3] = {fcols, frows, a.L}, fs[2] = {f.ld * 2, frows * f.ld * 2};
+    if ((st = encode_nd(&p.tmX, bf16, 2, a.x.p, xd, xs, rows, true)) != TMG_OK ||
         (st = encode_nd(&p.tmU, bf16, 2, a.U, ud, us, rows, true)) != TMG_OK ||
-        (st = encode_nd(&p.tmW, bf16, 2, W, wd, wst, half, true)) != TMG_OK ||
-        (st = encode_nd(&p.tmF, bf16, 3, F, fd, fs, half, true)) != TMG_OK)
+        (st = encode_nd(&p.tmW, bf16, 2, W.p, wd, wst, half, true)) != TMG_OK ||
+        (st = encode_nd(&p.tmF, bf16, 3, f.p, fd, fs, half, true)) != TMG_OK)
         return st;
     TcArgs t;
     std::memset(&t, 0, sizeof t);
@@ -264,20 +298,23 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
             if (!u)
                 return st;
         }
+        Rows x;
+        if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK)
+            return st;
         RankArgs k{g->x, g->A, g->adapters, g->scales, u, g->M, g->K, g->L, g->ldx, ldu, static_cast<int>(g->r), false};
-        if ((st = launched(launch_lora_rank(k, s), "adapter rank launch")) != TMG_OK)
+        if ((st = run_rank(*ds, k, x, s)) != TMG_OK)
             return st;
         if (g->u && u != g->u) {               // the caller's own, in its layout
             k.U = g->u;
             k.ldu = g->r;
-            if ((st = launched(launch_lora_rank(k, s), "adapter rank launch")) != TMG_OK)
+            if ((st = run_rank(*ds, k, x, s)) != TMG_OK)
                 return st;
         }
         if (g->N == 0)
             return TMG_OK;
         return run_adapted(*ds,
-                           AdaptedArgs{g->x, g->W, u, g->B, g->D, g->adapters, g->bias, g->residual, g->M, g->N, g->K, g->r,
-                                       g->L, g->ldx, g->ldw, ldu, g->ldd, g->ld_residual, false},
+                           AdaptedArgs{x, g->W, u, g->B, g->D, g->adapters, g->bias, g->residual, g->M, g->N, g->K, g->r,
+                                       g->L, g->ldw, ldu, g->ldd, g->ld_residual, false},
                            s);
     });
 }
@@ -309,11 +346,11 @@ tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *g, void *stream)
             return st;
         const int r = static_cast<int>(g->r);
         void *dU = ws;
+        Rows d{};
         if (in && (g->dx || g->dA) && g->K > 0 &&
-            (st = launched(launch_lora_rank(RankArgs{g->dD, g->B, g->adapters, g->scales, dU, g->M, g->N, g->L, g->ldd, ldu, r,
-                                                     true},
-                                            s),
-                           "adapter rank launch")) != TMG_OK)
+            ((st = tma_rows(*ds, kWsPackA, g->dD, g->ldd, g->M, g->N, g->M, s, &d)) != TMG_OK ||
+             (st = run_rank(*ds, RankArgs{g->dD, g->B, g->adapters, g->scales, dU, g->M, g->N, g->L, g->ldd, ldu, r, true}, d,
+                            s)) != TMG_OK))
             return st;
         if (g->dA && g->K > 0 &&
             (st = launched(launch_lora_factor_grad(FactorGradArgs{g->x, dU, g->adapters, g->dA, g->M, g->K, g->L, g->ldx, ldu,
@@ -330,8 +367,8 @@ tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *g, void *stream)
         if (!g->dx || !in || g->K == 0)
             return TMG_OK;
         return run_adapted(*ds,
-                           AdaptedArgs{g->dD, g->W, dU, g->A, g->dx, g->adapters, nullptr, nullptr, g->M, g->K, g->N, g->r,
-                                       g->L, g->ldd, g->ldw, ldu, g->K, 0, true},
+                           AdaptedArgs{d, g->W, dU, g->A, g->dx, g->adapters, nullptr, nullptr, g->M, g->K, g->N, g->r, g->L,
+                                       g->ldw, ldu, g->K, 0, true},
                            s);
     });
 }

@@ -19,6 +19,20 @@ struct RankArgs {
 };
 cudaError_t launch_lora_rank(const RankArgs &a, cudaStream_t s);
 
+// The same on the tensor cores.
+struct LoraRankArgs {
+    CUtensorMap tmX;           // (M, C): 128 rows of 64
+    CUtensorMap tmF;           // (L, r, C): r rounded up to 16 rows of 64; maj: (L, C, r), 64 x 64
+    const int32_t *adapters;
+    const float *scales;
+    void *U;
+    int64_t ldu;
+    int M, C, L, r;
+    // set by the launch
+    int cluster, chunk, block_bytes, stages, stage_bytes, ring_bytes, tmem_cols;
+};
+cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const ErrCtx &err, cudaStream_t s);
+
 // D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] on CTA pairs, or with
 // W (K, N) and F (L, r, N) given along their rows (`maj`).
 struct LoraPairArgs {
