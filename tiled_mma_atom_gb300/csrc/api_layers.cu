@@ -143,6 +143,47 @@ tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cud
     return launched(launch_lora_rank_tc(p, a.across, ds.num_sms, err_ctx(ds), s), "adapter rank launch");
 }
 
+// Arrival counters, zero between launches (the tile feed's counter comes before
+// them).
+tmg_status lora_counters(size_t n, cudaStream_t s, uint32_t **out)
+{
+    tmg_status st;
+    *out = static_cast<uint32_t *>(workspace(kWsCounters, (32 + n) * sizeof(uint32_t), s, &st));
+    if (*out)
+        *out += 32;
+    return st;
+}
+
+// G = the factors' gradient from Y (M, C) and Z (M, r), rows as tma_rows gave them.
+tmg_status run_factor_grad(const DeviceState &ds, const Rows &Y, int64_t C, const Rows &Z, int64_t M, int64_t L, int64_t r,
+                           const int32_t *offsets, const int32_t *rows, void *G, bool across, cudaStream_t s)
+{
+    tmg_status st;
+    LoraGradArgs p;
+    std::memset(&p, 0, sizeof p);
+    for (int i = 0; i < 3; ++i) {
+        const int64_t yd[2] = {C, M}, ys[1] = {Y.ld * 2}, zd[2] = {r, M}, zs[1] = {Z.ld * 2};
+        const int box[2] = {64, i == 0 ? 64 : i == 1 ? 16 : 1};
+        if ((st = encode_nd(&p.tmY[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y.p, yd, ys, box)) != TMG_OK ||
+            (st = encode_nd(&p.tmZ[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Z.p, zd, zs, box, true)) != TMG_OK)
+            return st;
+    }
+    p.G = G;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.M = static_cast<int>(M);
+    p.C = static_cast<int>(C);
+    p.L = static_cast<int>(L);
+    p.r = static_cast<int>(r);
+    p.across = across;
+    p.partials = static_cast<float *>(workspace(kWsPartials, lora_grad_partial_bytes(M, C, p.r, ds.num_sms), s, &st));
+    if (!p.partials)
+        return st;
+    if ((st = lora_counters(lora_grad_counters(M, C, ds.num_sms), s, &p.counters)) != TMG_OK)
+        return st;
+    return launched(launch_lora_grad(p, ds.num_sms, err_ctx(ds), s), "adapter gradient launch");
+}
+
 // D = x . W^T + U . F[adapters]^T + bias + residual.  The factors' own strides are
 // their contiguous ones; across: W is (K, N), F (L, r, N), as the input's gradient has
 // them.
@@ -165,7 +206,6 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     std::memset(&p, 0, sizeof p);
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t K = a.K > 0 ? a.K : 8;       // an empty contraction is one of zeros
-    const int pairs = ds.num_sms / 2;
     static const int wide[] = {256, 128};
     const int bn = a.across ? tc2_pick_bn_of(a.M, a.N, K, 64, ds.num_sms, wide, 2) : tc2_pick_bn(a.M, a.N, K, ds.num_sms);
     if ((a.M + 255) / 256 * ((a.N + bn - 1) / bn) > kMax31)
@@ -200,10 +240,8 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
         p.partials = static_cast<float *>(workspace(kWsPartials, tc2_partials_bytes(t), s, &st));
         if (!p.partials)
             return st;
-        p.counters = static_cast<uint32_t *>(workspace(kWsCounters, (32 + static_cast<size_t>(pairs) * 32) * sizeof(uint32_t), s, &st));
-        if (!p.counters)
+        if ((st = lora_counters(tc2_counters_bytes(t) / sizeof(uint32_t), s, &p.counters)) != TMG_OK)
             return st;
-        p.counters += 32;
     }
     p.D = a.D;
     p.adapters = a.adapters;
@@ -340,34 +378,59 @@ tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *g, void *stream)
             return st;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const StreamLock lock(s);
+        const bool want_a = g->dA && g->K > 0, want_b = g->dB && g->N > 0;
+        if (!in || g->N == 0) {                // no row, or no gradient of any
+            if (want_a && (st = launched(cudaMemsetAsync(g->dA, 0, static_cast<size_t>(g->L) * g->r * g->K * 2, s),
+                                         "cudaMemsetAsync(dA)")) != TMG_OK)
+                return st;
+            if (want_b && (st = launched(cudaMemsetAsync(g->dB, 0, static_cast<size_t>(g->L) * g->r * g->N * 2, s),
+                                         "cudaMemsetAsync(dB)")) != TMG_OK)
+                return st;
+            return g->dx && in && g->K > 0 ? launched(cudaMemsetAsync(g->dx, 0, static_cast<size_t>(g->M) * g->K * 2, s),
+                                                      "cudaMemsetAsync(dx)")
+                                           : TMG_OK;
+        }
         const int64_t ldu = up(g->r, 8);
-        char *ws = static_cast<char *>(workspace(kWsLayer, std::max<int64_t>(g->M, 1) * ldu * 2, s, &st));
+        const int r = static_cast<int>(g->r), L = static_cast<int>(g->L);
+        Pieces p;
+        const size_t du_at = p.take(g->M * ldu * 2), names = p.take(g->M * 4), slots = p.take(g->M * 4), rows = p.take(g->M * 4),
+                     offsets = p.take((g->L + 1) * 4);
+        char *ws = static_cast<char *>(workspace(kWsLayer, p.bytes, s, &st));
         if (!ws)
             return st;
-        const int r = static_cast<int>(g->r);
-        void *dU = ws;
-        Rows d{};
-        if (in && (g->dx || g->dA) && g->K > 0 &&
-            ((st = tma_rows(*ds, kWsPackA, g->dD, g->ldd, g->M, g->N, g->M, s, &d)) != TMG_OK ||
-             (st = run_rank(*ds, RankArgs{g->dD, g->B, g->adapters, g->scales, dU, g->M, g->N, g->L, g->ldd, ldu, r, true}, d,
-                            s)) != TMG_OK))
+        const Rows dU{ws + du_at, ldu};
+        RouteArgs plan{};
+        if (want_a || want_b) {
+            plan.T = g->M;
+            plan.E = L;
+            plan.k = 1;
+            plan.experts = reinterpret_cast<int32_t *>(ws + names);
+            plan.slots = reinterpret_cast<int32_t *>(ws + slots);
+            plan.rows = reinterpret_cast<int32_t *>(ws + rows);
+            plan.offsets = reinterpret_cast<int32_t *>(ws + offsets);
+            plan.counts = static_cast<uint16_t *>(workspace(kWsRoute, row_plan_counts_bytes(g->M, L, ds->num_sms), s, &st));
+            if (!plan.counts)
+                return st;
+            if ((st = launched(launch_row_plan(g->adapters, plan, ds->num_sms, s), "row plan launch")) != TMG_OK)
+                return st;
+        }
+        Rows d, x, u;
+        if ((st = tma_rows(*ds, kWsPackA, g->dD, g->ldd, g->M, g->N, g->M, s, &d)) != TMG_OK)
             return st;
-        if (g->dA && g->K > 0 &&
-            (st = launched(launch_lora_factor_grad(FactorGradArgs{g->x, dU, g->adapters, g->dA, g->M, g->K, g->L, g->ldx, ldu,
-                                                                  r, false},
-                                                   s),
-                           "adapter gradient launch")) != TMG_OK)
+        if (want_b && ((st = tma_rows(*ds, kWsGather, g->u, g->r, g->M, g->r, g->M, s, &u)) != TMG_OK ||
+                       (st = run_factor_grad(*ds, d, g->N, u, g->M, g->L, g->r, plan.offsets, plan.rows, g->dB, true, s)) != TMG_OK))
             return st;
-        if (g->dB && g->N > 0 &&
-            (st = launched(launch_lora_factor_grad(FactorGradArgs{g->dD, g->u, g->adapters, g->dB, g->M, g->N, g->L, g->ldd,
-                                                                  g->r, r, true},
-                                                   s),
-                           "adapter gradient launch")) != TMG_OK)
+        if ((want_a || (g->dx && g->K > 0)) &&
+            (st = run_rank(*ds, RankArgs{g->dD, g->B, g->adapters, g->scales, ws + du_at, g->M, g->N, g->L, g->ldd, ldu, r, true},
+                           d, s)) != TMG_OK)
             return st;
-        if (!g->dx || !in || g->K == 0)
+        if (want_a && ((st = tma_rows(*ds, kWsGather, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK ||
+                       (st = run_factor_grad(*ds, x, g->K, dU, g->M, g->L, g->r, plan.offsets, plan.rows, g->dA, false, s)) != TMG_OK))
+            return st;
+        if (!g->dx || g->K == 0)
             return TMG_OK;
         return run_adapted(*ds,
-                           AdaptedArgs{d, g->W, dU, g->A, g->dx, g->adapters, nullptr, nullptr, g->M, g->K, g->N, g->r, g->L,
+                           AdaptedArgs{d, g->W, dU.p, g->A, g->dx, g->adapters, nullptr, nullptr, g->M, g->K, g->N, g->r, g->L,
                                        g->ldw, ldu, g->K, 0, true},
                            s);
     });

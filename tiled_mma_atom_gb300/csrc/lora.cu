@@ -57,45 +57,11 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(RankArgs a)
     }
 }
 
-// A block per adapter, 256 columns and eight ranks; every thread walks all rows.
-__global__ void __launch_bounds__(kThreads) factor_grad_kernel(FactorGradArgs a)
-{
-    grid_release();
-    grid_wait();
-    const int64_t l = blockIdx.z, c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int j0 = blockIdx.y * 8;
-    float sum[8] = {};
-    for (int64_t m = 0; m < a.M; ++m) {
-        if (a.adapters[m] != l || c >= a.C)
-            continue;
-        const float y = bf(a.Y, m * a.ldy + c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (j0 + i < a.r)
-                sum[i] = fmaf(bf(a.Z, m * a.ldz + j0 + i), y, sum[i]);
-    }
-    if (c >= a.C)
-        return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (j0 + i < a.r)
-            static_cast<__nv_bfloat16 *>(a.G)[l * a.C * a.r + (a.across ? c * a.r + j0 + i : (j0 + i) * a.C + c)] =
-                __float2bfloat16_rn(sum[i]);
-}
-
 }  // namespace
 
 cudaError_t launch_lora_rank(const RankArgs &a, cudaStream_t s)
 {
     return launch_overlapped(rank_kernel, dim3(static_cast<unsigned>(a.M)), kThreads, 0, 1, s, a);
-}
-
-cudaError_t launch_lora_factor_grad(const FactorGradArgs &a, cudaStream_t s)
-{
-    return launch_overlapped(factor_grad_kernel,
-                             dim3(static_cast<unsigned>((a.C + kThreads - 1) / kThreads), static_cast<unsigned>((a.r + 7) / 8),
-                                  static_cast<unsigned>(a.L)),
-                             kThreads, 0, 1, s, a);
 }
 
 }  // namespace tmg

@@ -52,16 +52,20 @@ struct LoraPairArgs {
 };
 cudaError_t launch_lora_pair(const LoraPairArgs &a, int bn, bool maj, int pairs, const ErrCtx &err, cudaStream_t s);
 
-// G[l] = sum over the rows m with adapters[m] == l of Z[m]^T Y[m], (r, C), or, `across`, its
-// transpose (C, r); contiguous, zeros for an adapter without rows.
-struct FactorGradArgs {
-    const void *Y, *Z;         // bf16 (M, C), (M, r), row strides ldy, ldz
-    const int32_t *adapters;
+// G[l] = sum over the rows m of adapter l of Z[m]^T Y[m], (L, r, C), or, `across`, its
+// transpose (L, C, r); contiguous, zeros for an adapter without rows.  Adapter l's rows
+// are rows[offsets[l]] .. rows[offsets[l + 1] - 1].
+struct LoraGradArgs {
+    CUtensorMap tmY[3], tmZ[3];        // (M, C), (M, r): boxes of 64 columns by 64, 16 and one rows
     void *G;
-    int64_t M, C, L, ldy, ldz;
-    int r;
-    bool across;
+    const int32_t *offsets, *rows;
+    int M, C, L, r, across;
+    float *partials;                   // lora_grad_partial_bytes()
+    uint32_t *counters;                // lora_grad_counters(), zero between launches
+    int runs, stages, stage_bytes, tmem_cols;     // set by the launch
 };
-cudaError_t launch_lora_factor_grad(const FactorGradArgs &a, cudaStream_t s);
+size_t lora_grad_partial_bytes(int64_t M, int64_t C, int r, int num_sms);
+size_t lora_grad_counters(int64_t M, int64_t C, int num_sms);
+cudaError_t launch_lora_grad(LoraGradArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 }  // namespace tmg

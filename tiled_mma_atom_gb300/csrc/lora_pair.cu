@@ -21,6 +21,7 @@
 // Cut tiles: the piece with the last K block also takes the adapters' blocks.
 #include "feed.cuh"
 #include "launch.cuh"
+#include "lora.cuh"
 #include "lora.h"
 #include "pieces.cuh"
 #include "staging.cuh"
@@ -30,7 +31,6 @@ namespace tmg {
 namespace {
 
 constexpr int kLpThreads = 320;
-constexpr int kNone = 0x7fffffff;
 
 template <int BN>
 struct LoraCfg {
@@ -39,54 +39,6 @@ struct LoraCfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 218 * 1024 / STAGE_BYTES > 8 ? 8 : 218 * 1024 / STAGE_BYTES;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 16;
-};
-
-// One pair MMA that updates the rows (lanes) whose bit in `off` is clear.
-__device__ __forceinline__ void mma_bf16_pair_masked_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                       const uint32_t (&off)[8])
-{
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.eq.b32 p, 0, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]), "r"(off[5]),
-        "r"(off[6]), "r"(off[7])
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
-// The adapters of a tile's rows: lane i has those of rows 32 w + i.
-struct TileAdapters {
-    int id[8];
-
-    __device__ __forceinline__ void read(const LoraPairArgs &p, int tm, int lane)
-    {
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            const int64_t m = static_cast<int64_t>(tm) * kBM + 32 * w + lane;
-            const int l = m < p.M ? p.adapters[m] : -1;
-            id[w] = l >= 0 && l < p.L ? l : kNone;
-        }
-    }
-    // The smallest above `last`; kNone after the largest.
-    __device__ __forceinline__ int next(int last) const
-    {
-        int least = kNone;
-#pragma unroll
-        for (int w = 0; w < 8; ++w)
-            least = id[w] > last ? min(least, id[w]) : least;
-        return __reduce_min_sync(0xffffffffu, least);
-    }
 };
 
 template <int BN, bool MAJ>
@@ -140,7 +92,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
     SegWalk walk(cluster, nclusters, p.dp_tiles, p.sk_tiles, num_kb);
     int tile, kb0, kb1, slot, tm, tn;
     bool partial;
-    TileAdapters of;
+    RowAdapters<8> of;
 
     if (warp == 0) {
         // ---------------------------------------------- TMA producer
@@ -168,7 +120,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             tile_coords(tile, tiles_m, tiles_n, p.group_m, tm, tn);
             const int a_row = tm * kBM + static_cast<int>(rank) * kHalfM, b_row = tn * BN + static_cast<int>(rank) * (BN / 2);
             if (kb1 == num_kb)
-                of.read(p, tm, lane);
+                of.read(p.adapters, static_cast<int64_t>(tm) * kBM, p.M, p.L, lane);
             for (int kb = kb0; kb < kb1; ++kb) {
                 const int at = take();
                 if (at < 0)
@@ -185,7 +137,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             }
             if (!ok || kb1 != num_kb)
                 continue;
-            for (int l = of.next(-1); ok && l != kNone; l = of.next(l))
+            for (int l = of.next(-1); ok && l != kNoAdapter; l = of.next(l))
                 for (int c = 0; c < rank_blocks; ++c) {
                     const int at = take();
                     if (at < 0)
@@ -249,7 +201,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                 ++local;
                 tile_coords(tile, tiles_m, tiles_n, p.group_m, tm, tn);
                 if (kb1 == num_kb)
-                    of.read(p, tm, lane);
+                    of.read(p.adapters, static_cast<int64_t>(tm) * kBM, p.M, p.L, lane);
                 if (!mbar_wait_cluster_warp(&tempty[acc], acc_phase ^ 1u, err, abort_flag, kSiteMmaTmemEmpty))
                     break;
                 tc_fence_after();
@@ -261,11 +213,9 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                     give();
                 }
                 if (ok && kb1 == num_kb)
-                    for (int l = of.next(-1); ok && l != kNone; l = of.next(l)) {
+                    for (int l = of.next(-1); ok && l != kNoAdapter; l = of.next(l)) {
                         uint32_t off[8];
-#pragma unroll
-                        for (int w = 0; w < 8; ++w)
-                            off[w] = ~__ballot_sync(0xffffffffu, of.id[w] == l);
+                        of.others(l, off);
                         for (int c = 0; c < rank_blocks && take(); ++c) {
                             const int steps = min(4, ceil_div(p.r - c * 64, 16));
                             for (int k = 0; k < steps; ++k)

@@ -19,6 +19,7 @@
 // Bound by HBM: X once.
 #include "feed.cuh"
 #include "launch.cuh"
+#include "lora.cuh"
 #include "lora.h"
 #include "staging.cuh"
 #include "tc2_kernel.cuh"
@@ -29,32 +30,8 @@ namespace {
 constexpr int kRkThreads = 192;
 constexpr int kRkRows = 128;
 constexpr int kRkMaxStages = 8;
-constexpr int kRkNone = 0x7fffffff;
 constexpr int kRkBars = (2 * kRkMaxStages + 1) * 8 + 24;      // barriers; TMEM address, abort flag, number of adapters
 constexpr int kRkLists = kRkRows * (16 + 4);                  // masks and numbers of the tile's adapters
-
-// One MMA of the CTA that updates the rows (lanes) whose bit in `off` is clear.
-__device__ __forceinline__ void mma_bf16_masked_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                  const uint4 &off, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %8, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2)
-{
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank)
 {
@@ -104,30 +81,16 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
     grid_wait();
     if (warp == 0) {
         // the tile's adapters, smallest first, and the lanes that each leaves out
-        int id[4], n = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int64_t m = static_cast<int64_t>(row0) + 32 * w + lane;
-            const int l = m < p.M ? p.adapters[m] : -1;
-            id[w] = l >= 0 && l < p.L ? l : kRkNone;
-        }
-        for (int last = -1;;) {
-            int least = kRkNone;
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                least = id[w] > last ? min(least, id[w]) : least;
-            last = __reduce_min_sync(0xffffffffu, least);
-            if (last == kRkNone)
-                break;
+        RowAdapters<4> of;
+        of.read(p.adapters, row0, p.M, p.L, lane);
+        int n = 0;
+        for (int l = of.next(-1); l != kNoAdapter; l = of.next(l), ++n) {
             uint32_t off[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                off[w] = ~__ballot_sync(0xffffffffu, id[w] == last);
+            of.others(l, off);
             if (lane == 0) {
                 masks[n] = make_uint4(off[0], off[1], off[2], off[3]);
-                list[n] = last;
+                list[n] = l;
             }
-            ++n;
         }
         if (lane == 0)
             *count = n;
@@ -155,9 +118,9 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
                     const int l = list[first + i];
                     if constexpr (MAJ) {
                         for (int j = 0; j * 64 < p.r; ++j)
-                            tma_load_3d(sf + j * kMnBoxBytes, &p.tmF, &full[stage], j * 64, kb * 64, l);
+                            tma_load_3d_one(sf + j * kMnBoxBytes, &p.tmF, &full[stage], j * 64, kb * 64, l);
                     } else {
-                        tma_load_3d(sf, &p.tmF, &full[stage], kb * 64, 0, l);
+                        tma_load_3d_one(sf, &p.tmF, &full[stage], kb * 64, 0, l);
                     }
                 }
                 if (++stage == p.stages) {
