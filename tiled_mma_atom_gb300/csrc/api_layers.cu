@@ -5,6 +5,7 @@
 
 #include "act.cuh"
 #include "lora.h"
+#include "moe_few.h"
 #include "product.h"
 
 namespace tmg {
@@ -257,6 +258,50 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     return launched(launch_lora_pair(p, bn, a.across, t.pairs, err_ctx(ds), s), "product with adapters launch");
 }
 
+// The layer in two kernels, for few tokens.
+bool few_tokens(const tmg_moe_args &g)
+{
+    return g.T <= kFewTokens && g.E <= kFewExperts && g.H % 8 == 0 && g.F % 8 == 0 && g.F > 0 && aligned(g.W1) && aligned(g.W2) &&
+           rows_in_place(g.x, g.T, g.ldx, g.H, 1, 2) && g.F * g.H * 4 < (int64_t{1} << 40) && g.F <= kMax31 / 4;
+}
+
+tmg_status moe_few(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
+{
+    tmg_status st;
+    MoeFewArgs p;
+    std::memset(&p, 0, sizeof p);
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int64_t experts = std::min(g.E, g.T * g.k), tp = up(g.T, 16);
+    p.hidden = workspace(kWsLayer, experts * tp * g.F * 2, s, &st);
+    if (!p.hidden)
+        return st;
+    const int64_t d1[3] = {g.H, 2 * g.F, g.E}, s1[2] = {g.H * 2, g.F * g.H * 4};
+    const int64_t d2[3] = {g.F, g.H, g.E}, s2[2] = {g.F * 2, g.F * g.H * 2};
+    const int64_t dx[2] = {g.H, g.T}, sx[1] = {stride_or(g.T, g.ldx, g.H) * 2};
+    const int64_t dh[3] = {g.F, tp, experts}, sh[2] = {g.F * 2, tp * g.F * 2};
+    const int b1[3] = {64, 64, 1}, b2[3] = {64, 128, 1}, bt[3] = {64, static_cast<int>(tp), 1};
+    if ((st = encode_nd(&p.tmW1, bf16, 3, g.W1, d1, s1, b1)) != TMG_OK || (st = encode_nd(&p.tmW2, bf16, 3, g.W2, d2, s2, b2)) != TMG_OK ||
+        (st = encode_nd(&p.tmX, bf16, 2, g.x, dx, sx, bt, true)) != TMG_OK ||
+        (st = encode_nd(&p.tmHidden, bf16, 3, p.hidden, dh, sh, bt, true)) != TMG_OK)
+        return st;
+    p.logits = g.logits;
+    p.W2 = g.W2;
+    p.residual = g.residual;
+    p.out = g.out;
+    p.ld_logits = g.ld_logits;
+    p.ld_residual = g.ld_residual;
+    p.ld_out = g.ld_out;
+    p.T = static_cast<int>(g.T);
+    p.H = static_cast<int>(g.H);
+    p.F = static_cast<int>(g.F);
+    p.E = static_cast<int>(g.E);
+    p.k = static_cast<int>(g.k);
+    p.normalize = g.normalize != 0;
+    p.bf16 = g.logits_dtype == TMG_BF16;
+    p.tp = static_cast<int>(tp);
+    return launched(launch_moe_few(p, ds.num_sms, err_ctx(ds), s), "expert layer launch");
+}
+
 // Limits of the adapters' extents and pointers, common to both directions.
 tmg_status check_lora(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
 {
@@ -305,7 +350,7 @@ tmg_status tmg_moe_layer(const tmg_moe_args *g, void *stream)
             return st;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const StreamLock lock(s);
-        return moe_by_groups(*ds, *g, s);
+        return few_tokens(*g) ? moe_few(*ds, *g, s) : moe_by_groups(*ds, *g, s);
     });
 }
 

@@ -1,0 +1,411 @@
+// moe_few.cu — a whole expert layer for a few tokens, in two kernels: the choice of
+// the experts with the gate and up products and SwiGLU, then the down products with the
+// weighted sum and the residual.
+//
+// With few tokens the layer is the reading of the chosen experts' weights.  Both
+// kernels take 128 weight rows as the MMA's M and all T tokens (padded to tp, a
+// multiple of 16) as its N, for every expert that any token chose: nothing is sorted,
+// gathered or grouped, and a tile needs no more than its expert's number.
+//
+// Choice.  Every CTA chooses all tokens' experts from the logits by itself (a warp per
+// token, route.cuh), which takes it less time than a kernel of its own would.
+//
+// First kernel.  A tile is 64 gate rows and their 64 up rows of one chosen expert.
+// hidden[i][t] = bf16(w[t, e] silu(g) u) for the i-th chosen expert e, zeros for tokens
+// that did not choose it: the weight is folded in, so that
+//
+// the second kernel's sum over experts is one long contraction, out[t] = sum over (i, f)
+// of W2[e_i][:, f] hidden[i][t][f]: a tile of 128 columns of the layer's output
+// accumulates all chosen experts one after another.  A zero times a weight that is
+// infinite or NaN would be NaN in a token that did not choose that expert: where a sum
+// comes out as NaN, it is formed again from the token's own experts alone.
+//
+// Both split a tile's contraction over a cluster of CTAs, whose partial sums meet in
+// shared memory as in split_kernel.cuh.  Two CTAs fit an SM.  The second kernel starts
+// while the first one runs: it chooses the experts itself and fills its ring with
+// W2's first blocks, and only the hidden rows wait for the first kernel's end.  The
+// first one lets it start only after its own wait for the kernel before: so logits and
+// weights are complete by then.
+#include "act.cuh"
+#include "feed.cuh"
+#include "launch.cuh"
+#include "lora.cuh"
+#include "moe_few.h"
+#include "route.cuh"
+#include "staging.cuh"
+
+namespace tmg {
+namespace {
+
+constexpr int kFwThreads = 256;
+constexpr int kFwMaxStages = 8;
+constexpr int kFwRing = 96 * 1024;
+constexpr int kFwWeights = 16384;            // 128 weight rows of a K block
+
+struct FewSmem {
+    uint64_t full[kFwMaxStages], empty[kFwMaxStages], done;
+    uint32_t tmem_slot;
+    int abort, chosen;                       // chosen: experts with a token
+    float weights[kFewTokens * kFewChoices];
+    int32_t experts[kFewTokens * kFewChoices];
+    int32_t counts[kFewExperts];
+    int32_t list[kFewExperts];               // the chosen experts, smallest first
+    uint32_t tokens[kFewExperts][2];         // which tokens chose them
+    float weight[kFewTokens];                // first kernel: of its expert
+};
+
+// All threads: choose the tokens' experts.
+template <int C, bool BF16>
+__device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
+{
+    for (int i = threadIdx.x; i < kFewExperts; i += kFwThreads) {
+        sm.counts[i] = 0;
+        sm.tokens[i][0] = sm.tokens[i][1] = 0;
+    }
+    __syncthreads();
+    RouteArgs r{};
+    r.logits = p.logits;
+    r.T = p.T;
+    r.ld = p.ld_logits;
+    r.E = p.E;
+    r.k = p.k;
+    r.normalize = p.normalize;
+    r.weights = sm.weights;
+    r.experts = sm.experts;
+    choose<C, BF16, true>(r, 0, p.T, sm.counts, nullptr);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + threadIdx.x;
+            const bool on = e < p.E && sm.counts[e] > 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, on);
+            if (on) {
+                const int at = n + __popc(all & ((1u << threadIdx.x) - 1));
+                sm.list[at] = e;
+                sm.counts[e] = at;               // its place
+            }
+            n += __popc(all);
+        }
+        if (threadIdx.x == 0)
+            sm.chosen = n;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T * p.k; i += kFwThreads) {
+        const int e = sm.experts[i], t = i / p.k;
+        if (e >= 0)
+            atomicOr(&sm.tokens[sm.counts[e]][t >> 5], 1u << (t & 31));
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(mapa_shared(addr, rank))
+                 : "memory");
+    return v;
+}
+
+// Eight consecutive columns of token t of the cluster's S partial tiles.
+__device__ __forceinline__ void few_sum(uint32_t part, int t, int col, uint32_t S, float (&z)[8])
+{
+    const uint32_t at = part + (t * 128 + col) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        z[i] = 0.f;
+#pragma unroll 4
+    for (uint32_t s = 0; s < S; ++s) {
+        const float4 a = ld_cluster_f32x4(at, s), b = ld_cluster_f32x4(at + 16, s);
+        z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
+        z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+    }
+}
+
+__device__ __forceinline__ uint32_t few_cluster_size()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+// Barriers, TMEM.
+__device__ __forceinline__ void few_setup(const MoeFewArgs &p, FewSmem &sm, const CUtensorMap *weights, const CUtensorMap *rows)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane < 2)
+        tma_prefetch_desc(lane ? rows : weights);
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_slot, p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+}
+
+// The contraction of K blocks kb0 .. kb1 - 1 by warps 0 (weights' producer), 1 (MMA) and
+// 2 (rows' producer), then warps 4..7 put the accumulator into the partial tile
+// [token][128], over the ring.  load_weights(dst, bar, kb), load_rows(dst, bar, kb): the
+// copies of a K block, by a whole warp; wait_rows(): before the first of the rows.
+template <class LoadWeights, class LoadRows, class WaitRows>
+__device__ __forceinline__ void few_product(const MoeFewArgs &p, FewSmem &sm, uint8_t *ring, int kb0, int kb1,
+                                            LoadWeights &&load_weights, LoadRows &&load_rows, WaitRows &&wait_rows, const ErrCtx &err)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int *abort_flag = &sm.abort;
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    if (warp == 0 || warp == 2) {
+        const uint32_t tx = kFwWeights + static_cast<uint32_t>(p.tp) * 128u;
+        if (warp == 2)
+            wait_rows();
+        for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+            if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty))
+                break;
+            uint8_t *at = ring + stage * p.stage_bytes;
+            if (warp == 0) {
+                mbar_arrive_expect_tx_w(&sm.full[stage], tx);
+                load_weights(at, &sm.full[stage], kb);
+            } else {
+                load_rows(at + kFwWeights, &sm.full[stage], kb);
+            }
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_bf16_f32(128, p.tp);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(&sm.full[stage], phase, err, abort_flag, kSiteMmaFull))
+                break;
+            tc_fence_after();
+            const uint32_t w_s = smem_u32(ring + stage * p.stage_bytes);
+            const uint64_t wdesc = sdesc_kmajor_sw128(w_s), rdesc = sdesc_kmajor_sw128(w_s + kFwWeights);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16_w(sm.tmem_slot, wdesc + k * 2, rdesc + k * 2, idesc, (kb != kb0) || (k != 0));
+            mma_commit_w(&sm.empty[stage]);
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        mma_commit_w(&sm.done);
+    } else if (warp >= 4 && mbar_wait_warp(&sm.done, 0, err, abort_flag, kSiteEpiTmemFull)) {
+        tc_fence_after();
+        const int q = warp & 3;
+        const uint32_t part = smem_u32(ring);
+        for (int c = 0; c < p.tp; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(sm.tmem_slot + (static_cast<uint32_t>(q * 32) << 16) + c, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(part + ((c + j) * 128 + q * 32 + lane) * 4), "r"(kb0 < kb1 ? r[j] : 0u)
+                             : "memory");
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();                  // every CTA's partial tile is written
+    if (warp < 2 && *abort_flag) {
+        if (warp == 0)               // rows and weights share the stages' barriers
+            settle(sm.full, p.stages, stage, phase, issued, err.word, err.budget_ns);
+        else
+            settle(&sm.done, 1, 0, 1, 1, err.word, err.budget_ns);
+        __syncwarp();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(sm.tmem_slot, p.tmem_cols);
+    }
+}
+
+template <int C, bool BF16>
+__global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ FewSmem sm;
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t rank = cluster_ctarank(), S = few_cluster_size();
+    const int tiles = ceil_div(p.F, 64), tile = blockIdx.x / S, i = tile / tiles, f0 = tile % tiles * 64;
+    few_setup(p, sm, &p.tmW1, &p.tmX);
+    grid_wait();
+    grid_release();
+    few_choose<C, BF16>(p, sm);
+    tc_fence_after();
+    const bool work = i < sm.chosen;                 // the grid is an upper bound
+    const int e = work ? sm.list[i] : 0, num_kb = ceil_div(p.H, 64);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
+    const int kb1 = work ? static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S) : kb0;
+    for (int j = threadIdx.x; j < p.T * p.k; j += kFwThreads)
+        if (sm.experts[j] == e)
+            sm.weight[j / p.k] = sm.weights[j];
+    __syncthreads();
+    few_product(
+        p, sm, ring, kb0, kb1,
+        [&](uint8_t *dst, uint64_t *bar, int kb) {
+            tma_load_3d_one(dst, &p.tmW1, bar, kb * 64, f0, e);
+            tma_load_3d_one(dst + kFwWeights / 2, &p.tmW1, bar, kb * 64, p.F + f0, e);
+        },
+        [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_2d_w(dst, &p.tmX, bar, kb * 64, 0); }, [] {}, err);
+    if (work) {
+        // ------------------------- this CTA's share: sum, SwiGLU, weight
+        __nv_bfloat16 *hidden = static_cast<__nv_bfloat16 *>(p.hidden);
+        const int64_t limit = static_cast<int64_t>(min(p.E, p.T * p.k)) * p.tp * p.F;
+        const uint32_t part = smem_u32(ring);
+        const int items = p.tp * 8, first = items * rank / S, last = items * (rank + 1) / S;
+        for (int x = first + threadIdx.x; x < last; x += kFwThreads) {
+            const int t = x / 8, c = x % 8 * 8, f = f0 + c, n = min(8, p.F - f);
+            if (n <= 0)
+                continue;
+            float g[8] = {}, u[8] = {};
+            if (t < p.T && (sm.tokens[i][t >> 5] >> (t & 31) & 1u)) {
+                const float w = sm.weight[t];
+                few_sum(part, t, c, S, g);
+                few_sum(part, t, 64 + c, S, u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    g[j] = w * (silu_f(g[j]) * u[j]);
+            }
+            store_piece(hidden, (static_cast<int64_t>(i) * p.tp + t) * p.F + f,
+                        make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])),
+                        n, limit, err);
+        }
+    }
+    __syncwarp();
+    cluster_sync();                  // no CTA leaves while its partial sums may be read
+}
+
+template <int C, bool BF16>
+__global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ FewSmem sm;
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t rank = cluster_ctarank(), S = few_cluster_size();
+    const int n0 = blockIdx.x / S * 128;
+    few_setup(p, sm, &p.tmW2, &p.tmHidden);
+    grid_release();
+    few_choose<C, BF16>(p, sm);
+    tc_fence_after();
+    const int per = ceil_div(p.F, 64), num_kb = sm.chosen * per;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
+    few_product(
+        p, sm, ring, kb0, kb1,
+        [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_3d_one(dst, &p.tmW2, bar, kb % per * 64, n0, sm.list[kb / per]); },
+        [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_3d_one(dst, &p.tmHidden, bar, kb % per * 64, 0, kb / per); },
+        [] { grid_wait(); }, err);
+    grid_wait();                     // every warp: the first kernel's hidden rows
+    // ------------------------- this CTA's share: sum, residual
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+    const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
+    const __nv_bfloat16 *hidden = static_cast<const __nv_bfloat16 *>(p.hidden), *W2 = static_cast<const __nv_bfloat16 *>(p.W2);
+    const int64_t limit = (p.T - 1) * p.ld_out + p.H;
+    const uint32_t part = smem_u32(ring);
+    const int items = p.T * 16, first = items * rank / S, last = items * (rank + 1) / S;
+    for (int x = first + threadIdx.x; x < last; x += kFwThreads) {
+        const int t = x / 16, c = x % 16 * 8, col = n0 + c, n = min(8, p.H - col);
+        if (n <= 0)
+            continue;
+        float z[8];
+        few_sum(part, t, c, S, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n && z[j] != z[j]) {
+                float sum = 0.f;
+                for (int i = 0; i < sm.chosen; ++i)
+                    if (sm.tokens[i][t >> 5] >> (t & 31) & 1u) {
+                        const __nv_bfloat16 *w = W2 + (static_cast<int64_t>(sm.list[i]) * p.H + col + j) * p.F;
+                        const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.tp + t) * p.F;
+                        for (int f = 0; f < p.F; ++f)
+                            sum = fmaf(__bfloat162float(w[f]), __bfloat162float(h[f]), sum);
+                    }
+                z[j] = sum;
+            }
+        if (res) {
+            const __nv_bfloat16 *r = res + t * p.ld_residual + col;
+            if (n == 8 && (reinterpret_cast<uintptr_t>(r) & 15u) == 0) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(r);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    z[2 * j] += __uint_as_float(w[j] << 16);
+                    z[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < n)
+                        z[j] += __bfloat162float(r[j]);
+            }
+        }
+        store_piece(out, t * p.ld_out + col,
+                    make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])),
+                    n, limit, err);
+    }
+    __syncwarp();
+    cluster_sync();                  // no CTA leaves while its partial sums may be read
+}
+
+// CTAs that share a tile: two CTAs per SM, four K blocks each at least.
+int few_cluster(int64_t tiles, int64_t num_kb, int num_sms)
+{
+    int S = 1;
+    while (S < 8 && 2 * S * tiles <= 2 * num_sms && num_kb >= 8 * S)
+        S *= 2;
+    return S;
+}
+
+template <int C, bool BF16>
+cudaError_t launch_few_as(const MoeFewArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
+{
+    const int smem = 1024 + a.ring_bytes;
+    auto up = moe_few_up_kernel<C, BF16>;
+    auto down = moe_few_down_kernel<C, BF16>;
+    cudaError_t e;
+    if ((e = ensure_smem_attr(reinterpret_cast<const void *>(up), smem)) != cudaSuccess ||
+        (e = ensure_smem_attr(reinterpret_cast<const void *>(down), smem)) != cudaSuccess)
+        return e;
+    const int experts = a.T * a.k < a.E ? a.T * a.k : a.E;
+    const int64_t ups = static_cast<int64_t>(experts) * ((a.F + 63) / 64), downs = (a.H + 127) / 128;
+    const int s_up = few_cluster(ups, (a.H + 63) / 64, num_sms);
+    if ((e = launch_overlapped(up, dim3(static_cast<unsigned>(ups * s_up)), kFwThreads, smem, s_up, s, a, err)) != cudaSuccess)
+        return e;
+    const int s_down = few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), num_sms);
+    return launch_overlapped(down, dim3(static_cast<unsigned>(downs * s_down)), kFwThreads, smem, s_down, s, a, err);
+}
+
+template <int C>
+cudaError_t launch_few_of(const MoeFewArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
+{
+    return a.bf16 ? launch_few_as<C, true>(a, num_sms, err, s) : launch_few_as<C, false>(a, num_sms, err, s);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_few(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
+{
+    a.stage_bytes = kFwWeights + a.tp * 128;
+    a.stages = kFwRing / a.stage_bytes < kFwMaxStages ? kFwRing / a.stage_bytes : kFwMaxStages;
+    a.ring_bytes = a.stages * a.stage_bytes;
+    a.tmem_cols = a.tp <= 32 ? 32 : 64;
+    return a.E <= 64    ? launch_few_of<2>(a, num_sms, err, s)
+           : a.E <= 128 ? launch_few_of<4>(a, num_sms, err, s)
+                        : launch_few_of<8>(a, num_sms, err, s);
+}
+
+}  // namespace tmg
