@@ -432,6 +432,19 @@ def test_lora_gradients_requests(tmg, kind, M):
     check_grads(tmg, t, ids_of(kind, M, 12, M), normal((M, 392), 74), normal((M, 16), 75))
 
 
+@pytest.mark.parametrize("rows", [1, 64, 65, 128, 130, 192, 257])
+def test_lora_gradients_of_few_rows_among_many(tmg, rows):
+    """Fewer blocks of rows with an adapter than runs that share the work."""
+    M = 2900
+    t = lora_inputs(M, 136, 264, 16, 5, 76)
+    ids = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    ids[1000:1000 + rows] = 3
+    ids[2000:2000 + rows // 2] = 1
+    check_grads(tmg, t, ids, normal((M, 136), 77), normal((M, 16), 78))
+    ids[2000:2000 + rows // 2] = -1
+    check_grads(tmg, t, ids, normal((M, 136), 77), normal((M, 16), 78))
+
+
 def test_lora_of_a_large_model(tmg):
     for M, N, K, r, L in ((1, 4096, 4096, 16, 8), (16, 8192, 8192, 16, 64), (700, 1024, 4096, 32, 16), (2100, 4096, 2048, 64, 4),
                           (1500, 5000, 4104, 8, 3)):

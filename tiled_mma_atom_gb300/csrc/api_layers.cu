@@ -22,6 +22,17 @@ struct Pieces {
     }
 };
 
+// Arrival counters, zero between launches (the tile feed's counter comes before
+// them).
+tmg_status arrival_counters(size_t n, cudaStream_t s, uint32_t **out)
+{
+    tmg_status st;
+    *out = static_cast<uint32_t *>(workspace(kWsCounters, (32 + n) * sizeof(uint32_t), s, &st));
+    if (*out)
+        *out += 32;
+    return st;
+}
+
 // The layer by the separate operators: plan, up products, down products, sum.
 tmg_status moe_by_groups(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
 {
@@ -144,17 +155,6 @@ tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cud
     return launched(launch_lora_rank_tc(p, a.across, ds.num_sms, err_ctx(ds), s), "adapter rank launch");
 }
 
-// Arrival counters, zero between launches (the tile feed's counter comes before
-// them).
-tmg_status lora_counters(size_t n, cudaStream_t s, uint32_t **out)
-{
-    tmg_status st;
-    *out = static_cast<uint32_t *>(workspace(kWsCounters, (32 + n) * sizeof(uint32_t), s, &st));
-    if (*out)
-        *out += 32;
-    return st;
-}
-
 // G = the factors' gradient from Y (M, C) and Z (M, r), rows as tma_rows gave them.
 tmg_status run_factor_grad(const DeviceState &ds, const Rows &Y, int64_t C, const Rows &Z, int64_t M, int64_t L, int64_t r,
                            const int32_t *offsets, const int32_t *rows, void *G, bool across, cudaStream_t s)
@@ -180,7 +180,7 @@ tmg_status run_factor_grad(const DeviceState &ds, const Rows &Y, int64_t C, cons
     p.partials = static_cast<float *>(workspace(kWsPartials, lora_grad_partial_bytes(M, C, p.r, ds.num_sms), s, &st));
     if (!p.partials)
         return st;
-    if ((st = lora_counters(lora_grad_counters(M, C, ds.num_sms), s, &p.counters)) != TMG_OK)
+    if ((st = arrival_counters(lora_grad_counters(M, C, ds.num_sms), s, &p.counters)) != TMG_OK)
         return st;
     return launched(launch_lora_grad(p, ds.num_sms, err_ctx(ds), s), "adapter gradient launch");
 }
@@ -241,7 +241,7 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
         p.partials = static_cast<float *>(workspace(kWsPartials, tc2_partials_bytes(t), s, &st));
         if (!p.partials)
             return st;
-        if ((st = lora_counters(tc2_counters_bytes(t) / sizeof(uint32_t), s, &p.counters)) != TMG_OK)
+        if ((st = arrival_counters(tc2_counters_bytes(t) / sizeof(uint32_t), s, &p.counters)) != TMG_OK)
             return st;
     }
     p.D = a.D;
@@ -299,6 +299,9 @@ tmg_status moe_few(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
     p.normalize = g.normalize != 0;
     p.bf16 = g.logits_dtype == TMG_BF16;
     p.tp = static_cast<int>(tp);
+    p.partials = static_cast<float *>(workspace(kWsPartials, moe_few_partial_bytes(p.tp, ds.num_sms), s, &st));
+    if (!p.partials || (st = arrival_counters(ds.num_sms, s, &p.counters)) != TMG_OK)
+        return st;
     return launched(launch_moe_few(p, ds.num_sms, err_ctx(ds), s), "expert layer launch");
 }
 

@@ -36,7 +36,7 @@ constexpr int kGrBars = (2 * kGrMaxStages + 4) * 8 + 16;
 // The run of a CTA, adapter by adapter.
 struct GradWalk {
     const int *unit;
-    int L, u, u0, u_end;
+    int L, u, u_end;
 
     // Adapter, its blocks b0 .. b1 - 1 here, and whether it has others elsewhere.
     __device__ __forceinline__ bool next(int &l, int &b0, int &b1, bool &partial)
@@ -129,8 +129,10 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int units = unit[p.L];
-    GradWalk walk{unit, p.L, run_start(units, run, p.runs), run_start(units, run, p.runs), run_start(units, run + 1, p.runs)};
+    const int units = unit[p.L], runs = min(p.runs, units);        // no run is empty
+    GradWalk walk{unit, p.L, 0, 0};
+    if (run < runs)
+        walk = GradWalk{unit, p.L, run_start(units, run, runs), run_start(units, run + 1, runs)};
     int l, b0, b1;
     bool partial;
 
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
         const int64_t piece = static_cast<int64_t>(kGrCols) * r16, p_limit = static_cast<int64_t>(gridDim.x) * 2 * piece;
         // run x's partial sums of adapter a: its first adapter's, or its last's
         auto piece_of = [&](int x, int a) {
-            return ((static_cast<int64_t>(x) * tiles + tile) * 2 + (unit[a] <= run_start(units, x, p.runs) ? 0 : 1)) * piece + q * 32 + lane;
+            return ((static_cast<int64_t>(x) * tiles + tile) * 2 + (unit[a] <= run_start(units, x, runs) ? 0 : 1)) * piece + q * 32 + lane;
         };
         int local = 0;
         while (walk.next(l, b0, b1, partial)) {
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
                 mbar_arrive(&tempty[acc]);
             if (!partial)
                 continue;
-            const int r_first = unit_owner(unit[l], units, p.runs), r_last = unit_owner(unit[l + 1] - 1, units, p.runs);
+            const int r_first = unit_owner(unit[l], units, runs), r_last = unit_owner(unit[l + 1] - 1, units, runs);
             const int64_t counter = (static_cast<int64_t>(r_first) * tiles + tile) * 4 + q;
             if (!last_arrival(p.counters + counter, r_last - r_first, bounds_ok(counter, 4ll * gridDim.x, err, kBndCounters)))
                 continue;

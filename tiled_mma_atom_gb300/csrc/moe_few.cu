@@ -31,6 +31,7 @@
 #include "launch.cuh"
 #include "lora.cuh"
 #include "moe_few.h"
+#include "pieces.cuh"
 #include "route.cuh"
 #include "staging.cuh"
 
@@ -38,7 +39,7 @@ namespace tmg {
 namespace {
 
 constexpr int kFwThreads = 256;
-constexpr int kFwMaxStages = 8;
+constexpr int kFwMaxStages = 12;
 constexpr int kFwRing = 96 * 1024;
 constexpr int kFwWeights = 16384;            // 128 weight rows of a K block
 
@@ -231,61 +232,248 @@ __device__ __forceinline__ void few_product(const MoeFewArgs &p, FewSmem &sm, ui
     }
 }
 
+// What a CTA of the first kernel does: whole tiles in turn, or, where those would leave
+// many CTAs without one in the last wave, a run of the (tile, K block) units of all
+// tiles, cut into equal runs.  A cut costs about as much as kFewCutBlocks blocks (partial
+// sums through global memory).
+constexpr int kFewCutBlocks = 10;
+
+struct FewWalk {
+    int num_kb, tiles, ctas, runs;       // runs: 0 for whole tiles
+    int me, u, u_end;                    // whole tiles: u is the next one
+
+    __device__ __forceinline__ FewWalk(int tiles_, int num_kb_, int me_, int ctas_)
+        : num_kb(num_kb_), tiles(tiles_), ctas(ctas_), runs(0), me(me_), u(me_), u_end(0)
+    {
+        const int units = tiles * num_kb;
+        if (ceil_div(tiles, ctas) * num_kb > units / ctas + kFewCutBlocks) {
+            runs = min(ctas, units);     // no run is empty
+            u = me < runs ? start(me) : 0;
+            u_end = me < runs ? start(me + 1) : 0;
+        }
+    }
+    __device__ __forceinline__ int start(int c) const
+    {
+        return static_cast<int>(static_cast<int64_t>(tiles) * num_kb * c / runs);
+    }
+    // The run with unit x.
+    __device__ __forceinline__ int owner(int x) const
+    {
+        return static_cast<int>(((static_cast<int64_t>(x) + 1) * runs - 1) / (static_cast<int64_t>(tiles) * num_kb));
+    }
+    // Where run c leaves its partial sums of a tile: first those of its first tile.
+    __device__ __forceinline__ int slot(int c, int tile) const { return 2 * c + (tile * num_kb <= start(c) ? 0 : 1); }
+
+    __device__ __forceinline__ bool next(int &tile, int &kb0, int &kb1)
+    {
+        if (runs == 0) {
+            tile = u;
+            kb0 = 0;
+            kb1 = num_kb;
+            u += ctas;
+            return tile < tiles;
+        }
+        if (u >= u_end)
+            return false;
+        tile = u / num_kb;
+        kb0 = u - tile * num_kb;
+        kb1 = min(num_kb, kb0 + u_end - u);
+        u += kb1 - kb0;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void few_epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
 template <int C, bool BF16>
 __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ FewSmem sm;
+    __shared__ uint64_t tfull[2], tempty[2];
+    __shared__ int arrived;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    const uint32_t rank = cluster_ctarank(), S = few_cluster_size();
-    const int tiles = ceil_div(p.F, 64), tile = blockIdx.x / S, i = tile / tiles, f0 = tile % tiles * 64;
+    float *staged = reinterpret_cast<float *>(ring + p.ring_bytes);        // a tile's sums [token][128]
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int *abort_flag = &sm.abort;
+    if (threadIdx.x == 0)
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 4);
+        }
     few_setup(p, sm, &p.tmW1, &p.tmX);
     grid_wait();
     grid_release();
     few_choose<C, BF16>(p, sm);
     tc_fence_after();
-    const bool work = i < sm.chosen;                 // the grid is an upper bound
-    const int e = work ? sm.list[i] : 0, num_kb = ceil_div(p.H, 64);
-    const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
-    const int kb1 = work ? static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S) : kb0;
-    for (int j = threadIdx.x; j < p.T * p.k; j += kFwThreads)
-        if (sm.experts[j] == e)
-            sm.weight[j / p.k] = sm.weights[j];
-    __syncthreads();
-    few_product(
-        p, sm, ring, kb0, kb1,
-        [&](uint8_t *dst, uint64_t *bar, int kb) {
-            tma_load_3d_one(dst, &p.tmW1, bar, kb * 64, f0, e);
-            tma_load_3d_one(dst + kFwWeights / 2, &p.tmW1, bar, kb * 64, p.F + f0, e);
-        },
-        [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_2d_w(dst, &p.tmX, bar, kb * 64, 0); }, [] {}, err);
-    if (work) {
-        // ------------------------- this CTA's share: sum, SwiGLU, weight
-        __nv_bfloat16 *hidden = static_cast<__nv_bfloat16 *>(p.hidden);
-        const int64_t limit = static_cast<int64_t>(min(p.E, p.T * p.k)) * p.tp * p.F;
-        const uint32_t part = smem_u32(ring);
-        const int items = p.tp * 8, first = items * rank / S, last = items * (rank + 1) / S;
-        for (int x = first + threadIdx.x; x < last; x += kFwThreads) {
-            const int t = x / 8, c = x % 8 * 8, f = f0 + c, n = min(8, p.F - f);
-            if (n <= 0)
-                continue;
-            float g[8] = {}, u[8] = {};
-            if (t < p.T && (sm.tokens[i][t >> 5] >> (t & 31) & 1u)) {
-                const float w = sm.weight[t];
-                few_sum(part, t, c, S, g);
-                few_sum(part, t, 64 + c, S, u);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    g[j] = w * (silu_f(g[j]) * u[j]);
+    const uint32_t tmem = sm.tmem_slot;
+    const int f_tiles = ceil_div(p.F, 64), num_kb = ceil_div(p.H, 64), me = blockIdx.x, ctas = gridDim.x;
+    FewWalk walk(sm.chosen * f_tiles, num_kb, me, ctas);
+    int tile, kb0, kb1;
+
+    if (warp == 0 || warp == 2) {
+        // ------------------ TMA producers: the weights (warp 0), the rows (warp 2)
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t tx = kFwWeights + static_cast<uint32_t>(p.tp) * 128u;
+        while (ok && walk.next(tile, kb0, kb1)) {
+            const int e = sm.list[tile / f_tiles], f0 = tile % f_tiles * 64;
+            for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+                if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *at = ring + stage * p.stage_bytes;
+                if (warp == 0) {
+                    mbar_arrive_expect_tx_w(&sm.full[stage], tx);
+                    tma_load_3d_one(at, &p.tmW1, &sm.full[stage], kb * 64, f0, e);
+                    tma_load_3d_one(at + kFwWeights / 2, &p.tmW1, &sm.full[stage], kb * 64, p.F + f0, e);
+                } else {
+                    tma_load_2d_w(at + kFwWeights, &p.tmX, &sm.full[stage], kb * 64, 0);
+                }
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            store_piece(hidden, (static_cast<int64_t>(i) * p.tp + t) * p.F + f,
-                        make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])),
-                        n, limit, err);
+        }
+        for (int i = 0; i < p.stages && i < issued; ++i) {          // every stage is released
+            const int s = stage - 1 - i;
+            mbar_wait(&sm.empty[s < 0 ? s + p.stages : s], s < 0 ? phase ^ 1u : phase, err, abort_flag, kSiteDrain);
+        }
+        if (*abort_flag && warp == 0)
+            settle(sm.full, p.stages, stage, phase, min(issued, p.stages), err.word, err.budget_ns);
+    } else if (warp == 1) {
+        // -------------------------------------------- MMA issuer
+        const uint32_t idesc = idesc_bf16_f32(128, p.tp);
+        int stage = 0, local = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && walk.next(tile, kb0, kb1)) {
+            const int acc = local & 1;
+            const uint32_t acc_phase = (local >> 1) & 1;
+            ++local;
+            if (!mbar_wait_warp(&tempty[acc], acc_phase ^ 1u, err, abort_flag, kSiteMmaTmemEmpty))
+                break;
+            tc_fence_after();
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_warp(&sm.full[stage], phase, err, abort_flag, kSiteMmaFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t w_s = smem_u32(ring + stage * p.stage_bytes);
+                const uint64_t wdesc = sdesc_kmajor_sw128(w_s), rdesc = sdesc_kmajor_sw128(w_s + kFwWeights);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16_w(tmem + acc * 64, wdesc + k * 2, rdesc + k * 2, idesc, (kb != kb0) || (k != 0));
+                mma_commit_w(&sm.empty[stage]);
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok)
+                break;
+            mma_commit_w(&tfull[acc]);
+        }
+        if (*abort_flag)
+            settle(sm.empty, p.stages, stage, phase, 1, err.word, err.budget_ns);
+    } else if (warp >= 4) {
+        // ---------------------------------------------------- epilogue
+        const int q = warp & 3, id = threadIdx.x - 128, piece = p.tp * 128;
+        __nv_bfloat16 *hidden = static_cast<__nv_bfloat16 *>(p.hidden);
+        const int64_t limit = static_cast<int64_t>(min(p.E, p.T * p.k)) * p.tp * p.F, p_limit = 2ll * ctas * piece;
+        int local = 0;
+        while (walk.next(tile, kb0, kb1)) {
+            const int acc = local & 1, i = tile / f_tiles, e = sm.list[i], f0 = tile % f_tiles * 64;
+            const uint32_t acc_phase = (local >> 1) & 1;
+            const bool partial = kb0 != 0 || kb1 != num_kb;
+            ++local;
+            for (int j = id; j < p.T * p.k; j += 128)        // the last tile's reads are done
+                if (sm.experts[j] == e)
+                    sm.weight[j / p.k] = sm.weights[j];
+            // all 128 threads leave together: a wait that ran out raises the abort flag
+            const bool there = mbar_wait_warp(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull);
+            tc_fence_after();
+            if (there)
+                for (int c = 0; c < p.tp; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 64 + c, r);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        staged[(c + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&tempty[acc]);
+            few_epilogue_sync();
+            if (*abort_flag)
+                break;
+            int first = me, last = me;
+            if (partial) {
+                const int64_t at = static_cast<int64_t>(walk.slot(me, tile)) * piece;
+                for (int x = id * 4; x < piece; x += 512)
+                    if (span_ok(at + x, 4, p_limit, err, kBndPartials))
+                        *reinterpret_cast<float4 *>(p.partials + at + x) = *reinterpret_cast<const float4 *>(staged + x);
+                first = walk.owner(tile * num_kb);
+                last = walk.owner((tile + 1) * num_kb - 1);
+                few_epilogue_sync();
+                if (warp == 4) {
+                    const bool mine = last_arrival(p.counters + first, last - first, bounds_ok(first, ctas, err, kBndCounters));
+                    if (lane == 0)
+                        arrived = mine;
+                }
+                few_epilogue_sync();
+                if (!arrived)
+                    continue;
+            }
+            // sum, SwiGLU, weight: eight columns of a token per thread
+            for (int x = id; x < p.tp * 8; x += 128) {
+                const int t = x / 8, c = x % 8 * 8, f = f0 + c, n = min(8, p.F - f);
+                if (n <= 0)
+                    continue;
+                float g[8] = {}, u[8] = {};
+                if (t < p.T && (sm.tokens[i][t >> 5] >> (t & 31) & 1u)) {
+                    if (!partial) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            g[j] = staged[t * 128 + c + j];
+                            u[j] = staged[t * 128 + 64 + c + j];
+                        }
+                    } else {
+                        for (int o = first; o <= last; ++o) {
+                            const int64_t at = static_cast<int64_t>(walk.slot(o, tile)) * piece + t * 128 + c;
+                            if (!span_ok(at, 72, p_limit, err, kBndPartials))
+                                continue;
+                            const float4 *v = reinterpret_cast<const float4 *>(p.partials + at);
+                            const float4 a = __ldcg(v), b = __ldcg(v + 1), y = __ldcg(v + 16), z = __ldcg(v + 17);
+                            g[0] += a.x, g[1] += a.y, g[2] += a.z, g[3] += a.w, g[4] += b.x, g[5] += b.y, g[6] += b.z, g[7] += b.w;
+                            u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w, u[4] += z.x, u[5] += z.y, u[6] += z.z, u[7] += z.w;
+                        }
+                    }
+                    const float w = sm.weight[t];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        g[j] = w * (silu_f(g[j]) * u[j]);
+                }
+                store_piece(hidden, (static_cast<int64_t>(i) * p.tp + t) * p.F + f,
+                            make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])),
+                            n, limit, err);
+            }
+            few_epilogue_sync();                             // the staged tile and the weights are free
         }
     }
     __syncwarp();
-    cluster_sync();                  // no CTA leaves while its partial sums may be read
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, p.tmem_cols);
+    }
 }
 
 template <int C, bool BF16>
@@ -370,23 +558,32 @@ int few_cluster(int64_t tiles, int64_t num_kb, int num_sms)
     return S;
 }
 
-template <int C, bool BF16>
-cudaError_t launch_few_as(const MoeFewArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
+// The ring's stages within `bytes`.
+void few_ring(MoeFewArgs &a, int bytes)
 {
-    const int smem = 1024 + a.ring_bytes;
+    a.stage_bytes = kFwWeights + a.tp * 128;
+    a.stages = bytes / a.stage_bytes < kFwMaxStages ? bytes / a.stage_bytes : kFwMaxStages;
+    a.ring_bytes = a.stages * a.stage_bytes;
+}
+
+template <int C, bool BF16>
+cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
+{
+    MoeFewArgs b = a;
+    few_ring(a, kFwRing);
+    few_ring(b, kFwRing);
+    const int smem = 1024 + b.ring_bytes, smem_up = 1024 + a.ring_bytes + a.tp * 512;
     auto up = moe_few_up_kernel<C, BF16>;
     auto down = moe_few_down_kernel<C, BF16>;
     cudaError_t e;
-    if ((e = ensure_smem_attr(reinterpret_cast<const void *>(up), smem)) != cudaSuccess ||
+    if ((e = ensure_smem_attr(reinterpret_cast<const void *>(up), smem_up)) != cudaSuccess ||
         (e = ensure_smem_attr(reinterpret_cast<const void *>(down), smem)) != cudaSuccess)
         return e;
-    const int experts = a.T * a.k < a.E ? a.T * a.k : a.E;
-    const int64_t ups = static_cast<int64_t>(experts) * ((a.F + 63) / 64), downs = (a.H + 127) / 128;
-    const int s_up = few_cluster(ups, (a.H + 63) / 64, num_sms);
-    if ((e = launch_overlapped(up, dim3(static_cast<unsigned>(ups * s_up)), kFwThreads, smem, s_up, s, a, err)) != cudaSuccess)
+    const int64_t downs = (a.H + 127) / 128;
+    if ((e = launch_overlapped(up, dim3(static_cast<unsigned>(num_sms)), kFwThreads, smem_up, 1, s, a, err)) != cudaSuccess)
         return e;
     const int s_down = few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), num_sms);
-    return launch_overlapped(down, dim3(static_cast<unsigned>(downs * s_down)), kFwThreads, smem, s_down, s, a, err);
+    return launch_overlapped(down, dim3(static_cast<unsigned>(downs * s_down)), kFwThreads, smem, s_down, s, b, err);
 }
 
 template <int C>
@@ -397,12 +594,11 @@ cudaError_t launch_few_of(const MoeFewArgs &a, int num_sms, const ErrCtx &err, c
 
 }  // namespace
 
+size_t moe_few_partial_bytes(int tp, int num_sms) { return static_cast<size_t>(num_sms) * 2 * tp * 128 * sizeof(float); }
+
 cudaError_t launch_moe_few(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    a.stage_bytes = kFwWeights + a.tp * 128;
-    a.stages = kFwRing / a.stage_bytes < kFwMaxStages ? kFwRing / a.stage_bytes : kFwMaxStages;
-    a.ring_bytes = a.stages * a.stage_bytes;
-    a.tmem_cols = a.tp <= 32 ? 32 : 64;
+    a.tmem_cols = 128;
     return a.E <= 64    ? launch_few_of<2>(a, num_sms, err, s)
            : a.E <= 128 ? launch_few_of<4>(a, num_sms, err, s)
                         : launch_few_of<8>(a, num_sms, err, s);

@@ -20,9 +20,12 @@ struct MoeFewArgs {
     int T, H, F, E, k, normalize;
     bool bf16;                 // the logits
     int tp;                    // T rounded up to 16
+    float *partials;           // moe_few_partial_bytes()
+    uint32_t *counters;        // one per SM, zero between launches
     // set by the launch
     int stages, stage_bytes, ring_bytes, tmem_cols;
 };
+size_t moe_few_partial_bytes(int tp, int num_sms);
 cudaError_t launch_moe_few(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 }  // namespace tmg
