@@ -122,15 +122,19 @@ tmg_status tma_rows(const DeviceState &ds, Workspace which, const void *src, int
     return st;
 }
 
-// Rows by which the tensor cores take the ranks' side over, from more than these on.
-constexpr int64_t kRankRows = 64;
-
 // U = bf16(scales X . F[adapters]^T), (M, r) with rows of ldu; x: X's rows as tma_rows
-// gave them where M > kRankRows.
+// gave them.  A few rows by a warp per row and rank, where 16-byte loads read the
+// factors in place.
 tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cudaStream_t s)
 {
-    if (a.M <= kRankRows || a.C == 0)
-        return launched(launch_lora_rank(a, s), "adapter rank launch");
+    if (a.C == 0)
+        return launched(cudaMemsetAsync(a.U, 0, static_cast<size_t>(a.M) * a.ldu * 2, s), "cudaMemsetAsync(u)");
+    if (a.M <= kLoraFewRows && !a.across && a.C % 8 == 0 && aligned(a.F)) {
+        RankArgs b = a;
+        b.X = x.p;
+        b.ldx = x.ld;
+        return launched(launch_lora_few_rank(b, s), "adapter rank launch");
+    }
     tmg_status st;
     const int64_t rows = a.across ? a.C : a.r, cols = a.across ? a.r : a.C;
     Rows f;
@@ -298,11 +302,43 @@ tmg_status moe_few(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
     p.k = static_cast<int>(g.k);
     p.normalize = g.normalize != 0;
     p.bf16 = g.logits_dtype == TMG_BF16;
-    p.tp = static_cast<int>(tp);
-    p.partials = static_cast<float *>(workspace(kWsPartials, moe_few_partial_bytes(p.tp, ds.num_sms), s, &st));
+    p.shape.tp = static_cast<int>(tp);
+    p.partials = static_cast<float *>(workspace(kWsPartials, moe_few_partial_bytes(p.shape.tp, ds.num_sms), s, &st));
     if (!p.partials || (st = arrival_counters(ds.num_sms, s, &p.counters)) != TMG_OK)
         return st;
     return launched(launch_moe_few(p, ds.num_sms, err_ctx(ds), s), "expert layer launch");
+}
+
+// The same for a few rows, not across; W and F as tma_rows gave them (before the
+// kernel that makes U, beside which this one runs).
+tmg_status run_adapted_few(const DeviceState &ds, const AdaptedArgs &a, const Rows &W, const Rows &F, cudaStream_t s)
+{
+    tmg_status st;
+    LoraFewArgs p;
+    std::memset(&p, 0, sizeof p);
+    const int64_t K = a.K > 0 ? a.K : 8, tp = up(a.M, 16);
+    const int64_t wd[2] = {K, a.N}, wst[1] = {W.ld * 2}, xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2};
+    const int wbox[2] = {64, 128}, xbox[2] = {64, static_cast<int>(tp)};
+    if ((st = encode_nd(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, W.p, wd, wst, wbox)) != TMG_OK ||
+        (st = encode_nd(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x.p, xd, xs, xbox, true)) != TMG_OK)
+        return st;
+    p.U = a.U;
+    p.F = F.p;
+    p.D = a.D;
+    p.adapters = a.adapters;
+    p.bias = a.bias;
+    p.residual = a.residual;
+    p.ldu = a.ldu;
+    p.ldf = F.ld;
+    p.ldd = a.ldd;
+    p.ld_residual = a.ld_residual;
+    p.M = static_cast<int>(a.M);
+    p.N = static_cast<int>(a.N);
+    p.K = static_cast<int>(K);
+    p.L = static_cast<int>(a.L);
+    p.r = static_cast<int>(a.r);
+    p.shape.tp = static_cast<int>(tp);
+    return launched(launch_lora_few(p, ds.num_sms, err_ctx(ds), s), "product with adapters launch");
 }
 
 // Limits of the adapters' extents and pointers, common to both directions.
@@ -387,6 +423,12 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
         Rows x;
         if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK)
             return st;
+        const bool few = g->M <= kLoraFewRows;
+        Rows W{}, B{};
+        if (few && g->N > 0 &&
+            ((st = tma_rows(*ds, kWsPackB, g->W, g->ldw, g->N, g->K, g->N, s, &W)) != TMG_OK ||
+             (st = tma_rows(*ds, kWsLayoutB, g->B, g->r, g->L * g->N, g->r, g->L * g->N, s, &B)) != TMG_OK))
+            return st;
         RankArgs k{g->x, g->A, g->adapters, g->scales, u, g->M, g->K, g->L, g->ldx, ldu, static_cast<int>(g->r), false};
         if ((st = run_rank(*ds, k, x, s)) != TMG_OK)
             return st;
@@ -398,10 +440,9 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
         }
         if (g->N == 0)
             return TMG_OK;
-        return run_adapted(*ds,
-                           AdaptedArgs{x, g->W, u, g->B, g->D, g->adapters, g->bias, g->residual, g->M, g->N, g->K, g->r,
-                                       g->L, g->ldw, ldu, g->ldd, g->ld_residual, false},
-                           s);
+        const AdaptedArgs a{x, g->W, u, g->B, g->D, g->adapters, g->bias, g->residual, g->M, g->N, g->K, g->r, g->L, g->ldw, ldu,
+                            g->ldd, g->ld_residual, false};
+        return few ? run_adapted_few(*ds, a, W, B, s) : run_adapted(*ds, a, s);
     });
 }
 

@@ -1,0 +1,185 @@
+// few.cuh — the product of a few rows with many weights, split over a cluster: 128
+// weight rows are the MMA's M, the rows (padded to tp, a multiple of 16) its N, and
+// the CTAs of a cluster each sum a run of the tile's K blocks; the partial sums meet
+// in shared memory, where every CTA takes a share of the results.
+#pragma once
+
+#include "feed.cuh"
+#include "launch.cuh"
+#include "lora.cuh"
+
+namespace tmg {
+
+constexpr int kFwMaxStages = 12;
+constexpr int kFwRing = 96 * 1024;           // bytes that let two CTAs share an SM
+constexpr int kFwWeights = 16384;            // 128 weight rows of a K block
+
+struct FewShape {
+    int tp;                    // rows rounded up to 16
+    int stages, stage_bytes, ring_bytes, tmem_cols;
+};
+
+namespace {
+
+struct FewRing {
+    uint64_t full[kFwMaxStages], empty[kFwMaxStages], done;
+    uint32_t tmem_slot;
+    int abort;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(mapa_shared(addr, rank))
+                 : "memory");
+    return v;
+}
+
+// Eight consecutive columns of row t of the cluster's S partial tiles.
+__device__ __forceinline__ void few_sum(uint32_t part, int t, int col, uint32_t S, float (&z)[8])
+{
+    const uint32_t at = part + (t * 128 + col) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        z[i] = 0.f;
+#pragma unroll 4
+    for (uint32_t s = 0; s < S; ++s) {
+        const float4 a = ld_cluster_f32x4(at, s), b = ld_cluster_f32x4(at + 16, s);
+        z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
+        z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+    }
+}
+
+__device__ __forceinline__ uint32_t few_cluster_size()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+// Barriers, TMEM.
+__device__ __forceinline__ void few_setup(const FewShape &p, FewRing &sm, const CUtensorMap *weights, const CUtensorMap *rows)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane < 2)
+        tma_prefetch_desc(lane ? rows : weights);
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_slot, p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+}
+
+// The contraction of K blocks kb0 .. kb1 - 1 by warps 0 (weights' producer), 1 (MMA) and
+// 2 (rows' producer), then warps 4..7 put the accumulator into the partial tile
+// [row][128], over the ring.  load_weights(dst, bar, kb), load_rows(dst, bar, kb): the
+// copies of a K block, by a whole warp; wait_rows(): before the first of the rows;
+// meanwhile(): what the warps from 4 on do before they wait for the sums.
+template <class LoadWeights, class LoadRows, class WaitRows, class Meanwhile>
+__device__ __forceinline__ void few_product(const FewShape &p, FewRing &sm, uint8_t *ring, int kb0, int kb1,
+                                            LoadWeights &&load_weights, LoadRows &&load_rows, WaitRows &&wait_rows, Meanwhile &&meanwhile,
+                                            const ErrCtx &err)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    volatile int *abort_flag = &sm.abort;
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    if (warp == 0 || warp == 2) {
+        const uint32_t tx = kFwWeights + static_cast<uint32_t>(p.tp) * 128u;
+        if (warp == 2)
+            wait_rows();
+        for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+            if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty))
+                break;
+            uint8_t *at = ring + stage * p.stage_bytes;
+            if (warp == 0) {
+                mbar_arrive_expect_tx_w(&sm.full[stage], tx);
+                load_weights(at, &sm.full[stage], kb);
+            } else {
+                load_rows(at + kFwWeights, &sm.full[stage], kb);
+            }
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_bf16_f32(128, p.tp);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(&sm.full[stage], phase, err, abort_flag, kSiteMmaFull))
+                break;
+            tc_fence_after();
+            const uint32_t w_s = smem_u32(ring + stage * p.stage_bytes);
+            const uint64_t wdesc = sdesc_kmajor_sw128(w_s), rdesc = sdesc_kmajor_sw128(w_s + kFwWeights);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16_w(sm.tmem_slot, wdesc + k * 2, rdesc + k * 2, idesc, (kb != kb0) || (k != 0));
+            mma_commit_w(&sm.empty[stage]);
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        mma_commit_w(&sm.done);
+    } else if (warp >= 4) {
+        meanwhile();
+        if (warp < 8 && mbar_wait_warp(&sm.done, 0, err, abort_flag, kSiteEpiTmemFull)) {
+            tc_fence_after();
+            const int q = warp & 3;
+            const uint32_t part = smem_u32(ring);
+            for (int c = 0; c < p.tp; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(sm.tmem_slot + (static_cast<uint32_t>(q * 32) << 16) + c, r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(part + ((c + j) * 128 + q * 32 + lane) * 4), "r"(kb0 < kb1 ? r[j] : 0u)
+                                 : "memory");
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    cluster_sync();                  // every CTA's partial tile is written
+    if (warp < 2 && *abort_flag) {
+        if (warp == 0)               // rows and weights share the stages' barriers
+            settle(sm.full, p.stages, stage, phase, issued, err.word, err.budget_ns);
+        else
+            settle(&sm.done, 1, 0, 1, 1, err.word, err.budget_ns);
+        __syncwarp();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(sm.tmem_slot, p.tmem_cols);
+    }
+}
+
+// The ring's stages within `bytes`.
+inline void few_ring(FewShape &a, int bytes)
+{
+    a.stage_bytes = kFwWeights + a.tp * 128;
+    a.stages = bytes / a.stage_bytes < kFwMaxStages ? bytes / a.stage_bytes : kFwMaxStages;
+    a.ring_bytes = a.stages * a.stage_bytes;
+}
+
+// CTAs that share a tile: two CTAs per SM, four K blocks each at least.
+inline int few_cluster(int64_t tiles, int64_t num_kb, int num_sms)
+{
+    int S = 1;
+    while (S < 8 && 2 * S * tiles <= 2 * num_sms && num_kb >= 8 * S)
+        S *= 2;
+    return S;
+}
+
+}  // namespace
+}  // namespace tmg

@@ -1,13 +1,13 @@
 // lora.h — arguments of the kernels of dense projections with low-rank adapters.
 #pragma once
 
-#include "internal.h"
+#include "few.cuh"
 
 namespace tmg {
 
 // U[m][j] = bf16(scales[a] sum_c X[m][c] F[a][j][c]) with a = adapters[m], or, `across`,
-// of F[a][c][j]; zeros where a is not one of 0 .. L - 1.  F is contiguous per
-// adapter, (r, C) or (C, r).
+// of F[a][c][j]; zeros where a is not one of 0 .. L - 1.  F is contiguous, (L, r, C) or
+// (L, C, r).
 struct RankArgs {
     const void *X, *F;
     const int32_t *adapters;
@@ -17,7 +17,8 @@ struct RankArgs {
     int r;
     bool across;
 };
-cudaError_t launch_lora_rank(const RankArgs &a, cudaStream_t s);
+// For a few rows: not across, C a multiple of 8, X's and F's rows 16-byte aligned.
+cudaError_t launch_lora_few_rank(const RankArgs &a, cudaStream_t s);
 
 // The same on the tensor cores.
 struct LoraRankArgs {
@@ -32,6 +33,23 @@ struct LoraRankArgs {
     int cluster, chunk, block_bytes, stages, stage_bytes, ring_bytes, tmem_cols;
 };
 cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const ErrCtx &err, cudaStream_t s);
+
+// D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] for at most
+// kLoraFewRows rows.
+constexpr int kLoraFewRows = 64;
+struct LoraFewArgs {
+    CUtensorMap tmW;           // (N, K): 128 rows of 64
+    CUtensorMap tmX;           // (M, K): shape.tp rows of 64
+    const void *U, *F;         // rows of ldu, and (L, N) rows of ldf, both 16-byte aligned
+    void *D;
+    const int32_t *adapters;
+    const float *bias;
+    const void *residual;
+    int64_t ldu, ldf, ldd, ld_residual;
+    int M, N, K, L, r;
+    FewShape shape;            // tp; the rest is set by the launch
+};
+cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 // D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] on CTA pairs, or with
 // W (K, N) and F (L, r, N) given along their rows (`maj`).

@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
     }
-    grid_release();
     grid_wait();
+    grid_release();                  // only now: lora_few_kernel reads x without a wait
     if (warp == 0) {
         // the tile's adapters, smallest first, and the lanes that each leaves out
         RowAdapters<4> of;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
     }
     // ------------------------- this CTA's share of the rows, eight ranks at a time
     __nv_bfloat16 *U = static_cast<__nv_bfloat16 *>(p.U);
-    const int64_t limit = (p.M - 1) * p.ldu + p.r;
+    const int64_t limit = p.M * p.ldu;
     const int share = kRkRows / S, groups = ceil_div(p.r, 8);
     for (int i = threadIdx.x; i < share * groups; i += kRkThreads) {
         const int row = static_cast<int>(rank) * share + i % share, j0 = i / share * 8;
@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
         if (on)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] *= scale;
+                v[j] = j0 + j < p.r ? v[j] * scale : 0.f;        // zeros in the columns that pad a row
         store_piece(U, m * p.ldu + j0,
                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])),
-                    min(8, p.r - j0), limit, err);
+                    static_cast<int>(min(static_cast<int64_t>(8), p.ldu - j0)), limit, err);
     }
     __syncwarp();
     cluster_sync();                  // no CTA leaves while its partial sums may be read

@@ -27,9 +27,7 @@
 // first one lets it start only after its own wait for the kernel before: so logits and
 // weights are complete by then.
 #include "act.cuh"
-#include "feed.cuh"
-#include "launch.cuh"
-#include "lora.cuh"
+#include "few.cuh"
 #include "moe_few.h"
 #include "pieces.cuh"
 #include "route.cuh"
@@ -39,14 +37,9 @@ namespace tmg {
 namespace {
 
 constexpr int kFwThreads = 256;
-constexpr int kFwMaxStages = 12;
-constexpr int kFwRing = 96 * 1024;
-constexpr int kFwWeights = 16384;            // 128 weight rows of a K block
 
-struct FewSmem {
-    uint64_t full[kFwMaxStages], empty[kFwMaxStages], done;
-    uint32_t tmem_slot;
-    int abort, chosen;                       // chosen: experts with a token
+struct FewSmem : FewRing {
+    int chosen;                              // experts with a token
     float weights[kFewTokens * kFewChoices];
     int32_t experts[kFewTokens * kFewChoices];
     int32_t counts[kFewExperts];
@@ -98,138 +91,6 @@ __device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
             atomicOr(&sm.tokens[sm.counts[e]][t >> 5], 1u << (t & 31));
     }
     __syncthreads();
-}
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(mapa_shared(addr, rank))
-                 : "memory");
-    return v;
-}
-
-// Eight consecutive columns of token t of the cluster's S partial tiles.
-__device__ __forceinline__ void few_sum(uint32_t part, int t, int col, uint32_t S, float (&z)[8])
-{
-    const uint32_t at = part + (t * 128 + col) * 4;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        z[i] = 0.f;
-#pragma unroll 4
-    for (uint32_t s = 0; s < S; ++s) {
-        const float4 a = ld_cluster_f32x4(at, s), b = ld_cluster_f32x4(at + 16, s);
-        z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
-        z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
-    }
-}
-
-__device__ __forceinline__ uint32_t few_cluster_size()
-{
-    uint32_t n;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-    return n;
-}
-
-// Barriers, TMEM.
-__device__ __forceinline__ void few_setup(const MoeFewArgs &p, FewSmem &sm, const CUtensorMap *weights, const CUtensorMap *rows)
-{
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 1);
-        }
-        mbar_init(&sm.done, 1);
-        sm.abort = 0;
-        fence_mbar_init();
-    }
-    if (warp == 0 && lane < 2)
-        tma_prefetch_desc(lane ? rows : weights);
-    if (warp == 1) {
-        tmem_alloc(&sm.tmem_slot, p.tmem_cols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-}
-
-// The contraction of K blocks kb0 .. kb1 - 1 by warps 0 (weights' producer), 1 (MMA) and
-// 2 (rows' producer), then warps 4..7 put the accumulator into the partial tile
-// [token][128], over the ring.  load_weights(dst, bar, kb), load_rows(dst, bar, kb): the
-// copies of a K block, by a whole warp; wait_rows(): before the first of the rows.
-template <class LoadWeights, class LoadRows, class WaitRows>
-__device__ __forceinline__ void few_product(const MoeFewArgs &p, FewSmem &sm, uint8_t *ring, int kb0, int kb1,
-                                            LoadWeights &&load_weights, LoadRows &&load_rows, WaitRows &&wait_rows, const ErrCtx &err)
-{
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    volatile int *abort_flag = &sm.abort;
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
-    if (warp == 0 || warp == 2) {
-        const uint32_t tx = kFwWeights + static_cast<uint32_t>(p.tp) * 128u;
-        if (warp == 2)
-            wait_rows();
-        for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-            if (!mbar_wait_warp(&sm.empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty))
-                break;
-            uint8_t *at = ring + stage * p.stage_bytes;
-            if (warp == 0) {
-                mbar_arrive_expect_tx_w(&sm.full[stage], tx);
-                load_weights(at, &sm.full[stage], kb);
-            } else {
-                load_rows(at + kFwWeights, &sm.full[stage], kb);
-            }
-            if (++stage == p.stages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-    } else if (warp == 1) {
-        const uint32_t idesc = idesc_bf16_f32(128, p.tp);
-        for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait_warp(&sm.full[stage], phase, err, abort_flag, kSiteMmaFull))
-                break;
-            tc_fence_after();
-            const uint32_t w_s = smem_u32(ring + stage * p.stage_bytes);
-            const uint64_t wdesc = sdesc_kmajor_sw128(w_s), rdesc = sdesc_kmajor_sw128(w_s + kFwWeights);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_bf16_w(sm.tmem_slot, wdesc + k * 2, rdesc + k * 2, idesc, (kb != kb0) || (k != 0));
-            mma_commit_w(&sm.empty[stage]);
-            if (++stage == p.stages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-        mma_commit_w(&sm.done);
-    } else if (warp >= 4 && mbar_wait_warp(&sm.done, 0, err, abort_flag, kSiteEpiTmemFull)) {
-        tc_fence_after();
-        const int q = warp & 3;
-        const uint32_t part = smem_u32(ring);
-        for (int c = 0; c < p.tp; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(sm.tmem_slot + (static_cast<uint32_t>(q * 32) << 16) + c, r);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(part + ((c + j) * 128 + q * 32 + lane) * 4), "r"(kb0 < kb1 ? r[j] : 0u)
-                             : "memory");
-        }
-        tc_fence_before();
-    }
-    __syncwarp();
-    cluster_sync();                  // every CTA's partial tile is written
-    if (warp < 2 && *abort_flag) {
-        if (warp == 0)               // rows and weights share the stages' barriers
-            settle(sm.full, p.stages, stage, phase, issued, err.word, err.budget_ns);
-        else
-            settle(&sm.done, 1, 0, 1, 1, err.word, err.budget_ns);
-        __syncwarp();
-    }
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(sm.tmem_slot, p.tmem_cols);
-    }
 }
 
 // What a CTA of the first kernel does: whole tiles in turn, or, where those would leave
@@ -294,7 +155,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
     __shared__ int arrived;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    float *staged = reinterpret_cast<float *>(ring + p.ring_bytes);        // a tile's sums [token][128]
+    float *staged = reinterpret_cast<float *>(ring + p.shape.ring_bytes);        // a tile's sums [token][128]
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     volatile int *abort_flag = &sm.abort;
     if (threadIdx.x == 0)
@@ -302,7 +163,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 4);
         }
-    few_setup(p, sm, &p.tmW1, &p.tmX);
+    few_setup(p.shape, sm, &p.tmW1, &p.tmX);
     grid_wait();
     grid_release();
     few_choose<C, BF16>(p, sm);
@@ -317,7 +178,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t tx = kFwWeights + static_cast<uint32_t>(p.tp) * 128u;
+        const uint32_t tx = kFwWeights + static_cast<uint32_t>(p.shape.tp) * 128u;
         while (ok && walk.next(tile, kb0, kb1)) {
             const int e = sm.list[tile / f_tiles], f0 = tile % f_tiles * 64;
             for (int kb = kb0; kb < kb1; ++kb, ++issued) {
@@ -325,7 +186,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
                     ok = false;
                     break;
                 }
-                uint8_t *at = ring + stage * p.stage_bytes;
+                uint8_t *at = ring + stage * p.shape.stage_bytes;
                 if (warp == 0) {
                     mbar_arrive_expect_tx_w(&sm.full[stage], tx);
                     tma_load_3d_one(at, &p.tmW1, &sm.full[stage], kb * 64, f0, e);
@@ -333,21 +194,21 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
                 } else {
                     tma_load_2d_w(at + kFwWeights, &p.tmX, &sm.full[stage], kb * 64, 0);
                 }
-                if (++stage == p.stages) {
+                if (++stage == p.shape.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
         }
-        for (int i = 0; i < p.stages && i < issued; ++i) {          // every stage is released
+        for (int i = 0; i < p.shape.stages && i < issued; ++i) {          // every stage is released
             const int s = stage - 1 - i;
-            mbar_wait(&sm.empty[s < 0 ? s + p.stages : s], s < 0 ? phase ^ 1u : phase, err, abort_flag, kSiteDrain);
+            mbar_wait(&sm.empty[s < 0 ? s + p.shape.stages : s], s < 0 ? phase ^ 1u : phase, err, abort_flag, kSiteDrain);
         }
         if (*abort_flag && warp == 0)
-            settle(sm.full, p.stages, stage, phase, min(issued, p.stages), err.word, err.budget_ns);
+            settle(sm.full, p.shape.stages, stage, phase, min(issued, p.shape.stages), err.word, err.budget_ns);
     } else if (warp == 1) {
         // -------------------------------------------- MMA issuer
-        const uint32_t idesc = idesc_bf16_f32(128, p.tp);
+        const uint32_t idesc = idesc_bf16_f32(128, p.shape.tp);
         int stage = 0, local = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -364,13 +225,13 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
                     break;
                 }
                 tc_fence_after();
-                const uint32_t w_s = smem_u32(ring + stage * p.stage_bytes);
+                const uint32_t w_s = smem_u32(ring + stage * p.shape.stage_bytes);
                 const uint64_t wdesc = sdesc_kmajor_sw128(w_s), rdesc = sdesc_kmajor_sw128(w_s + kFwWeights);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_bf16_w(tmem + acc * 64, wdesc + k * 2, rdesc + k * 2, idesc, (kb != kb0) || (k != 0));
                 mma_commit_w(&sm.empty[stage]);
-                if (++stage == p.stages) {
+                if (++stage == p.shape.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -380,12 +241,12 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
             mma_commit_w(&tfull[acc]);
         }
         if (*abort_flag)
-            settle(sm.empty, p.stages, stage, phase, 1, err.word, err.budget_ns);
+            settle(sm.empty, p.shape.stages, stage, phase, 1, err.word, err.budget_ns);
     } else if (warp >= 4) {
         // ---------------------------------------------------- epilogue
-        const int q = warp & 3, id = threadIdx.x - 128, piece = p.tp * 128;
+        const int q = warp & 3, id = threadIdx.x - 128, piece = p.shape.tp * 128;
         __nv_bfloat16 *hidden = static_cast<__nv_bfloat16 *>(p.hidden);
-        const int64_t limit = static_cast<int64_t>(min(p.E, p.T * p.k)) * p.tp * p.F, p_limit = 2ll * ctas * piece;
+        const int64_t limit = static_cast<int64_t>(min(p.E, p.T * p.k)) * p.shape.tp * p.F, p_limit = 2ll * ctas * piece;
         int local = 0;
         while (walk.next(tile, kb0, kb1)) {
             const int acc = local & 1, i = tile / f_tiles, e = sm.list[i], f0 = tile % f_tiles * 64;
@@ -399,7 +260,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
             const bool there = mbar_wait_warp(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull);
             tc_fence_after();
             if (there)
-                for (int c = 0; c < p.tp; c += 16) {
+                for (int c = 0; c < p.shape.tp; c += 16) {
                     uint32_t r[16];
                     tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 64 + c, r);
 #pragma unroll
@@ -432,7 +293,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
                     continue;
             }
             // sum, SwiGLU, weight: eight columns of a token per thread
-            for (int x = id; x < p.tp * 8; x += 128) {
+            for (int x = id; x < p.shape.tp * 8; x += 128) {
                 const int t = x / 8, c = x % 8 * 8, f = f0 + c, n = min(8, p.F - f);
                 if (n <= 0)
                     continue;
@@ -460,7 +321,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
                     for (int j = 0; j < 8; ++j)
                         g[j] = w * (silu_f(g[j]) * u[j]);
                 }
-                store_piece(hidden, (static_cast<int64_t>(i) * p.tp + t) * p.F + f,
+                store_piece(hidden, (static_cast<int64_t>(i) * p.shape.tp + t) * p.F + f,
                             make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])),
                             n, limit, err);
             }
@@ -472,7 +333,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, p.tmem_cols);
+        tmem_dealloc(tmem, p.shape.tmem_cols);
     }
 }
 
@@ -485,7 +346,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_c
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t rank = cluster_ctarank(), S = few_cluster_size();
     const int n0 = blockIdx.x / S * 128;
-    few_setup(p, sm, &p.tmW2, &p.tmHidden);
+    few_setup(p.shape, sm, &p.tmW2, &p.tmHidden);
     grid_release();
     few_choose<C, BF16>(p, sm);
     tc_fence_after();
@@ -493,10 +354,10 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_c
     const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
     few_product(
-        p, sm, ring, kb0, kb1,
+        p.shape, sm, ring, kb0, kb1,
         [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_3d_one(dst, &p.tmW2, bar, kb % per * 64, n0, sm.list[kb / per]); },
         [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_3d_one(dst, &p.tmHidden, bar, kb % per * 64, 0, kb / per); },
-        [] { grid_wait(); }, err);
+        [] { grid_wait(); }, [] {}, err);
     grid_wait();                     // every warp: the first kernel's hidden rows
     // ------------------------- this CTA's share: sum, residual
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
@@ -518,7 +379,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_c
                 for (int i = 0; i < sm.chosen; ++i)
                     if (sm.tokens[i][t >> 5] >> (t & 31) & 1u) {
                         const __nv_bfloat16 *w = W2 + (static_cast<int64_t>(sm.list[i]) * p.H + col + j) * p.F;
-                        const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.tp + t) * p.F;
+                        const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.shape.tp + t) * p.F;
                         for (int f = 0; f < p.F; ++f)
                             sum = fmaf(__bfloat162float(w[f]), __bfloat162float(h[f]), sum);
                     }
@@ -549,30 +410,13 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_c
     cluster_sync();                  // no CTA leaves while its partial sums may be read
 }
 
-// CTAs that share a tile: two CTAs per SM, four K blocks each at least.
-int few_cluster(int64_t tiles, int64_t num_kb, int num_sms)
-{
-    int S = 1;
-    while (S < 8 && 2 * S * tiles <= 2 * num_sms && num_kb >= 8 * S)
-        S *= 2;
-    return S;
-}
-
-// The ring's stages within `bytes`.
-void few_ring(MoeFewArgs &a, int bytes)
-{
-    a.stage_bytes = kFwWeights + a.tp * 128;
-    a.stages = bytes / a.stage_bytes < kFwMaxStages ? bytes / a.stage_bytes : kFwMaxStages;
-    a.ring_bytes = a.stages * a.stage_bytes;
-}
-
 template <int C, bool BF16>
 cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
     MoeFewArgs b = a;
-    few_ring(a, kFwRing);
-    few_ring(b, kFwRing);
-    const int smem = 1024 + b.ring_bytes, smem_up = 1024 + a.ring_bytes + a.tp * 512;
+    few_ring(a.shape, kFwRing);
+    few_ring(b.shape, kFwRing);
+    const int smem = 1024 + b.shape.ring_bytes, smem_up = 1024 + a.shape.ring_bytes + a.shape.tp * 512;
     auto up = moe_few_up_kernel<C, BF16>;
     auto down = moe_few_down_kernel<C, BF16>;
     cudaError_t e;
@@ -598,7 +442,7 @@ size_t moe_few_partial_bytes(int tp, int num_sms) { return static_cast<size_t>(n
 
 cudaError_t launch_moe_few(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    a.tmem_cols = 128;
+    a.shape.tmem_cols = 128;
     return a.E <= 64    ? launch_few_of<2>(a, num_sms, err, s)
            : a.E <= 128 ? launch_few_of<4>(a, num_sms, err, s)
                         : launch_few_of<8>(a, num_sms, err, s);

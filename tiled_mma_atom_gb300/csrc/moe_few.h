@@ -2,7 +2,7 @@
 // tokens (moe_few.cu).
 #pragma once
 
-#include "internal.h"
+#include "few.cuh"
 
 namespace tmg {
 
@@ -19,11 +19,9 @@ struct MoeFewArgs {
     int64_t ld_logits, ld_residual, ld_out;
     int T, H, F, E, k, normalize;
     bool bf16;                 // the logits
-    int tp;                    // T rounded up to 16
     float *partials;           // moe_few_partial_bytes()
     uint32_t *counters;        // one per SM, zero between launches
-    // set by the launch
-    int stages, stage_bytes, ring_bytes, tmem_cols;
+    FewShape shape;            // tp; the rest is set by the launch
 };
 size_t moe_few_partial_bytes(int tp, int num_sms);
 cudaError_t launch_moe_few(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
