@@ -129,7 +129,7 @@ tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cud
 {
     if (a.C == 0)
         return launched(cudaMemsetAsync(a.U, 0, static_cast<size_t>(a.M) * a.ldu * 2, s), "cudaMemsetAsync(u)");
-    if (a.M <= kLoraFewRows && !a.across && a.C % 8 == 0 && aligned(a.F)) {
+    if (a.M <= kLoraFewRows && a.r <= kLoraFewRanks && !a.across && a.C % 8 == 0 && aligned(a.F)) {
         RankArgs b = a;
         b.X = x.p;
         b.ldx = x.ld;
@@ -423,7 +423,7 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
         Rows x;
         if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK)
             return st;
-        const bool few = g->M <= kLoraFewRows;
+        const bool few = g->M <= kLoraFewRows && g->r <= kLoraFewRanks;
         Rows W{}, B{};
         if (few && g->N > 0 &&
             ((st = tma_rows(*ds, kWsPackB, g->W, g->ldw, g->N, g->K, g->N, s, &W)) != TMG_OK ||

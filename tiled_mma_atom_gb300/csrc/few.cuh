@@ -172,11 +172,11 @@ inline void few_ring(FewShape &a, int bytes)
     a.ring_bytes = a.stages * a.stage_bytes;
 }
 
-// CTAs that share a tile: two CTAs per SM, four K blocks each at least.
-inline int few_cluster(int64_t tiles, int64_t num_kb, int num_sms)
+// CTAs that share a tile: `ctas` in all at most, four K blocks each at least.
+inline int few_cluster(int64_t tiles, int64_t num_kb, int ctas)
 {
     int S = 1;
-    while (S < 8 && 2 * S * tiles <= 2 * num_sms && num_kb >= 8 * S)
+    while (S < 8 && 2 * S * tiles <= ctas && num_kb >= 8 * S)
         S *= 2;
     return S;
 }

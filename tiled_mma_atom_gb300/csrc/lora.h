@@ -35,8 +35,9 @@ struct LoraRankArgs {
 cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 // D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] for at most
-// kLoraFewRows rows.
-constexpr int kLoraFewRows = 64;
+// kLoraFewRows rows and kLoraFewRanks ranks (the factors of 32 columns of every warp,
+// U and the results must fit shared memory beside the ring).
+constexpr int kLoraFewRows = 64, kLoraFewRanks = 128;
 struct LoraFewArgs {
     CUtensorMap tmW;           // (N, K): 128 rows of 64
     CUtensorMap tmX;           // (M, K): shape.tp rows of 64
@@ -48,6 +49,7 @@ struct LoraFewArgs {
     int64_t ldu, ldf, ldd, ld_residual;
     int M, N, K, L, r;
     FewShape shape;            // tp; the rest is set by the launch
+    int room_bytes;            // set by the launch
 };
 cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 

@@ -1,13 +1,12 @@
 // lora_few.cu — the dense product with low-rank adapters for a few rows (decoding): W
 // is read once, every row has an adapter of its own.
 //
-// First kernel: U[m][j], a warp per (row, rank), 16 bytes of X and F per lane and load.
-// Second kernel: W's product as in few.cuh, for which nothing but x is needed, so it
-// starts while the first one runs and waits for U only in the warps that add the
-// adapters' share: those form U[m] . F[a_m][n] for the results of their CTA, a thread
-// per result, while W's blocks come in.  The first kernel lets the second one start
-// only after its own wait for the kernel before, so x and the weights are complete
-// by then.
+// First kernel: U[m][j], one to eight warps per (row, rank), 16 bytes of X and F per
+// lane and load.  Second kernel: W's product as in few.cuh, for which nothing but x is
+// needed, so it starts while the first one runs and waits for U only in the eight warps
+// that add the adapters' share, whose factors they fetch meanwhile.  The first kernel
+// lets the second one start only after its own wait for the kernel before, so x and
+// the weights are complete by then.
 //
 // Bound by HBM: W and the rows' factors once.
 #include <cuda_bf16.h>
@@ -18,8 +17,10 @@
 namespace tmg {
 namespace {
 
-constexpr int kLfThreads = 384;
-constexpr int kLfRanks = 8;                  // ranks (warps) of a block of the first kernel
+constexpr int kLfThreads = 384, kLfWarps = 8;       // warps 4 .. 11 form the adapters' share
+constexpr int kLfMaxDepth = 8;
+constexpr int kLfSmem = 108 * 1024;          // of a CTA, where two share an SM
+constexpr int kLfBuffer = 4096;              // a warp's room for factors, at least one unit of 32 columns
 
 __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
 {
@@ -32,40 +33,58 @@ __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
     return sum;
 }
 
-__global__ void __launch_bounds__(kLfRanks * 32) lora_few_rank_kernel(RankArgs a, int groups)
+// A row's rank per `parts` warps of the block (a power of two), each with a run of C.
+// Every load of up to 2048 elements a warp is in flight before the next kernel may
+// start: behind its flood of W's blocks they would take 5 us and more.
+__global__ void __launch_bounds__(256) lora_few_rank_kernel(RankArgs a, int parts, int ranks)
 {
+    __shared__ float part[8];
     grid_wait();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t unit = blockIdx.x * static_cast<int64_t>(8 / parts) + warp / parts;
+    const int64_t m = unit / ranks;
+    const int j = static_cast<int>(unit % ranks), p = warp % parts;
+    const int l = m < a.M ? a.adapters[m] : -1;
+    const bool on = l >= 0 && l < a.L && j < a.r;        // columns past r pad a row: zeros
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.X) + (on ? m * a.ldx : 0));
+    const uint4 *f = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.F) +
+                                                     (on ? (static_cast<int64_t>(l) * a.r + j) * a.C : 0));
+    const int n = on ? static_cast<int>(a.C / 8) : 0;
+    float sum = 0.f;
+    uint4 v[8], w[8];
+    auto load = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = c + 32 * i < n ? f[c + 32 * i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = c + 32 * i < n ? x[c + 32 * i] : make_uint4(0, 0, 0, 0);
+    };
+    int c = p * 256 + lane;
+    load(c);
     grid_release();
-    const int64_t m = blockIdx.x / groups;
-    const int j = blockIdx.x % groups * kLfRanks + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (j >= a.r && j >= a.ldu)
-        return;
-    const int l = a.adapters[m];
-    float sum = 0.f;                     // also in the columns past r that pad a row
-    if (l >= 0 && l < a.L && j < a.r) {
-        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.X) + m * a.ldx);
-        const uint4 *f = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.F) + (static_cast<int64_t>(l) * a.r + j) * a.C);
-        const int n = static_cast<int>(a.C / 8);
-        for (int c = lane; c < n; c += 256) {
-            uint4 v[8], w[8];
+    for (;;) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool in = c + 32 * i < n;
-                v[i] = in ? f[c + 32 * i] : make_uint4(0, 0, 0, 0);
-                w[i] = in ? x[c + 32 * i] : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sum = dot8(v[i], w[i], sum);
-        }
-        if (a.scales)
-            sum *= a.scales[l];
+        for (int i = 0; i < 8; ++i)
+            sum = dot8(v[i], w[i], sum);
+        c += parts * 256;
+        if (c - lane >= n)
+            break;
+        load(c);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0)
-        static_cast<__nv_bfloat16 *>(a.U)[m * a.ldu + j] = __float2bfloat16_rn(sum);
+        part[warp] = sum;
+    __syncthreads();
+    if (lane != 0 || p != 0 || m >= a.M)
+        return;
+    for (int i = 1; i < parts; ++i)
+        sum += part[warp + i];
+    if (on && a.scales)
+        sum *= a.scales[l];
+    static_cast<__nv_bfloat16 *>(a.U)[m * a.ldu + j] = __float2bfloat16_rn(sum);
 }
 
 __device__ __forceinline__ float ld_cluster_one(uint32_t addr, uint32_t rank)
@@ -75,68 +94,116 @@ __device__ __forceinline__ float ld_cluster_one(uint32_t addr, uint32_t rank)
     return v;
 }
 
+// Warps 4 .. 11.  The results of this CTA in units of 32 columns of a row, a warp's
+// in turn: their factor rows, 32 x ldf contiguous elements, come by bulk copies, as
+// many units ahead as the warp's room holds and the first ones before U is there.
+// share[] = U[m] . F[a_m][n] + bias + residual.  A lane takes the 16-byte chunks of
+// its factor row from a start of its own, so that eight lanes touch all banks.
+__device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *room, uint64_t *bars, __nv_bfloat16 *us, float *share,
+                                               int n0, int first, int last, volatile int *abort_flag, const ErrCtx &err)
+{
+    const int warp = threadIdx.x / 32 - 4, lane = threadIdx.x % 32;
+    const int unit_bytes = static_cast<int>(32 * p.ldf * 2), depth = p.room_bytes / unit_bytes, chunks = static_cast<int>(p.ldf / 8);
+    const __nv_bfloat16 *U = static_cast<const __nv_bfloat16 *>(p.U), *F = static_cast<const __nv_bfloat16 *>(p.F);
+    const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
+    uint32_t pending = 0;                                // slots with a copy under way
+    // copy unit x's factor rows (of columns inside N) if its row has an adapter
+    auto fetch = [&](int x, int slot) {
+        const int m = x / 4, n = n0 + x % 4 * 32, l = p.adapters[m];
+        if (n >= p.N || l < 0 || l >= p.L)
+            return;
+        pending |= 1u << slot;
+        const uint32_t bytes = static_cast<uint32_t>(min(32, p.N - n)) * static_cast<uint32_t>(p.ldf * 2);
+        mbar_arrive_expect_tx_w(&bars[slot], bytes);
+        bulk_load_w(room + slot * unit_bytes, F + (static_cast<int64_t>(l) * p.N + n) * p.ldf, bytes, &bars[slot]);
+    };
+    for (int d = 0; d < depth && first + warp + d * kLfWarps < last; ++d)
+        fetch(first + warp + d * kLfWarps, d);
+    const int m0 = first / 4, rows = last > first ? (last - 1) / 4 - m0 + 1 : 0;
+    grid_wait();                                         // U
+    const int per = static_cast<int>(p.ldu / 8);
+    for (int i = threadIdx.x - 128; i < rows * per; i += kLfWarps * 32)
+        reinterpret_cast<uint4 *>(us)[i] = __ldcg(reinterpret_cast<const uint4 *>(U + (m0 + i / per) * p.ldu) + i % per);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    uint32_t phases = 0;                                 // of the slots
+    int slot = 0;
+    for (int x = first + warp; x < last; x += kLfWarps) {
+        const int m = x / 4, n = n0 + x % 4 * 32 + lane, l = p.adapters[m];
+        float sum = 0.f, add = 0.f;
+        if (n < p.N) {
+            add = p.bias ? p.bias[n] : 0.f;
+            if (res)
+                add += __bfloat162float(res[m * p.ld_residual + n]);
+        }
+        if (l >= 0 && l < p.L && n - lane < p.N) {
+            if (!mbar_wait_warp(&bars[slot], phases >> slot & 1u, err, abort_flag, kSiteMmaFull)) {
+                for (int d = 0; d < depth; ++d)          // leave when the copies have landed
+                    if (pending >> d & 1u)
+                        settle(&bars[d], 1, 0, phases >> d & 1u ? 0u : 1u, 1, err.word, err.budget_ns);
+                return;
+            }
+            phases ^= 1u << slot;
+            pending &= ~(1u << slot);
+            const uint4 *f = reinterpret_cast<const uint4 *>(room + slot * unit_bytes) + lane * chunks;
+            const uint4 *u = reinterpret_cast<const uint4 *>(us) + (m - m0) * per;
+            int k = (lane * chunks >> 3) % chunks;
+            if (n < p.N)
+                for (int i = 0; i < chunks; ++i) {
+                    sum = dot8(u[k], f[k], sum);
+                    k = k + 1 == chunks ? 0 : k + 1;
+                }
+        }
+        share[(x - first) * 32 + lane] = sum + add;
+        __syncwarp();
+        if (x + depth * kLfWarps < last)
+            fetch(x + depth * kLfWarps, slot);
+        slot = slot + 1 == depth ? 0 : slot + 1;
+    }
+}
+
 __global__ void __launch_bounds__(kLfThreads) lora_few_kernel(const __grid_constant__ LoraFewArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ FewRing sm;
+    __shared__ uint64_t bars[kLfWarps][kLfMaxDepth];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    float *share = reinterpret_cast<float *>(ring + p.shape.ring_bytes);   // the adapters' share of this CTA's results
+    uint8_t *room = ring + p.shape.ring_bytes;
+    __nv_bfloat16 *us = reinterpret_cast<__nv_bfloat16 *>(room + kLfWarps * p.room_bytes);
     const uint32_t rank = cluster_ctarank(), S = few_cluster_size();
-    const int n0 = blockIdx.x / S * 128, num_kb = ceil_div(p.K, 64);
+    const int n0 = blockIdx.x / S * 128, num_kb = ceil_div(p.K, 64), warp = threadIdx.x / 32;
     const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * rank / S);
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
+    // this CTA's results: units of 32 columns of a row
+    const int units = p.M * 4, first = units * rank / S, last = units * (rank + 1) / S;
+    float *share = reinterpret_cast<float *>(us + (ceil_div(last - first, 4) + 1) * p.ldu);
+    if (threadIdx.x < kLfWarps * kLfMaxDepth)
+        mbar_init(&bars[0][0] + threadIdx.x, 1);
     few_setup(p.shape, sm, &p.tmW, &p.tmX);
+    fence_mbar_init();
     grid_release();
     __syncthreads();
     tc_fence_after();
-    const int items = p.M * 128, first = items * rank / S, last = items * (rank + 1) / S;
     few_product(
         p.shape, sm, ring, kb0, kb1, [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_2d_w(dst, &p.tmW, bar, kb * 64, n0); },
         [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_2d_w(dst, &p.tmX, bar, kb * 64, 0); }, [] {},
         [&] {
-            grid_wait();                         // U
-            const __nv_bfloat16 *U = static_cast<const __nv_bfloat16 *>(p.U), *F = static_cast<const __nv_bfloat16 *>(p.F);
-            for (int x = first + static_cast<int>(threadIdx.x) - 128; x < last; x += kLfThreads - 128) {
-                const int m = x / 128, n = n0 + x % 128;
-                const int l = n < p.N ? p.adapters[m] : -1;
-                float sum = 0.f;
-                if (l >= 0 && l < p.L) {
-                    const __nv_bfloat16 *u = U + m * p.ldu, *f = F + (static_cast<int64_t>(l) * p.N + n) * p.ldf;
-                    for (int j = 0; j < p.r; j += 64) {
-                        uint4 a[8], b[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const bool in = j + 8 * i < p.r;
-                            b[i] = in ? *reinterpret_cast<const uint4 *>(f + j + 8 * i) : make_uint4(0, 0, 0, 0);
-                            a[i] = in ? __ldcg(reinterpret_cast<const uint4 *>(u + j + 8 * i)) : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            sum = dot8(a[i], b[i], sum);
-                    }
-                }
-                share[x - first] = sum;
-            }
+            adapters_share(p, room + (warp - 4) * p.room_bytes, bars[warp - 4], us, share, n0, first, last, &sm.abort, err);
         },
         err);
     grid_wait();                     // every warp: no later kernel may start before U's is done
-    const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
     __nv_bfloat16 *D = static_cast<__nv_bfloat16 *>(p.D);
     const int64_t limit = (p.M - 1) * p.ldd + p.N;
     const uint32_t part = smem_u32(ring);
-    for (int x = first + threadIdx.x; x < last; x += kLfThreads) {
+    for (int x = first * 32 + threadIdx.x; x < last * 32; x += kLfThreads) {
         const int m = x / 128, c = x % 128, n = n0 + c;
         if (n >= p.N)
             continue;
-        const float b = p.bias ? p.bias[n] : 0.f, e = res ? __bfloat162float(res[m * p.ld_residual + n]) : 0.f;
         float z = 0.f;
 #pragma unroll 8
         for (uint32_t s = 0; s < S; ++s)
             z += ld_cluster_one(part + (m * 128 + c) * 4, s);
-        z += share[x - first];
-        z += b;
-        z += e;
+        z += share[x - first * 32];
         const int64_t at = m * p.ldd + n;
         if (bounds_ok(at, limit, err, kBndStoreD))
             D[at] = __float2bfloat16_rn(z);
@@ -149,17 +216,32 @@ __global__ void __launch_bounds__(kLfThreads) lora_few_kernel(const __grid_const
 
 cudaError_t launch_lora_few_rank(const RankArgs &a, cudaStream_t s)
 {
-    const int groups = (a.r + kLfRanks - 1) / kLfRanks;
-    return launch_overlapped(lora_few_rank_kernel, dim3(static_cast<unsigned>(a.M * groups)), kLfRanks * 32, 0, 1, s, a, groups);
+    int parts = 1;
+    while (parts < 8 && a.C > 2048 * parts)
+        parts *= 2;
+    const int ranks = static_cast<int>(a.ldu > a.r && a.ldu < a.r + 8 ? a.ldu : a.r);
+    const int64_t blocks = (a.M * ranks + 8 / parts - 1) / (8 / parts);
+    return launch_overlapped(lora_few_rank_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, s, a, parts, ranks);
 }
 
 cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    few_ring(a.shape, kFwRing);
-    a.shape.tmem_cols = a.shape.tp <= 32 ? 32 : 64;
     const int64_t tiles = (a.N + 127) / 128;
-    const int S = few_cluster(tiles, (a.K + 63) / 64, num_sms);
-    const int smem = 1024 + a.shape.ring_bytes + (a.M * 128 / S + 1) * 4;
+    const int unit = static_cast<int>(32 * a.ldf * 2);
+    a.room_bytes = unit >= kLfBuffer ? unit : kLfBuffer / unit > kLfMaxDepth ? kLfMaxDepth * unit : kLfBuffer / unit * unit;
+    a.shape.tmem_cols = a.shape.tp <= 32 ? 32 : 64;
+    int S = 1, rest = 0;
+    for (int per_sm = 2; per_sm >= 1; --per_sm) {      // two CTAs per SM where two stages fit so, else one
+        S = few_cluster(tiles, (a.K + 63) / 64, per_sm * num_sms);
+        const int units = (a.M * 4 + S - 1) / S;       // of a CTA, at most
+        rest = kLfWarps * a.room_bytes + ((units + 3) / 4 + 1) * static_cast<int>(a.ldu) * 2 + units * 128;
+        few_ring(a.shape, 2 / per_sm * kLfSmem - rest);
+        if (a.shape.stages >= 2)
+            break;
+    }
+    if (a.shape.stages < 2)
+        return cudaErrorInvalidValue;                  // more ranks than kLoraFewRanks
+    const int smem = 1024 + a.shape.ring_bytes + rest;
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(lora_few_kernel), smem);
     if (e != cudaSuccess)
         return e;

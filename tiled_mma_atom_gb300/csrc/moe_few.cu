@@ -426,7 +426,7 @@ cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStre
     const int64_t downs = (a.H + 127) / 128;
     if ((e = launch_overlapped(up, dim3(static_cast<unsigned>(num_sms)), kFwThreads, smem_up, 1, s, a, err)) != cudaSuccess)
         return e;
-    const int s_down = few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), num_sms);
+    const int s_down = few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), 2 * num_sms);
     return launch_overlapped(down, dim3(static_cast<unsigned>(downs * s_down)), kFwThreads, smem, s_down, s, b, err);
 }
 
