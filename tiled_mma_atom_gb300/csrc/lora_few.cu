@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kLfThreads = 384, kLfWarps = 8;       // warps 4 .. 11 form the adapters' share
 constexpr int kLfMaxDepth = 8;
+constexpr int kLfManyWarps = 2432;           // of the ranks: two blocks of eight per SM
 constexpr int kLfSmem = 108 * 1024;          // of a CTA, where two share an SM
 constexpr int kLfBuffer = 4096;              // a warp's room for factors, at least one unit of 32 columns
 
@@ -33,58 +34,65 @@ __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
     return sum;
 }
 
-// A row's rank per `parts` warps of the block (a power of two), each with a run of C.
-// Every load of up to 2048 elements a warp is in flight before the next kernel may
-// start: behind its flood of W's blocks they would take 5 us and more.
-__global__ void __launch_bounds__(256) lora_few_rank_kernel(RankArgs a, int parts, int ranks)
+// J ranks of a row per `parts` warps of the block (a power of two), each with a run
+// of C.  Every load of up to 2048 elements a warp is in flight at once, about when the
+// next kernel starts: behind its flood of W's blocks they would take 5 us and more.
+// Two ranks a warp where there are many: a row's x is read half as often.
+template <int J>
+__global__ void __launch_bounds__(256, J == 1 ? 3 : 2) lora_few_rank_kernel(RankArgs a, int parts, int groups)
 {
-    __shared__ float part[8];
+    __shared__ float part[8][J];
     grid_wait();
+    grid_release();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t unit = blockIdx.x * static_cast<int64_t>(8 / parts) + warp / parts;
-    const int64_t m = unit / ranks;
-    const int j = static_cast<int>(unit % ranks), p = warp % parts;
+    const int64_t m = unit / groups;
+    const int j0 = static_cast<int>(unit % groups) * J, p = warp % parts;
     const int l = m < a.M ? a.adapters[m] : -1;
-    const bool on = l >= 0 && l < a.L && j < a.r;        // columns past r pad a row: zeros
+    const bool on = l >= 0 && l < a.L;
     const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.X) + (on ? m * a.ldx : 0));
-    const uint4 *f = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.F) +
-                                                     (on ? (static_cast<int64_t>(l) * a.r + j) * a.C : 0));
     const int n = on ? static_cast<int>(a.C / 8) : 0;
-    float sum = 0.f;
-    uint4 v[8], w[8];
-    auto load = [&](int c) {
+    const uint4 *f[J];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = c + 32 * i < n ? f[c + 32 * i] : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < J; ++j)                          // columns past r pad a row: zeros
+        f[j] = on && j0 + j < a.r ? reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.F) +
+                                                                    (static_cast<int64_t>(l) * a.r + j0 + j) * a.C)
+                                  : nullptr;
+    float sum[J] = {};
+    for (int c = p * 256 + lane; c - lane < n; c += parts * 256) {
+        uint4 v[J][8], w[8];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[j][i] = f[j] && c + 32 * i < n ? f[j][c + 32 * i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             w[i] = c + 32 * i < n ? x[c + 32 * i] : make_uint4(0, 0, 0, 0);
-    };
-    int c = p * 256 + lane;
-    load(c);
-    grid_release();
-    for (;;) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            sum = dot8(v[i], w[i], sum);
-        c += parts * 256;
-        if (c - lane >= n)
-            break;
-        load(c);
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum[j] = dot8(v[j][i], w[i], sum[j]);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0)
-        part[warp] = sum;
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+        if (lane == 0)
+            part[warp][j] = sum[j];
+    }
     __syncthreads();
-    if (lane != 0 || p != 0 || m >= a.M)
+    const int j = j0 + lane;
+    if (lane >= J || p != 0 || m >= a.M || (j >= a.r && j >= a.ldu))
         return;
-    for (int i = 1; i < parts; ++i)
-        sum += part[warp + i];
+    float u = 0.f;
+    for (int i = 0; i < parts; ++i)
+        u += part[warp + i][lane];
     if (on && a.scales)
-        sum *= a.scales[l];
-    static_cast<__nv_bfloat16 *>(a.U)[m * a.ldu + j] = __float2bfloat16_rn(sum);
+        u *= a.scales[l];
+    static_cast<__nv_bfloat16 *>(a.U)[m * a.ldu + j] = __float2bfloat16_rn(j < a.r ? u : 0.f);
 }
 
 __device__ __forceinline__ float ld_cluster_one(uint32_t addr, uint32_t rank)
@@ -220,8 +228,10 @@ cudaError_t launch_lora_few_rank(const RankArgs &a, cudaStream_t s)
     while (parts < 8 && a.C > 2048 * parts)
         parts *= 2;
     const int ranks = static_cast<int>(a.ldu > a.r && a.ldu < a.r + 8 ? a.ldu : a.r);
-    const int64_t blocks = (a.M * ranks + 8 / parts - 1) / (8 / parts);
-    return launch_overlapped(lora_few_rank_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, s, a, parts, ranks);
+    const int J = a.M * ranks * parts > kLfManyWarps ? 2 : 1, groups = (ranks + J - 1) / J;
+    const int64_t blocks = (a.M * groups + 8 / parts - 1) / (8 / parts);
+    return launch_overlapped(J == 1 ? lora_few_rank_kernel<1> : lora_few_rank_kernel<2>, dim3(static_cast<unsigned>(blocks)), 256, 0,
+                             1, s, a, parts, groups);
 }
 
 cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
