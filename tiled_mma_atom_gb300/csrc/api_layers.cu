@@ -122,14 +122,47 @@ tmg_status tma_rows(const DeviceState &ds, Workspace which, const void *src, int
     return st;
 }
 
-// U = bf16(scales X . F[adapters]^T), (M, r) with rows of ldu; x: X's rows as tma_rows
-// gave them.  A few rows by a warp per row and rank, where 16-byte loads read the
-// factors in place.
-tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cudaStream_t s)
+// One side of the factors' gradients: G from Y (M, C) and Z (M, r).
+tmg_status grad_side(LoraGradSide &g, const Rows &Y, int64_t C, const Rows &Z, int64_t M, int64_t r, void *G, bool across)
+{
+    tmg_status st;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t yd[2] = {C, M}, ys[1] = {Y.ld * 2}, zd[2] = {r, M}, zs[1] = {Z.ld * 2};
+        const int box[2] = {64, i == 0 ? 64 : i == 1 ? 16 : 1};
+        if ((st = encode_nd(&g.tmY[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y.p, yd, ys, box)) != TMG_OK ||
+            (st = encode_nd(&g.tmZ[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Z.p, zd, zs, box, true)) != TMG_OK)
+            return st;
+    }
+    g.G = G;
+    g.C = static_cast<int>(C);
+    g.across = across;
+    return TMG_OK;
+}
+
+tmg_status run_grad(const DeviceState &ds, LoraGradArgs &p, cudaStream_t s)
+{
+    tmg_status st;
+    p.partials = static_cast<float *>(workspace(kWsPartials, lora_grad_partial_bytes(p, ds.num_sms), s, &st));
+    if (!p.partials || (st = arrival_counters(lora_grad_counters(p, ds.num_sms), s, &p.counters)) != TMG_OK)
+        return st;
+    return launched(launch_lora_grad(p, ds.num_sms, err_ctx(ds), s), "adapter gradient launch");
+}
+
+// A few rows' ranks: a warp per row and rank, where 16-byte loads read the factors in
+// place.
+bool few_ranks(const RankArgs &a)
+{
+    return a.M <= kLoraFewRows && a.r <= kLoraFewRanks && !a.across && a.C % 8 == 0 && aligned(a.F);
+}
+
+// U = bf16(scales X . F[adapters]^T), (M, r) with rows of ldu; x, f: X's and F's rows
+// as tma_rows gave them, f only where few_ranks() does not hold.  beside: the kernel
+// before is launch_lora_plan's.
+tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, const Rows &f, bool beside, cudaStream_t s)
 {
     if (a.C == 0)
         return launched(cudaMemsetAsync(a.U, 0, static_cast<size_t>(a.M) * a.ldu * 2, s), "cudaMemsetAsync(u)");
-    if (a.M <= kLoraFewRows && a.r <= kLoraFewRanks && !a.across && a.C % 8 == 0 && aligned(a.F)) {
+    if (few_ranks(a)) {
         RankArgs b = a;
         b.X = x.p;
         b.ldx = x.ld;
@@ -137,9 +170,6 @@ tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cud
     }
     tmg_status st;
     const int64_t rows = a.across ? a.C : a.r, cols = a.across ? a.r : a.C;
-    Rows f;
-    if ((st = tma_rows(ds, kWsFactor, a.F, cols, a.L * rows, cols, a.L * rows, s, &f)) != TMG_OK)
-        return st;
     LoraRankArgs p;
     std::memset(&p, 0, sizeof p);
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -156,51 +186,22 @@ tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, cud
     p.C = static_cast<int>(a.C);
     p.L = static_cast<int>(a.L);
     p.r = a.r;
+    p.beside = beside;
     return launched(launch_lora_rank_tc(p, a.across, ds.num_sms, err_ctx(ds), s), "adapter rank launch");
-}
-
-// G = the factors' gradient from Y (M, C) and Z (M, r), rows as tma_rows gave them.
-tmg_status run_factor_grad(const DeviceState &ds, const Rows &Y, int64_t C, const Rows &Z, int64_t M, int64_t L, int64_t r,
-                           const int32_t *offsets, const int32_t *rows, void *G, bool across, cudaStream_t s)
-{
-    tmg_status st;
-    LoraGradArgs p;
-    std::memset(&p, 0, sizeof p);
-    for (int i = 0; i < 3; ++i) {
-        const int64_t yd[2] = {C, M}, ys[1] = {Y.ld * 2}, zd[2] = {r, M}, zs[1] = {Z.ld * 2};
-        const int box[2] = {64, i == 0 ? 64 : i == 1 ? 16 : 1};
-        if ((st = encode_nd(&p.tmY[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y.p, yd, ys, box)) != TMG_OK ||
-            (st = encode_nd(&p.tmZ[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Z.p, zd, zs, box, true)) != TMG_OK)
-            return st;
-    }
-    p.G = G;
-    p.offsets = offsets;
-    p.rows = rows;
-    p.M = static_cast<int>(M);
-    p.C = static_cast<int>(C);
-    p.L = static_cast<int>(L);
-    p.r = static_cast<int>(r);
-    p.across = across;
-    p.partials = static_cast<float *>(workspace(kWsPartials, lora_grad_partial_bytes(M, C, p.r, ds.num_sms), s, &st));
-    if (!p.partials)
-        return st;
-    if ((st = arrival_counters(lora_grad_counters(M, C, ds.num_sms), s, &p.counters)) != TMG_OK)
-        return st;
-    return launched(launch_lora_grad(p, ds.num_sms, err_ctx(ds), s), "adapter gradient launch");
 }
 
 // D = x . W^T + U . F[adapters]^T + bias + residual.  The factors' own strides are
 // their contiguous ones; across: W is (K, N), F (L, r, N), as the input's gradient has
 // them.
 struct AdaptedArgs {
-    Rows x;                    // as tma_rows gave them
-    const void *W, *U, *F;
+    Rows x, W, F;              // as tma_rows gave them, before the kernel that makes U
+    const void *U;
     void *D;
     const int32_t *adapters;
     const float *bias;
     const void *residual;
     int64_t M, N, K, r, L;
-    int64_t ldw, ldu, ldd, ld_residual;
+    int64_t ldu, ldd, ld_residual;
     bool across;
 };
 
@@ -215,21 +216,15 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     const int bn = a.across ? tc2_pick_bn_of(a.M, a.N, K, 64, ds.num_sms, wide, 2) : tc2_pick_bn(a.M, a.N, K, ds.num_sms);
     if ((a.M + 255) / 256 * ((a.N + bn - 1) / bn) > kMax31)
         return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
-    Rows W, f;
-    const int64_t wrows = a.across ? a.K : a.N, wcols = a.across ? a.N : a.K;
-    if ((st = tma_rows(ds, kWsPackB, a.W, a.ldw, wrows, wcols, a.across ? K : a.N, s, &W)) != TMG_OK)
-        return st;
     const int64_t frows = a.across ? a.r : a.N, fcols = a.across ? a.N : a.r;
-    if ((st = tma_rows(ds, kWsFactor, a.F, fcols, a.L * frows, fcols, a.L * frows, s, &f)) != TMG_OK)
-        return st;
     const int64_t xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2}, ud[2] = {a.r, a.M}, us[1] = {a.ldu * 2};
     const int rows[2] = {64, 128}, half[3] = {64, a.across ? 64 : bn / 2, 1};
-    const int64_t wd[2] = {a.across ? a.N : K, a.across ? K : a.N}, wst[1] = {W.ld * 2};
-    const int64_t fd[3] = {fcols, frows, a.L}, fs[2] = {f.ld * 2, frows * f.ld * 2};
+    const int64_t wd[2] = {a.across ? a.N : K, a.across ? K : a.N}, wst[1] = {a.W.ld * 2};
+    const int64_t fd[3] = {fcols, frows, a.L}, fs[2] = {a.F.ld * 2, frows * a.F.ld * 2};
     if ((st = encode_nd(&p.tmX, bf16, 2, a.x.p, xd, xs, rows, true)) != TMG_OK ||
         (st = encode_nd(&p.tmU, bf16, 2, a.U, ud, us, rows, true)) != TMG_OK ||
-        (st = encode_nd(&p.tmW, bf16, 2, W.p, wd, wst, half, true)) != TMG_OK ||
-        (st = encode_nd(&p.tmF, bf16, 3, f.p, fd, fs, half, true)) != TMG_OK)
+        (st = encode_nd(&p.tmW, bf16, 2, a.W.p, wd, wst, half, true)) != TMG_OK ||
+        (st = encode_nd(&p.tmF, bf16, 3, a.F.p, fd, fs, half, true)) != TMG_OK)
         return st;
     TcArgs t;
     std::memset(&t, 0, sizeof t);
@@ -242,10 +237,11 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     p.sk_tiles = t.sk_tiles;
     p.group_m = t.group_m;
     if (t.sk_tiles > 0) {
-        p.partials = static_cast<float *>(workspace(kWsPartials, tc2_partials_bytes(t), s, &st));
+        p.partials = static_cast<float *>(workspace(kWsTc2Partials, tc2_partials_bytes(t), s, &st));
         if (!p.partials)
             return st;
-        if ((st = arrival_counters(tc2_counters_bytes(t) / sizeof(uint32_t), s, &p.counters)) != TMG_OK)
+        p.counters = static_cast<uint32_t *>(workspace(kWsTc2Counters, tc2_counters_bytes(t), s, &st));
+        if (!p.counters)
             return st;
     }
     p.D = a.D;
@@ -309,27 +305,26 @@ tmg_status moe_few(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
     return launched(launch_moe_few(p, ds.num_sms, err_ctx(ds), s), "expert layer launch");
 }
 
-// The same for a few rows, not across; W and F as tma_rows gave them (before the
-// kernel that makes U, beside which this one runs).
-tmg_status run_adapted_few(const DeviceState &ds, const AdaptedArgs &a, const Rows &W, const Rows &F, cudaStream_t s)
+// The same for a few rows, not across.
+tmg_status run_adapted_few(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t s)
 {
     tmg_status st;
     LoraFewArgs p;
     std::memset(&p, 0, sizeof p);
     const int64_t K = a.K > 0 ? a.K : 8, tp = up(a.M, 16);
-    const int64_t wd[2] = {K, a.N}, wst[1] = {W.ld * 2}, xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2};
+    const int64_t wd[2] = {K, a.N}, wst[1] = {a.W.ld * 2}, xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2};
     const int wbox[2] = {64, 128}, xbox[2] = {64, static_cast<int>(tp)};
-    if ((st = encode_nd(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, W.p, wd, wst, wbox)) != TMG_OK ||
+    if ((st = encode_nd(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.W.p, wd, wst, wbox)) != TMG_OK ||
         (st = encode_nd(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x.p, xd, xs, xbox, true)) != TMG_OK)
         return st;
     p.U = a.U;
-    p.F = F.p;
+    p.F = a.F.p;
     p.D = a.D;
     p.adapters = a.adapters;
     p.bias = a.bias;
     p.residual = a.residual;
     p.ldu = a.ldu;
-    p.ldf = F.ld;
+    p.ldf = a.F.ld;
     p.ldd = a.ldd;
     p.ld_residual = a.ld_residual;
     p.M = static_cast<int>(a.M);
@@ -423,26 +418,40 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
         Rows x;
         if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK)
             return st;
-        const bool few = g->M <= kLoraFewRows && g->r <= kLoraFewRanks;
-        Rows W{}, B{};
-        if (few && g->N > 0 &&
-            ((st = tma_rows(*ds, kWsPackB, g->W, g->ldw, g->N, g->K, g->N, s, &W)) != TMG_OK ||
-             (st = tma_rows(*ds, kWsLayoutB, g->B, g->r, g->L * g->N, g->r, g->L * g->N, s, &B)) != TMG_OK))
-            return st;
+        // every copy of an operand comes before the kernel that makes u: the product runs
+        // beside that one
+        AdaptedArgs a{};
+        Rows f{};
         RankArgs k{g->x, g->A, g->adapters, g->scales, u, g->M, g->K, g->L, g->ldx, ldu, static_cast<int>(g->r), false};
-        if ((st = run_rank(*ds, k, x, s)) != TMG_OK)
+        if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &a.x)) != TMG_OK ||
+            (g->N > 0 && (st = tma_rows(*ds, kWsPackB, g->W, g->ldw, g->N, g->K, g->N, s, &a.W)) != TMG_OK) ||
+            (g->N > 0 && (st = tma_rows(*ds, kWsLayoutB, g->B, g->r, g->L * g->N, g->r, g->L * g->N, s, &a.F)) != TMG_OK) ||
+            (g->K > 0 && !few_ranks(k) &&
+             (st = tma_rows(*ds, kWsFactor, g->A, g->K, g->L * g->r, g->K, g->L * g->r, s, &f)) != TMG_OK) ||
+            (st = run_rank(*ds, k, a.x, f, false, s)) != TMG_OK)
             return st;
         if (g->u && u != g->u) {               // the caller's own, in its layout
             k.U = g->u;
             k.ldu = g->r;
-            if ((st = run_rank(*ds, k, x, s)) != TMG_OK)
+            if ((st = run_rank(*ds, k, a.x, f, false, s)) != TMG_OK)
                 return st;
         }
         if (g->N == 0)
             return TMG_OK;
-        const AdaptedArgs a{x, g->W, u, g->B, g->D, g->adapters, g->bias, g->residual, g->M, g->N, g->K, g->r, g->L, g->ldw, ldu,
-                            g->ldd, g->ld_residual, false};
-        return few ? run_adapted_few(*ds, a, W, B, s) : run_adapted(*ds, a, s);
+        a.U = u;
+        a.D = g->D;
+        a.adapters = g->adapters;
+        a.bias = g->bias;
+        a.residual = g->residual;
+        a.M = g->M;
+        a.N = g->N;
+        a.K = g->K;
+        a.r = g->r;
+        a.L = g->L;
+        a.ldu = ldu;
+        a.ldd = g->ldd;
+        a.ld_residual = g->ld_residual;
+        return g->M <= kLoraFewRows && g->r <= kLoraFewRanks ? run_adapted_few(*ds, a, s) : run_adapted(*ds, a, s);
     });
 }
 
@@ -479,49 +488,60 @@ tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *g, void *stream)
                                                       "cudaMemsetAsync(dx)")
                                            : TMG_OK;
         }
+        const bool want_x = g->dx && g->K > 0;
         const int64_t ldu = up(g->r, 8);
-        const int r = static_cast<int>(g->r), L = static_cast<int>(g->L);
         Pieces p;
-        const size_t du_at = p.take(g->M * ldu * 2), names = p.take(g->M * 4), slots = p.take(g->M * 4), rows = p.take(g->M * 4),
-                     offsets = p.take((g->L + 1) * 4);
+        const size_t du_at = p.take(g->M * ldu * 2), rows = p.take(g->M * 4), offsets = p.take((g->L + 1) * 4);
         char *ws = static_cast<char *>(workspace(kWsLayer, p.bytes, s, &st));
         if (!ws)
             return st;
         const Rows dU{ws + du_at, ldu};
-        RouteArgs plan{};
-        if (want_a || want_b) {
-            plan.T = g->M;
-            plan.E = L;
-            plan.k = 1;
-            plan.experts = reinterpret_cast<int32_t *>(ws + names);
-            plan.slots = reinterpret_cast<int32_t *>(ws + slots);
-            plan.rows = reinterpret_cast<int32_t *>(ws + rows);
-            plan.offsets = reinterpret_cast<int32_t *>(ws + offsets);
-            plan.counts = static_cast<uint16_t *>(workspace(kWsRoute, row_plan_counts_bytes(g->M, L, ds->num_sms), s, &st));
-            if (!plan.counts)
-                return st;
-            if ((st = launched(launch_row_plan(g->adapters, plan, ds->num_sms, s), "row plan launch")) != TMG_OK)
+        // copies of operands first: dx's kernel runs beside the one that makes dU, and
+        // that one beside the plan's
+        AdaptedArgs a{};
+        LoraGradArgs grads;
+        std::memset(&grads, 0, sizeof grads);
+        Rows x{}, u{}, f{};
+        if ((st = tma_rows(*ds, kWsPackA, g->dD, g->ldd, g->M, g->N, g->M, s, &a.x)) != TMG_OK ||
+            (want_x && ((st = tma_rows(*ds, kWsPackB, g->W, g->ldw, g->N, g->K, g->N, s, &a.W)) != TMG_OK ||
+                        (st = tma_rows(*ds, kWsLayoutB, g->A, g->K, g->L * g->r, g->K, g->L * g->r, s, &a.F)) != TMG_OK)) ||
+            ((want_x || want_a) && (st = tma_rows(*ds, kWsFactor, g->B, g->r, g->L * g->N, g->r, g->L * g->N, s, &f)) != TMG_OK) ||
+            (want_a && ((st = tma_rows(*ds, kWsGather, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK ||
+                        (st = grad_side(grads.side[grads.sides++], x, g->K, dU, g->M, g->r, g->dA, false)) != TMG_OK)) ||
+            (want_b && ((st = tma_rows(*ds, kWsLayoutA, g->u, g->r, g->M, g->r, g->M, s, &u)) != TMG_OK ||
+                        (st = grad_side(grads.side[grads.sides++], a.x, g->N, u, g->M, g->r, g->dB, true)) != TMG_OK)))
+            return st;
+        if (grads.sides) {
+            grads.offsets = reinterpret_cast<int32_t *>(ws + offsets);
+            grads.rows = reinterpret_cast<int32_t *>(ws + rows);
+            grads.M = static_cast<int>(g->M);
+            grads.L = static_cast<int>(g->L);
+            grads.r = static_cast<int>(g->r);
+            if ((st = launched(launch_lora_plan(g->adapters, grads.M, grads.L, reinterpret_cast<int32_t *>(ws + offsets),
+                                                reinterpret_cast<int32_t *>(ws + rows), s),
+                               "row plan launch")) != TMG_OK)
                 return st;
         }
-        Rows d, x, u;
-        if ((st = tma_rows(*ds, kWsPackA, g->dD, g->ldd, g->M, g->N, g->M, s, &d)) != TMG_OK)
+        if ((want_x || want_a) &&
+            (st = run_rank(*ds, RankArgs{g->dD, g->B, g->adapters, g->scales, ws + du_at, g->M, g->N, g->L, g->ldd, ldu,
+                                         static_cast<int>(g->r), true},
+                           a.x, f, grads.sides > 0, s)) != TMG_OK)
             return st;
-        if (want_b && ((st = tma_rows(*ds, kWsGather, g->u, g->r, g->M, g->r, g->M, s, &u)) != TMG_OK ||
-                       (st = run_factor_grad(*ds, d, g->N, u, g->M, g->L, g->r, plan.offsets, plan.rows, g->dB, true, s)) != TMG_OK))
-            return st;
-        if ((want_a || (g->dx && g->K > 0)) &&
-            (st = run_rank(*ds, RankArgs{g->dD, g->B, g->adapters, g->scales, ws + du_at, g->M, g->N, g->L, g->ldd, ldu, r, true},
-                           d, s)) != TMG_OK)
-            return st;
-        if (want_a && ((st = tma_rows(*ds, kWsGather, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK ||
-                       (st = run_factor_grad(*ds, x, g->K, dU, g->M, g->L, g->r, plan.offsets, plan.rows, g->dA, false, s)) != TMG_OK))
-            return st;
-        if (!g->dx || g->K == 0)
-            return TMG_OK;
-        return run_adapted(*ds,
-                           AdaptedArgs{d, g->W, dU.p, g->A, g->dx, g->adapters, nullptr, nullptr, g->M, g->K, g->N, g->r, g->L,
-                                       g->ldw, ldu, g->K, 0, true},
-                           s);
+        if (want_x) {
+            a.U = dU.p;
+            a.D = g->dx;
+            a.adapters = g->adapters;
+            a.M = g->M;
+            a.N = a.ldd = g->K;
+            a.K = g->N;
+            a.r = g->r;
+            a.L = g->L;
+            a.ldu = ldu;
+            a.across = true;
+            if ((st = run_adapted(*ds, a, s)) != TMG_OK)
+                return st;
+        }
+        return grads.sides ? run_grad(*ds, grads, s) : TMG_OK;
     });
 }
 

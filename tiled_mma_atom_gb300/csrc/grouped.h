@@ -73,10 +73,6 @@ struct RouteArgs {
 };
 size_t route_counts_bytes(int64_t T, int E, int num_sms);
 cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t s);
-// The same plan for rows that name their group (outside 0 .. E - 1: none): fills
-// offsets, rows and slots of `a`, with experts and counts as workspace; k = 1, T rows.
-size_t row_plan_counts_bytes(int64_t rows, int E, int num_sms);
-cudaError_t launch_row_plan(const int32_t *names, const RouteArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
                                   const int32_t *experts, const float *dweights, void *dlogits, int num_sms,
                                   cudaStream_t s);

@@ -29,6 +29,7 @@ struct LoraRankArgs {
     void *U;
     int64_t ldu;
     int M, C, L, r;
+    int beside;                // the kernel before leaves X, F and the adapters alone: no wait for it
     // set by the launch
     int cluster, chunk, block_bytes, stages, stage_bytes, ring_bytes, tmem_cols;
 };
@@ -72,20 +73,28 @@ struct LoraPairArgs {
 };
 cudaError_t launch_lora_pair(const LoraPairArgs &a, int bn, bool maj, int pairs, const ErrCtx &err, cudaStream_t s);
 
+// The rows sorted by adapter: adapter l's are rows[offsets[l]] .. rows[offsets[l + 1] - 1],
+// in order.  Reads only the adapters and lets its successor start at once.
+cudaError_t launch_lora_plan(const int32_t *adapters, int M, int L, int32_t *offsets, int32_t *rows, cudaStream_t s);
+
 // G[l] = sum over the rows m of adapter l of Z[m]^T Y[m], (L, r, C), or, `across`, its
-// transpose (L, C, r); contiguous, zeros for an adapter without rows.  Adapter l's rows
-// are rows[offsets[l]] .. rows[offsets[l + 1] - 1].
-struct LoraGradArgs {
+// transpose (L, C, r); contiguous, zeros for an adapter without rows.
+struct LoraGradSide {
     CUtensorMap tmY[3], tmZ[3];        // (M, C), (M, r): boxes of 64 columns by 64, 16 and one rows
     void *G;
-    const int32_t *offsets, *rows;
-    int M, C, L, r, across;
+    int C, across;
+};
+struct LoraGradArgs {
+    LoraGradSide side[2];
+    int sides;                         // 1 or 2
+    const int32_t *offsets, *rows;     // launch_lora_plan's
+    int M, L, r;
     float *partials;                   // lora_grad_partial_bytes()
     uint32_t *counters;                // lora_grad_counters(), zero between launches
     int runs, stages, stage_bytes, tmem_cols;     // set by the launch
 };
-size_t lora_grad_partial_bytes(int64_t M, int64_t C, int r, int num_sms);
-size_t lora_grad_counters(int64_t M, int64_t C, int num_sms);
+size_t lora_grad_partial_bytes(const LoraGradArgs &a, int num_sms);
+size_t lora_grad_counters(const LoraGradArgs &a, int num_sms);
 cudaError_t launch_lora_grad(LoraGradArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 }  // namespace tmg

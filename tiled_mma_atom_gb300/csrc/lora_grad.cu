@@ -1,8 +1,13 @@
 // lora_grad.cu — the gradients of the adapters' factors: G[l] = sum over the rows m of
 // adapter l of Z[m]^T Y[m], (r, C) or its transpose, on the tensor cores.
 //
-// The rows come sorted by adapter (the routing's counting sort), the contraction
-// over an adapter's rows in blocks of 64 of them.  A CTA has a tile of 128 columns of Y
+// Plan.  One block sorts the rows by adapter: a stable counting sort, as the routing's,
+// ranking 32 rows at a time per warp with match.any.  It runs beside the kernel that
+// makes dU.
+//
+// Both gradients are one launch: the CTAs of the first side's column tiles, then those
+// of the second's.  The contraction over an adapter's rows goes in blocks of 64 of
+// them.  A CTA has a tile of 128 columns of Y
 // and a run of all adapters' blocks: P runs per tile fill the SMs whatever the
 // adapters' shares.  An adapter inside one run is rounded and stored; one that runs
 // on leaves fp32 partial sums, which the last of its runs to arrive adds up in
@@ -66,6 +71,92 @@ __device__ __forceinline__ int run_start(int units, int p, int P)
     return static_cast<int>(static_cast<int64_t>(units) * p / P);
 }
 
+// Shared memory: wc [32][L], totals [L].
+__global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t *adapters, int M, int L, int32_t *offsets, int32_t *rows)
+{
+    extern __shared__ int32_t wc[];
+    int32_t *total = wc + 32 * L;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int i = threadIdx.x; i < 32 * L; i += 1024)
+        wc[i] = 0;
+    grid_wait();
+    grid_release();
+    __syncthreads();
+    // each warp's rows are contiguous; four loads of a lane at a time
+    const int64_t each = (static_cast<int64_t>(M) + 1023) / 1024 * 32;
+    const int64_t m0 = min(static_cast<int64_t>(M), warp * each), m1 = min(static_cast<int64_t>(M), m0 + each);
+    int32_t *mine = wc + warp * L;
+    auto walk = [&](auto &&with) {
+        for (int64_t m = m0; m < m1; m += 128) {
+            int l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t at = m + 32 * i + lane;
+                const int x = at < m1 ? adapters[at] : -1;
+                l[i] = x < L ? x : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (m + 32 * i >= m1)
+                    break;
+                with(m + 32 * i + lane, l[i], __match_any_sync(0xffffffffu, l[i]));
+                __syncwarp();
+            }
+        }
+    };
+    walk([&](int64_t, int l, uint32_t same) {
+        if (l >= 0 && lane == __ffs(same) - 1)
+            mine[l] += __popc(same);
+    });
+    __syncthreads();
+    for (int l = threadIdx.x; l < L; l += 1024) {
+        int sum = 0;
+        for (int w = 0; w < 32; ++w)
+            sum += wc[w * L + l];
+        total[l] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int run = 0;
+        for (int l0 = 0; l0 < L; l0 += 32) {
+            const int l = l0 + lane, n = l < L ? total[l] : 0;
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o)
+                    inc += x;
+            }
+            if (l < L) {
+                total[l] = run + inc - n;
+                offsets[l] = run + inc - n;
+            }
+            run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0)
+            offsets[L] = run;
+    }
+    __syncthreads();
+    for (int l = threadIdx.x; l < L; l += 1024) {
+        int at = total[l];
+        for (int w = 0; w < 32; ++w) {
+            const int n = wc[w * L + l];
+            wc[w * L + l] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    walk([&](int64_t m, int l, uint32_t same) {
+        const int first = l >= 0 ? mine[l] : 0;
+        __syncwarp();
+        if (l >= 0) {
+            rows[first + __popc(same & ((1u << lane) - 1))] = static_cast<int32_t>(m);
+            if (lane == __ffs(same) - 1)
+                mine[l] = first + __popc(same);
+        }
+    });
+}
+
 __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_constant__ LoraGradArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -80,7 +171,10 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
     int *off = reinterpret_cast<int *>(tmem_slot + 4), *unit = off + p.L + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int tiles = ceil_div(p.C, kGrCols), tile = blockIdx.x % tiles, run = blockIdx.x / tiles;
+    const int tiles0 = ceil_div(p.side[0].C, kGrCols);
+    const int which = static_cast<int>(blockIdx.x) >= tiles0 * p.runs ? 1 : 0, cta = blockIdx.x - which * tiles0 * p.runs;
+    const LoraGradSide &side = p.side[which];
+    const int C = side.C, tiles = ceil_div(C, kGrCols), tile = cta % tiles, run = cta / tiles;
     const int r16 = (p.r + 15) & ~15, acc_cols = (p.r + 31) & ~31, zboxes = ceil_div(p.r, 64);
 
     if (threadIdx.x == 0) {
@@ -96,7 +190,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
         fence_mbar_init();
     }
     if (warp == 0 && lane < 6)
-        tma_prefetch_desc(lane < 3 ? &p.tmY[lane] : &p.tmZ[lane - 3]);
+        tma_prefetch_desc(lane < 3 ? &side.tmY[lane] : &side.tmZ[lane - 3]);
     if (warp == 1) {
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
@@ -178,7 +272,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
                 uint8_t *sy = smem + stage * p.stage_bytes;
                 for (int x = 0; x < 2 + zboxes; ++x) {            // Y's two boxes of 64 columns, then Z's
                     uint8_t *dst = sy + x * kMnBoxBytes;
-                    const CUtensorMap *maps = x < 2 ? p.tmY : p.tmZ;
+                    const CUtensorMap *maps = x < 2 ? side.tmY : side.tmZ;
                     const int c0 = x < 2 ? tile * kGrCols + x * 64 : (x - 2) * 64;
                     if (block) {
                         tma_load_2d_w(dst, &maps[0], &full[stage], c0, first[0]);
@@ -252,14 +346,14 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
     } else {
         // ---------------------------------------------------- epilogue
         const int q = warp & 3, col = tile * kGrCols + q * 32 + lane;
-        const int64_t limit = static_cast<int64_t>(p.L) * p.C * p.r;
-        __nv_bfloat16 *G = static_cast<__nv_bfloat16 *>(p.G);
+        const int64_t limit = static_cast<int64_t>(p.L) * C * p.r;
+        __nv_bfloat16 *G = static_cast<__nv_bfloat16 *>(side.G);
         // sixteen ranks from j0 on of this lane's column
         auto store = [&](int adapter, int j0, const float (&v)[16]) {
-            if (col >= p.C)
+            if (col >= C)
                 return;
-            if (p.across) {
-                const int64_t at = (static_cast<int64_t>(adapter) * p.C + col) * p.r + j0;
+            if (side.across) {
+                const int64_t at = (static_cast<int64_t>(adapter) * C + col) * p.r + j0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (j0 + 8 * h < p.r)
@@ -270,7 +364,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int64_t at = (static_cast<int64_t>(adapter) * p.r + j0 + j) * p.C + col;
+                    const int64_t at = (static_cast<int64_t>(adapter) * p.r + j0 + j) * C + col;
                     if (j0 + j < p.r && bounds_ok(at, limit, err, kBndStoreD))
                         G[at] = __float2bfloat16_rn(v[j]);
                 }
@@ -279,7 +373,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
         const int64_t piece = static_cast<int64_t>(kGrCols) * r16, p_limit = static_cast<int64_t>(gridDim.x) * 2 * piece;
         // run x's partial sums of adapter a: its first adapter's, or its last's
         auto piece_of = [&](int x, int a) {
-            return ((static_cast<int64_t>(x) * tiles + tile) * 2 + (unit[a] <= run_start(units, x, runs) ? 0 : 1)) * piece + q * 32 + lane;
+            return ((static_cast<int64_t>(which) * tiles0 * p.runs + static_cast<int64_t>(x) * tiles + tile) * 2 + (unit[a] <= run_start(units, x, runs) ? 0 : 1)) * piece + q * 32 + lane;
         };
         int local = 0;
         while (walk.next(l, b0, b1, partial)) {
@@ -315,7 +409,7 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
             if (!partial)
                 continue;
             const int r_first = unit_owner(unit[l], units, runs), r_last = unit_owner(unit[l + 1] - 1, units, runs);
-            const int64_t counter = (static_cast<int64_t>(r_first) * tiles + tile) * 4 + q;
+            const int64_t counter = (static_cast<int64_t>(which) * tiles0 * p.runs + static_cast<int64_t>(r_first) * tiles + tile) * 4 + q;
             if (!last_arrival(p.counters + counter, r_last - r_first, bounds_ok(counter, 4ll * gridDim.x, err, kBndCounters)))
                 continue;
             for (int j0 = 0; j0 < p.r; j0 += 16) {
@@ -347,30 +441,42 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
     }
 }
 
-// Runs of a column tile: two CTAs per SM, four blocks each at least.
-int grad_runs(int64_t M, int64_t C, int num_sms)
+int64_t grad_tiles(const LoraGradArgs &a)
 {
-    const int64_t tiles = (C + kGrCols - 1) / kGrCols, most = (M + 255) / 256, fill = 2 * num_sms / tiles;
+    int64_t n = 0;
+    for (int i = 0; i < a.sides; ++i)
+        n += (a.side[i].C + kGrCols - 1) / kGrCols;
+    return n;
+}
+
+// Runs of a column tile: two CTAs per SM, four blocks each at least.
+int grad_runs(const LoraGradArgs &a, int num_sms)
+{
+    const int64_t most = (static_cast<int64_t>(a.M) + 255) / 256, fill = 2 * num_sms / grad_tiles(a);
     return static_cast<int>(fill < 1 ? 1 : fill < most ? fill : most);
 }
 
 }  // namespace
 
-size_t lora_grad_partial_bytes(int64_t M, int64_t C, int r, int num_sms)
+size_t lora_grad_partial_bytes(const LoraGradArgs &a, int num_sms)
 {
-    return static_cast<size_t>(grad_runs(M, C, num_sms)) * ((C + kGrCols - 1) / kGrCols) * 2 * kGrCols * ((r + 15) & ~15) *
-           sizeof(float);
+    return static_cast<size_t>(grad_runs(a, num_sms)) * grad_tiles(a) * 2 * kGrCols * ((a.r + 15) & ~15) * sizeof(float);
 }
 
-size_t lora_grad_counters(int64_t M, int64_t C, int num_sms)
+size_t lora_grad_counters(const LoraGradArgs &a, int num_sms) { return static_cast<size_t>(grad_runs(a, num_sms)) * grad_tiles(a) * 4; }
+
+cudaError_t launch_lora_plan(const int32_t *adapters, int M, int L, int32_t *offsets, int32_t *rows, cudaStream_t s)
 {
-    return static_cast<size_t>(grad_runs(M, C, num_sms)) * ((C + kGrCols - 1) / kGrCols) * 4;
+    const int smem = 33 * L * static_cast<int>(sizeof(int32_t));
+    const cudaError_t e = smem > 48 * 1024 ? ensure_smem_attr(reinterpret_cast<const void *>(lora_plan_kernel), smem) : cudaSuccess;
+    if (e != cudaSuccess)
+        return e;
+    return launch_overlapped(lora_plan_kernel, dim3(1), 1024, smem, 1, s, adapters, M, L, offsets, rows);
 }
 
 cudaError_t launch_lora_grad(LoraGradArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    const int tiles = (a.C + kGrCols - 1) / kGrCols;
-    a.runs = grad_runs(a.M, a.C, num_sms);
+    a.runs = grad_runs(a, num_sms);
     a.stage_bytes = (2 + (a.r + 63) / 64) * kMnBoxBytes;
     a.stages = kGrMaxStages;
     a.tmem_cols = 32;
@@ -380,7 +486,7 @@ cudaError_t launch_lora_grad(LoraGradArgs a, int num_sms, const ErrCtx &err, cud
     const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(lora_grad_kernel), smem);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(lora_grad_kernel, dim3(static_cast<unsigned>(tiles) * a.runs), kGrThreads, smem, 1, s, a, err);
+    return launch_overlapped(lora_grad_kernel, dim3(static_cast<unsigned>(grad_tiles(a)) * a.runs), kGrThreads, smem, 1, s, a, err);
 }
 
 }  // namespace tmg

@@ -19,6 +19,9 @@
 // Roles (ten warps): 0 TMA producer, 1 MMA issuer (CTA 0) and TMEM owner, 2..9
 // epilogue, two warps per lane quarter sharing the columns.  Schedule: tc2_plan's.
 // Cut tiles: the piece with the last K block also takes the adapters' blocks.
+//
+// The kernel that makes U lets this one start as soon as the kernel before it has ended,
+// so x, W, F and the row numbers are there; only U's loads wait.
 #include "feed.cuh"
 #include "launch.cuh"
 #include "lora.cuh"
@@ -87,7 +90,6 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
     cluster_sync();          // barriers of both CTAs initialised, TMEM allocated
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    grid_wait();
 
     SegWalk walk(cluster, nclusters, p.dp_tiles, p.sk_tiles, num_kb);
     int tile, kb0, kb1, slot, tm, tn;
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             }
             if (!ok || kb1 != num_kb)
                 continue;
+            grid_wait();                     // U
             for (int l = of.next(-1); ok && l != kNoAdapter; l = of.next(l))
                 for (int c = 0; c < rank_blocks; ++c) {
                     const int at = take();
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
         }
     }
 
+    grid_wait();             // every warp: no later kernel may start before U's is done
     __syncwarp();
     tc_fence_before();
     cluster_sync();          // no CTA leaves while its peer may still touch it

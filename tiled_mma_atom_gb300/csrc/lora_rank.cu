@@ -30,6 +30,7 @@ namespace {
 constexpr int kRkThreads = 192;
 constexpr int kRkRows = 128;
 constexpr int kRkMaxStages = 8;
+constexpr int kRkChunk = 8192;          // a stage's room for adapters' blocks, one at least
 constexpr int kRkBars = (2 * kRkMaxStages + 1) * 8 + 24;      // barriers; TMEM address, abort flag, number of adapters
 constexpr int kRkLists = kRkRows * (16 + 4);                  // masks and numbers of the tile's adapters
 
@@ -77,8 +78,9 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
     }
-    grid_wait();
-    grid_release();                  // only now: lora_few_kernel reads x without a wait
+    if (!p.beside)
+        grid_wait();
+    grid_release();                  // only now: the product reads x without a wait
     if (warp == 0) {
         // the tile's adapters, smallest first, and the lanes that each leaves out
         RowAdapters<4> of;
@@ -211,6 +213,8 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])),
                     static_cast<int>(min(static_cast<int64_t>(8), p.ldu - j0)), limit, err);
     }
+    if (p.beside)
+        grid_wait();                 // what comes after this kernel comes after the one before it
     __syncwarp();
     cluster_sync();                  // no CTA leaves while its partial sums may be read
 }
@@ -225,9 +229,10 @@ cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const Err
     while (a.cluster < 8 && 2ll * a.cluster * tiles <= 2 * num_sms && num_kb >= 8 * a.cluster)
         a.cluster *= 2;
     a.block_bytes = maj ? (a.r + 63) / 64 * kMnBoxBytes : r16 * kKBlockBytes;
-    a.chunk = a.block_bytes >= 16384 ? 1 : 16384 / a.block_bytes;
+    a.chunk = a.block_bytes >= kRkChunk ? 1 : kRkChunk / a.block_bytes;
     a.stage_bytes = kRkRows * kKBlockBytes + a.chunk * a.block_bytes;
-    a.stages = 98304 / a.stage_bytes < 2 ? 2 : 98304 / a.stage_bytes > kRkMaxStages ? kRkMaxStages : 98304 / a.stage_bytes;
+    const int ring = tiles * a.cluster <= num_sms ? 196608 : 98304;
+    a.stages = ring / a.stage_bytes < 2 ? 2 : ring / a.stage_bytes > kRkMaxStages ? kRkMaxStages : ring / a.stage_bytes;
     a.ring_bytes = a.stages * a.stage_bytes;
     if (a.ring_bytes < r16 * kRkRows * 4)
         a.ring_bytes = r16 * kRkRows * 4;

@@ -223,30 +223,6 @@ __global__ void __launch_bounds__(1024) route_plan_kernel(RouteArgs a, int token
         a.rows[i] = -1;
 }
 
-// Rows that name their group themselves: a run's counts, and the names with -1 for
-// those outside 0 .. E - 1.
-__global__ void __launch_bounds__(1024) plan_count_kernel(const int32_t *names, RouteArgs a, int rows_per_block)
-{
-    extern __shared__ int32_t counts[];
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        counts[e] = 0;
-    grid_release();
-    grid_wait();
-    __syncthreads();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows_per_block, t1 = min(a.T, t0 + rows_per_block);
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += blockDim.x) {
-        const int32_t e = names[t];
-        const bool in = e >= 0 && e < a.E;
-        a.experts[t] = in ? e : -1;
-        if (in)
-            atomicAdd(&counts[e], 1);
-    }
-    __syncthreads();
-    const int row = count_row(a.E);
-    for (int e = threadIdx.x; e < row; e += blockDim.x)
-        a.counts[static_cast<int64_t>(blockIdx.x) * row + e] = e < a.E ? static_cast<uint16_t>(counts[e]) : 0;
-}
-
 // Gradient of the weights.  With the softmax over the selected logits,
 // dlogit_j = w_j (dw_j - sum_i w_i dw_i) at the selected ones and 0 elsewhere;
 // with the softmax p over all, dlogit_e = p_e ([e selected] dw - sum_i p_i dw_i).
@@ -541,23 +517,6 @@ cudaError_t launch_route(const RouteArgs &a, int num_sms, cudaStream_t s)
            : a.E <= 128 ? launch_route_of<4>(a, num_sms, s)
            : a.E <= 256 ? launch_route_of<8>(a, num_sms, s)
                         : launch_route_of<32>(a, num_sms, s);
-}
-
-cudaError_t launch_row_plan(const int32_t *names, const RouteArgs &a, int num_sms, cudaStream_t s)
-{
-    const int each = tokens_per_run(a.T, num_sms), runs = route_runs(a.T, num_sms);
-    cudaError_t e;
-    if ((e = launch_overlapped(plan_count_kernel, dim3(runs), 1024, a.E * sizeof(int32_t), 1, s, names, a, each)) != cudaSuccess)
-        return e;
-    const int span = 2 * each, bytes = static_cast<int>((34 * a.E + (span <= kPlanPairs ? span : 0)) * sizeof(int32_t));
-    if ((e = smem_limit(reinterpret_cast<const void *>(route_plan_kernel), bytes)) != cudaSuccess)
-        return e;
-    return launch_overlapped(route_plan_kernel, dim3((runs + 1) / 2), 1024, bytes, 1, s, a, each, runs);
-}
-
-size_t row_plan_counts_bytes(int64_t rows, int E, int num_sms)
-{
-    return static_cast<size_t>(route_runs(rows, num_sms)) * count_row(E) * sizeof(uint16_t);
 }
 
 cudaError_t launch_route_backward(const void *logits, bool bf16, int64_t T, int64_t ld, int E, int k, bool normalize,
