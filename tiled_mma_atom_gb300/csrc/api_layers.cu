@@ -7,6 +7,7 @@
 #include "lora.h"
 #include "moe_few.h"
 #include "product.h"
+#include "swap_kernel.cuh"
 
 namespace tmg {
 namespace {
@@ -212,10 +213,27 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     std::memset(&p, 0, sizeof p);
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t K = a.K > 0 ? a.K : 8;       // an empty contraction is one of zeros
-    static const int wide[] = {256, 128};
-    const int bn = a.across ? tc2_pick_bn_of(a.M, a.N, K, 64, ds.num_sms, wide, 2) : tc2_pick_bn(a.M, a.N, K, ds.num_sms);
-    if ((a.M + 255) / 256 * ((a.N + bn - 1) / bn) > kMax31)
-        return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
+    // Tile width and the cut of the last wave: the least time of the waves, a K block of
+    // a tile taking as long as in the GEMM's pair kernel.
+    const int pairs = ds.num_sms / 2, num_kb = static_cast<int>((K + 63) / 64);
+    int bn = 0;
+    float best = 0.f;
+    SwapTail tail{0, 1};
+    for (int w : {256, 224, 192, 128}) {
+        if (a.across && w != 256 && w != 128)
+            continue;                          // boxes of 64 columns for each CTA of the pair
+        const int64_t tiles = (a.M + 255) / 256 * ((a.N + w - 1) / w);
+        if (tiles > kMax31)
+            return fail(TMG_ERR_UNSUPPORTED, "more than 2^31 tiles");
+        SwapTail t;
+        const float ns = swap_time(static_cast<int>(tiles), pairs, num_kb, w, w == 256 ? 320.f : w == 224 ? 281.f : w == 192 ? 244.f : 204.f,
+                                   0.f, t);
+        if (!bn || ns < best) {
+            bn = w;
+            best = ns;
+            tail = t;
+        }
+    }
     const int64_t frows = a.across ? a.r : a.N, fcols = a.across ? a.N : a.r;
     const int64_t xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2}, ud[2] = {a.r, a.M}, us[1] = {a.ldu * 2};
     const int rows[2] = {64, 128}, half[3] = {64, a.across ? 64 : bn / 2, 1};
@@ -226,24 +244,22 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
         (st = encode_nd(&p.tmW, bf16, 2, a.W.p, wd, wst, half, true)) != TMG_OK ||
         (st = encode_nd(&p.tmF, bf16, 3, a.F.p, fd, fs, half, true)) != TMG_OK)
         return st;
-    TcArgs t;
-    std::memset(&t, 0, sizeof t);
-    t.M = p.M = static_cast<int>(a.M);
-    t.N = p.N = static_cast<int>(a.N);
-    t.K = p.K = static_cast<int>(K);
-    t.bn = bn;
-    tc2_plan(t, ds.num_sms);
-    p.dp_tiles = t.dp_tiles;
-    p.sk_tiles = t.sk_tiles;
-    p.group_m = t.group_m;
-    if (t.sk_tiles > 0) {
-        p.partials = static_cast<float *>(workspace(kWsTc2Partials, tc2_partials_bytes(t), s, &st));
+    p.M = static_cast<int>(a.M);
+    p.N = static_cast<int>(a.N);
+    p.K = static_cast<int>(K);
+    p.group_m = 16 * 256 * static_cast<int64_t>(K) * 2 <= (int64_t{32} << 20) ? 16 : 8;
+    p.cut_tiles = tail.tiles;
+    p.cut_pieces = tail.each;
+    if (tail.tiles > 0) {
+        p.partials = static_cast<float *>(workspace(kWsTc2Partials, pairs * sw_partial_floats(bn) * sizeof(float), s, &st));
         if (!p.partials)
             return st;
-        p.counters = static_cast<uint32_t *>(workspace(kWsTc2Counters, tc2_counters_bytes(t), s, &st));
-        if (!p.counters)
-            return st;
     }
+    // counters apart from those of the adapters' gradients, beside which this kernel may run
+    p.feed = static_cast<uint32_t *>(workspace(kWsTc2Counters, (32 + static_cast<size_t>(pairs) * 16) * sizeof(uint32_t), s, &st));
+    if (!p.feed)
+        return st;
+    p.counters = p.feed + 32;
     p.D = a.D;
     p.adapters = a.adapters;
     p.bias = a.bias;
@@ -255,7 +271,7 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     p.vec_ok = a.ldd % 8 == 0 && aligned(a.D);
     log_choice("bf16 with adapters: %d rows, N=%d K=%d rank %d -> lora_pair_kernel: 256 x %d tiles, weights %s", p.M, p.N, p.K,
                p.r, bn, a.across ? "MN-major" : "K-major");
-    return launched(launch_lora_pair(p, bn, a.across, t.pairs, err_ctx(ds), s), "product with adapters launch");
+    return launched(launch_lora_pair(p, bn, a.across, pairs, err_ctx(ds), s), "product with adapters launch");
 }
 
 // The layer in two kernels, for few tokens.

@@ -67,9 +67,11 @@ struct LoraPairArgs {
     int64_t ldd, ld_residual;
     int M, N, K, L, r;
     int vec_ok;                // rows of D are 16-byte aligned
-    int dp_tiles, sk_tiles, group_m;   // tc2_plan's
-    float *partials;
-    uint32_t *counters;
+    int group_m;               // row tiles per band
+    int cut_tiles, cut_pieces; // swap_time's
+    float *partials;           // of cut tiles: sw_partial_floats(bn) per pair
+    uint32_t *counters;        // 16 per cut tile
+    uint32_t *feed;            // the tile counter
 };
 cudaError_t launch_lora_pair(const LoraPairArgs &a, int bn, bool maj, int pairs, const ErrCtx &err, cudaStream_t s);
 

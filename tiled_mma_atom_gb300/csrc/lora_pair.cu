@@ -16,24 +16,28 @@
 // boxes of 64 x 64).  Ranks beyond 64 take several blocks; the columns past r
 // are out of range and read as zeros in both operands.
 //
-// Roles (ten warps): 0 TMA producer, 1 MMA issuer (CTA 0) and TMEM owner, 2..9
-// epilogue, two warps per lane quarter sharing the columns.  Schedule: tc2_plan's.
-// Cut tiles: the piece with the last K block also takes the adapters' blocks.
+// Roles (eleven warps): 0 TMA producer, 1 MMA issuer (CTA 0) and TMEM owner, 2..9
+// epilogue, two warps per lane quarter sharing the columns, 10 the tile feed.
+// Schedule: swap_kernel.cuh's, tiles taken as pairs get free and the last wave's cut
+// along K where that pays.  Cut tiles: the piece with the last K block also takes the
+// adapters' blocks.
 //
 // The kernel that makes U lets this one start as soon as the kernel before it has ended,
-// so x, W, F and the row numbers are there; only U's loads wait.
+// so x, W, F and the row numbers are there; only U's loads wait.  Pairs start as that
+// kernel's blocks leave their SMs, up to 10 us apart, which the feed evens out.
 #include "feed.cuh"
 #include "launch.cuh"
 #include "lora.cuh"
 #include "lora.h"
 #include "pieces.cuh"
 #include "staging.cuh"
+#include "swap_kernel.cuh"
 #include "tc2_kernel.cuh"
 
 namespace tmg {
 namespace {
 
-constexpr int kLpThreads = 320;
+constexpr int kLpThreads = 352;
 
 template <int BN>
 struct LoraCfg {
@@ -41,7 +45,7 @@ struct LoraCfg {
     static constexpr int B_BYTES = (BN / 2) * kKBlockBytes;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 218 * 1024 / STAGE_BYTES > 8 ? 8 : 218 * 1024 / STAGE_BYTES;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 16;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + sizeof(FeedSmem) + 16;
 };
 
 template <int BN, bool MAJ>
@@ -58,7 +62,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
+    FeedSmem *feed_smem = reinterpret_cast<FeedSmem *>(tempty + 2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(feed_smem + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -76,6 +81,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 16);
         }
+        feed_init(feed_smem);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -91,8 +97,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    SegWalk walk(cluster, nclusters, p.dp_tiles, p.sk_tiles, num_kb);
-    int tile, kb0, kb1, slot, tm, tn;
+    const SwapTail tail{p.cut_tiles, p.cut_pieces};
+    const int total = tiles_m * tiles_n;
+    SwapWalk walk(feed_smem, cluster, nclusters, total, tail, num_kb, err, abort_flag);
+    int tile, kb0, kb1, tm, tn;
     bool partial;
     RowAdapters<8> of;
 
@@ -102,6 +110,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
         uint32_t phase = 0;
         int64_t issued = 0;
         bool ok = true;
+        walk.feed.producer = rank == 0;
         // The next stage of the ring, announced: its place, or -1 where the wait ran out.
         auto take = [&]() -> int {
             if (!mbar_wait_cluster_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             }
             return at;
         };
-        while (ok && walk.next(tile, kb0, kb1, partial, slot)) {
+        while (ok && walk.next(tile, kb0, kb1, partial)) {
             tile_coords(tile, tiles_m, tiles_n, p.group_m, tm, tn);
             const int a_row = tm * kBM + static_cast<int>(rank) * kHalfM, b_row = tn * BN + static_cast<int>(rank) * (BN / 2);
             if (kb1 == num_kb)
@@ -198,24 +207,30 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                     phase ^= 1u;
                 }
             };
-            while (ok && walk.next(tile, kb0, kb1, partial, slot)) {
-                const int acc = local & 1;
+            // The next tile is fetched while the last K blocks of this one are under way.
+            bool more = walk.next(tile, kb0, kb1, partial);
+            while (ok && more) {
+                const int acc = local & 1, b0 = kb0, b1 = kb1, turn = max(b0, b1 - 3);
                 const uint32_t acc_phase = (local >> 1) & 1;
                 ++local;
                 tile_coords(tile, tiles_m, tiles_n, p.group_m, tm, tn);
-                if (kb1 == num_kb)
+                if (b1 == num_kb)
                     of.read(p.adapters, static_cast<int64_t>(tm) * kBM, p.M, p.L, lane);
                 if (!mbar_wait_cluster_warp(&tempty[acc], acc_phase ^ 1u, err, abort_flag, kSiteMmaTmemEmpty))
                     break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * BN;
-                for (int kb = kb0; kb < kb1 && take(); ++kb) {
+                for (int kb = b0; kb < b1; ++kb) {
+                    if (kb == turn)
+                        more = walk.next(tile, kb0, kb1, partial);
+                    if (!take())
+                        break;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16_pair_w(d_tmem, adesc + k * 2, bdesc + k * bstep, idesc, (kb != kb0) || (k != 0));
+                        mma_bf16_pair_w(d_tmem, adesc + k * 2, bdesc + k * bstep, idesc, (kb != b0) || (k != 0));
                     give();
                 }
-                if (ok && kb1 == num_kb)
+                if (ok && b1 == num_kb)
                     for (int l = of.next(-1); ok && l != kNoAdapter; l = of.next(l)) {
                         uint32_t off[8];
                         of.others(l, off);
@@ -233,18 +248,19 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             if (*abort_flag)         // the last block's commit (or, before the first, none)
                 settle(empty, STAGES, stage, phase, 1, err.word, err.budget_ns);
         }
+    } else if (warp == 10) {
+        feed_run(feed_smem, rank, total - tail.tiles, nclusters, p.feed, err, abort_flag);
     } else {
         // ---------------------------------------------------- epilogue
         constexpr int CHUNKS = (BN / 32 + 1) / 2;
         const int ew = warp - 2, q = warp & 3;
         const int c_begin = (ew / 4) * CHUNKS, c_end = min(BN / 32, c_begin + CHUNKS);
         const int64_t d_limit = static_cast<int64_t>(p.M - 1) * p.ldd + p.N;
-        const int64_t U = static_cast<int64_t>(p.sk_tiles) * num_kb;
-        const int64_t piece = 32 * BN, limit = static_cast<int64_t>(nclusters) * 2 * 2 * 4 * piece;
+        const int64_t piece = 32 * BN, limit = static_cast<int64_t>(nclusters) * sw_partial_floats(BN);
         __nv_bfloat16 *D = static_cast<__nv_bfloat16 *>(p.D);
         const __nv_bfloat16 *R = static_cast<const __nv_bfloat16 *>(p.residual);
         int local = 0;
-        while (walk.next(tile, kb0, kb1, partial, slot)) {
+        while (walk.next(tile, kb0, kb1, partial)) {
             tile_coords(tile, tiles_m, tiles_n, p.group_m, tm, tn);
             const int acc = local & 1;
             const uint32_t acc_phase = (local >> 1) & 1;
@@ -293,7 +309,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                 break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
-            const int64_t mine = ((static_cast<int64_t>(2 * cluster + slot) * 2 + rank) * 4 + q) * piece;
+            const int64_t mine = ((static_cast<int64_t>(cluster) * 2 + rank) * 4 + q) * piece;
 #pragma unroll 1
             for (int c = c_begin; c < c_end; ++c) {
                 uint32_t t[32];
@@ -319,11 +335,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                 mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
             if (!partial)
                 continue;
-            const int c_first = unit_owner(static_cast<int64_t>(tile) * num_kb, U, nclusters);
-            const int c_last = unit_owner(static_cast<int64_t>(tile + 1) * num_kb - 1, U, nclusters);
+            const int c_first = tile * walk.each, c_last = c_first + walk.each - 1;
             const int64_t counter = (static_cast<int64_t>(tile) * 2 + rank) * 8 + ew;
             if (!last_arrival(p.counters + counter, c_last - c_first,
-                              bounds_ok(counter, static_cast<int64_t>(p.sk_tiles) * 16, err, kBndCounters)))
+                              bounds_ok(counter, static_cast<int64_t>(tail.tiles) * 16, err, kBndCounters)))
                 continue;
 #pragma unroll 1
             for (int c = c_begin; c < c_end; ++c) {
@@ -332,8 +347,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                 for (int j = 0; j < 32; ++j)
                     v[j] = 0.f;
                 add_pieces(v, p.partials, limit, c * 1024 + lane * 4, c_first, c_last, [&](int cc) {
-                    const int first_tile = static_cast<int>((U * cc / nclusters) / num_kb);
-                    return ((static_cast<int64_t>(2 * cc + (first_tile == tile ? 0 : 1)) * 2 + rank) * 4 + q) * piece;
+                    return ((static_cast<int64_t>(cc) * 2 + rank) * 4 + q) * piece;
                 }, err);
                 finish(c, v);
             }
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
 }
 
 template <int BN, bool MAJ>
-cudaError_t launch_as(const LoraPairArgs &a, int pairs, const ErrCtx &err, cudaStream_t s)
+cudaError_t launch_lora_as(const LoraPairArgs &a, int pairs, const ErrCtx &err, cudaStream_t s)
 {
     using C = LoraCfg<BN>;
     static_assert(C::SMEM <= 232448 && C::STAGES >= 4 && C::B_BYTES % 1024 == 0, "shared memory");
@@ -367,11 +381,11 @@ cudaError_t launch_as(const LoraPairArgs &a, int pairs, const ErrCtx &err, cudaS
 cudaError_t launch_lora_pair(const LoraPairArgs &a, int bn, bool maj, int pairs, const ErrCtx &err, cudaStream_t s)
 {
     if (maj)
-        return bn == 256 ? launch_as<256, true>(a, pairs, err, s) : launch_as<128, true>(a, pairs, err, s);
-    return bn == 256   ? launch_as<256, false>(a, pairs, err, s)
-           : bn == 224 ? launch_as<224, false>(a, pairs, err, s)
-           : bn == 192 ? launch_as<192, false>(a, pairs, err, s)
-                       : launch_as<128, false>(a, pairs, err, s);
+        return bn == 256 ? launch_lora_as<256, true>(a, pairs, err, s) : launch_lora_as<128, true>(a, pairs, err, s);
+    return bn == 256   ? launch_lora_as<256, false>(a, pairs, err, s)
+           : bn == 224 ? launch_lora_as<224, false>(a, pairs, err, s)
+           : bn == 192 ? launch_lora_as<192, false>(a, pairs, err, s)
+                       : launch_lora_as<128, false>(a, pairs, err, s);
 }
 
 }  // namespace tmg

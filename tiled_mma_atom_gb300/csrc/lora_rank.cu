@@ -231,7 +231,7 @@ cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const Err
     a.block_bytes = maj ? (a.r + 63) / 64 * kMnBoxBytes : r16 * kKBlockBytes;
     a.chunk = a.block_bytes >= kRkChunk ? 1 : kRkChunk / a.block_bytes;
     a.stage_bytes = kRkRows * kKBlockBytes + a.chunk * a.block_bytes;
-    const int ring = tiles * a.cluster <= num_sms ? 196608 : 98304;
+    const int ring = 2 * tiles * a.cluster <= num_sms ? 196608 : 98304;
     a.stages = ring / a.stage_bytes < 2 ? 2 : ring / a.stage_bytes > kRkMaxStages ? kRkMaxStages : ring / a.stage_bytes;
     a.ring_bytes = a.stages * a.stage_bytes;
     if (a.ring_bytes < r16 * kRkRows * 4)
