@@ -150,7 +150,8 @@ tmg_status run_grad(const DeviceState &ds, LoraGradArgs &p, cudaStream_t s)
 }
 
 // A few rows' ranks: a warp per row and rank, where 16-byte loads read the factors in
-// place.
+// place.  With more rows the tensor cores' way is faster (65 x 4096 x 4096 18.7 us
+// against 19.4 in all, 100 18.0 and 21.5; 60 rows of rank 64 38.0 and 18.7).
 bool few_ranks(const RankArgs &a)
 {
     return a.M <= kLoraFewRows && a.r <= kLoraFewRanks && !a.across && a.C % 8 == 0 && aligned(a.F);
@@ -206,6 +207,22 @@ struct AdaptedArgs {
     bool across;
 };
 
+// The CTAs that share a tile of 128 x 128 (lora_split.cu), or 0 for the pair kernel.
+// Where such tiles are at most one for two SMs and the contraction is long, splitting
+// it beats the pairs' larger tiles (100 x 4096 x 4096 17.7 us against 20.0, 128 x 8192 x
+// 8192 37.9 and 46.7, 700 x 1024 x 4096 19.0 and 20.5); with more tiles or a short one it
+// does not (400 x 4096 x 4096 27.3 and 25.9, 1000 x 1024 x 1024 13.1 and 10.1).
+int split_cluster(int64_t M, int64_t N, int num_kb, int num_sms)
+{
+    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
+    if (2 * tiles > num_sms || num_kb < 32)
+        return 0;
+    int S = 2;
+    while (S < 8 && 2 * S * tiles <= num_sms && num_kb >= 8 * S)
+        S *= 2;
+    return S;
+}
+
 tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t s)
 {
     tmg_status st;
@@ -234,6 +251,9 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
             tail = t;
         }
     }
+    const int split = split_cluster(a.M, a.N, num_kb, ds.num_sms);
+    if (split)
+        bn = 256;                              // boxes of 128 rows
     const int64_t frows = a.across ? a.r : a.N, fcols = a.across ? a.N : a.r;
     const int64_t xd[2] = {K, a.M}, xs[1] = {a.x.ld * 2}, ud[2] = {a.r, a.M}, us[1] = {a.ldu * 2};
     const int rows[2] = {64, 128}, half[3] = {64, a.across ? 64 : bn / 2, 1};
@@ -247,6 +267,17 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     p.M = static_cast<int>(a.M);
     p.N = static_cast<int>(a.N);
     p.K = static_cast<int>(K);
+    if (split) {
+        p.D = a.D;
+        p.adapters = a.adapters;
+        p.bias = a.bias;
+        p.residual = a.residual;
+        p.ldd = a.ldd;
+        p.ld_residual = a.ld_residual;
+        p.L = static_cast<int>(a.L);
+        p.r = static_cast<int>(a.r);
+        return launched(launch_lora_split(p, a.across, split, err_ctx(ds), s), "product with adapters launch");
+    }
     p.group_m = 16 * 256 * static_cast<int64_t>(K) * 2 <= (int64_t{32} << 20) ? 16 : 8;
     p.cut_tiles = tail.tiles;
     p.cut_pieces = tail.each;

@@ -27,29 +27,10 @@ struct FewRing {
     int abort;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(mapa_shared(addr, rank))
-                 : "memory");
-    return v;
-}
-
 // Eight consecutive columns of row t of the cluster's S partial tiles.
 __device__ __forceinline__ void few_sum(uint32_t part, int t, int col, uint32_t S, float (&z)[8])
 {
-    const uint32_t at = part + (t * 128 + col) * 4;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        z[i] = 0.f;
-#pragma unroll 4
-    for (uint32_t s = 0; s < S; ++s) {
-        const float4 a = ld_cluster_f32x4(at, s), b = ld_cluster_f32x4(at + 16, s);
-        z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w;
-        z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
-    }
+    cluster_sum8(part + (t * 128 + col) * 4, S, z);
 }
 
 __device__ __forceinline__ uint32_t few_cluster_size()

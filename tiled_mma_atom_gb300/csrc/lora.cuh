@@ -65,6 +65,29 @@ __device__ __forceinline__ void mma_bf16_pair_masked_w(uint32_t d_tmem, uint64_t
         : "memory");
 }
 
+// Eight consecutive floats at the same shared-memory place in the S <= 8 CTAs of the
+// cluster, summed in rank order; all loads in flight together.
+__device__ __forceinline__ void cluster_sum8(uint32_t at, uint32_t S, float (&z)[8])
+{
+    float4 a[8], b[8];
+#pragma unroll
+    for (uint32_t s = 0; s < 8; ++s)
+        if (s < S) {
+            const uint32_t there = mapa_shared(at, s);
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a[s].x), "=f"(a[s].y), "=f"(a[s].z), "=f"(a[s].w) : "r"(there));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(b[s].x), "=f"(b[s].y), "=f"(b[s].z), "=f"(b[s].w) : "r"(there + 16));
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        z[i] = 0.f;
+#pragma unroll
+    for (uint32_t s = 0; s < 8; ++s)
+        if (s < S) {
+            z[0] += a[s].x, z[1] += a[s].y, z[2] += a[s].z, z[3] += a[s].w;
+            z[4] += b[s].x, z[5] += b[s].y, z[6] += b[s].z, z[7] += b[s].w;
+        }
+}
+
 // The adapters of 32 W rows from row0 on: lane i has those of rows 32 w + i, kNoAdapter
 // where there is none (rows past M, numbers outside 0 .. L - 1).
 template <int W>

@@ -73,6 +73,8 @@ struct LoraPairArgs {
     uint32_t *counters;        // 16 per cut tile
     uint32_t *feed;            // the tile counter
 };
+// The same in tiles of 128 x 128 over clusters (W and F K-major: boxes of 128 rows).
+cudaError_t launch_lora_split(const LoraPairArgs &a, bool maj, int cluster, const ErrCtx &err, cudaStream_t s);
 cudaError_t launch_lora_pair(const LoraPairArgs &a, int bn, bool maj, int pairs, const ErrCtx &err, cudaStream_t s);
 
 // The rows sorted by adapter: adapter l's are rows[offsets[l]] .. rows[offsets[l + 1] - 1],

@@ -220,9 +220,16 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                     break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * BN;
+                int l = kNoAdapter;                  // the tile's first adapter, found ahead of its turn
+                uint32_t off[8];
                 for (int kb = b0; kb < b1; ++kb) {
-                    if (kb == turn)
+                    if (kb == turn) {
+                        if (b1 == num_kb) {
+                            l = of.next(-1);
+                            of.others(l, off);
+                        }
                         more = walk.next(tile, kb0, kb1, partial);
+                    }
                     if (!take())
                         break;
 #pragma unroll
@@ -230,17 +237,16 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                         mma_bf16_pair_w(d_tmem, adesc + k * 2, bdesc + k * bstep, idesc, (kb != b0) || (k != 0));
                     give();
                 }
-                if (ok && b1 == num_kb)
-                    for (int l = of.next(-1); ok && l != kNoAdapter; l = of.next(l)) {
-                        uint32_t off[8];
-                        of.others(l, off);
-                        for (int c = 0; c < rank_blocks && take(); ++c) {
-                            const int steps = min(4, ceil_div(p.r - c * 64, 16));
-                            for (int k = 0; k < steps; ++k)
-                                mma_bf16_pair_masked_w(d_tmem, adesc + k * 2, bdesc + k * bstep, idesc, off);
-                            give();
-                        }
+                while (ok && l != kNoAdapter) {
+                    for (int c = 0; c < rank_blocks && take(); ++c) {
+                        const int steps = min(4, ceil_div(p.r - c * 64, 16));
+                        for (int k = 0; k < steps; ++k)
+                            mma_bf16_pair_masked_w(d_tmem, adesc + k * 2, bdesc + k * bstep, idesc, off);
+                        give();
                     }
+                    l = of.next(l);
+                    of.others(l, off);
+                }
                 if (!ok)
                     break;
                 mma_commit_pair_w(&tfull[acc], 0x3);
@@ -266,9 +272,28 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             const uint32_t acc_phase = (local >> 1) & 1;
             ++local;
             const int row = tm * kBM + static_cast<int>(rank) * kHalfM + q * 32 + lane;
+            // a chunk's residual, read ahead: the next chunk's while one is finished
+            uint4 ahead[4];
+            const __nv_bfloat16 *res_row = R + static_cast<int64_t>(row) * p.ld_residual;
+            auto wide = [&](int c) {
+                const int col0 = tn * BN + c * 32;
+                return R && c < c_end && row < p.M && col0 + 32 <= p.N && (reinterpret_cast<uintptr_t>(res_row + col0) & 15u) == 0;
+            };
+            auto read = [&](int c) {
+                if (wide(c))
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ahead[j] = reinterpret_cast<const uint4 *>(res_row + tn * BN + c * 32)[j];
+            };
             // bias, residual, rounding and store of a finished chunk
             auto finish = [&](int c, float (&v)[32]) {
                 const int col0 = tn * BN + c * 32;
+                const bool w = wide(c);
+                uint4 here[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    here[j] = ahead[j];
+                read(c + 1);
                 if (col0 >= p.N)
                     return;
                 if (p.bias) {
@@ -278,33 +303,28 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                 }
                 if (row >= p.M)
                     return;
-                if (R) {
-                    const __nv_bfloat16 *res = R + row * p.ld_residual + col0;
-                    if (col0 + 32 <= p.N && (reinterpret_cast<uintptr_t>(res) & 15u) == 0) {
-                        uint4 w[4];
+                if (w) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = reinterpret_cast<const uint4 *>(res)[j];
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t u4[4] = {here[j].x, here[j].y, here[j].z, here[j].w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t u4[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                v[8 * j + 2 * i] += __uint_as_float(u4[i] << 16);
-                                v[8 * j + 2 * i + 1] += __uint_as_float(u4[i] & 0xffff0000u);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            v[8 * j + 2 * i] += __uint_as_float(u4[i] << 16);
+                            v[8 * j + 2 * i + 1] += __uint_as_float(u4[i] & 0xffff0000u);
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col0 + j < p.N)
-                                v[j] += __bfloat162float(res[j]);
                     }
+                } else if (R) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col0 + j < p.N)
+                            v[j] += __bfloat162float(res_row[col0 + j]);
                 }
                 const int64_t at = static_cast<int64_t>(row) * p.ldd;
                 if (span_ok(at + col0, min(32, p.N - col0), d_limit, err, kBndStoreD))
                     store_row_chunk(D + at, col0, p.N, p.vec_ok, v);
             };
+            if (!partial)
+                read(c_begin);
             if (!mbar_wait_cluster(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull))
                 break;
             tc_fence_after();
@@ -340,6 +360,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
             if (!last_arrival(p.counters + counter, c_last - c_first,
                               bounds_ok(counter, static_cast<int64_t>(tail.tiles) * 16, err, kBndCounters)))
                 continue;
+            read(c_begin);
 #pragma unroll 1
             for (int c = c_begin; c < c_end; ++c) {
                 float v[32];

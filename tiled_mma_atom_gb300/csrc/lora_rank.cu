@@ -14,7 +14,7 @@
 //
 // F K-major, (L, r, C), or MN-major, (L, C, r), in boxes of 64 x 64 whose columns past
 // r read as zeros.  Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2..5 the
-// accumulator's way to shared memory; all six add up the partials.
+// rows' scales and the accumulator's way to shared memory; all six add up the partials.
 //
 // Bound by HBM: X once.
 #include "feed.cuh"
@@ -32,14 +32,7 @@ constexpr int kRkRows = 128;
 constexpr int kRkMaxStages = 8;
 constexpr int kRkChunk = 8192;          // a stage's room for adapters' blocks, one at least
 constexpr int kRkBars = (2 * kRkMaxStages + 1) * 8 + 24;      // barriers; TMEM address, abort flag, number of adapters
-constexpr int kRkLists = kRkRows * (16 + 4);                  // masks and numbers of the tile's adapters
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(addr, rank)) : "memory");
-    return v;
-}
+constexpr int kRkLists = kRkRows * (16 + 4 + 8);              // masks and numbers of the tile's adapters; rows' scales and whether they have one
 
 template <bool MAJ>
 __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_constant__ LoraRankArgs p, ErrCtx err)
@@ -49,7 +42,9 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint4 *masks = reinterpret_cast<uint4 *>(smem + p.ring_bytes);
     int *list = reinterpret_cast<int *>(masks + kRkRows);
-    uint64_t *full = reinterpret_cast<uint64_t *>(list + kRkRows);
+    float *scale = reinterpret_cast<float *>(list + kRkRows);
+    int *has = reinterpret_cast<int *>(scale + kRkRows);
+    uint64_t *full = reinterpret_cast<uint64_t *>(has + kRkRows);
     uint64_t *empty = full + kRkMaxStages;
     uint64_t *done = empty + kRkMaxStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
@@ -102,7 +97,7 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int n = *count;
-    const uint32_t part = smem_u32(smem);              // the partial sums [rank][128], over the ring
+    const uint32_t part = smem_u32(smem), width = ((p.r + 15) & ~15) + 4;      // the partial sums [row][width], over the ring
 
     int stage = 0, issued = 0;
     uint32_t phase = 0;
@@ -159,20 +154,24 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
             }
         }
         mma_commit_w(done);
-    } else if (mbar_wait_warp(done, 0, err, abort_flag, kSiteEpiTmemFull)) {
-        // ------------------------- the accumulator to shared memory, [rank][row]
-        tc_fence_after();
-        const int q = warp & 3;
-        for (int c = 0; c < p.r; c += 16) {
-            uint32_t t[16];
-            tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, t);
+    } else {
+        const int q = warp & 3, row = q * 32 + lane;
+        const int64_t m = static_cast<int64_t>(row0) + row;
+        const int l = m < p.M ? p.adapters[m] : -1;
+        has[row] = l >= 0 && l < p.L;
+        scale[row] = has[row] && p.scales ? p.scales[l] : 1.f;
+        if (mbar_wait_warp(done, 0, err, abort_flag, kSiteEpiTmemFull)) {
+            // --------------------- the accumulator to shared memory
+            tc_fence_after();
+            for (int c = 0; c < p.r; c += 16) {
+                uint32_t t[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, t);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(part + ((c + j) * kRkRows + q * 32 + lane) * 4),
-                             "r"(kb0 < kb1 ? t[j] : 0u)
-                             : "memory");
+                for (int j = 0; j < 16; j += 4)
+                    sts128(part + (row * width + c + j) * 4, kb0 < kb1 ? make_uint4(t[j], t[j + 1], t[j + 2], t[j + 3]) : make_uint4(0, 0, 0, 0));
+            }
+            tc_fence_before();
         }
-        tc_fence_before();
     }
     __syncwarp();
     cluster_sync();                  // every CTA's partial sums are written
@@ -192,23 +191,15 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
     const int64_t limit = p.M * p.ldu;
     const int share = kRkRows / S, groups = ceil_div(p.r, 8);
     for (int i = threadIdx.x; i < share * groups; i += kRkThreads) {
-        const int row = static_cast<int>(rank) * share + i % share, j0 = i / share * 8;
+        const int row = static_cast<int>(rank) * share + i / groups, j0 = i % groups * 8;
         const int64_t m = static_cast<int64_t>(row0) + row;
         if (m >= p.M)
             continue;
-        const int l = p.adapters[m];
-        const bool on = l >= 0 && l < p.L;
-        const float scale = on && p.scales ? p.scales[l] : 1.f;
-        float v[8] = {};
-        if (on)
-            for (int s = 0; s < S; ++s)
+        float v[8];
+        cluster_sum8(part + (row * width + j0) * 4, S, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] += ld_cluster_f32(part + ((j0 + j) * kRkRows + row) * 4, s);
-        if (on)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = j0 + j < p.r ? v[j] * scale : 0.f;        // zeros in the columns that pad a row
+        for (int j = 0; j < 8; ++j)              // zeros without an adapter, and in the columns that pad a row
+            v[j] = has[row] && j0 + j < p.r ? v[j] * scale[row] : 0.f;
         store_piece(U, m * p.ldu + j0,
                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])),
                     static_cast<int>(min(static_cast<int64_t>(8), p.ldu - j0)), limit, err);
@@ -229,13 +220,14 @@ cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const Err
     while (a.cluster < 8 && 2ll * a.cluster * tiles <= 2 * num_sms && num_kb >= 8 * a.cluster)
         a.cluster *= 2;
     a.block_bytes = maj ? (a.r + 63) / 64 * kMnBoxBytes : r16 * kKBlockBytes;
-    a.chunk = a.block_bytes >= kRkChunk ? 1 : kRkChunk / a.block_bytes;
+    // The ring: half an SM's shared memory, or more where few CTAs run.
+    const int few = 2 * tiles * a.cluster <= num_sms, ring = few ? 196608 : 98304, room = few ? 2 * kRkChunk : kRkChunk;
+    a.chunk = a.block_bytes >= room ? 1 : room / a.block_bytes;
     a.stage_bytes = kRkRows * kKBlockBytes + a.chunk * a.block_bytes;
-    const int ring = 2 * tiles * a.cluster <= num_sms ? 196608 : 98304;
     a.stages = ring / a.stage_bytes < 2 ? 2 : ring / a.stage_bytes > kRkMaxStages ? kRkMaxStages : ring / a.stage_bytes;
     a.ring_bytes = a.stages * a.stage_bytes;
-    if (a.ring_bytes < r16 * kRkRows * 4)
-        a.ring_bytes = r16 * kRkRows * 4;
+    if (a.ring_bytes < (r16 + 4) * kRkRows * 4)
+        a.ring_bytes = (r16 + 4) * kRkRows * 4;
     a.tmem_cols = 32;
     while (a.tmem_cols < r16)
         a.tmem_cols *= 2;
