@@ -112,7 +112,8 @@ tmg_status tma_rows(const DeviceState &ds, Workspace which, const void *src, int
                     int64_t rows_p, cudaStream_t s, Rows *out)
 {
     const int64_t least = up(std::max<int64_t>(cols, 1), 8);
-    if (rows_in_place(src, rows, ld, cols, 1, 2)) {
+    // a single row's end is not padded, and some kernels read whole 16 bytes
+    if (rows_in_place(src, rows, ld, cols, 1, 2) && (rows > 1 || cols % 8 == 0)) {
         *out = Rows{src, stride_or(rows, ld, least)};
         return TMG_OK;
     }
@@ -124,16 +125,17 @@ tmg_status tma_rows(const DeviceState &ds, Workspace which, const void *src, int
 }
 
 // One side of the factors' gradients: G from Y (M, C) and Z (M, r).
-tmg_status grad_side(LoraGradSide &g, const Rows &Y, int64_t C, const Rows &Z, int64_t M, int64_t r, void *G, bool across)
+tmg_status grad_side(LoraGradSide &g, const Rows &Y, int64_t C, const Rows &Z, int64_t M, void *G, bool across)
 {
     tmg_status st;
     for (int i = 0; i < 3; ++i) {
-        const int64_t yd[2] = {C, M}, ys[1] = {Y.ld * 2}, zd[2] = {r, M}, zs[1] = {Z.ld * 2};
+        const int64_t dims[2] = {C, M}, strides[1] = {Y.ld * 2};
         const int box[2] = {64, i == 0 ? 64 : i == 1 ? 16 : 1};
-        if ((st = encode_nd(&g.tmY[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y.p, yd, ys, box)) != TMG_OK ||
-            (st = encode_nd(&g.tmZ[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Z.p, zd, zs, box, true)) != TMG_OK)
+        if ((st = encode_nd(&g.tmY[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y.p, dims, strides, box)) != TMG_OK)
             return st;
     }
+    g.Z = Z.p;
+    g.ldz = Z.ld;
     g.G = G;
     g.C = static_cast<int>(C);
     g.across = across;
@@ -554,9 +556,9 @@ tmg_status tmg_lora_linear_backward(const tmg_lora_grad_args *g, void *stream)
                         (st = tma_rows(*ds, kWsLayoutB, g->A, g->K, g->L * g->r, g->K, g->L * g->r, s, &a.F)) != TMG_OK)) ||
             ((want_x || want_a) && (st = tma_rows(*ds, kWsFactor, g->B, g->r, g->L * g->N, g->r, g->L * g->N, s, &f)) != TMG_OK) ||
             (want_a && ((st = tma_rows(*ds, kWsGather, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK ||
-                        (st = grad_side(grads.side[grads.sides++], x, g->K, dU, g->M, g->r, g->dA, false)) != TMG_OK)) ||
+                        (st = grad_side(grads.side[grads.sides++], x, g->K, dU, g->M, g->dA, false)) != TMG_OK)) ||
             (want_b && ((st = tma_rows(*ds, kWsLayoutA, g->u, g->r, g->M, g->r, g->M, s, &u)) != TMG_OK ||
-                        (st = grad_side(grads.side[grads.sides++], a.x, g->N, u, g->M, g->r, g->dB, true)) != TMG_OK)))
+                        (st = grad_side(grads.side[grads.sides++], a.x, g->N, u, g->M, g->dB, true)) != TMG_OK)))
             return st;
         if (grads.sides) {
             grads.offsets = reinterpret_cast<int32_t *>(ws + offsets);

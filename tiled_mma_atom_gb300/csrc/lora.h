@@ -84,7 +84,9 @@ cudaError_t launch_lora_plan(const int32_t *adapters, int M, int L, int32_t *off
 // G[l] = sum over the rows m of adapter l of Z[m]^T Y[m], (L, r, C), or, `across`, its
 // transpose (L, C, r); contiguous, zeros for an adapter without rows.
 struct LoraGradSide {
-    CUtensorMap tmY[3], tmZ[3];        // (M, C), (M, r): boxes of 64 columns by 64, 16 and one rows
+    CUtensorMap tmY[3];        // (M, C): boxes of 64 columns by 64, 16 and one rows
+    const void *Z;             // (M, r), 16-byte rows of ldz
+    int64_t ldz;
     void *G;
     int C, across;
 };

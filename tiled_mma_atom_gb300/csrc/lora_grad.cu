@@ -14,14 +14,16 @@
 // order, so results do not depend on timing.
 //
 // Both operands are MN-major (Y's columns on the MMA's M, Z's on its N).  Requests'
-// rows are adjacent, so most blocks are 64 rows in a row and come by one box for
+// rows are adjacent, so most blocks are 64 rows of Y in a row and come by one box for
 // each 64 columns; sixteens of a block that are in a row come by boxes of 16, and
 // the others by gathers of four rows, whose numbers past the adapter's last row
 // are out of range and read as zeros.  No other adapter's row is ever multiplied: 0
-// times its NaN would be NaN.
+// times its NaN would be NaN.  A row of a box costs the TMA unit about 2.5 ns whatever
+// its bytes, so Z's short rows come by cp.async of a warp of their own (by boxes the
+// gradients of 8191 x 4096 and 8191 x 4096 took 37 us).
 //
-// Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2..5 epilogue; two
-// accumulators in turn.  Bound by HBM: Y once.
+// Warps: 0 Y's TMA producer, 1 MMA issuer and TMEM owner, 2..5 epilogue, 6 Z's copies;
+// two accumulators in turn.  Bound by HBM: Y once.
 #include "feed.cuh"
 #include "launch.cuh"
 #include "lora.cuh"
@@ -33,7 +35,7 @@
 namespace tmg {
 namespace {
 
-constexpr int kGrThreads = 192;
+constexpr int kGrThreads = 224;
 constexpr int kGrMaxStages = 4;
 constexpr int kGrCols = 128;
 constexpr int kGrBars = (2 * kGrMaxStages + 4) * 8 + 16;
@@ -175,11 +177,11 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
     const int which = static_cast<int>(blockIdx.x) >= tiles0 * p.runs ? 1 : 0, cta = blockIdx.x - which * tiles0 * p.runs;
     const LoraGradSide &side = p.side[which];
     const int C = side.C, tiles = ceil_div(C, kGrCols), tile = cta % tiles, run = cta / tiles;
-    const int r16 = (p.r + 15) & ~15, acc_cols = (p.r + 31) & ~31, zboxes = ceil_div(p.r, 64);
+    const int r16 = (p.r + 15) & ~15, acc_cols = (p.r + 31) & ~31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -189,8 +191,8 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 0 && lane < 6)
-        tma_prefetch_desc(lane < 3 ? &side.tmY[lane] : &side.tmZ[lane - 3]);
+    if (warp == 0 && lane < 3)
+        tma_prefetch_desc(&side.tmY[lane]);
     if (warp == 1) {
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
@@ -268,12 +270,12 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx_w(&full[stage], static_cast<uint32_t>(sixteens * 16 * kKBlockBytes * (2 + zboxes)));
+                mbar_arrive_expect_tx_w(&full[stage], static_cast<uint32_t>(sixteens * 16 * kKBlockBytes * 2));
                 uint8_t *sy = smem + stage * p.stage_bytes;
-                for (int x = 0; x < 2 + zboxes; ++x) {            // Y's two boxes of 64 columns, then Z's
+                for (int x = 0; x < 2; ++x) {                     // boxes of 64 columns
                     uint8_t *dst = sy + x * kMnBoxBytes;
-                    const CUtensorMap *maps = x < 2 ? side.tmY : side.tmZ;
-                    const int c0 = x < 2 ? tile * kGrCols + x * 64 : (x - 2) * 64;
+                    const CUtensorMap *maps = side.tmY;
+                    const int c0 = tile * kGrCols + x * 64;
                     if (block) {
                         tma_load_2d_w(dst, &maps[0], &full[stage], c0, first[0]);
                         continue;
@@ -306,6 +308,67 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
         }
         if (*abort_flag)
             settle(full, p.stages, stage, phase, min(issued, p.stages), err.word, err.budget_ns);
+    } else if (warp == 6) {
+        // ------------------------------ Z's rows, as the MMA reads them: 64-rank boxes of
+        // rows of 128 bytes, 16-byte chunks swizzled; zeros for rows past the adapter's
+        const int chunks = ceil_div(p.r, 8);
+        const __nv_bfloat16 *Z = static_cast<const __nv_bfloat16 *>(side.Z);
+        int stage = 0, pending = 0, oldest = 0;           // copies under way: stages oldest ..
+        uint32_t phase = 0;
+        bool ok = true;
+        auto land = [&] {                                 // the oldest copies are there: hand them to the MMA
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&full[oldest]);
+            oldest = oldest + 1 == p.stages ? 0 : oldest + 1;
+            --pending;
+        };
+        while (ok && walk.next(l, b0, b1, partial)) {
+            const int end = off[l + 1];
+            int next[2];                                  // lane i: rows i and 32 + i of the next block
+            auto fetch = [&](int b) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = off[l] + b * 64 + 32 * h + lane;
+                    next[h] = b < b1 && at < end ? p.rows[at] : -1;
+                }
+            };
+            fetch(b0);
+            for (int b = b0; b < b1; ++b) {
+                const int m[2] = {next[0], next[1]};
+                fetch(b + 1);
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1u, err, abort_flag, kSiteProducerEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t base = smem_u32(smem + stage * p.stage_bytes) + 2 * kMnBoxBytes + lane * kKBlockBytes;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool in = m[h] >= 0 && m[h] < p.M;
+                    const __nv_bfloat16 *from = Z + (in ? m[h] * side.ldz : 0);
+#pragma unroll 4
+                    for (int c = 0; c < chunks; ++c)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         base + (c >> 3) * kMnBoxBytes + 32 * h * kKBlockBytes + (((c & 7) ^ (lane & 7)) << 4)),
+                                     "l"(from + c * 8), "r"(in ? 16 : 0)
+                                     : "memory");
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                ++pending;
+                if (pending == 3) {
+                    asm volatile("cp.async.wait_group 2;" ::: "memory");
+                    land();
+                }
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        while (pending > 0)
+            land();
     } else if (warp == 1) {
         // -------------------------------------------- MMA issuer
         const uint32_t idesc = idesc_bf16_major(kGrCols, r16, 3);
@@ -414,12 +477,22 @@ __global__ void __launch_bounds__(kGrThreads) lora_grad_kernel(const __grid_cons
                 continue;
             for (int j0 = 0; j0 < p.r; j0 += 16) {
                 float v[16] = {};
-                for (int x = r_first; x <= r_last; ++x) {
-                    const int64_t at = piece_of(x, l) + j0 * kGrCols;
+                for (int x0 = r_first; x0 <= r_last; x0 += 4) {          // four runs' loads in flight
+                    float f[4][16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (bounds_ok(at + j * kGrCols, p_limit, err, kBndPartials))
-                            v[j] += __ldcg(p.partials + at + j * kGrCols);
+                    for (int x = 0; x < 4; ++x) {
+                        const int64_t at = x0 + x <= r_last ? piece_of(x0 + x, l) + j0 * kGrCols : 0;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            f[x][j] = x0 + x <= r_last && bounds_ok(at + j * kGrCols, p_limit, err, kBndPartials)
+                                          ? __ldcg(p.partials + at + j * kGrCols)
+                                          : 0.f;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] += f[x][j];
                 }
                 store(l, j0, v);
             }
@@ -449,10 +522,11 @@ int64_t grad_tiles(const LoraGradArgs &a)
     return n;
 }
 
-// Runs of a column tile: two CTAs per SM, four blocks each at least.
+// Runs of a column tile: two CTAs per SM, sixteen blocks each at least (a cut costs what
+// ten blocks take).
 int grad_runs(const LoraGradArgs &a, int num_sms)
 {
-    const int64_t most = (static_cast<int64_t>(a.M) + 255) / 256, fill = 2 * num_sms / grad_tiles(a);
+    const int64_t most = (static_cast<int64_t>(a.M) + 1023) / 1024, fill = 2 * num_sms / grad_tiles(a);
     return static_cast<int>(fill < 1 ? 1 : fill < most ? fill : most);
 }
 
