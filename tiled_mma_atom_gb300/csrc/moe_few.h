@@ -6,7 +6,7 @@
 
 namespace tmg {
 
-constexpr int kFewTokens = 64, kFewExperts = 256, kFewChoices = 16;
+constexpr int kFewTokens = 16, kFewExperts = 256, kFewChoices = 16;
 
 struct MoeFewArgs {
     CUtensorMap tmW1;          // (E, 2 F, H): 64 rows of 64
@@ -19,11 +19,8 @@ struct MoeFewArgs {
     int64_t ld_logits, ld_residual, ld_out;
     int T, H, F, E, k, normalize;
     bool bf16;                 // the logits
-    float *partials;           // moe_few_partial_bytes()
-    uint32_t *counters;        // one per SM, zero between launches
     FewShape shape;            // tp; the rest is set by the launch
 };
-size_t moe_few_partial_bytes(int tp, int num_sms);
 cudaError_t launch_moe_few(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 }  // namespace tmg
