@@ -112,3 +112,42 @@ def test_gradient_formulas():
         dA[a], dB[a] = dU.T @ x[m], dD[m].T @ u
     for got, w in zip((dx, dA, dB), want):
         assert torch.allclose(got, w)
+
+
+def _source(name):
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tiled_mma_atom_gb300", "csrc", name)) as f:
+        return re.sub(r"\s+", " ", re.sub(r"//[^\n]*", "", f.read()))
+
+
+@pytest.mark.parametrize("name,kernel", [("lora_few.cu", "lora_few_rank_kernel(RankArgs"), ("lora_rank.cu", "lora_rank_kernel(const"),
+                                         ("lora_grad.cu", "lora_plan_kernel(const"), ("moe_few.cu", "moe_few_up_kernel(const")])
+def test_successors_start_after_the_wait(name, kernel):
+    """Kernels whose successor reads the call's inputs without a wait of its own let it start only after their own
+    wait for the kernel before."""
+    body = _source(name).split(kernel)[1]
+    assert 0 < body.index("grid_wait();") < body.index("grid_release();")
+
+
+@pytest.mark.parametrize("name,kernel", [("lora_few.cu", "lora_few_kernel(const"), ("lora_split.cu", "lora_split_kernel(const"),
+                                         ("lora_pair.cu", "lora_pair_kernel(const"), ("moe_few.cu", "moe_few_down_kernel(const")])
+def test_late_waits_are_every_warps(name, kernel):
+    """Kernels that start beside the one before them end after it: every warp waits for it."""
+    body = _source(name).split(kernel)[1].split("template <")[0]
+    depth, found = 0, False
+    for part in body.replace("{", " { ").replace("}", " } ").split(" "):
+        depth += part == "{"
+        depth -= part == "}"
+        found |= depth == 1 and part == "grid_wait();"
+    assert found
+
+
+def test_kernels_settle_after_giving_up():
+    """A kernel whose wait ran out leaves only when its loads have landed and its MMAs have run."""
+    for name, loads, mmas in (("lora_pair.cu", "settle(full,", "settle(empty,"), ("lora_rank.cu", "settle(full,", "settle(done,"),
+                              ("lora_split.cu", "settle(full,", "settle(done,"), ("lora_grad.cu", "settle(full,", "settle(empty,"),
+                              ("few.cuh", "settle(sm.full,", "settle(&sm.done,"), ("moe_few.cu", "settle(sm.full,", "settle(sm.empty,"),
+                              ("lora_few.cu", "settle(&bars[d],", "few_product(")):
+        text = _source(name)
+        assert loads in text and mmas in text, name

@@ -97,7 +97,20 @@ __device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
     __syncthreads();
 }
 
-__device__ __forceinline__ void few_epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four epilogue warps meet; whether any of their threads says so.
+__device__ __forceinline__ bool few_epilogue_any(bool mine)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, 1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(any)
+        : "r"(mine ? 1u : 0u)
+        : "memory");
+    return any != 0;
+}
 
 // The tile of the i-th chosen expert's columns f0 ..: sum of the cluster's partial
 // sums, SwiGLU, weight; eight columns of a token per thread, items x, x + step, ...
@@ -233,7 +246,6 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
             for (int j = id; j < p.T * p.k; j += 128)        // the last tile's reads are done
                 if (sm.experts[j] == e)
                     sm.weight[j / p.k] = sm.weights[j];
-            // all 128 threads leave together: a wait that ran out raises the abort flag
             const bool there = mbar_wait_warp(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull);
             tc_fence_after();
             if (there)
@@ -250,11 +262,10 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
                 mbar_arrive(&tempty[acc]);
             if (S > 1)
                 break;
-            few_epilogue_sync();
-            if (*abort_flag)
+            if (few_epilogue_any(!there))                    // a wait ran out: all leave together
                 break;
             few_hidden(p, sm, smem_u32(staged), 1, tile / f_tiles, tile % f_tiles * 64, id, p.shape.tp * 8, 128, err);
-            few_epilogue_sync();                             // the staged tile and the weights are free
+            few_epilogue_any(false);                         // the staged tile and the weights are free
         }
     }
     __syncwarp();
