@@ -307,9 +307,10 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t
     return launched(launch_lora_pair(p, bn, a.across, pairs, err_ctx(ds), s), "product with adapters launch");
 }
 
-// The layer in two kernels, for few tokens.  All of them meet every chosen expert, which
-// costs more than the groups' sorting when they are many: 16 tokens of 64 experts, 2048
-// x 1024, 121 us against 131, 24 tokens 144 and 140, 61 tokens 155 and 146.
+// The layer in two kernels (three with more than 16 tokens), for few tokens: 16 tokens of
+// 64 experts, 2048 x 1024, 119 us against 131 by groups, 61 tokens 143 and 147, 61 of 32
+// experts, 4096 x 2048, 250 and 258; with one rounding between the products where the groups
+// have two.
 bool few_tokens(const tmg_moe_args &g)
 {
     return g.T <= kFewTokens && g.E <= kFewExperts && g.H % 8 == 0 && g.F % 8 == 0 && g.F > 0 && aligned(g.W1) && aligned(g.W2) &&
@@ -323,9 +324,14 @@ tmg_status moe_few(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
     std::memset(&p, 0, sizeof p);
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t experts = std::min(g.E, g.T * g.k), tp = up(g.T, 16);
-    p.hidden = workspace(kWsLayer, experts * tp * g.F * 2, s, &st);
-    if (!p.hidden)
+    Pieces w;
+    const size_t hidden = w.take(experts * tp * g.F * 2), weights = w.take(g.T * g.k * 4), chosen = w.take(g.T * g.k * 4);
+    char *ws = static_cast<char *>(workspace(kWsLayer, w.bytes, s, &st));
+    if (!ws)
         return st;
+    p.hidden = ws + hidden;
+    p.weights = reinterpret_cast<float *>(ws + weights);
+    p.chosen = reinterpret_cast<int32_t *>(ws + chosen);
     const int64_t d1[3] = {g.H, 2 * g.F, g.E}, s1[2] = {g.H * 2, g.F * g.H * 4};
     const int64_t d2[3] = {g.F, g.H, g.E}, s2[2] = {g.F * 2, g.F * g.H * 2};
     const int64_t dx[2] = {g.H, g.T}, sx[1] = {stride_or(g.T, g.ldx, g.H) * 2};

@@ -7,8 +7,9 @@
 // multiple of 16) as its N, for every expert that any token chose: nothing is sorted,
 // gathered or grouped, and a tile needs no more than its expert's number.
 //
-// Choice.  Every CTA chooses all tokens' experts from the logits by itself (a warp per
-// token, route.cuh), which takes it less time than a kernel of its own would.
+// Choice.  Up to 16 tokens every CTA chooses all tokens' experts from the logits by
+// itself (a warp per token, route.cuh), which takes it less time than a kernel of its
+// own would; for more there is one.
 //
 // First kernel.  A tile is 64 gate rows and their 64 up rows of one chosen expert.
 // hidden[i][t] = bf16(w[t, e] silu(g) u) for the i-th chosen expert e, zeros for tokens
@@ -43,7 +44,9 @@ struct FewSmem : FewRing {
     int32_t experts[kFewTokens * kFewChoices];
     int32_t counts[kFewExperts];
     int32_t list[kFewExperts];               // the chosen experts, smallest first
-    uint32_t tokens[kFewExperts];            // which tokens chose them
+    uint32_t tokens[kFewExperts][2];         // which tokens chose them
+
+    __device__ __forceinline__ bool chose(int i, int t) const { return tokens[i][t >> 5] >> (t & 31) & 1u; }
     float weight[kFewTokens];                // first kernel: of its expert
 };
 
@@ -52,14 +55,12 @@ __device__ __forceinline__ void few_clear(FewSmem &sm)
 {
     for (int i = threadIdx.x; i < kFewExperts; i += kFwThreads) {
         sm.counts[i] = 0;
-        sm.tokens[i] = 0;
+        sm.tokens[i][0] = sm.tokens[i][1] = 0;
     }
     __syncthreads();
 }
 
-// All threads: choose the tokens' experts.
-template <int C, bool BF16>
-__device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
+__device__ __forceinline__ RouteArgs few_route(const MoeFewArgs &p, float *weights, int32_t *experts)
 {
     RouteArgs r{};
     r.logits = p.logits;
@@ -68,9 +69,38 @@ __device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
     r.E = p.E;
     r.k = p.k;
     r.normalize = p.normalize;
-    r.weights = sm.weights;
-    r.experts = sm.experts;
-    choose<C, BF16, true>(r, 0, p.T, sm.counts, nullptr);
+    r.weights = weights;
+    r.experts = experts;
+    return r;
+}
+
+// The choices of many tokens, a warp per token.
+constexpr int kFwChoosers = 8;
+template <int C, bool BF16>
+__global__ void __launch_bounds__(32 * kFwChoosers) moe_few_choose_kernel(MoeFewArgs p)
+{
+    __shared__ int32_t counts[kFewExperts];      // no one reads them here
+    grid_wait();
+    grid_release();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kFwChoosers;
+    choose<C, BF16>(few_route(p, p.weights, p.chosen), t0, min(static_cast<int64_t>(p.T), t0 + kFwChoosers), counts, nullptr);
+}
+
+// All threads: choose the tokens' experts (C = 0: read the choices).
+template <int C, bool BF16>
+__device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
+{
+    if constexpr (C == 0) {
+        for (int i = threadIdx.x; i < p.T * p.k; i += kFwThreads) {
+            const int e = __ldcg(p.chosen + i);
+            sm.experts[i] = e;
+            sm.weights[i] = __ldcg(p.weights + i);
+            if (e >= 0)
+                atomicAdd(&sm.counts[e], 1);
+        }
+    } else {
+        choose<C, BF16, true>(few_route(p, sm.weights, sm.experts), 0, p.T, sm.counts, nullptr);
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
         int n = 0;
@@ -92,7 +122,7 @@ __device__ __forceinline__ void few_choose(const MoeFewArgs &p, FewSmem &sm)
     for (int i = threadIdx.x; i < p.T * p.k; i += kFwThreads) {
         const int e = sm.experts[i], t = i / p.k;
         if (e >= 0)
-            atomicOr(&sm.tokens[sm.counts[e]], 1u << t);
+            atomicOr(&sm.tokens[sm.counts[e]][t >> 5], 1u << (t & 31));
     }
     __syncthreads();
 }
@@ -123,7 +153,7 @@ __device__ __forceinline__ void few_hidden(const MoeFewArgs &p, const FewSmem &s
         if (n <= 0)
             continue;
         float g[8] = {}, u[8];
-        if (t < p.T && (sm.tokens[i] >> t & 1u)) {
+        if (t < p.T && sm.chose(i, t)) {
             const float w = sm.weight[t];
             few_sum(sums, t, c, S, g);
             few_sum(sums, t, 64 + c, S, u);
@@ -349,7 +379,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_c
             if (j < n && z[j] != z[j]) {
                 float sum = 0.f;
                 for (int i = 0; i < sm.chosen; ++i)
-                    if (sm.tokens[i] >> t & 1u) {
+                    if (sm.chose(i, t)) {
                         const __nv_bfloat16 *w = W2 + (static_cast<int64_t>(sm.list[i]) * p.H + col + j) * p.F;
                         const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.shape.tp + t) * p.F;
                         for (int f = 0; f < p.F; ++f)
@@ -370,9 +400,20 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_c
 template <int C, bool BF16>
 cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    // half an SM's shared memory each, so that the second kernel starts beside the first
-    few_ring(a.shape, kFwRing);
-    const int smem = 1024 + a.shape.ring_bytes, smem_up = smem + a.shape.tp * 512;
+    // Half an SM's shared memory each, so that the second kernel starts beside the first;
+    // with many tokens, and so much to read, the first one takes all of an SM's (61 tokens
+    // of 64 experts, 2048 x 1024: 143 us against 152).
+    MoeFewArgs b = a;
+    few_ring(a.shape, C == 0 ? 2 * kFwRing - a.shape.tp * 512 : kFwRing);
+    // The second kernel: two CTAs per SM, or, where clusters of four with one per SM take
+    // three quarters of the SMs, those and all of an SM's shared memory (13 tokens, 4 of 32
+    // experts, 4096 x 2048, 32 tiles: 206 us against 222; 24 tiles 50 and 52 the other way;
+    // clusters of eight need eight free SMs of one part of the chip and wait for them: 245).
+    const int64_t downs = (a.H + 127) / 128;
+    const bool deep = 4 * downs <= num_sms && 16 * downs >= 3 * num_sms;
+    const int s_down = deep ? 4 : few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), 2 * num_sms);
+    few_ring(b.shape, deep ? 2 * kFwRing - 16384 : kFwRing);
+    const int smem = 1024 + b.shape.ring_bytes, smem_up = 1024 + a.shape.ring_bytes + a.shape.tp * 512;
     auto up = moe_few_up_kernel<C, BF16>;
     auto down = moe_few_down_kernel<C, BF16>;
     cudaError_t e;
@@ -383,19 +424,28 @@ cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStre
     // are few (one token's 2 of 8 experts, 4096 -> 2 x 2048, 64 tiles: 27.0 us
     // against 30.1).
     const int experts = a.T * a.k < a.E ? a.T * a.k : a.E;
-    const int64_t ups = static_cast<int64_t>(experts) * ((a.F + 63) / 64), downs = (a.H + 127) / 128;
+    const int64_t ups = static_cast<int64_t>(experts) * ((a.F + 63) / 64);
     const int s_up = few_cluster(ups, (a.H + 63) / 64, num_sms);
     if ((e = launch_overlapped(up, dim3(static_cast<unsigned>(s_up > 1 ? ups * s_up : num_sms)), kFwThreads, smem_up, s_up, s, a,
                                err)) != cudaSuccess)
         return e;
-    const int s_down = few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), 2 * num_sms);
-    return launch_overlapped(down, dim3(static_cast<unsigned>(downs * s_down)), kFwThreads, smem, s_down, s, a, err);
+    return launch_overlapped(down, dim3(static_cast<unsigned>(downs * s_down)), kFwThreads, smem, s_down, s, b, err);
+}
+
+template <int C, bool BF16>
+cudaError_t launch_few_choice(const MoeFewArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
+{
+    if (a.T <= kFewOwnChoice)
+        return launch_few_as<C, BF16>(a, num_sms, err, s);
+    const cudaError_t e = launch_overlapped(moe_few_choose_kernel<C, BF16>, dim3((a.T + kFwChoosers - 1) / kFwChoosers),
+                                            32 * kFwChoosers, 0, 1, s, a);
+    return e != cudaSuccess ? e : launch_few_as<0, false>(a, num_sms, err, s);
 }
 
 template <int C>
 cudaError_t launch_few_of(const MoeFewArgs &a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
-    return a.bf16 ? launch_few_as<C, true>(a, num_sms, err, s) : launch_few_as<C, false>(a, num_sms, err, s);
+    return a.bf16 ? launch_few_choice<C, true>(a, num_sms, err, s) : launch_few_choice<C, false>(a, num_sms, err, s);
 }
 
 }  // namespace

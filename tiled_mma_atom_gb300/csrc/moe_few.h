@@ -6,7 +6,8 @@
 
 namespace tmg {
 
-constexpr int kFewTokens = 16, kFewExperts = 256, kFewChoices = 16;
+// Tokens of the two kernels, and those whose experts every CTA chooses by itself.
+constexpr int kFewTokens = 64, kFewOwnChoice = 16, kFewExperts = 256, kFewChoices = 16;
 
 struct MoeFewArgs {
     CUtensorMap tmW1;          // (E, 2 F, H): 64 rows of 64
@@ -14,6 +15,8 @@ struct MoeFewArgs {
     CUtensorMap tmW2;          // (E, H, F): 128 rows of 64
     CUtensorMap tmHidden;      // (experts, tp, F): tp rows of 64
     const void *logits, *W2, *residual;
+    float *weights;            // with more than kFewOwnChoice tokens: the choices, (T, k)
+    int32_t *chosen;
     void *hidden;              // bf16 (experts, tp, F), experts = min(E, T k)
     void *out;
     int64_t ld_logits, ld_residual, ld_out;
