@@ -13,18 +13,53 @@ from __future__ import annotations
 import torch
 
 from . import _native
-from .grouped import _LOGITS, _bf16, _check, _current, _empty, _f32, _flat, _handle, _i32, _matrix, _side
+from .grouped import _LOGITS, _bf16, _current, _empty, _f32, _handle, _i32, _side
+
+_device = torch._C._cuda_getDevice
 
 
-def _run(call, args, stream, dev):
+def _run(call, args, stream, index):
     """The library call, with the tensors' device current (a launch needs it)."""
-    if torch.cuda.current_device() == dev.index:
+    if _device() == index:
         st = call(args, stream)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             st = call(args, stream)
     if st:
         _native.raise_on(st)
+
+
+def _wrong(name, t, dtype, shape, index, what):
+    raise ValueError(f"{name} must be a {what} {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _rows(name, t, dtype, shape, index):
+    """The pointer of a matrix on GPU `index` with unit column stride."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+        _wrong(name, t, dtype, shape, index, "row-wise contiguous")
+    return t.data_ptr()
+
+
+def _flat(name, t, dtype, shape, index):
+    """The pointer of a contiguous tensor on GPU `index`."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        _wrong(name, t, dtype, shape, index, "contiguous")
+    return t.data_ptr()
+
+
+def _gpu(name, t, dims):
+    """The number of the GPU of a tensor with `dims` dimensions."""
+    index = t.get_device()
+    if index < 0 or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D CUDA tensor, got shape {tuple(t.shape)} on {t.device}")
+    return index
+
+
+def _dims(name, t, dims):
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def moe_layer(x: torch.Tensor, logits: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, k: int, *,
@@ -39,34 +74,24 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, W1: torch.Tensor, W2: torch
     allowed).  The same as moe_route, grouped_gemm with SwiGLU, grouped_gemm and
     moe_combine, which it runs for many tokens; training takes those, since the
     gradients need what lies between them."""
-    T, H = _matrix("x", x)
-    E = _matrix("logits", logits)[1]
-    F = _matrix("W2", W2, 3)[2]
+    i = _gpu("x", x, 2)
+    T, H = x.shape
+    E = _dims("logits", logits, 2)[1]
+    F = _dims("W2", W2, 3)[2]
     dt = _LOGITS.get(logits.dtype)
     if dt is None:
         raise TypeError(f"unsupported logits dtype {logits.dtype}: use float32 or bfloat16")
-    dev = x.device
-    side = None if stream is None else _side(stream, dev)
-    _check("x", x, _bf16, (T, H))
-    _check("logits", logits, logits.dtype, (T, E), dev)
-    w1, w2 = _flat("W1", W1, _bf16, (E, 2 * F, H), dev), _flat("W2", W2, _bf16, (E, H, F), dev)
-    if residual is not None:
-        _check("residual", residual, _bf16, (T, H), dev)
+    side = None if stream is None else _side(stream, x.device)
     if out is None:
-        out = _empty(side)((T, H), dtype=_bf16, device=dev)
-    else:
-        _check("out", out, _bf16, (T, H), dev)
-    a = _native.pack_moe(x.data_ptr(), logits.data_ptr(), w1, w2, 0 if residual is None else residual.data_ptr(),
-                         out.data_ptr(), T, H, F, E, k, x.stride(0), logits.stride(0),
+        out = _empty(side)((T, H), dtype=_bf16, device=x.device)
+    a = _native.pack_moe(_rows("x", x, _bf16, (T, H), i), _rows("logits", logits, logits.dtype, (T, E), i),
+                         _flat("W1", W1, _bf16, (E, 2 * F, H), i), _flat("W2", W2, _bf16, (E, H, F), i),
+                         0 if residual is None else _rows("residual", residual, _bf16, (T, H), i),
+                         _rows("out", out, _bf16, (T, H), i), T, H, F, E, k, x.stride(0), logits.stride(0),
                          0 if residual is None else residual.stride(0), out.stride(0), dt, 1 if normalize else 0)
-    s = _current(dev.index) if side is None else _handle(side, (x, logits, W1, W2, residual, out))
-    _run(_native.lib().tmg_moe_layer, a, s, dev)
+    s = _current(i) if side is None else _handle(side, (x, logits, W1, W2, residual, out))
+    _run(_native.lib().tmg_moe_layer, a, s, i)
     return out
-
-
-def _adapter_shapes(A, B, N, K, dev):
-    L, r, _ = _matrix("A", A, 3)
-    return L, r, _flat("A", A, _bf16, (L, r, K), dev), _flat("B", B, _bf16, (L, N, r), dev)
 
 
 def lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, adapters: torch.Tensor,
@@ -81,27 +106,23 @@ def lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tens
     zeros); adapters (M,) int32, where -1 (or any number outside) is no adapter;
     scales (L,) and bias (N,) float32; residual (M, N) bfloat16 (D itself is
     allowed); u (M, r) bfloat16: u is saved there for lora_linear_backward."""
-    M, K = _matrix("x", x)
-    N = _matrix("W", W)[0]
-    dev = x.device
-    side = None if stream is None else _side(stream, dev)
-    _check("x", x, _bf16, (M, K))
-    _check("W", W, _bf16, (N, K), dev)
-    L, r, a_ptr, b_ptr = _adapter_shapes(A, B, N, K, dev)
-    if residual is not None:
-        _check("residual", residual, _bf16, (M, N), dev)
+    i = _gpu("x", x, 2)
+    M, K = x.shape
+    N = _dims("W", W, 2)[0]
+    L, r, _ = _dims("A", A, 3)
+    side = None if stream is None else _side(stream, x.device)
     if D is None:
-        D = _empty(side)((M, N), dtype=_bf16, device=dev)
-    else:
-        _check("D", D, _bf16, (M, N), dev)
-    a = _native.pack_lora(x.data_ptr(), W.data_ptr(), a_ptr, b_ptr, D.data_ptr(), _flat("adapters", adapters, _i32, (M,), dev),
-                          0 if scales is None else _flat("scales", scales, _f32, (L,), dev),
-                          0 if bias is None else _flat("bias", bias, _f32, (N,), dev),
-                          0 if residual is None else residual.data_ptr(),
-                          0 if u is None else _flat("u", u, _bf16, (M, r), dev), M, N, K, r, L, x.stride(0), W.stride(0),
+        D = _empty(side)((M, N), dtype=_bf16, device=x.device)
+    a = _native.pack_lora(_rows("x", x, _bf16, (M, K), i), _rows("W", W, _bf16, (N, K), i), _flat("A", A, _bf16, (L, r, K), i),
+                          _flat("B", B, _bf16, (L, N, r), i), _rows("D", D, _bf16, (M, N), i),
+                          _flat("adapters", adapters, _i32, (M,), i),
+                          0 if scales is None else _flat("scales", scales, _f32, (L,), i),
+                          0 if bias is None else _flat("bias", bias, _f32, (N,), i),
+                          0 if residual is None else _rows("residual", residual, _bf16, (M, N), i),
+                          0 if u is None else _flat("u", u, _bf16, (M, r), i), M, N, K, r, L, x.stride(0), W.stride(0),
                           D.stride(0), 0 if residual is None else residual.stride(0))
-    s = _current(dev.index) if side is None else _handle(side, (x, W, A, B, D, adapters, scales, bias, residual, u))
-    _run(_native.lib().tmg_lora_linear, a, s, dev)
+    s = _current(i) if side is None else _handle(side, (x, W, A, B, D, adapters, scales, bias, residual, u))
+    _run(_native.lib().tmg_lora_linear, a, s, i)
     return D
 
 
@@ -113,21 +134,20 @@ def lora_linear_backward(dD: torch.Tensor, x: torch.Tensor, W: torch.Tensor, A: 
     adapter l (zeros without any), shaped as A and B.  u: as lora_linear saved
     it.  The residual's gradient is dD; for those of W and the bias there is
     linear_backward."""
-    M, N = _matrix("dD", dD)
-    K = _matrix("x", x)[1]
+    i = _gpu("dD", dD, 2)
+    M, N = dD.shape
+    K = _dims("x", x, 2)[1]
+    L, r, _ = _dims("A", A, 3)
     dev = dD.device
     side = None if stream is None else _side(stream, dev)
     new = _empty(side)
-    _check("dD", dD, _bf16, (M, N))
-    _check("x", x, _bf16, (M, K), dev)
-    _check("W", W, _bf16, (N, K), dev)
-    L, r, a_ptr, b_ptr = _adapter_shapes(A, B, N, K, dev)
-    of, u_ptr = _flat("adapters", adapters, _i32, (M,), dev), _flat("u", u, _bf16, (M, r), dev)
     dx = new((M, K), dtype=_bf16, device=dev)
     dA, dB = new((L, r, K), dtype=_bf16, device=dev), new((L, N, r), dtype=_bf16, device=dev)
-    a = _native.pack_lora_grad(dD.data_ptr(), x.data_ptr(), W.data_ptr(), a_ptr, b_ptr, of,
-                               0 if scales is None else _flat("scales", scales, _f32, (L,), dev), u_ptr, dx.data_ptr(),
-                               dA.data_ptr(), dB.data_ptr(), M, N, K, r, L, dD.stride(0), x.stride(0), W.stride(0))
-    s = _current(dev.index) if side is None else _handle(side, (dD, x, W, A, B, adapters, scales, u, dx, dA, dB))
-    _run(_native.lib().tmg_lora_linear_backward, a, s, dev)
+    a = _native.pack_lora_grad(_rows("dD", dD, _bf16, (M, N), i), _rows("x", x, _bf16, (M, K), i), _rows("W", W, _bf16, (N, K), i),
+                               _flat("A", A, _bf16, (L, r, K), i), _flat("B", B, _bf16, (L, N, r), i),
+                               _flat("adapters", adapters, _i32, (M,), i),
+                               0 if scales is None else _flat("scales", scales, _f32, (L,), i), _flat("u", u, _bf16, (M, r), i),
+                               dx.data_ptr(), dA.data_ptr(), dB.data_ptr(), M, N, K, r, L, dD.stride(0), x.stride(0), W.stride(0))
+    s = _current(i) if side is None else _handle(side, (dD, x, W, A, B, adapters, scales, u, dx, dA, dB))
+    _run(_native.lib().tmg_lora_linear_backward, a, s, i)
     return dx, dA, dB
