@@ -396,8 +396,9 @@ tmg_status check_lora(int64_t M, int64_t N, int64_t K, int64_t r, int64_t L)
     if (M < 0 || N < 0 || K < 0 || r < 1 || r > 256 || L < 1 || L > 1024)
         return fail(TMG_ERR_INVALID_ARG, "adapters need M, N, K >= 0, 1 <= rank <= 256 and 1 <= L <= 1024 (M=%lld N=%lld K=%lld "
                     "rank=%lld L=%lld)", (long long)M, (long long)N, (long long)K, (long long)r, (long long)L);
-    if (M > kMax31 || N > kMax31 || K > kMax31 || M * ((std::max(N, K) + 255) / 256) > kMax31)
-        return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31");
+    const int64_t most = kMax31 - 1024;          // a tile past the last row or column is still an int
+    if (M > most || N > most || K > most)
+        return fail(TMG_ERR_UNSUPPORTED, "extents beyond 2^31 - 1024");
     return TMG_OK;
 }
 
@@ -426,8 +427,8 @@ tmg_status tmg_moe_layer(const tmg_moe_args *g, void *stream)
                         (long long)g->E);
         if (!extents_ok(g->T, g->ldx, g->H, 1) || !extents_ok(g->T, g->residual ? g->ld_residual : 0, g->H, 1) ||
             !extents_ok(g->T, g->ld_out, g->H, 1) || !out_rows_ok(g->T, g->H, g->ld_out) ||
-            !extents_ok(g->E, 1, 1, 1, 2 * g->F, g->H > 0 ? g->H * g->E : 0))
-            return fail(TMG_ERR_INVALID_ARG, "row strides out of range (the output's must be at least H)");
+            static_cast<__int128>(g->E) * 2 * g->F * g->H >= static_cast<__int128>(1) << 60)
+            return fail(TMG_ERR_INVALID_ARG, "row strides out of range (the output's must be at least H), or weights beyond int64");
         if (g->T == 0 || g->H == 0)
             return TMG_OK;
         if (!g->logits || !g->out || !g->x || (g->F > 0 && (!g->W1 || !g->W2)))

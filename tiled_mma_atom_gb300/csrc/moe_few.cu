@@ -168,7 +168,7 @@ __device__ __forceinline__ void few_hidden(const MoeFewArgs &p, const FewSmem &s
 }
 
 template <int C, bool BF16>
-__global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
+__global__ void __launch_bounds__(kFwThreads, 2) moe_few_up_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ FewSmem sm;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kFwThreads) moe_few_up_kernel(const __grid_con
 }
 
 template <int C, bool BF16>
-__global__ void __launch_bounds__(kFwThreads) moe_few_down_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
+__global__ void __launch_bounds__(kFwThreads, 2) moe_few_down_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ FewSmem sm;
