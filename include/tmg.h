@@ -460,8 +460,16 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
 /* The whole expert layer in one call:
  *   z = x[t] . W1[e]^T (2 F columns), h = silu(z[f]) * z[F + f],
  *   out[t] = bf16(residual[t] + sum_j w[t, j] * W2[e[t, j]] . h),
- * with experts e and weights w as tmg_moe_route chooses them from the logits.
- * Sums are fp32; h is rounded to bf16. */
+ * with experts e and weights w as tmg_moe_route chooses them from the logits, fp32
+ * sums; a token without a choice gets its residual (or zeros).  No token's result
+ * depends on what others, or experts that only others chose, hold.
+ * Up to 64 tokens and 256 experts, with H and F multiples of 8 and x, W1 and W2
+ * readable in 16-byte rows, it runs in kernels of its own, which round w * h to
+ * bf16; else tmg_moe_route, both products and tmg_moe_combine follow one
+ * another, which round h and each expert's answer.  Training takes those calls,
+ * as the gradients need what lies between them.
+ * Results do not depend on timing.  Workspace as above: 2 F times the padded
+ * tokens of every expert in use, or what lies between those calls. */
 typedef struct {
     const void *x;          /* device, bf16 (T, H), row stride ldx */
     const void *logits;     /* device, (T, E) of logits_dtype, row stride ld_logits (>= E) */
@@ -484,9 +492,13 @@ tmg_status tmg_moe_layer(const tmg_moe_args *args, void *stream);
  *   u[m] = bf16(scales[a] * x[m] . A[a]^T);
  *   D[m] = bf16(x[m] . W^T + u[m] . B[a]^T + bias + residual[m]).
  * A row whose adapter is not one of 0 .. L - 1 (-1, say) has u = 0 and adds
- * nothing: what another row's adapter holds, infinities and NaN too, never
- * reaches it.  Rows of one request are best adjacent: the time grows with the
- * number of different adapters in 128 or 256 rows in a row. */
+ * nothing.  What another row or its adapter holds, infinities and NaN too,
+ * never reaches a row.  Rows of one request are best adjacent: beyond 64 rows the
+ * time grows with the number of different adapters in 128 or 256 rows in a row.
+ * x, W, A and B whose rows (of K, of K, of K and of r elements) are 16-byte aligned
+ * are read in place, others copied to workspace.  Adapters of a lower rank are
+ * padded with zeros.  Results do not depend on timing.  Workspace as for the
+ * grouped products. */
 typedef struct {
     const void *x;          /* device, bf16 (M, K), row stride ldx */
     const void *W;          /* device, bf16 (N, K), row stride ldw */
@@ -498,7 +510,7 @@ typedef struct {
     const float *bias;      /* device, fp32 (N) or NULL */
     const void *residual;   /* bf16 (M, N), row stride ld_residual, or NULL; may be D */
     void *u;                /* bf16 (M, r) contiguous, for the gradient, or NULL */
-    int64_t M, N, K, r, L;  /* 1 <= r <= 256, 1 <= L <= 1024 */
+    int64_t M, N, K, r, L;  /* M, N, K below 2^31 - 1024; 1 <= r <= 256; 1 <= L <= 1024 */
     int64_t ldx, ldw, ldd, ld_residual;
 } tmg_lora_args;
 
@@ -513,7 +525,7 @@ tmg_status tmg_lora_linear(const tmg_lora_args *args, void *stream);
 typedef struct {
     const void *dD;         /* device, bf16 (M, N), row stride ldd */
     const void *x, *W;      /* as above; x may be NULL without dA, W without dx */
-    const void *A, *B;      /* as above; A may be NULL without dx */
+    const void *A, *B;      /* as above; A may be NULL without dx, B without dx and dA */
     const int32_t *adapters;
     const float *scales;
     const void *u;          /* bf16 (M, r) contiguous, as tmg_lora_linear left it; NULL without dB */

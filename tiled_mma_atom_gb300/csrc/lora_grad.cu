@@ -23,7 +23,8 @@
 // gradients of 8191 x 4096 and 8191 x 4096 took 37 us).
 //
 // Warps: 0 Y's TMA producer, 1 MMA issuer and TMEM owner, 2..5 epilogue, 6 Z's copies;
-// two accumulators in turn.  Bound by HBM: Y once.
+// two accumulators in turn.  Bound by HBM: Y once; both gradients of 8191 x 4096 and 8191 x
+// 4096, rank 16, 134 MB, 26 us (5.2 TB/s).
 #include "feed.cuh"
 #include "launch.cuh"
 #include "lora.cuh"

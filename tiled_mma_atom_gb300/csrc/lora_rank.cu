@@ -16,7 +16,8 @@
 // r read as zeros.  Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2..5 the
 // rows' scales and the accumulator's way to shared memory; all six add up the partials.
 //
-// Bound by HBM: X once.
+// Bound by HBM: X once.  8191 x 4096, rank 16: 12 - 15 us (4.5 - 5.6 TB/s); 700 x 4096, rank
+// 32: 7 us, latency.
 #include "feed.cuh"
 #include "launch.cuh"
 #include "lora.cuh"

@@ -71,9 +71,9 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, W1: torch.Tensor, W2: torch
     x (T, H) bfloat16; logits (T, E) float32 or bfloat16, from which experts and
     weights are chosen as by moe_route (`normalize` as there); W1 (E, 2F, H) and
     W2 (E, H, F) bfloat16, contiguous; residual (T, H) bfloat16 (out itself is
-    allowed).  The same as moe_route, grouped_gemm with SwiGLU, grouped_gemm and
-    moe_combine, which it runs for many tokens; training takes those, since the
-    gradients need what lies between them."""
+    allowed).  Up to 64 tokens the layer has kernels of its own; more run
+    moe_route, grouped_gemm with SwiGLU, grouped_gemm and moe_combine.  Training
+    takes those, since the gradients need what lies between them."""
     i = _gpu("x", x, 2)
     T, H = x.shape
     E = _dims("logits", logits, 2)[1]
