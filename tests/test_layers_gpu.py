@@ -581,3 +581,26 @@ def test_training_step(tmg, M):
         # over the sum the relative error of its root of squares is below 8 * 2^-8
         bound = 8 * ROUND * (g.to(W) * way).pow(2).sum().sqrt() * 4 + 8 * ROUND * slope.abs()
         assert ((g.to(W) * way).sum() - slope).abs() <= bound, i
+
+
+def test_lora_results_past_2_31_elements(tmg):
+    """More than 2^31 elements of D and of dx; rows at both ends and around the border."""
+    M, N, K, r, L = 66000, 33000, 64, 8, 3
+    t = lora_inputs(M, N, K, r, L, 190)
+    ids = ids_of("runs", M, L, 191)
+    D = tmg.lora_linear(t["x"], t["W"], t["A"], t["B"], ids, scales=t["scales"])
+    tmg.check()
+    rows = torch.tensor([0, 1, 130, 65075, 65076, 65077, M - 2, M - 1], device=DEV)
+    want, err, _, _ = adapted(t["x"][rows], t["W"], t["A"], t["B"], ids[rows], t["scales"])
+    close(D[rows], want, err)
+    del D
+    dD, u = normal((M, K), 192), normal((M, r), 193)
+    b = lora_inputs(8, K, N, r, L, 194)
+    x = torch.zeros(M, N, dtype=BF16, device=DEV)
+    dx, dA, dB = tmg.lora_linear_backward(dD, x, b["W"], b["A"], b["B"], ids, u)
+    tmg.check()
+    (want, err), _, _ = gradients(dD[rows], x[rows], b["W"], b["A"], b["B"], ids[rows], u[rows])
+    close(dx[rows], want, err)
+    assert not dA.any()
+    _, _, (want, err) = gradients(dD, x[:, :1], b["W"][:, :1], b["A"][:, :, :1], b["B"], ids, u)
+    close(dB, want, err)
