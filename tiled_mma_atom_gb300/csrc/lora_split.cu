@@ -5,14 +5,14 @@
 //
 // As in lora_pair.cu the accumulator's lanes are the rows, and an MMA on an adapter's
 // block leaves out the rows of others.  The fp32 partial sums meet in shared memory as
-// in split_kernel.cuh, in rank order; each CTA finishes a share of the rows.  Two CTAs
-// fit an SM.  Only U's loads wait for the kernel that makes it.
+// in split_kernel.cuh, in rank order; each CTA finishes a share of the rows.
+// Only U's loads wait for the kernel that makes it.
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 4..7 the accumulator's way to
 // shared memory; all eight add up the partial sums.
 //
-// Bound by latency: 700 x 1024 x 4096, rank 32, 48 tiles over clusters of two, 12 us for
-// x and W beside the ranks, 2 for the adapters' blocks, 4 for the sums.
+// Bound by latency: 700 x 1024 x 4096, rank 32, 48 tiles over clusters of two, 16 us, of
+// them 9 for x and W beside the ranks, 2 for the adapters' blocks, 4 for the sums.
 #include "feed.cuh"
 #include "launch.cuh"
 #include "lora.cuh"
@@ -24,25 +24,24 @@ namespace tmg {
 namespace {
 
 constexpr int kLsThreads = 256;
-constexpr int kLsStages = 3;
+constexpr int kLsMinStages = 3, kLsMaxStages = 5;
 constexpr int kLsStageBytes = 32768;
 constexpr int kLsTile = 128;
-constexpr int kLsBars = (2 * kLsStages + 1) * 8 + 24;       // barriers; TMEM address, abort flag, number of adapters
-constexpr int kLsSmem = 1024 + kLsStages * kLsStageBytes + kLsTile * 20 + kLsBars;
+constexpr int kLsBars = (2 * kLsMaxStages + 1) * 8 + 24;    // barriers; TMEM address, abort flag, number of adapters
 constexpr int kLsWidth = kLsTile + 4;                       // of a row of partial sums
-static_assert(kLsTile * kLsWidth * 4 <= kLsStages * kLsStageBytes, "the partial sums lie over the ring");
+static_assert(kLsTile * kLsWidth * 4 <= kLsMinStages * kLsStageBytes, "the partial sums lie over the ring");
 
 template <bool MAJ>
-__global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_constant__ LoraPairArgs p, int S, ErrCtx err)
+__global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_constant__ LoraPairArgs p, int S, int stages, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    uint4 *masks = reinterpret_cast<uint4 *>(smem + kLsStages * kLsStageBytes);
+    uint4 *masks = reinterpret_cast<uint4 *>(smem + stages * kLsStageBytes);
     int *list = reinterpret_cast<int *>(masks + kLsTile);
     uint64_t *full = reinterpret_cast<uint64_t *>(list + kLsTile);
-    uint64_t *empty = full + kLsStages;
-    uint64_t *done = empty + kLsStages;
+    uint64_t *empty = full + kLsMaxStages;
+    uint64_t *done = empty + kLsMaxStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *count = reinterpret_cast<int *>(tmem_slot + 2);
@@ -55,7 +54,7 @@ __global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_con
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kLsStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_con
         };
         auto step = [&] {
             ++issued;
-            if (++stage == kLsStages) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_con
         };
         auto give = [&] {
             mma_commit_w(&empty[stage]);
-            if (++stage == kLsStages) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_con
     cluster_sync();                  // every CTA's partial sums are written
     if (warp < 2 && *abort_flag) {
         if (warp == 0)
-            settle(full, kLsStages, stage, phase, issued, err.word, err.budget_ns);
+            settle(full, stages, stage, phase, issued, err.word, err.budget_ns);
         else
             settle(done, 1, 0, 1, 1, err.word, err.budget_ns);
         __syncwarp();
@@ -244,11 +243,18 @@ __global__ void __launch_bounds__(kLsThreads) lora_split_kernel(const __grid_con
 cudaError_t launch_lora_split(const LoraPairArgs &a, bool maj, int cluster, const ErrCtx &err, cudaStream_t s)
 {
     auto kern = maj ? lora_split_kernel<true> : lora_split_kernel<false>;
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), kLsSmem);
+    // One CTA per SM and a deep ring (700 x 1024 x 4096 19.0 -> 16.0 us, 128 x 8192 x 8192
+    // 37.7 -> 33.5), but two for clusters of eight, of which too few find eight free SMs
+    // otherwise (500 x 512 x 8192 23.1 us, 28.8 deep), and for gradients, whose next kernel
+    // starts on the SMs beside this one (100 x 4096 x 4096 34.8 us, 37.7 deep; 128 x 8192 x
+    // 8192 57.7, 54.5 deep).
+    const int stages = (maj || cluster > 4) ? kLsMinStages : kLsMaxStages;
+    const int smem = 1024 + stages * kLsStageBytes + kLsTile * 20 + kLsBars;
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = static_cast<int64_t>((a.M + kLsTile - 1) / kLsTile) * ((a.N + kLsTile - 1) / kLsTile);
-    return launch_overlapped(kern, dim3(static_cast<unsigned>(tiles * cluster)), kLsThreads, kLsSmem, cluster, s, a, cluster, err);
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(tiles * cluster)), kLsThreads, smem, cluster, s, a, cluster, stages, err);
 }
 
 }  // namespace tmg
