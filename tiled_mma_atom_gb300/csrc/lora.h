@@ -99,6 +99,7 @@ struct LoraGradArgs {
     uint32_t *counters;                // lora_grad_counters(), zero between launches
     int runs, stages, stage_bytes, tmem_cols;     // set by the launch
 };
+int64_t lora_grad_ctas(const LoraGradArgs &a, int num_sms);
 size_t lora_grad_partial_bytes(const LoraGradArgs &a, int num_sms);
 size_t lora_grad_counters(const LoraGradArgs &a, int num_sms);
 cudaError_t launch_lora_grad(LoraGradArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
