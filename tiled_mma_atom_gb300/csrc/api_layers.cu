@@ -317,7 +317,7 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, const Adapte
     p.vec_ok = a.ldd % 8 == 0 && aligned(a.D);
     log_choice("bf16 with adapters: %d rows, N=%d K=%d rank %d -> lora_pair_kernel: 256 x %d tiles, weights %s", p.M, p.N, p.K,
                p.r, bn, a.across ? "MN-major" : "K-major");
-    return launched(launch_lora_pair(p, bn, a.across, pairs, err_ctx(ds), s), "product with adapters launch");
+    return launched(launch_lora_pair(p, bn, a.across, static_cast<int>(t.ctas / 2), err_ctx(ds), s), "product with adapters launch");
 }
 
 // The layer in two kernels (three with more than 16 tokens), for few tokens: 16 tokens of
