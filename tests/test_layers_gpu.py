@@ -371,6 +371,68 @@ def test_lora_strides_and_in_place(tmg, M):
     assert torch.equal(here, want)
 
 
+@pytest.mark.parametrize("K", [448, 512, 520, 1024, 2056, 4096, 8200])
+@pytest.mark.parametrize("M,r", [(1, 1), (1, 8), (1, 16), (1, 20), (1, 32), (2, 16), (3, 5), (4, 8), (5, 6), (32, 1), (33, 1), (3, 16)])
+def test_lora_of_few_ranks(tmg, M, r, K):
+    """Up to 32 ranks of all rows, where one kernel does it all, and just above."""
+    N = 300
+    t = lora_inputs(M, N, K, r, 6, 35)
+    wide = normal((M, K + 24), 36)
+    for off, kind in ((0, "each"), (8, "outside"), (3, "runs")):
+        t["x"] = wide[:, off:off + K]
+        ids = ids_of(kind, M, 6, K)
+        _, u = check_lora(tmg, t, ids, bias=normal(N, 37, dtype=F32), residual=normal((M, N), 38), scaled=off > 0, name=kind)
+        room = torch.full((M * r + 2,), 7.0, dtype=BF16, device=DEV)
+        tmg.lora_linear(t["x"], t["W"], t["A"], t["B"], ids, scales=t["scales"] if off else None, u=room[1:-1].view(M, r))
+        assert torch.equal(room[1:-1].view(M, r), u) and room[0] == 7 and room[-1] == 7
+
+
+@pytest.mark.parametrize("r", [16, 24])
+def test_lora_of_few_ranks_keeps_requests_apart(tmg, r):
+    """Infinities of an adapter and of a row reach the rows that have them alone."""
+    N, K = 264, 2048
+    t = lora_inputs(2, N, K, r, 3, 39)
+    ids = torch.tensor([0, 2], dtype=torch.int32, device=DEV)
+    want = tmg.lora_linear(t["x"], t["W"], t["A"], t["B"], ids)
+    t["A"][1], t["B"][1] = float("inf"), float("nan")
+    assert torch.equal(tmg.lora_linear(t["x"], t["W"], t["A"], t["B"], ids), want)
+    t["A"][2, 1, K - 1] = float("inf")
+    got = tmg.lora_linear(t["x"], t["W"], t["A"], t["B"], ids)
+    assert torch.equal(got[0], want[0]) and not got[1].isfinite().any()
+
+
+def test_lora_of_few_ranks_in_a_row(tmg):
+    """Calls that read the results of the ones before, in one stream and in a graph."""
+    H = 1024
+    t = [lora_inputs(2, H, H, 16, 4, 40 + i) for i in range(6)]
+    ids = ids_of("each", 2, 4, 1)
+    first = t[0]["x"].clone()
+
+    def chain(sync):
+        x = first
+        for c in t + t:
+            x = tmg.lora_linear(x, c["W"], c["A"], c["B"], ids, residual=x)
+            if sync:
+                torch.cuda.synchronize()
+        return x
+
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain(False)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = chain(False)
+        first.copy_(t[1]["x"])
+        graph.replay()
+    s.synchronize()
+    assert torch.equal(out, chain(True)) and not torch.equal(out, want)
+    tmg.check()
+
+
 @pytest.mark.parametrize("M", [4, 50, 64, 300])
 def test_lora_keeps_requests_apart(tmg, M):
     """NaN and infinities of one request, or of its adapter, reach no other request's rows or gradients."""

@@ -372,8 +372,9 @@ tmg_status moe_few(const DeviceState &ds, const tmg_moe_args &g, cudaStream_t s)
     return launched(launch_moe_few(p, ds.num_sms, err_ctx(ds), s), "expert layer launch");
 }
 
-// The same for a few rows, not across.
-tmg_status run_adapted_few(const DeviceState &ds, const AdaptedArgs &a, cudaStream_t s)
+// The same for a few rows, not across; with: U by the same kernel, to with->U if that is
+// not null.
+tmg_status run_adapted_few(const DeviceState &ds, const AdaptedArgs &a, const RankArgs *with, cudaStream_t s)
 {
     tmg_status st;
     LoraFewArgs p;
@@ -384,7 +385,15 @@ tmg_status run_adapted_few(const DeviceState &ds, const AdaptedArgs &a, cudaStre
     if ((st = encode_nd(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.W.p, wd, wst, wbox)) != TMG_OK ||
         (st = encode_nd(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x.p, xd, xs, xbox, true)) != TMG_OK)
         return st;
-    p.U = a.U;
+    if (with) {
+        p.U = with->U;
+        p.X = a.x.p;
+        p.ldx = a.x.ld;
+        p.A = with->F;
+        p.scales = with->scales;
+    } else {
+        p.U = const_cast<void *>(a.U);
+    }
     p.F = a.F.p;
     p.D = a.D;
     p.adapters = a.adapters;
@@ -476,29 +485,28 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
             return st;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const StreamLock lock(s);
-        const int64_t ldu = g->u && g->r % 8 == 0 && aligned(g->u) ? g->r : up(g->r, 8);
-        void *u = g->u;
-        if (!u || ldu != g->r || !aligned(u)) {
-            u = workspace(kWsLayer, g->M * ldu * 2, s, &st);
-            if (!u)
+        RankArgs k{g->x, g->A, g->adapters, g->scales, g->u, g->M, g->K, g->L, g->ldx, up(g->r, 8), static_cast<int>(g->r), false};
+        const bool few = g->M <= kLoraFewRows && g->r <= kLoraFewRanks;
+        const bool with = few_ranks(k) && lora_few_with(g->M, g->N, g->K, g->r, ds->num_sms);
+        const int64_t ldu = k.ldu;
+        if (!with && (!k.U || ldu != g->r || !aligned(k.U))) {
+            k.U = workspace(kWsLayer, g->M * ldu * 2, s, &st);
+            if (!k.U)
                 return st;
         }
-        Rows x;
-        if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &x)) != TMG_OK)
-            return st;
         // every copy of an operand comes before the kernel that makes u: the product runs
         // beside that one
         AdaptedArgs a{};
         Rows f{};
-        RankArgs k{g->x, g->A, g->adapters, g->scales, u, g->M, g->K, g->L, g->ldx, ldu, static_cast<int>(g->r), false};
         if ((st = tma_rows(*ds, kWsPackA, g->x, g->ldx, g->M, g->K, g->M, s, &a.x)) != TMG_OK ||
             (g->N > 0 && (st = tma_rows(*ds, kWsPackB, g->W, g->ldw, g->N, g->K, g->N, s, &a.W)) != TMG_OK) ||
             (g->N > 0 && (st = tma_rows(*ds, kWsLayoutB, g->B, g->r, g->L * g->N, g->r, g->L * g->N, s, &a.F)) != TMG_OK) ||
             (g->K > 0 && !few_ranks(k) &&
              (st = tma_rows(*ds, kWsFactor, g->A, g->K, g->L * g->r, g->K, g->L * g->r, s, &f)) != TMG_OK) ||
-            (st = run_rank(*ds, k, a.x, f, false, s)) != TMG_OK)
+            (!with && (st = run_rank(*ds, k, a.x, f, false, s)) != TMG_OK))
             return st;
-        if (g->u && u != g->u) {               // the caller's own, in its layout
+        a.U = k.U;
+        if (g->u && k.U != g->u) {             // the caller's own, in its layout
             k.U = g->u;
             k.ldu = g->r;
             if ((st = run_rank(*ds, k, a.x, f, false, s)) != TMG_OK)
@@ -506,7 +514,6 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
         }
         if (g->N == 0)
             return TMG_OK;
-        a.U = u;
         a.D = g->D;
         a.adapters = g->adapters;
         a.bias = g->bias;
@@ -519,8 +526,8 @@ tmg_status tmg_lora_linear(const tmg_lora_args *g, void *stream)
         a.ldu = ldu;
         a.ldd = g->ldd;
         a.ld_residual = g->ld_residual;
-        if (g->M <= kLoraFewRows && g->r <= kLoraFewRanks)
-            return run_adapted_few(*ds, a, s);
+        if (few)
+            return run_adapted_few(*ds, a, with ? &k : nullptr, s);
         AdaptedTiles t;
         return (st = adapted_tiles(a, ds->num_sms, &t)) != TMG_OK ? st : run_adapted(*ds, a, t, s);
     });

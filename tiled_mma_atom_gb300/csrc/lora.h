@@ -38,20 +38,25 @@ cudaError_t launch_lora_rank_tc(LoraRankArgs a, bool maj, int num_sms, const Err
 // D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] for at most
 // kLoraFewRows rows and kLoraFewRanks ranks (the factors of 32 columns of every warp,
 // U and the results must fit shared memory beside the ring).
-constexpr int kLoraFewRows = 64, kLoraFewRanks = 128;
+// With A given, U is made by the same kernel, where lora_few_with() holds.
+constexpr int kLoraFewRows = 64, kLoraFewRanks = 128, kLoraFewWith = 32;
 struct LoraFewArgs {
     CUtensorMap tmW;           // (N, K): 128 rows of 64
     CUtensorMap tmX;           // (M, K): shape.tp rows of 64
-    const void *U, *F;         // rows of ldu, and (L, N) rows of ldf, both 16-byte aligned
+    const void *F;             // (L, N) rows of ldf, 16-byte aligned
+    void *U;                   // rows of ldu, 16-byte aligned; with A: (M, r), written, or null
+    const void *X, *A;         // with A: rows of ldx and (L, r, K), 16-byte aligned, K a multiple of 8
+    const float *scales;       // or null
     void *D;
     const int32_t *adapters;
     const float *bias;
     const void *residual;
-    int64_t ldu, ldf, ldd, ld_residual;
+    int64_t ldu, ldx, ldf, ldd, ld_residual;
     int M, N, K, L, r;
     FewShape shape;            // tp; the rest is set by the launch
     int room_bytes;            // set by the launch
 };
+bool lora_few_with(int64_t M, int64_t N, int64_t K, int64_t r, int num_sms);
 cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s);
 
 // D[m] = x[m] . W^T + U[m] . F[adapters[m]]^T + bias + residual[m] on CTA pairs, or with

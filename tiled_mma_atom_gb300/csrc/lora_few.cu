@@ -8,8 +8,14 @@
 // lets the second one start only after its own wait for the kernel before, so x and
 // the weights are complete by then.
 //
+// One kernel for both where the rows have few ranks in all: every cluster makes U again,
+// each CTA over the K blocks whose W it streams, beside W's flood.  Up to 32 ranks cost
+// 0.1 to 0.6 us on top of the product (1 x 4096 x 4096, rank 16, 9.1 us, in two kernels 10.5;
+// 2 x 11000 x 4096 18.1 and 20.0; 1 x 4096 x 1024 6.1 and 5.7), 48 more than the other
+// kernel (3 x 4096 x 4096 11.9 and 11.1).
+//
 // Bound by HBM: W and the rows' factors once.  16 x 8192 x 8192 of rank 16, 139 MB, 27.1
-// us (5.1 TB/s, 6.3 while W streams); 1 x 4096 x 4096 10.1 us; 61 rows of rank 64, 32
+// us (5.1 TB/s, 6.3 while W streams); 1 x 4096 x 4096 9.1 us; 61 rows of rank 64, 32
 // adapters, 4096 x 4096 19.5 us.
 #include <cuda_bf16.h>
 
@@ -104,17 +110,71 @@ __device__ __forceinline__ float ld_cluster_one(uint32_t addr, uint32_t rank)
     return v;
 }
 
+// Warps 4 .. 11, where U is made here: the rows' ranks, four a warp at most, over this
+// CTA's K blocks.  The sums go to every CTA of the cluster, part[CTA][rank].
+__device__ __forceinline__ void send_ranks(const LoraFewArgs &p, float (*part)[kLoraFewWith], uint64_t *bar, int kb0, int kb1, uint32_t S,
+                                           uint32_t rank)
+{
+    constexpr int n = kLoraFewWith / kLfWarps;
+    const int warp = threadIdx.x / 32 - 4, lane = threadIdx.x % 32, units = p.M * p.r;
+    const int lo = kb0 * 8, hi = min(kb1 * 64, p.K) / 8;       // in 16 bytes
+    const uint4 *f[n], *x[n];
+    float sum[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        const int unit = warp + i * kLfWarps, m = unit / p.r, j = unit - m * p.r;
+        const int l = unit < units ? p.adapters[m] : -1;
+        sum[i] = 0.f;
+        x[i] = f[i] = nullptr;
+        if (l >= 0 && l < p.L) {
+            x[i] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.X) + m * p.ldx);
+            f[i] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.A) + (static_cast<int64_t>(l) * p.r + j) * p.K);
+        }
+    }
+    for (int c = lo + lane; c - lane < hi; c += 64) {
+        uint4 v[n][2], w[n][2];
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = f[i] && c + 32 * h < hi;
+                v[i][h] = in ? f[i][c + 32 * h] : make_uint4(0, 0, 0, 0);
+                w[i][h] = in ? x[i][c + 32 * h] : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                sum[i] = dot8(v[i][h], w[i][h], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+        const int unit = warp + i * kLfWarps;
+        if (unit >= units)
+            break;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        if (lane < static_cast<int>(S))
+            st_async_u32(mapa_shared(smem_u32(&part[rank][unit]), lane), __float_as_uint(sum[i]), mapa_shared(smem_u32(bar), lane));
+        __syncwarp();
+    }
+}
+
 // Warps 4 .. 11.  The results of this CTA in units of 32 columns of a row, a warp's
 // in turn: their factor rows, 32 x ldf contiguous elements, come by bulk copies, as
 // many units ahead as the warp's room holds and the first ones before U is there.
 // share[] = U[m] . F[a_m][n] + bias + residual.  A lane takes the 16-byte chunks of
 // its factor row from a start of its own, so that eight lanes touch all banks.
+// get_ranks(m0, rows): those rows' U to us[row][ldu], by all eight warps.
+template <class GetRanks>
 __device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *room, uint64_t *bars, __nv_bfloat16 *us, float *share,
-                                               int n0, int first, int last, volatile int *abort_flag, const ErrCtx &err)
+                                               int n0, int first, int last, GetRanks &&get_ranks, volatile int *abort_flag,
+                                               const ErrCtx &err)
 {
     const int warp = threadIdx.x / 32 - 4, lane = threadIdx.x % 32;
     const int unit_bytes = static_cast<int>(32 * p.ldf * 2), depth = p.room_bytes / unit_bytes, chunks = static_cast<int>(p.ldf / 8);
-    const __nv_bfloat16 *U = static_cast<const __nv_bfloat16 *>(p.U), *F = static_cast<const __nv_bfloat16 *>(p.F);
+    const __nv_bfloat16 *F = static_cast<const __nv_bfloat16 *>(p.F);
     const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
     uint32_t pending = 0;                                // slots with a copy under way
     // copy unit x's factor rows (of columns inside N) if its row has an adapter
@@ -130,10 +190,8 @@ __device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *ro
     for (int d = 0; d < depth && first + warp + d * kLfWarps < last; ++d)
         fetch(first + warp + d * kLfWarps, d);
     const int m0 = first / 4, rows = last > first ? (last - 1) / 4 - m0 + 1 : 0;
-    grid_wait();                                         // U
     const int per = static_cast<int>(p.ldu / 8);
-    for (int i = threadIdx.x - 128; i < rows * per; i += kLfWarps * 32)
-        reinterpret_cast<uint4 *>(us)[i] = __ldcg(reinterpret_cast<const uint4 *>(U + (m0 + i / per) * p.ldu) + i % per);
+    get_ranks(m0, rows);
     asm volatile("bar.sync 1, 256;" ::: "memory");
     uint32_t phases = 0;                                 // of the slots
     int slot = 0;
@@ -171,11 +229,15 @@ __device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *ro
     }
 }
 
-__global__ void __launch_bounds__(kLfThreads) lora_few_kernel(const __grid_constant__ LoraFewArgs p, ErrCtx err)
+// WITH: U is made here too.
+template <bool WITH>
+__global__ void __launch_bounds__(kLfThreads, 2) lora_few_kernel(const __grid_constant__ LoraFewArgs p, ErrCtx err)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ FewRing sm;
     __shared__ uint64_t bars[kLfWarps][kLfMaxDepth];
+    __shared__ uint64_t ranks_bar;
+    __shared__ float ranks_part[WITH ? 8 : 1][kLoraFewWith];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t *room = ring + p.shape.ring_bytes;
@@ -190,18 +252,61 @@ __global__ void __launch_bounds__(kLfThreads) lora_few_kernel(const __grid_const
     if (threadIdx.x < kLfWarps * kLfMaxDepth)
         mbar_init(&bars[0][0] + threadIdx.x, 1);
     few_setup(p.shape, sm, &p.tmW, &p.tmX);
+    if (WITH && threadIdx.x == 0) {
+        mbar_init(&ranks_bar, 1);
+        mbar_arrive_expect_tx(&ranks_bar, S * static_cast<uint32_t>(p.M * p.r) * 4u);
+    }
+    __syncwarp();
     fence_mbar_init();
     grid_release();
-    __syncthreads();
+    if constexpr (WITH) {
+        cluster_sync();              // the barriers that the others' sums arrive at
+        grid_wait();
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
+    auto get_ranks = [&](int m0, int rows) {
+        const int thread = threadIdx.x - 128;
+        if constexpr (WITH) {
+            send_ranks(p, ranks_part, &ranks_bar, kb0, kb1, S, rank);
+            if (!mbar_wait_cluster_warp(&ranks_bar, 0, err, &sm.abort, kSiteMmaFull))
+                settle(&ranks_bar, 1, 0, 1, 1, err.word, err.budget_ns);
+            auto sum = [&](int m, int j) {
+                const int l = p.adapters[m];
+                float u = 0.f;
+                if (j < p.r && l >= 0 && l < p.L) {
+                    for (uint32_t x = 0; x < S; ++x)
+                        u += ranks_part[x][m * p.r + j];
+                    if (p.scales)
+                        u *= p.scales[l];
+                }
+                return __float2bfloat16_rn(u);
+            };
+            const int ldu = static_cast<int>(p.ldu);
+            for (int i = thread; i < rows * ldu; i += kLfWarps * 32)
+                us[i] = sum(m0 + i / ldu, i % ldu);
+            if (p.U && blockIdx.x == 0)
+                for (int i = thread; i < p.M * p.r; i += kLfWarps * 32)
+                    static_cast<__nv_bfloat16 *>(p.U)[i] = sum(i / p.r, i % p.r);
+        } else {
+            grid_wait();
+            const int per = static_cast<int>(p.ldu / 8);
+            for (int i = thread; i < rows * per; i += kLfWarps * 32)
+                reinterpret_cast<uint4 *>(us)[i] =
+                    __ldcg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.U) + (m0 + i / per) * p.ldu) + i % per);
+        }
+    };
     few_product(
         p.shape, sm, ring, kb0, kb1, [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_2d_w(dst, &p.tmW, bar, kb * 64, n0); },
         [&](uint8_t *dst, uint64_t *bar, int kb) { tma_load_2d_w(dst, &p.tmX, bar, kb * 64, 0); }, [] {},
         [&] {
-            adapters_share(p, room + (warp - 4) * p.room_bytes, bars[warp - 4], us, share, n0, first, last, &sm.abort, err);
+            adapters_share(p, room + (warp - 4) * p.room_bytes, bars[warp - 4], us, share, n0, first, last, get_ranks, &sm.abort,
+                           err);
         },
         err);
-    grid_wait();                     // every warp: no later kernel may start before U's is done
+    if (!WITH)
+        grid_wait();                 // every warp: no later kernel may start before U's is done
     __nv_bfloat16 *D = static_cast<__nv_bfloat16 *>(p.D);
     const int64_t limit = (p.M - 1) * p.ldd + p.N;
     const uint32_t part = smem_u32(ring);
@@ -236,6 +341,13 @@ cudaError_t launch_lora_few_rank(const RankArgs &a, cudaStream_t s)
                              1, s, a, parts, groups);
 }
 
+// Where a cluster reads few ranks beside the weights of its 128 columns, and is one:
+// st.async, by which the sums travel, needs a launch in clusters.
+bool lora_few_with(int64_t M, int64_t N, int64_t K, int64_t r, int num_sms)
+{
+    return N > 0 && K > 0 && M * r <= kLoraFewWith && few_cluster((N + 127) / 128, (K + 63) / 64, 2 * num_sms) > 1;
+}
+
 cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
     const int64_t tiles = (a.N + 127) / 128;
@@ -251,13 +363,14 @@ cudaError_t launch_lora_few(LoraFewArgs a, int num_sms, const ErrCtx &err, cudaS
         if (a.shape.stages >= 2)
             break;
     }
-    if (a.shape.stages < 2)
-        return cudaErrorInvalidValue;                  // more ranks than kLoraFewRanks
+    if (a.shape.stages < 2 || (a.A && S < 2))
+        return cudaErrorInvalidValue;                  // more ranks than kLoraFewRanks; not lora_few_with()
     const int smem = 1024 + a.shape.ring_bytes + rest;
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(lora_few_kernel), smem);
+    auto kern = a.A ? lora_few_kernel<true> : lora_few_kernel<false>;
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(lora_few_kernel, dim3(static_cast<unsigned>(tiles * S)), kLfThreads, smem, S, s, a, err);
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(tiles * S)), kLfThreads, smem, S, s, a, err);
 }
 
 }  // namespace tmg
