@@ -507,6 +507,40 @@ def test_lora_gradients_of_few_rows_among_many(tmg, rows):
     check_grads(tmg, t, ids, normal((M, 136), 77), normal((M, 16), 78))
 
 
+@pytest.mark.parametrize("L", [1, 2, 5, 40])
+@pytest.mark.parametrize("M,N,K,r", [(2500, 264, 200, 16), (1500, 520, 136, 64), (700, 1024, 512, 32)])
+def test_lora_gradients_in_runs(tmg, M, N, K, r, L):
+    """Adapters in one run and cut over several, the factors before dx and after it."""
+    t = lora_inputs(M, N, K, r, L, 75)
+    for kind in ("runs", "one", "outside"):
+        check_grads(tmg, t, ids_of(kind, M, L, L), normal((M, N), 79), normal((M, r), 80), name=kind)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 136, 72), (700, 512, 256), (300, 2048, 1000)])
+def test_lora_gradients_alone(tmg, M, N, K):
+    """Each gradient without the others, and without what only the others need."""
+    from tiled_mma_atom_gb300 import _native
+
+    r, L = 16, 3
+    t = lora_inputs(M, N, K, r, L, 81)
+    ids, d, u = ids_of("runs", M, L, 2), normal((M, N), 82), normal((M, r), 83)
+    exact = gradients(d, t["x"], t["W"], t["A"], t["B"], ids, u, t["scales"])
+    ptr = lambda x, there: x.data_ptr() if there else 0
+    for want in range(8):
+        dx, dA, dB = (bool(want >> i & 1) for i in range(3))
+        out = [torch.full(shape, 3.0, dtype=BF16, device=DEV) for shape in ((M, K), (L, r, K), (L, N, r))]
+        args = _native.pack_lora_grad(d.data_ptr(), ptr(t["x"], dA), ptr(t["W"], dx), ptr(t["A"], dx), ptr(t["B"], dx or dA),
+                                      ids.data_ptr(), t["scales"].data_ptr(), ptr(u, dB), ptr(out[0], dx), ptr(out[1], dA),
+                                      ptr(out[2], dB), M, N, K, r, L, N, K, K)
+        assert _native.lib().tmg_lora_linear_backward(args, torch.cuda.current_stream().cuda_stream) == 0
+        tmg.check()
+        for i, (g, (w, err)) in enumerate(zip(out, exact)):
+            if want >> i & 1:
+                close(g, w, err, f"{want} {i}")
+            else:
+                assert (g == 3).all()
+
+
 def test_lora_of_a_large_model(tmg):
     for M, N, K, r, L in ((1, 4096, 4096, 16, 8), (16, 8192, 8192, 16, 64), (700, 1024, 4096, 32, 16), (2100, 4096, 2048, 64, 4),
                           (1500, 5000, 4104, 8, 3)):
