@@ -36,7 +36,7 @@ def _wrong(name, t, dtype, shape, index, what):
 
 def _rows(name, t, dtype, shape, index):
     """The pointer of a matrix on GPU `index` with unit column stride."""
-    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not (t.is_contiguous() or t.stride(1) == 1 or shape[1] <= 1):
         _wrong(name, t, dtype, shape, index, "row-wise contiguous")
     return t.data_ptr()
 
@@ -84,10 +84,13 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, W1: torch.Tensor, W2: torch
     side = None if stream is None else _side(stream, x.device)
     if out is None:
         out = _empty(side)((T, H), dtype=_bf16, device=x.device)
+        to = out.data_ptr()
+    else:
+        to = _rows("out", out, _bf16, (T, H), i)
     a = _native.pack_moe(_rows("x", x, _bf16, (T, H), i), _rows("logits", logits, logits.dtype, (T, E), i),
                          _flat("W1", W1, _bf16, (E, 2 * F, H), i), _flat("W2", W2, _bf16, (E, H, F), i),
                          0 if residual is None else _rows("residual", residual, _bf16, (T, H), i),
-                         _rows("out", out, _bf16, (T, H), i), T, H, F, E, k, x.stride(0), logits.stride(0),
+                         to, T, H, F, E, k, x.stride(0), logits.stride(0),
                          0 if residual is None else residual.stride(0), out.stride(0), dt, 1 if normalize else 0)
     s = _current(i) if side is None else _handle(side, (x, logits, W1, W2, residual, out))
     _run(_native.lib().tmg_moe_layer, a, s, i)
@@ -113,9 +116,11 @@ def lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tens
     side = None if stream is None else _side(stream, x.device)
     if D is None:
         D = _empty(side)((M, N), dtype=_bf16, device=x.device)
+        to = D.data_ptr()
+    else:
+        to = _rows("D", D, _bf16, (M, N), i)
     a = _native.pack_lora(_rows("x", x, _bf16, (M, K), i), _rows("W", W, _bf16, (N, K), i), _flat("A", A, _bf16, (L, r, K), i),
-                          _flat("B", B, _bf16, (L, N, r), i), _rows("D", D, _bf16, (M, N), i),
-                          _flat("adapters", adapters, _i32, (M,), i),
+                          _flat("B", B, _bf16, (L, N, r), i), to, _flat("adapters", adapters, _i32, (M,), i),
                           0 if scales is None else _flat("scales", scales, _f32, (L,), i),
                           0 if bias is None else _flat("bias", bias, _f32, (N,), i),
                           0 if residual is None else _rows("residual", residual, _bf16, (M, N), i),
