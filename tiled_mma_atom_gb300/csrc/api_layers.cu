@@ -211,9 +211,9 @@ struct AdaptedArgs {
 
 // The CTAs that share a tile of 128 x 128 (lora_split.cu), or 0 for the pair kernel.
 // Where such tiles are at most one for two SMs and the contraction is long, splitting
-// it beats the pairs' larger tiles (100 x 4096 x 4096 17.7 us against 20.0, 128 x 8192 x
-// 8192 37.9 and 46.7, 700 x 1024 x 4096 19.0 and 20.5); with more tiles or a short one it
-// does not (400 x 4096 x 4096 27.3 and 25.9, 1000 x 1024 x 1024 13.1 and 10.1).
+// it beats the pairs' larger tiles (100 x 4096 x 4096 17.6 us against 20.0, 128 x 8192 x
+// 8192 33.4 and 46.7, 700 x 1024 x 4096 16.1 and 20.5); with more tiles or a short one it
+// does not (400 x 4096 x 4096 28.4 and 26.6, 1000 x 1024 x 1024 13.1 and 10.1).
 int split_cluster(int64_t M, int64_t N, int num_kb, int num_sms)
 {
     const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
