@@ -27,6 +27,18 @@ struct FewRing {
     int abort;
 };
 
+// sum + the products of eight bf16 with eight others.
+__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
+{
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
+        sum = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), sum);
+    }
+    return sum;
+}
+
 // Eight consecutive columns of row t of the cluster's S partial tiles.
 __device__ __forceinline__ void few_sum(uint32_t part, int t, int col, uint32_t S, float (&z)[8])
 {

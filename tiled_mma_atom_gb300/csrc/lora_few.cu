@@ -31,17 +31,6 @@ constexpr int kLfManyWarps = 2432;           // of the ranks: two blocks of eigh
 constexpr int kLfSmem = 108 * 1024;          // of a CTA, where two share an SM
 constexpr int kLfBuffer = 4096;              // a warp's room for factors, at least one unit of 32 columns
 
-__device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float sum)
-{
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), sum);
-        sum = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), sum);
-    }
-    return sum;
-}
-
 // J ranks of a row per `parts` warps of the block (a power of two), each with a run
 // of C.  Every load of up to 2048 elements a warp is in flight at once, about when the
 // next kernel starts: behind its flood of W's blocks they would take 5 us and more.

@@ -19,7 +19,8 @@
 // of W2[e_i][:, f] hidden[i][t][f]: a tile of 128 columns of the layer's output
 // accumulates all chosen experts one after another.  A zero times a weight that is
 // infinite or NaN would be NaN in a token that did not choose that expert: where a sum
-// comes out as NaN, it is formed again from the token's own experts alone.
+// comes out as NaN, it is formed again from the token's own experts alone, by a warp for
+// eight columns (few_again()).
 //
 // Where tiles are few, a cluster of CTAs splits a tile's contraction, and the partial sums
 // meet in shared memory as in split_kernel.cuh.  Two CTAs fit an SM.  The second kernel starts
@@ -320,6 +321,100 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_up_kernel(const __grid_
     }
 }
 
+// Columns col .. col + n - 1 of token t's residual, zeros without one.
+__device__ __forceinline__ void few_residual(const MoeFewArgs &p, int t, int col, int n, bool on, float (&f)[8])
+{
+    const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
+    const __nv_bfloat16 *r = res + t * p.ld_residual + col;
+    const bool wide = res && on && n == 8 && (reinterpret_cast<uintptr_t>(r) & 15u) == 0;
+    const uint4 v = wide ? *reinterpret_cast<const uint4 *>(r) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+    if (res && on && !wide)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = j < n ? __bfloat162float(r[j]) : 0.f;
+}
+
+// Eight columns of a token's result: sum + residual, rounded.
+__device__ __forceinline__ void few_store(const MoeFewArgs &p, int t, int col, int n, const float (&z)[8], const float (&add)[8],
+                                          const ErrCtx &err)
+{
+    store_piece(static_cast<__nv_bfloat16 *>(p.out), t * p.ld_out + col,
+                make_uint4(pack_bf16x2(z[0] + add[0], z[1] + add[1]), pack_bf16x2(z[2] + add[2], z[3] + add[3]),
+                           pack_bf16x2(z[4] + add[4], z[5] + add[5]), pack_bf16x2(z[6] + add[6], z[7] + add[7])),
+                n, (p.T - 1) * p.ld_out + p.H, err);
+}
+
+// The results of this CTA with a NaN among their eight columns, a warp for each.  Where the
+// token's own hidden values hold a NaN, that is the sum, whatever the weights hold;
+// else its NaN columns are formed again from its own experts, 256 elements of all
+// eight columns a step.  Out of line: no call reaches it unless a sum is NaN.  8 of 64
+// experts, 2048 x 1024, a NaN in one token's x: one token 23 -> 27 us, 61 tokens 145 -> 155
+// (a thread for eight columns, 1126 and 2523); all weights of eight experts that one
+// of 61 tokens chose infinite, so that every other token's row is formed again, 2.1 ms.
+static __device__ __noinline__ void few_again(const MoeFewArgs &p, const FewSmem &sm, const uint8_t *again, uint32_t part, uint32_t S,
+                                              int n0, int first, int last, const ErrCtx &err)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const __nv_bfloat16 *hidden = static_cast<const __nv_bfloat16 *>(p.hidden), *W2 = static_cast<const __nv_bfloat16 *>(p.W2);
+    int token = -1;
+    bool own = false;                        // the token's hidden values hold a NaN
+    for (int x = first + warp; x < last; x += kFwThreads / 32) {
+        if (!again[x - first])
+            continue;
+        const int t = x / 16, c = x % 16 * 8, col = n0 + c, n = min(8, p.H - col);
+        if (t != token) {
+            token = t;
+            bool nan = false;
+            for (int i = 0; i < sm.chosen; ++i)
+                if (sm.chose(i, t)) {
+                    const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.shape.tp + t) * p.F;
+#pragma unroll 4
+                    for (int f = lane * 8; f < p.F; f += 256) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(h + f);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            nan |= (w[j] & 0x7fffu) > 0x7f80u || (w[j] & 0x7fff0000u) > 0x7f800000u;
+                    }
+                }
+            own = __any_sync(0xffffffffu, nan);
+        }
+        float z[8], add[8];
+        few_sum(part, t, c, S, z);
+        few_residual(p, t, col, n, true, add);
+        if (!own) {
+            float sum[8] = {};
+            for (int i = 0; i < sm.chosen; ++i)
+                if (sm.chose(i, t)) {
+                    const __nv_bfloat16 *w = W2 + (static_cast<int64_t>(sm.list[i]) * p.H + col) * p.F;
+                    const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.shape.tp + t) * p.F;
+                    for (int f = lane * 8; f < p.F; f += 256) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(h + f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < n && z[j] != z[j])
+                                sum[j] = dot8(*reinterpret_cast<const uint4 *>(w + j * static_cast<int64_t>(p.F) + f), v, sum[j]);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+                z[j] = z[j] != z[j] ? sum[j] : z[j];
+            }
+        }
+        if (lane == 0)
+            few_store(p, t, col, n, z, add, err);
+    }
+}
+
 template <int C, bool BF16>
 __global__ void __launch_bounds__(kFwThreads, 2) moe_few_down_kernel(const __grid_constant__ MoeFewArgs p, ErrCtx err)
 {
@@ -339,24 +434,11 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_down_kernel(const __gri
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (rank + 1) / S);
     // this CTA's share of the results, eight columns of a token at a time, the free
     // warps first; the residual is read ahead
-    const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
     const int items = p.T * 16, first = items * rank / S, last = items * (rank + 1) / S;
     const int item0 = first + (threadIdx.x + kFwThreads / 2) % kFwThreads;
     auto read = [&](int x, float (&f)[8]) {
-        const int t = x / 16, col = n0 + x % 16 * 8, n = min(8, p.H - col);
-        const __nv_bfloat16 *r = res + t * p.ld_residual + col;
-        const bool wide = res && x < last && n == 8 && (reinterpret_cast<uintptr_t>(r) & 15u) == 0;
-        const uint4 v = wide ? *reinterpret_cast<const uint4 *>(r) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(w[j] << 16);
-            f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-        if (res && x < last && !wide)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f[j] = j < n ? __bfloat162float(r[j]) : 0.f;
+        const int col = n0 + x % 16 * 8;
+        few_residual(p, x / 16, col, min(8, p.H - col), x < last, f);
     };
     float add[8];
     few_product(
@@ -367,37 +449,29 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_down_kernel(const __gri
     if (threadIdx.x < kFwThreads / 2)
         read(item0, add);
     grid_wait();                     // every warp: the first kernel's hidden rows
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-    const __nv_bfloat16 *hidden = static_cast<const __nv_bfloat16 *>(p.hidden), *W2 = static_cast<const __nv_bfloat16 *>(p.W2);
-    const int64_t limit = (p.T - 1) * p.ld_out + p.H;
     const uint32_t part = smem_u32(ring);
+    uint8_t *again = reinterpret_cast<uint8_t *>(sm.counts);       // of each result: it has a NaN
+    static_assert(kFewTokens * 16 <= sizeof(sm.counts), "a byte per result of a CTA");
+    bool any = false;
     for (int x = item0; x < last; x += kFwThreads) {
         const int t = x / 16, c = x % 16 * 8, col = n0 + c, n = min(8, p.H - col);
-        if (n <= 0)
-            continue;
-        if (x != item0)
-            read(x, add);
-        float z[8];
-        few_sum(part, t, c, S, z);
+        bool nan = false;
+        if (n > 0) {
+            if (x != item0)
+                read(x, add);
+            float z[8];
+            few_sum(part, t, c, S, z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j < n && z[j] != z[j]) {
-                float sum = 0.f;
-                for (int i = 0; i < sm.chosen; ++i)
-                    if (sm.chose(i, t)) {
-                        const __nv_bfloat16 *w = W2 + (static_cast<int64_t>(sm.list[i]) * p.H + col + j) * p.F;
-                        const __nv_bfloat16 *h = hidden + (static_cast<int64_t>(i) * p.shape.tp + t) * p.F;
-                        for (int f = 0; f < p.F; ++f)
-                            sum = fmaf(__bfloat162float(w[f]), __bfloat162float(h[f]), sum);
-                    }
-                z[j] = sum;
-            }
-            z[j] += add[j];
+            for (int j = 0; j < 8; ++j)
+                nan |= j < n && z[j] != z[j];
+            if (!nan)
+                few_store(p, t, col, n, z, add, err);
         }
-        store_piece(out, t * p.ld_out + col,
-                    make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]), pack_bf16x2(z[6], z[7])),
-                    n, limit, err);
+        again[x - first] = nan;
+        any |= nan;
     }
+    if (__syncthreads_or(any))
+        few_again(p, sm, again, part, S, n0, first, last, err);
     __syncwarp();
     cluster_sync();                  // no CTA leaves while its partial sums may be read
 }
