@@ -11,7 +11,10 @@
 //
 // What such a kernel reads may therefore still be written while its grid lives, so
 // it uses plain loads after the wait: no __ldg and no `const __restrict__` pointers
-// (non-coherent loads, for data that nothing writes during the grid's life).  Measured on one call after
+// (non-coherent loads, for data that nothing writes during the grid's life).  A
+// kernel whose predecessor lets it start only after a wait of its own may read the call's
+// inputs before it waits itself: past L1 (TMA, __ldcg), since only its own wait makes
+// earlier kernels' writes visible to all of its loads.  Measured on one call after
 // another: a product of one tile 7.1 -> 5.8 us, 488 rows over 64 groups
 // 48.1 -> 46.9.
 #pragma once

@@ -89,7 +89,8 @@ __device__ __forceinline__ void cluster_sum8(uint32_t at, uint32_t S, float (&z)
 }
 
 // The adapters of 32 W rows from row0 on: lane i has those of rows 32 w + i, kNoAdapter
-// where there is none (rows past M, numbers outside 0 .. L - 1).
+// where there is none (rows past M, numbers outside 0 .. L - 1).  Read past L1: before
+// the kernel's own wait.
 template <int W>
 struct RowAdapters {
     int id[W];
@@ -99,7 +100,7 @@ struct RowAdapters {
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const int64_t m = row0 + 32 * w + lane;
-            const int l = m < M ? adapters[m] : -1;
+            const int l = m < M ? __ldcg(adapters + m) : -1;
             id[w] = l >= 0 && l < L ? l : kNoAdapter;
         }
     }

@@ -166,9 +166,9 @@ __device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *ro
     const __nv_bfloat16 *F = static_cast<const __nv_bfloat16 *>(p.F);
     const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
     uint32_t pending = 0;                                // slots with a copy under way
-    // copy unit x's factor rows (of columns inside N) if its row has an adapter
-    auto fetch = [&](int x, int slot) {
-        const int m = x / 4, n = n0 + x % 4 * 32, l = p.adapters[m];
+    // copy unit x's factor rows (of columns inside N) if its row has an adapter, l
+    auto fetch = [&](int x, int slot, int l) {
+        const int n = n0 + x % 4 * 32;
         if (n >= p.N || l < 0 || l >= p.L)
             return;
         pending |= 1u << slot;
@@ -176,8 +176,10 @@ __device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *ro
         mbar_arrive_expect_tx_w(&bars[slot], bytes);
         bulk_load_w(room + slot * unit_bytes, F + (static_cast<int64_t>(l) * p.N + n) * p.ldf, bytes, &bars[slot]);
     };
-    for (int d = 0; d < depth && first + warp + d * kLfWarps < last; ++d)
-        fetch(first + warp + d * kLfWarps, d);
+    for (int d = 0; d < depth && first + warp + d * kLfWarps < last; ++d) {
+        const int x = first + warp + d * kLfWarps;
+        fetch(x, d, __ldcg(p.adapters + x / 4));         // before the wait: past L1
+    }
     const int m0 = first / 4, rows = last > first ? (last - 1) / 4 - m0 + 1 : 0;
     const int per = static_cast<int>(p.ldu / 8);
     get_ranks(m0, rows);
@@ -213,7 +215,7 @@ __device__ __forceinline__ void adapters_share(const LoraFewArgs &p, uint8_t *ro
         share[(x - first) * 32 + lane] = sum + add;
         __syncwarp();
         if (x + depth * kLfWarps < last)
-            fetch(x + depth * kLfWarps, slot);
+            fetch(x + depth * kLfWarps, slot, p.adapters[(x + depth * kLfWarps) / 4]);
         slot = slot + 1 == depth ? 0 : slot + 1;
     }
 }

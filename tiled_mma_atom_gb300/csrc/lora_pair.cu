@@ -327,6 +327,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) lora_pair_kernel(const __grid_c
                 if (span_ok(at + col0, min(32, p.N - col0), d_limit, err, kBndStoreD))
                     store_row_chunk(D + at, col0, p.N, p.vec_ok, v);
             };
+            // The bias's and the residual's loads go through L1, so after this kernel's own
+            // wait; the tile's accumulator waits for U's kernel too.
+            if (R || p.bias)
+                grid_wait();
             if (!partial)
                 read(c_begin);
             if (!mbar_wait_cluster(&tfull[acc], acc_phase, err, abort_flag, kSiteEpiTmemFull))

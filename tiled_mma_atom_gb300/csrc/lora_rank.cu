@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(kRkThreads) lora_rank_kernel(const __grid_cons
     } else {
         const int q = warp & 3, row = q * 32 + lane;
         const int64_t m = static_cast<int64_t>(row0) + row;
-        const int l = m < p.M ? p.adapters[m] : -1;
+        const int l = m < p.M ? __ldcg(p.adapters + m) : -1;         // `beside`: before this kernel's wait
         has[row] = l >= 0 && l < p.L;
-        scale[row] = has[row] && p.scales ? p.scales[l] : 1.f;
+        scale[row] = has[row] && p.scales ? __ldcg(p.scales + l) : 1.f;
         if (mbar_wait_warp(done, 0, err, abort_flag, kSiteEpiTmemFull)) {
             // --------------------- the accumulator to shared memory
             tc_fence_after();

@@ -321,13 +321,14 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_up_kernel(const __grid_
     }
 }
 
-// Columns col .. col + n - 1 of token t's residual, zeros without one.
+// Columns col .. col + n - 1 of token t's residual, zeros without one; past L1, since the
+// first ones are read before the kernel's own wait.
 __device__ __forceinline__ void few_residual(const MoeFewArgs &p, int t, int col, int n, bool on, float (&f)[8])
 {
     const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(p.residual);
     const __nv_bfloat16 *r = res + t * p.ld_residual + col;
     const bool wide = res && on && n == 8 && (reinterpret_cast<uintptr_t>(r) & 15u) == 0;
-    const uint4 v = wide ? *reinterpret_cast<const uint4 *>(r) : make_uint4(0, 0, 0, 0);
+    const uint4 v = wide ? __ldcg(reinterpret_cast<const uint4 *>(r)) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -337,7 +338,7 @@ __device__ __forceinline__ void few_residual(const MoeFewArgs &p, int t, int col
     if (res && on && !wide)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            f[j] = j < n ? __bfloat162float(r[j]) : 0.f;
+            f[j] = j < n ? __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short *>(r + j))) << 16) : 0.f;
 }
 
 // Eight columns of a token's result: sum + residual, rounded.

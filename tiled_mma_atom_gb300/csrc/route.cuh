@@ -18,7 +18,7 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i, bool bf16)
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
 }
 
-// The same past L1, for a kernel that may share the SM with an earlier reader.
+// The same past L1, for a kernel that reads them before its own wait (launch.cuh).
 __device__ __forceinline__ float load_logit_l2(const void *p, int64_t i, bool bf16)
 {
     if (!bf16)
