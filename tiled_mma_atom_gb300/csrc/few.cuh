@@ -25,6 +25,7 @@ struct FewRing {
     uint64_t full[kFwMaxStages], empty[kFwMaxStages], done;
     uint32_t tmem_slot;
     int abort;
+    int issued[2];             // stages that the weights' and the rows' producer have issued
 };
 
 // sum + the products of eight bf16 with eight others.
@@ -74,6 +75,19 @@ __device__ __forceinline__ void few_setup(const FewShape &p, FewRing &sm, const 
     tc_fence_before();
 }
 
+// After a wait ran out and both producers have ended, by one of their warps: the stages that
+// settle() has to wait for, the last uses of the ring before the returned number.  Where the
+// weights' producer gave up first, the rows' copies of later stages (a ring of them at
+// most) are on their way to barriers at which no one arrives any more: announce them.
+__device__ __forceinline__ int few_announce(const FewShape &p, FewRing &sm)
+{
+    int u = sm.issued[0];
+    for (; u < sm.issued[1]; ++u)
+        mbar_arrive_expect_tx_w(&sm.full[u % p.stages], static_cast<uint32_t>(p.tp) * 128u);
+    __syncwarp();
+    return u;
+}
+
 // The contraction of K blocks kb0 .. kb1 - 1 by warps 0 (weights' producer), 1 (MMA) and
 // 2 (rows' producer), then warps 4..7 put the accumulator into the partial tile
 // [row][128], over the ring.  load_weights(dst, bar, kb), load_rows(dst, bar, kb): the
@@ -107,6 +121,8 @@ __device__ __forceinline__ void few_product(const FewShape &p, FewRing &sm, uint
                 phase ^= 1u;
             }
         }
+        if (lane == 0)
+            sm.issued[warp / 2] = issued;
     } else if (warp == 1) {
         const uint32_t idesc = idesc_bf16_f32(128, p.tp);
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -145,9 +161,10 @@ __device__ __forceinline__ void few_product(const FewShape &p, FewRing &sm, uint
     __syncwarp();
     cluster_sync();                  // every CTA's partial tile is written
     if (warp < 2 && *abort_flag) {
-        if (warp == 0)               // rows and weights share the stages' barriers
-            settle(sm.full, p.stages, stage, phase, issued, err.word, err.budget_ns);
-        else
+        if (warp == 0) {             // rows and weights share the stages' barriers
+            const int n = few_announce(p, sm);
+            settle(sm.full, p.stages, n % p.stages, n / p.stages & 1, n, err.word, err.budget_ns);
+        } else
             settle(&sm.done, 1, 0, 1, 1, err.word, err.budget_ns);
         __syncwarp();
     }

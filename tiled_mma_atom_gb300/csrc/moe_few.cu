@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_up_kernel(const __grid_
             const int s = stage - 1 - i;
             mbar_wait(&sm.empty[s < 0 ? s + p.shape.stages : s], s < 0 ? phase ^ 1u : phase, err, abort_flag, kSiteDrain);
         }
-        if (*abort_flag && warp == 0)
-            settle(sm.full, p.shape.stages, stage, phase, min(issued, p.shape.stages), err.word, err.budget_ns);
+        if (lane == 0)
+            sm.issued[warp / 2] = issued;
     } else if (warp == 1) {
         // -------------------------------------------- MMA issuer
         const uint32_t idesc = idesc_bf16_f32(128, p.shape.tp);
@@ -315,6 +315,10 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_up_kernel(const __grid_
     }
     tc_fence_before();
     __syncthreads();
+    if (warp == 0 && *abort_flag) {
+        const int n = few_announce(p.shape, sm);
+        settle(sm.full, p.shape.stages, n % p.shape.stages, n / p.shape.stages & 1, n, err.word, err.budget_ns);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, p.shape.tmem_cols);
