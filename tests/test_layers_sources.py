@@ -27,3 +27,11 @@ def test_reads_before_the_kernels_own_wait_go_past_l1():
     assert residual.count("__ldcg(") == 2 and "= *reinterpret_cast" not in residual and "(r[j])" not in residual
     epilogue = source("lora_pair.cu").split("int local = 0; while (walk.next(tile, kb0, kb1, partial))")[1]
     assert 0 < epilogue.index("if (R || p.bias) grid_wait();") < epilogue.index("read(c_begin);")
+
+
+def test_launch_rules_count_the_devices_sms():
+    """No number of SMs, nor a multiple of one, stands in the kernels' sources."""
+    for name in ("lora_few.cu", "lora_grad.cu", "lora_pair.cu", "lora_rank.cu", "lora_split.cu", "moe_few.cu", "few.cuh", "api_layers.cu"):
+        numbers = [int(n) for n in re.findall(r"(?<![\w.])\d{3,}(?![\w.])", source(name))]
+        assert not [n for n in numbers if n % 152 == 0 or n % 148 == 0], name
+    assert "num_sms" in between(source("lora_few.cu"), "cudaError_t launch_lora_few_rank(", "}")

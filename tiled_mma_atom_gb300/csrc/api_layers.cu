@@ -170,7 +170,7 @@ tmg_status run_rank(const DeviceState &ds, const RankArgs &a, const Rows &x, con
         RankArgs b = a;
         b.X = x.p;
         b.ldx = x.ld;
-        return launched(launch_lora_few_rank(b, s), "adapter rank launch");
+        return launched(launch_lora_few_rank(b, ds.num_sms, s), "adapter rank launch");
     }
     tmg_status st;
     const int64_t rows = a.across ? a.C : a.r, cols = a.across ? a.r : a.C;

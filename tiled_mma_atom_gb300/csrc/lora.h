@@ -18,7 +18,7 @@ struct RankArgs {
     bool across;
 };
 // For a few rows: not across, C a multiple of 8, X's and F's rows 16-byte aligned.
-cudaError_t launch_lora_few_rank(const RankArgs &a, cudaStream_t s);
+cudaError_t launch_lora_few_rank(const RankArgs &a, int num_sms, cudaStream_t s);
 
 // The same on the tensor cores.
 struct LoraRankArgs {

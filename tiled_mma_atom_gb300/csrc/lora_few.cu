@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kLfThreads = 384, kLfWarps = 8;       // warps 4 .. 11 form the adapters' share
 constexpr int kLfMaxDepth = 8;
-constexpr int kLfManyWarps = 2432;           // of the ranks: two blocks of eight per SM
+constexpr int kLfManyWarps = 16;             // of the ranks, per SM: two blocks of eight
 constexpr int kLfSmem = 108 * 1024;          // of a CTA, where two share an SM
 constexpr int kLfBuffer = 4096;              // a warp's room for factors, at least one unit of 32 columns
 
@@ -320,13 +320,13 @@ __global__ void __launch_bounds__(kLfThreads, 2) lora_few_kernel(const __grid_co
 
 }  // namespace
 
-cudaError_t launch_lora_few_rank(const RankArgs &a, cudaStream_t s)
+cudaError_t launch_lora_few_rank(const RankArgs &a, int num_sms, cudaStream_t s)
 {
     int parts = 1;
     while (parts < 8 && a.C > 2048 * parts)
         parts *= 2;
     const int ranks = static_cast<int>(a.ldu > a.r && a.ldu < a.r + 8 ? a.ldu : a.r);
-    const int J = a.M * ranks * parts > kLfManyWarps ? 2 : 1, groups = (ranks + J - 1) / J;
+    const int J = a.M * ranks * parts > int64_t{kLfManyWarps} * num_sms ? 2 : 1, groups = (ranks + J - 1) / J;
     const int64_t blocks = (a.M * groups + 8 / parts - 1) / (8 / parts);
     return launch_overlapped(J == 1 ? lora_few_rank_kernel<1> : lora_few_rank_kernel<2>, dim3(static_cast<unsigned>(blocks)), 256, 0,
                              1, s, a, parts, groups);
