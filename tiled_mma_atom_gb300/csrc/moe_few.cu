@@ -33,6 +33,8 @@
 // one token's 8 of 64 experts, 2048 x 1024, 101 MB, 26.4 us, of them 2 for the choice, 13
 // for the first kernel's stream (6.1 TB/s, W2's first blocks in it), 1.2 until the
 // second one learns of its end, 6 for the rest of W2 and 1 for the sums.
+#include <atomic>
+
 #include "act.cuh"
 #include "few.cuh"
 #include "moe_few.h"
@@ -481,6 +483,38 @@ __global__ void __launch_bounds__(kFwThreads, 2) moe_few_down_kernel(const __gri
     cluster_sync();                  // no CTA leaves while its partial sums may be read
 }
 
+// The clusters of four CTAs that run at once with an SM for each: a cluster stays within
+// a part of the chip whose SMs need not be a multiple of four (36 on 152 SMs).
+int quads_at_once()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        const int smem = 1024 + 2 * kFwRing - 16384;
+        auto kern = moe_few_down_kernel<0, false>;
+        cudaLaunchAttribute cluster = {};
+        cluster.id = cudaLaunchAttributeClusterDimension;
+        cluster.val.clusterDim.x = 4;
+        cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(4);
+        cfg.blockDim = dim3(kFwThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &cluster;
+        cfg.numAttrs = 1;
+        if (ensure_smem_attr(reinterpret_cast<const void *>(kern), smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();                    // not an error of the next launch
+            return 0;
+        }
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 template <int C, bool BF16>
 cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStream_t s)
 {
@@ -489,13 +523,20 @@ cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStre
     // of 64 experts, 2048 x 1024: 143 us against 152).
     MoeFewArgs b = a;
     few_ring(a.shape, C == 0 ? 2 * kFwRing - a.shape.tp * 512 : kFwRing);
-    // The second kernel: two CTAs per SM, or, where clusters of four with one per SM take
-    // three quarters of the SMs, those and all of an SM's shared memory (13 tokens, 4 of 32
-    // experts, 4096 x 2048, 32 tiles: 206 us against 222; 24 tiles 50 and 52 the other way;
-    // clusters of eight need eight free SMs of one part of the chip and wait for them: 245).
+    // The second kernel: two CTAs per SM in clusters of up to eight; or clusters of four
+    // where those take three quarters of the SMs at one CTA each, with all of an SM's
+    // shared memory if they all fit at once so (32 experts of width 1024: 35 tiles, 13
+    // tokens 122 -> 118 us, 61 tokens 169 -> 147; 32 tiles 205 and 204, 151 -> 137, one token 20.0
+    // and 20.3; 25 tiles 90 and 94), else with half of it (38 tiles, where 36 clusters fit: 157
+    // us with all of it, 144 in clusters of eight, 127 so); or pairs where clusters of four do not
+    // fit at two CTAs per SM (75 tiles, 16 experts, 13 tokens 170 -> 152, one token of 8 experts
+    // 34 -> 30; 68 tiles, where they do, 28.0 and 29.2 in pairs, 64 tiles 137 and 135 at 61 tokens).
     const int64_t downs = (a.H + 127) / 128;
-    const bool deep = 4 * downs <= num_sms && 16 * downs >= 3 * num_sms;
-    const int s_down = deep ? 4 : few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), 2 * num_sms);
+    const bool four = 4 * downs <= num_sms && 16 * downs >= 3 * num_sms;
+    const bool pairs = 2 * downs <= num_sms && 8 * downs >= 3 * num_sms;
+    const int quads = four || pairs ? quads_at_once() : 0;
+    const bool two = pairs && downs > 2 * quads, deep = two || (four && downs <= quads);
+    const int s_down = four ? 4 : two ? 2 : few_cluster(downs, static_cast<int64_t>(a.k) * ((a.F + 63) / 64), 2 * num_sms);
     few_ring(b.shape, deep ? 2 * kFwRing - 16384 : kFwRing);
     const int smem = 1024 + b.shape.ring_bytes, smem_up = 1024 + a.shape.ring_bytes + a.shape.tp * 512;
     auto up = moe_few_up_kernel<C, BF16>;
