@@ -315,8 +315,8 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, const Adapte
     p.L = static_cast<int>(a.L);
     p.r = static_cast<int>(a.r);
     p.vec_ok = a.ldd % 8 == 0 && aligned(a.D);
-    log_choice("bf16 with adapters: %d rows, N=%d K=%d rank %d -> lora_pair_kernel: 256 x %d tiles, weights %s", p.M, p.N, p.K,
-               p.r, bn, a.across ? "MN-major" : "K-major");
+    log_choice("bf16 with adapters: %d rows, N=%d K=%d rank %d -> lora_pair_kernel: 256 x %d tiles, weights %s, %d tiles cut over %d pairs",
+               p.M, p.N, p.K, p.r, bn, a.across ? "MN-major" : "K-major", t.tail.tiles, t.tail.tiles * t.tail.each);
     return launched(launch_lora_pair(p, bn, a.across, static_cast<int>(t.ctas / 2), err_ctx(ds), s), "product with adapters launch");
 }
 
