@@ -160,3 +160,24 @@ def test_weights_of_experts_at_any_element(tmg, T, by):
         check_layer(tmg, shifted(x, by) if "x" in names else x, shifted(logits, by) if "r" in names else logits,
                     shifted(W1, by) if "1" in names else W1, shifted(W2, by) if "2" in names else W2, 3,
                     residual=shifted(res, by) if "r" in names else res, name=names)
+
+
+@pytest.mark.parametrize("M", [40, 130, 700])
+def test_rows_that_overlap(tmg, M):
+    """Inputs whose row stride is less than a row: any other one is read, so are these."""
+    N, K, r = 136, 72, 8
+    t, of, u = lora_inputs(M, N, K, r, 3, 470), ids_of("runs", M, 3, 471), normal((M, r), 472)
+    t["x"] = normal((M * 8 + K,), 473).as_strided((M, K), (8, 1))
+    t["W"] = normal((N * 64 + K,), 474, 0.1).as_strided((N, K), (64, 1))
+    check_lora(tmg, t, of, residual=normal((M * 8 + N,), 475).as_strided((M, N), (8, 1)))
+    check_grads(tmg, t, of, normal((M * 8 + N,), 476).as_strided((M, N), (8, 1)), u)
+    _, logits, W1, W2, _ = moe_inputs(M, 8, K, 40, 477)
+    check_layer(tmg, t["x"], logits, W1, W2, 2)
+    offsets = torch.tensor([0, M // 3, M], dtype=torch.int32, device=DEV)
+    ints = lambda rows, cols, ld, seed: normal((rows * ld + cols,), seed).round().as_strided((rows, cols), (ld, 1))       # exact sums
+    a, b = ints(M, K, 8, 478), ints(N, K, 64, 479)
+    assert torch.equal(tmg.linear(a, b), (a.double() @ b.double().T).to(BF16))
+    B = normal((2, N, K), 480).round()
+    want = torch.cat([a[:M // 3].double() @ B[0].double().T, a[M // 3:].double() @ B[1].double().T]).to(BF16)
+    assert torch.equal(tmg.grouped_gemm(a, B, offsets), want)
+    tmg.check()

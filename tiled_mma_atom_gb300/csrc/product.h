@@ -44,11 +44,11 @@ inline bool out_rows_ok(int64_t rows, int64_t cols, int64_t ld) { return rows <=
 inline bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Whether TMA reads a (rows, cols) operand of `elem`-byte elements in place:
-// 16-byte aligned base and rows, positive strides below 2^40 bytes.
+// 16-byte aligned base and rows, strides below 2^40 bytes, and rows that do not overlap.
 inline bool rows_in_place(const void *p, int64_t rows, int64_t row, int64_t cols, int64_t col, int elem)
 {
     return aligned(p) && cols > 0 && rows > 0 && (cols == 1 || col == 1) &&
-           (rows == 1 || (row > 0 && row * elem % 16 == 0 && row * elem < (int64_t{1} << 40)));
+           (rows == 1 || (row >= cols && row * elem % 16 == 0 && row * elem < (int64_t{1} << 40)));
 }
 
 // A stride for a dimension of extent 1, where the caller's says nothing.
