@@ -461,8 +461,9 @@ tmg_status tmg_linear_backward(const void *dD, int64_t ldd, const void *preact,
  *   z = x[t] . W1[e]^T (2 F columns), h = silu(z[f]) * z[F + f],
  *   out[t] = bf16(residual[t] + sum_j w[t, j] * W2[e[t, j]] . h),
  * with experts e and weights w as tmg_moe_route chooses them from the logits, fp32
- * sums; a token without a choice gets its residual (or zeros).  No token's result
- * depends on what others, or experts that only others chose, hold.
+ * sums; a token without a choice gets its residual (or zeros).  What other tokens, or
+ * experts that only others chose, hold never enters a token's result; the order of its
+ * fp32 sums, and with it the last bit, may depend on which experts the others chose.
  * Up to 64 tokens and 256 experts, with H and F multiples of 8 and x, W1 and W2
  * readable in 16-byte rows, it runs in kernels of its own, which round w * h to
  * bf16; else tmg_moe_route, both products and tmg_moe_combine follow one
@@ -493,7 +494,8 @@ tmg_status tmg_moe_layer(const tmg_moe_args *args, void *stream);
  *   D[m] = bf16(x[m] . W^T + u[m] . B[a]^T + bias + residual[m]).
  * A row whose adapter is not one of 0 .. L - 1 (-1, say) has u = 0 and adds
  * nothing.  What another row or its adapter holds, infinities and NaN too,
- * never reaches a row.  Rows of one request are best adjacent: beyond 64 rows the
+ * never reaches a row; the order of a row's fp32 sums, and with it the last bit, may
+ * depend on the adapters of the rows beside it.  Rows of one request are best adjacent: beyond 64 rows the
  * time grows with the number of different adapters in 128 or 256 rows in a row.
  * x, W, A and B whose rows (of K, of K, of K and of r elements) are 16-byte aligned
  * are read in place, others copied to workspace.  Adapters of a lower rank are

@@ -321,8 +321,8 @@ tmg_status run_adapted(const DeviceState &ds, const AdaptedArgs &a, const Adapte
 }
 
 // The layer in two kernels (three with more than 16 tokens), for few tokens: 16 tokens of
-// 64 experts, 2048 x 1024, 119 us against 131 by groups, 61 tokens 143 and 147, 61 of 32
-// experts, 4096 x 2048, 250 and 258; with one rounding between the products where the groups
+// 64 experts, 2048 x 1024, 119 us against 131 by groups, 13 of 32 experts, 4096 x 2048, 171
+// and 184, 61 of 64 experts, 2048 x 1024, 143 and 145, one token 26 and 33; with one rounding between the products where the groups
 // have two.
 bool few_tokens(const tmg_moe_args &g)
 {

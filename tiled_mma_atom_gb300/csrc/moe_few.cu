@@ -29,8 +29,8 @@
 // first one lets it start only after its own wait for the kernel before: so logits (or
 // choices) and weights are complete by then.
 //
-// Bound by HBM: 13 tokens, 4 of 32 experts, 4096 x 2048, 1.11 GB, 168 us (6.6 TB/s);
-// one token's 8 of 64 experts, 2048 x 1024, 101 MB, 26.4 us, of them 2 for the choice, 13
+// Bound by HBM: 13 tokens, 4 of 32 experts, 4096 x 2048, 20 to 22 in use, 1.07 GB, 168 to
+// 172 us (6.3 TB/s); one token's 8 of 64 experts, 2048 x 1024, 101 MB, 25.8 us, of them 2 for the choice, 13
 // for the first kernel's stream (6.1 TB/s, W2's first blocks in it), 1.2 until the
 // second one learns of its end, 6 for the rest of W2 and 1 for the sums.
 #include <atomic>
@@ -523,14 +523,15 @@ cudaError_t launch_few_as(MoeFewArgs a, int num_sms, const ErrCtx &err, cudaStre
     // of 64 experts, 2048 x 1024: 143 us against 152).
     MoeFewArgs b = a;
     few_ring(a.shape, C == 0 ? 2 * kFwRing - a.shape.tp * 512 : kFwRing);
-    // The second kernel: two CTAs per SM in clusters of up to eight; or clusters of four
-    // where those take three quarters of the SMs at one CTA each, with all of an SM's
-    // shared memory if they all fit at once so (32 experts of width 1024: 35 tiles, 13
-    // tokens 122 -> 118 us, 61 tokens 169 -> 147; 32 tiles 205 and 204, 151 -> 137, one token 20.0
-    // and 20.3; 25 tiles 90 and 94), else with half of it (38 tiles, where 36 clusters fit: 157
-    // us with all of it, 144 in clusters of eight, 127 so); or pairs where clusters of four do not
-    // fit at two CTAs per SM (75 tiles, 16 experts, 13 tokens 170 -> 152, one token of 8 experts
-    // 34 -> 30; 68 tiles, where they do, 28.0 and 29.2 in pairs, 64 tiles 137 and 135 at 61 tokens).
+    // The second kernel: two CTAs per SM in clusters of up to eight, with these exceptions.
+    // Clusters of four where those take three quarters of the SMs at one CTA each: with all
+    // of an SM's shared memory if they all fit at once so (4 of 32 experts, width 1024, 35
+    // tiles, 13 tokens 122 -> 118 us, 61 tokens 169 -> 147; width 2048, 32 tiles, 13 tokens 205
+    // and 204; 25 tiles 90 and 94), else with half of it (38 tiles, where 36 clusters fit:
+    // 157 us with all of it, 144 in clusters of eight, 127 so).  Pairs with an SM for each
+    // CTA where clusters of four do not all fit at two per SM (4 of 16 experts, 75 tiles,
+    // 13 tokens 170 -> 152, one token's 2 of 8 experts 34 -> 30; 68 tiles, where they fit, 28.0
+    // and 29.2 in pairs).
     const int64_t downs = (a.H + 127) / 128;
     const bool four = 4 * downs <= num_sms && 16 * downs >= 3 * num_sms;
     const bool pairs = 2 * downs <= num_sms && 8 * downs >= 3 * num_sms;
