@@ -30,9 +30,9 @@
 // choices) and weights are complete by then.
 //
 // Bound by HBM: 13 tokens, 4 of 32 experts, 4096 x 2048, 20 to 22 in use, 1.07 GB, 168 to
-// 172 us (6.3 TB/s); one token's 8 of 64 experts, 2048 x 1024, 101 MB, 25.8 us, of them 2 for the choice, 13
-// for the first kernel's stream (6.1 TB/s, W2's first blocks in it), 1.2 until the
-// second one learns of its end, 6 for the rest of W2 and 1 for the sums.
+// 172 us (6.3 TB/s); one token's 8 of 64 experts, 2048 x 1024, 101 MB, 25.8 us, of them 2
+// for the choice, 13 for the first kernel's stream (6.1 TB/s, W2's first blocks in it), 1
+// until the second one learns of its end, 6 for the rest of W2 and 1 for the sums.
 #include <atomic>
 
 #include "act.cuh"
